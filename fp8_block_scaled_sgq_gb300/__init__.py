@@ -2,8 +2,9 @@
 
 The compute lives in ``libsgq.so`` (hand-written CUDA behind the C ABI of
 ``include/sgq.h``).  This package holds the ctypes binding (``binding``), the
-nvcc build (``build``), seeded synthetic inputs (``synth``) and a few
-torch-facing helpers below that only allocate outputs and call the binding.
+nvcc build (``build``), seeded synthetic inputs (``synth``), a few
+torch-facing helpers below that only allocate outputs and call the binding, and
+the latent attention between the linears (``latent``).
 """
 from __future__ import annotations
 
@@ -15,7 +16,10 @@ from .binding import (  # noqa: F401
     sgq_quant_per_tensor, sgq_quant_per_token, sgq_quant_token_group_v2, sgq_launch_count, sgq_quant_token_group,
     sgq_allocated_bytes, sgq_fp8_block_gemm_ue8m0, sgq_quant_token_group_ue8m0, sgq_scales_to_ue8m0,
     sgq_gemm_plan, sgq_gemm_plan_pow2,
-    sgq_quant_weight_block, sgq_version, status_string)
+    sgq_quant_weight_block, sgq_version, status_string,
+    SGQ_BF16, SGQ_FP16, sgq_rotary, sgq_latent_append, sgq_latent_attention, sgq_latent_attention_workspace,
+    sgq_latent_prefill)
+from .latent import latent_append, latent_attention, latent_prefill, rotary, rotary_table  # noqa: F401
 
 
 def quant_token_group(x, group: int, ue8m0: bool, stream=None):

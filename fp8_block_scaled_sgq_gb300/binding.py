@@ -30,6 +30,9 @@ SGQ_GEMM_ISSUE_SINGLE = 4
 SGQ_GEMM_TEST_TIMEOUT = 8
 SGQ_GEMM_SCALES_POW2 = 16
 
+SGQ_BF16 = 0
+SGQ_FP16 = 1
+
 # Symbols declared in include/sgq.h (checked by the tests).
 EXPORTS = (
     "sgq_quant_token_group",
@@ -45,6 +48,11 @@ EXPORTS = (
     "sgq_quant_per_token",
     "sgq_quant_per_tensor",
     "sgq_fp8_scaled_mm",
+    "sgq_rotary",
+    "sgq_latent_append",
+    "sgq_latent_attention_workspace",
+    "sgq_latent_attention",
+    "sgq_latent_prefill",
     "sgq_status_string",
     "sgq_device_status",
     "sgq_launch_count",
@@ -93,6 +101,18 @@ def load_library(path: str = LIB_PATH):
                   "sgq_fp8_block_gemm_ex", "sgq_fp8_block_gemm_noalloc", "sgq_fp8_block_linear",
                   "sgq_fp8_block_gemm_ue8m0", "sgq_quant_token_group_ue8m0", "sgq_scales_to_ue8m0",
                   "sgq_quant_per_token", "sgq_quant_per_tensor", "sgq_fp8_scaled_mm", "sgq_quant_token_group_v2"):
+            getattr(lib, f).restype = ci
+        cf = ctypes.c_float
+        lib.sgq_rotary.argtypes = [P, i64, i64, i64, i64, i64, P, P, i64, ci, i64, ci, ci, ci, P, i64, i64, P]
+        lib.sgq_latent_append.argtypes = [P, i64, i64, P, i64, P, i64, P, P, P, i64, i64, i64, i64, ci, ci, ci, P, i64,
+                                          i64, P, i64, P, i64, i64, i64, i64, P]
+        lib.sgq_latent_attention_workspace.argtypes = [i64, i64, i64, P]
+        lib.sgq_latent_attention.argtypes = [P, i64, i64, i64, P, i64, i64, i64, i64, i64, ci, P, i64, i64, P, P, cf,
+                                             ci, P, P, P, i64, P]
+        lib.sgq_latent_prefill.argtypes = [P, i64, i64, i64, P, i64, i64, P, i64, P, i64, i64, i64, i64, i64, ci, P, P,
+                                           i64, cf, ci, ci, P, P, P]
+        for f in ("sgq_rotary", "sgq_latent_append", "sgq_latent_attention_workspace", "sgq_latent_attention",
+                  "sgq_latent_prefill"):
             getattr(lib, f).restype = ci
         lib.sgq_status_string.argtypes = [ci]
         lib.sgq_status_string.restype = ctypes.c_char_p
@@ -212,6 +232,49 @@ def sgq_fp8_scaled_mm(Aq, sa, sa_n, Wq, sb, sb_n, bias, D, M, N, K, stream=None)
     _check(load_library().sgq_fp8_scaled_mm(_ptr(Aq), _ptr(sa), sa_n, _ptr(Wq), _ptr(sb), sb_n, _ptr(bias),
                                             _ptr(D), M, N, K, _stream(stream)),
            "sgq_fp8_scaled_mm")
+
+
+def sgq_rotary(x, T, H, D, x_stride_t, x_stride_h, pos, table, max_pos, R, offset, interleaved, inverse, dtype, y,
+               y_stride_t, y_stride_h, stream=None):
+    _check(load_library().sgq_rotary(_ptr(x), T, H, D, x_stride_t, x_stride_h, _ptr(pos), _ptr(table), max_pos, R,
+                                     offset, int(interleaved), int(inverse), dtype, _ptr(y), y_stride_t, y_stride_h,
+                                     _stream(stream)), "sgq_rotary")
+
+
+def sgq_latent_append(q, q_stride_t, q_stride_h, k, k_stride, latent, latent_stride, pos, slots, table, max_pos, T, H,
+                      L, R, interleaved, dtype, q_out, qo_stride_t, qo_stride_h, k_out, ko_stride, cache, pages, page,
+                      cache_stride_page, cache_stride_row, stream=None):
+    _check(load_library().sgq_latent_append(_ptr(q), q_stride_t, q_stride_h, _ptr(k), k_stride, _ptr(latent),
+                                            latent_stride, _ptr(pos), _ptr(slots), _ptr(table), max_pos, T, H, L, R,
+                                            int(interleaved), dtype, _ptr(q_out), qo_stride_t, qo_stride_h,
+                                            _ptr(k_out), ko_stride, _ptr(cache), pages, page, cache_stride_page,
+                                            cache_stride_row, _stream(stream)), "sgq_latent_append")
+
+
+def sgq_latent_attention_workspace(T, H, L) -> int:
+    """Bytes of device memory that sgq_latent_attention needs as its workspace."""
+    out = ctypes.c_int64()
+    _check(load_library().sgq_latent_attention_workspace(T, H, L, ctypes.byref(out)),
+           "sgq_latent_attention_workspace")
+    return out.value
+
+
+def sgq_latent_attention(q, q_stride_row, T, H, cache, pages, page, cache_stride_page, cache_stride_row, L, R,
+                         page_table, table_width, B, kv_lens, q_starts, scale, dtype, out, lse, workspace,
+                         workspace_bytes, stream=None):
+    _check(load_library().sgq_latent_attention(_ptr(q), q_stride_row, T, H, _ptr(cache), pages, page,
+                                               cache_stride_page, cache_stride_row, L, R, _ptr(page_table),
+                                               table_width, B, _ptr(kv_lens), _ptr(q_starts), scale, dtype, _ptr(out),
+                                               _ptr(lse), _ptr(workspace), workspace_bytes, _stream(stream)),
+           "sgq_latent_attention")
+
+
+def sgq_latent_prefill(q, q_stride_t, q_stride_h, T, k, k_stride_t, k_stride_h, k_rot, kr_stride, v, v_stride_t,
+                       v_stride_h, S, H, N, R, q_starts, kv_starts, B, scale, causal, dtype, out, lse, stream=None):
+    _check(load_library().sgq_latent_prefill(_ptr(q), q_stride_t, q_stride_h, T, _ptr(k), k_stride_t, k_stride_h,
+                                             _ptr(k_rot), kr_stride, _ptr(v), v_stride_t, v_stride_h, S, H, N, R,
+                                             _ptr(q_starts), _ptr(kv_starts), B, scale, int(causal), dtype, _ptr(out),
+                                             _ptr(lse), _stream(stream)), "sgq_latent_prefill")
 
 
 def sgq_device_status(stream=None) -> int:

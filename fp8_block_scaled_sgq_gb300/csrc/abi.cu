@@ -4,7 +4,9 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdint>
+#include <initializer_list>
 #include <mutex>
 
 #include "sgq_internal.h"
@@ -18,6 +20,19 @@ bool g_dev_ok[64] = {};
 std::mutex g_dev_mu;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned_to(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+
+// The latent-attention calls: element type, rotated width (whole 16-byte
+// columns of pairs), strides (16-byte columns).
+bool good_dtype(int dtype) { return dtype == SGQ_BF16 || dtype == SGQ_FP16; }
+bool good_rotation(int R, int interleaved) {
+    return (interleaved == 0 || interleaved == 1) && R > 0 && R <= 2048 && R % (interleaved ? 8 : 16) == 0;
+}
+bool good_strides(std::initializer_list<int64_t> strides) {
+    for (const int64_t s : strides)
+        if (s < 0 || s % 8 != 0 || s > (int64_t(1) << 40)) return false;
+    return true;
+}
 
 }  // namespace
 
@@ -45,6 +60,10 @@ sgq_status device_info(DeviceInfo* out) {
 }  // namespace sgq
 
 using sgq::aligned16;
+using sgq::aligned_to;
+using sgq::good_dtype;
+using sgq::good_rotation;
+using sgq::good_strides;
 
 extern "C" {
 
@@ -215,6 +234,112 @@ sgq_status sgq_fp8_block_linear(const void* x, int ue8m0, const void* Wq, const 
         return SGQ_ERR_MISALIGNED;
     return sgq::launch_fp8_block_linear(x, ue8m0, Wq, Ws, D, M, N, K, blk_n, blk_k, xq, xs,
                                         reinterpret_cast<cudaStream_t>(stream));
+}
+
+sgq_status sgq_rotary(const void* x, int64_t T, int64_t H, int64_t D, int64_t x_stride_t, int64_t x_stride_h,
+                      const int64_t* pos, const float* table, int64_t max_pos, int R, int64_t offset, int interleaved,
+                      int inverse, int dtype, void* y, int64_t y_stride_t, int64_t y_stride_h, sgq_stream_t stream) {
+    if (T < 0 || H < 0 || H > 65535 || D <= 0 || D > 2048 || D % 8 != 0 || max_pos <= 0 || offset < 0 || offset % 8 != 0 ||
+        !good_rotation(R, interleaved) || offset + R > D || (inverse != 0 && inverse != 1) || !good_dtype(dtype) ||
+        !good_strides({x_stride_t, x_stride_h, y_stride_t, y_stride_h}) || T >= (int64_t(1) << 31))
+        return SGQ_ERR_INVALID_ARG;
+    if (T == 0 || H == 0) return SGQ_OK;
+    if (x == y && (x_stride_t != y_stride_t || x_stride_h != y_stride_h)) return SGQ_ERR_INVALID_ARG;
+    if ((T > 1 && y_stride_t < D) || (H > 1 && y_stride_h < D)) return SGQ_ERR_INVALID_ARG;   // heads of y apart
+    if (!x || !pos || !table || !y) return SGQ_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(table) || !aligned16(y) || !aligned_to(pos, 8)) return SGQ_ERR_MISALIGNED;
+    return sgq::launch_rotary(x, T, H, D, x_stride_t, x_stride_h, pos, table, max_pos, R, offset, interleaved, inverse,
+                              dtype, y, y_stride_t, y_stride_h, reinterpret_cast<cudaStream_t>(stream));
+}
+
+sgq_status sgq_latent_append(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k, int64_t k_stride,
+                             const void* latent, int64_t latent_stride, const int64_t* pos, const int64_t* slots,
+                             const float* table, int64_t max_pos, int64_t T, int64_t H, int64_t L, int R,
+                             int interleaved, int dtype, void* q_out, int64_t qo_stride_t, int64_t qo_stride_h,
+                             void* k_out, int64_t ko_stride, void* cache, int64_t pages, int64_t page,
+                             int64_t cache_stride_page, int64_t cache_stride_row, sgq_stream_t stream) {
+    if (T < 0 || T >= (int64_t(1) << 31) || H < 0 || H > 65535 || L <= 0 || L % 8 != 0 || L > 65536 || max_pos <= 0 ||
+        !good_rotation(R, interleaved) || R > 256 || !good_dtype(dtype) ||
+        !good_strides({q_stride_t, q_stride_h, k_stride, latent_stride, qo_stride_t, qo_stride_h, ko_stride,
+                       cache_stride_page, cache_stride_row}))
+        return SGQ_ERR_INVALID_ARG;
+    if (pages < 0 || page <= 0 || page >= (int64_t(1) << 31) || pages >= (int64_t(1) << 31) ||
+        cache_stride_row < L + R || cache_stride_page < 0)
+        return SGQ_ERR_INVALID_ARG;
+    if (T == 0) return SGQ_OK;
+    if (q == q_out && H > 0 && (q_stride_t != qo_stride_t || q_stride_h != qo_stride_h)) return SGQ_ERR_INVALID_ARG;
+    if (H > 0 && ((T > 1 && qo_stride_t < R) || (H > 1 && qo_stride_h < R))) return SGQ_ERR_INVALID_ARG;
+    if (k_out && T > 1 && ko_stride < R) return SGQ_ERR_INVALID_ARG;
+    if (!k || !latent || !pos || !slots || !table || !cache || (H > 0 && (!q || !q_out))) return SGQ_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(q_out) || !aligned16(k) || !aligned16(latent) || !aligned16(table) ||
+        !aligned16(k_out) || !aligned16(cache) || !aligned_to(pos, 8) || !aligned_to(slots, 8))
+        return SGQ_ERR_MISALIGNED;
+    return sgq::launch_latent_append(q, q_stride_t, q_stride_h, k, k_stride, latent, latent_stride, pos, slots, table,
+                                     max_pos, T, H, L, R, interleaved, dtype, q_out, qo_stride_t, qo_stride_h, k_out,
+                                     ko_stride, cache, pages, page, cache_stride_page, cache_stride_row,
+                                     reinterpret_cast<cudaStream_t>(stream));
+}
+
+sgq_status sgq_latent_attention_workspace(int64_t T, int64_t H, int64_t L, int64_t* bytes) {
+    if (bytes == nullptr || T < 0 || H <= 0 || H > 65535 || L <= 0 || L % 128 != 0 || L > 512) return SGQ_ERR_INVALID_ARG;
+    return sgq::latent_attention_workspace(T, H, L, bytes);
+}
+
+sgq_status sgq_latent_attention(const void* q, int64_t q_stride_row, int64_t T, int64_t H, const void* cache,
+                                int64_t pages, int64_t page, int64_t cache_stride_page, int64_t cache_stride_row,
+                                int64_t L, int R, const int32_t* page_table, int64_t table_width, int64_t B,
+                                const int32_t* kv_lens, const int32_t* q_starts, float scale, int dtype, void* out,
+                                float* lse, void* workspace, int64_t workspace_bytes, sgq_stream_t stream) {
+    if (T < 0 || B < 0 || H <= 0 || H > 65535 || T * H >= (int64_t(1) << 31) || B >= (int64_t(1) << 31) || L <= 0 ||
+        L % 128 != 0 || L > 512 || R < 8 || R > 64 || R % 8 != 0 || !good_dtype(dtype) ||
+        !good_strides({q_stride_row, cache_stride_page, cache_stride_row}) || !std::isfinite(scale))
+        return SGQ_ERR_INVALID_ARG;
+    if (pages <= 0 || pages >= (int64_t(1) << 31) || page <= 0 || page % 16 != 0 || page >= (int64_t(1) << 31) ||
+        table_width < 0 || table_width * page >= (int64_t(1) << 31) || q_stride_row < L + R ||
+        cache_stride_row < L + R || cache_stride_page < cache_stride_row * page)
+        return SGQ_ERR_INVALID_ARG;
+    if (q_starts == nullptr && T != B) return SGQ_ERR_INVALID_ARG;
+    if (T == 0) return SGQ_OK;
+    if (B == 0 || !q || !cache || !kv_lens || !out || (table_width > 0 && !page_table) || !workspace)
+        return SGQ_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(cache) || !aligned16(out) || !aligned16(workspace) || !aligned_to(page_table, 4) ||
+        !aligned_to(kv_lens, 4) || !aligned_to(q_starts, 4) || !aligned_to(lse, 4))
+        return SGQ_ERR_MISALIGNED;
+    int64_t need = 0;
+    sgq_status rc = sgq::latent_attention_workspace(T, H, L, &need);
+    if (rc != SGQ_OK) return rc;
+    if (workspace_bytes < need) return SGQ_ERR_INVALID_ARG;
+    sgq::LatentArgs a{};
+    a.q = q; a.cache = cache; a.page_table = page_table; a.kv_lens = kv_lens; a.q_starts = q_starts; a.out = out;
+    a.lse = lse; a.workspace = workspace; a.q_row = q_stride_row; a.T = T; a.B = B; a.pages = pages;
+    a.c_page = cache_stride_page; a.c_row = cache_stride_row; a.table_width = table_width;
+    a.H = static_cast<int>(H); a.L = static_cast<int>(L); a.R = R; a.page = static_cast<int>(page); a.dtype = dtype;
+    a.scale = scale;
+    return sgq::launch_latent_attention(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+sgq_status sgq_latent_prefill(const void* q, int64_t q_stride_t, int64_t q_stride_h, int64_t T, const void* k,
+                              int64_t k_stride_t, int64_t k_stride_h, const void* k_rot, int64_t kr_stride,
+                              const void* v, int64_t v_stride_t, int64_t v_stride_h, int64_t S, int64_t H, int64_t N,
+                              int R, const int32_t* q_starts, const int32_t* kv_starts, int64_t B, float scale,
+                              int causal, int dtype, void* out, float* lse, sgq_stream_t stream) {
+    if (T < 0 || S < 0 || B < 0 || H <= 0 || H > 65535 || T >= (int64_t(1) << 31) || S >= (int64_t(1) << 31) ||
+        B >= (int64_t(1) << 31) || (N != 64 && N != 128) || R < 8 || R > 64 || R % 8 != 0 || !good_dtype(dtype) ||
+        !good_strides({q_stride_t, q_stride_h, k_stride_t, k_stride_h, kr_stride, v_stride_t, v_stride_h}) ||
+        (causal != 0 && causal != 1) || !std::isfinite(scale))
+        return SGQ_ERR_INVALID_ARG;
+    if (T == 0) return SGQ_OK;
+    if (B == 0 || !q || !q_starts || !kv_starts || !out || (S > 0 && (!k || !k_rot || !v))) return SGQ_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(k_rot) || !aligned16(v) || !aligned16(out) ||
+        !aligned_to(q_starts, 4) || !aligned_to(kv_starts, 4) || !aligned_to(lse, 4))
+        return SGQ_ERR_MISALIGNED;
+    sgq::PrefillArgs a{};
+    a.q = q; a.k = k; a.k_rot = k_rot; a.v = v; a.q_starts = q_starts; a.kv_starts = kv_starts; a.out = out; a.lse = lse;
+    a.q_t = q_stride_t; a.q_h = q_stride_h; a.k_t = k_stride_t; a.k_h = k_stride_h; a.kr_t = kr_stride;
+    a.v_t = v_stride_t; a.v_h = v_stride_h; a.T = T; a.S = S; a.B = B;
+    a.H = static_cast<int>(H); a.N = static_cast<int>(N); a.R = R; a.causal = causal; a.dtype = dtype;
+    a.scale = scale;
+    return sgq::launch_latent_prefill(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 const char* sgq_status_string(sgq_status s) {

@@ -50,6 +50,43 @@ sgq_status launch_fp8_block_linear(const void* x, int ue8m0, const void* Wq, con
 sgq_status launch_fp8_scaled_mm(const void* Aq, const float* sa, int64_t sa_n, const void* Wq,
                                 const float* sb, int64_t sb_n, const void* bias, void* D, int64_t M,
                                 int64_t N, int64_t K, cudaStream_t stream);
+sgq_status launch_rotary(const void* x, int64_t T, int64_t H, int64_t D, int64_t x_t, int64_t x_h, const int64_t* pos,
+                         const float* table, int64_t max_pos, int R, int64_t offset, int inter, int inverse, int dtype,
+                         void* y, int64_t y_t, int64_t y_h, cudaStream_t stream);
+sgq_status launch_latent_append(const void* q, int64_t q_t, int64_t q_h, const void* k, int64_t k_t, const void* latent,
+                                int64_t l_t, const int64_t* pos, const int64_t* slots, const float* table,
+                                int64_t max_pos, int64_t T, int64_t H, int64_t L, int R, int inter, int dtype,
+                                void* q_out, int64_t qo_t, int64_t qo_h, void* k_out, int64_t ko_t, void* cache,
+                                int64_t pages, int64_t page, int64_t c_page, int64_t c_row, cudaStream_t stream);
+// Arguments of the absorbed latent attention (sizes in elements).
+struct LatentArgs {
+    const void* q;
+    const void* cache;
+    const int32_t* page_table;
+    const int32_t* kv_lens;
+    const int32_t* q_starts;   // null: one query token a request
+    void* out;
+    float* lse;                // or null
+    void* workspace;
+    uint32_t* status;
+    int64_t q_row, T, B, pages, c_page, c_row, table_width;
+    int H, L, R, page, dtype;
+    float scale;
+};
+sgq_status latent_attention_workspace(int64_t T, int64_t H, int64_t L, int64_t* bytes);
+sgq_status launch_latent_attention(const LatentArgs& a, cudaStream_t stream);
+// Arguments of the expanded latent attention.
+struct PrefillArgs {
+    const void *q, *k, *k_rot, *v;
+    const int32_t *q_starts, *kv_starts;
+    void* out;
+    float* lse;                // or null
+    uint32_t* status;
+    int64_t q_t, q_h, k_t, k_h, kr_t, v_t, v_h, T, S, B;
+    int H, N, R, causal, dtype;
+    float scale;
+};
+sgq_status launch_latent_prefill(const PrefillArgs& a, cudaStream_t stream);
 // The GEMM's launch plan for a device with sm_count SMs (host only):
 // out[0..7] = swap-AB, BN, K splits, work items, grid, alternating issuers,
 // cluster split-K, CTA pairs.

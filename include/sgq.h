@@ -326,6 +326,116 @@ sgq_status sgq_fp8_scaled_mm(const void* Aq, const float* sa, int64_t sa_n, cons
                              const float* sb, int64_t sb_n, const void* bias, void* D, int64_t M,
                              int64_t N, int64_t K, sgq_stream_t stream);
 
+/*
+ * Latent attention: the steps between a layer's W8A8 linears when its keys
+ * and values are one shared latent vector a token (the linears of
+ * 24576 = 128 heads x (128 + 64) and 2048 = 16 heads x 128 columns).  Element
+ * types are SGQ_BF16 or SGQ_FP16 (`dtype`, one for all of a call's tensors);
+ * sums, softmax statistics and rotations are fp32, rounded once on the way
+ * out (and the softmax weights once, to `dtype`, as a matrix product's
+ * operand).  Strides are in elements, the innermost one is 1; every address
+ * and stride is a multiple of 16 bytes, i.e. 8 elements.  int64_t arrays on
+ * the device hold positions and slots, int32_t ones lengths and page numbers;
+ * they need natural alignment only.  Values on the device that point outside
+ * their tensor (a position, a slot, a page, a length) are never followed:
+ * they set the device status (sgq_device_status -> SGQ_ERR_INVALID_ARG) and
+ * the outputs that they concern are undefined.
+ */
+#define SGQ_BF16 0
+#define SGQ_FP16 1
+
+/*
+ * Rotary positions: y = x with elements [offset, offset + R) of every head
+ * rotated by its token's position.  table: fp32 [max_pos, R], row p holding
+ * the R/2 cosines and then the R/2 sines of position p's angles (any base and
+ * any long-context scaling are the table's).  Pair i, (a, b) -> (a cos - b
+ * sin, b cos + a sin), is elements 2i, 2i + 1 (interleaved = 1) or i, i + R/2
+ * (interleaved = 0).  inverse = 1 rotates back: the transpose, i.e. the
+ * gradient.
+ *
+ * x, y: [T, H, D] with token and head strides; y == x (and equal strides)
+ * rotates in place, otherwise they do not overlap.  pos: int64 [T].
+ * D % 8 == 0, D <= 2048, offset % 8 == 0, offset + R <= D, R % 8 == 0
+ * (interleaved) or R % 16 == 0; T, H >= 0 (0 is a no-op).
+ */
+sgq_status sgq_rotary(const void* x, int64_t T, int64_t H, int64_t D, int64_t x_stride_t, int64_t x_stride_h,
+                      const int64_t* pos, const float* table, int64_t max_pos, int R, int64_t offset, int interleaved,
+                      int inverse, int dtype, void* y, int64_t y_stride_t, int64_t y_stride_h, sgq_stream_t stream);
+
+/*
+ * The step before attention, in one launch: rotates the positional parts of
+ * the queries (q [T, H, R] -> q_out) and of the keys (k [T, R]) and writes
+ * row [latent | rotated k] of every token into a paged cache.
+ *
+ * cache: [pages, page, L + R] with page and row strides; token t goes to
+ * page slots[t] / page, row slots[t] % page.  A negative slot is padding: no
+ * row is written.  Slots of one call are distinct.  k_out: the rotated keys
+ * [T, R], or NULL.  H = 0: no queries (q and q_out NULL).  q_out == q rotates
+ * in place.  L % 8 == 0, R as for sgq_rotary, R <= 256.
+ */
+sgq_status sgq_latent_append(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k, int64_t k_stride,
+                             const void* latent, int64_t latent_stride, const int64_t* pos, const int64_t* slots,
+                             const float* table, int64_t max_pos, int64_t T, int64_t H, int64_t L, int R,
+                             int interleaved, int dtype, void* q_out, int64_t qo_stride_t, int64_t qo_stride_h,
+                             void* k_out, int64_t ko_stride, void* cache, int64_t pages, int64_t page,
+                             int64_t cache_stride_page, int64_t cache_stride_row, sgq_stream_t stream);
+
+/*
+ * Absorbed latent attention over a paged cache: single tokens and chunks.
+ * Request b has query tokens q_starts[b] .. q_starts[b + 1] - 1 (q_starts
+ * NULL: token b alone, T == B) and kv_lens[b] cached rows, its own tokens'
+ * rows among them as the last ones.  Query token i of n sees rows
+ * j <= kv_lens[b] - n + i.  With c_j row j of the request,
+ *
+ *   out[t, h] = sum_j softmax_j(scale * q[t, h] . c_j) c_j[0 .. L)
+ *
+ * and lse[t, h] = log sum_j exp(scale * q[t, h] . c_j) (natural logarithm).
+ * A query token without a row to see gets zeros, and lse -inf.
+ *
+ * q: [T, H, L + R], every (token, head) row q_stride_row after the one
+ * before.  cache: as for sgq_latent_append.  page_table: int32, row b the
+ * page numbers of request b, table_width columns.  out: [T, H, L], lse: fp32
+ * [T, H] or NULL, both contiguous.  q_starts: int32 [B + 1], rising, ending
+ * at T.  L in {128, 256, 384, 512}; R % 8 == 0, 8 <= R <= 64; page % 16 == 0;
+ * H <= 65535.  Cached rows a token sees, and rows of the same 128 that some
+ * other token of its request sees, are finite; rows at kv_lens[b] and later
+ * may hold anything.
+ *
+ * workspace: device memory of at least sgq_latent_attention_workspace bytes,
+ * 16-byte aligned, that no other call uses until this one is done.  Nothing
+ * in it has to be set, and nothing in it is kept.
+ */
+sgq_status sgq_latent_attention_workspace(int64_t T, int64_t H, int64_t L, int64_t* bytes);
+sgq_status sgq_latent_attention(const void* q, int64_t q_stride_row, int64_t T, int64_t H, const void* cache,
+                                int64_t pages, int64_t page, int64_t cache_stride_page, int64_t cache_stride_row,
+                                int64_t L, int R, const int32_t* page_table, int64_t table_width, int64_t B,
+                                const int32_t* kv_lens, const int32_t* q_starts, float scale, int dtype, void* out,
+                                float* lse, void* workspace, int64_t workspace_bytes, sgq_stream_t stream);
+
+/*
+ * Expanded latent attention for ragged prompts: request b's queries are rows
+ * q_starts[b] .. q_starts[b + 1] - 1 of q, its keys and values rows
+ * kv_starts[b] .. kv_starts[b + 1] - 1.  Head h's key j is
+ * [k[j, h] | k_rot[j]] (the rotated part is shared by all heads):
+ *
+ *   out[i, h] = sum_j softmax_j(scale * (q[i, h, 0 .. N) . k[j, h]
+ *                                        + q[i, h, N .. N + R) . k_rot[j])) v[j, h]
+ *
+ * over j <= m - n + i (causal = 1; n queries, m keys) or all j (causal = 0).
+ * A query without a key to see gets zeros, and lse -inf.
+ *
+ * q: [T, H, N + R]; k, v: [S, H, N]; k_rot: [S, R]; token (and head) strides.
+ * out: [T, H, N], lse: fp32 [T, H] or NULL, both contiguous.  q_starts,
+ * kv_starts: int32 [B + 1], rising, ending at T and S.  N in {64, 128};
+ * R % 8 == 0, 8 <= R <= 64; H <= 65535.  All rows of k, v and k_rot that
+ * belong to a request are finite.
+ */
+sgq_status sgq_latent_prefill(const void* q, int64_t q_stride_t, int64_t q_stride_h, int64_t T, const void* k,
+                              int64_t k_stride_t, int64_t k_stride_h, const void* k_rot, int64_t kr_stride,
+                              const void* v, int64_t v_stride_t, int64_t v_stride_h, int64_t S, int64_t H, int64_t N,
+                              int R, const int32_t* q_starts, const int32_t* kv_starts, int64_t B, float scale,
+                              int causal, int dtype, void* out, float* lse, sgq_stream_t stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char* sgq_status_string(sgq_status s);
 
