@@ -1,178 +1,861 @@
-// Latent attention, absorbed (paged cache) and expanded (ragged prompts):
-// a simple form, one warp for each (query token, head).
+// Absorbed latent attention over a paged cache, for sm_103a.
 //
-// Softmax in one pass with a running maximum m and sum l: a key with score s
-// (in powers of two) turns (m, l, o) into (m', l 2^(m-m') + 2^(s-m'),
-// o 2^(m-m') + 2^(s-m') v), m' = max(m, s).  Lane i holds elements i, i + 32,
-// ... of a row, so a key costs one row read and one warp sum.
+// All heads and all new tokens of a request read the same rows c_j of the
+// cache, so a block of `NR` (token, head) rows q_i and a tile of 128 cached
+// rows make two matrix products, written with the cache on the MMA's 128-row
+// side and the queries on its N side (so few heads cost few columns):
+//     S^T [128 tokens, NR] = C Q^T          over L + R columns
+//     O^T [L, NR]         += C[:, :L]^T P^T over 128 tokens
+// Softmax keeps a reference m and a sum l for every row i: p = 2^(s - m)
+// with s in powers of two.  m follows the running maximum only when that has
+// grown by more than 2^8: p then stays below 2^8, every sum is a sum of
+// positive terms in fp32 with the same reference, and the accumulator in TMEM
+// is rescaled only on those steps.  P is rounded once, to the cache's type,
+// as the second product's operand; l sums the unrounded p.
+//
+// What bounds it: a tile is 147 KB of cache (L + R = 576), 22 us of HBM time
+// for 151 MB; the MMAs of a tile take 68 steps of about 36 (NR = 16) to 48
+// cycles (NR = 64: the operands' shared-memory reads), which is below a tile's
+// share of HBM time for up to 64 rows.
+//
+// Layout.  A tile sits in shared memory once, as chunks of 128 rows x 64
+// columns with 128-byte swizzle: read K-major for S^T and, by the descriptor's
+// other operand order, MN-major for O^T.  Chunks of the latent part come in
+// pairs (128 columns, one MMA's M) through a ring; the rotated part has a slot
+// of its own, which takes P once S^T is done.  Warps: 0 loads (TMA, one box a
+// run of rows inside a page), 1 issues MMAs, 2 to 9 do softmax: thread = token,
+// two warps a TMEM lane quarter, half of the columns each.
+//
+// Work: the tiles of all (request, row block) items, in order, are cut into
+// equal runs, one a CTA, from the lengths on the device.  An item that a cut
+// splits leaves fp32 partial sums, which a second kernel joins in order: the
+// result does not depend on timing.
+#include <cuda.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <type_traits>
 
 #include "latent_common.cuh"
+#include "latent_ptx.cuh"
 #include "sgq_internal.h"
 
 namespace sgq {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kMaxPer = 18;   // (512 + 64) / 32 elements a lane
+using lat::Pair;
 
-template <typename T>
-__device__ __forceinline__ float to_f(T v);
-template <>
-__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <>
-__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
-template <typename T>
-__device__ __forceinline__ T from_f(float v);
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __float2bfloat16_rn(v); }
-template <>
-__device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
+constexpr int kThreads = 320;
+constexpr int kTile = 128;                    // cached rows a tile
+constexpr int kChunkBytes = kTile * 128;      // 64 columns of a tile
+constexpr int kMaxPairs = 5, kMaxRope = 2;
+constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
+constexpr float kGrow = 8.0f;                 // powers of two the maximum may outgrow the reference by
 
-struct RowState {
-    float q[kMaxPer], o[kMaxPer], m = -INFINITY, l = 0.0f;
+template <int NR>
+struct Cfg {
+    static constexpr int kPairs = NR == 64 ? 4 : 5;
+    static constexpr int kRope = NR == 16 ? 2 : 1;
+    static constexpr int kQChunk = NR * 128;
+    static constexpr int kOffRope = kPairs * 2 * kChunkBytes;
+    static constexpr int kOffQ = kOffRope + kRope * kChunkBytes;
+    static constexpr int kOffMisc = kOffQ + 9 * kQChunk;
+    static constexpr int kMisc = 2560;                     // barriers, schedule, statistics
+    static constexpr int kSmem = kOffMisc + kMisc + 1024;  // alignment slack
+    static constexpr int kHalf = NR / 2;                   // columns a softmax warp
+    static constexpr int kRowBytes = NR * 2;               // a token's row of P
+    static constexpr uint32_t kColS = 4 * NR;
+    static_assert(kSmem <= 232448, "shared memory");
 };
-__device__ __forceinline__ void take(RowState& r, const float (&k)[kMaxPer], const float (&v)[kMaxPer], float scale2) {
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kMaxPer; ++i) s = fmaf(r.q[i], k[i], s);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-    s *= scale2;
-    const float m = fmaxf(r.m, s);
-    const float a = exp2f(r.m - m), p = exp2f(s - m);
-    r.l = r.l * a + p;
-#pragma unroll
-    for (int i = 0; i < kMaxPer; ++i) r.o[i] = r.o[i] * a + p * v[i];
-    r.m = m;
+
+struct Args {
+    const int32_t* table;
+    const int32_t* kv_lens;
+    const int32_t* q_starts;
+    void* out;
+    float* lse;
+    float* partial;      // [2 grid][NR][L]
+    float2* stats;       // [2 grid][NR]: reference, sum
+    int4* joins;         // [grid]: first row, rows, parts (0: nothing to join)
+    uint32_t* status;
+    int64_t T, B, pages, width;
+    int H, L, R, page, box;
+    int tpn, hb;         // tokens an item, items a token (one of them is 1)
+    float scale2;        // scale log2(e)
+};
+
+// One request: its query tokens [t0, t0 + n) and cached rows m.
+struct Request {
+    int64_t t0;
+    int n, m;
+};
+__device__ __forceinline__ Request request(const Args& a, int64_t b, bool report) {
+    Request r;
+    if (a.q_starts == nullptr) {
+        r.t0 = b;
+        r.n = 1;
+    } else {
+        const int64_t s = a.q_starts[b], e = a.q_starts[b + 1];
+        r.t0 = min(max(s, int64_t(0)), a.T);
+        r.n = static_cast<int>(min(max(e, r.t0), a.T) - r.t0);
+        if (report && (r.t0 != s || r.t0 + r.n != e || (b == 0 && s != 0) || (b == a.B - 1 && e != a.T)))
+            atomicOr(a.status, kStatusBadValue);
+    }
+    const int64_t m = a.kv_lens[b], most = a.width * a.page;
+    r.m = static_cast<int>(min(max(m, int64_t(0)), most));
+    if (report && r.m != m) atomicOr(a.status, kStatusBadValue);
+    return r;
 }
-template <typename T>
-__device__ __forceinline__ void finish(const RowState& r, T* out, int width, float* lse) {
-    const int lane = threadIdx.x & 31;
-    const float inv = r.l > 0.0f ? 1.0f / r.l : 0.0f;
-#pragma unroll
-    for (int i = 0; i < kMaxPer; ++i)
-        if (lane + 32 * i < width) out[lane + 32 * i] = from_f<T>(r.o[i] * inv);
-    if (lse != nullptr && lane == 0) *lse = r.l > 0.0f ? r.m * 0.69314718055994531f + logf(r.l) : -INFINITY;
+// Rows of the cache that token t of the request sees, and the tiles of the
+// token block i (its last token's rows; at least one tile, so that every item
+// is visited and writes its result).
+__device__ __forceinline__ int sees(const Request& r, int t) { return max(0, r.m - r.n + t + 1); }
+__device__ __forceinline__ int tiles(const Request& r, int tpn, int i) {
+    return max(1, (sees(r, min((i + 1) * tpn, r.n) - 1) + kTile - 1) / kTile);
+}
+// First token block whose tile count exceeds that of block i (or the number of blocks).
+__device__ __forceinline__ int next_step(const Request& r, int tpn, int blocks, int c) {
+    // block i counts more than c tiles from (i + 1) tpn > 128 c - (m - n) on
+    const int64_t last = (int64_t(c) * kTile - (r.m - r.n)) / tpn;
+    return static_cast<int>(min(int64_t(blocks), max(last, int64_t(0))));
+}
+__device__ __forceinline__ int64_t request_tiles(const Request& r, const Args& a) {
+    const int blocks = (r.n + a.tpn - 1) / a.tpn;
+    int64_t sum = 0;
+    for (int i = 0; i < blocks;) {
+        const int c = tiles(r, a.tpn, i);
+        const int e = max(next_step(r, a.tpn, blocks, c), i + 1);
+        sum += int64_t(c) * (e - i);
+        i = e;
+    }
+    return sum * a.hb;
 }
 
-// The request that token t belongs to, in [0, B); starts clamped to [0, T].
-__device__ __forceinline__ int64_t request_of(const int32_t* starts, int64_t B, int64_t t) {
-    int64_t lo = 0, hi = B;
-    while (hi - lo > 1) {
-        const int64_t mid = (lo + hi) / 2;
-        if (starts[mid] <= t) lo = mid;
-        else hi = mid;
-    }
-    return lo;
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kWarps * 32) latent_attention_simple(const LatentArgs a) {
-    const int64_t row = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (row >= a.T * a.H) return;
-    const int64_t t = row / a.H;
-    int64_t b = t, i = 0, n = 1;
-    if (a.q_starts != nullptr) {
-        b = request_of(a.q_starts, a.B, t);
-        i = t - a.q_starts[b];
-        n = a.q_starts[b + 1] - a.q_starts[b];
-    }
-    int64_t len = a.kv_lens[b];
-    if (len < 0 || len > a.table_width * a.page) {
-        if (lane == 0) atomicOr(a.status, kStatusBadValue);
-        len = len < 0 ? 0 : a.table_width * a.page;
-    }
-    const int W = a.L + a.R;
-    RowState r;
-    const T* q = static_cast<const T*>(a.q) + row * a.q_row;
-#pragma unroll
-    for (int e = 0; e < kMaxPer; ++e) {
-        r.q[e] = lane + 32 * e < W ? to_f(q[lane + 32 * e]) : 0.0f;
-        r.o[e] = 0.0f;
-    }
-    const int64_t end = min(len, len - n + i + 1);
-    for (int64_t j = 0; j < end; ++j) {
-        const int64_t page = a.page_table[b * a.table_width + j / a.page];
-        if (page < 0 || page >= a.pages) {
-            if (lane == 0) atomicOr(a.status, kStatusBadValue);
-            continue;
+// A CTA's run of tiles: item (b, block, head block), tile `at` of its `count`.
+struct Walk {
+    int64_t b;
+    int block, hblk, at, count;
+    int64_t left;        // tiles of the run from here on
+    Request r;
+    __device__ __forceinline__ void settle(const Args& a) { count = tiles(r, a.tpn, block); }
+    __device__ __forceinline__ int end() const { return static_cast<int>(min(int64_t(count), at + left)); }
+    __device__ __forceinline__ bool next(const Args& a) {
+        left -= end() - at;
+        if (left <= 0) return false;
+        at = 0;
+        if (++hblk == a.hb) {
+            hblk = 0;
+            if (++block * a.tpn >= r.n) {
+                block = 0;
+                do {
+                    if (++b >= a.B) return false;
+                    r = request(a, b, false);
+                } while (r.n == 0);
+            }
+            settle(a);
         }
-        const T* c = static_cast<const T*>(a.cache) + page * a.c_page + (j % a.page) * a.c_row;
-        float k[kMaxPer];
-#pragma unroll
-        for (int e = 0; e < kMaxPer; ++e) k[e] = lane + 32 * e < W ? to_f(c[lane + 32 * e]) : 0.0f;
-        take(r, k, k, a.scale * 1.44269504088896341f);
+        return true;
     }
-    finish(r, static_cast<T*>(a.out) + row * a.L, a.L, a.lse ? a.lse + row : nullptr);
+    __device__ __forceinline__ int64_t row0(const Args& a) const {
+        return (r.t0 + int64_t(block) * a.tpn) * a.H + hblk * ((a.H + a.hb - 1) / a.hb);
+    }
+    __device__ __forceinline__ int rows(const Args& a) const {
+        if (a.hb == 1) return min(a.tpn, r.n - block * a.tpn) * a.H;
+        const int per = (a.H + a.hb - 1) / a.hb;
+        return min(per, a.H - hblk * per);
+    }
+};
+
+struct Shared {
+    uint64_t full[kMaxPairs], empty[kMaxPairs], rope_full[kMaxRope], rope_empty[kMaxRope];
+    uint64_t q_full, q_empty, s_full, p_full, o_full, drain;
+    uint32_t tmem, abort;
+    // the schedule: totals of the threads' requests, then the CTA's start
+    int64_t b, per, total;
+    int block, hblk, at, pad;
+    int64_t warp_sum[kThreads / 32];
+    float top[2][4][32], sum[2][4][32];   // [column half][lane quarter][column]
+};
+static_assert(sizeof(Shared) <= Cfg<16>::kMisc, "statistics");
+
+// Where this CTA's run starts; every thread takes part.  Thread i adds up the
+// requests [i k, (i + 1) k); the one whose span holds the start walks it again.
+__device__ __forceinline__ void plan(const Args& a, Shared& sh) {
+    const int64_t k = (a.B + kThreads - 1) / kThreads;
+    const int64_t b0 = min(a.B, threadIdx.x * k), b1 = min(a.B, b0 + k);
+    int64_t mine = 0;
+    for (int64_t b = b0; b < b1; ++b) mine += request_tiles(request(a, b, blockIdx.x == 0), a);
+    int64_t scan = mine;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t up = __shfl_up_sync(0xFFFFFFFFu, scan, o);
+        if (lane >= o) scan += up;
+    }
+    if (lane == 31) sh.warp_sum[warp] = scan;
+    __syncthreads();
+    int64_t total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) scan += sh.warp_sum[w];
+        total += sh.warp_sum[w];
+    }
+    const int64_t per = (total + gridDim.x - 1) / gridDim.x;
+    const int64_t start = per * blockIdx.x;
+    int64_t at = scan - mine;
+    if (start >= at && start < scan) {
+        for (int64_t b = b0; b < b1; ++b) {
+            const Request r = request(a, b, false);
+            const int64_t n = request_tiles(r, a);
+            if (start >= at + n) {
+                at += n;
+                continue;
+            }
+            const int blocks = (r.n + a.tpn - 1) / a.tpn;
+            int i = 0, c = 1;
+            while (i < blocks) {
+                c = tiles(r, a.tpn, i);
+                const int e = max(next_step(r, a.tpn, blocks, c), i + 1);
+                const int64_t span = int64_t(c) * (e - i) * a.hb;
+                if (start < at + span) break;
+                at += span;
+                i = e;
+            }
+            const int64_t item = (start - at) / c;
+            sh.b = b;
+            sh.block = i + static_cast<int>(item / a.hb);
+            sh.hblk = static_cast<int>(item % a.hb);
+            sh.at = static_cast<int>((start - at) % c);
+            break;
+        }
+    }
+    if (threadIdx.x == 0) {
+        sh.per = per;
+        sh.total = total;
+    }
+    __syncthreads();
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kWarps * 32) latent_prefill_simple(const PrefillArgs a) {
-    const int64_t row = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+// The columns' sums over the 32 lanes, column c of the N in lane c (and c + N ...).
+template <int N>
+__device__ __forceinline__ float lane_sums(float (&v)[N]) {
     const int lane = threadIdx.x & 31;
-    if (row >= a.T * a.H) return;
-    const int64_t t = row / a.H, h = row % a.H;
-    const int64_t b = request_of(a.q_starts, a.B, t);
-    const int64_t i = t - a.q_starts[b], n = a.q_starts[b + 1] - a.q_starts[b];
-    const int64_t k0 = min(max(int64_t(a.kv_starts[b]), int64_t(0)), a.S);
-    const int64_t m = min(max(int64_t(a.kv_starts[b + 1]), k0), a.S) - k0;
-    const int W = a.N + a.R;
-    RowState r;
-    const T* q = static_cast<const T*>(a.q) + t * a.q_t + h * a.q_h;
 #pragma unroll
-    for (int e = 0; e < kMaxPer; ++e) {
-        r.q[e] = lane + 32 * e < W ? to_f(q[lane + 32 * e]) : 0.0f;
-        r.o[e] = 0.0f;
-    }
-    const int64_t end = a.causal ? min(m, m - n + i + 1) : m;
-    for (int64_t j = k0; j < k0 + end; ++j) {
-        const T* kp = static_cast<const T*>(a.k) + j * a.k_t + h * a.k_h;
-        const T* rp = static_cast<const T*>(a.k_rot) + j * a.kr_t - a.N;
-        const T* vp = static_cast<const T*>(a.v) + j * a.v_t + h * a.v_h;
-        float k[kMaxPer], v[kMaxPer];
+    for (int o = 16; o >= N; o >>= 1)
 #pragma unroll
-        for (int e = 0; e < kMaxPer; ++e) {
-            const int c = lane + 32 * e;
-            k[e] = c < a.N ? to_f(kp[c]) : (c < W ? to_f(rp[c]) : 0.0f);
-            v[e] = c < a.N ? to_f(vp[c]) : 0.0f;
+        for (int j = 0; j < N; ++j) v[j] += __shfl_xor_sync(0xFFFFFFFFu, v[j], o);
+#pragma unroll
+    for (int o = N / 2; o >= 1; o >>= 1) {
+        const bool up = (lane & o) != 0;
+#pragma unroll
+        for (int j = 0; j < o; ++j) {
+            const float send = up ? v[j] : v[j + o];
+            const float keep = up ? v[j + o] : v[j];
+            v[j] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, o);
         }
-        take(r, k, v, a.scale * 1.44269504088896341f);
     }
-    finish(r, static_cast<T*>(a.out) + row * a.N, a.N, a.lse ? a.lse + row : nullptr);
+    return v[0];
+}
+
+template <typename T, int NR>
+__global__ void __launch_bounds__(kThreads, 1)
+    latent_attention_kernel(const __grid_constant__ CUtensorMap tm_cache, const __grid_constant__ CUtensorMap tm_q,
+                            const Args a) {
+    using C = Cfg<NR>;
+    constexpr int HC = C::kHalf;
+    constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+    extern __shared__ uint8_t raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    Shared& sh = *reinterpret_cast<Shared*>(smem + C::kOffMisc);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const lat::Sync sync{&sh.abort, a.status};
+    auto bar = [](uint64_t& b) { return ptx::smem_u32(&b); };
+    const uint32_t s_pairs = ptx::smem_u32(smem), s_rope = s_pairs + C::kOffRope, s_q = s_pairs + C::kOffQ;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kPairs; ++i) {
+            ptx::mbar_init(bar(sh.full[i]), 1);
+            ptx::mbar_init(bar(sh.empty[i]), 1);
+        }
+        for (int i = 0; i < C::kRope; ++i) {
+            ptx::mbar_init(bar(sh.rope_full[i]), 1);
+            ptx::mbar_init(bar(sh.rope_empty[i]), 1);
+        }
+        ptx::mbar_init(bar(sh.q_full), 1);
+        ptx::mbar_init(bar(sh.q_empty), 1);
+        ptx::mbar_init(bar(sh.s_full), 1);
+        ptx::mbar_init(bar(sh.p_full), 8);
+        ptx::mbar_init(bar(sh.o_full), 1);
+        ptx::mbar_init(bar(sh.drain), 1);
+        sh.abort = 0;
+        ptx::fence_mbar_init();
+        ptx::prefetch_tmap(&tm_cache);
+        ptx::prefetch_tmap(&tm_q);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(ptx::smem_u32(&sh.tmem), 512);
+        ptx::tmem_relinquish();
+    }
+    ptx::launch_dependents();
+    ptx::grid_dependency_wait();
+    ptx::tc_fence_before();
+    plan(a, sh);
+    ptx::tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    const int np = a.L / 128;                       // pairs of latent chunks a tile
+
+    if (threadIdx.x == 64) a.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
+    Walk w;
+    w.left = min(sh.per, sh.total - sh.per * blockIdx.x);
+    const bool any = w.left > 0;
+    if (any) {
+        w.b = sh.b;
+        w.block = sh.block;
+        w.hblk = sh.hblk;
+        w.at = sh.at;
+        w.r = request(a, w.b, false);
+        w.settle(a);
+    }
+
+    uint32_t pair = 0, rope = 0, seg = 0;            // slots and segments used so far
+    if (warp == 0 && any) {
+        // ------------------------------------------------------------ loads
+        bool ok = true;
+        do {
+            ok = lat::wait_warp(bar(sh.q_empty), (seg & 1u) ^ 1u, sync);
+            if (!ok) break;
+            ++seg;
+            if (lane == 0) {
+                ptx::mbar_arrive_expect_tx(bar(sh.q_full), (2 * np + 1) * C::kQChunk);
+                const int row = static_cast<int>(w.row0(a));
+                for (int c = 0; c <= 2 * np; ++c)
+                    ptx::tma_load_2d(s_q + c * C::kQChunk, &tm_q, c * 64, row, bar(sh.q_full));
+            }
+            const int end = w.end();
+            for (int tile = w.at; tile < end && ok; ++tile) {
+                const int rows = min(kTile, w.r.m - tile * kTile);
+                const int boxes = rows > 0 ? (rows + a.box - 1) / a.box : 0;
+                int page = 0, in_page = 0;
+                if (lane < boxes) {
+                    const int64_t j = int64_t(tile) * kTile + lane * a.box;
+                    page = __ldg(a.table + w.b * a.width + j / a.page);
+                    in_page = static_cast<int>(j % a.page);
+                    if (page < 0 || page >= a.pages) {   // nowhere: the box past the last page reads as zeros
+                        atomicOr(a.status, kStatusBadValue);
+                        page = static_cast<int>(a.pages);
+                    }
+                }
+                const uint32_t dst = lane * a.box * 128;
+                for (int p = 0; p <= np && ok; ++p) {
+                    const bool tail = p == np;
+                    const uint32_t n = tail ? rope : pair;
+                    const uint32_t slots = tail ? C::kRope : C::kPairs, slot = n % slots, phase = (n / slots) & 1u;
+                    ok = lat::wait_warp(bar(tail ? sh.rope_empty[slot] : sh.empty[slot]), phase ^ 1u, sync);
+                    if (!ok) break;
+                    const uint32_t full = bar(tail ? sh.rope_full[slot] : sh.full[slot]);
+                    if (lane == 0) ptx::mbar_arrive_expect_tx(full, boxes * a.box * (tail ? 128 : 256));
+                    __syncwarp();
+                    if (tail) {
+                        if (lane < boxes) lat::tma_load_3d(s_rope + slot * kChunkBytes + dst, &tm_cache, a.L, in_page, page, full);
+                        ++rope;
+                    } else {
+                        if (lane < boxes) {
+                            const uint32_t to = s_pairs + slot * 2 * kChunkBytes + dst;
+                            lat::tma_load_3d(to, &tm_cache, p * 128, in_page, page, full);
+                            lat::tma_load_3d(to + kChunkBytes, &tm_cache, p * 128 + 64, in_page, page, full);
+                        }
+                        ++pair;
+                    }
+                }
+            }
+        } while (ok && w.next(a));
+    } else if (warp == 1 && any) {
+        // ------------------------------------------------------------ MMAs
+        constexpr uint32_t kIdS = lat::idesc_f16(128, NR, kBf16, false, false);
+        constexpr uint32_t kIdO = lat::idesc_f16(128, NR, kBf16, true, true);
+        constexpr uint32_t kPLayout = lat::layout_of(C::kRowBytes);
+        const int rope_steps = (a.R + 15) / 16;
+        uint32_t tiles_done = 0;
+        bool ok = true;
+        do {
+            ok = lat::wait_warp(bar(sh.q_full), seg & 1u, sync);
+            if (!ok) break;
+            ++seg;
+            const int end = w.end();
+            for (int tile = w.at; tile < end; ++tile) {
+                const uint32_t first_pair = pair;
+                const uint32_t rope_slot = rope % C::kRope;
+                for (int p = 0; p <= np && ok; ++p) {
+                    const bool tail = p == np;
+                    const uint32_t n = tail ? rope : pair;
+                    const uint32_t slots = tail ? C::kRope : C::kPairs, slot = n % slots;
+                    ok = lat::wait_warp(bar(tail ? sh.rope_full[slot] : sh.full[slot]), (n / slots) & 1u, sync);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    if (lane == 0) {
+                        const uint32_t ka = tail ? s_rope + slot * kChunkBytes : s_pairs + slot * 2 * kChunkBytes;
+                        const uint64_t da = ptx::smem_desc(ka, 16, 1024, ptx::kLayoutSw128);
+                        const uint64_t db = ptx::smem_desc(s_q + p * 2 * C::kQChunk, 16, 1024, ptx::kLayoutSw128);
+                        const int steps = tail ? rope_steps : 8;
+                        for (int k = 0; k < steps; ++k)   // 16 columns: 32 bytes on, or the next chunk
+                            lat::mma_f16(tmem + C::kColS, da + (k >> 2) * (kChunkBytes >> 4) + (k & 3) * 2,
+                                         db + (k >> 2) * (C::kQChunk >> 4) + (k & 3) * 2, kIdS, p > 0 || k > 0);
+                    }
+                    __syncwarp();
+                    if (tail) ++rope;
+                    else ++pair;
+                }
+                if (!ok) break;
+                if (lane == 0) {
+                    ptx::tc_commit(bar(sh.s_full));
+                    if (tile + 1 == end) ptx::tc_commit(bar(sh.q_empty));
+                }
+                __syncwarp();
+                ok = lat::wait_warp(bar(sh.p_full), tiles_done & 1u, sync);
+                if (!ok) break;
+                ++tiles_done;
+                ptx::tc_fence_after();
+                if (lane == 0) {
+                    const uint64_t db = ptx::smem_desc(s_rope + rope_slot * kChunkBytes, 16, 8 * C::kRowBytes, kPLayout);
+                    for (int p = 0; p < np; ++p) {
+                        const uint32_t slot = (first_pair + p) % C::kPairs;
+                        const uint64_t da = ptx::smem_desc(s_pairs + slot * 2 * kChunkBytes, kChunkBytes, 1024, ptx::kLayoutSw128);
+                        for (int k = 0; k < kTile / 16; ++k)
+                            lat::mma_f16(tmem + p * NR, da + k * (2048 >> 4), db + k * ((16 * C::kRowBytes) >> 4), kIdO,
+                                         tile > w.at || k > 0);
+                        ptx::tc_commit(bar(sh.empty[slot]));
+                    }
+                    ptx::tc_commit(bar(sh.rope_empty[rope_slot]));
+                    if (tile + 1 == end) ptx::tc_commit(bar(sh.o_full));
+                }
+                __syncwarp();
+            }
+        } while (ok && w.next(a));
+    } else if (warp >= 2 && any) {
+        // ------------------------------------------------------------ softmax
+        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        const int row = quarter * 32 + lane;                      // token of the tile
+        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+        const uint32_t t_s = tmem + lanes + C::kColS + half * HC, t_o = tmem + lanes + half * HC;
+        const int id = 1 + half;
+        uint32_t tiles_done = 0;
+        bool ok = true;
+        do {
+            const int end = w.end();
+            const int first_token = w.block * a.tpn;
+            const int tokens = min(a.tpn, w.r.n - first_token);
+            const int low = sees(w.r, first_token);                // rows that every row of the block sees
+            float ref = -INFINITY, l[HC];                          // ref: of column `lane`
+#pragma unroll
+            for (int j = 0; j < HC; ++j) l[j] = 0.0f;
+            bool failed = false;
+            for (int tile = w.at; tile < end; ++tile) {
+                ok = lat::wait_warp(bar(sh.s_full), tiles_done & 1u, sync);
+                ++tiles_done;
+                ptx::tc_fence_after();
+                uint32_t raw_s[HC];
+                ptx::tmem_ld<HC>(t_s, raw_s);
+                ptx::tmem_wait_ld();
+                float x[HC];
+#pragma unroll
+                for (int j = 0; j < HC; ++j) x[j] = __uint_as_float(raw_s[j]) * a.scale2;
+                const int token = tile * kTile + row;
+                if ((tile + 1) * kTile > low) {
+                    // rows past the request's, and rows newer than a query token, are not seen
+#pragma unroll
+                    for (int j = 0; j < HC; ++j) {
+                        const int t = tokens == 1 ? 0 : (half * HC + j) / a.H;
+                        if (token >= sees(w.r, min(first_token + t, w.r.n - 1))) x[j] = -INFINITY;
+                    }
+                }
+                float top = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < HC; ++j) {
+                    const float m = lat::warp_max(x[j]);
+                    if ((lane & (HC - 1)) == j) top = m;
+                }
+                if (lane < HC) sh.top[half][quarter][lane] = top;
+                failed = lat::named_any(id, 128, !ok);
+                if (failed) break;
+                const float4 tops = make_float4(sh.top[half][0][lane & (HC - 1)], sh.top[half][1][lane & (HC - 1)],
+                                                sh.top[half][2][lane & (HC - 1)], sh.top[half][3][lane & (HC - 1)]);
+                top = fmaxf(fmaxf(tops.x, tops.y), fmaxf(tops.z, tops.w));
+                const bool grow = top > ref + kGrow || (ref == -INFINITY && top > -INFINITY);
+                if (__any_sync(0xFFFFFFFFu, grow)) {
+                    const float scale = grow ? lat::ex2(ref - top) : 1.0f;   // 0 where there was nothing before
+                    if (grow) ref = top;
+#pragma unroll
+                    for (int j = 0; j < HC; ++j) l[j] *= __shfl_sync(0xFFFFFFFFu, scale, j);
+                    if (tile > w.at) {
+                        for (int p = 0; p < np; ++p) {
+                            uint32_t o[HC];
+                            ptx::tmem_ld<HC>(t_o + p * NR, o);
+                            ptx::tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < HC; ++j)
+                                o[j] = __float_as_uint(__uint_as_float(o[j]) * __shfl_sync(0xFFFFFFFFu, scale, j));
+                            lat::tmem_st<HC>(t_o + p * NR, o);
+                        }
+                        lat::tmem_wait_st();
+                    }
+                }
+                const float base = ref == -INFINITY ? 0.0f : ref;
+                uint32_t packed[HC / 2];
+#pragma unroll
+                for (int j = 0; j < HC; j += 2) {
+                    const float p0 = lat::ex2(x[j] - __shfl_sync(0xFFFFFFFFu, base, j));
+                    const float p1 = lat::ex2(x[j + 1] - __shfl_sync(0xFFFFFFFFu, base, j + 1));
+                    l[j] += p0;
+                    l[j + 1] += p1;
+                    packed[j / 2] = Pair<T>::pack(p0, p1);
+                }
+                uint8_t* prow = smem + C::kOffRope + (rope % C::kRope) * kChunkBytes;
+#pragma unroll
+                for (int c = 0; c < HC / 8; ++c) {
+                    uint32_t off = row * C::kRowBytes + (half * HC / 8 + c) * 16;
+                    off ^= ((off >> 7) & (C::kRowBytes / 16 - 1)) << 4;
+                    *reinterpret_cast<uint4*>(prow + off) =
+                        make_uint4(packed[4 * c], packed[4 * c + 1], packed[4 * c + 2], packed[4 * c + 3]);
+                }
+                // Weights past the request's rows are zero, but 0 times what lies there need not be.
+                if (token >= w.r.m) {
+                    for (int c = half; c < 2 * np; c += 2) {
+                        uint4* z = reinterpret_cast<uint4*>(smem + ((pair + c / 2) % C::kPairs) * 2 * kChunkBytes +
+                                                            (c & 1) * kChunkBytes + row * 128);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) z[i] = make_uint4(0, 0, 0, 0);
+                    }
+                }
+                pair += np;
+                ++rope;
+                ptx::fence_proxy_async_smem();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar(sh.p_full));
+            }
+            if (failed) break;
+            // ---- the segment's result
+            const float mine = lane_sums<HC>(l);
+            if (lane < HC) sh.sum[half][quarter][lane] = mine;
+            ok = lat::wait_warp(bar(sh.o_full), seg & 1u, sync);
+            ++seg;
+            if (lat::named_any(id, 128, !ok)) break;
+            const int cl = lane & (HC - 1);
+            const float total = (sh.sum[half][0][cl] + sh.sum[half][1][cl]) + (sh.sum[half][2][cl] + sh.sum[half][3][cl]);
+            const int64_t row0 = w.row0(a);
+            const int rows = w.rows(a);
+            const int col = half * HC + cl;                        // of the statistics
+            const bool whole = w.at == 0 && end == w.count;
+            ptx::tc_fence_after();
+            if (whole) {
+                const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+                if (a.lse != nullptr && quarter == 0 && lane < HC && col < rows)
+                    a.lse[row0 + col] = total > 0.0f ? (ref + log2f(total)) * kLn2 : -INFINITY;
+                for (int p = 0; p < np; ++p) {
+                    uint32_t o[HC];
+                    ptx::tmem_ld<HC>(t_o + p * NR, o);
+                    ptx::tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < HC; j += 2) {
+                        // two rows, one element each -> one row, two elements: even lanes keep row j
+                        const float v0 = __uint_as_float(o[j]) * __shfl_sync(0xFFFFFFFFu, inv, j);
+                        const float v1 = __uint_as_float(o[j + 1]) * __shfl_sync(0xFFFFFFFFu, inv, j + 1);
+                        const bool odd = (lane & 1) != 0;
+                        const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? v0 : v1, 1);
+                        const int r = half * HC + j + (odd ? 1 : 0);
+                        if (r < rows)
+                            reinterpret_cast<uint32_t*>(a.out)[((row0 + r) * a.L + p * 128 + quarter * 32 + (lane & ~1)) >> 1] =
+                                odd ? Pair<T>::pack(got, v1) : Pair<T>::pack(v0, got);
+                    }
+                }
+            } else {
+                // The part that begins an item owns its joining: parts up to the CTA of the item's last tile.
+                if (w.at == 0 && threadIdx.x == 64)
+                    a.joins[blockIdx.x] = make_int4(static_cast<int>(row0), rows,
+                                                    static_cast<int>((w.count - w.left + sh.per - 1) / sh.per) + 1, 0);
+                const int64_t part = 2 * int64_t(blockIdx.x) + (w.at > 0 ? 0 : 1);
+                if (quarter == 0 && lane < HC && col < rows) a.stats[part * NR + col] = make_float2(ref, total);
+                float* dst = a.partial + (part * NR + half * HC) * a.L + quarter * 32 + lane;
+                for (int p = 0; p < np; ++p) {
+                    uint32_t o[HC];
+                    ptx::tmem_ld<HC>(t_o + p * NR, o);
+                    ptx::tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < HC; ++j)
+                        if (half * HC + j < rows) dst[j * a.L + p * 128] = __uint_as_float(o[j]);
+                }
+            }
+            ptx::tc_fence_before();
+        } while (w.next(a));
+    }
+    __syncthreads();
+    if (sh.abort) {
+        // A wait ran out: copies in flight land and MMAs end (both bounded) before the CTA does.
+        const uint64_t t0 = ptx::globaltimer();
+        auto land = [&](uint64_t& b, uint32_t uses) {
+            while (uses > 0 && !ptx::mbar_test_wait(bar(b), (uses - 1) & 1u) && ptx::globaltimer() - t0 < (1ull << 26)) {}
+        };
+        if (warp == 0) {
+            for (uint32_t i = 0; i < C::kPairs; ++i) land(sh.full[i], pair / C::kPairs + (i < pair % C::kPairs ? 1 : 0));
+            for (uint32_t i = 0; i < C::kRope; ++i) land(sh.rope_full[i], rope / C::kRope + (i < rope % C::kRope ? 1 : 0));
+            land(sh.q_full, seg);
+        } else if (threadIdx.x == 32) {
+            ptx::tc_commit(bar(sh.drain));
+            land(sh.drain, 1);
+        }
+        __syncthreads();
+    }
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, 512);
+    }
+}
+
+// Joins the parts of the items that the cuts split: row r of part i holds an
+// unnormalised sum o_i with reference m_i and sum l_i, and
+//     out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i,  M = max m_i,
+// in the order of the parts.  A block takes whole rows: L / 4 threads across a
+// row, the others on other parts.
+constexpr int kJoinThreads = 256;
+constexpr int kMaxGrid = 512;
+template <typename T>
+__global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const Args a, int grid, int NR) {
+    ptx::launch_dependents();
+    ptx::grid_dependency_wait();
+    __shared__ int first[kMaxGrid + 1];
+    __shared__ float weight[kMaxGrid];
+    __shared__ float red[2][kJoinThreads / 32];
+    __shared__ float4 acc[kJoinThreads];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int run = 0;
+    for (int base = 0; base < grid; base += kJoinThreads) {   // prefix sums of the rows to join
+        const int c = base + threadIdx.x;
+        int4 j = make_int4(0, 0, 0, 0);
+        if (c < grid) j = a.joins[c];
+        int v = j.z > 0 ? j.y : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(0xFFFFFFFFu, v, o);
+            if (lane >= o) v += up;
+        }
+        int* sums = reinterpret_cast<int*>(red[0]);
+        __syncthreads();
+        if (lane == 31) sums[warp] = v;
+        __syncthreads();
+        int all = run;
+        for (int w = 0; w < kJoinThreads / 32; ++w) {
+            if (w < warp) v += sums[w];
+            all += sums[w];
+        }
+        if (c < grid) first[c + 1] = run + v;
+        run = all;
+    }
+    if (threadIdx.x == 0) first[0] = 0;
+    __syncthreads();
+    const int total = first[grid];
+    const int per_row = a.L / 4, groups = kJoinThreads / per_row;
+    const int group = threadIdx.x / per_row, at = threadIdx.x % per_row;
+    for (int u = blockIdx.x; u < total; u += gridDim.x) {
+        int lo = 0, hi = grid;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (first[mid] <= u) lo = mid;
+            else hi = mid;
+        }
+        // (CTAs without rows share their neighbour's prefix: the last one with first <= u has rows)
+        const int4 j = a.joins[lo];
+        const int r = u - first[lo], parts = j.z;
+        auto slot = [&](int i) { return (i == 0 ? int64_t(2) * lo + 1 : int64_t(2) * (lo + i)) * NR + r; };
+        float m = -INFINITY;
+        for (int i = threadIdx.x; i < parts; i += kJoinThreads) m = fmaxf(m, a.stats[slot(i)].x);
+        m = lat::warp_max(m);
+        if (lane == 0) red[0][warp] = m;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kJoinThreads / 32; ++w) m = fmaxf(m, red[0][w]);
+        float l = 0.0f;
+        for (int i = threadIdx.x; i < parts; i += kJoinThreads) {
+            const float2 s = a.stats[slot(i)];
+            const float f = s.x == -INFINITY ? 0.0f : lat::ex2(s.x - m);
+            weight[i] = f;
+            l += f * s.y;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+        if (lane == 0) red[1][warp] = l;
+        __syncthreads();
+        l = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kJoinThreads / 32; ++w) l += red[1][w];
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (group < groups) {
+#pragma unroll 8
+            for (int i = group; i < parts; i += groups) {
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(a.partial + slot(i) * a.L) + at);
+                const float f = weight[i];
+                if (f > 0.0f) {   // (a part without a row to see left nothing to add)
+                    o.x = fmaf(f, v.x, o.x);
+                    o.y = fmaf(f, v.y, o.y);
+                    o.z = fmaf(f, v.z, o.z);
+                    o.w = fmaf(f, v.w, o.w);
+                }
+            }
+            acc[threadIdx.x] = o;
+        }
+        __syncthreads();
+        if (group == 0) {
+            for (int g = 1; g < groups; ++g) {
+                const float4 v = acc[g * per_row + at];
+                o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
+            }
+            const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+            const int64_t row = int64_t(j.x) + r;
+            reinterpret_cast<uint2*>(a.out)[row * per_row + at] =
+                make_uint2(Pair<T>::pack(o.x * inv, o.y * inv), Pair<T>::pack(o.z * inv, o.w * inv));
+            if (a.lse != nullptr && at == 0) a.lse[row] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------- host
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }();
+    return fn;
+}
+
+// Rows (token, head) of a block: as many as a request has on average, up to 64.
+int row_block(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+
+struct Sizes {
+    int64_t partial, stats, joins, total;
+};
+Sizes workspace_of(int64_t grid, int64_t NR, int64_t L) {
+    Sizes s;
+    s.partial = 2 * grid * NR * L * 4;
+    s.stats = 2 * grid * NR * 8;
+    s.joins = grid * 16;
+    s.total = s.partial + s.stats + s.joins;
+    return s;
+}
+
+template <typename T, int NR>
+sgq_status run(const CUtensorMap& tm_cache, const CUtensorMap& tm_q, const Args& a, int grid, int join_grid,
+               cudaStream_t st) {
+    auto kern = latent_attention_kernel<T, NR>;
+    static bool configured[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SGQ_ERR_CUDA;
+    if (!configured[dev]) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<NR>::kSmem) != cudaSuccess)
+            return SGQ_ERR_CUDA;
+        configured[dev] = true;
+    }
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Cfg<NR>::kSmem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kern, tm_cache, tm_q, a) != cudaSuccess) return SGQ_ERR_CUDA;
+    note_launch();
+    if (grid == 1) return SGQ_OK;   // nothing is split
+    cfg.gridDim = dim3(static_cast<unsigned>(join_grid));
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.dynamicSmemBytes = 0;
+    if (cudaLaunchKernelEx(&cfg, latent_join_kernel<T>, a, grid, NR) != cudaSuccess) return SGQ_ERR_CUDA;
+    note_launch();
+    return SGQ_OK;
+}
+template <typename T>
+sgq_status run_rows(int NR, const CUtensorMap& tm_cache, const CUtensorMap& tm_q, const Args& a, int grid,
+                    int join_grid, cudaStream_t st) {
+    if (NR == 16) return run<T, 16>(tm_cache, tm_q, a, grid, join_grid, st);
+    if (NR == 32) return run<T, 32>(tm_cache, tm_q, a, grid, join_grid, st);
+    return run<T, 64>(tm_cache, tm_q, a, grid, join_grid, st);
 }
 
 }  // namespace
 
-sgq_status latent_attention_workspace(int64_t, int64_t, int64_t, int64_t* bytes) {
-    *bytes = 16;
+sgq_status latent_attention_workspace(int64_t T, int64_t H, int64_t L, int64_t* bytes) {
+    DeviceInfo di;
+    const sgq_status rc = device_info(&di);
+    if (rc != SGQ_OK) return rc;
+    *bytes = workspace_of(std::min(di.sm_count, kMaxGrid), row_block(T * H), L).total;
     return SGQ_OK;
 }
 
-sgq_status launch_latent_attention(const LatentArgs& args, cudaStream_t st) {
-    LatentArgs a = args;
-    const sgq_status rc = gemm::status_word(&a.status);
+sgq_status launch_latent_attention(const LatentArgs& x, cudaStream_t st) {
+    DeviceInfo di;
+    sgq_status rc = device_info(&di);
     if (rc != SGQ_OK) return rc;
-    const unsigned blocks = static_cast<unsigned>((a.T * a.H + kWarps - 1) / kWarps);
-    if (a.dtype == SGQ_BF16) latent_attention_simple<__nv_bfloat16><<<blocks, kWarps * 32, 0, st>>>(a);
-    else latent_attention_simple<__half><<<blocks, kWarps * 32, 0, st>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return SGQ_ERR_CUDA;
-    note_launch();
-    return SGQ_OK;
-}
+    if (di.cc_major != 10 || encoder() == nullptr) return SGQ_ERR_UNSUPPORTED;
+    Args a{};
+    rc = gemm::status_word(&a.status);
+    if (rc != SGQ_OK) return rc;
+    const int NR = row_block((x.T + x.B - 1) / x.B * x.H);
+    a.table = x.page_table;
+    a.kv_lens = x.kv_lens;
+    a.q_starts = x.q_starts;
+    a.out = x.out;
+    a.lse = x.lse;
+    a.T = x.T;
+    a.B = x.B;
+    a.pages = x.pages;
+    a.width = x.table_width;
+    a.H = x.H;
+    a.L = x.L;
+    a.R = x.R;
+    a.page = x.page;
+    a.box = std::min(x.page & -x.page, kTile);   // rows of a box: whole boxes in a page and in a tile
+    a.tpn = std::max(1, NR / x.H);
+    a.hb = (x.H + NR - 1) / NR;
+    a.scale2 = x.scale * kLog2e;
+    // No more CTAs than the tables could hold tiles.
+    const int64_t most = (x.T + x.B) * a.hb * std::max<int64_t>(1, (x.table_width * x.page + kTile - 1) / kTile);
+    const int grid = static_cast<int>(std::min<int64_t>(std::min(di.sm_count, kMaxGrid), most));
+    const Sizes s = workspace_of(grid, NR, x.L);
+    char* ws = static_cast<char*>(x.workspace);
+    a.partial = reinterpret_cast<float*>(ws);
+    a.stats = reinterpret_cast<float2*>(ws + s.partial);
+    a.joins = reinterpret_cast<int4*>(ws + s.partial + s.stats);
 
-sgq_status launch_latent_prefill(const PrefillArgs& args, cudaStream_t st) {
-    PrefillArgs a = args;
-    const sgq_status rc = gemm::status_word(&a.status);
-    if (rc != SGQ_OK) return rc;
-    const int64_t blocks = (a.T * a.H + kWarps - 1) / kWarps;
-    if (blocks > INT32_MAX) return SGQ_ERR_INVALID_ARG;
-    if (a.dtype == SGQ_BF16) latent_prefill_simple<__nv_bfloat16><<<blocks, kWarps * 32, 0, st>>>(a);
-    else latent_prefill_simple<__half><<<blocks, kWarps * 32, 0, st>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return SGQ_ERR_CUDA;
-    note_launch();
-    return SGQ_OK;
+    const cuuint32_t ones[3] = {1, 1, 1};
+    const cuuint64_t W = static_cast<cuuint64_t>(x.L + x.R);
+    CUtensorMap tm_cache, tm_q;
+    {
+        const cuuint64_t dims[3] = {W, static_cast<cuuint64_t>(x.page), static_cast<cuuint64_t>(x.pages)};
+        const cuuint64_t strides[2] = {static_cast<cuuint64_t>(x.c_row) * 2, static_cast<cuuint64_t>(x.c_page) * 2};
+        const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(a.box), 1};
+        if (encoder()(&tm_cache, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(x.cache), dims, strides, box, ones,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return SGQ_ERR_CUDA;
+    }
+    {
+        const cuuint64_t dims[2] = {W, static_cast<cuuint64_t>(x.T * x.H)};
+        const cuuint64_t strides[1] = {static_cast<cuuint64_t>(x.q_row) * 2};
+        const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(NR)};
+        if (encoder()(&tm_q, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(x.q), dims, strides, box, ones,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return SGQ_ERR_CUDA;
+    }
+    const int join_grid = di.sm_count * 4;
+    return x.dtype == SGQ_BF16 ? run_rows<__nv_bfloat16>(NR, tm_cache, tm_q, a, grid, join_grid, st)
+                               : run_rows<__half>(NR, tm_cache, tm_q, a, grid, join_grid, st);
 }
 
 }  // namespace sgq

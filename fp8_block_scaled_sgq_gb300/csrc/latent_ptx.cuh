@@ -1,0 +1,136 @@
+// Inline PTX of the latent-attention kernels beyond ptx.cuh: 16-bit MMAs with
+// either operand order, TMEM stores, TMA boxes of three dimensions, and the
+// shared bounded wait.
+#pragma once
+#include <cstdint>
+
+#include "ptx.cuh"
+
+namespace sgq {
+namespace lat {
+
+// D[tmem] (+)= A[smem] B[smem]^T, 16-bit operands, fp32 accumulator.
+__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// The same with A in TMEM (row i in lane i, two elements a 32-bit column).
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Instruction descriptor, kind::f16: fp32 D; both operands bf16 or both fp16;
+// an operand is K-major, or MN-major where its flag is set.
+__host__ __device__ constexpr uint32_t idesc_f16(uint32_t M, uint32_t N, bool bf16, bool a_mn, bool b_mn) {
+    return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((a_mn ? 1u : 0u) << 15) |
+           ((b_mn ? 1u : 0u) << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+// Descriptor layout code of a row of 128, 64 or 32 bytes (its swizzle span).
+__host__ __device__ constexpr uint32_t layout_of(uint32_t row_bytes) {
+    return row_bytes == 128 ? 2u : row_bytes == 64 ? 4u : 6u;
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, int32_t x, int32_t y, int32_t z,
+                                            uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+// 32 lanes x N consecutive 32-bit columns; thread t writes lane (base_lane + t).
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[N]);
+template <>
+__device__ __forceinline__ void tmem_st<8>(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+        : "memory");
+}
+template <>
+__device__ __forceinline__ void tmem_st<16>(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+template <>
+__device__ __forceinline__ void tmem_st<32>(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 2^x (flushing tiny results to zero); 2^-inf = 0.
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// Maximum over the warp, in every lane.
+__device__ __forceinline__ float warp_max(float x) {
+    float y;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void named_sync(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// The same barrier with a vote: true where some thread passes true.
+__device__ __forceinline__ bool named_any(int id, int threads, bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n.reg .pred p, q;\nsetp.ne.u32 q, %3, 0;\n"
+        "bar.red.or.pred p, %1, %2, q;\nselp.u32 %0, 1, 0, p;\n}"
+        : "=r"(r)
+        : "r"(id), "r"(threads), "r"(x ? 1u : 0u)
+        : "memory");
+    return r != 0u;
+}
+
+// Bounded waits: a wait that runs out raises the CTA's abort flag and the
+// device status; every other wait of the CTA then gives up as well.
+constexpr uint32_t kStatusTimeout = 1u;
+constexpr uint64_t kTimeoutNs = 2000000000ull;
+constexpr uint64_t kAbortPollNs = 1000000ull;
+struct Sync {
+    volatile uint32_t* abort_flag;
+    uint32_t* status;
+};
+static __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, const Sync& s) {
+    const uint64_t t0 = ptx::globaltimer();
+    for (uint32_t spins = 1;; ++spins) {
+        if (ptx::mbar_try_wait(bar, parity)) return true;
+        if ((spins & 15u) == 0) {
+            const uint64_t dt = ptx::globaltimer() - t0;
+            if (dt > kAbortPollNs && *s.abort_flag) return false;
+            if (dt > kTimeoutNs) {
+                *s.abort_flag = 1u;
+                atomicOr(s.status, kStatusTimeout);
+                return false;
+            }
+        }
+    }
+}
+// The whole warp waits for a phase; false: gave up.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const Sync& s) {
+    uint32_t ok = 1;
+    if ((threadIdx.x & 31) == 0 && !ptx::mbar_try_wait(bar, parity)) ok = wait_slow(bar, parity, s) ? 1u : 0u;
+    ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+    __syncwarp();
+    return ok != 0;
+}
+
+}  // namespace lat
+}  // namespace sgq
