@@ -292,7 +292,7 @@ sgq_status sgq_latent_attention(const void* q, int64_t q_stride_row, int64_t T, 
                                 float* lse, void* workspace, int64_t workspace_bytes, sgq_stream_t stream) {
     if (T < 0 || B < 0 || H <= 0 || H > 65535 || T * H >= (int64_t(1) << 31) || B >= (int64_t(1) << 31) || L <= 0 ||
         L % 128 != 0 || L > 512 || R < 8 || R > 64 || R % 8 != 0 || !good_dtype(dtype) ||
-        !good_strides({q_stride_row, cache_stride_page, cache_stride_row}) || !std::isfinite(scale))
+        !good_strides({q_stride_row, cache_stride_page, cache_stride_row}) || !(std::isfinite(scale) && scale > 0.0f))
         return SGQ_ERR_INVALID_ARG;
     if (pages <= 0 || pages >= (int64_t(1) << 31) || page <= 0 || page % 16 != 0 || page >= (int64_t(1) << 31) ||
         table_width < 0 || table_width * page >= (int64_t(1) << 31) || q_stride_row < L + R ||
@@ -326,7 +326,7 @@ sgq_status sgq_latent_prefill(const void* q, int64_t q_stride_t, int64_t q_strid
     if (T < 0 || S < 0 || B < 0 || H <= 0 || H > 65535 || T >= (int64_t(1) << 31) || S >= (int64_t(1) << 31) ||
         B >= (int64_t(1) << 31) || (N != 64 && N != 128) || R < 8 || R > 64 || R % 8 != 0 || !good_dtype(dtype) ||
         !good_strides({q_stride_t, q_stride_h, k_stride_t, k_stride_h, kr_stride, v_stride_t, v_stride_h}) ||
-        (causal != 0 && causal != 1) || !std::isfinite(scale))
+        (causal != 0 && causal != 1) || !(std::isfinite(scale) && scale > 0.0f))
         return SGQ_ERR_INVALID_ARG;
     if (T == 0) return SGQ_OK;
     if (B == 0 || !q || !q_starts || !kv_starts || !out || (S > 0 && (!k || !k_rot || !v))) return SGQ_ERR_INVALID_ARG;

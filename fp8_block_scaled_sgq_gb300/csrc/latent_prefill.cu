@@ -1,120 +1,525 @@
-// Expanded latent attention of ragged prompts: a simple form, one warp for
-// each (query token, head).
+// Expanded latent attention of ragged prompts, for sm_103a.
 //
-// Softmax in one pass with a running maximum m and sum l: a key with score s
-// (in powers of two) turns (m, l, o) into (m', l 2^(m-m') + 2^(s-m'),
-// o 2^(m-m') + 2^(s-m') v), m' = max(m, s).  Lane i holds elements i, i + 32,
-// ... of a row, so a key costs one row read and one warp sum.
+// A CTA takes two tiles of 128 queries of one head and walks over the keys in
+// tiles of 128, each tile a pair of MMAs with an fp32 accumulator in TMEM:
+//     S [128, 128] = Q K^T   over N + R columns (the R are shared by the heads)
+//     O [128, N]  += P V     over 128 keys, P from TMEM (it overlays S)
+// Softmax keeps a reference m and a sum l a row: p = 2^(s - m), s in powers of
+// two.  m follows the running maximum only when that has grown by more than
+// 2^8, so O is rescaled on few steps; sums are fp32.  P is rounded once, to
+// the inputs' type, as the second product's operand; l sums the unrounded p.
+//
+// What bounds it: the tensor cores.  A tile of N + R = 192, N = 128 takes 1280
+// cycles of MMAs at full rate; its exponentials take up to 1024 on the special
+// function units.  So two query tiles alternate: one group of four warps does
+// the softmax of its tile while the MMAs of the other run.  Warps: 0 loads
+// (TMA), 1 issues MMAs, 2 to 5 and 6 to 9 softmax of a query tile each
+// (thread = query row = TMEM lane).  Keys and values share a ring of chunks of
+// 128 rows x 64 columns: values of a tile arrive while the products before
+// them run.
+//
+// Order of the CTAs: the query tiles of a head follow one another, longest
+// first, so that the heads in flight keep their keys and values in L2.
+#include <cuda.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <type_traits>
 
 #include "latent_common.cuh"
+#include "latent_ptx.cuh"
 #include "sgq_internal.h"
 
 namespace sgq {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kMaxPer = 6;   // (128 + 64) / 32 elements a lane
+using lat::Pair;
 
-template <typename T>
-__device__ __forceinline__ float to_f(T v);
-template <>
-__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <>
-__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
-template <typename T>
-__device__ __forceinline__ T from_f(float v);
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __float2bfloat16_rn(v); }
-template <>
-__device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
+constexpr int kThreads = 320;
+constexpr int kTile = 128;
+constexpr int kChunkBytes = kTile * 128;
+constexpr int kSlots = 8;
+constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
+constexpr float kGrow = 8.0f;   // powers of two the maximum may outgrow the reference by
+constexpr int kOffQ = kSlots * kChunkBytes;
+constexpr int kOffMisc = kOffQ + 6 * kChunkBytes;
+constexpr int kMisc = 512;
+constexpr int kSmem = kOffMisc + kMisc + 1024;   // alignment slack
+static_assert(kSmem <= 232448, "shared memory");
 
-struct RowState {
-    float q[kMaxPer], o[kMaxPer], m = -INFINITY, l = 0.0f;
+struct Args {
+    const int32_t* q_starts;
+    const int32_t* kv_starts;
+    void* out;
+    float* lse;
+    uint32_t* status;
+    int64_t T, S, B;
+    int H, N, R, causal;
+    float scale2;
 };
-__device__ __forceinline__ void take(RowState& r, const float (&k)[kMaxPer], const float (&v)[kMaxPer], float scale2) {
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kMaxPer; ++i) s = fmaf(r.q[i], k[i], s);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-    s *= scale2;
-    const float m = fmaxf(r.m, s);
-    const float a = exp2f(r.m - m), p = exp2f(s - m);
-    r.l = r.l * a + p;
-#pragma unroll
-    for (int i = 0; i < kMaxPer; ++i) r.o[i] = r.o[i] * a + p * v[i];
-    r.m = m;
-}
-template <typename T>
-__device__ __forceinline__ void finish(const RowState& r, T* out, int width, float* lse) {
-    const int lane = threadIdx.x & 31;
-    const float inv = r.l > 0.0f ? 1.0f / r.l : 0.0f;
-#pragma unroll
-    for (int i = 0; i < kMaxPer; ++i)
-        if (lane + 32 * i < width) out[lane + 32 * i] = from_f<T>(r.o[i] * inv);
-    if (lse != nullptr && lane == 0) *lse = r.l > 0.0f ? r.m * 0.69314718055994531f + logf(r.l) : -INFINITY;
+
+struct Shared {
+    uint64_t full[kSlots], empty[kSlots];
+    uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drain;
+    uint32_t tmem, abort;
+    int64_t b;
+    int qb, pad;
+    int64_t warp_sum[kThreads / 32];
+};
+static_assert(sizeof(Shared) <= kMisc, "barriers");
+
+struct Request {
+    int q0, n, k0, m;   // queries [q0, q0 + n), keys [k0, k0 + m)
+};
+__device__ __forceinline__ Request request(const Args& a, int64_t b, bool report) {
+    const int64_t qs = a.q_starts[b], qe = a.q_starts[b + 1], ks = a.kv_starts[b], ke = a.kv_starts[b + 1];
+    const int64_t q0 = min(max(qs, int64_t(0)), a.T), q1 = min(max(qe, q0), a.T);
+    const int64_t k0 = min(max(ks, int64_t(0)), a.S), k1 = min(max(ke, k0), a.S);
+    if (report && (q0 != qs || q1 != qe || k0 != ks || k1 != ke || (b == 0 && (qs != 0 || ks != 0)) ||
+                   (b == a.B - 1 && (qe != a.T || ke != a.S))))
+        atomicOr(a.status, kStatusBadValue);
+    return Request{static_cast<int>(q0), static_cast<int>(q1 - q0), static_cast<int>(k0), static_cast<int>(k1 - k0)};
 }
 
-// The request that token t belongs to, in [0, B); starts clamped to [0, T].
-__device__ __forceinline__ int64_t request_of(const int32_t* starts, int64_t B, int64_t t) {
-    int64_t lo = 0, hi = B;
-    while (hi - lo > 1) {
-        const int64_t mid = (lo + hi) / 2;
-        if (starts[mid] <= t) lo = mid;
-        else hi = mid;
-    }
-    return lo;
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kWarps * 32) latent_prefill_simple(const PrefillArgs a) {
-    const int64_t row = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (row >= a.T * a.H) return;
-    const int64_t t = row / a.H, h = row % a.H;
-    const int64_t b = request_of(a.q_starts, a.B, t);
-    const int64_t i = t - a.q_starts[b], n = a.q_starts[b + 1] - a.q_starts[b];
-    const int64_t k0 = min(max(int64_t(a.kv_starts[b]), int64_t(0)), a.S);
-    const int64_t m = min(max(int64_t(a.kv_starts[b + 1]), k0), a.S) - k0;
-    const int W = a.N + a.R;
-    RowState r;
-    const T* q = static_cast<const T*>(a.q) + t * a.q_t + h * a.q_h;
+// The CTA's item: block index -> (request, head, pair of query tiles); every
+// thread takes part.  False: no such item (the grid is an upper bound).
+__device__ __forceinline__ bool find_item(const Args& a, Shared& sh, int64_t item, int64_t& b, int& head, int& qb) {
+    const int64_t k = (a.B + kThreads - 1) / kThreads;
+    const int64_t b0 = min(a.B, threadIdx.x * k), b1 = min(a.B, b0 + k);
+    int64_t mine = 0;
+    for (int64_t i = b0; i < b1; ++i) mine += int64_t((request(a, i, blockIdx.x == 0).n + 2 * kTile - 1) / (2 * kTile)) * a.H;
+    int64_t scan = mine;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-    for (int e = 0; e < kMaxPer; ++e) {
-        r.q[e] = lane + 32 * e < W ? to_f(q[lane + 32 * e]) : 0.0f;
-        r.o[e] = 0.0f;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t up = __shfl_up_sync(0xFFFFFFFFu, scan, o);
+        if (lane >= o) scan += up;
     }
-    const int64_t end = a.causal ? min(m, m - n + i + 1) : m;
-    for (int64_t j = k0; j < k0 + end; ++j) {
-        const T* kp = static_cast<const T*>(a.k) + j * a.k_t + h * a.k_h;
-        const T* rp = static_cast<const T*>(a.k_rot) + j * a.kr_t - a.N;
-        const T* vp = static_cast<const T*>(a.v) + j * a.v_t + h * a.v_h;
-        float k[kMaxPer], v[kMaxPer];
-#pragma unroll
-        for (int e = 0; e < kMaxPer; ++e) {
-            const int c = lane + 32 * e;
-            k[e] = c < a.N ? to_f(kp[c]) : (c < W ? to_f(rp[c]) : 0.0f);
-            v[e] = c < a.N ? to_f(vp[c]) : 0.0f;
+    if (lane == 31) sh.warp_sum[warp] = scan;
+    if (threadIdx.x == 0) sh.b = -1;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) scan += sh.warp_sum[w];
+    int64_t at = scan - mine;
+    if (item >= at && item < scan) {
+        for (int64_t i = b0; i < b1; ++i) {
+            const int64_t n = int64_t((request(a, i, false).n + 2 * kTile - 1) / (2 * kTile)) * a.H;
+            if (item < at + n) {
+                sh.b = i;
+                sh.qb = static_cast<int>(item - at);
+                break;
+            }
+            at += n;
         }
-        take(r, k, v, a.scale * 1.44269504088896341f);
     }
-    finish(r, static_cast<T*>(a.out) + row * a.N, a.N, a.lse ? a.lse + row : nullptr);
+    __syncthreads();
+    b = sh.b;
+    if (b < 0) return false;
+    const int blocks = (request(a, b, false).n + 2 * kTile - 1) / (2 * kTile);
+    head = sh.qb / blocks;
+    qb = blocks - 1 - sh.qb % blocks;
+    return true;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 1)
+    latent_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                          const __grid_constant__ CUtensorMap tm_r, const __grid_constant__ CUtensorMap tm_v, const Args a) {
+    constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+    extern __shared__ uint8_t raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    Shared& sh = *reinterpret_cast<Shared*>(smem + kOffMisc);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const lat::Sync sync{&sh.abort, a.status};
+    auto bar = [](uint64_t& b) { return ptx::smem_u32(&b); };
+    const uint32_t s_ring = ptx::smem_u32(smem), s_q = s_ring + kOffQ;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kSlots; ++i) {
+            ptx::mbar_init(bar(sh.full[i]), 1);
+            ptx::mbar_init(bar(sh.empty[i]), 1);
+        }
+        for (int g = 0; g < 2; ++g) {
+            ptx::mbar_init(bar(sh.q_full[g]), 1);
+            ptx::mbar_init(bar(sh.s_full[g]), 1);
+            ptx::mbar_init(bar(sh.p_full[g]), 4);
+            ptx::mbar_init(bar(sh.o_full[g]), 1);
+        }
+        ptx::mbar_init(bar(sh.drain), 1);
+        sh.abort = 0;
+        ptx::fence_mbar_init();
+        ptx::prefetch_tmap(&tm_q);
+        ptx::prefetch_tmap(&tm_k);
+        ptx::prefetch_tmap(&tm_r);
+        ptx::prefetch_tmap(&tm_v);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(ptx::smem_u32(&sh.tmem), 512);
+        ptx::tmem_relinquish();
+    }
+    ptx::launch_dependents();
+    ptx::grid_dependency_wait();
+    ptx::tc_fence_before();
+    int64_t b;
+    int head = 0, qb = 0;
+    const bool any = find_item(a, sh, blockIdx.x, b, head, qb);
+    ptx::tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    // TMEM columns: S (and P) of the two query tiles at 0 and 128, O at 256 and 384.
+    const int vc = a.N / 64, kc = vc + 1, per = kc + vc;   // chunks a tile: values, keys, both
+    Request r{0, 0, 0, 0};
+    int first[2] = {0, 0}, count[2] = {0, 0};              // query tile g: its first query, its key tiles
+    if (any) {
+        r = request(a, b, false);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            first[g] = qb * 2 * kTile + g * kTile;
+            const int last = min(first[g] + kTile, r.n) - 1;
+            const int seen = first[g] >= r.n ? 0 : (a.causal ? max(0, r.m - r.n + last + 1) : r.m);
+            count[g] = (seen + kTile - 1) / kTile;
+        }
+    }
+    const int tiles = max(count[0], count[1]);
+    uint32_t used = 0;                                     // chunks loaded
+    if (warp == 0) {
+        // ------------------------------------------------------------ loads
+        bool ok = true;
+        auto q_tile = [&](int g) {
+            if (count[g] > 0 && lane == 0) {
+                ptx::mbar_arrive_expect_tx(bar(sh.q_full[g]), kc * kChunkBytes);
+                for (int c = 0; c < kc; ++c)
+                    lat::tma_load_3d(s_q + (g * 3 + c) * kChunkBytes, &tm_q, c * 64, head, r.q0 + first[g], bar(sh.q_full[g]));
+            }
+        };
+        if (tiles > 0) q_tile(0);
+        for (int t = 0; t < tiles && ok; ++t) {
+            for (int c = 0; c < per; ++c) {
+                const uint32_t slot = used % kSlots;
+                ok = lat::wait_warp(bar(sh.empty[slot]), ((used / kSlots) & 1u) ^ 1u, sync);
+                if (!ok) break;
+                if (lane == 0) {
+                    const uint32_t full = bar(sh.full[slot]), dst = s_ring + slot * kChunkBytes;
+                    const int row = r.k0 + t * kTile;
+                    ptx::mbar_arrive_expect_tx(full, kChunkBytes);
+                    if (c < vc) lat::tma_load_3d(dst, &tm_k, c * 64, head, row, full);
+                    else if (c == vc) ptx::tma_load_2d(dst, &tm_r, 0, row, full);
+                    else lat::tma_load_3d(dst, &tm_v, (c - kc) * 64, head, row, full);
+                }
+                ++used;
+                if (t == 0 && c == vc) q_tile(1);
+            }
+        }
+    } else if (warp == 1 && tiles > 0) {
+        // ------------------------------------------------------------ MMAs
+        constexpr uint32_t kIdS = lat::idesc_f16(128, kTile, kBf16, false, false);
+        const uint32_t id_o = lat::idesc_f16(128, a.N, kBf16, false, true);
+        constexpr uint32_t kIdO64 = lat::idesc_f16(128, 64, kBf16, false, true);
+        const int rope_steps = (a.R + 15) / 16;
+        bool ok = true;
+        auto wait_chunks = [&](uint32_t n, int chunks) {
+            for (int c = 0; c < chunks && ok; ++c, ++n) ok = lat::wait_warp(bar(sh.full[n % kSlots]), (n / kSlots) & 1u, sync);
+            ptx::tc_fence_after();
+        };
+        auto scores = [&](int g, uint32_t n) {   // S of query tile g, keys in chunks n ...
+            if (lane == 0) {
+                for (int c = 0; c < kc; ++c) {
+                    const uint64_t da = ptx::smem_desc(s_q + (g * 3 + c) * kChunkBytes, 16, 1024, ptx::kLayoutSw128);
+                    const uint64_t db = ptx::smem_desc(s_ring + ((n + c) % kSlots) * kChunkBytes, 16, 1024, ptx::kLayoutSw128);
+                    const int steps = c == vc ? rope_steps : 4;
+                    for (int k = 0; k < steps; ++k) lat::mma_f16(tmem + g * 128, da + k * 2, db + k * 2, kIdS, c > 0 || k > 0);
+                }
+                ptx::tc_commit(bar(sh.s_full[g]));
+            }
+            __syncwarp();
+        };
+        auto release = [&](uint32_t n, int chunks) {
+            if (lane == 0)
+                for (int c = 0; c < chunks; ++c) ptx::tc_commit(bar(sh.empty[(n + c) % kSlots]));
+            __syncwarp();
+        };
+        for (int g = 0; g < 2 && ok; ++g) {
+            if (count[g] == 0) continue;
+            ok = lat::wait_warp(bar(sh.q_full[g]), 0, sync);
+            if (ok) wait_chunks(0, kc);
+            if (ok) scores(g, 0);
+        }
+        if (ok) release(0, kc);
+        for (int t = 0; t < tiles && ok; ++t) {
+            const uint32_t nv = t * per + kc, nk = (t + 1) * per;   // this tile's values, the next one's keys
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                if (t < count[g] && ok) {
+                    ok = lat::wait_warp(bar(sh.p_full[g]), t & 1u, sync);
+                    if (ok) wait_chunks(nv, vc);
+                    if (ok && lane == 0) {
+                        const uint32_t o = tmem + 256 + g * 128, p = tmem + g * 128;
+                        const uint32_t s0 = nv % kSlots, s1 = (nv + 1) % kSlots;
+                        const uint64_t d0 = ptx::smem_desc(s_ring + s0 * kChunkBytes, kChunkBytes, 1024, ptx::kLayoutSw128);
+                        if (vc == 1 || s1 == s0 + 1) {
+                            for (int k = 0; k < kTile / 16; ++k)
+                                lat::mma_f16_ts(o, p + k * 8, d0 + k * (2048 >> 4), id_o, t > 0 || k > 0);
+                        } else {   // the two chunks of values at the ring's two ends
+                            const uint64_t d1 = ptx::smem_desc(s_ring + s1 * kChunkBytes, kChunkBytes, 1024, ptx::kLayoutSw128);
+                            for (int k = 0; k < kTile / 16; ++k) {
+                                lat::mma_f16_ts(o, p + k * 8, d0 + k * (2048 >> 4), kIdO64, t > 0 || k > 0);
+                                lat::mma_f16_ts(o + 64, p + k * 8, d1 + k * (2048 >> 4), kIdO64, t > 0 || k > 0);
+                            }
+                        }
+                        if (t + 1 == count[g]) ptx::tc_commit(bar(sh.o_full[g]));
+                    }
+                    __syncwarp();
+                }
+                if (t + 1 < count[g] && ok) {
+                    wait_chunks(nk, kc);
+                    if (ok) scores(g, nk);
+                }
+            }
+            if (ok) {
+                release(nv, vc);
+                if (t + 1 < tiles) release(nk, kc);
+            }
+        }
+    } else if (warp >= 2) {
+        // ------------------------------------------------------------ softmax
+        const int g = (warp - 2) >> 2, quarter = warp & 3;
+        const int row = quarter * 32 + lane;
+        const int q = first[g] + row;                              // query of the request
+        const int mine = g == 0 ? count[0] : count[1];
+        if (any && first[g] < r.n) {
+            const int sees = a.causal ? min(r.m, r.m - r.n + q + 1) : r.m;
+            const int low = a.causal ? r.m - r.n + first[g] + quarter * 32 + 1 : r.m;   // what every row of the warp sees
+            const uint32_t t_s = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + g * 128, t_o = t_s + 256;
+            float ref = -INFINITY, l = 0.0f;
+            bool ok = true;
+            for (int t = 0; t < mine; ++t) {
+                ok = lat::wait_warp(bar(sh.s_full[g]), t & 1u, sync);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                uint32_t s[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) ptx::tmem_ld<32>(t_s + c * 32, s[c]);
+                ptx::tmem_wait_ld();
+                if ((t + 1) * kTile > low || (t + 1) * kTile > r.m) {
+                    const int end = sees - t * kTile;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (c * 32 + j >= end) s[c][j] = __float_as_uint(-INFINITY);
+                }
+                float top = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) top = fmaxf(top, __uint_as_float(s[c][j]));
+                top *= a.scale2;
+                const bool grow = top > ref + kGrow || (ref == -INFINITY && top > -INFINITY);
+                if (__any_sync(0xFFFFFFFFu, grow)) {
+                    const float f = grow ? lat::ex2(ref - top) : 1.0f;
+                    if (grow) ref = top;
+                    l *= f;
+                    if (t > 0) {
+#pragma unroll 1
+                        for (int c = 0; c < vc * 8; ++c) {
+                            uint32_t o[8];
+                            ptx::tmem_ld<8>(t_o + c * 8, o);
+                            ptx::tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                            lat::tmem_st<8>(t_o + c * 8, o);
+                        }
+                    }
+                }
+                const float base = ref == -INFINITY ? 0.0f : ref;
+                float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        const float p0 = lat::ex2(fmaf(__uint_as_float(s[c][j]), a.scale2, -base));
+                        const float p1 = lat::ex2(fmaf(__uint_as_float(s[c][j + 1]), a.scale2, -base));
+                        sum[0] += p0;
+                        sum[1] += p1;
+                        p[j / 2] = Pair<T>::pack(p0, p1);
+                    }
+                    lat::tmem_st<16>(t_s + c * 16, p);
+                }
+                l += sum[0] + sum[1];
+                // Weights past the request's keys are zero, but 0 times what lies there need not be: the
+                // group whose product comes first clears those rows of the values.
+                if ((t + 1) * kTile > r.m && (g == 0 || t >= count[0])) {
+                    const uint32_t nv = t * per + kc;
+                    for (int c = 0; c < vc && ok; ++c)
+                        ok = lat::wait_warp(bar(sh.full[(nv + c) % kSlots]), ((nv + c) / kSlots) & 1u, sync);
+                    if (!ok) break;
+                    if (t * kTile + row >= r.m) {
+                        for (int c = 0; c < vc; ++c) {
+                            uint4* z = reinterpret_cast<uint4*>(smem + ((nv + c) % kSlots) * kChunkBytes + row * 128);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) z[i] = make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                    ptx::fence_proxy_async_smem();
+                }
+                lat::tmem_wait_st();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar(sh.p_full[g]));
+            }
+            if (ok && mine > 0) {
+                ok = lat::wait_warp(bar(sh.o_full[g]), 0, sync);
+                ptx::tc_fence_after();
+            }
+            if (ok) {
+                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+                const int64_t at = (int64_t(r.q0) + q) * a.H + head;
+                if (a.lse != nullptr && q < r.n) a.lse[at] = l > 0.0f ? (ref + log2f(l)) * kLn2 : -INFINITY;
+                uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + at * a.N);
+                for (int c = 0; c < vc * 2; ++c) {
+                    uint32_t o[32];
+                    if (mine > 0) {
+                        ptx::tmem_ld<32>(t_o + c * 32, o);
+                        ptx::tmem_wait_ld();
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = 0u;
+                    }
+                    if (q < r.n) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint4 w;
+                            uint32_t* pw = &w.x;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                pw[j] = Pair<T>::pack(__uint_as_float(o[i * 8 + 2 * j]) * inv, __uint_as_float(o[i * 8 + 2 * j + 1]) * inv);
+                            out[c * 4 + i] = w;
+                        }
+                    }
+                }
+            }
+            ptx::tc_fence_before();
+        }
+    }
+    __syncthreads();
+    if (sh.abort) {
+        // A wait ran out: copies in flight land and MMAs end (both bounded) before the CTA does.
+        const uint64_t t0 = ptx::globaltimer();
+        auto land = [&](uint64_t& x, uint32_t uses) {
+            while (uses > 0 && !ptx::mbar_test_wait(bar(x), (uses - 1) & 1u) && ptx::globaltimer() - t0 < (1ull << 26)) {}
+        };
+        if (warp == 0) {
+            for (uint32_t i = 0; i < kSlots; ++i) land(sh.full[i], used / kSlots + (i < used % kSlots ? 1 : 0));
+            for (int g = 0; g < 2; ++g)
+                if (count[g] > 0 && (g == 0 || used > static_cast<uint32_t>(vc))) land(sh.q_full[g], 1);
+        } else if (threadIdx.x == 32) {
+            ptx::tc_commit(bar(sh.drain));
+            land(sh.drain, 1);
+        }
+        __syncthreads();
+    }
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------- host
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }();
+    return fn;
+}
+
+// [rows, heads, width] as boxes of 64 columns x 128 rows of one head.
+sgq_status head_map(CUtensorMap* m, const void* p, int64_t width, int64_t heads, int64_t rows, int64_t s_head,
+                    int64_t s_row) {
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(s_head) * 2, static_cast<cuuint64_t>(s_row) * 2};
+    const cuuint32_t box[3] = {64, 1, kTile}, ones[3] = {1, 1, 1};
+    return encoder()(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(p), dims, strides, box, ones,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? SGQ_OK
+               : SGQ_ERR_CUDA;
+}
+sgq_status row_map(CUtensorMap* m, const void* p, int64_t width, int64_t rows, int64_t s_row) {
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(s_row) * 2};
+    const cuuint32_t box[2] = {64, kTile}, ones[2] = {1, 1};
+    return encoder()(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(p), dims, strides, box, ones,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? SGQ_OK
+               : SGQ_ERR_CUDA;
+}
+
+template <typename T>
+sgq_status run(const CUtensorMap (&tm)[4], const Args& a, int64_t grid, cudaStream_t st) {
+    auto kern = latent_prefill_kernel<T>;
+    static bool configured[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SGQ_ERR_CUDA;
+    if (!configured[dev]) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess) return SGQ_ERR_CUDA;
+        configured[dev] = true;
+    }
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kern, tm[0], tm[1], tm[2], tm[3], a) != cudaSuccess) return SGQ_ERR_CUDA;
+    note_launch();
+    return SGQ_OK;
 }
 
 }  // namespace
 
-sgq_status launch_latent_prefill(const PrefillArgs& args, cudaStream_t st) {
-    PrefillArgs a = args;
-    const sgq_status rc = gemm::status_word(&a.status);
+sgq_status launch_latent_prefill(const PrefillArgs& x, cudaStream_t st) {
+    DeviceInfo di;
+    sgq_status rc = device_info(&di);
     if (rc != SGQ_OK) return rc;
-    const int64_t blocks = (a.T * a.H + kWarps - 1) / kWarps;
+    if (di.cc_major != 10 || encoder() == nullptr) return SGQ_ERR_UNSUPPORTED;
+    Args a{};
+    rc = gemm::status_word(&a.status);
+    if (rc != SGQ_OK) return rc;
+    a.q_starts = x.q_starts;
+    a.kv_starts = x.kv_starts;
+    a.out = x.out;
+    a.lse = x.lse;
+    a.T = x.T;
+    a.S = x.S;
+    a.B = x.B;
+    a.H = x.H;
+    a.N = x.N;
+    a.R = x.R;
+    a.causal = x.causal;
+    a.scale2 = x.scale * kLog2e;
+    const int64_t blocks = (x.T / (2 * kTile) + x.B) * x.H;   // at least the query tile pairs of any split of T
     if (blocks > INT32_MAX) return SGQ_ERR_INVALID_ARG;
-    if (a.dtype == SGQ_BF16) latent_prefill_simple<__nv_bfloat16><<<blocks, kWarps * 32, 0, st>>>(a);
-    else latent_prefill_simple<__half><<<blocks, kWarps * 32, 0, st>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return SGQ_ERR_CUDA;
-    note_launch();
-    return SGQ_OK;
+    CUtensorMap tm[4];
+    // (without keys nothing is loaded through the maps of keys and values: any address does)
+    const bool none = x.S == 0;
+    const int64_t W = x.N + x.R, S = none ? 1 : x.S;
+    if (head_map(&tm[0], x.q, W, x.H, x.T, x.q_h, x.q_t) != SGQ_OK ||
+        head_map(&tm[1], none ? x.q : x.k, x.N, x.H, S, none ? x.q_h : x.k_h, none ? x.q_t : x.k_t) != SGQ_OK ||
+        row_map(&tm[2], none ? x.q : x.k_rot, x.R, S, none ? x.q_t : x.kr_t) != SGQ_OK ||
+        head_map(&tm[3], none ? x.q : x.v, x.N, x.H, S, none ? x.q_h : x.v_h, none ? x.q_t : x.v_t) != SGQ_OK)
+        return SGQ_ERR_CUDA;
+    return x.dtype == SGQ_BF16 ? run<__nv_bfloat16>(tm, a, blocks, st) : run<__half>(tm, a, blocks, st);
 }
 
 }  // namespace sgq

@@ -397,7 +397,7 @@ sgq_status sgq_latent_append(const void* q, int64_t q_stride_t, int64_t q_stride
  * page numbers of request b, table_width columns.  out: [T, H, L], lse: fp32
  * [T, H] or NULL, both contiguous.  q_starts: int32 [B + 1], rising, ending
  * at T.  L in {128, 256, 384, 512}; R % 8 == 0, 8 <= R <= 64; page % 16 == 0;
- * H <= 65535.  Cached rows a token sees, and rows of the same 128 that some
+ * H <= 65535; scale > 0.  Cached rows a token sees, and rows of the same 128 that some
  * other token of its request sees, are finite; rows at kv_lens[b] and later
  * may hold anything.
  *
@@ -427,7 +427,7 @@ sgq_status sgq_latent_attention(const void* q, int64_t q_stride_row, int64_t T, 
  * q: [T, H, N + R]; k, v: [S, H, N]; k_rot: [S, R]; token (and head) strides.
  * out: [T, H, N], lse: fp32 [T, H] or NULL, both contiguous.  q_starts,
  * kv_starts: int32 [B + 1], rising, ending at T and S.  N in {64, 128};
- * R % 8 == 0, 8 <= R <= 64; H <= 65535.  All rows of k, v and k_rot that
+ * R % 8 == 0, 8 <= R <= 64; H <= 65535; scale > 0.  All rows of k, v and k_rot that
  * belong to a request are finite.
  */
 sgq_status sgq_latent_prefill(const void* q, int64_t q_stride_t, int64_t q_stride_h, int64_t T, const void* k,

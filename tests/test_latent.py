@@ -63,7 +63,7 @@ def test_attention_validation(lib):
     for bad in (dict(T=-1), dict(H=0), dict(H=65536), dict(T=1 << 27), dict(B=-1), dict(L=64), dict(L=640), dict(L=200),
                 dict(R=0), dict(R=72), dict(R=12), dict(dtype=7), dict(qr=568), dict(qr=580), dict(cr=568),
                 dict(cp=9208), dict(page=24), dict(page=0), dict(pages=0), dict(width=-1), dict(width=1 << 28),
-                dict(T=5), dict(scale=float("nan")), dict(scale=float("inf")), dict(q=None), dict(cache=None),
+                dict(T=5), dict(scale=0.0), dict(scale=-0.1), dict(scale=float("nan")), dict(scale=float("inf")), dict(q=None), dict(cache=None),
                 dict(table=None), dict(lens=None), dict(out=None), dict(ws=None), dict(B=0, starts=G)):
         assert f(**bad) == INV, bad
     for bad in (dict(q=A + 8), dict(cache=B + 8), dict(out=E + 4), dict(ws=F + 4), dict(table=C + 2), dict(lens=D + 1),
@@ -88,7 +88,7 @@ def test_prefill_validation(lib):
     for bad in (dict(T=-1), dict(S=-1), dict(H=0), dict(N=96), dict(N=256), dict(R=0), dict(R=72), dict(R=20),
                 dict(dtype=2), dict(causal=2), dict(qt=3073), dict(vh=-256), dict(krt=4), dict(B=0), dict(q=None),
                 dict(k=None), dict(kr=None), dict(v=None), dict(qs=None), dict(ks=None), dict(out=None),
-                dict(scale=float("inf"))):
+                dict(scale=float("inf")), dict(scale=-1.0)):
         assert f(**bad) == INV, bad
     for bad in (dict(q=A + 8), dict(k=B + 2), dict(kr=C + 8), dict(v=D + 8), dict(out=G + 8), dict(qs=E + 2),
                 dict(ks=F + 1), dict(lse=A + 2)):
