@@ -76,6 +76,8 @@ _lib = None
 def load_library(path: str = LIB_PATH):
     """Loads libsgq.so (built by ``fp8_block_scaled_sgq_gb300.build``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -133,19 +135,19 @@ def load_library(path: str = LIB_PATH):
 
 
 def _ptr(t):
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or isinstance(t, int):
         return t
-    if hasattr(t, "data_ptr"):
+    try:
         return t.data_ptr()
-    raise TypeError(f"expected a tensor or an int address, got {type(t)!r}")
+    except AttributeError:
+        raise TypeError(f"expected a tensor or an int address, got {type(t)!r}") from None
 
 
 def _stream(s):
     if s is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the handle of torch.cuda.current_stream(), without the Stream object around it (2.9 -> 0.3 us)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(s, int):
         return s
     return s.cuda_stream

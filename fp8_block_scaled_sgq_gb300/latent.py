@@ -8,56 +8,71 @@ ValueError before anything is launched.
 """
 from __future__ import annotations
 
-import contextlib
 import math
 
 from . import binding
 
 
-def _on(stream):
-    """The allocations of a call belong to its stream, so that their memory is
-    not handed out again while its kernels run."""
+def _empty(shape, like, stream):
+    """A new tensor of like's type and device that belongs to the call's stream,
+    so that its memory is not handed out again while its kernels run."""
     import torch
     if stream is None:
-        return contextlib.nullcontext()
+        return torch.empty(shape, dtype=like.dtype, device=like.device)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream)
-    return torch.cuda.stream(stream)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=like.dtype, device=like.device)
 
+
+# The checks below run on every call of a decode step: plain comparisons, the
+# message made only when one fails.
 
 def _dtype(x, *others) -> int:
     import torch
+    dt = x.dtype
     for t in others:
-        if t is not None and t.dtype != x.dtype:
-            raise ValueError(f"one element type a call: {x.dtype} and {t.dtype}")
-    if x.dtype == torch.bfloat16:
+        if t is not None and t.dtype != dt:
+            raise ValueError(f"one element type a call: {dt} and {t.dtype}")
+    if dt == torch.bfloat16:
         return binding.SGQ_BF16
-    if x.dtype == torch.float16:
+    if dt == torch.float16:
         return binding.SGQ_FP16
-    raise ValueError(f"element type {x.dtype} is neither bfloat16 nor float16")
+    raise ValueError(f"element type {dt} is neither bfloat16 nor float16")
 
 
-def _need(ok: bool, what: str):
-    if not ok:
-        raise ValueError(what)
+def _fail(what: str):
+    raise ValueError(what)
 
 
-def _inner(name: str, t):
-    _need(t.shape[-1] <= 1 or t.stride(-1) == 1, f"{name}: the last dimension is not contiguous")
-    return t
+def _strides(name: str, t, dims: int):
+    """t's strides but the last, which has to be 1."""
+    s = t.stride()
+    if len(s) != dims:
+        _fail(f"{name}: expected {dims} dimensions, got {tuple(t.shape)}")
+    if s[-1] != 1 and t.shape[-1] > 1:
+        _fail(f"{name}: the last dimension is not contiguous")
+    return s[:-1]
 
 
 def _index(name: str, t, dtype, n: int):
     """A whole-number tensor of the given type with n contiguous entries."""
-    _need(t.dtype == dtype and t.dim() == 1 and t.shape[0] == n and t.is_contiguous(),
-          f"{name}: expected {n} contiguous {dtype} entries, got {tuple(t.shape)} of {t.dtype}")
-    return t
+    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        _fail(f"{name}: expected {n} contiguous {dtype} entries, got {tuple(t.shape)} of {t.dtype}")
 
 
 def _device(x, *others):
-    _need(x.is_cuda, "the tensors are not on a CUDA device")
+    if not x.is_cuda:
+        _fail("the tensors are not on a CUDA device")
+    at = x.get_device()
     for t in others:
-        _need(t is None or t.device == x.device, "the tensors are on different devices")
+        if t is not None and t.get_device() != at:
+            _fail("the tensors are on different devices")
+
+
+def _contiguous(name: str, t, shape, dtype=None):
+    if t.shape != shape or not t.is_contiguous() or (dtype is not None and t.dtype != dtype):
+        _fail(f"{name}: expected a contiguous {tuple(shape)} tensor{'' if dtype is None else f' of {dtype}'}")
 
 
 def rotary_table(max_pos: int, rot: int, base: float = 10000.0, factor: float = 1.0, original_max: int = 0,
@@ -74,8 +89,10 @@ def rotary_table(max_pos: int, rot: int, base: float = 10000.0, factor: float = 
     64 bits, once, when the table is made.
     """
     import torch
-    _need(max_pos > 0 and rot > 0 and rot % 2 == 0, "max_pos and an even rot are needed")
-    _need(base > 1.0 and factor >= 1.0, "base > 1 and factor >= 1 are needed")
+    if max_pos <= 0 or rot <= 0 or rot % 2 != 0:
+        _fail("max_pos > 0 and an even rot > 0 are needed")
+    if base <= 1.0 or factor < 1.0:
+        _fail("base > 1 and factor >= 1 are needed")
     i = torch.arange(rot // 2, dtype=torch.float64, device=device)
     freq = base ** (-2.0 * i / rot)
     if factor > 1.0:
@@ -92,9 +109,9 @@ def rotary_table(max_pos: int, rot: int, base: float = 10000.0, factor: float = 
 
 def _table(table):
     import torch
-    _need(table.dim() == 2 and table.dtype == torch.float32 and table.is_contiguous(),
-          "table: expected a contiguous float32 [max_pos, rot] tensor")
-    return table
+    if table.dim() != 2 or table.dtype != torch.float32 or not table.is_contiguous():
+        _fail("table: expected a contiguous float32 [max_pos, rot] tensor")
+    return table.shape
 
 
 def rotary(x, positions, table, offset: int = 0, interleaved: bool = True, inverse: bool = False, out=None,
@@ -105,25 +122,22 @@ def rotary(x, positions, table, offset: int = 0, interleaved: bool = True, inver
     inverse: rotate back, which is also the gradient.  out may be x (in place); returns out.
     """
     import torch
-    _need(x.dim() == 3, f"x: expected [T, H, D], got {tuple(x.shape)}")
     dt = _dtype(x, out)
-    T, H, D = _inner("x", x).shape
+    if x.dim() != 3:
+        _fail(f"x: expected [T, H, D], got {tuple(x.shape)}")
+    T, H, D = x.shape
+    xt, xh = _strides("x", x, 3)
     _index("positions", positions, torch.int64, T)
-    max_pos, R = _table(table).shape
+    max_pos, R = _table(table)
     _device(x, positions, table, out)
     if out is None:
-        with _on(stream):
-            out = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
-    _need(out.shape == x.shape, "out: not of x's shape")
-    _inner("out", out)
-    binding.sgq_rotary(x, T, H, D, x.stride(0), x.stride(1), positions, table, max_pos, R, offset, interleaved, inverse,
-                       dt, out, out.stride(0), out.stride(1), stream)
+        out = _empty((T, H, D), x, stream)
+    elif out.shape != x.shape:
+        _fail("out: not of x's shape")
+    yt, yh = _strides("out", out, 3)
+    binding.sgq_rotary(x, T, H, D, xt, xh, positions, table, max_pos, R, offset, interleaved, inverse, dt, out, yt, yh,
+                       stream)
     return out
-
-
-def _cache(cache):
-    _need(cache.dim() == 3, f"cache: expected [pages, page, width], got {tuple(cache.shape)}")
-    return _inner("cache", cache)
 
 
 def latent_append(q_rot, k_rot, latent, positions, slots, table, cache, interleaved: bool = True, q_out=None,
@@ -136,36 +150,40 @@ def latent_append(q_rot, k_rot, latent, positions, slots, table, cache, interlea
     receives the rotated keys.
     """
     import torch
-    T, R = _inner("k_rot", k_rot).shape
-    L = _inner("latent", latent).shape[1]
     dt = _dtype(k_rot, q_rot, latent, cache, q_out, k_out)
-    _need(latent.shape[0] == T, "latent: not one row a token")
+    (kt,), (lt,), (cp, cr) = _strides("k_rot", k_rot, 2), _strides("latent", latent, 2), _strides("cache", cache, 3)
+    T, R = k_rot.shape
+    L = latent.shape[1]
+    if latent.shape[0] != T:
+        _fail("latent: not one row a token")
     _index("positions", positions, torch.int64, T)
     _index("slots", slots, torch.int64, T)
-    max_pos = _table(table).shape[0]
-    _need(table.shape[1] == R, "table: not of the rotated width")
-    pages, page, width = _cache(cache).shape
-    _need(width == L + R, f"cache: rows of {width}, not {L} + {R}")
+    max_pos, rot = _table(table)
+    if rot != R:
+        _fail("table: not of the rotated width")
+    pages, page, width = cache.shape
+    if width != L + R:
+        _fail(f"cache: rows of {width}, not {L} + {R}")
     _device(k_rot, q_rot, latent, positions, slots, table, cache, q_out, k_out)
-    H, qs, qo = 0, (0, 0), (0, 0)
+    H = qt = qh = ot = oh = ko = 0
     if q_rot is not None:
-        _need(q_rot.dim() == 3 and q_rot.shape[0] == T and q_rot.shape[2] == R, "q_rot: expected [T, H, R]")
-        H = _inner("q_rot", q_rot).shape[1]
+        qt, qh = _strides("q_rot", q_rot, 3)
+        H = q_rot.shape[1]
+        if q_rot.shape[0] != T or q_rot.shape[2] != R:
+            _fail("q_rot: expected [T, H, R]")
         if q_out is None:
-            with _on(stream):
-                q_out = torch.empty((T, H, R), dtype=q_rot.dtype, device=q_rot.device)
-        _need(q_out.shape == q_rot.shape, "q_out: not of q_rot's shape")
-        _inner("q_out", q_out)
-        qs, qo = (q_rot.stride(0), q_rot.stride(1)), (q_out.stride(0), q_out.stride(1))
-    else:
-        _need(q_out is None, "q_out without q_rot")
+            q_out = _empty((T, H, R), q_rot, stream)
+        elif q_out.shape != q_rot.shape:
+            _fail("q_out: not of q_rot's shape")
+        ot, oh = _strides("q_out", q_out, 3)
+    elif q_out is not None:
+        _fail("q_out without q_rot")
     if k_out is not None:
-        _need(k_out.shape == k_rot.shape, "k_out: not of k_rot's shape")
-        _inner("k_out", k_out)
-    binding.sgq_latent_append(q_rot, qs[0], qs[1], k_rot, k_rot.stride(0), latent, latent.stride(0), positions, slots,
-                              table, max_pos, T, H, L, R, interleaved, dt, q_out, qo[0], qo[1], k_out,
-                              k_out.stride(0) if k_out is not None else 0, cache, pages, page, cache.stride(0),
-                              cache.stride(1), stream)
+        if k_out.shape != k_rot.shape:
+            _fail("k_out: not of k_rot's shape")
+        ko, = _strides("k_out", k_out, 2)
+    binding.sgq_latent_append(q_rot, qt, qh, k_rot, kt, latent, lt, positions, slots, table, max_pos, T, H, L, R,
+                              interleaved, dt, q_out, ot, oh, k_out, ko, cache, pages, page, cp, cr, stream)
     return q_out
 
 
@@ -180,34 +198,37 @@ def latent_attention(q, cache, page_table, kv_lens, scale: float, latent: int, q
     same time uses; None: allocated here.
     """
     import torch
-    _need(q.dim() == 3, f"q: expected [T, H, latent + R], got {tuple(q.shape)}")
     dt = _dtype(q, cache, out)
-    T, H, W = _inner("q", q).shape
-    pages, page, width = _cache(cache).shape
-    _need(width == W, f"cache: rows of {width}, queries of {W}")
-    _need(T <= 1 or H == 1 or q.stride(0) == H * q.stride(1), "q: tokens and heads are not evenly spaced rows")
-    row = q.stride(1) if H > 1 else q.stride(0) if T > 1 else W
-    _need(page_table.dim() == 2 and page_table.dtype == torch.int32 and page_table.is_contiguous(),
-          "page_table: expected a contiguous int32 [B, width] tensor")
-    B = page_table.shape[0]
+    (qt, qh), (cp, cr) = _strides("q", q, 3), _strides("cache", cache, 3)
+    T, H, W = q.shape
+    pages, page, width = cache.shape
+    if width != W:
+        _fail(f"cache: rows of {width}, queries of {W}")
+    if T > 1 and H > 1 and qt != H * qh:
+        _fail("q: tokens and heads are not evenly spaced rows")
+    row = qh if H > 1 else qt if T > 1 else W
+    if page_table.dim() != 2 or page_table.dtype != torch.int32 or not page_table.is_contiguous():
+        _fail("page_table: expected a contiguous int32 [B, width] tensor")
+    B, table_width = page_table.shape
     _index("kv_lens", kv_lens, torch.int32, B)
     if q_starts is not None:
         _index("q_starts", q_starts, torch.int32, B + 1)
-    else:
-        _need(T == B, f"{T} query tokens for {B} requests, without q_starts")
+    elif T != B:
+        _fail(f"{T} query tokens for {B} requests, without q_starts")
     _device(q, cache, page_table, kv_lens, q_starts, out, lse, workspace)
-    with _on(stream):
-        if out is None:
-            out = torch.empty((T, H, latent), dtype=q.dtype, device=q.device)
-        if workspace is None:
-            workspace = torch.empty(binding.sgq_latent_attention_workspace(T, H, latent), dtype=torch.uint8,
-                                    device=q.device)
-    _need(out.shape == (T, H, latent) and out.is_contiguous(), "out: expected a contiguous [T, H, latent] tensor")
-    _need(lse is None or (lse.shape == (T, H) and lse.dtype == torch.float32 and lse.is_contiguous()),
-          "lse: expected a contiguous float32 [T, H] tensor")
-    binding.sgq_latent_attention(q, row, T, H, cache, pages, page, cache.stride(0), cache.stride(1), latent, W - latent,
-                                 page_table, page_table.shape[1], B, kv_lens, q_starts, scale, dt, out, lse, workspace,
-                                 workspace.numel() * workspace.element_size(), stream)
+    if out is None:
+        out = _empty((T, H, latent), q, stream)
+    else:
+        _contiguous("out", out, (T, H, latent))
+    if lse is not None:
+        _contiguous("lse", lse, (T, H), torch.float32)
+    if workspace is None:
+        nbytes = binding.sgq_latent_attention_workspace(T, H, latent)
+        workspace = _empty(nbytes // 2, q, stream)
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
+    binding.sgq_latent_attention(q, row, T, H, cache, pages, page, cp, cr, latent, W - latent, page_table, table_width,
+                                 B, kv_lens, q_starts, scale, dt, out, lse, workspace, nbytes, stream)
     return out
 
 
@@ -220,25 +241,26 @@ def latent_prefill(q, k, k_rot, v, q_starts, kv_starts, scale: float, causal: bo
     logarithm of the softmax sums.
     """
     import torch
-    _need(q.dim() == 3 and k.dim() == 3 and v.dim() == 3 and k_rot.dim() == 2, "expected q, k, v of 3 dimensions, k_rot of 2")
     dt = _dtype(q, k, k_rot, v, out)
-    T, H, W = _inner("q", q).shape
-    S, _, N = _inner("k", k).shape
-    _need(k.shape == (S, H, N) and v.shape == (S, H, N), "k, v: expected [S, H, N] with q's heads")
+    (qt, qh), (kt, kh), (vt, vh) = _strides("q", q, 3), _strides("k", k, 3), _strides("v", v, 3)
+    rt, = _strides("k_rot", k_rot, 2)
+    T, H, W = q.shape
+    S, _, N = k.shape
     R = W - N
-    _need(k_rot.shape == (S, R), f"k_rot: expected [{S}, {R}]")
-    _inner("k_rot", k_rot), _inner("v", v)
+    if k.shape[1] != H or v.shape != k.shape:
+        _fail("k, v: expected [S, H, N] with q's heads")
+    if k_rot.shape[0] != S or k_rot.shape[1] != R:
+        _fail(f"k_rot: expected [{S}, {R}]")
     B = q_starts.shape[0] - 1
     _index("q_starts", q_starts, torch.int32, B + 1)
     _index("kv_starts", kv_starts, torch.int32, B + 1)
     _device(q, k, k_rot, v, q_starts, kv_starts, out, lse)
     if out is None:
-        with _on(stream):
-            out = torch.empty((T, H, N), dtype=q.dtype, device=q.device)
-    _need(out.shape == (T, H, N) and out.is_contiguous(), "out: expected a contiguous [T, H, N] tensor")
-    _need(lse is None or (lse.shape == (T, H) and lse.dtype == torch.float32 and lse.is_contiguous()),
-          "lse: expected a contiguous float32 [T, H] tensor")
-    binding.sgq_latent_prefill(q, q.stride(0), q.stride(1), T, k, k.stride(0), k.stride(1), k_rot, k_rot.stride(0), v,
-                               v.stride(0), v.stride(1), S, H, N, R, q_starts, kv_starts, B, scale, causal, dt, out,
-                               lse, stream)
+        out = _empty((T, H, N), q, stream)
+    else:
+        _contiguous("out", out, (T, H, N))
+    if lse is not None:
+        _contiguous("lse", lse, (T, H), torch.float32)
+    binding.sgq_latent_prefill(q, qt, qh, T, k, kt, kh, k_rot, rt, v, vt, vh, S, H, N, R, q_starts, kv_starts, B, scale,
+                               causal, dt, out, lse, stream)
     return out
