@@ -61,7 +61,7 @@ struct Cfg {
     static constexpr int kOffRope = kPairs * 2 * kChunkBytes;
     static constexpr int kOffQ = kOffRope + kRope * kChunkBytes;
     static constexpr int kOffMisc = kOffQ + 9 * kQChunk;
-    static constexpr int kMisc = 2560;                     // barriers, schedule, statistics
+    static constexpr int kMisc = 2816;                     // barriers, schedule, statistics
     static constexpr int kSmem = kOffMisc + kMisc + 1024;  // alignment slack
     static constexpr int kHalf = NR / 2;                   // columns a softmax warp
     static constexpr int kRowBytes = NR * 2;               // a token's row of P
@@ -117,8 +117,8 @@ __device__ __forceinline__ int tiles(const Request& r, int tpn, int i) {
 // First token block whose tile count exceeds that of block i (or the number of blocks).
 __device__ __forceinline__ int next_step(const Request& r, int tpn, int blocks, int c) {
     // block i counts more than c tiles from (i + 1) tpn > 128 c - (m - n) on
-    const int64_t last = (int64_t(c) * kTile - (r.m - r.n)) / tpn;
-    return static_cast<int>(min(int64_t(blocks), max(last, int64_t(0))));
+    // (c kTile is less than m + kTile, which fits: m is a table's width times its page)
+    return min(blocks, max(c * kTile - (r.m - r.n), 0) / tpn);
 }
 __device__ __forceinline__ int64_t request_tiles(const Request& r, const Args& a) {
     const int blocks = (r.n + a.tpn - 1) / a.tpn;
@@ -176,6 +176,7 @@ struct Shared {
     int block, hblk, at, pad;
     int64_t warp_sum[kThreads / 32];
     float top[2][4][32], sum[2][4][32];   // [column half][lane quarter][column]
+    alignas(16) int sees[64];                 // rows of the cache that each column's token sees
 };
 static_assert(sizeof(Shared) <= Cfg<16>::kMisc, "statistics");
 
@@ -332,24 +333,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ptx::tma_load_2d(s_q + c * C::kQChunk, &tm_q, c * 64, row, bar(sh.q_full));
             }
             const int end = w.end();
+#pragma unroll 1
             for (int tile = w.at; tile < end && ok; ++tile) {
                 const int rows = min(kTile, w.r.m - tile * kTile);
                 const int boxes = rows > 0 ? (rows + a.box - 1) / a.box : 0;
                 int page = 0, in_page = 0;
                 if (lane < boxes) {
-                    const int64_t j = int64_t(tile) * kTile + lane * a.box;
-                    page = __ldg(a.table + w.b * a.width + j / a.page);
-                    in_page = static_cast<int>(j % a.page);
+                    const int j = tile * kTile + lane * a.box, in_table = j / a.page;
+                    page = __ldg(a.table + w.b * a.width + in_table);
+                    in_page = j - in_table * a.page;
                     if (page < 0 || page >= a.pages) {   // nowhere: the box past the last page reads as zeros
                         atomicOr(a.status, kStatusBadValue);
                         page = static_cast<int>(a.pages);
                     }
                 }
                 const uint32_t dst = lane * a.box * 128;
+#pragma unroll 1
                 for (int p = 0; p <= np && ok; ++p) {
                     const bool tail = p == np;
-                    const uint32_t n = tail ? rope : pair;
-                    const uint32_t slots = tail ? C::kRope : C::kPairs, slot = n % slots, phase = (n / slots) & 1u;
+                    const uint32_t slot = tail ? rope % C::kRope : pair % C::kPairs;
+                    const uint32_t phase = (tail ? rope / C::kRope : pair / C::kPairs) & 1u;
                     ok = lat::wait_warp(bar(tail ? sh.rope_empty[slot] : sh.empty[slot]), phase ^ 1u, sync);
                     if (!ok) break;
                     const uint32_t full = bar(tail ? sh.rope_full[slot] : sh.full[slot]);
@@ -374,7 +377,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t kIdS = lat::idesc_f16(128, NR, kBf16, false, false);
         constexpr uint32_t kIdO = lat::idesc_f16(128, NR, kBf16, true, true);
         constexpr uint32_t kPLayout = lat::layout_of(C::kRowBytes);
-        const int rope_steps = (a.R + 15) / 16;
         uint32_t tiles_done = 0;
         bool ok = true;
         do {
@@ -382,53 +384,47 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             ++seg;
             const int end = w.end();
+#pragma unroll 1
             for (int tile = w.at; tile < end; ++tile) {
                 const uint32_t first_pair = pair;
                 const uint32_t rope_slot = rope % C::kRope;
+#pragma unroll 1
                 for (int p = 0; p <= np && ok; ++p) {
                     const bool tail = p == np;
-                    const uint32_t n = tail ? rope : pair;
-                    const uint32_t slots = tail ? C::kRope : C::kPairs, slot = n % slots;
-                    ok = lat::wait_warp(bar(tail ? sh.rope_full[slot] : sh.full[slot]), (n / slots) & 1u, sync);
+                    const uint32_t slot = tail ? rope % C::kRope : pair % C::kPairs;
+                    const uint32_t phase = (tail ? rope / C::kRope : pair / C::kPairs) & 1u;
+                    ok = lat::wait_warp(bar(tail ? sh.rope_full[slot] : sh.full[slot]), phase, sync);
                     if (!ok) break;
                     ptx::tc_fence_after();
-                    if (lane == 0) {
-                        const uint32_t ka = tail ? s_rope + slot * kChunkBytes : s_pairs + slot * 2 * kChunkBytes;
-                        const uint64_t da = ptx::smem_desc(ka, 16, 1024, ptx::kLayoutSw128);
-                        const uint64_t db = ptx::smem_desc(s_q + p * 2 * C::kQChunk, 16, 1024, ptx::kLayoutSw128);
-                        const int steps = tail ? rope_steps : 8;
-                        for (int k = 0; k < steps; ++k)   // 16 columns: 32 bytes on, or the next chunk
-                            lat::mma_f16(tmem + C::kColS, da + (k >> 2) * (kChunkBytes >> 4) + (k & 3) * 2,
-                                         db + (k >> 2) * (C::kQChunk >> 4) + (k & 3) * 2, kIdS, p > 0 || k > 0);
-                    }
-                    __syncwarp();
+                    // 16 columns are 32 bytes; the rotated part is zero from R columns on
+                    const uint32_t at = lat::uniform(tail ? s_rope + slot * kChunkBytes : s_pairs + slot * 2 * kChunkBytes);
+                    const uint64_t da = ptx::smem_desc(at, 16, 1024, ptx::kLayoutSw128);
+                    const uint64_t db = ptx::smem_desc(s_q + p * 2 * C::kQChunk, 16, 1024, ptx::kLayoutSw128);
+                    lat::mma4_f16<2, 2>(tmem + C::kColS, da, db, kIdS, p > 0);
+                    if (!tail) lat::mma4_f16<2, 2>(tmem + C::kColS, da + (kChunkBytes >> 4), db + (C::kQChunk >> 4), kIdS, 1u);
                     if (tail) ++rope;
                     else ++pair;
                 }
                 if (!ok) break;
-                if (lane == 0) {
-                    ptx::tc_commit(bar(sh.s_full));
-                    if (tile + 1 == end) ptx::tc_commit(bar(sh.q_empty));
-                }
-                __syncwarp();
+                ptx::commit_elect(bar(sh.s_full));
+                if (tile + 1 == end) ptx::commit_elect(bar(sh.q_empty));
                 ok = lat::wait_warp(bar(sh.p_full), tiles_done & 1u, sync);
                 if (!ok) break;
                 ++tiles_done;
                 ptx::tc_fence_after();
-                if (lane == 0) {
-                    const uint64_t db = ptx::smem_desc(s_rope + rope_slot * kChunkBytes, 16, 8 * C::kRowBytes, kPLayout);
-                    for (int p = 0; p < np; ++p) {
-                        const uint32_t slot = (first_pair + p) % C::kPairs;
-                        const uint64_t da = ptx::smem_desc(s_pairs + slot * 2 * kChunkBytes, kChunkBytes, 1024, ptx::kLayoutSw128);
-                        for (int k = 0; k < kTile / 16; ++k)
-                            lat::mma_f16(tmem + p * NR, da + k * (2048 >> 4), db + k * ((16 * C::kRowBytes) >> 4), kIdO,
-                                         tile > w.at || k > 0);
-                        ptx::tc_commit(bar(sh.empty[slot]));
-                    }
-                    ptx::tc_commit(bar(sh.rope_empty[rope_slot]));
-                    if (tile + 1 == end) ptx::tc_commit(bar(sh.o_full));
+                const uint32_t more = lat::uniform(tile > w.at ? 1u : 0u);
+                const uint64_t db = ptx::smem_desc(lat::uniform(s_rope + rope_slot * kChunkBytes), 16, 8 * C::kRowBytes, kPLayout);
+                constexpr int kStepB = C::kRowBytes;           // 16 tokens of P, in units of 16 bytes
+#pragma unroll 1
+                for (int p = 0; p < np; ++p) {
+                    const uint32_t slot = lat::uniform((first_pair + p) % C::kPairs);
+                    const uint64_t da = ptx::smem_desc(s_pairs + slot * 2 * kChunkBytes, kChunkBytes, 1024, ptx::kLayoutSw128);
+                    lat::mma4_f16<128, kStepB>(tmem + p * NR, da, db, kIdO, more);
+                    lat::mma4_f16<128, kStepB>(tmem + p * NR, da + 4 * 128, db + 4 * kStepB, kIdO, 1u);
+                    ptx::commit_elect(bar(sh.empty[slot]));
                 }
-                __syncwarp();
+                ptx::commit_elect(bar(sh.rope_empty[rope_slot]));
+                if (tile + 1 == end) ptx::commit_elect(bar(sh.o_full));
             }
         } while (ok && w.next(a));
     } else if (warp >= 2 && any) {
@@ -443,12 +439,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         do {
             const int end = w.end();
             const int first_token = w.block * a.tpn;
-            const int tokens = min(a.tpn, w.r.n - first_token);
             const int low = sees(w.r, first_token);                // rows that every row of the block sees
             float ref = -INFINITY, l[HC];                          // ref: of column `lane`
 #pragma unroll
             for (int j = 0; j < HC; ++j) l[j] = 0.0f;
+            // (the group's barriers of the segment before came after its last reads)
+            if (quarter == 0 && lane < HC)
+                sh.sees[half * HC + lane] = sees(w.r, min(first_token + (a.hb == 1 ? (half * HC + lane) / a.H : 0), w.r.n - 1));
+            lat::named_sync(id, 128);
             bool failed = false;
+#pragma unroll 1
             for (int tile = w.at; tile < end; ++tile) {
                 ok = lat::wait_warp(bar(sh.s_full), tiles_done & 1u, sync);
                 ++tiles_done;
@@ -463,9 +463,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if ((tile + 1) * kTile > low) {
                     // rows past the request's, and rows newer than a query token, are not seen
 #pragma unroll
-                    for (int j = 0; j < HC; ++j) {
-                        const int t = tokens == 1 ? 0 : (half * HC + j) / a.H;
-                        if (token >= sees(w.r, min(first_token + t, w.r.n - 1))) x[j] = -INFINITY;
+                    for (int j = 0; j < HC; j += 4) {
+                        const int4 s = *reinterpret_cast<const int4*>(&sh.sees[half * HC + j]);
+                        if (token >= s.x) x[j] = -INFINITY;
+                        if (token >= s.y) x[j + 1] = -INFINITY;
+                        if (token >= s.z) x[j + 2] = -INFINITY;
+                        if (token >= s.w) x[j + 3] = -INFINITY;
                     }
                 }
                 float top = -INFINITY;
@@ -487,6 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < HC; ++j) l[j] *= __shfl_sync(0xFFFFFFFFu, scale, j);
                     if (tile > w.at) {
+#pragma unroll 1
                         for (int p = 0; p < np; ++p) {
                             uint32_t o[HC];
                             ptx::tmem_ld<HC>(t_o + p * NR, o);
@@ -519,6 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 // Weights past the request's rows are zero, but 0 times what lies there need not be.
                 if (token >= w.r.m) {
+#pragma unroll 1
                     for (int c = half; c < 2 * np; c += 2) {
                         uint4* z = reinterpret_cast<uint4*>(smem + ((pair + c / 2) % C::kPairs) * 2 * kChunkBytes +
                                                             (c & 1) * kChunkBytes + row * 128);
@@ -551,6 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float inv = total > 0.0f ? 1.0f / total : 0.0f;
                 if (a.lse != nullptr && quarter == 0 && lane < HC && col < rows)
                     a.lse[row0 + col] = total > 0.0f ? (ref + log2f(total)) * kLn2 : -INFINITY;
+#pragma unroll 1
                 for (int p = 0; p < np; ++p) {
                     uint32_t o[HC];
                     ptx::tmem_ld<HC>(t_o + p * NR, o);
@@ -576,6 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int64_t part = 2 * int64_t(blockIdx.x) + (w.at > 0 ? 0 : 1);
                 if (quarter == 0 && lane < HC && col < rows) a.stats[part * NR + col] = make_float2(ref, total);
                 float* dst = a.partial + (part * NR + half * HC) * a.L + quarter * 32 + lane;
+#pragma unroll 1
                 for (int p = 0; p < np; ++p) {
                     uint32_t o[HC];
                     ptx::tmem_ld<HC>(t_o + p * NR, o);

@@ -214,28 +214,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t kIdS = lat::idesc_f16(128, kTile, kBf16, false, false);
         const uint32_t id_o = lat::idesc_f16(128, a.N, kBf16, false, true);
         constexpr uint32_t kIdO64 = lat::idesc_f16(128, 64, kBf16, false, true);
-        const int rope_steps = (a.R + 15) / 16;
         bool ok = true;
         auto wait_chunks = [&](uint32_t n, int chunks) {
             for (int c = 0; c < chunks && ok; ++c, ++n) ok = lat::wait_warp(bar(sh.full[n % kSlots]), (n / kSlots) & 1u, sync);
             ptx::tc_fence_after();
         };
-        auto scores = [&](int g, uint32_t n) {   // S of query tile g, keys in chunks n ...
-            if (lane == 0) {
-                for (int c = 0; c < kc; ++c) {
-                    const uint64_t da = ptx::smem_desc(s_q + (g * 3 + c) * kChunkBytes, 16, 1024, ptx::kLayoutSw128);
-                    const uint64_t db = ptx::smem_desc(s_ring + ((n + c) % kSlots) * kChunkBytes, 16, 1024, ptx::kLayoutSw128);
-                    const int steps = c == vc ? rope_steps : 4;
-                    for (int k = 0; k < steps; ++k) lat::mma_f16(tmem + g * 128, da + k * 2, db + k * 2, kIdS, c > 0 || k > 0);
-                }
-                ptx::tc_commit(bar(sh.s_full[g]));
-            }
-            __syncwarp();
+        auto scores = [&](int g, uint32_t at) {   // S of query tile g, keys in chunks at ...
+            const uint32_t n = lat::uniform(at);
+            for (int c = 0; c < kc; ++c)     // (the rotated part is zero from R columns on)
+                lat::mma4_f16<2, 2>(tmem + g * 128, ptx::smem_desc(s_q + (g * 3 + c) * kChunkBytes, 16, 1024, ptx::kLayoutSw128),
+                                    ptx::smem_desc(s_ring + ((n + c) % kSlots) * kChunkBytes, 16, 1024, ptx::kLayoutSw128), kIdS, c > 0);
+            ptx::commit_elect(bar(sh.s_full[g]));
         };
         auto release = [&](uint32_t n, int chunks) {
-            if (lane == 0)
-                for (int c = 0; c < chunks; ++c) ptx::tc_commit(bar(sh.empty[(n + c) % kSlots]));
-            __syncwarp();
+            for (int c = 0; c < chunks; ++c) ptx::commit_elect(bar(sh.empty[lat::uniform((n + c) % kSlots)]));
         };
         for (int g = 0; g < 2 && ok; ++g) {
             if (count[g] == 0) continue;
@@ -251,23 +243,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (t < count[g] && ok) {
                     ok = lat::wait_warp(bar(sh.p_full[g]), t & 1u, sync);
                     if (ok) wait_chunks(nv, vc);
-                    if (ok && lane == 0) {
+                    if (ok) {
                         const uint32_t o = tmem + 256 + g * 128, p = tmem + g * 128;
-                        const uint32_t s0 = nv % kSlots, s1 = (nv + 1) % kSlots;
+                        const uint32_t s0 = lat::uniform(nv % kSlots), s1 = lat::uniform((nv + 1) % kSlots), more = lat::uniform(t > 0 ? 1u : 0u);
                         const uint64_t d0 = ptx::smem_desc(s_ring + s0 * kChunkBytes, kChunkBytes, 1024, ptx::kLayoutSw128);
                         if (vc == 1 || s1 == s0 + 1) {
-                            for (int k = 0; k < kTile / 16; ++k)
-                                lat::mma_f16_ts(o, p + k * 8, d0 + k * (2048 >> 4), id_o, t > 0 || k > 0);
+                            lat::mma4_f16_ts<128>(o, p, d0, id_o, more);
+                            lat::mma4_f16_ts<128>(o, p + 32, d0 + 512, id_o, 1u);
                         } else {   // the two chunks of values at the ring's two ends
                             const uint64_t d1 = ptx::smem_desc(s_ring + s1 * kChunkBytes, kChunkBytes, 1024, ptx::kLayoutSw128);
-                            for (int k = 0; k < kTile / 16; ++k) {
-                                lat::mma_f16_ts(o, p + k * 8, d0 + k * (2048 >> 4), kIdO64, t > 0 || k > 0);
-                                lat::mma_f16_ts(o + 64, p + k * 8, d1 + k * (2048 >> 4), kIdO64, t > 0 || k > 0);
-                            }
+                            lat::mma4_f16_ts<128>(o, p, d0, kIdO64, more);
+                            lat::mma4_f16_ts<128>(o, p + 32, d0 + 512, kIdO64, 1u);
+                            lat::mma4_f16_ts<128>(o + 64, p, d1, kIdO64, more);
+                            lat::mma4_f16_ts<128>(o + 64, p + 32, d1 + 512, kIdO64, 1u);
                         }
-                        if (t + 1 == count[g]) ptx::tc_commit(bar(sh.o_full[g]));
+                        if (t + 1 == count[g]) ptx::commit_elect(bar(sh.o_full[g]));
                     }
-                    __syncwarp();
                 }
                 if (t + 1 < count[g] && ok) {
                     wait_chunks(nk, kc);

@@ -9,20 +9,45 @@
 namespace sgq {
 namespace lat {
 
-// D[tmem] (+)= A[smem] B[smem]^T, 16-bit operands, fp32 accumulator.
-__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// A value that is the same in all lanes, in a form that the compiler knows to
+// be (MMA operands sit in uniform registers; without it every MMA is wrapped
+// in code that makes them so, at twice an MMA's time).
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xFFFFFFFFu, x, 0); }
+
+// Four MMAs D[tmem] (+)= A B^T of K = 16 each, 16-bit operands in shared
+// memory, fp32 accumulator: descriptors kA and kB (units of 16 bytes) apart,
+// the first one starting over where acc == 0.  Executed by a converged warp,
+// issued by its elected lane: from a branch of one lane an MMA took 90 to 170
+// cycles to issue, several times its execution.
+template <int kA, int kB>
+__device__ __forceinline__ void mma4_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "{\n.reg .pred e, q, t;\n.reg .b64 a1, a2, a3, b1, b2, b3;\n"
+        "elect.sync _|e, 0xffffffff;\n"
+        "setp.ne.b32 q, %4, 0;\nsetp.eq.u32 t, %0, %0;\n"
+        "add.s64 a1, %1, %5;\nadd.s64 a2, %1, %6;\nadd.s64 a3, %1, %7;\n"
+        "add.s64 b1, %2, %8;\nadd.s64 b2, %2, %9;\nadd.s64 b3, %2, %10;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, q;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc), "n"(kA), "n"(2 * kA), "n"(3 * kA), "n"(kB), "n"(2 * kB), "n"(3 * kB)
         : "memory");
 }
 // The same with A in TMEM (row i in lane i, two elements a 32-bit column).
-__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+template <int kB>
+__device__ __forceinline__ void mma4_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "{\n.reg .pred e, q, t;\n.reg .b32 a1, a2, a3;\n.reg .b64 b1, b2, b3;\n"
+        "elect.sync _|e, 0xffffffff;\n"
+        "setp.ne.b32 q, %4, 0;\nsetp.eq.u32 t, %0, %0;\n"
+        "add.u32 a1, %1, 8;\nadd.u32 a2, %1, 16;\nadd.u32 a3, %1, 24;\n"
+        "add.s64 b1, %2, %5;\nadd.s64 b2, %2, %6;\nadd.s64 b3, %2, %7;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, q;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc), "n"(kB), "n"(2 * kB), "n"(3 * kB)
         : "memory");
 }
 // Instruction descriptor, kind::f16: fp32 D; both operands bf16 or both fp16;
@@ -102,34 +127,34 @@ __device__ __forceinline__ bool named_any(int id, int threads, bool x) {
 // Bounded waits: a wait that runs out raises the CTA's abort flag and the
 // device status; every other wait of the CTA then gives up as well.
 constexpr uint32_t kStatusTimeout = 1u;
-constexpr uint64_t kTimeoutNs = 2000000000ull;
-constexpr uint64_t kAbortPollNs = 1000000ull;
+constexpr long long kTimeoutClocks = 4000000000ll;    // about 2 s
+constexpr long long kAbortPollClocks = 2000000ll;
 struct Sync {
     volatile uint32_t* abort_flag;
     uint32_t* status;
 };
+// The whole warp waits for a phase; false: gave up.  All lanes poll together:
+// a warp whose lane 0 went through a polling loop alone stayed split in two
+// afterwards, and its MMA issue slowed down three to four times.
 static __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, const Sync& s) {
-    const uint64_t t0 = ptx::globaltimer();
+    const long long t0 = clock64();
     for (uint32_t spins = 1;; ++spins) {
-        if (ptx::mbar_try_wait(bar, parity)) return true;
-        if ((spins & 15u) == 0) {
-            const uint64_t dt = ptx::globaltimer() - t0;
-            if (dt > kAbortPollNs && *s.abort_flag) return false;
-            if (dt > kTimeoutNs) {
+        if (__all_sync(0xFFFFFFFFu, ptx::mbar_try_wait(bar, parity))) return true;
+        if ((spins & 63u) == 0) {
+            const long long dt = clock64() - t0;
+            if (__any_sync(0xFFFFFFFFu, dt > kTimeoutClocks)) {
                 *s.abort_flag = 1u;
-                atomicOr(s.status, kStatusTimeout);
+                if ((threadIdx.x & 31) == 0) atomicOr(s.status, kStatusTimeout);
+                __syncwarp();
                 return false;
             }
+            if (__any_sync(0xFFFFFFFFu, dt > kAbortPollClocks && *s.abort_flag)) return false;
         }
     }
 }
-// The whole warp waits for a phase; false: gave up.
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const Sync& s) {
-    uint32_t ok = 1;
-    if ((threadIdx.x & 31) == 0 && !ptx::mbar_try_wait(bar, parity)) ok = wait_slow(bar, parity, s) ? 1u : 0u;
-    ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-    __syncwarp();
-    return ok != 0;
+    if (__all_sync(0xFFFFFFFFu, ptx::mbar_try_wait(bar, parity))) return true;
+    return wait_slow(bar, parity, s);
 }
 
 }  // namespace lat
