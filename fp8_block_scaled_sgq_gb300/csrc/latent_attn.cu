@@ -22,9 +22,9 @@
 // columns with 128-byte swizzle: read K-major for S^T and, by the descriptor's
 // other operand order, MN-major for O^T.  Chunks of the latent part come in
 // pairs (128 columns, one MMA's M) through a ring; the rotated part has a slot
-// of its own, which takes P once S^T is done.  Warps: 0 loads (TMA, one box a
-// run of rows inside a page), 1 issues MMAs, 2 to 9 do softmax: thread = token,
-// two warps a TMEM lane quarter, half of the columns each.
+// of its own, which takes P once S^T is done.  Warps: 0 issues MMAs, 1 to 3
+// load (TMA, one box a run of rows inside a page), the others do softmax:
+// thread = token, groups of four warps with a share of the columns each.
 //
 // Work: the tiles of all (request, row block) items, in order, are cut into
 // equal runs, one a CTA, from the lengths on the device.  An item that a cut
@@ -46,12 +46,13 @@ namespace {
 
 using lat::Pair;
 
-constexpr int kThreads = 320;
 constexpr int kTile = 128;                    // cached rows a tile
 constexpr int kChunkBytes = kTile * 128;      // 64 columns of a tile
 constexpr int kMaxPairs = 5, kMaxRope = 2;
+constexpr int kLoaders = 3;                   // warps that issue loads: one alone keeps a third of this rate
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
-constexpr float kGrow = 8.0f;                 // powers of two the maximum may outgrow the reference by
+constexpr float kGrow = 8.0f;                 // powers of two a score may outgrow the reference by
+constexpr float kNone = -1.0e38f;             // reference of a row that has seen nothing
 
 template <int NR>
 struct Cfg {
@@ -61,15 +62,18 @@ struct Cfg {
     static constexpr int kOffRope = kPairs * 2 * kChunkBytes;
     static constexpr int kOffQ = kOffRope + kRope * kChunkBytes;
     static constexpr int kOffMisc = kOffQ + 9 * kQChunk;
-    static constexpr int kMisc = 2816;                     // barriers, schedule, statistics
+    static constexpr int kMisc = 3584;                     // barriers, schedule, statistics
     static constexpr int kSmem = kOffMisc + kMisc + 1024;  // alignment slack
-    static constexpr int kHalf = NR / 2;                   // columns a softmax warp
+    static constexpr int kGroups = NR == 64 ? 4 : 2;       // groups of four softmax warps, a share of the columns each
+    static constexpr int kThreads = 128 + kGroups * 128;
+    static constexpr int kHC = NR / kGroups;               // columns a softmax warp
     static constexpr int kRowBytes = NR * 2;               // a token's row of P
     static constexpr uint32_t kColS = 4 * NR;
     static_assert(kSmem <= 232448, "shared memory");
 };
 
 struct Args {
+    const char* cache;
     const int32_t* table;
     const int32_t* kv_lens;
     const int32_t* q_starts;
@@ -79,7 +83,8 @@ struct Args {
     float2* stats;       // [2 grid][NR]: reference, sum
     int4* joins;         // [grid]: first row, rows, parts (0: nothing to join)
     uint32_t* status;
-    int64_t T, B, pages, width;
+    int64_t T, B, pages, width, c_page, c_row;   // strides in bytes
+    uint32_t box_bytes;
     int H, L, R, page, box;
     int tpn, hb;         // tokens an item, items a token (one of them is 1)
     float scale2;        // scale log2(e)
@@ -87,23 +92,22 @@ struct Args {
 
 // One request: its query tokens [t0, t0 + n) and cached rows m.
 struct Request {
-    int64_t t0;
-    int n, m;
+    int t0, n, m;
 };
-__device__ __forceinline__ Request request(const Args& a, int64_t b, bool report) {
+__device__ __forceinline__ Request request(const Args& a, int b, bool report) {
     Request r;
     if (a.q_starts == nullptr) {
         r.t0 = b;
         r.n = 1;
     } else {
-        const int64_t s = a.q_starts[b], e = a.q_starts[b + 1];
-        r.t0 = min(max(s, int64_t(0)), a.T);
-        r.n = static_cast<int>(min(max(e, r.t0), a.T) - r.t0);
+        const int s = a.q_starts[b], e = a.q_starts[b + 1], T = static_cast<int>(a.T);
+        r.t0 = min(max(s, 0), T);
+        r.n = min(max(e, r.t0), T) - r.t0;
         if (report && (r.t0 != s || r.t0 + r.n != e || (b == 0 && s != 0) || (b == a.B - 1 && e != a.T)))
             atomicOr(a.status, kStatusBadValue);
     }
-    const int64_t m = a.kv_lens[b], most = a.width * a.page;
-    r.m = static_cast<int>(min(max(m, int64_t(0)), most));
+    const int m = a.kv_lens[b], most = static_cast<int>(a.width * a.page);
+    r.m = min(max(m, 0), most);
     if (report && r.m != m) atomicOr(a.status, kStatusBadValue);
     return r;
 }
@@ -134,8 +138,7 @@ __device__ __forceinline__ int64_t request_tiles(const Request& r, const Args& a
 
 // A CTA's run of tiles: item (b, block, head block), tile `at` of its `count`.
 struct Walk {
-    int64_t b;
-    int block, hblk, at, count;
+    int b, block, hblk, at, count;
     int64_t left;        // tiles of the run from here on
     Request r;
     __device__ __forceinline__ void settle(const Args& a) { count = tiles(r, a.tpn, block); }
@@ -158,7 +161,7 @@ struct Walk {
         return true;
     }
     __device__ __forceinline__ int64_t row0(const Args& a) const {
-        return (r.t0 + int64_t(block) * a.tpn) * a.H + hblk * ((a.H + a.hb - 1) / a.hb);
+        return (int64_t(r.t0) + block * a.tpn) * a.H + hblk * ((a.H + a.hb - 1) / a.hb);
     }
     __device__ __forceinline__ int rows(const Args& a) const {
         if (a.hb == 1) return min(a.tpn, r.n - block * a.tpn) * a.H;
@@ -172,21 +175,23 @@ struct Shared {
     uint64_t q_full, q_empty, s_full, p_full, o_full, drain;
     uint32_t tmem, abort;
     // the schedule: totals of the threads' requests, then the CTA's start
-    int64_t b, per, total;
-    int block, hblk, at, pad;
-    int64_t warp_sum[kThreads / 32];
-    float top[2][4][32], sum[2][4][32];   // [column half][lane quarter][column]
+    int64_t per, total;
+    int b, block, hblk, at;
+    int64_t warp_sum[20];
+    alignas(16) float ref[4][16], fade[4][16];   // [column group][column]: new reference, 2^(old - new)
+    float top[4][4][16], sum[4][4][16];          // [column group][lane quarter][column]
     alignas(16) int sees[64];                 // rows of the cache that each column's token sees
 };
 static_assert(sizeof(Shared) <= Cfg<16>::kMisc, "statistics");
 
 // Where this CTA's run starts; every thread takes part.  Thread i adds up the
 // requests [i k, (i + 1) k); the one whose span holds the start walks it again.
+template <int kThreads>
 __device__ __forceinline__ void plan(const Args& a, Shared& sh) {
-    const int64_t k = (a.B + kThreads - 1) / kThreads;
-    const int64_t b0 = min(a.B, threadIdx.x * k), b1 = min(a.B, b0 + k);
+    const int B = static_cast<int>(a.B), k = (B - 1) / kThreads + 1;
+    const int b0 = static_cast<int>(min(int64_t(B), int64_t(threadIdx.x) * k)), b1 = min(B - b0, k) + b0;
     int64_t mine = 0;
-    for (int64_t b = b0; b < b1; ++b) mine += request_tiles(request(a, b, blockIdx.x == 0), a);
+    for (int b = b0; b < b1; ++b) mine += request_tiles(request(a, b, blockIdx.x == 0), a);
     int64_t scan = mine;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -205,7 +210,7 @@ __device__ __forceinline__ void plan(const Args& a, Shared& sh) {
     const int64_t start = per * blockIdx.x;
     int64_t at = scan - mine;
     if (start >= at && start < scan) {
-        for (int64_t b = b0; b < b1; ++b) {
+        for (int b = b0; b < b1; ++b) {
             const Request r = request(a, b, false);
             const int64_t n = request_tiles(r, a);
             if (start >= at + n) {
@@ -259,11 +264,11 @@ __device__ __forceinline__ float lane_sums(float (&v)[N]) {
 }
 
 template <typename T, int NR>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
     latent_attention_kernel(const __grid_constant__ CUtensorMap tm_cache, const __grid_constant__ CUtensorMap tm_q,
                             const Args a) {
     using C = Cfg<NR>;
-    constexpr int HC = C::kHalf;
+    constexpr int HC = C::kHC;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     extern __shared__ uint8_t raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
@@ -285,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::mbar_init(bar(sh.q_full), 1);
         ptx::mbar_init(bar(sh.q_empty), 1);
         ptx::mbar_init(bar(sh.s_full), 1);
-        ptx::mbar_init(bar(sh.p_full), 8);
+        ptx::mbar_init(bar(sh.p_full), 4 * C::kGroups);
         ptx::mbar_init(bar(sh.o_full), 1);
         ptx::mbar_init(bar(sh.drain), 1);
         sh.abort = 0;
@@ -293,19 +298,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::prefetch_tmap(&tm_cache);
         ptx::prefetch_tmap(&tm_q);
     }
-    if (warp == 1) {
+    if (warp == 0) {
         ptx::tmem_alloc(ptx::smem_u32(&sh.tmem), 512);
         ptx::tmem_relinquish();
     }
     ptx::launch_dependents();
     ptx::grid_dependency_wait();
     ptx::tc_fence_before();
-    plan(a, sh);
+    plan<C::kThreads>(a, sh);
     ptx::tc_fence_after();
     const uint32_t tmem = sh.tmem;
     const int np = a.L / 128;                       // pairs of latent chunks a tile
 
-    if (threadIdx.x == 64) a.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (threadIdx.x == 128) a.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
     Walk w;
     w.left = min(sh.per, sh.total - sh.per * blockIdx.x);
     const bool any = w.left > 0;
@@ -319,64 +324,100 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 
     uint32_t pair = 0, rope = 0, seg = 0;            // slots and segments used so far
-    if (warp == 0 && any) {
+    if (warp >= 1 && warp < 1 + kLoaders && any) {
         // ------------------------------------------------------------ loads
+        // Pairs go to the loading warps in turn, the rotated parts all to the last one.  A wait for a
+        // slot's release tells phases apart by parity, so no loader may be two uses of a slot ahead:
+        // the rotated parts' loader waits for every release in order; a loader of pair n has loaded
+        // pair n - kLoaders, so pair n - kLoaders - kPairs is released, which is later than the
+        // slot's use before the awaited one, n - 2 kPairs.
+        static_assert(C::kPairs > kLoaders, "parity of the pairs' releases");
+        const int id = warp - 1;
+        int turn = 0;
         bool ok = true;
-        do {
-            ok = lat::wait_warp(bar(sh.q_empty), (seg & 1u) ^ 1u, sync);
-            if (!ok) break;
-            ++seg;
-            if (lane == 0) {
-                ptx::mbar_arrive_expect_tx(bar(sh.q_full), (2 * np + 1) * C::kQChunk);
-                const int row = static_cast<int>(w.row0(a));
-                for (int c = 0; c <= 2 * np; ++c)
-                    ptx::tma_load_2d(s_q + c * C::kQChunk, &tm_q, c * 64, row, bar(sh.q_full));
+        // Lane i's box of a tile: rows [i box, (i + 1) box), inside one page.
+        auto locate = [&](int tile, int& boxes, int& page, int& in_page) {
+            const int rows = min(kTile, w.r.m - tile * kTile);
+            boxes = rows > 0 ? (rows + a.box - 1) / a.box : 0;
+            page = in_page = 0;
+            if (lane < boxes) {
+                const int j = tile * kTile + lane * a.box, in_table = j / a.page;
+                page = __ldg(a.table + int64_t(w.b) * a.width + in_table);
+                in_page = j - in_table * a.page;
             }
+        };
+        do {
             const int end = w.end();
+            int boxes, page, in_page, next_boxes = 0, next_page = 0, next_in = 0;
+            locate(w.at, boxes, page, in_page);
+            if (id == 0) {
+                ok = lat::wait_warp(bar(sh.q_empty), (seg & 1u) ^ 1u, sync);
+                if (!ok) break;
+                if (lane == 0) {
+                    ptx::mbar_arrive_expect_tx(bar(sh.q_full), (2 * np + 1) * C::kQChunk);
+                    const int row = static_cast<int>(w.row0(a));
+#pragma unroll 1
+                    for (int c = 0; c <= 2 * np; ++c)
+                        ptx::tma_load_2d(s_q + c * C::kQChunk, &tm_q, c * 64, row, bar(sh.q_full));
+                }
+                __syncwarp();
+            }
+            ++seg;
 #pragma unroll 1
             for (int tile = w.at; tile < end && ok; ++tile) {
-                const int rows = min(kTile, w.r.m - tile * kTile);
-                const int boxes = rows > 0 ? (rows + a.box - 1) / a.box : 0;
-                int page = 0, in_page = 0;
-                if (lane < boxes) {
-                    const int j = tile * kTile + lane * a.box, in_table = j / a.page;
-                    page = __ldg(a.table + w.b * a.width + in_table);
-                    in_page = j - in_table * a.page;
-                    if (page < 0 || page >= a.pages) {   // nowhere: the box past the last page reads as zeros
-                        atomicOr(a.status, kStatusBadValue);
-                        page = static_cast<int>(a.pages);
-                    }
+                if (lane < boxes && (page < 0 || page >= a.pages)) {   // nowhere: the box past the last page reads as zeros
+                    atomicOr(a.status, kStatusBadValue);
+                    page = static_cast<int>(a.pages);
+                }
+                if (tile + 1 < end) {
+                    // The next tile goes to L2 while this one's loads wait for their slots.
+                    locate(tile + 1, next_boxes, next_page, next_in);
+                    if (id == 0 && lane < next_boxes && next_page >= 0 && next_page < a.pages)
+                        lat::bulk_prefetch(a.cache + next_page * a.c_page + next_in * a.c_row, a.box_bytes);
                 }
                 const uint32_t dst = lane * a.box * 128;
 #pragma unroll 1
-                for (int p = 0; p <= np && ok; ++p) {
-                    const bool tail = p == np;
-                    const uint32_t slot = tail ? rope % C::kRope : pair % C::kPairs;
-                    const uint32_t phase = (tail ? rope / C::kRope : pair / C::kPairs) & 1u;
-                    ok = lat::wait_warp(bar(tail ? sh.rope_empty[slot] : sh.empty[slot]), phase ^ 1u, sync);
+                for (int p = 0; p < np; ++p, ++pair, turn = turn + 1 == kLoaders ? 0 : turn + 1) {
+                    if (turn != id) continue;
+                    const uint32_t slot = pair % C::kPairs, full = bar(sh.full[slot]);
+                    ok = lat::wait_warp(bar(sh.empty[slot]), ((pair / C::kPairs) & 1u) ^ 1u, sync);
                     if (!ok) break;
-                    const uint32_t full = bar(tail ? sh.rope_full[slot] : sh.full[slot]);
-                    if (lane == 0) ptx::mbar_arrive_expect_tx(full, boxes * a.box * (tail ? 128 : 256));
+                    if (lane == 0) ptx::mbar_arrive_expect_tx(full, boxes * a.box * 256);
                     __syncwarp();
-                    if (tail) {
-                        if (lane < boxes) lat::tma_load_3d(s_rope + slot * kChunkBytes + dst, &tm_cache, a.L, in_page, page, full);
-                        ++rope;
-                    } else {
-                        if (lane < boxes) {
-                            const uint32_t to = s_pairs + slot * 2 * kChunkBytes + dst;
-                            lat::tma_load_3d(to, &tm_cache, p * 128, in_page, page, full);
-                            lat::tma_load_3d(to + kChunkBytes, &tm_cache, p * 128 + 64, in_page, page, full);
-                        }
-                        ++pair;
+                    if (lane < boxes) {
+                        const uint32_t to = s_pairs + slot * 2 * kChunkBytes + dst;
+                        lat::tma_load_3d(to, &tm_cache, p * 128, in_page, page, full);
+                        lat::tma_load_3d(to + kChunkBytes, &tm_cache, p * 128 + 64, in_page, page, full);
                     }
+                    __syncwarp();
                 }
+                if (!ok) break;
+                if (id == kLoaders - 1) {
+                    const uint32_t slot = rope % C::kRope, full = bar(sh.rope_full[slot]);
+                    ok = lat::wait_warp(bar(sh.rope_empty[slot]), ((rope / C::kRope) & 1u) ^ 1u, sync);
+                    if (!ok) break;
+                    if (lane == 0) ptx::mbar_arrive_expect_tx(full, boxes * a.box * 128);
+                    __syncwarp();
+                    if (lane < boxes) lat::tma_load_3d(s_rope + slot * kChunkBytes + dst, &tm_cache, a.L, in_page, page, full);
+                    __syncwarp();
+                }
+                ++rope;
+                boxes = next_boxes;
+                page = next_page;
+                in_page = next_in;
             }
         } while (ok && w.next(a));
-    } else if (warp == 1 && any) {
+    } else if (warp == 0 && any) {
         // ------------------------------------------------------------ MMAs
         constexpr uint32_t kIdS = lat::idesc_f16(128, NR, kBf16, false, false);
         constexpr uint32_t kIdO = lat::idesc_f16(128, NR, kBf16, true, true);
-        constexpr uint32_t kPLayout = lat::layout_of(C::kRowBytes);
+        constexpr uint32_t kHiK = lat::desc_hi(1024, ptx::kLayoutSw128);                               // rows of 128 bytes
+        constexpr uint32_t kHiP = lat::desc_hi(8 * C::kRowBytes, lat::layout_of(C::kRowBytes));
+        constexpr uint32_t kPair = 2 * kChunkBytes >> 4, kChunk = kChunkBytes >> 4, kQ = C::kQChunk >> 4;
+        constexpr int kStepP = C::kRowBytes;                       // 16 tokens of P, in units of 16 bytes
+        const uint32_t lo_k = lat::uniform(lat::desc_lo(s_pairs, 16)), lo_v = lat::uniform(lat::desc_lo(s_pairs, kChunkBytes));
+        const uint32_t lo_r = lat::uniform(lat::desc_lo(s_rope, 16)), lo_q = lat::uniform(lat::desc_lo(s_q, 16));
+        const uint32_t t_o = lat::uniform(tmem), t_s = t_o + C::kColS;
         uint32_t tiles_done = 0;
         bool ok = true;
         do {
@@ -386,66 +427,70 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int end = w.end();
 #pragma unroll 1
             for (int tile = w.at; tile < end; ++tile) {
-                const uint32_t first_pair = pair;
-                const uint32_t rope_slot = rope % C::kRope;
+                const uint32_t first = lat::uniform(pair % C::kPairs), rope_slot = lat::uniform(rope % C::kRope);
+                uint32_t slot = first, phase = (pair / C::kPairs) & 1u;
 #pragma unroll 1
-                for (int p = 0; p <= np && ok; ++p) {
-                    const bool tail = p == np;
-                    const uint32_t slot = tail ? rope % C::kRope : pair % C::kPairs;
-                    const uint32_t phase = (tail ? rope / C::kRope : pair / C::kPairs) & 1u;
-                    ok = lat::wait_warp(bar(tail ? sh.rope_full[slot] : sh.full[slot]), phase, sync);
-                    if (!ok) break;
-                    ptx::tc_fence_after();
-                    // 16 columns are 32 bytes; the rotated part is zero from R columns on
-                    const uint32_t at = lat::uniform(tail ? s_rope + slot * kChunkBytes : s_pairs + slot * 2 * kChunkBytes);
-                    const uint64_t da = ptx::smem_desc(at, 16, 1024, ptx::kLayoutSw128);
-                    const uint64_t db = ptx::smem_desc(s_q + p * 2 * C::kQChunk, 16, 1024, ptx::kLayoutSw128);
-                    lat::mma4_f16<2, 2>(tmem + C::kColS, da, db, kIdS, p > 0);
-                    if (!tail) lat::mma4_f16<2, 2>(tmem + C::kColS, da + (kChunkBytes >> 4), db + (C::kQChunk >> 4), kIdS, 1u);
-                    if (tail) ++rope;
-                    else ++pair;
+                for (int p = 0; p < np && ok; ++p) {               // S^T, 128 columns at a time
+                    ok = lat::wait_warp(bar(sh.full[slot]), phase, sync);
+                    const uint32_t da = lo_k + slot * kPair, db = lo_q + p * 2 * kQ;
+                    lat::mma4_f16<2, 2>(t_s, da, kHiK, db, kHiK, kIdS, p > 0);
+                    lat::mma4_f16<2, 2>(t_s, da + kChunk, kHiK, db + kQ, kHiK, kIdS, 1u);
+                    if (++slot == C::kPairs) {
+                        slot = 0;
+                        phase ^= 1u;
+                    }
                 }
+                if (ok) ok = lat::wait_warp(bar(sh.rope_full[rope_slot]), (rope / C::kRope) & 1u, sync);
                 if (!ok) break;
+                // (the rotated part is zero from R columns on)
+                lat::mma4_f16<2, 2>(t_s, lo_r + rope_slot * kChunk, kHiK, lo_q + np * 2 * kQ, kHiK, kIdS, 1u);
                 ptx::commit_elect(bar(sh.s_full));
                 if (tile + 1 == end) ptx::commit_elect(bar(sh.q_empty));
+                pair += np;
+                ++rope;
                 ok = lat::wait_warp(bar(sh.p_full), tiles_done & 1u, sync);
                 if (!ok) break;
                 ++tiles_done;
                 ptx::tc_fence_after();
-                const uint32_t more = lat::uniform(tile > w.at ? 1u : 0u);
-                const uint64_t db = ptx::smem_desc(lat::uniform(s_rope + rope_slot * kChunkBytes), 16, 8 * C::kRowBytes, kPLayout);
-                constexpr int kStepB = C::kRowBytes;           // 16 tokens of P, in units of 16 bytes
+                const uint32_t more = lat::uniform(tile > w.at ? 1u : 0u), db = lat::uniform(lat::desc_lo(s_rope + rope_slot * kChunkBytes, 16));
+                slot = first;
 #pragma unroll 1
-                for (int p = 0; p < np; ++p) {
-                    const uint32_t slot = lat::uniform((first_pair + p) % C::kPairs);
-                    const uint64_t da = ptx::smem_desc(s_pairs + slot * 2 * kChunkBytes, kChunkBytes, 1024, ptx::kLayoutSw128);
-                    lat::mma4_f16<128, kStepB>(tmem + p * NR, da, db, kIdO, more);
-                    lat::mma4_f16<128, kStepB>(tmem + p * NR, da + 4 * 128, db + 4 * kStepB, kIdO, 1u);
+                for (int p = 0; p < np; ++p) {                     // O^T, 128 rows at a time
+                    const uint32_t da = lo_v + slot * kPair, d = t_o + p * NR;
+                    lat::mma4_f16<128, kStepP>(d, da, kHiK, db, kHiP, kIdO, more);
+                    lat::mma4_f16<128, kStepP>(d, da + 4 * 128, kHiK, db + 4 * kStepP, kHiP, kIdO, 1u);
                     ptx::commit_elect(bar(sh.empty[slot]));
+                    if (++slot == C::kPairs) slot = 0;
                 }
                 ptx::commit_elect(bar(sh.rope_empty[rope_slot]));
                 if (tile + 1 == end) ptx::commit_elect(bar(sh.o_full));
             }
         } while (ok && w.next(a));
-    } else if (warp >= 2 && any) {
+    } else if (warp > kLoaders && any) {
         // ------------------------------------------------------------ softmax
-        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        const int quarter = warp & 3, group = (warp - 1 - kLoaders) >> 2;
         const int row = quarter * 32 + lane;                      // token of the tile
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-        const uint32_t t_s = tmem + lanes + C::kColS + half * HC, t_o = tmem + lanes + half * HC;
-        const int id = 1 + half;
+        const uint32_t t_s = tmem + lanes + C::kColS + group * HC, t_o = tmem + lanes + group * HC;
+        const int id = 1 + group;
         uint32_t tiles_done = 0;
         bool ok = true;
         do {
             const int end = w.end();
             const int first_token = w.block * a.tpn;
             const int low = sees(w.r, first_token);                // rows that every row of the block sees
-            float ref = -INFINITY, l[HC];                          // ref: of column `lane`
+            // l, ref: sum and reference of every column, the sums of this thread's token only
+            float ref[HC], l[HC];
 #pragma unroll
-            for (int j = 0; j < HC; ++j) l[j] = 0.0f;
+            for (int j = 0; j < HC; ++j) {
+                l[j] = 0.0f;
+                ref[j] = kNone;
+            }
             // (the group's barriers of the segment before came after its last reads)
-            if (quarter == 0 && lane < HC)
-                sh.sees[half * HC + lane] = sees(w.r, min(first_token + (a.hb == 1 ? (half * HC + lane) / a.H : 0), w.r.n - 1));
+            if (quarter == 0 && lane < HC) {
+                sh.ref[group][lane] = kNone;
+                sh.sees[group * HC + lane] = sees(w.r, min(first_token + (a.hb == 1 ? (group * HC + lane) / a.H : 0), w.r.n - 1));
+            }
             lat::named_sync(id, 128);
             bool failed = false;
 #pragma unroll 1
@@ -456,67 +501,78 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t raw_s[HC];
                 ptx::tmem_ld<HC>(t_s, raw_s);
                 ptx::tmem_wait_ld();
-                float x[HC];
-#pragma unroll
-                for (int j = 0; j < HC; ++j) x[j] = __uint_as_float(raw_s[j]) * a.scale2;
                 const int token = tile * kTile + row;
                 if ((tile + 1) * kTile > low) {
                     // rows past the request's, and rows newer than a query token, are not seen
 #pragma unroll
                     for (int j = 0; j < HC; j += 4) {
-                        const int4 s = *reinterpret_cast<const int4*>(&sh.sees[half * HC + j]);
-                        if (token >= s.x) x[j] = -INFINITY;
-                        if (token >= s.y) x[j + 1] = -INFINITY;
-                        if (token >= s.z) x[j + 2] = -INFINITY;
-                        if (token >= s.w) x[j + 3] = -INFINITY;
+                        const int4 s = *reinterpret_cast<const int4*>(&sh.sees[group * HC + j]);
+                        if (token >= s.x) raw_s[j] = __float_as_uint(-INFINITY);
+                        if (token >= s.y) raw_s[j + 1] = __float_as_uint(-INFINITY);
+                        if (token >= s.z) raw_s[j + 2] = __float_as_uint(-INFINITY);
+                        if (token >= s.w) raw_s[j + 3] = __float_as_uint(-INFINITY);
                     }
                 }
-                float top = -INFINITY;
+                // Weights with the references as they are; if some score is past its reference by
+                // more than 2^kGrow (or is the first one seen), all of the group move them first.
+                uint32_t packed[HC / 2];
+                float p[HC], most = -INFINITY;
 #pragma unroll
                 for (int j = 0; j < HC; ++j) {
-                    const float m = lat::warp_max(x[j]);
-                    if ((lane & (HC - 1)) == j) top = m;
+                    p[j] = fmaf(__uint_as_float(raw_s[j]), a.scale2, -ref[j]);
+                    most = fmaxf(most, p[j]);
                 }
-                if (lane < HC) sh.top[half][quarter][lane] = top;
-                failed = lat::named_any(id, 128, !ok);
-                if (failed) break;
-                const float4 tops = make_float4(sh.top[half][0][lane & (HC - 1)], sh.top[half][1][lane & (HC - 1)],
-                                                sh.top[half][2][lane & (HC - 1)], sh.top[half][3][lane & (HC - 1)]);
-                top = fmaxf(fmaxf(tops.x, tops.y), fmaxf(tops.z, tops.w));
-                const bool grow = top > ref + kGrow || (ref == -INFINITY && top > -INFINITY);
-                if (__any_sync(0xFFFFFFFFu, grow)) {
-                    const float scale = grow ? lat::ex2(ref - top) : 1.0f;   // 0 where there was nothing before
-                    if (grow) ref = top;
 #pragma unroll
-                    for (int j = 0; j < HC; ++j) l[j] *= __shfl_sync(0xFFFFFFFFu, scale, j);
+                for (int j = 0; j < HC; ++j) p[j] = lat::ex2(p[j]);
+                const bool move = lat::named_any(id, 128, most > kGrow || !ok);
+                if (move) {
+                    float top = kNone;                             // of column cl
+                    const int cl = lane & (HC - 1);
+#pragma unroll
+                    for (int j = 0; j < HC; ++j) {
+                        const float m = lat::warp_max(__uint_as_float(raw_s[j]) * a.scale2);
+                        if (cl == j) top = fmaxf(top, m);
+                    }
+                    if (lane < HC) sh.top[group][quarter][lane] = top;
+                    failed = lat::named_any(id, 128, !ok);
+                    if (failed) break;
+                    if (quarter == 0 && lane < HC) {
+                        top = fmaxf(fmaxf(sh.top[group][0][cl], sh.top[group][1][cl]), fmaxf(sh.top[group][2][cl], sh.top[group][3][cl]));
+                        const float old = sh.ref[group][cl], to = top > old + kGrow ? top : old;
+                        sh.ref[group][cl] = to;
+                        sh.fade[group][cl] = lat::ex2(old - to);   // 0 where there was nothing before
+                    }
+                    lat::named_sync(id, 128);
+#pragma unroll
+                    for (int j = 0; j < HC; ++j) {
+                        ref[j] = sh.ref[group][j];
+                        l[j] *= sh.fade[group][j];
+                        p[j] = lat::ex2(fmaf(__uint_as_float(raw_s[j]), a.scale2, -ref[j]));
+                    }
                     if (tile > w.at) {
 #pragma unroll 1
-                        for (int p = 0; p < np; ++p) {
+                        for (int b = 0; b < np; ++b) {
                             uint32_t o[HC];
-                            ptx::tmem_ld<HC>(t_o + p * NR, o);
+                            ptx::tmem_ld<HC>(t_o + b * NR, o);
                             ptx::tmem_wait_ld();
 #pragma unroll
-                            for (int j = 0; j < HC; ++j)
-                                o[j] = __float_as_uint(__uint_as_float(o[j]) * __shfl_sync(0xFFFFFFFFu, scale, j));
-                            lat::tmem_st<HC>(t_o + p * NR, o);
+                            for (int j = 0; j < HC; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * sh.fade[group][j]);
+                            lat::tmem_st<HC>(t_o + b * NR, o);
                         }
                         lat::tmem_wait_st();
                     }
+                    lat::named_sync(id, 128);                      // sh.ref and sh.fade have been read
                 }
-                const float base = ref == -INFINITY ? 0.0f : ref;
-                uint32_t packed[HC / 2];
 #pragma unroll
                 for (int j = 0; j < HC; j += 2) {
-                    const float p0 = lat::ex2(x[j] - __shfl_sync(0xFFFFFFFFu, base, j));
-                    const float p1 = lat::ex2(x[j + 1] - __shfl_sync(0xFFFFFFFFu, base, j + 1));
-                    l[j] += p0;
-                    l[j + 1] += p1;
-                    packed[j / 2] = Pair<T>::pack(p0, p1);
+                    l[j] += p[j];
+                    l[j + 1] += p[j + 1];
+                    packed[j / 2] = Pair<T>::pack(p[j], p[j + 1]);
                 }
                 uint8_t* prow = smem + C::kOffRope + (rope % C::kRope) * kChunkBytes;
 #pragma unroll
                 for (int c = 0; c < HC / 8; ++c) {
-                    uint32_t off = row * C::kRowBytes + (half * HC / 8 + c) * 16;
+                    uint32_t off = row * C::kRowBytes + (group * HC / 8 + c) * 16;
                     off ^= ((off >> 7) & (C::kRowBytes / 16 - 1)) << 4;
                     *reinterpret_cast<uint4*>(prow + off) =
                         make_uint4(packed[4 * c], packed[4 * c + 1], packed[4 * c + 2], packed[4 * c + 3]);
@@ -524,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // Weights past the request's rows are zero, but 0 times what lies there need not be.
                 if (token >= w.r.m) {
 #pragma unroll 1
-                    for (int c = half; c < 2 * np; c += 2) {
+                    for (int c = group; c < 2 * np; c += C::kGroups) {
                         uint4* z = reinterpret_cast<uint4*>(smem + ((pair + c / 2) % C::kPairs) * 2 * kChunkBytes +
                                                             (c & 1) * kChunkBytes + row * 128);
 #pragma unroll
@@ -541,21 +597,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (failed) break;
             // ---- the segment's result
             const float mine = lane_sums<HC>(l);
-            if (lane < HC) sh.sum[half][quarter][lane] = mine;
+            if (lane < HC) sh.sum[group][quarter][lane] = mine;
             ok = lat::wait_warp(bar(sh.o_full), seg & 1u, sync);
             ++seg;
             if (lat::named_any(id, 128, !ok)) break;
             const int cl = lane & (HC - 1);
-            const float total = (sh.sum[half][0][cl] + sh.sum[half][1][cl]) + (sh.sum[half][2][cl] + sh.sum[half][3][cl]);
+            const float mine_ref = quarter == 0 ? sh.ref[group][cl] : kNone;   // (the warp that sets it)
+            const float total = (sh.sum[group][0][cl] + sh.sum[group][1][cl]) + (sh.sum[group][2][cl] + sh.sum[group][3][cl]);
             const int64_t row0 = w.row0(a);
             const int rows = w.rows(a);
-            const int col = half * HC + cl;                        // of the statistics
+            const int col = group * HC + cl;                        // of the statistics
             const bool whole = w.at == 0 && end == w.count;
             ptx::tc_fence_after();
             if (whole) {
                 const float inv = total > 0.0f ? 1.0f / total : 0.0f;
                 if (a.lse != nullptr && quarter == 0 && lane < HC && col < rows)
-                    a.lse[row0 + col] = total > 0.0f ? (ref + log2f(total)) * kLn2 : -INFINITY;
+                    a.lse[row0 + col] = total > 0.0f ? (mine_ref + log2f(total)) * kLn2 : -INFINITY;
 #pragma unroll 1
                 for (int p = 0; p < np; ++p) {
                     uint32_t o[HC];
@@ -568,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const float v1 = __uint_as_float(o[j + 1]) * __shfl_sync(0xFFFFFFFFu, inv, j + 1);
                         const bool odd = (lane & 1) != 0;
                         const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? v0 : v1, 1);
-                        const int r = half * HC + j + (odd ? 1 : 0);
+                        const int r = group * HC + j + (odd ? 1 : 0);
                         if (r < rows)
                             reinterpret_cast<uint32_t*>(a.out)[((row0 + r) * a.L + p * 128 + quarter * 32 + (lane & ~1)) >> 1] =
                                 odd ? Pair<T>::pack(got, v1) : Pair<T>::pack(v0, got);
@@ -576,12 +633,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             } else {
                 // The part that begins an item owns its joining: parts up to the CTA of the item's last tile.
-                if (w.at == 0 && threadIdx.x == 64)
+                if (w.at == 0 && threadIdx.x == 128)
                     a.joins[blockIdx.x] = make_int4(static_cast<int>(row0), rows,
                                                     static_cast<int>((w.count - w.left + sh.per - 1) / sh.per) + 1, 0);
                 const int64_t part = 2 * int64_t(blockIdx.x) + (w.at > 0 ? 0 : 1);
-                if (quarter == 0 && lane < HC && col < rows) a.stats[part * NR + col] = make_float2(ref, total);
-                float* dst = a.partial + (part * NR + half * HC) * a.L + quarter * 32 + lane;
+                if (quarter == 0 && lane < HC && col < rows) a.stats[part * NR + col] = make_float2(mine_ref, total);
+                float* dst = a.partial + (part * NR + group * HC) * a.L + quarter * 32 + lane;
 #pragma unroll 1
                 for (int p = 0; p < np; ++p) {
                     uint32_t o[HC];
@@ -589,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ptx::tmem_wait_ld();
 #pragma unroll
                     for (int j = 0; j < HC; ++j)
-                        if (half * HC + j < rows) dst[j * a.L + p * 128] = __uint_as_float(o[j]);
+                        if (group * HC + j < rows) dst[j * a.L + p * 128] = __uint_as_float(o[j]);
                 }
             }
             ptx::tc_fence_before();
@@ -602,17 +659,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto land = [&](uint64_t& b, uint32_t uses) {
             while (uses > 0 && !ptx::mbar_test_wait(bar(b), (uses - 1) & 1u) && ptx::globaltimer() - t0 < (1ull << 26)) {}
         };
-        if (warp == 0) {
+        if (warp >= 1 && warp < 1 + kLoaders) {
             for (uint32_t i = 0; i < C::kPairs; ++i) land(sh.full[i], pair / C::kPairs + (i < pair % C::kPairs ? 1 : 0));
             for (uint32_t i = 0; i < C::kRope; ++i) land(sh.rope_full[i], rope / C::kRope + (i < rope % C::kRope ? 1 : 0));
             land(sh.q_full, seg);
-        } else if (threadIdx.x == 32) {
+        } else if (threadIdx.x == 0) {
             ptx::tc_commit(bar(sh.drain));
             land(sh.drain, 1);
         }
         __syncthreads();
     }
-    if (warp == 1) {
+    if (warp == 0) {
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, 512);
     }
@@ -683,7 +740,7 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const Args a,
         float l = 0.0f;
         for (int i = threadIdx.x; i < parts; i += kJoinThreads) {
             const float2 s = a.stats[slot(i)];
-            const float f = s.x == -INFINITY ? 0.0f : lat::ex2(s.x - m);
+            const float f = lat::ex2(s.x - m);
             weight[i] = f;
             l += f * s.y;
         }
@@ -700,12 +757,10 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const Args a,
             for (int i = group; i < parts; i += groups) {
                 const float4 v = __ldcg(reinterpret_cast<const float4*>(a.partial + slot(i) * a.L) + at);
                 const float f = weight[i];
-                if (f > 0.0f) {   // (a part without a row to see left nothing to add)
-                    o.x = fmaf(f, v.x, o.x);
-                    o.y = fmaf(f, v.y, o.y);
-                    o.z = fmaf(f, v.z, o.z);
-                    o.w = fmaf(f, v.w, o.w);
-                }
+                o.x = fmaf(f, v.x, o.x);
+                o.y = fmaf(f, v.y, o.y);
+                o.z = fmaf(f, v.z, o.z);
+                o.w = fmaf(f, v.w, o.w);
             }
             acc[threadIdx.x] = o;
         }
@@ -771,7 +826,7 @@ sgq_status run(const CUtensorMap& tm_cache, const CUtensorMap& tm_q, const Args&
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(Cfg<NR>::kThreads);
     cfg.dynamicSmemBytes = Cfg<NR>::kSmem;
     cfg.stream = st;
     cfg.attrs = attr;
@@ -813,6 +868,9 @@ sgq_status launch_latent_attention(const LatentArgs& x, cudaStream_t st) {
     rc = gemm::status_word(&a.status);
     if (rc != SGQ_OK) return rc;
     const int NR = row_block((x.T + x.B - 1) / x.B * x.H);
+    a.cache = static_cast<const char*>(x.cache);
+    a.c_page = 2 * x.c_page;
+    a.c_row = 2 * x.c_row;
     a.table = x.page_table;
     a.kv_lens = x.kv_lens;
     a.q_starts = x.q_starts;
@@ -827,6 +885,7 @@ sgq_status launch_latent_attention(const LatentArgs& x, cudaStream_t st) {
     a.R = x.R;
     a.page = x.page;
     a.box = std::min(x.page & -x.page, kTile);   // rows of a box: whole boxes in a page and in a tile
+    a.box_bytes = static_cast<uint32_t>((a.box - 1) * a.c_row + 2 * (x.L + x.R));
     a.tpn = std::max(1, NR / x.H);
     a.hb = (x.H + NR - 1) / NR;
     a.scale2 = x.scale * kLog2e;

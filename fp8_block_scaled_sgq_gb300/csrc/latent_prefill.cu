@@ -214,6 +214,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t kIdS = lat::idesc_f16(128, kTile, kBf16, false, false);
         const uint32_t id_o = lat::idesc_f16(128, a.N, kBf16, false, true);
         constexpr uint32_t kIdO64 = lat::idesc_f16(128, 64, kBf16, false, true);
+        constexpr uint32_t kHi = lat::desc_hi(1024, ptx::kLayoutSw128), kChunk = kChunkBytes >> 4;
+        const uint32_t lo_k = lat::uniform(lat::desc_lo(s_ring, 16)), lo_v = lat::uniform(lat::desc_lo(s_ring, kChunkBytes));
+        const uint32_t lo_q = lat::uniform(lat::desc_lo(s_q, 16)), t_s = lat::uniform(tmem);
         bool ok = true;
         auto wait_chunks = [&](uint32_t n, int chunks) {
             for (int c = 0; c < chunks && ok; ++c, ++n) ok = lat::wait_warp(bar(sh.full[n % kSlots]), (n / kSlots) & 1u, sync);
@@ -221,9 +224,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         auto scores = [&](int g, uint32_t at) {   // S of query tile g, keys in chunks at ...
             const uint32_t n = lat::uniform(at);
+#pragma unroll 1
             for (int c = 0; c < kc; ++c)     // (the rotated part is zero from R columns on)
-                lat::mma4_f16<2, 2>(tmem + g * 128, ptx::smem_desc(s_q + (g * 3 + c) * kChunkBytes, 16, 1024, ptx::kLayoutSw128),
-                                    ptx::smem_desc(s_ring + ((n + c) % kSlots) * kChunkBytes, 16, 1024, ptx::kLayoutSw128), kIdS, c > 0);
+                lat::mma4_f16<2, 2>(t_s + g * 128, lo_q + (g * 3 + c) * kChunk, kHi, lo_k + ((n + c) % kSlots) * kChunk, kHi, kIdS, c > 0);
             ptx::commit_elect(bar(sh.s_full[g]));
         };
         auto release = [&](uint32_t n, int chunks) {
@@ -244,18 +247,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = lat::wait_warp(bar(sh.p_full[g]), t & 1u, sync);
                     if (ok) wait_chunks(nv, vc);
                     if (ok) {
-                        const uint32_t o = tmem + 256 + g * 128, p = tmem + g * 128;
-                        const uint32_t s0 = lat::uniform(nv % kSlots), s1 = lat::uniform((nv + 1) % kSlots), more = lat::uniform(t > 0 ? 1u : 0u);
-                        const uint64_t d0 = ptx::smem_desc(s_ring + s0 * kChunkBytes, kChunkBytes, 1024, ptx::kLayoutSw128);
+                        const uint32_t o = t_s + 256 + g * 128, p = t_s + g * 128, more = lat::uniform(t > 0 ? 1u : 0u);
+                        const uint32_t s0 = lat::uniform(nv % kSlots), s1 = lat::uniform((nv + 1) % kSlots);
+                        const uint32_t d0 = lo_v + s0 * kChunk;
                         if (vc == 1 || s1 == s0 + 1) {
-                            lat::mma4_f16_ts<128>(o, p, d0, id_o, more);
-                            lat::mma4_f16_ts<128>(o, p + 32, d0 + 512, id_o, 1u);
+                            lat::mma4_f16_ts<128>(o, p, d0, kHi, id_o, more);
+                            lat::mma4_f16_ts<128>(o, p + 32, d0 + 512, kHi, id_o, 1u);
                         } else {   // the two chunks of values at the ring's two ends
-                            const uint64_t d1 = ptx::smem_desc(s_ring + s1 * kChunkBytes, kChunkBytes, 1024, ptx::kLayoutSw128);
-                            lat::mma4_f16_ts<128>(o, p, d0, kIdO64, more);
-                            lat::mma4_f16_ts<128>(o, p + 32, d0 + 512, kIdO64, 1u);
-                            lat::mma4_f16_ts<128>(o + 64, p, d1, kIdO64, more);
-                            lat::mma4_f16_ts<128>(o + 64, p + 32, d1 + 512, kIdO64, 1u);
+                            const uint32_t d1 = lo_v + s1 * kChunk;
+                            lat::mma4_f16_ts<128>(o, p, d0, kHi, kIdO64, more);
+                            lat::mma4_f16_ts<128>(o, p + 32, d0 + 512, kHi, kIdO64, 1u);
+                            lat::mma4_f16_ts<128>(o + 64, p, d1, kHi, kIdO64, more);
+                            lat::mma4_f16_ts<128>(o + 64, p + 32, d1 + 512, kHi, kIdO64, 1u);
                         }
                         if (t + 1 == count[g]) ptx::commit_elect(bar(sh.o_full[g]));
                     }

@@ -9,45 +9,58 @@
 namespace sgq {
 namespace lat {
 
-// A value that is the same in all lanes, in a form that the compiler knows to
-// be (MMA operands sit in uniform registers; without it every MMA is wrapped
-// in code that makes them so, at twice an MMA's time).
+// A value that is the same in all lanes, in a form that the compiler knows to be.
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xFFFFFFFFu, x, 0); }
+
+// A shared-memory matrix descriptor in halves: the low word holds the address
+// (and the leading offset), the high word the stride and the layout.  Steps
+// through shared memory only ever change the low word.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo_bytes) {
+    return ((saddr >> 4) & 0x3FFFu) | ((lbo_bytes >> 4) << 16);
+}
+__host__ __device__ constexpr uint32_t desc_hi(uint32_t sbo_bytes, uint32_t layout) {
+    return (sbo_bytes >> 4) | (1u << 14) | (layout << 29);
+}
 
 // Four MMAs D[tmem] (+)= A B^T of K = 16 each, 16-bit operands in shared
 // memory, fp32 accumulator: descriptors kA and kB (units of 16 bytes) apart,
 // the first one starting over where acc == 0.  Executed by a converged warp,
-// issued by its elected lane: from a branch of one lane an MMA took 90 to 170
-// cycles to issue, several times its execution.
+// issued by its elected lane.
 template <int kA, int kB>
-__device__ __forceinline__ void mma4_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma4_f16(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                         uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n.reg .pred e, q, t;\n.reg .b64 a1, a2, a3, b1, b2, b3;\n"
+        "{\n.reg .pred e, q, t;\n.reg .b32 x, y;\n.reg .b64 a0, a1, a2, a3, b0, b1, b2, b3;\n"
         "elect.sync _|e, 0xffffffff;\n"
-        "setp.ne.b32 q, %4, 0;\nsetp.eq.u32 t, %0, %0;\n"
-        "add.s64 a1, %1, %5;\nadd.s64 a2, %1, %6;\nadd.s64 a3, %1, %7;\n"
-        "add.s64 b1, %2, %8;\nadd.s64 b2, %2, %9;\nadd.s64 b3, %2, %10;\n"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, q;\n"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc), "n"(kA), "n"(2 * kA), "n"(3 * kA), "n"(kB), "n"(2 * kB), "n"(3 * kB)
+        "setp.ne.b32 q, %6, 0;\nsetp.eq.u32 t, %0, %0;\n"
+        "mov.b64 a0, {%1, %2};\nmov.b64 b0, {%3, %4};\n"
+        "add.u32 x, %1, %7;\nadd.u32 y, %3, %10;\nmov.b64 a1, {x, %2};\nmov.b64 b1, {y, %4};\n"
+        "add.u32 x, %1, %8;\nadd.u32 y, %3, %11;\nmov.b64 a2, {x, %2};\nmov.b64 b2, {y, %4};\n"
+        "add.u32 x, %1, %9;\nadd.u32 y, %3, %12;\nmov.b64 a3, {x, %2};\nmov.b64 b3, {y, %4};\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a0, b0, %5, q;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %5, t;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %5, t;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %5, t;\n}" ::"r"(d),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc), "n"(kA), "n"(2 * kA), "n"(3 * kA), "n"(kB),
+        "n"(2 * kB), "n"(3 * kB)
         : "memory");
 }
 // The same with A in TMEM (row i in lane i, two elements a 32-bit column).
 template <int kB>
-__device__ __forceinline__ void mma4_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma4_f16_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                            uint32_t acc) {
     asm volatile(
-        "{\n.reg .pred e, q, t;\n.reg .b32 a1, a2, a3;\n.reg .b64 b1, b2, b3;\n"
+        "{\n.reg .pred e, q, t;\n.reg .b32 a1, a2, a3, y;\n.reg .b64 b0, b1, b2, b3;\n"
         "elect.sync _|e, 0xffffffff;\n"
-        "setp.ne.b32 q, %4, 0;\nsetp.eq.u32 t, %0, %0;\n"
+        "setp.ne.b32 q, %5, 0;\nsetp.eq.u32 t, %0, %0;\n"
         "add.u32 a1, %1, 8;\nadd.u32 a2, %1, 16;\nadd.u32 a3, %1, 24;\n"
-        "add.s64 b1, %2, %5;\nadd.s64 b2, %2, %6;\nadd.s64 b3, %2, %7;\n"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, q;\n"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(acc), "n"(kB), "n"(2 * kB), "n"(3 * kB)
+        "mov.b64 b0, {%2, %3};\nadd.u32 y, %2, %6;\nmov.b64 b1, {y, %3};\n"
+        "add.u32 y, %2, %7;\nmov.b64 b2, {y, %3};\nadd.u32 y, %2, %8;\nmov.b64 b3, {y, %3};\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b0, %4, q;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %4, t;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %4, t;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %4, t;\n}" ::"r"(d),
+        "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc), "n"(kB), "n"(2 * kB), "n"(3 * kB)
         : "memory");
 }
 // Instruction descriptor, kind::f16: fp32 D; both operands bf16 or both fp16;
@@ -68,6 +81,11 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, 
         " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
+}
+
+// `bytes` (a multiple of 16) from a 16-byte aligned address into L2.
+__device__ __forceinline__ void bulk_prefetch(const void* p, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
 // 32 lanes x N consecutive 32-bit columns; thread t writes lane (base_lane + t).
