@@ -86,7 +86,8 @@ struct Args {
     int64_t T, B, pages, width, c_page, c_row;   // strides in bytes
     uint32_t box_bytes;
     int H, L, R, page, box;
-    int tpn, hb;         // tokens an item, items a token (one of them is 1)
+    int tpn, hb;         // tokens a block, head blocks a token (one of them is 1)
+    int team;            // CTAs that walk over the same tiles, a head block each: hb, or 1
     float scale2;        // scale log2(e)
 };
 
@@ -133,10 +134,13 @@ __device__ __forceinline__ int64_t request_tiles(const Request& r, const Args& a
         sum += int64_t(c) * (e - i);
         i = e;
     }
-    return sum * a.hb;
+    return sum * (a.hb / a.team);
 }
 
 // A CTA's run of tiles: item (b, block, head block), tile `at` of its `count`.
+// The head blocks of a token read the same tiles: a team of CTAs takes them
+// side by side, so that the second read finds them in L2 (read apart, B = 128
+// with H = 128 moved 0.99 GB from HBM instead of 0.54).
 struct Walk {
     int b, block, hblk, at, count;
     int64_t left;        // tiles of the run from here on
@@ -147,7 +151,7 @@ struct Walk {
         left -= end() - at;
         if (left <= 0) return false;
         at = 0;
-        if (++hblk == a.hb) {
+        if (++hblk == a.hb / a.team) {
             hblk = 0;
             if (++block * a.tpn >= r.n) {
                 block = 0;
@@ -161,12 +165,15 @@ struct Walk {
         return true;
     }
     __device__ __forceinline__ int64_t row0(const Args& a) const {
-        return (int64_t(r.t0) + block * a.tpn) * a.H + hblk * ((a.H + a.hb - 1) / a.hb);
+        return (int64_t(r.t0) + block * a.tpn) * a.H + head_block(a) * ((a.H + a.hb - 1) / a.hb);
+    }
+    __device__ __forceinline__ int head_block(const Args& a) const {
+        return a.team == 1 ? hblk : static_cast<int>(blockIdx.x) % a.team;
     }
     __device__ __forceinline__ int rows(const Args& a) const {
         if (a.hb == 1) return min(a.tpn, r.n - block * a.tpn) * a.H;
         const int per = (a.H + a.hb - 1) / a.hb;
-        return min(per, a.H - hblk * per);
+        return min(per, a.H - head_block(a) * per);
     }
 };
 
@@ -206,8 +213,9 @@ __device__ __forceinline__ void plan(const Args& a, Shared& sh) {
         if (w < warp) scan += sh.warp_sum[w];
         total += sh.warp_sum[w];
     }
-    const int64_t per = (total + gridDim.x - 1) / gridDim.x;
-    const int64_t start = per * blockIdx.x;
+    const int teams = gridDim.x / a.team;
+    const int64_t per = (total + teams - 1) / teams;
+    const int64_t start = per * (blockIdx.x / a.team);
     int64_t at = scan - mine;
     if (start >= at && start < scan) {
         for (int b = b0; b < b1; ++b) {
@@ -222,15 +230,15 @@ __device__ __forceinline__ void plan(const Args& a, Shared& sh) {
             while (i < blocks) {
                 c = tiles(r, a.tpn, i);
                 const int e = max(next_step(r, a.tpn, blocks, c), i + 1);
-                const int64_t span = int64_t(c) * (e - i) * a.hb;
+                const int64_t span = int64_t(c) * (e - i) * (a.hb / a.team);
                 if (start < at + span) break;
                 at += span;
                 i = e;
             }
             const int64_t item = (start - at) / c;
             sh.b = b;
-            sh.block = i + static_cast<int>(item / a.hb);
-            sh.hblk = static_cast<int>(item % a.hb);
+            sh.block = i + static_cast<int>(item / (a.hb / a.team));
+            sh.hblk = static_cast<int>(item % (a.hb / a.team));
             sh.at = static_cast<int>((start - at) % c);
             break;
         }
@@ -312,7 +320,7 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
 
     if (threadIdx.x == 128) a.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
     Walk w;
-    w.left = min(sh.per, sh.total - sh.per * blockIdx.x);
+    w.left = min(sh.per, sh.total - sh.per * (blockIdx.x / a.team));
     const bool any = w.left > 0;
     if (any) {
         w.b = sh.b;
@@ -678,36 +686,36 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
 // Joins the parts of the items that the cuts split: row r of part i holds an
 // unnormalised sum o_i with reference m_i and sum l_i, and
 //     out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i,  M = max m_i,
-// in the order of the parts.  A block takes whole rows: L / 4 threads across a
-// row, the others on other parts.
-constexpr int kJoinThreads = 256;
+// in a fixed order.  Rows of few parts take a warp each, eight rows a block;
+// rows of many parts a block each, a warp every eighth part.
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 constexpr int kMaxGrid = 512;
+constexpr int kFewParts = kJoinWarps;
 template <typename T>
 __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const Args a, int grid, int NR) {
     ptx::launch_dependents();
     ptx::grid_dependency_wait();
-    __shared__ int first[kMaxGrid + 1];
-    __shared__ float weight[kMaxGrid];
-    __shared__ float red[2][kJoinThreads / 32];
-    __shared__ float4 acc[kJoinThreads];
+    __shared__ int first[kMaxGrid + 1];                   // prefix sums of the CTAs' units of work
+    __shared__ int sums[kJoinWarps];
+    __shared__ alignas(16) float acc[kJoinWarps][512];
+    __shared__ float acc_l[kJoinWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int run = 0;
-    for (int base = 0; base < grid; base += kJoinThreads) {   // prefix sums of the rows to join
+    for (int base = 0; base < grid; base += kJoinThreads) {
         const int c = base + threadIdx.x;
         int4 j = make_int4(0, 0, 0, 0);
         if (c < grid) j = a.joins[c];
-        int v = j.z > 0 ? j.y : 0;
+        int v = j.z == 0 ? 0 : j.z <= kFewParts ? (j.y + kJoinWarps - 1) / kJoinWarps : j.y;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int up = __shfl_up_sync(0xFFFFFFFFu, v, o);
             if (lane >= o) v += up;
         }
-        int* sums = reinterpret_cast<int*>(red[0]);
         __syncthreads();
         if (lane == 31) sums[warp] = v;
         __syncthreads();
         int all = run;
-        for (int w = 0; w < kJoinThreads / 32; ++w) {
+        for (int w = 0; w < kJoinWarps; ++w) {
             if (w < warp) v += sums[w];
             all += sums[w];
         }
@@ -716,66 +724,81 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const Args a,
     }
     if (threadIdx.x == 0) first[0] = 0;
     __syncthreads();
-    const int total = first[grid];
-    const int per_row = a.L / 4, groups = kJoinThreads / per_row;
-    const int group = threadIdx.x / per_row, at = threadIdx.x % per_row;
-    for (int u = blockIdx.x; u < total; u += gridDim.x) {
+    const int nq = a.L / 128;                             // 128 columns: four a lane
+    for (int u = blockIdx.x; u < first[grid]; u += gridDim.x) {
         int lo = 0, hi = grid;
         while (hi - lo > 1) {
             const int mid = (lo + hi) / 2;
             if (first[mid] <= u) lo = mid;
             else hi = mid;
         }
-        // (CTAs without rows share their neighbour's prefix: the last one with first <= u has rows)
+        // (CTAs without work share their neighbour's prefix: the last one with first <= u has some)
         const int4 j = a.joins[lo];
-        const int r = u - first[lo], parts = j.z;
-        auto slot = [&](int i) { return (i == 0 ? int64_t(2) * lo + 1 : int64_t(2) * (lo + i)) * NR + r; };
-        float m = -INFINITY;
-        for (int i = threadIdx.x; i < parts; i += kJoinThreads) m = fmaxf(m, a.stats[slot(i)].x);
-        m = lat::warp_max(m);
-        if (lane == 0) red[0][warp] = m;
-        __syncthreads();
+        const bool few = j.z <= kFewParts;
+        const int r = few ? (u - first[lo]) * kJoinWarps + warp : u - first[lo], parts = j.z;
+        const int step = few ? 1 : kJoinWarps;
+        const bool mine = r < j.y;
+        auto slot = [&](int i) { return (i == 0 ? int64_t(2) * lo + 1 : int64_t(2) * (lo + i * a.team)) * NR + r; };
+        float m = kNone, l = 0.0f;
+        float4 o[4];
 #pragma unroll
-        for (int w = 0; w < kJoinThreads / 32; ++w) m = fmaxf(m, red[0][w]);
-        float l = 0.0f;
-        for (int i = threadIdx.x; i < parts; i += kJoinThreads) {
-            const float2 s = a.stats[slot(i)];
-            const float f = lat::ex2(s.x - m);
-            weight[i] = f;
-            l += f * s.y;
+        for (int q = 0; q < 4; ++q) o[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (mine) {
+            for (int i = lane; i < parts; i += 32) m = fmaxf(m, __ldcg(&a.stats[slot(i)]).x);
+            m = lat::warp_max(m);
+#pragma unroll 2
+            for (int i = few ? 0 : warp; i < parts; i += step) {
+                const int64_t s = slot(i);
+                const float2 st = __ldcg(&a.stats[s]);
+                const float4* src = reinterpret_cast<const float4*>(a.partial + s * a.L) + lane;
+                const float f = lat::ex2(st.x - m);
+                l = fmaf(f, st.y, l);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    if (q < nq) {
+                        const float4 v = __ldcg(src + q * 32);
+                        o[q].x = fmaf(f, v.x, o[q].x);
+                        o[q].y = fmaf(f, v.y, o[q].y);
+                        o[q].z = fmaf(f, v.z, o[q].z);
+                        o[q].w = fmaf(f, v.w, o[q].w);
+                    }
+                }
+            }
+        }
+        const int64_t row = int64_t(j.x) + r;
+        if (few) {
+            if (mine) {
+                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+                uint2* out = reinterpret_cast<uint2*>(static_cast<T*>(a.out) + row * a.L) + lane;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (q < nq)
+                        out[q * 32] = make_uint2(Pair<T>::pack(o[q].x * inv, o[q].y * inv), Pair<T>::pack(o[q].z * inv, o[q].w * inv));
+                if (a.lse != nullptr && lane == 0) a.lse[row] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+            }
+            continue;
         }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
-        if (lane == 0) red[1][warp] = l;
+        for (int q = 0; q < 4; ++q)
+            if (q < nq) reinterpret_cast<float4*>(acc[warp])[q * 32 + lane] = o[q];
+        if (lane == 0) acc_l[warp] = l;
         __syncthreads();
         l = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kJoinThreads / 32; ++w) l += red[1][w];
-        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (group < groups) {
-#pragma unroll 8
-            for (int i = group; i < parts; i += groups) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(a.partial + slot(i) * a.L) + at);
-                const float f = weight[i];
-                o.x = fmaf(f, v.x, o.x);
-                o.y = fmaf(f, v.y, o.y);
-                o.z = fmaf(f, v.z, o.z);
-                o.w = fmaf(f, v.w, o.w);
+        for (int w = 0; w < kJoinWarps; ++w) l += acc_l[w];
+        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+        const int c = 2 * threadIdx.x;
+        if (c < a.L) {
+            float x = 0.0f, y = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kJoinWarps; ++w) {
+                const float2 v = *reinterpret_cast<const float2*>(&acc[w][c]);
+                x += v.x;
+                y += v.y;
             }
-            acc[threadIdx.x] = o;
+            *reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + row * a.L + c) = Pair<T>::pack(x * inv, y * inv);
         }
-        __syncthreads();
-        if (group == 0) {
-            for (int g = 1; g < groups; ++g) {
-                const float4 v = acc[g * per_row + at];
-                o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
-            }
-            const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-            const int64_t row = int64_t(j.x) + r;
-            reinterpret_cast<uint2*>(a.out)[row * per_row + at] =
-                make_uint2(Pair<T>::pack(o.x * inv, o.y * inv), Pair<T>::pack(o.z * inv, o.w * inv));
-            if (a.lse != nullptr && at == 0) a.lse[row] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
-        }
+        if (a.lse != nullptr && threadIdx.x == 0) a.lse[row] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
         __syncthreads();
     }
 }
@@ -833,7 +856,7 @@ sgq_status run(const CUtensorMap& tm_cache, const CUtensorMap& tm_q, const Args&
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, kern, tm_cache, tm_q, a) != cudaSuccess) return SGQ_ERR_CUDA;
     note_launch();
-    if (grid == 1) return SGQ_OK;   // nothing is split
+    if (grid == a.team) return SGQ_OK;   // nothing is split
     cfg.gridDim = dim3(static_cast<unsigned>(join_grid));
     cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
@@ -888,10 +911,13 @@ sgq_status launch_latent_attention(const LatentArgs& x, cudaStream_t st) {
     a.box_bytes = static_cast<uint32_t>((a.box - 1) * a.c_row + 2 * (x.L + x.R));
     a.tpn = std::max(1, NR / x.H);
     a.hb = (x.H + NR - 1) / NR;
+    // (more head blocks than that are a walk of one CTA: teams would leave CTAs over)
+    a.team = a.hb <= 4 ? a.hb : 1;
     a.scale2 = x.scale * kLog2e;
     // No more CTAs than the tables could hold tiles.
-    const int64_t most = (x.T + x.B) * a.hb * std::max<int64_t>(1, (x.table_width * x.page + kTile - 1) / kTile);
-    const int grid = static_cast<int>(std::min<int64_t>(std::min(di.sm_count, kMaxGrid), most));
+    const int64_t most = (x.T + x.B) * (a.hb / a.team) * std::max<int64_t>(1, (x.table_width * x.page + kTile - 1) / kTile);
+    const int sms = std::min(di.sm_count, kMaxGrid) / a.team * a.team;
+    const int grid = static_cast<int>(std::min<int64_t>(sms, most * a.team));
     const Sizes s = workspace_of(grid, NR, x.L);
     char* ws = static_cast<char*>(x.workspace);
     a.partial = reinterpret_cast<float*>(ws);
