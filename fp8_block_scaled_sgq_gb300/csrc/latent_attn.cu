@@ -27,9 +27,10 @@
 // thread = token, groups of four warps with a share of the columns each.
 //
 // Work: the tiles of all (request, row block) items, in order, are cut into
-// equal runs, one a CTA, from the lengths on the device.  An item that a cut
-// splits leaves fp32 partial sums, which a second kernel joins in order: the
-// result does not depend on timing.
+// equal runs, one a CTA, from the lengths on the device; an item counts
+// kItemCost tiles more than it has, which is what starting and ending one
+// takes.  An item that a cut splits leaves fp32 partial sums, which a second
+// kernel joins in order: the result does not depend on timing.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -50,6 +51,7 @@ constexpr int kTile = 128;                    // cached rows a tile
 constexpr int kChunkBytes = kTile * 128;      // 64 columns of a tile
 constexpr int kMaxPairs = 5, kMaxRope = 2;
 constexpr int kLoaders = 3;                   // warps that issue loads: one alone keeps a third of this rate
+constexpr int kItemCost = 2;                  // tiles that an item's start and end cost (measured 3.5 to 5.4 us at 3 a tile)
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
 constexpr float kGrow = 8.0f;                 // powers of two a score may outgrow the reference by
 constexpr float kNone = -1.0e38f;             // reference of a row that has seen nothing
@@ -87,6 +89,7 @@ struct Args {
     uint32_t box_bytes;
     int H, L, R, page, box;
     int tpn, hb;         // tokens a block, head blocks a token (one of them is 1)
+    uint64_t inv_teams;  // 2^64 / teams, rounded up
     int team;            // CTAs that walk over the same tiles, a head block each: hb, or 1
     float scale2;        // scale log2(e)
 };
@@ -131,24 +134,26 @@ __device__ __forceinline__ int64_t request_tiles(const Request& r, const Args& a
     for (int i = 0; i < blocks;) {
         const int c = tiles(r, a.tpn, i);
         const int e = max(next_step(r, a.tpn, blocks, c), i + 1);
-        sum += int64_t(c) * (e - i);
+        sum += int64_t(c + kItemCost) * (e - i);
         i = e;
     }
     return sum * (a.hb / a.team);
 }
 
-// A CTA's run of tiles: item (b, block, head block), tile `at` of its `count`.
+// A CTA's run: item (b, block, head block), tile `at` of its `count`; a run's
+// length counts each item's tiles and then its cost.
 // The head blocks of a token read the same tiles: a team of CTAs takes them
 // side by side, so that the second read finds them in L2 (read apart, B = 128
 // with H = 128 moved 0.99 GB from HBM instead of 0.54).
 struct Walk {
     int b, block, hblk, at, count;
-    int64_t left;        // tiles of the run from here on
+    int64_t left;        // length of the run from here on
     Request r;
     __device__ __forceinline__ void settle(const Args& a) { count = tiles(r, a.tpn, block); }
     __device__ __forceinline__ int end() const { return static_cast<int>(min(int64_t(count), at + left)); }
+    // The run's next item with tiles in it; false: the run is over.
     __device__ __forceinline__ bool next(const Args& a) {
-        left -= end() - at;
+        left -= count + kItemCost - at;
         if (left <= 0) return false;
         at = 0;
         if (++hblk == a.hb / a.team) {
@@ -214,7 +219,7 @@ __device__ __forceinline__ void plan(const Args& a, Shared& sh) {
         total += sh.warp_sum[w];
     }
     const int teams = gridDim.x / a.team;
-    const int64_t per = (total + teams - 1) / teams;
+    const int64_t per = __umul64hi(static_cast<uint64_t>(total + teams - 1), a.inv_teams) + (teams == 1 ? total : 0);   // / teams, exact below 2^40
     const int64_t start = per * (blockIdx.x / a.team);
     int64_t at = scan - mine;
     if (start >= at && start < scan) {
@@ -230,16 +235,16 @@ __device__ __forceinline__ void plan(const Args& a, Shared& sh) {
             while (i < blocks) {
                 c = tiles(r, a.tpn, i);
                 const int e = max(next_step(r, a.tpn, blocks, c), i + 1);
-                const int64_t span = int64_t(c) * (e - i) * (a.hb / a.team);
+                const int64_t span = int64_t(c + kItemCost) * (e - i) * (a.hb / a.team);
                 if (start < at + span) break;
                 at += span;
                 i = e;
             }
-            const int64_t item = (start - at) / c;
+            const int64_t item = (start - at) / (c + kItemCost);
             sh.b = b;
             sh.block = i + static_cast<int>(item / (a.hb / a.team));
             sh.hblk = static_cast<int>(item % (a.hb / a.team));
-            sh.at = static_cast<int>((start - at) % c);
+            sh.at = static_cast<int>((start - at) - item * (c + kItemCost));
             break;
         }
     }
@@ -321,7 +326,7 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
     if (threadIdx.x == 128) a.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
     Walk w;
     w.left = min(sh.per, sh.total - sh.per * (blockIdx.x / a.team));
-    const bool any = w.left > 0;
+    bool any = w.left > 0;
     if (any) {
         w.b = sh.b;
         w.block = sh.block;
@@ -329,6 +334,7 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
         w.at = sh.at;
         w.r = request(a, w.b, false);
         w.settle(a);
+        if (w.at >= w.count) any = w.next(a);       // the run starts in an item's cost
     }
 
     uint32_t pair = 0, rope = 0, seg = 0;            // slots and segments used so far
@@ -377,12 +383,7 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
                     atomicOr(a.status, kStatusBadValue);
                     page = static_cast<int>(a.pages);
                 }
-                if (tile + 1 < end) {
-                    // The next tile goes to L2 while this one's loads wait for their slots.
-                    locate(tile + 1, next_boxes, next_page, next_in);
-                    if (id == 0 && lane < next_boxes && next_page >= 0 && next_page < a.pages)
-                        lat::bulk_prefetch(a.cache + next_page * a.c_page + next_in * a.c_row, a.box_bytes);
-                }
+                if (tile + 1 < end) locate(tile + 1, next_boxes, next_page, next_in);
                 const uint32_t dst = lane * a.box * 128;
 #pragma unroll 1
                 for (int p = 0; p < np; ++p, ++pair, turn = turn + 1 == kLoaders ? 0 : turn + 1) {
@@ -410,6 +411,10 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
                     __syncwarp();
                 }
                 ++rope;
+                // The next tile goes to L2 while its loads wait for their slots.
+                if (id == 0 && tile + 1 < end && lane < next_boxes && next_page >= 0 && next_page < a.pages)
+                    lat::bulk_prefetch(a.cache + next_page * a.c_page + next_in * a.c_row, a.box_bytes);
+                __syncwarp();
                 boxes = next_boxes;
                 page = next_page;
                 in_page = next_in;
@@ -621,22 +626,24 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
                 const float inv = total > 0.0f ? 1.0f / total : 0.0f;
                 if (a.lse != nullptr && quarter == 0 && lane < HC && col < rows)
                     a.lse[row0 + col] = total > 0.0f ? (mine_ref + log2f(total)) * kLn2 : -INFINITY;
+                const bool odd = (lane & 1) != 0;
+                uint32_t* out = reinterpret_cast<uint32_t*>(a.out) +
+                                (((row0 + group * HC + (odd ? 1 : 0)) * a.L + quarter * 32 + (lane & ~1)) >> 1);
+                const int last = rows - group * HC - (odd ? 1 : 0);   // this lane's rows j < last exist
+                float f[HC];
+#pragma unroll
+                for (int j = 0; j < HC; ++j) f[j] = __shfl_sync(0xFFFFFFFFu, inv, j);
 #pragma unroll 1
-                for (int p = 0; p < np; ++p) {
+                for (int p = 0; p < np; ++p, out += 64) {
                     uint32_t o[HC];
                     ptx::tmem_ld<HC>(t_o + p * NR, o);
                     ptx::tmem_wait_ld();
 #pragma unroll
                     for (int j = 0; j < HC; j += 2) {
                         // two rows, one element each -> one row, two elements: even lanes keep row j
-                        const float v0 = __uint_as_float(o[j]) * __shfl_sync(0xFFFFFFFFu, inv, j);
-                        const float v1 = __uint_as_float(o[j + 1]) * __shfl_sync(0xFFFFFFFFu, inv, j + 1);
-                        const bool odd = (lane & 1) != 0;
+                        const float v0 = __uint_as_float(o[j]) * f[j], v1 = __uint_as_float(o[j + 1]) * f[j + 1];
                         const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? v0 : v1, 1);
-                        const int r = group * HC + j + (odd ? 1 : 0);
-                        if (r < rows)
-                            reinterpret_cast<uint32_t*>(a.out)[((row0 + r) * a.L + p * 128 + quarter * 32 + (lane & ~1)) >> 1] =
-                                odd ? Pair<T>::pack(got, v1) : Pair<T>::pack(v0, got);
+                        if (j < last) out[j * (a.L / 2)] = odd ? Pair<T>::pack(got, v1) : Pair<T>::pack(v0, got);
                     }
                 }
             } else {
@@ -918,6 +925,7 @@ sgq_status launch_latent_attention(const LatentArgs& x, cudaStream_t st) {
     const int64_t most = (x.T + x.B) * (a.hb / a.team) * std::max<int64_t>(1, (x.table_width * x.page + kTile - 1) / kTile);
     const int sms = std::min(di.sm_count, kMaxGrid) / a.team * a.team;
     const int grid = static_cast<int>(std::min<int64_t>(sms, most * a.team));
+    a.inv_teams = grid == a.team ? 0 : ~uint64_t(0) / static_cast<uint64_t>(grid / a.team) + 1;
     const Sizes s = workspace_of(grid, NR, x.L);
     char* ws = static_cast<char*>(x.workspace);
     a.partial = reinterpret_cast<float*>(ws);
