@@ -60,7 +60,7 @@ struct Args {
 };
 
 struct Shared {
-    uint64_t full[kSlots], empty[kSlots];
+    uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];   // of tile t: entry t % 4
     uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drain;
     uint32_t tmem, abort;
     int64_t b;
@@ -121,11 +121,19 @@ __device__ __forceinline__ bool find_item(const Args& a, Shared& sh, int64_t ite
     return true;
 }
 
-template <typename T>
+// VC: chunks of 64 columns of the values (N / 64).
+template <typename T, int VC>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                           const __grid_constant__ CUtensorMap tm_r, const __grid_constant__ CUtensorMap tm_v, const Args a) {
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+    // A tile's chunks follow one another in the ring: KC of keys (the rotated part last), then VC of
+    // values.  Tile t's keys take the slots of what was loaded up to the values of tile t - kBackK,
+    // its values those up to the keys of tile t - kBackV.
+    constexpr int KC = VC + 1, kPer = KC + VC;
+    constexpr int kBackK = VC == 2 ? 2 : 3, kBackV = VC == 2 ? 1 : 2;
+    // (chunks from the first one still needed to the last one loaded, both included)
+    static_assert((kBackK - 1) * kPer + KC <= kSlots && kBackV * kPer - KC + kPer <= kSlots, "the ring holds what is needed");
     extern __shared__ uint8_t raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     Shared& sh = *reinterpret_cast<Shared*>(smem + kOffMisc);
@@ -135,9 +143,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_ring = ptx::smem_u32(smem), s_q = s_ring + kOffQ;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kSlots; ++i) {
-            ptx::mbar_init(bar(sh.full[i]), 1);
-            ptx::mbar_init(bar(sh.empty[i]), 1);
+        for (int i = 0; i < 4; ++i) {
+            ptx::mbar_init(bar(sh.k_full[i]), 1);
+            ptx::mbar_init(bar(sh.k_empty[i]), 1);
+            ptx::mbar_init(bar(sh.v_full[i]), 1);
+            ptx::mbar_init(bar(sh.v_empty[i]), 1);
         }
         for (int g = 0; g < 2; ++g) {
             ptx::mbar_init(bar(sh.q_full[g]), 1);
@@ -166,7 +176,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tc_fence_after();
     const uint32_t tmem = sh.tmem;
     // TMEM columns: S (and P) of the two query tiles at 0 and 128, O at 256 and 384.
-    const int vc = a.N / 64, kc = vc + 1, per = kc + vc;   // chunks a tile: values, keys, both
     Request r{0, 0, 0, 0};
     int first[2] = {0, 0}, count[2] = {0, 0};              // query tile g: its first query, its key tiles
     if (any) {
@@ -180,97 +189,108 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     const int tiles = max(count[0], count[1]);
-    uint32_t used = 0;                                     // chunks loaded
+    uint32_t keys = 0, values = 0;                         // tiles loaded
     if (warp == 0) {
         // ------------------------------------------------------------ loads
         bool ok = true;
         auto q_tile = [&](int g) {
             if (count[g] > 0 && lane == 0) {
-                ptx::mbar_arrive_expect_tx(bar(sh.q_full[g]), kc * kChunkBytes);
-                for (int c = 0; c < kc; ++c)
+                ptx::mbar_arrive_expect_tx(bar(sh.q_full[g]), KC * kChunkBytes);
+#pragma unroll
+                for (int c = 0; c < KC; ++c)
                     lat::tma_load_3d(s_q + (g * 3 + c) * kChunkBytes, &tm_q, c * 64, head, r.q0 + first[g], bar(sh.q_full[g]));
             }
+            __syncwarp();
         };
         if (tiles > 0) q_tile(0);
-        for (int t = 0; t < tiles && ok; ++t) {
-            for (int c = 0; c < per; ++c) {
-                const uint32_t slot = used % kSlots;
-                ok = lat::wait_warp(bar(sh.empty[slot]), ((used / kSlots) & 1u) ^ 1u, sync);
-                if (!ok) break;
-                if (lane == 0) {
-                    const uint32_t full = bar(sh.full[slot]), dst = s_ring + slot * kChunkBytes;
-                    const int row = r.k0 + t * kTile;
-                    ptx::mbar_arrive_expect_tx(full, kChunkBytes);
-                    if (c < vc) lat::tma_load_3d(dst, &tm_k, c * 64, head, row, full);
-                    else if (c == vc) ptx::tma_load_2d(dst, &tm_r, 0, row, full);
-                    else lat::tma_load_3d(dst, &tm_v, (c - kc) * 64, head, row, full);
-                }
-                ++used;
-                if (t == 0 && c == vc) q_tile(1);
+#pragma unroll 1
+        for (int t = 0; t < tiles; ++t) {
+            const uint32_t n = t * kPer;
+            const int row = r.k0 + t * kTile;
+            if (t >= kBackK) ok = lat::wait_warp(bar(sh.v_empty[(t - kBackK) & 3]), ((t - kBackK) >> 2) & 1, sync);
+            if (!ok) break;
+            if (lane == 0) {
+                const uint32_t full = bar(sh.k_full[t & 3]);
+                ptx::mbar_arrive_expect_tx(full, KC * kChunkBytes);
+#pragma unroll
+                for (int c = 0; c < VC; ++c) lat::tma_load_3d(s_ring + ((n + c) % kSlots) * kChunkBytes, &tm_k, c * 64, head, row, full);
+                ptx::tma_load_2d(s_ring + ((n + VC) % kSlots) * kChunkBytes, &tm_r, 0, row, full);
             }
+            __syncwarp();
+            ++keys;
+            if (t == 0) q_tile(1);
+            if (t >= kBackV) ok = lat::wait_warp(bar(sh.k_empty[(t - kBackV) & 3]), ((t - kBackV) >> 2) & 1, sync);
+            if (!ok) break;
+            if (lane == 0) {
+                const uint32_t full = bar(sh.v_full[t & 3]);
+                ptx::mbar_arrive_expect_tx(full, VC * kChunkBytes);
+#pragma unroll
+                for (int c = 0; c < VC; ++c) lat::tma_load_3d(s_ring + ((n + KC + c) % kSlots) * kChunkBytes, &tm_v, c * 64, head, row, full);
+            }
+            __syncwarp();
+            ++values;
         }
     } else if (warp == 1 && tiles > 0) {
         // ------------------------------------------------------------ MMAs
         constexpr uint32_t kIdS = lat::idesc_f16(128, kTile, kBf16, false, false);
-        const uint32_t id_o = lat::idesc_f16(128, a.N, kBf16, false, true);
+        constexpr uint32_t kIdO = lat::idesc_f16(128, VC * 64, kBf16, false, true);
         constexpr uint32_t kIdO64 = lat::idesc_f16(128, 64, kBf16, false, true);
         constexpr uint32_t kHi = lat::desc_hi(1024, ptx::kLayoutSw128), kChunk = kChunkBytes >> 4;
         const uint32_t lo_k = lat::uniform(lat::desc_lo(s_ring, 16)), lo_v = lat::uniform(lat::desc_lo(s_ring, kChunkBytes));
         const uint32_t lo_q = lat::uniform(lat::desc_lo(s_q, 16)), t_s = lat::uniform(tmem);
         bool ok = true;
-        auto wait_chunks = [&](uint32_t n, int chunks) {
-            for (int c = 0; c < chunks && ok; ++c, ++n) ok = lat::wait_warp(bar(sh.full[n % kSlots]), (n / kSlots) & 1u, sync);
-            ptx::tc_fence_after();
-        };
-        auto scores = [&](int g, uint32_t at) {   // S of query tile g, keys in chunks at ...
-            const uint32_t n = lat::uniform(at);
-#pragma unroll 1
-            for (int c = 0; c < kc; ++c)     // (the rotated part is zero from R columns on)
+        auto scores = [&](int g, uint32_t n) {   // S of query tile g, keys in chunks n ... (zero from R columns on)
+#pragma unroll
+            for (int c = 0; c < KC; ++c)
                 lat::mma4_f16<2, 2>(t_s + g * 128, lo_q + (g * 3 + c) * kChunk, kHi, lo_k + ((n + c) % kSlots) * kChunk, kHi, kIdS, c > 0);
             ptx::commit_elect(bar(sh.s_full[g]));
         };
-        auto release = [&](uint32_t n, int chunks) {
-            for (int c = 0; c < chunks; ++c) ptx::commit_elect(bar(sh.empty[lat::uniform((n + c) % kSlots)]));
+        auto product = [&](int g, uint32_t n, uint32_t more) {   // O of query tile g, values in chunks n ...
+            const uint32_t o = t_s + 256 + g * 128, p = t_s + g * 128, d0 = lo_v + n * kChunk;
+            if (VC == 1 || n + 1 < kSlots) {
+                lat::mma4_f16_ts<128>(o, p, d0, kHi, kIdO, more);
+                lat::mma4_f16_ts<128>(o, p + 32, d0 + 512, kHi, kIdO, 1u);
+            } else {   // the two chunks at the ring's two ends
+                lat::mma4_f16_ts<128>(o, p, d0, kHi, kIdO64, more);
+                lat::mma4_f16_ts<128>(o, p + 32, d0 + 512, kHi, kIdO64, 1u);
+                lat::mma4_f16_ts<128>(o + 64, p, lo_v, kHi, kIdO64, more);
+                lat::mma4_f16_ts<128>(o + 64, p + 32, lo_v + 512, kHi, kIdO64, 1u);
+            }
         };
-        for (int g = 0; g < 2 && ok; ++g) {
-            if (count[g] == 0) continue;
+        ok = lat::wait_warp(bar(sh.k_full[0]), 0, sync);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            if (count[g] == 0 || !ok) continue;
             ok = lat::wait_warp(bar(sh.q_full[g]), 0, sync);
-            if (ok) wait_chunks(0, kc);
             if (ok) scores(g, 0);
         }
-        if (ok) release(0, kc);
+        if (ok) ptx::commit_elect(bar(sh.k_empty[0]));
+#pragma unroll 1
         for (int t = 0; t < tiles && ok; ++t) {
-            const uint32_t nv = t * per + kc, nk = (t + 1) * per;   // this tile's values, the next one's keys
+            // this tile's values, the next one's keys
+            const uint32_t nv = lat::uniform((t * kPer + KC) % kSlots), nk = lat::uniform((t + 1) * kPer % kSlots);
+            const uint32_t more = lat::uniform(t > 0 ? 1u : 0u);
+            bool have_v = false, have_k = false;
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
-                if (t < count[g] && ok) {
-                    ok = lat::wait_warp(bar(sh.p_full[g]), t & 1u, sync);
-                    if (ok) wait_chunks(nv, vc);
-                    if (ok) {
-                        const uint32_t o = t_s + 256 + g * 128, p = t_s + g * 128, more = lat::uniform(t > 0 ? 1u : 0u);
-                        const uint32_t s0 = lat::uniform(nv % kSlots), s1 = lat::uniform((nv + 1) % kSlots);
-                        const uint32_t d0 = lo_v + s0 * kChunk;
-                        if (vc == 1 || s1 == s0 + 1) {
-                            lat::mma4_f16_ts<128>(o, p, d0, kHi, id_o, more);
-                            lat::mma4_f16_ts<128>(o, p + 32, d0 + 512, kHi, id_o, 1u);
-                        } else {   // the two chunks of values at the ring's two ends
-                            const uint32_t d1 = lo_v + s1 * kChunk;
-                            lat::mma4_f16_ts<128>(o, p, d0, kHi, kIdO64, more);
-                            lat::mma4_f16_ts<128>(o, p + 32, d0 + 512, kHi, kIdO64, 1u);
-                            lat::mma4_f16_ts<128>(o + 64, p, d1, kHi, kIdO64, more);
-                            lat::mma4_f16_ts<128>(o + 64, p + 32, d1 + 512, kHi, kIdO64, 1u);
-                        }
-                        if (t + 1 == count[g]) ptx::commit_elect(bar(sh.o_full[g]));
-                    }
-                }
-                if (t + 1 < count[g] && ok) {
-                    wait_chunks(nk, kc);
+                if (t >= count[g] || !ok) continue;
+                ok = lat::wait_warp(bar(sh.p_full[g]), t & 1u, sync);
+                if (ok && !have_v) ok = lat::wait_warp(bar(sh.v_full[t & 3]), (t >> 2) & 1, sync);
+                have_v = true;
+                if (!ok) break;
+                ptx::tc_fence_after();
+                product(g, nv, more);
+                if (t + 1 == count[g]) {
+                    ptx::commit_elect(bar(sh.o_full[g]));
+                } else {
+                    if (!have_k) ok = lat::wait_warp(bar(sh.k_full[(t + 1) & 3]), ((t + 1) >> 2) & 1, sync);
+                    have_k = true;
                     if (ok) scores(g, nk);
                 }
             }
             if (ok) {
-                release(nv, vc);
-                if (t + 1 < tiles) release(nk, kc);
+                ptx::commit_elect(bar(sh.v_empty[t & 3]));
+                if (t + 1 < tiles) ptx::commit_elect(bar(sh.k_empty[(t + 1) & 3]));
             }
         }
     } else if (warp >= 2) {
@@ -314,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     l *= f;
                     if (t > 0) {
 #pragma unroll 1
-                        for (int c = 0; c < vc * 8; ++c) {
+                        for (int c = 0; c < VC * 8; ++c) {
                             uint32_t o[8];
                             ptx::tmem_ld<8>(t_o + c * 8, o);
                             ptx::tmem_wait_ld();
@@ -343,13 +363,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // Weights past the request's keys are zero, but 0 times what lies there need not be: the
                 // group whose product comes first clears those rows of the values.
                 if ((t + 1) * kTile > r.m && (g == 0 || t >= count[0])) {
-                    const uint32_t nv = t * per + kc;
-                    for (int c = 0; c < vc && ok; ++c)
-                        ok = lat::wait_warp(bar(sh.full[(nv + c) % kSlots]), ((nv + c) / kSlots) & 1u, sync);
+                    ok = lat::wait_warp(bar(sh.v_full[t & 3]), (t >> 2) & 1, sync);
                     if (!ok) break;
                     if (t * kTile + row >= r.m) {
-                        for (int c = 0; c < vc; ++c) {
-                            uint4* z = reinterpret_cast<uint4*>(smem + ((nv + c) % kSlots) * kChunkBytes + row * 128);
+#pragma unroll
+                        for (int c = 0; c < VC; ++c) {
+                            uint4* z = reinterpret_cast<uint4*>(smem + ((t * kPer + KC + c) % kSlots) * kChunkBytes + row * 128);
 #pragma unroll
                             for (int i = 0; i < 8; ++i) z[i] = make_uint4(0, 0, 0, 0);
                         }
@@ -370,7 +389,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int64_t at = (int64_t(r.q0) + q) * a.H + head;
                 if (a.lse != nullptr && q < r.n) a.lse[at] = l > 0.0f ? (ref + log2f(l)) * kLn2 : -INFINITY;
                 uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + at * a.N);
-                for (int c = 0; c < vc * 2; ++c) {
+#pragma unroll 1
+                for (int c = 0; c < VC * 2; ++c) {
                     uint32_t o[32];
                     if (mine > 0) {
                         ptx::tmem_ld<32>(t_o + c * 32, o);
@@ -403,9 +423,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             while (uses > 0 && !ptx::mbar_test_wait(bar(x), (uses - 1) & 1u) && ptx::globaltimer() - t0 < (1ull << 26)) {}
         };
         if (warp == 0) {
-            for (uint32_t i = 0; i < kSlots; ++i) land(sh.full[i], used / kSlots + (i < used % kSlots ? 1 : 0));
-            for (int g = 0; g < 2; ++g)
-                if (count[g] > 0 && (g == 0 || used > static_cast<uint32_t>(vc))) land(sh.q_full[g], 1);
+            for (uint32_t i = 0; i < 4; ++i) {
+                land(sh.k_full[i], keys / 4 + (i < keys % 4 ? 1 : 0));
+                land(sh.v_full[i], values / 4 + (i < values % 4 ? 1 : 0));
+            }
+            if (tiles > 0 && count[0] > 0) land(sh.q_full[0], 1);
+            if (keys > 0 && count[1] > 0) land(sh.q_full[1], 1);
         } else if (threadIdx.x == 32) {
             ptx::tc_commit(bar(sh.drain));
             land(sh.drain, 1);
@@ -455,9 +478,9 @@ sgq_status row_map(CUtensorMap* m, const void* p, int64_t width, int64_t rows, i
                : SGQ_ERR_CUDA;
 }
 
-template <typename T>
+template <typename T, int VC>
 sgq_status run(const CUtensorMap (&tm)[4], const Args& a, int64_t grid, cudaStream_t st) {
-    auto kern = latent_prefill_kernel<T>;
+    auto kern = latent_prefill_kernel<T, VC>;
     static bool configured[64] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SGQ_ERR_CUDA;
@@ -513,7 +536,9 @@ sgq_status launch_latent_prefill(const PrefillArgs& x, cudaStream_t st) {
         row_map(&tm[2], none ? x.q : x.k_rot, x.R, S, none ? x.q_t : x.kr_t) != SGQ_OK ||
         head_map(&tm[3], none ? x.q : x.v, x.N, x.H, S, none ? x.q_h : x.v_h, none ? x.q_t : x.v_t) != SGQ_OK)
         return SGQ_ERR_CUDA;
-    return x.dtype == SGQ_BF16 ? run<__nv_bfloat16>(tm, a, blocks, st) : run<__half>(tm, a, blocks, st);
+    if (x.N == 128)
+        return x.dtype == SGQ_BF16 ? run<__nv_bfloat16, 2>(tm, a, blocks, st) : run<__half, 2>(tm, a, blocks, st);
+    return x.dtype == SGQ_BF16 ? run<__nv_bfloat16, 1>(tm, a, blocks, st) : run<__half, 1>(tm, a, blocks, st);
 }
 
 }  // namespace sgq
