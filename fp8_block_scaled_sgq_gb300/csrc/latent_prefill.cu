@@ -11,10 +11,12 @@
 //
 // What bounds it: the tensor cores.  A tile of N + R = 192, N = 128 takes 1280
 // cycles of MMAs at full rate; its exponentials take up to 1024 on the special
-// function units.  So two query tiles alternate: one group of four warps does
-// the softmax of its tile while the MMAs of the other run.  Warps: 0 loads
-// (TMA), 1 issues MMAs, 2 to 5 and 6 to 9 softmax of a query tile each
-// (thread = query row = TMEM lane).  Keys and values share a ring of chunks of
+// function units.  So two query tiles share the CTA: one group of four warps
+// does the softmax of its tile while the MMAs of the other run, and each has a
+// warp of its own that issues them (one for both left the tensor cores idle in
+// its waits).  Warps: 0 and 3 load (keys; values), 1 and 2 issue MMAs, 4 to 7
+// and 8 to 11 softmax of a query tile each (thread = query row = TMEM lane).
+// Keys and values share a ring of chunks of
 // 128 rows x 64 columns: values of a tile arrive while the products before
 // them run.
 //
@@ -36,7 +38,7 @@ namespace {
 
 using lat::Pair;
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
 constexpr int kTile = 128;
 constexpr int kChunkBytes = kTile * 128;
 constexpr int kSlots = 8;
@@ -145,9 +147,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < 4; ++i) {
             ptx::mbar_init(bar(sh.k_full[i]), 1);
-            ptx::mbar_init(bar(sh.k_empty[i]), 1);
+            ptx::mbar_init(bar(sh.k_empty[i]), 2);   // a commit of each issuing warp
             ptx::mbar_init(bar(sh.v_full[i]), 1);
-            ptx::mbar_init(bar(sh.v_empty[i]), 1);
+            ptx::mbar_init(bar(sh.v_empty[i]), 2);
         }
         for (int g = 0; g < 2; ++g) {
             ptx::mbar_init(bar(sh.q_full[g]), 1);
@@ -155,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_init(bar(sh.p_full[g]), 4);
             ptx::mbar_init(bar(sh.o_full[g]), 1);
         }
-        ptx::mbar_init(bar(sh.drain), 1);
+        ptx::mbar_init(bar(sh.drain), 2);
         sh.abort = 0;
         ptx::fence_mbar_init();
         ptx::prefetch_tmap(&tm_q);
@@ -219,6 +221,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             ++keys;
             if (t == 0) q_tile(1);
+        }
+    } else if (warp == 3) {
+        bool ok = true;
+#pragma unroll 1
+        for (int t = 0; t < tiles; ++t) {
+            const uint32_t n = t * kPer;
+            const int row = r.k0 + t * kTile;
             if (t >= kBackV) ok = lat::wait_warp(bar(sh.k_empty[(t - kBackV) & 3]), ((t - kBackV) >> 2) & 1, sync);
             if (!ok) break;
             if (lane == 0) {
@@ -230,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             ++values;
         }
-    } else if (warp == 1 && tiles > 0) {
+    } else if (warp < 3) {
         // ------------------------------------------------------------ MMAs
         constexpr uint32_t kIdS = lat::idesc_f16(128, kTile, kBf16, false, false);
         constexpr uint32_t kIdO = lat::idesc_f16(128, VC * 64, kBf16, false, true);
@@ -257,45 +266,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                 lat::mma4_f16_ts<128>(o + 64, p + 32, lo_v + 512, kHi, kIdO64, 1u);
             }
         };
-        ok = lat::wait_warp(bar(sh.k_full[0]), 0, sync);
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            if (count[g] == 0 || !ok) continue;
+        const int g = lat::uniform(warp - 1), mine = g == 0 ? count[0] : count[1];
+        if (tiles > 0) ok = lat::wait_warp(bar(sh.k_full[0]), 0, sync);
+        if (ok && mine > 0) {
             ok = lat::wait_warp(bar(sh.q_full[g]), 0, sync);
             if (ok) scores(g, 0);
         }
-        if (ok) ptx::commit_elect(bar(sh.k_empty[0]));
+        if (ok && tiles > 0) ptx::commit_elect(bar(sh.k_empty[0]));
 #pragma unroll 1
         for (int t = 0; t < tiles && ok; ++t) {
-            // this tile's values, the next one's keys
+            // This tile's values, the next one's keys.  A tile that this query tile does not see is waited
+            // for all the same before its release, so that no warp releases a slot's next use early.
             const uint32_t nv = lat::uniform((t * kPer + KC) % kSlots), nk = lat::uniform((t + 1) * kPer % kSlots);
-            const uint32_t more = lat::uniform(t > 0 ? 1u : 0u);
-            bool have_v = false, have_k = false;
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                if (t >= count[g] || !ok) continue;
-                ok = lat::wait_warp(bar(sh.p_full[g]), t & 1u, sync);
-                if (ok && !have_v) ok = lat::wait_warp(bar(sh.v_full[t & 3]), (t >> 2) & 1, sync);
-                have_v = true;
+            ok = lat::wait_warp(bar(sh.v_full[t & 3]), (t >> 2) & 1, sync);
+            if (t < mine) {
+                ok = ok && lat::wait_warp(bar(sh.p_full[g]), t & 1u, sync);
                 if (!ok) break;
                 ptx::tc_fence_after();
-                product(g, nv, more);
-                if (t + 1 == count[g]) {
-                    ptx::commit_elect(bar(sh.o_full[g]));
-                } else {
-                    if (!have_k) ok = lat::wait_warp(bar(sh.k_full[(t + 1) & 3]), ((t + 1) >> 2) & 1, sync);
-                    have_k = true;
-                    if (ok) scores(g, nk);
-                }
+                product(g, nv, lat::uniform(t > 0 ? 1u : 0u));
+                if (t + 1 == mine) ptx::commit_elect(bar(sh.o_full[g]));
             }
-            if (ok) {
-                ptx::commit_elect(bar(sh.v_empty[t & 3]));
-                if (t + 1 < tiles) ptx::commit_elect(bar(sh.k_empty[(t + 1) & 3]));
+            if (!ok) break;
+            ptx::commit_elect(bar(sh.v_empty[t & 3]));
+            if (t + 1 < tiles) {
+                ok = lat::wait_warp(bar(sh.k_full[(t + 1) & 3]), ((t + 1) >> 2) & 1, sync);
+                if (!ok) break;
+                if (t + 1 < mine) scores(g, nk);
+                ptx::commit_elect(bar(sh.k_empty[(t + 1) & 3]));
             }
         }
-    } else if (warp >= 2) {
+    } else {
         // ------------------------------------------------------------ softmax
-        const int g = (warp - 2) >> 2, quarter = warp & 3;
+        const int g = (warp - 4) >> 2, quarter = warp & 3;
         const int row = quarter * 32 + lane;
         const int q = first[g] + row;                              // query of the request
         const int mine = g == 0 ? count[0] : count[1];
@@ -309,24 +311,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = lat::wait_warp(bar(sh.s_full[g]), t & 1u, sync);
                 if (!ok) break;
                 ptx::tc_fence_after();
+                // the second half arrives while the first one's maximum is taken
                 uint32_t s[4][32];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) ptx::tmem_ld<32>(t_s + c * 32, s[c]);
+                ptx::tmem_ld<32>(t_s, s[0]);
+                ptx::tmem_ld<32>(t_s + 32, s[1]);
                 ptx::tmem_wait_ld();
-                if ((t + 1) * kTile > low || (t + 1) * kTile > r.m) {
-                    const int end = sees - t * kTile;
+                ptx::tmem_ld<32>(t_s + 64, s[2]);
+                ptx::tmem_ld<32>(t_s + 96, s[3]);
+                const bool edge = (t + 1) * kTile > low || (t + 1) * kTile > r.m;
+                const int end = sees - t * kTile;
+                float tops[4];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                for (int h = 0; h < 2; ++h) {
+                    if (h == 1) ptx::tmem_wait_ld();
+                    if (edge) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (c * 32 + j >= end) s[c][j] = __float_as_uint(-INFINITY);
+                        for (int c = 2 * h; c < 2 * h + 2; ++c)
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (c * 32 + j >= end) s[c][j] = __float_as_uint(-INFINITY);
+                    }
+#pragma unroll
+                    for (int c = 2 * h; c < 2 * h + 2; ++c) {
+                        tops[c] = __uint_as_float(s[c][0]);
+#pragma unroll
+                        for (int j = 1; j < 32; ++j) tops[c] = fmaxf(tops[c], __uint_as_float(s[c][j]));
+                    }
                 }
-                float top = -INFINITY;
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) top = fmaxf(top, __uint_as_float(s[c][j]));
-                top *= a.scale2;
+                const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * a.scale2;
                 const bool grow = top > ref + kGrow || (ref == -INFINITY && top > -INFINITY);
                 if (__any_sync(0xFFFFFFFFu, grow)) {
                     const float f = grow ? lat::ex2(ref - top) : 1.0f;
@@ -345,24 +357,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 const float base = ref == -INFINITY ? 0.0f : ref;
-                float sum[2] = {0.0f, 0.0f};
+                const float2 scale = make_float2(a.scale2, a.scale2), minus = make_float2(-base, -base);
+                float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     uint32_t p[16];
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
-                        const float p0 = lat::ex2(fmaf(__uint_as_float(s[c][j]), a.scale2, -base));
-                        const float p1 = lat::ex2(fmaf(__uint_as_float(s[c][j + 1]), a.scale2, -base));
-                        sum[0] += p0;
-                        sum[1] += p1;
-                        p[j / 2] = Pair<T>::pack(p0, p1);
+                        float2 x = make_float2(__uint_as_float(s[c][j]), __uint_as_float(s[c][j + 1]));
+                        x = lat::fma2(x, scale, minus);
+                        x.x = lat::ex2(x.x);
+                        x.y = lat::ex2(x.y);
+                        sum[(j >> 1) & 1] = lat::add2(sum[(j >> 1) & 1], x);
+                        p[j / 2] = Pair<T>::pack(x.x, x.y);
                     }
                     lat::tmem_st<16>(t_s + c * 16, p);
                 }
-                l += sum[0] + sum[1];
-                // Weights past the request's keys are zero, but 0 times what lies there need not be: the
-                // group whose product comes first clears those rows of the values.
-                if ((t + 1) * kTile > r.m && (g == 0 || t >= count[0])) {
+                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                // Weights past the request's keys are zero, but 0 times what lies there need not be: each
+                // group clears those rows of the values before its own product.
+                if ((t + 1) * kTile > r.m) {
                     ok = lat::wait_warp(bar(sh.v_full[t & 3]), (t >> 2) & 1, sync);
                     if (!ok) break;
                     if (t * kTile + row >= r.m) {
@@ -422,14 +436,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto land = [&](uint64_t& x, uint32_t uses) {
             while (uses > 0 && !ptx::mbar_test_wait(bar(x), (uses - 1) & 1u) && ptx::globaltimer() - t0 < (1ull << 26)) {}
         };
-        if (warp == 0) {
+        if (warp == 0 || warp == 3) {
             for (uint32_t i = 0; i < 4; ++i) {
                 land(sh.k_full[i], keys / 4 + (i < keys % 4 ? 1 : 0));
                 land(sh.v_full[i], values / 4 + (i < values % 4 ? 1 : 0));
             }
-            if (tiles > 0 && count[0] > 0) land(sh.q_full[0], 1);
+            if (warp == 0 && tiles > 0 && count[0] > 0) land(sh.q_full[0], 1);
             if (keys > 0 && count[1] > 0) land(sh.q_full[1], 1);
-        } else if (threadIdx.x == 32) {
+        } else if (threadIdx.x == 32 || threadIdx.x == 64) {
             ptx::tc_commit(bar(sh.drain));
             land(sh.drain, 1);
         }
