@@ -63,7 +63,7 @@ struct Args {
 
 struct Shared {
     uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];   // of tile t: entry t % 4
-    uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drain;
+    uint64_t q_full[2], s_full[2], p_full[2], turn[2], o_full[2], drain;
     uint32_t tmem, abort;
     int64_t b;
     int qb, pad;
@@ -155,6 +155,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_init(bar(sh.q_full[g]), 1);
             ptx::mbar_init(bar(sh.s_full[g]), 1);
             ptx::mbar_init(bar(sh.p_full[g]), 4);
+            ptx::mbar_init(bar(sh.turn[g]), 1);
             ptx::mbar_init(bar(sh.o_full[g]), 1);
         }
         ptx::mbar_init(bar(sh.drain), 2);
@@ -204,23 +205,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
         };
-        if (tiles > 0) q_tile(0);
+        if (tiles > 0) q_tile(1);   // (the one with the most keys first)
 #pragma unroll 1
         for (int t = 0; t < tiles; ++t) {
             const uint32_t n = t * kPer;
             const int row = r.k0 + t * kTile;
+            // (the first chunk's slot held the last keys of tile t - kBackK, the others' its values)
+            const uint32_t full = bar(sh.k_full[t & 3]);
+            if (t >= kBackK) ok = lat::wait_warp(bar(sh.k_empty[(t - kBackK) & 3]), ((t - kBackK) >> 2) & 1, sync);
+            if (!ok) break;
+            if (lane == 0) {
+                ptx::mbar_arrive_expect_tx(full, KC * kChunkBytes);
+                lat::tma_load_3d(s_ring + (n % kSlots) * kChunkBytes, &tm_k, 0, head, row, full);
+            }
+            __syncwarp();
             if (t >= kBackK) ok = lat::wait_warp(bar(sh.v_empty[(t - kBackK) & 3]), ((t - kBackK) >> 2) & 1, sync);
             if (!ok) break;
             if (lane == 0) {
-                const uint32_t full = bar(sh.k_full[t & 3]);
-                ptx::mbar_arrive_expect_tx(full, KC * kChunkBytes);
 #pragma unroll
-                for (int c = 0; c < VC; ++c) lat::tma_load_3d(s_ring + ((n + c) % kSlots) * kChunkBytes, &tm_k, c * 64, head, row, full);
+                for (int c = 1; c < VC; ++c) lat::tma_load_3d(s_ring + ((n + c) % kSlots) * kChunkBytes, &tm_k, c * 64, head, row, full);
                 ptx::tma_load_2d(s_ring + ((n + VC) % kSlots) * kChunkBytes, &tm_r, 0, row, full);
             }
             __syncwarp();
             ++keys;
-            if (t == 0) q_tile(1);
+            if (t == 0) q_tile(0);
         }
     } else if (warp == 3) {
         bool ok = true;
@@ -279,8 +287,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             // for all the same before its release, so that no warp releases a slot's next use early.
             const uint32_t nv = lat::uniform((t * kPer + KC) % kSlots), nk = lat::uniform((t + 1) * kPer % kSlots);
             ok = lat::wait_warp(bar(sh.v_full[t & 3]), (t >> 2) & 1, sync);
+            if (ok && t < mine) ok = lat::wait_warp(bar(sh.p_full[g]), t & 1u, sync);
+            // The issuing warps take turns, the second query tile's first: MMAs of both at once would
+            // make both query tiles wait, instead of one of them doing its softmax meanwhile.
+            if (ok && (g == 0 || t > 0)) ok = lat::wait_warp(bar(sh.turn[g]), g == 0 ? t & 1 : (t - 1) & 1, sync);
             if (t < mine) {
-                ok = ok && lat::wait_warp(bar(sh.p_full[g]), t & 1u, sync);
                 if (!ok) break;
                 ptx::tc_fence_after();
                 product(g, nv, lat::uniform(t > 0 ? 1u : 0u));
@@ -294,6 +305,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (t + 1 < mine) scores(g, nk);
                 ptx::commit_elect(bar(sh.k_empty[(t + 1) & 3]));
             }
+            if (lane == 0) ptx::mbar_arrive(bar(sh.turn[1 - g]));
+            __syncwarp();
         }
     } else {
         // ------------------------------------------------------------ softmax
