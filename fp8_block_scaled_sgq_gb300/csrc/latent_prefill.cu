@@ -20,8 +20,12 @@
 // 128 rows x 64 columns: values of a tile arrive while the products before
 // them run.
 //
-// Order of the CTAs: the query tiles of a head follow one another, longest
-// first, so that the heads in flight keep their keys and values in L2.
+// Work: an item is a pair of query tiles of a head; the items of a head follow
+// one another, longest first, so that the heads in flight keep their keys and
+// values in L2.  The grid has a CTA for every item, but a CTA that runs takes
+// over the next one that has not started yet (cluster launch control) while it
+// works: its loads run ahead into that item, and its barriers and tensor
+// memory stay (an item by itself spent 9000 cycles on its start and its end).
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -46,7 +50,7 @@ constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
 constexpr float kGrow = 8.0f;   // powers of two the maximum may outgrow the reference by
 constexpr int kOffQ = kSlots * kChunkBytes;
 constexpr int kOffMisc = kOffQ + 6 * kChunkBytes;
-constexpr int kMisc = 512;
+constexpr int kMisc = 2048;
 constexpr int kSmem = kOffMisc + kMisc + 1024;   // alignment slack
 static_assert(kSmem <= 232448, "shared memory");
 
@@ -57,23 +61,33 @@ struct Args {
     float* lse;
     uint32_t* status;
     int64_t T, S, B;
-    int H, N, R, causal;
+    int H, N, R, causal, span_size;
     float scale2;
 };
-
-struct Shared {
-    uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];   // of tile t: entry t % 4
-    uint64_t q_full[2], s_full[2], p_full[2], turn[2], o_full[2], drain;
-    uint32_t tmem, abort;
-    int64_t b;
-    int qb, pad;
-    int64_t warp_sum[kThreads / 32];
-};
-static_assert(sizeof(Shared) <= kMisc, "barriers");
 
 struct Request {
     int q0, n, k0, m;   // queries [q0, q0 + n), keys [k0, k0 + m)
 };
+// An item: two query tiles of a head, what they see of the request's keys.
+struct alignas(16) Item {
+    Request r;
+    int head, first, count0, count1;   // first query of the pair; key tiles of each query tile (first < r.n: it has rows)
+    __device__ __forceinline__ int tiles() const { return max(count0, count1); }
+    __device__ __forceinline__ int count(int g) const { return g == 0 ? count0 : count1; }
+};
+constexpr int kSpans = 256;
+struct Shared {
+    uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];   // of the CTA's tile T: entry T % 4
+    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], turn[2];
+    uint64_t taken, item_full[2], item_empty[2], drain;
+    alignas(16) uint32_t answer[4];    // to the request for another item
+    Item item[2];                      // the CTA's items, in turn
+    uint32_t tmem, abort;
+    int64_t warp_sum[kThreads / 32];
+    int span[kSpans];                  // items up to the end of each span of a.span_size requests
+};
+static_assert(sizeof(Shared) <= kMisc, "barriers");
+
 __device__ __forceinline__ Request request(const Args& a, int64_t b, bool report) {
     const int64_t qs = a.q_starts[b], qe = a.q_starts[b + 1], ks = a.kv_starts[b], ke = a.kv_starts[b + 1];
     const int64_t q0 = min(max(qs, int64_t(0)), a.T), q1 = min(max(qe, q0), a.T);
@@ -84,14 +98,15 @@ __device__ __forceinline__ Request request(const Args& a, int64_t b, bool report
     return Request{static_cast<int>(q0), static_cast<int>(q1 - q0), static_cast<int>(k0), static_cast<int>(k1 - k0)};
 }
 
-// The CTA's item: block index -> (request, head, pair of query tiles); every
-// thread takes part.  False: no such item (the grid is an upper bound).
-__device__ __forceinline__ bool find_item(const Args& a, Shared& sh, int64_t item, int64_t& b, int& head, int& qb) {
-    const int64_t k = (a.B + kThreads - 1) / kThreads;
-    const int64_t b0 = min(a.B, threadIdx.x * k), b1 = min(a.B, b0 + k);
-    int64_t mine = 0;
-    for (int64_t i = b0; i < b1; ++i) mine += int64_t((request(a, i, blockIdx.x == 0).n + 2 * kTile - 1) / (2 * kTile)) * a.H;
-    int64_t scan = mine;
+// Items of a request, and the prefix sums of all of them by spans of
+// span_size requests; every thread takes part.  (The host has checked
+// that an upper bound of the items fits 31 bits.)
+__device__ __forceinline__ int items_of(const Args& a, const Request& r) { return (r.n + 2 * kTile - 1) / (2 * kTile) * a.H; }
+__device__ __forceinline__ void sum_items(const Args& a, Shared& sh) {
+    const int64_t b0 = min(a.B, int64_t(threadIdx.x) * a.span_size), b1 = min(a.B, b0 + a.span_size);
+    int64_t scan = 0;   // (starts that do not rise are reported, and may make more items than there are CTAs)
+    if (threadIdx.x < kSpans)
+        for (int64_t i = b0; i < b1; ++i) scan += items_of(a, request(a, i, blockIdx.x == 0));
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -99,28 +114,41 @@ __device__ __forceinline__ bool find_item(const Args& a, Shared& sh, int64_t ite
         if (lane >= o) scan += up;
     }
     if (lane == 31) sh.warp_sum[warp] = scan;
-    if (threadIdx.x == 0) sh.b = -1;
     __syncthreads();
     for (int w = 0; w < warp; ++w) scan += sh.warp_sum[w];
-    int64_t at = scan - mine;
-    if (item >= at && item < scan) {
-        for (int64_t i = b0; i < b1; ++i) {
-            const int64_t n = int64_t((request(a, i, false).n + 2 * kTile - 1) / (2 * kTile)) * a.H;
-            if (item < at + n) {
-                sh.b = i;
-                sh.qb = static_cast<int>(item - at);
-                break;
-            }
-            at += n;
-        }
-    }
+    if (threadIdx.x < kSpans) sh.span[threadIdx.x] = static_cast<int>(min(scan, int64_t(INT32_MAX)));
     __syncthreads();
-    b = sh.b;
-    if (b < 0) return false;
-    const int blocks = (request(a, b, false).n + 2 * kTile - 1) / (2 * kTile);
-    head = sh.qb / blocks;
-    qb = blocks - 1 - sh.qb % blocks;
-    return true;
+}
+
+// (Past the last item, where the grid is an upper bound: an item without rows.)
+__device__ __forceinline__ Item find_item(const Args& a, const Shared& sh, int index) {
+    Item it{Request{0, 0, 0, 0}, 0, 0, 0, 0};
+    if (index >= sh.span[kSpans - 1]) return it;
+    int lo = 0, hi = kSpans - 1;   // the first span that ends past the index
+    while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (sh.span[mid] > index) hi = mid;
+        else lo = mid + 1;
+    }
+    int at = lo > 0 ? sh.span[lo - 1] : 0;
+    int64_t b = int64_t(lo) * a.span_size;
+    for (; b < a.B; ++b) {
+        it.r = request(a, b, false);
+        const int n = items_of(a, it.r);
+        if (index - at < n) break;
+        at += n;
+    }
+    if (b >= a.B) return Item{Request{0, 0, 0, 0}, 0, 0, 0, 0};
+    const int blocks = (it.r.n + 2 * kTile - 1) / (2 * kTile);
+    it.head = (index - at) / blocks;
+    it.first = (blocks - 1 - (index - at - it.head * blocks)) * 2 * kTile;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+        const int first = it.first + g * kTile, last = min(first + kTile, it.r.n) - 1;
+        const int seen = first >= it.r.n ? 0 : (a.causal ? max(0, it.r.m - it.r.n + last + 1) : it.r.m);
+        (g == 0 ? it.count0 : it.count1) = (seen + kTile - 1) / kTile;
+    }
+    return it;
 }
 
 // VC: chunks of 64 columns of the values (N / 64).
@@ -151,8 +179,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_init(bar(sh.v_full[i]), 1);
             ptx::mbar_init(bar(sh.v_empty[i]), 2);
         }
+        ptx::mbar_init(bar(sh.taken), 1);
         for (int g = 0; g < 2; ++g) {
+            ptx::mbar_init(bar(sh.item_full[g]), 1);
+            ptx::mbar_init(bar(sh.item_empty[g]), kThreads / 32 - 1);
             ptx::mbar_init(bar(sh.q_full[g]), 1);
+            ptx::mbar_init(bar(sh.q_empty[g]), 1);
             ptx::mbar_init(bar(sh.s_full[g]), 1);
             ptx::mbar_init(bar(sh.p_full[g]), 4);
             ptx::mbar_init(bar(sh.turn[g]), 1);
@@ -173,79 +205,109 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::launch_dependents();
     ptx::grid_dependency_wait();
     ptx::tc_fence_before();
-    int64_t b;
-    int head = 0, qb = 0;
-    const bool any = find_item(a, sh, blockIdx.x, b, head, qb);
+    sum_items(a, sh);
     ptx::tc_fence_after();
     const uint32_t tmem = sh.tmem;
     // TMEM columns: S (and P) of the two query tiles at 0 and 128, O at 256 and 384.
-    Request r{0, 0, 0, 0};
-    int first[2] = {0, 0}, count[2] = {0, 0};              // query tile g: its first query, its key tiles
-    if (any) {
-        r = request(a, b, false);
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            first[g] = qb * 2 * kTile + g * kTile;
-            const int last = min(first[g] + kTile, r.n) - 1;
-            const int seen = first[g] >= r.n ? 0 : (a.causal ? max(0, r.m - r.n + last + 1) : r.m);
-            count[g] = (seen + kTile - 1) / kTile;
-        }
-    }
-    const int tiles = max(count[0], count[1]);
-    uint32_t keys = 0, values = 0;                         // tiles loaded
+
+    // Warp 0 finds the CTA's items and leaves them in sh.item, entry `number` % 2 (first < 0: no more);
+    // the other warps take them from there.  False: no more, or a wait ran out.
+    int number = 0;
+    auto next_item = [&](Item& it) {
+        const int e = number & 1;
+        if (!lat::wait_warp(bar(sh.item_full[e]), (number >> 1) & 1, sync)) return false;
+        it = sh.item[e];
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(sh.item_empty[e]));
+        ++number;
+        return it.first >= 0;
+    };
+    Item it;
+    uint32_t kt = 0;                                       // key tiles so far
+    uint32_t q_used[2] = {0, 0};                           // query tiles loaded
+    bool ok = true;
     if (warp == 0) {
-        // ------------------------------------------------------------ loads
-        bool ok = true;
-        auto q_tile = [&](int g) {
-            if (count[g] > 0 && lane == 0) {
-                ptx::mbar_arrive_expect_tx(bar(sh.q_full[g]), KC * kChunkBytes);
-#pragma unroll
-                for (int c = 0; c < KC; ++c)
-                    lat::tma_load_3d(s_q + (g * 3 + c) * kChunkBytes, &tm_q, c * 64, head, r.q0 + first[g], bar(sh.q_full[g]));
+        // ------------------------------------------------------------ loads: queries, keys
+        uint32_t index = blockIdx.x;
+        bool more = true;
+        do {
+            const int e = number & 1;
+            ok = lat::wait_warp(bar(sh.item_empty[e]), ((number >> 1) & 1) ^ 1, sync);
+            if (!ok) break;
+            if (more) it = find_item(a, sh, static_cast<int>(index));
+            else it.first = -1;
+            if (lane == 0) {
+                sh.item[e] = it;
+                ptx::mbar_arrive(bar(sh.item_full[e]));
+                if (more) {
+                    ptx::mbar_arrive_expect_tx(bar(sh.taken), 16);
+                    lat::take_item(ptx::smem_u32(sh.answer), bar(sh.taken));
+                }
             }
             __syncwarp();
-        };
-        if (tiles > 0) q_tile(1);   // (the one with the most keys first)
+            ++number;
+            if (!more) break;
+            const int tiles = it.tiles();
+            auto q_tile = [&](int g) {
+                if (!ok || it.count(g) == 0) return;
+                ok = lat::wait_warp(bar(sh.q_empty[g]), (q_used[g] & 1u) ^ 1u, sync);
+                if (!ok) return;
+                if (lane == 0) {
+                    ptx::mbar_arrive_expect_tx(bar(sh.q_full[g]), KC * kChunkBytes);
+#pragma unroll
+                    for (int c = 0; c < KC; ++c)
+                        lat::tma_load_3d(s_q + (g * 3 + c) * kChunkBytes, &tm_q, c * 64, it.head, it.r.q0 + it.first + g * kTile,
+                                         bar(sh.q_full[g]));
+                }
+                __syncwarp();
+                ++q_used[g];
+            };
+            q_tile(1);   // (the one with the most keys first)
 #pragma unroll 1
-        for (int t = 0; t < tiles; ++t) {
-            const uint32_t n = t * kPer;
-            const int row = r.k0 + t * kTile;
-            // (the first chunk's slot held the last keys of tile t - kBackK, the others' its values)
-            const uint32_t full = bar(sh.k_full[t & 3]);
-            if (t >= kBackK) ok = lat::wait_warp(bar(sh.k_empty[(t - kBackK) & 3]), ((t - kBackK) >> 2) & 1, sync);
-            if (!ok) break;
-            if (lane == 0) {
-                ptx::mbar_arrive_expect_tx(full, KC * kChunkBytes);
-                lat::tma_load_3d(s_ring + (n % kSlots) * kChunkBytes, &tm_k, 0, head, row, full);
-            }
-            __syncwarp();
-            if (t >= kBackK) ok = lat::wait_warp(bar(sh.v_empty[(t - kBackK) & 3]), ((t - kBackK) >> 2) & 1, sync);
-            if (!ok) break;
-            if (lane == 0) {
+            for (int t = 0; t < tiles && ok; ++t, ++kt) {
+                const uint32_t n = kt * kPer, back = kt - kBackK;
+                const int row = it.r.k0 + t * kTile;
+                // (the first chunk's slot held the last keys of the tile kBackK before, the others' its values)
+                const uint32_t full = bar(sh.k_full[kt & 3]);
+                if (kt >= kBackK) ok = lat::wait_warp(bar(sh.k_empty[back & 3]), (back >> 2) & 1, sync);
+                if (!ok) break;
+                if (lane == 0) {
+                    ptx::mbar_arrive_expect_tx(full, KC * kChunkBytes);
+                    lat::tma_load_3d(s_ring + (n % kSlots) * kChunkBytes, &tm_k, 0, it.head, row, full);
+                }
+                __syncwarp();
+                if (kt >= kBackK) ok = lat::wait_warp(bar(sh.v_empty[back & 3]), (back >> 2) & 1, sync);
+                if (lane == 0 && ok) {
 #pragma unroll
-                for (int c = 1; c < VC; ++c) lat::tma_load_3d(s_ring + ((n + c) % kSlots) * kChunkBytes, &tm_k, c * 64, head, row, full);
-                ptx::tma_load_2d(s_ring + ((n + VC) % kSlots) * kChunkBytes, &tm_r, 0, row, full);
+                    for (int c = 1; c < VC; ++c) lat::tma_load_3d(s_ring + ((n + c) % kSlots) * kChunkBytes, &tm_k, c * 64, it.head, row, full);
+                    ptx::tma_load_2d(s_ring + ((n + VC) % kSlots) * kChunkBytes, &tm_r, 0, row, full);
+                }
+                __syncwarp();
+                if (t == 0) q_tile(0);
             }
+            ok = ok && lat::wait_warp(bar(sh.taken), (number - 1) & 1, sync);
+            more = ok && lat::taken_item(ptx::smem_u32(sh.answer), index);
+            ptx::fence_proxy_async_smem();              // (the answer has been read before the next one is asked for)
             __syncwarp();
-            ++keys;
-            if (t == 0) q_tile(0);
-        }
+        } while (ok);
     } else if (warp == 3) {
-        bool ok = true;
+        // ------------------------------------------------------------ loads: values
+        while (ok && next_item(it)) {
+            const int tiles = it.tiles();
 #pragma unroll 1
-        for (int t = 0; t < tiles; ++t) {
-            const uint32_t n = t * kPer;
-            const int row = r.k0 + t * kTile;
-            if (t >= kBackV) ok = lat::wait_warp(bar(sh.k_empty[(t - kBackV) & 3]), ((t - kBackV) >> 2) & 1, sync);
-            if (!ok) break;
-            if (lane == 0) {
-                const uint32_t full = bar(sh.v_full[t & 3]);
-                ptx::mbar_arrive_expect_tx(full, VC * kChunkBytes);
+            for (int t = 0; t < tiles; ++t, ++kt) {
+                const uint32_t n = kt * kPer + KC, back = kt - kBackV;
+                if (kt >= kBackV) ok = lat::wait_warp(bar(sh.k_empty[back & 3]), (back >> 2) & 1, sync);
+                if (!ok) break;
+                if (lane == 0) {
+                    const uint32_t full = bar(sh.v_full[kt & 3]);
+                    ptx::mbar_arrive_expect_tx(full, VC * kChunkBytes);
 #pragma unroll
-                for (int c = 0; c < VC; ++c) lat::tma_load_3d(s_ring + ((n + KC + c) % kSlots) * kChunkBytes, &tm_v, c * 64, head, row, full);
+                    for (int c = 0; c < VC; ++c)
+                        lat::tma_load_3d(s_ring + ((n + c) % kSlots) * kChunkBytes, &tm_v, c * 64, it.head, it.r.k0 + t * kTile, full);
+                }
+                __syncwarp();
             }
-            __syncwarp();
-            ++values;
         }
     } else if (warp < 3) {
         // ------------------------------------------------------------ MMAs
@@ -255,7 +317,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t kHi = lat::desc_hi(1024, ptx::kLayoutSw128), kChunk = kChunkBytes >> 4;
         const uint32_t lo_k = lat::uniform(lat::desc_lo(s_ring, 16)), lo_v = lat::uniform(lat::desc_lo(s_ring, kChunkBytes));
         const uint32_t lo_q = lat::uniform(lat::desc_lo(s_q, 16)), t_s = lat::uniform(tmem);
-        bool ok = true;
         auto scores = [&](int g, uint32_t n) {   // S of query tile g, keys in chunks n ... (zero from R columns on)
 #pragma unroll
             for (int c = 0; c < KC; ++c)
@@ -274,172 +335,189 @@ __global__ void __launch_bounds__(kThreads, 1)
                 lat::mma4_f16_ts<128>(o + 64, p + 32, lo_v + 512, kHi, kIdO64, 1u);
             }
         };
-        const int g = lat::uniform(warp - 1), mine = g == 0 ? count[0] : count[1];
-        if (tiles > 0) ok = lat::wait_warp(bar(sh.k_full[0]), 0, sync);
-        if (ok && mine > 0) {
-            ok = lat::wait_warp(bar(sh.q_full[g]), 0, sync);
-            if (ok) scores(g, 0);
-        }
-        if (ok && tiles > 0) ptx::commit_elect(bar(sh.k_empty[0]));
-#pragma unroll 1
-        for (int t = 0; t < tiles && ok; ++t) {
-            // This tile's values, the next one's keys.  A tile that this query tile does not see is waited
-            // for all the same before its release, so that no warp releases a slot's next use early.
-            const uint32_t nv = lat::uniform((t * kPer + KC) % kSlots), nk = lat::uniform((t + 1) * kPer % kSlots);
-            ok = lat::wait_warp(bar(sh.v_full[t & 3]), (t >> 2) & 1, sync);
-            if (ok && t < mine) ok = lat::wait_warp(bar(sh.p_full[g]), t & 1u, sync);
-            // The issuing warps take turns, the second query tile's first: MMAs of both at once would
-            // make both query tiles wait, instead of one of them doing its softmax meanwhile.
-            if (ok && (g == 0 || t > 0)) ok = lat::wait_warp(bar(sh.turn[g]), g == 0 ? t & 1 : (t - 1) & 1, sync);
-            if (t < mine) {
+        const int g = lat::uniform(warp - 1);
+        uint32_t p_used = 0;
+        while (ok && next_item(it)) {
+            const int tiles = it.tiles(), mine = it.count(g);
+            if (tiles == 0) continue;
+            ok = lat::wait_warp(bar(sh.k_full[kt & 3]), (kt >> 2) & 1, sync);
+            if (ok && mine > 0) {
+                ok = lat::wait_warp(bar(sh.q_full[g]), q_used[0] & 1u, sync);
                 if (!ok) break;
-                ptx::tc_fence_after();
-                product(g, nv, lat::uniform(t > 0 ? 1u : 0u));
-                if (t + 1 == mine) ptx::commit_elect(bar(sh.o_full[g]));
+                ++q_used[0];
+                scores(g, lat::uniform(kt * kPer % kSlots));
+                if (mine == 1) ptx::commit_elect(bar(sh.q_empty[g]));
             }
             if (!ok) break;
-            ptx::commit_elect(bar(sh.v_empty[t & 3]));
-            if (t + 1 < tiles) {
-                ok = lat::wait_warp(bar(sh.k_full[(t + 1) & 3]), ((t + 1) >> 2) & 1, sync);
+            ptx::commit_elect(bar(sh.k_empty[kt & 3]));
+#pragma unroll 1
+            for (int t = 0; t < tiles; ++t, ++kt) {
+                // This tile's values, the next one's keys.  A tile that this query tile does not see is waited
+                // for all the same before its release, so that no warp releases a slot's next use early.
+                const uint32_t nv = lat::uniform((kt * kPer + KC) % kSlots), nk = lat::uniform((kt + 1) * kPer % kSlots);
+                ok = lat::wait_warp(bar(sh.v_full[kt & 3]), (kt >> 2) & 1, sync);
+                if (ok && t < mine) ok = lat::wait_warp(bar(sh.p_full[g]), p_used++ & 1u, sync);
+                // The issuing warps take turns, the second query tile's first: MMAs of both at once would
+                // make both query tiles wait, instead of one of them doing its softmax meanwhile.
+                if (ok && (g == 0 || kt > 0)) ok = lat::wait_warp(bar(sh.turn[g]), (g == 0 ? kt : kt - 1) & 1u, sync);
                 if (!ok) break;
-                if (t + 1 < mine) scores(g, nk);
-                ptx::commit_elect(bar(sh.k_empty[(t + 1) & 3]));
+                if (t < mine) {
+                    ptx::tc_fence_after();
+                    product(g, nv, lat::uniform(t > 0 ? 1u : 0u));
+                    if (t + 1 == mine) ptx::commit_elect(bar(sh.o_full[g]));
+                }
+                ptx::commit_elect(bar(sh.v_empty[kt & 3]));
+                if (t + 1 < tiles) {
+                    ok = lat::wait_warp(bar(sh.k_full[(kt + 1) & 3]), ((kt + 1) >> 2) & 1, sync);
+                    if (!ok) break;
+                    if (t + 1 < mine) scores(g, nk);
+                    if (t + 2 == mine) ptx::commit_elect(bar(sh.q_empty[g]));
+                    ptx::commit_elect(bar(sh.k_empty[(kt + 1) & 3]));
+                }
+                if (lane == 0) ptx::mbar_arrive(bar(sh.turn[1 - g]));
+                __syncwarp();
             }
-            if (lane == 0) ptx::mbar_arrive(bar(sh.turn[1 - g]));
-            __syncwarp();
         }
     } else {
         // ------------------------------------------------------------ softmax
         const int g = (warp - 4) >> 2, quarter = warp & 3;
         const int row = quarter * 32 + lane;
-        const int q = first[g] + row;                              // query of the request
-        const int mine = g == 0 ? count[0] : count[1];
-        if (any && first[g] < r.n) {
-            const int sees = a.causal ? min(r.m, r.m - r.n + q + 1) : r.m;
-            const int low = a.causal ? r.m - r.n + first[g] + quarter * 32 + 1 : r.m;   // what every row of the warp sees
-            const uint32_t t_s = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + g * 128, t_o = t_s + 256;
-            float ref = -INFINITY, l = 0.0f;
-            bool ok = true;
-            for (int t = 0; t < mine; ++t) {
-                ok = lat::wait_warp(bar(sh.s_full[g]), t & 1u, sync);
-                if (!ok) break;
-                ptx::tc_fence_after();
-                // the second half arrives while the first one's maximum is taken
-                uint32_t s[4][32];
-                ptx::tmem_ld<32>(t_s, s[0]);
-                ptx::tmem_ld<32>(t_s + 32, s[1]);
-                ptx::tmem_wait_ld();
-                ptx::tmem_ld<32>(t_s + 64, s[2]);
-                ptx::tmem_ld<32>(t_s + 96, s[3]);
-                const bool edge = (t + 1) * kTile > low || (t + 1) * kTile > r.m;
-                const int end = sees - t * kTile;
-                float tops[4];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (h == 1) ptx::tmem_wait_ld();
-                    if (edge) {
-#pragma unroll
-                        for (int c = 2 * h; c < 2 * h + 2; ++c)
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (c * 32 + j >= end) s[c][j] = __float_as_uint(-INFINITY);
-                    }
-#pragma unroll
-                    for (int c = 2 * h; c < 2 * h + 2; ++c) {
-                        tops[c] = __uint_as_float(s[c][0]);
-#pragma unroll
-                        for (int j = 1; j < 32; ++j) tops[c] = fmaxf(tops[c], __uint_as_float(s[c][j]));
-                    }
-                }
-                const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * a.scale2;
-                const bool grow = top > ref + kGrow || (ref == -INFINITY && top > -INFINITY);
-                if (__any_sync(0xFFFFFFFFu, grow)) {
-                    const float f = grow ? lat::ex2(ref - top) : 1.0f;
-                    if (grow) ref = top;
-                    l *= f;
-                    if (t > 0) {
+        const uint32_t t_s = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + g * 128, t_o = t_s + 256;
+        uint32_t s_used = 0, o_used = 0;
+        while (ok && next_item(it)) {
+            const Request& r = it.r;
+            const int q = it.first + g * kTile + row;                  // query of the request
+            const int mine = it.count(g);
+            if (it.first + g * kTile < r.n) {
+                const int sees = a.causal ? min(r.m, r.m - r.n + q + 1) : r.m;
+                const int low = a.causal ? r.m - r.n + q - lane + 1 : r.m;   // what every row of the warp sees
+                float ref = -INFINITY, l = 0.0f;
 #pragma unroll 1
-                        for (int c = 0; c < VC * 8; ++c) {
-                            uint32_t o[8];
-                            ptx::tmem_ld<8>(t_o + c * 8, o);
-                            ptx::tmem_wait_ld();
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                            lat::tmem_st<8>(t_o + c * 8, o);
-                        }
-                    }
-                }
-                const float base = ref == -INFINITY ? 0.0f : ref;
-                const float2 scale = make_float2(a.scale2, a.scale2), minus = make_float2(-base, -base);
-                float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t p[16];
-#pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        float2 x = make_float2(__uint_as_float(s[c][j]), __uint_as_float(s[c][j + 1]));
-                        x = lat::fma2(x, scale, minus);
-                        x.x = lat::ex2(x.x);
-                        x.y = lat::ex2(x.y);
-                        sum[(j >> 1) & 1] = lat::add2(sum[(j >> 1) & 1], x);
-                        p[j / 2] = Pair<T>::pack(x.x, x.y);
-                    }
-                    lat::tmem_st<16>(t_s + c * 16, p);
-                }
-                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                // Weights past the request's keys are zero, but 0 times what lies there need not be: each
-                // group clears those rows of the values before its own product.
-                if ((t + 1) * kTile > r.m) {
-                    ok = lat::wait_warp(bar(sh.v_full[t & 3]), (t >> 2) & 1, sync);
+                for (int t = 0; t < mine; ++t) {
+                    ok = lat::wait_warp(bar(sh.s_full[g]), s_used++ & 1u, sync);
                     if (!ok) break;
-                    if (t * kTile + row >= r.m) {
+                    ptx::tc_fence_after();
+                    // the second half arrives while the first one's maximum is taken
+                    uint32_t s[4][32];
+                    ptx::tmem_ld<32>(t_s, s[0]);
+                    ptx::tmem_ld<32>(t_s + 32, s[1]);
+                    ptx::tmem_wait_ld();
+                    ptx::tmem_ld<32>(t_s + 64, s[2]);
+                    ptx::tmem_ld<32>(t_s + 96, s[3]);
+                    const bool edge = (t + 1) * kTile > low || (t + 1) * kTile > r.m;
+                    const int end = sees - t * kTile;
+                    float tops[4];
 #pragma unroll
-                        for (int c = 0; c < VC; ++c) {
-                            uint4* z = reinterpret_cast<uint4*>(smem + ((t * kPer + KC + c) % kSlots) * kChunkBytes + row * 128);
+                    for (int h = 0; h < 2; ++h) {
+                        if (h == 1) ptx::tmem_wait_ld();
+                        if (edge) {
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) z[i] = make_uint4(0, 0, 0, 0);
+                            for (int c = 2 * h; c < 2 * h + 2; ++c)
+#pragma unroll
+                                for (int j = 0; j < 32; ++j)
+                                    if (c * 32 + j >= end) s[c][j] = __float_as_uint(-INFINITY);
+                        }
+#pragma unroll
+                        for (int c = 2 * h; c < 2 * h + 2; ++c) {
+                            tops[c] = __uint_as_float(s[c][0]);
+#pragma unroll
+                            for (int j = 1; j < 32; ++j) tops[c] = fmaxf(tops[c], __uint_as_float(s[c][j]));
                         }
                     }
-                    ptx::fence_proxy_async_smem();
-                }
-                lat::tmem_wait_st();
-                ptx::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(bar(sh.p_full[g]));
-            }
-            if (ok && mine > 0) {
-                ok = lat::wait_warp(bar(sh.o_full[g]), 0, sync);
-                ptx::tc_fence_after();
-            }
-            if (ok) {
-                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-                const int64_t at = (int64_t(r.q0) + q) * a.H + head;
-                if (a.lse != nullptr && q < r.n) a.lse[at] = l > 0.0f ? (ref + log2f(l)) * kLn2 : -INFINITY;
-                uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + at * a.N);
+                    const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * a.scale2;
+                    const bool grow = top > ref + kGrow || (ref == -INFINITY && top > -INFINITY);
+                    if (__any_sync(0xFFFFFFFFu, grow)) {
+                        const float f = grow ? lat::ex2(ref - top) : 1.0f;
+                        if (grow) ref = top;
+                        l *= f;
+                        if (t > 0) {
 #pragma unroll 1
-                for (int c = 0; c < VC * 2; ++c) {
-                    uint32_t o[32];
-                    if (mine > 0) {
-                        ptx::tmem_ld<32>(t_o + c * 32, o);
-                        ptx::tmem_wait_ld();
-                    } else {
+                            for (int c = 0; c < VC * 8; ++c) {
+                                uint32_t o[8];
+                                ptx::tmem_ld<8>(t_o + c * 8, o);
+                                ptx::tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] = 0u;
+                                for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                                lat::tmem_st<8>(t_o + c * 8, o);
+                            }
+                        }
                     }
-                    if (q < r.n) {
+                    const float base = ref == -INFINITY ? 0.0f : ref;
+                    const float2 scale = make_float2(a.scale2, a.scale2), minus = make_float2(-base, -base);
+                    float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint4 w;
-                            uint32_t* pw = &w.x;
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t p[16];
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                pw[j] = Pair<T>::pack(__uint_as_float(o[i * 8 + 2 * j]) * inv, __uint_as_float(o[i * 8 + 2 * j + 1]) * inv);
-                            out[c * 4 + i] = w;
+                        for (int j = 0; j < 32; j += 2) {
+                            float2 x = make_float2(__uint_as_float(s[c][j]), __uint_as_float(s[c][j + 1]));
+                            x = lat::fma2(x, scale, minus);
+                            x.x = lat::ex2(x.x);
+                            x.y = lat::ex2(x.y);
+                            sum[(j >> 1) & 1] = lat::add2(sum[(j >> 1) & 1], x);
+                            p[j / 2] = Pair<T>::pack(x.x, x.y);
+                        }
+                        lat::tmem_st<16>(t_s + c * 16, p);
+                    }
+                    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                    // Weights past the request's keys are zero, but 0 times what lies there need not be: each
+                    // group clears those rows of the values before its own product.
+                    if ((t + 1) * kTile > r.m) {
+                        ok = lat::wait_warp(bar(sh.v_full[(kt + t) & 3]), ((kt + t) >> 2) & 1, sync);
+                        if (!ok) break;
+                        if (t * kTile + row >= r.m) {
+#pragma unroll
+                            for (int c = 0; c < VC; ++c) {
+                                uint4* z = reinterpret_cast<uint4*>(smem + (((kt + t) * kPer + KC + c) % kSlots) * kChunkBytes + row * 128);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) z[i] = make_uint4(0, 0, 0, 0);
+                            }
+                        }
+                        ptx::fence_proxy_async_smem();
+                    }
+                    lat::tmem_wait_st();
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(bar(sh.p_full[g]));
+                }
+                if (ok && mine > 0) {
+                    ok = lat::wait_warp(bar(sh.o_full[g]), o_used++ & 1u, sync);
+                    ptx::tc_fence_after();
+                }
+                if (ok) {
+                    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+                    const int64_t at = (int64_t(r.q0) + q) * a.H + it.head;
+                    if (a.lse != nullptr && q < r.n) a.lse[at] = l > 0.0f ? (ref + log2f(l)) * kLn2 : -INFINITY;
+                    uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + at * a.N);
+                    const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
+#pragma unroll 1
+                    for (int c = 0; c < VC * 2; ++c) {
+                        uint32_t o[32];
+                        if (mine > 0) {
+                            ptx::tmem_ld<32>(t_o + c * 32, o);
+                            ptx::tmem_wait_ld();
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) o[j] = 0u;
+                        }
+                        if (q < r.n) {
+                            uint32_t w[16];
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                w[j] = Pair<T>::pack(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
+                            if (wide) {   // a row a thread: whole sectors of 32 bytes
+                                ptx::st_global_v8(out + c * 4, *reinterpret_cast<uint32_t (*)[8]>(w));
+                                ptx::st_global_v8(out + c * 4 + 2, *reinterpret_cast<uint32_t (*)[8]>(w + 8));
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) out[c * 4 + i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                            }
                         }
                     }
                 }
+                ptx::tc_fence_before();
             }
-            ptx::tc_fence_before();
+            kt += it.tiles();
         }
     }
     __syncthreads();
@@ -450,12 +528,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             while (uses > 0 && !ptx::mbar_test_wait(bar(x), (uses - 1) & 1u) && ptx::globaltimer() - t0 < (1ull << 26)) {}
         };
         if (warp == 0 || warp == 3) {
-            for (uint32_t i = 0; i < 4; ++i) {
-                land(sh.k_full[i], keys / 4 + (i < keys % 4 ? 1 : 0));
-                land(sh.v_full[i], values / 4 + (i < values % 4 ? 1 : 0));
+            for (uint32_t i = 0; i < 4; ++i) land(warp == 0 ? sh.k_full[i] : sh.v_full[i], kt / 4 + (i < kt % 4 ? 1 : 0));
+            if (warp == 0) {
+                land(sh.q_full[0], q_used[0]);
+                land(sh.q_full[1], q_used[1]);
+                land(sh.taken, number);
             }
-            if (warp == 0 && tiles > 0 && count[0] > 0) land(sh.q_full[0], 1);
-            if (keys > 0 && count[1] > 0) land(sh.q_full[1], 1);
         } else if (threadIdx.x == 32 || threadIdx.x == 64) {
             ptx::tc_commit(bar(sh.drain));
             land(sh.drain, 1);
@@ -552,6 +630,7 @@ sgq_status launch_latent_prefill(const PrefillArgs& x, cudaStream_t st) {
     a.R = x.R;
     a.causal = x.causal;
     a.scale2 = x.scale * kLog2e;
+    a.span_size = static_cast<int>((x.B + kSpans - 1) / kSpans);
     const int64_t blocks = (x.T / (2 * kTile) + x.B) * x.H;   // at least the query tile pairs of any split of T
     if (blocks > INT32_MAX) return SGQ_ERR_INVALID_ARG;
     CUtensorMap tm[4];

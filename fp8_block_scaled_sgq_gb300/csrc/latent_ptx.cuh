@@ -88,6 +88,31 @@ __device__ __forceinline__ void bulk_prefetch(const void* p, uint32_t bytes) {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
+// Asks to take over a CTA of this grid that has not started: the answer (16
+// bytes at a 16-byte aligned shared address) completes 16 bytes of
+// transactions on `bar`.  Not to be asked again after an answer of no.
+__device__ __forceinline__ void take_item(uint32_t answer, uint32_t bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     answer),
+                 "r"(bar)
+                 : "memory");
+}
+// Whether the answer is yes, and then the block index (x) taken over.
+__device__ __forceinline__ bool taken_item(uint32_t answer, uint32_t& x) {
+    uint32_t yes, index;
+    asm volatile(
+        "{\n.reg .pred p;\n.reg .b128 r;\n"
+        "ld.shared.b128 r, [%2];\n"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n"
+        "selp.u32 %0, 1, 0, p;\nmov.u32 %1, 0;\n"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n}"
+        : "=r"(yes), "=r"(index)
+        : "r"(answer)
+        : "memory");
+    x = index;
+    return yes != 0u;
+}
+
 // 32 lanes x N consecutive 32-bit columns; thread t writes lane (base_lane + t).
 template <int N>
 __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[N]);
