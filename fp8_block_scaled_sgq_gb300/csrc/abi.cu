@@ -295,7 +295,7 @@ sgq_status sgq_latent_attention(const void* q, int64_t q_stride_row, int64_t T, 
         !good_strides({q_stride_row, cache_stride_page, cache_stride_row}) || !(std::isfinite(scale) && scale > 0.0f))
         return SGQ_ERR_INVALID_ARG;
     if (pages <= 0 || pages >= (int64_t(1) << 31) || page <= 0 || page % 16 != 0 || page >= (int64_t(1) << 31) ||
-        table_width < 0 || table_width * page >= (int64_t(1) << 31) || q_stride_row < L + R ||
+        table_width < 0 || table_width * page > (int64_t(1) << 31) - 256 || q_stride_row < L + R ||
         cache_stride_row < L + R || cache_stride_page < cache_stride_row * page)
         return SGQ_ERR_INVALID_ARG;
     if (q_starts == nullptr && T != B) return SGQ_ERR_INVALID_ARG;

@@ -8,6 +8,7 @@ ValueError before anything is launched.
 """
 from __future__ import annotations
 
+import functools
 import math
 
 from . import binding
@@ -187,6 +188,11 @@ def latent_append(q_rot, k_rot, latent, positions, slots, table, cache, interlea
     return q_out
 
 
+@functools.lru_cache(maxsize=256)
+def _workspace_bytes(T: int, H: int, latent: int) -> int:
+    return binding.sgq_latent_attention_workspace(T, H, latent)
+
+
 def latent_attention(q, cache, page_table, kv_lens, scale: float, latent: int, q_starts=None, out=None, lse=None,
                      workspace=None, stream=None):
     """Absorbed latent attention over a paged cache: out [T, H, latent].
@@ -223,7 +229,7 @@ def latent_attention(q, cache, page_table, kv_lens, scale: float, latent: int, q
     if lse is not None:
         _contiguous("lse", lse, (T, H), torch.float32)
     if workspace is None:
-        nbytes = binding.sgq_latent_attention_workspace(T, H, latent)
+        nbytes = _workspace_bytes(T, H, latent)
         workspace = _empty(nbytes // 2, q, stream)
     else:
         nbytes = workspace.numel() * workspace.element_size()
