@@ -189,6 +189,7 @@ struct Shared {
     // the schedule: totals of the threads' requests, then the CTA's start
     int64_t per, total;
     int b, block, hblk, at;
+    Request r;
     int64_t warp_sum[20];
     alignas(16) float ref[4][16], fade[4][16];   // [column group][column]: new reference, 2^(old - new)
     float top[4][4][16], sum[4][4][16];          // [column group][lane quarter][column]
@@ -242,6 +243,7 @@ __device__ __forceinline__ void plan(const Args& a, Shared& sh) {
             }
             const int64_t item = (start - at) / (c + kItemCost);
             sh.b = b;
+            sh.r = r;
             sh.block = i + static_cast<int>(item / (a.hb / a.team));
             sh.hblk = static_cast<int>(item % (a.hb / a.team));
             sh.at = static_cast<int>((start - at) - item * (c + kItemCost));
@@ -332,7 +334,7 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
         w.block = sh.block;
         w.hblk = sh.hblk;
         w.at = sh.at;
-        w.r = request(a, w.b, false);
+        w.r = sh.r;
         w.settle(a);
         if (w.at >= w.count) any = w.next(a);       // the run starts in an item's cost
     }
@@ -694,7 +696,8 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
 // unnormalised sum o_i with reference m_i and sum l_i, and
 //     out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i,  M = max m_i,
 // in a fixed order.  Rows of few parts take a warp each, eight rows a block;
-// rows of many parts a block each, a warp every eighth part.
+// of rows of many parts, every 128 columns take a block, a warp every eighth
+// part.
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 constexpr int kMaxGrid = 512;
 constexpr int kFewParts = kJoinWarps;
@@ -704,7 +707,7 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const Args a,
     ptx::grid_dependency_wait();
     __shared__ int first[kMaxGrid + 1];                   // prefix sums of the CTAs' units of work
     __shared__ int sums[kJoinWarps];
-    __shared__ alignas(16) float acc[kJoinWarps][512];
+    __shared__ alignas(16) float acc[kJoinWarps][128];
     __shared__ float acc_l[kJoinWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int run = 0;
@@ -712,7 +715,7 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const Args a,
         const int c = base + threadIdx.x;
         int4 j = make_int4(0, 0, 0, 0);
         if (c < grid) j = a.joins[c];
-        int v = j.z == 0 ? 0 : j.z <= kFewParts ? (j.y + kJoinWarps - 1) / kJoinWarps : j.y;
+        int v = j.z == 0 ? 0 : j.z <= kFewParts ? (j.y + kJoinWarps - 1) / kJoinWarps : j.y * (a.L / 128);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int up = __shfl_up_sync(0xFFFFFFFFu, v, o);
@@ -731,7 +734,7 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const Args a,
     }
     if (threadIdx.x == 0) first[0] = 0;
     __syncthreads();
-    const int nq = a.L / 128;                             // 128 columns: four a lane
+    const int blocks = a.L / 128;                         // of 128 columns: four a lane
     for (int u = blockIdx.x; u < first[grid]; u += gridDim.x) {
         int lo = 0, hi = grid;
         while (hi - lo > 1) {
@@ -742,7 +745,8 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const Args a,
         // (CTAs without work share their neighbour's prefix: the last one with first <= u has some)
         const int4 j = a.joins[lo];
         const bool few = j.z <= kFewParts;
-        const int r = few ? (u - first[lo]) * kJoinWarps + warp : u - first[lo], parts = j.z;
+        const int r = few ? (u - first[lo]) * kJoinWarps + warp : (u - first[lo]) / blocks, parts = j.z;
+        const int q0 = few ? 0 : (u - first[lo]) % blocks, nq = few ? blocks : 1;   // this unit's column blocks
         const int step = few ? 1 : kJoinWarps;
         const bool mine = r < j.y;
         auto slot = [&](int i) { return (i == 0 ? int64_t(2) * lo + 1 : int64_t(2) * (lo + i * a.team)) * NR + r; };
@@ -757,7 +761,7 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const Args a,
             for (int i = few ? 0 : warp; i < parts; i += step) {
                 const int64_t s = slot(i);
                 const float2 st = __ldcg(&a.stats[s]);
-                const float4* src = reinterpret_cast<const float4*>(a.partial + s * a.L) + lane;
+                const float4* src = reinterpret_cast<const float4*>(a.partial + s * a.L) + q0 * 32 + lane;
                 const float f = lat::ex2(st.x - m);
                 l = fmaf(f, st.y, l);
 #pragma unroll
@@ -785,9 +789,7 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const Args a,
             }
             continue;
         }
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            if (q < nq) reinterpret_cast<float4*>(acc[warp])[q * 32 + lane] = o[q];
+        reinterpret_cast<float4*>(acc[warp])[lane] = o[0];
         if (lane == 0) acc_l[warp] = l;
         __syncthreads();
         l = 0.0f;
@@ -795,7 +797,7 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const Args a,
         for (int w = 0; w < kJoinWarps; ++w) l += acc_l[w];
         const float inv = l > 0.0f ? 1.0f / l : 0.0f;
         const int c = 2 * threadIdx.x;
-        if (c < a.L) {
+        if (c < 128) {
             float x = 0.0f, y = 0.0f;
 #pragma unroll
             for (int w = 0; w < kJoinWarps; ++w) {
@@ -803,9 +805,9 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const Args a,
                 x += v.x;
                 y += v.y;
             }
-            *reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + row * a.L + c) = Pair<T>::pack(x * inv, y * inv);
+            *reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + row * a.L + q0 * 128 + c) = Pair<T>::pack(x * inv, y * inv);
         }
-        if (a.lse != nullptr && threadIdx.x == 0) a.lse[row] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        if (a.lse != nullptr && threadIdx.x == 0 && q0 == 0) a.lse[row] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
         __syncthreads();
     }
 }
