@@ -217,6 +217,21 @@ def test_long_axis_is_split(H, lens):
     check_attention(H, [1] * len(lens), lens, 512, 64, 64, torch.bfloat16, singles=True)
 
 
+@pytest.mark.parametrize("H", [65, 130, 200, 257, 300])
+def test_more_heads_than_a_block(H):
+    """Two, three and four head blocks side by side, and more of them one after the other."""
+    check_attention(H, [1] * 5, [1000, 3, 0, 129, 2500], 512, 64, 32, torch.bfloat16, singles=True)
+    check_attention(H, [3, 1, 40], [300, 2, 45], 256, 32, 16, torch.float16)
+
+
+def test_tables_without_pages():
+    cache = torch.full((2, 16, 576), float("nan"), dtype=torch.bfloat16, device="cuda")
+    q = normal(3, 16, 576, dtype=torch.bfloat16, seed=1)
+    lse = torch.empty(3, 16, device="cuda")
+    out = sgq.latent_attention(q, cache, torch.empty(3, 0, dtype=torch.int32, device="cuda"), ints([0, 0, 0]), 0.1, 512, lse=lse)
+    assert (out == 0).all() and torch.isneginf(lse).all()
+
+
 def test_many_requests():
     lens = [(i * 37) % 300 for i in range(700)]
     check_attention(4, [1] * 700, lens, 128, 16, 16, torch.bfloat16, singles=True)
@@ -294,6 +309,33 @@ def test_page_and_length_outside_are_reported():
     assert sgq.sgq_device_status() == 1 and torch.equal(out[1], good[1])
     sgq.latent_attention(q, cache, table.clamp(max=3), ints([40, 2000]), 0.1, 128)
     assert sgq.sgq_device_status() == 1
+
+
+@pytest.mark.parametrize("starts", [[0, 1, 2], [1, 2, 3], [0, 3, 2], [0, 1, 4], [0, -1, 3]])
+def test_starts_that_do_not_fit_are_reported(starts):
+    cache, table, _ = paged([40, 20], 16, 192, torch.bfloat16, seed=1)
+    q = normal(3, 4, 192, dtype=torch.bfloat16, seed=2)
+    sgq.latent_attention(q, cache, table, ints([40, 20]), 0.1, 128, q_starts=ints(starts))
+    assert sgq.sgq_device_status() == 1
+    kv = normal(3, 4, 256, dtype=torch.bfloat16, seed=3)
+    kr = normal(3, 64, dtype=torch.bfloat16, seed=4)
+    q = normal(3, 4, 192, dtype=torch.bfloat16, seed=5)
+    for a, b in ((starts, [0, 1, 3]), ([0, 1, 3], starts)):
+        sgq.latent_prefill(q, kv[..., :128], kr, kv[..., 128:], ints(a), ints(b), 0.1)
+        assert sgq.sgq_device_status() == 1
+
+
+def test_workspace_given_and_too_small():
+    cache, table, _ = paged([1000, 20], 16, 576, torch.bfloat16, seed=1)
+    q, lens = normal(2, 16, 576, dtype=torch.bfloat16, seed=2), ints([1000, 20])
+    want = sgq.latent_attention(q, cache, table, lens, 0.1, 512)
+    n = sgq.sgq_latent_attention_workspace(2, 16, 512)
+    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")       # what it holds before does not matter
+    for _ in range(2):
+        assert torch.equal(sgq.latent_attention(q, cache, table, lens, 0.1, 512, workspace=ws), want)
+    with pytest.raises(sgq.SgqError) as e:
+        sgq.latent_attention(q, cache, table, lens, 0.1, 512, workspace=ws[:n - 16])
+    assert e.value.status == 1
 
 
 def test_another_stream_and_graph():
@@ -374,6 +416,33 @@ def test_prefill_many_requests():
     check_prefill(2, lens, lens, 64, 32, torch.bfloat16)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+def test_prefill_more_items_than_sms(causal):
+    """CTAs take over items: pairs of query tiles with one and two tiles, without keys, of many lengths."""
+    check_prefill(40, [700, 300, 1, 513, 20], [700, 350, 1, 513, 0], 128, 64, torch.bfloat16, causal)
+
+
+def test_prefill_long():
+    check_prefill(2, [3001], [3001], 128, 64, torch.bfloat16)
+    check_prefill(1, [130], [4500], 64, 32, torch.float16, causal=False)
+
+
+def test_prefill_strides_and_alignment():
+    """Heads outside tokens, rows with gaps, an output that is aligned to 16 bytes only."""
+    T, H = 300, 3
+    q = normal(H, T, 192 + 8, dtype=torch.bfloat16, seed=1).transpose(0, 1)[..., 8:]
+    k, v = (normal(H, T, 128, dtype=torch.bfloat16, seed=s).transpose(0, 1) for s in (2, 3))
+    kr = normal(T, 96, dtype=torch.bfloat16, seed=4)[:, 16:80]
+    starts = ints([0, 100, T])
+    want = sgq.latent_prefill(q.contiguous(), k.contiguous(), kr.contiguous(), v.contiguous(), starts, starts, 0.1)
+    got = sgq.latent_prefill(q, k, kr, v, starts, starts, 0.1)
+    assert torch.equal(got, want)
+    flat = torch.full((T * H * 128 + 16,), 5.0, dtype=torch.bfloat16, device="cuda")
+    out = flat[8:8 + T * H * 128].view(T, H, 128)
+    assert torch.equal(sgq.latent_prefill(q, k, kr, v, starts, starts, 0.1, out=out), want)
+    assert (flat[:8] == 5).all() and (flat[-8:] == 5).all()
+
+
 def test_prefill_another_stream():
     q = normal(300, 2, 192, dtype=torch.bfloat16, seed=1)
     up, kr = normal(300, 2, 256, dtype=torch.bfloat16, seed=2), normal(300, 64, dtype=torch.bfloat16, seed=3)
@@ -408,3 +477,11 @@ def test_absorbed_equals_expanded():
     absorbed = torch.einsum("hnl,thl->thn", down, o.float())
     # operands and outputs rounded to fp16 on the way: a few 2^-11 of values of order 1, scores of order 3
     assert (absorbed - expanded.float()).abs().max() < 0.02
+
+
+def test_layer_on_all_of_them():
+    """A prompt and tokens through FP8 linears and the four operators: the two forms differ by the quantisation of the
+    expanded keys' and values' input (E4M3, 3 significand bits after the point: 2^-4 relative at most an element, some
+    3% of a row's norm), which both the projections after it and the attention average."""
+    from fp8_block_scaled_sgq_gb300 import latent_example
+    assert latent_example.main() < 2 ** -4
