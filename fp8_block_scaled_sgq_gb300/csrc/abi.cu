@@ -328,6 +328,10 @@ sgq_status sgq_latent_prefill(const void* q, int64_t q_stride_t, int64_t q_strid
         !good_strides({q_stride_t, q_stride_h, k_stride_t, k_stride_h, kr_stride, v_stride_t, v_stride_h}) ||
         (causal != 0 && causal != 1) || !(std::isfinite(scale) && scale > 0.0f))
         return SGQ_ERR_INVALID_ARG;
+    // (rows and heads one after the other in memory: no broadcast dimensions)
+    if ((T > 1 && q_stride_t == 0) || (S > 1 && (k_stride_t == 0 || v_stride_t == 0 || kr_stride == 0)) ||
+        (H > 1 && (q_stride_h == 0 || k_stride_h == 0 || v_stride_h == 0)))
+        return SGQ_ERR_INVALID_ARG;
     if (T == 0) return SGQ_OK;
     if (B == 0 || !q || !q_starts || !kv_starts || !out || (S > 0 && (!k || !k_rot || !v))) return SGQ_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(k) || !aligned16(k_rot) || !aligned16(v) || !aligned16(out) ||

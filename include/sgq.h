@@ -424,7 +424,8 @@ sgq_status sgq_latent_attention(const void* q, int64_t q_stride_row, int64_t T, 
  * over j <= m - n + i (causal = 1; n queries, m keys) or all j (causal = 0).
  * A query without a key to see gets zeros, and lse -inf.
  *
- * q: [T, H, N + R]; k, v: [S, H, N]; k_rot: [S, R]; token (and head) strides.
+ * q: [T, H, N + R]; k, v: [S, H, N]; k_rot: [S, R]; token (and head) strides,
+ * none of them 0 where there is more than one token or head.
  * out: [T, H, N], lse: fp32 [T, H] or NULL, both contiguous.  q_starts,
  * kv_starts: int32 [B + 1], rising, ending at T and S.  N in {64, 128};
  * R % 8 == 0, 8 <= R <= 64; H <= 65535; scale > 0.  All rows of k, v and k_rot that

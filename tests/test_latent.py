@@ -86,7 +86,7 @@ def test_prefill_validation(lib):
              qs=E, ks=F, B=1, scale=0.1, causal=1, dtype=0, out=G, lse=None)
     f = caller(lib.sgq_latent_prefill, list(d), d)
     for bad in (dict(T=-1), dict(S=-1), dict(H=0), dict(N=96), dict(N=256), dict(R=0), dict(R=72), dict(R=20),
-                dict(dtype=2), dict(causal=2), dict(qt=3073), dict(vh=-256), dict(krt=4), dict(B=0), dict(q=None),
+                dict(dtype=2), dict(causal=2), dict(qt=3073), dict(vh=-256), dict(krt=4), dict(krt=0), dict(kh=0), dict(qt=0), dict(vt=0), dict(B=0), dict(q=None),
                 dict(k=None), dict(kr=None), dict(v=None), dict(qs=None), dict(ks=None), dict(out=None),
                 dict(scale=float("inf")), dict(scale=-1.0)):
         assert f(**bad) == INV, bad
