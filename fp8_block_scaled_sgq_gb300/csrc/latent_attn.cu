@@ -13,10 +13,17 @@
 // is rescaled only on those steps.  P is rounded once, to the cache's type,
 // as the second product's operand; l sums the unrounded p.
 //
-// What bounds it: a tile is 147 KB of cache (L + R = 576), 22 us of HBM time
-// for 151 MB; the MMAs of a tile take 68 steps of about 36 (NR = 16) to 48
-// cycles (NR = 64: the operands' shared-memory reads), which is below a tile's
-// share of HBM time for up to 64 rows.
+// What bounds it.  A tile is 147 KB of cache (L + R = 576) and takes 68 steps
+// of MMAs, of 40 cycles (NR = 16) to 49 (NR = 64, the operands' reads of shared
+// memory).  With 16 rows a tile's MMAs and softmax take less than its share of
+// HBM time, and HBM is the bound once a CTA is under way: 64 sequences of 130
+// to 16384 rows with 16 heads (200 MB) in 50 us, of which 30 are the bytes at
+// the measured copy rate and 7 the joining kernel and its launch.  With 64
+// rows it is shared memory: reads by the MMAs and writes by TMA take 4470
+// cycles a tile at least.  Only the tile in use fits beside the queries, so
+// shared memory idles while softmax runs between the two products: 5540 cycles
+// a tile.  128 sequences of 1024 to 8192 rows with 128 heads: 171 us (538 MB);
+// one of 131071 rows: 73 us (151 MB); chunks: 392 us (692 TFLOP/s).
 //
 // Layout.  A tile sits in shared memory once, as chunks of 128 rows x 64
 // columns with 128-byte swizzle: read K-major for S^T and, by the descriptor's
@@ -86,7 +93,7 @@ struct Args {
     int4* joins;         // [grid]: first row, rows, parts (0: nothing to join)
     uint32_t* status;
     int64_t T, B, pages, width, c_page, c_row;   // strides in bytes
-    uint32_t box_bytes;
+    uint32_t box_bytes;                          // a box's span, fetched ahead into L2 (0: not)
     int H, L, R, page, box;
     int tpn, hb;         // tokens a block, head blocks a token (one of them is 1)
     uint64_t inv_teams;  // 2^64 / teams, rounded up
@@ -414,7 +421,7 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
                 }
                 ++rope;
                 // The next tile goes to L2 while its loads wait for their slots.
-                if (id == 0 && tile + 1 < end && lane < next_boxes && next_page >= 0 && next_page < a.pages)
+                if (id == 0 && a.box_bytes != 0 && tile + 1 < end && lane < next_boxes && next_page >= 0 && next_page < a.pages)
                     lat::bulk_prefetch(a.cache + next_page * a.c_page + next_in * a.c_row, a.box_bytes);
                 __syncwarp();
                 boxes = next_boxes;
@@ -917,7 +924,9 @@ sgq_status launch_latent_attention(const LatentArgs& x, cudaStream_t st) {
     a.R = x.R;
     a.page = x.page;
     a.box = std::min(x.page & -x.page, kTile);   // rows of a box: whole boxes in a page and in a tile
-    a.box_bytes = static_cast<uint32_t>((a.box - 1) * a.c_row + 2 * (x.L + x.R));
+    // (rows that lie apart, as those of a layer between others, are not: what is between them is not wanted)
+    const int64_t row_bytes = 2 * int64_t(x.L + x.R);
+    a.box_bytes = a.c_row <= row_bytes + row_bytes / 8 ? static_cast<uint32_t>((a.box - 1) * a.c_row + row_bytes) : 0u;
     a.tpn = std::max(1, NR / x.H);
     a.hb = (x.H + NR - 1) / NR;
     // (more head blocks than that are a walk of one CTA: teams would leave CTAs over)
