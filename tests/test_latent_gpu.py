@@ -296,6 +296,19 @@ def test_strided_queries_and_cache():
         ref.check_rows(a[i], None, *want, torch.float16)
 
 
+def test_cache_of_several_layers_side_by_side():
+    L, R, page, H = 512, 64, 32, 16
+    W = L + R
+    lens = [700, 33, 0, 257]
+    cache, table, rows = paged(lens, page, W, torch.bfloat16, seed=23)
+    layers = torch.full((cache.shape[0], page, 3, W), float("nan"), dtype=torch.bfloat16, device="cuda")
+    layers[:, :, 1] = cache
+    q = normal(4, H, W, dtype=torch.bfloat16, seed=24)
+    a = sgq.latent_attention(q, layers[:, :, 1], table, ints(lens), 0.1, L)
+    b = sgq.latent_attention(q, cache, table, ints(lens), 0.1, L)
+    assert torch.equal(a, b)
+
+
 def test_page_and_length_outside_are_reported():
     cache, table, _ = paged([40, 20], 16, 192, torch.bfloat16, seed=1)
     q = normal(2, 4, 192, dtype=torch.bfloat16, seed=2)
