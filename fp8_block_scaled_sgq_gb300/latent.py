@@ -228,19 +228,20 @@ def latent_attention(q, cache, page_table, kv_lens, scale: float, latent: int, q
         _contiguous("out", out, (T, H, latent))
     if lse is not None:
         _contiguous("lse", lse, (T, H), torch.float32)
-    if workspace is not None:
-        binding.sgq_latent_attention(q, row, T, H, cache, pages, page, cp, cr, latent, W - latent, page_table, table_width, B, kv_lens,
-                   q_starts, scale, dt, out, lse, workspace, workspace.numel() * workspace.element_size(), stream)
-        return out
-    # Memory of torch's allocator without a tensor around it (a short call's 21 us of host time -> 19); it
-    # belongs to the call's stream, and goes back to that stream's memory as soon as the call is queued.
-    nbytes, stream = _workspace_bytes(T, H, latent), binding._stream(stream)
-    workspace = torch._C._cuda_cudaCachingAllocator_raw_alloc(nbytes, stream)
+    stream, own = binding._stream(stream), None
+    if workspace is None:
+        # Memory of torch's allocator without a tensor around it (a short call's 21 us of host time -> 19); it
+        # belongs to the call's stream, and goes back to that stream's memory as soon as the call is queued.
+        nbytes = _workspace_bytes(T, H, latent)
+        workspace = own = torch._C._cuda_cudaCachingAllocator_raw_alloc(nbytes, stream)
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
     try:
-        binding.sgq_latent_attention(q, row, T, H, cache, pages, page, cp, cr, latent, W - latent, page_table, table_width, B, kv_lens,
-                   q_starts, scale, dt, out, lse, workspace, nbytes, stream)
+        binding.sgq_latent_attention(q, row, T, H, cache, pages, page, cp, cr, latent, W - latent, page_table,
+                                     table_width, B, kv_lens, q_starts, scale, dt, out, lse, workspace, nbytes, stream)
     finally:
-        torch._C._cuda_cudaCachingAllocator_raw_delete(workspace)
+        if own is not None:
+            torch._C._cuda_cudaCachingAllocator_raw_delete(own)
     return out
 
 
