@@ -189,9 +189,18 @@ struct Walk {
     }
 };
 
+// What the softmax warps need to know of an item.
+struct alignas(16) Item {
+    int64_t row0;
+    int rows, at, end;   // rows (0: no more items), tiles [at, end)
+    int m, n, first;     // the request's cached rows and tokens, the block's first token
+    int parts;           // of its result: 1: this is all of it; 0: some other CTA's
+};
+
 struct Shared {
     uint64_t full[kMaxPairs], empty[kMaxPairs], rope_full[kMaxRope], rope_empty[kMaxRope];
-    uint64_t q_full, q_empty, s_full, p_full, o_full, drain;
+    uint64_t q_full, q_empty, s_full, p_full, o_full, item_full[2], drain;
+    Item item[2];        // the CTA's items, in turn
     uint32_t tmem, abort;
     // the schedule: totals of the threads' requests, then the CTA's start
     int64_t per, total;
@@ -314,6 +323,8 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
         ptx::mbar_init(bar(sh.s_full), 1);
         ptx::mbar_init(bar(sh.p_full), 4 * C::kGroups);
         ptx::mbar_init(bar(sh.o_full), 1);
+        ptx::mbar_init(bar(sh.item_full[0]), 1);
+        ptx::mbar_init(bar(sh.item_full[1]), 1);
         ptx::mbar_init(bar(sh.drain), 1);
         sh.abort = 0;
         ptx::fence_mbar_init();
@@ -442,6 +453,28 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
         const uint32_t t_o = lat::uniform(tmem), t_s = t_o + C::kColS;
         uint32_t tiles_done = 0;
         bool ok = true;
+        Walk next = w;
+        bool more = true;
+        // An entry is written again two items later, after the first scores of the item between: by then the
+        // softmax warps have taken it over.
+        uint32_t items = 0;
+        auto tell = [&]() {
+            if (lane == 0) {
+                Item& i = sh.item[items & 1];
+                i.rows = more ? next.rows(a) : 0;
+                i.row0 = next.row0(a);
+                i.at = next.at;
+                i.end = next.end();
+                i.m = next.r.m;
+                i.n = next.r.n;
+                i.first = next.block * a.tpn;
+                i.parts = i.at > 0 ? 0 : i.end == next.count ? 1 : static_cast<int>((next.count - next.left + sh.per - 1) / sh.per) + 1;
+                ptx::mbar_arrive(bar(sh.item_full[items & 1]));
+            }
+            __syncwarp();
+            ++items;
+        };
+        tell();
         do {
             ok = lat::wait_warp(bar(sh.q_full), seg & 1u, sync);
             if (!ok) break;
@@ -468,6 +501,10 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
                 lat::mma4_f16<2, 2>(t_s, lo_r + rope_slot * kChunk, kHiK, lo_q + np * 2 * kQ, kHiK, kIdS, 1u);
                 ptx::commit_elect(bar(sh.s_full));
                 if (tile + 1 == end) ptx::commit_elect(bar(sh.q_empty));
+                if (tile == w.at) {
+                    more = next.next(a);
+                    tell();
+                }
                 pair += np;
                 ++rope;
                 ok = lat::wait_warp(bar(sh.p_full), tiles_done & 1u, sync);
@@ -487,7 +524,8 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
                 ptx::commit_elect(bar(sh.rope_empty[rope_slot]));
                 if (tile + 1 == end) ptx::commit_elect(bar(sh.o_full));
             }
-        } while (ok && w.next(a));
+            w = next;
+        } while (ok && more);
     } else if (warp > kLoaders && any) {
         // ------------------------------------------------------------ softmax
         const int quarter = warp & 3, group = (warp - 1 - kLoaders) >> 2;
@@ -497,10 +535,17 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
         const int id = 1 + group;
         uint32_t tiles_done = 0;
         bool ok = true;
-        do {
-            const int end = w.end();
-            const int first_token = w.block * a.tpn;
-            const int low = sees(w.r, first_token);                // rows that every row of the block sees
+        for (;; ++seg) {
+            ok = ok && lat::wait_warp(bar(sh.item_full[seg & 1u]), (seg >> 1) & 1u, sync);
+            const Item it = sh.item[seg & 1u];
+            // What the item's tiles find in shared memory: no reference, and what each column's token sees.
+            if (quarter == 0 && lane < HC) {
+                sh.ref[group][lane] = kNone;
+                const int token = min(it.first + (a.hb == 1 ? (group * HC + lane) / a.H : 0), it.n - 1);
+                sh.sees[group * HC + lane] = max(0, it.m - it.n + token + 1);
+            }
+            if (lat::named_any(id, 128, !ok) || it.rows == 0) break;
+            const int low = max(0, it.m - it.n + it.first + 1);    // rows that every row of the block sees
             // l, ref: sum and reference of every column, the sums of this thread's token only
             float ref[HC], l[HC];
 #pragma unroll
@@ -508,15 +553,9 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
                 l[j] = 0.0f;
                 ref[j] = kNone;
             }
-            // (the group's barriers of the segment before came after its last reads)
-            if (quarter == 0 && lane < HC) {
-                sh.ref[group][lane] = kNone;
-                sh.sees[group * HC + lane] = sees(w.r, min(first_token + (a.hb == 1 ? (group * HC + lane) / a.H : 0), w.r.n - 1));
-            }
-            lat::named_sync(id, 128);
             bool failed = false;
 #pragma unroll 1
-            for (int tile = w.at; tile < end; ++tile) {
+            for (int tile = it.at; tile < it.end; ++tile) {
                 ok = lat::wait_warp(bar(sh.s_full), tiles_done & 1u, sync);
                 ++tiles_done;
                 ptx::tc_fence_after();
@@ -538,15 +577,19 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
                 // Weights with the references as they are; if some score is past its reference by
                 // more than 2^kGrow (or is the first one seen), all of the group move them first.
                 uint32_t packed[HC / 2];
-                float p[HC], most = -INFINITY;
+                float p[HC];
+                bool move = true;                                  // an item's first tile sets them
+                if (tile > it.at) {
+                    float most = -INFINITY;
 #pragma unroll
-                for (int j = 0; j < HC; ++j) {
-                    p[j] = fmaf(__uint_as_float(raw_s[j]), a.scale2, -ref[j]);
-                    most = fmaxf(most, p[j]);
+                    for (int j = 0; j < HC; ++j) {
+                        p[j] = fmaf(__uint_as_float(raw_s[j]), a.scale2, -ref[j]);
+                        most = fmaxf(most, p[j]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < HC; ++j) p[j] = lat::ex2(p[j]);
+                    move = lat::named_any(id, 128, most > kGrow || !ok);
                 }
-#pragma unroll
-                for (int j = 0; j < HC; ++j) p[j] = lat::ex2(p[j]);
-                const bool move = lat::named_any(id, 128, most > kGrow || !ok);
                 if (move) {
                     float top = kNone;                             // of column cl
                     const int cl = lane & (HC - 1);
@@ -571,7 +614,7 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
                         l[j] *= sh.fade[group][j];
                         p[j] = lat::ex2(fmaf(__uint_as_float(raw_s[j]), a.scale2, -ref[j]));
                     }
-                    if (tile > w.at) {
+                    if (tile > it.at) {
 #pragma unroll 1
                         for (int b = 0; b < np; ++b) {
                             uint32_t o[HC];
@@ -600,7 +643,7 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
                         make_uint4(packed[4 * c], packed[4 * c + 1], packed[4 * c + 2], packed[4 * c + 3]);
                 }
                 // Weights past the request's rows are zero, but 0 times what lies there need not be.
-                if (token >= w.r.m) {
+                if (token >= it.m) {
 #pragma unroll 1
                     for (int c = group; c < 2 * np; c += C::kGroups) {
                         uint4* z = reinterpret_cast<uint4*>(smem + ((pair + c / 2) % C::kPairs) * 2 * kChunkBytes +
@@ -620,24 +663,21 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
             // ---- the segment's result
             const float mine = lane_sums<HC>(l);
             if (lane < HC) sh.sum[group][quarter][lane] = mine;
-            ok = lat::wait_warp(bar(sh.o_full), seg & 1u, sync);
-            ++seg;
-            if (lat::named_any(id, 128, !ok)) break;
+            lat::named_sync(id, 128);
             const int cl = lane & (HC - 1);
             const float mine_ref = quarter == 0 ? sh.ref[group][cl] : kNone;   // (the warp that sets it)
             const float total = (sh.sum[group][0][cl] + sh.sum[group][1][cl]) + (sh.sum[group][2][cl] + sh.sum[group][3][cl]);
-            const int64_t row0 = w.row0(a);
-            const int rows = w.rows(a);
+            const int rows = it.rows;
             const int col = group * HC + cl;                        // of the statistics
-            const bool whole = w.at == 0 && end == w.count;
+            const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+            ok = lat::wait_warp(bar(sh.o_full), seg & 1u, sync);   // (the next vote ends it where this ran out)
             ptx::tc_fence_after();
-            if (whole) {
-                const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+            if (it.parts == 1) {
                 if (a.lse != nullptr && quarter == 0 && lane < HC && col < rows)
-                    a.lse[row0 + col] = total > 0.0f ? (mine_ref + log2f(total)) * kLn2 : -INFINITY;
+                    a.lse[it.row0 + col] = total > 0.0f ? (mine_ref + log2f(total)) * kLn2 : -INFINITY;
                 const bool odd = (lane & 1) != 0;
                 uint32_t* out = reinterpret_cast<uint32_t*>(a.out) +
-                                (((row0 + group * HC + (odd ? 1 : 0)) * a.L + quarter * 32 + (lane & ~1)) >> 1);
+                                (((it.row0 + group * HC + (odd ? 1 : 0)) * a.L + quarter * 32 + (lane & ~1)) >> 1);
                 const int last = rows - group * HC - (odd ? 1 : 0);   // this lane's rows j < last exist
                 float f[HC];
 #pragma unroll
@@ -657,24 +697,24 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
                 }
             } else {
                 // The part that begins an item owns its joining: parts up to the CTA of the item's last tile.
-                if (w.at == 0 && threadIdx.x == 128)
-                    a.joins[blockIdx.x] = make_int4(static_cast<int>(row0), rows,
-                                                    static_cast<int>((w.count - w.left + sh.per - 1) / sh.per) + 1, 0);
-                const int64_t part = 2 * int64_t(blockIdx.x) + (w.at > 0 ? 0 : 1);
+                if (it.parts > 1 && threadIdx.x == 128)
+                    a.joins[blockIdx.x] = make_int4(static_cast<int>(it.row0), rows, it.parts, 0);
+                const int64_t part = 2 * int64_t(blockIdx.x) + (it.at > 0 ? 0 : 1);
                 if (quarter == 0 && lane < HC && col < rows) a.stats[part * NR + col] = make_float2(mine_ref, total);
-                float* dst = a.partial + (part * NR + group * HC) * a.L + quarter * 32 + lane;
+                float* const dst = a.partial + (part * NR + group * HC) * a.L + quarter * 32 + lane;
 #pragma unroll 1
-                for (int p = 0; p < np; ++p) {
-                    uint32_t o[HC];
-                    ptx::tmem_ld<HC>(t_o + p * NR, o);
+                for (int c = 0; c < HC / 8 * np; ++c) {
+                    const int p = HC == 8 ? c : c >> 1, j0 = HC == 8 ? 0 : (c & 1) * 8;
+                    uint32_t o[8];
+                    ptx::tmem_ld<8>(t_o + p * NR + j0, o);
                     ptx::tmem_wait_ld();
+                    float* row = dst + j0 * a.L + p * 128;
 #pragma unroll
-                    for (int j = 0; j < HC; ++j)
-                        if (group * HC + j < rows) dst[j * a.L + p * 128] = __uint_as_float(o[j]);
+                    for (int j = 0; j < 8; ++j, row += a.L) *row = __uint_as_float(o[j]);   // (rows that are none, too)
                 }
             }
             ptx::tc_fence_before();
-        } while (w.next(a));
+        }
     }
     __syncthreads();
     if (sh.abort) {
