@@ -670,6 +670,9 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
             const int rows = it.rows;
             const int col = group * HC + cl;                        // of the statistics
             const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+            float f[HC];
+#pragma unroll
+            for (int j = 0; j < HC; ++j) f[j] = __shfl_sync(0xFFFFFFFFu, inv, j);
             ok = lat::wait_warp(bar(sh.o_full), seg & 1u, sync);   // (the next vote ends it where this ran out)
             ptx::tc_fence_after();
             if (it.parts == 1) {
@@ -679,9 +682,6 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
                 uint32_t* out = reinterpret_cast<uint32_t*>(a.out) +
                                 (((it.row0 + group * HC + (odd ? 1 : 0)) * a.L + quarter * 32 + (lane & ~1)) >> 1);
                 const int last = rows - group * HC - (odd ? 1 : 0);   // this lane's rows j < last exist
-                float f[HC];
-#pragma unroll
-                for (int j = 0; j < HC; ++j) f[j] = __shfl_sync(0xFFFFFFFFu, inv, j);
 #pragma unroll 1
                 for (int p = 0; p < np; ++p, out += 64) {
                     uint32_t o[HC];
