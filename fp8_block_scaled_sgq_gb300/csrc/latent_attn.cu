@@ -17,13 +17,15 @@
 // of MMAs, of 40 cycles (NR = 16) to 49 (NR = 64, the operands' reads of shared
 // memory).  With 16 rows a tile's MMAs and softmax take less than its share of
 // HBM time, and HBM is the bound once a CTA is under way: 64 sequences of 130
-// to 16384 rows with 16 heads (200 MB) in 50 us, of which 30 are the bytes at
+// to 16384 rows with 16 heads (200 MB) in 49 us, of which 30 are the bytes at
 // the measured copy rate and 7 the joining kernel and its launch.  With 64
 // rows it is shared memory: reads by the MMAs and writes by TMA take 4470
 // cycles a tile at least.  Only the tile in use fits beside the queries, so
-// shared memory idles while softmax runs between the two products: 5540 cycles
-// a tile.  128 sequences of 1024 to 8192 rows with 128 heads: 171 us (538 MB);
-// one of 131071 rows: 73 us (151 MB); chunks: 392 us (692 TFLOP/s).
+// shared memory idles while softmax runs between the two products: 5250 cycles
+// a tile.  128 sequences of 1024 to 8192 rows with 128 heads: 164 us (538 MB);
+// one of 131071 rows: 69 us (151 MB); chunks: 373 us (728 TFLOP/s).  Between
+// items code runs that a CTA executes once an item, and it comes cold (a
+// hundred instructions take some 1000 cycles), so it is kept short.
 //
 // Layout.  A tile sits in shared memory once, as chunks of 128 rows x 64
 // columns with 128-byte swizzle: read K-major for S^T and, by the descriptor's
@@ -58,7 +60,7 @@ constexpr int kTile = 128;                    // cached rows a tile
 constexpr int kChunkBytes = kTile * 128;      // 64 columns of a tile
 constexpr int kMaxPairs = 5, kMaxRope = 2;
 constexpr int kLoaders = 3;                   // warps that issue loads: one alone keeps a third of this rate
-constexpr int kItemCost = 2;                  // tiles that an item's start and end cost (measured 3.5 to 5.4 us at 3 a tile)
+constexpr int kItemCost = 2;                  // tiles that an item's start and end cost (chunks, 128 heads: 1 377 us, 2 373, 3 387; 128 requests: 168.5, 164.7, 163.3)
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
 constexpr float kGrow = 8.0f;                 // powers of two a score may outgrow the reference by
 constexpr float kNone = -1.0e38f;             // reference of a row that has seen nothing
