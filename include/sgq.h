@@ -397,9 +397,9 @@ sgq_status sgq_latent_append(const void* q, int64_t q_stride_t, int64_t q_stride
  * page numbers of request b, table_width columns.  out: [T, H, L], lse: fp32
  * [T, H] or NULL, both contiguous.  q_starts: int32 [B + 1], rising, ending
  * at T.  L in {128, 256, 384, 512}; R % 8 == 0, 8 <= R <= 64; page % 16 == 0;
- * H <= 65535; scale > 0.  Cached rows a token sees, and rows of the same 128 that some
- * other token of its request sees, are finite; rows at kv_lens[b] and later
- * may hold anything.
+ * H <= 65535; scale > 0.  The cached rows of a request are finite, those
+ * that are newer than some of its query tokens included; rows at kv_lens[b]
+ * and later may hold anything.
  *
  * workspace: device memory of at least sgq_latent_attention_workspace bytes,
  * 16-byte aligned, that no other call uses until this one is done.  Nothing
