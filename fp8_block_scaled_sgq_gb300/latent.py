@@ -85,7 +85,8 @@ def rotary_table(max_pos: int, rot: int, base: float = 10000.0, factor: float = 
     (positions interpolated); with the trained length in ``original_max``,
     pairs that turn more than ``beta_fast`` times over it keep their frequency,
     pairs that turn less than ``beta_slow`` times are divided by ``factor``, and
-    those between are blended linearly in the pair's index.
+    those between are blended linearly in the pair's index (the two bounds
+    rounded outwards to whole pairs).
     ``attention_factor`` multiplies cosines and sines.  Angles are computed in
     64 bits, once, when the table is made.
     """
@@ -101,8 +102,11 @@ def rotary_table(max_pos: int, rot: int, base: float = 10000.0, factor: float = 
         if original_max > 0:
             def pair_of(turns):   # the pair that turns so many times over the trained length
                 return rot * math.log(original_max / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))
-            lo, hi = max(math.floor(pair_of(beta_fast)), 0), min(math.ceil(pair_of(beta_slow)), rot // 2 - 1)
-            keep = 1.0 - ((i - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
+            # The blend's end may lie past the last pair (all pairs turn more than beta_slow times over a long trained
+            # length) or before the first one (none does); its start is the first pair at the earliest.
+            lo, hi = max(math.floor(pair_of(beta_fast)), 0), math.ceil(pair_of(beta_slow))
+            if hi > 0:
+                keep = 1.0 - ((i - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
         freq = freq * keep + freq / factor * (1.0 - keep)
     angle = torch.arange(max_pos, dtype=torch.float64, device=device)[:, None] * freq
     return (torch.cat([angle.cos(), angle.sin()], dim=1) * attention_factor).float()

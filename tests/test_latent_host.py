@@ -1,0 +1,37 @@
+"""Latent attention's helpers without a GPU: rotary tables of long contexts."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import fp8_block_scaled_sgq_gb300 as sgq
+
+
+# ---------------------------------------------------------------- rotary tables of stretched contexts
+
+def table_by_parts(max_pos, rot, base, factor, trained, fast=32.0, slow=1.0):
+    """Pair i turns trained base^(-2i/rot) / (2 pi) times over the trained length.  The pairs at which that is `fast` and
+    `slow` (rounded outwards, the first one not below 0) bound the blend, linear in i."""
+    def pair_at(turns):
+        return rot / 2 * math.log(trained / (2 * math.pi * turns)) / math.log(base)
+    lo, hi = max(math.floor(pair_at(fast)), 0), math.ceil(pair_at(slow))
+    keep = [0.0 if i >= hi else 1.0 if i <= lo else (hi - i) / (hi - lo) for i in range(rot // 2)]
+    freq = [base ** (-2.0 * i / rot) * (k + (1 - k) / factor) for i, k in enumerate(keep)]
+    angle = np.arange(max_pos, dtype=np.float64)[:, None] * np.array(freq)
+    return np.concatenate([np.cos(angle), np.sin(angle)], axis=1), keep
+
+
+@pytest.mark.parametrize("rot,base,trained", [
+    (64, 10000.0, 1000), (64, 10000.0, 4096), (64, 10000.0, 65536), (64, 10000.0, 131072), (32, 10000.0, 1 << 20),
+    (128, 500000.0, 8192), (64, 10000.0, 100), (64, 10000.0, 5),
+])
+def test_table_by_parts_is_the_definition(rot, base, trained):
+    """From trained lengths over which every pair turns more often than `slow` (the blend ends past the last pair: 65536,
+    131072, 2^20) to one over which none does (5).  Both sides round an angle's 64-bit cosine to fp32 once: 2^-25 of 1,
+    and angles up to 2000 in 64 bits differ by less than 2^-40."""
+    want, keep = table_by_parts(2000, rot, base, 8.0, trained)
+    got = sgq.rotary_table(2000, rot, base=base, factor=8.0, original_max=trained, device="cpu").double().numpy()
+    assert np.abs(got - want).max() <= 2.0 ** -25 + 2.0 ** -40
+    if trained == 131072:
+        assert keep[28] == pytest.approx(0.538, abs=1e-3) and keep[31] == pytest.approx(0.308, abs=1e-3)
