@@ -8,10 +8,10 @@
 //     O^T [L, NR]         += C[:, :L]^T P^T over 128 tokens
 // Softmax keeps a reference m and a sum l for every row i: p = 2^(s - m)
 // with s in powers of two.  m follows the running maximum only when that has
-// grown by more than 2^8: p then stays below 2^8, every sum is a sum of
-// positive terms in fp32 with the same reference, and the accumulator in TMEM
-// is rescaled only on those steps.  P is rounded once, to the cache's type,
-// as the second product's operand; l sums the unrounded p.
+// grown by more than 2^kGrow (lat::Weights): every sum is a sum of positive
+// terms in fp32 with the same reference, and the accumulator in TMEM is
+// rescaled only on those steps.  P is rounded once, to the cache's type, as the
+// second product's operand; l sums the unrounded p.
 //
 // What bounds it.  A tile is 147 KB of cache (L + R = 576) and takes 68 steps
 // of MMAs, of 40 cycles (NR = 16) to 49 (NR = 64, the operands' reads of shared
@@ -62,7 +62,6 @@ constexpr int kMaxPairs = 5, kMaxRope = 2;
 constexpr int kLoaders = 3;                   // warps that issue loads: one alone keeps a third of this rate
 constexpr int kItemCost = 2;                  // tiles that an item's start and end cost (chunks, 128 heads: 1 377 us, 2 373, 3 387; 128 requests: 168.5, 164.7, 163.3)
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
-constexpr float kGrow = 8.0f;                 // powers of two a score may outgrow the reference by
 constexpr float kNone = -1.0e38f;             // reference of a row that has seen nothing
 
 template <int NR>
@@ -303,6 +302,7 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
     using C = Cfg<NR>;
     constexpr int HC = C::kHC;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+    constexpr float kLift = lat::Weights<T>::kLift, kMost = kLift + lat::Weights<T>::kGrow;   // powers of two of the weights
     extern __shared__ uint8_t raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     Shared& sh = *reinterpret_cast<Shared*>(smem + C::kOffMisc);
@@ -576,8 +576,8 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
                         if (token >= s.w) raw_s[j + 3] = __float_as_uint(-INFINITY);
                     }
                 }
-                // Weights with the references as they are; if some score is past its reference by
-                // more than 2^kGrow (or is the first one seen), all of the group move them first.
+                // Weights with the references as they are; if one is above 2^kMost (or the first one
+                // seen), all of the group move them first.
                 uint32_t packed[HC / 2];
                 float p[HC];
                 bool move = true;                                  // an item's first tile sets them
@@ -590,7 +590,7 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
                     }
 #pragma unroll
                     for (int j = 0; j < HC; ++j) p[j] = lat::ex2(p[j]);
-                    move = lat::named_any(id, 128, most > kGrow || !ok);
+                    move = lat::named_any(id, 128, most > kMost || !ok);
                 }
                 if (move) {
                     float top = kNone;                             // of column cl
@@ -605,7 +605,7 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
                     if (failed) break;
                     if (quarter == 0 && lane < HC) {
                         top = fmaxf(fmaxf(sh.top[group][0][cl], sh.top[group][1][cl]), fmaxf(sh.top[group][2][cl], sh.top[group][3][cl]));
-                        const float old = sh.ref[group][cl], to = top > old + kGrow ? top : old;
+                        const float old = sh.ref[group][cl], to = top > old + kMost ? top - kLift : old;
                         sh.ref[group][cl] = to;
                         sh.fade[group][cl] = lat::ex2(old - to);   // 0 where there was nothing before
                     }

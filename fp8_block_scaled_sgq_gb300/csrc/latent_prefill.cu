@@ -6,8 +6,9 @@
 //     O [128, N]  += P V     over 128 keys, P from TMEM (it overlays S)
 // Softmax keeps a reference m and a sum l a row: p = 2^(s - m), s in powers of
 // two.  m follows the running maximum only when that has grown by more than
-// 2^8, so O is rescaled on few steps; sums are fp32.  P is rounded once, to
-// the inputs' type, as the second product's operand; l sums the unrounded p.
+// 2^kGrow (lat::Weights), so O is rescaled on few steps; sums are fp32.  P is
+// rounded once, to the inputs' type, as the second product's operand; l sums
+// the unrounded p.
 //
 // What bounds it: the tensor cores.  A tile of N + R = 192, N = 128 takes 1280
 // cycles of MMAs at full rate; its exponentials take up to 1024 on the special
@@ -53,7 +54,6 @@ constexpr int kTile = 128;
 constexpr int kChunkBytes = kTile * 128;
 constexpr int kSlots = 8;
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
-constexpr float kGrow = 8.0f;   // powers of two the maximum may outgrow the reference by
 constexpr int kOffQ = kSlots * kChunkBytes;
 constexpr int kOffMisc = kOffQ + 6 * kChunkBytes;
 constexpr int kMisc = 2048;
@@ -172,6 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     latent_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                           const __grid_constant__ CUtensorMap tm_r, const __grid_constant__ CUtensorMap tm_v, const Args a) {
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+    constexpr float kLift = lat::Weights<T>::kLift, kMost = kLift + lat::Weights<T>::kGrow;   // powers of two of the weights
     // A tile's chunks follow one another in the ring: KC of keys (the rotated part last), then VC of
     // values.  Tile t's keys take the slots of what was loaded up to the values of tile t - kBackK,
     // its values those up to the keys of tile t - kBackV.
@@ -446,10 +447,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * a.scale2;
-                    const bool grow = top > ref + kGrow || (ref == -INFINITY && top > -INFINITY);
+                    const bool grow = top > ref + kMost || (ref == -INFINITY && top > -INFINITY);
                     if (__any_sync(0xFFFFFFFFu, grow)) {
-                        const float f = grow ? lat::ex2(ref - top) : 1.0f;
-                        if (grow) ref = top;
+                        const float to = top - kLift, f = grow ? lat::ex2(ref - to) : 1.0f;
+                        if (grow) ref = to;
                         l *= f;
                         if (t > 0) {
 #pragma unroll 1

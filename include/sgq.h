@@ -333,13 +333,14 @@ sgq_status sgq_fp8_scaled_mm(const void* Aq, const float* sa, int64_t sa_n, cons
  * types are SGQ_BF16 or SGQ_FP16 (`dtype`, one for all of a call's tensors);
  * sums, softmax statistics and rotations are fp32, rounded once on the way
  * out (and the softmax weights once, to `dtype`, as a matrix product's
- * operand).  Strides are in elements, the innermost one is 1; every address
- * and stride is a multiple of 16 bytes, i.e. 8 elements.  int64_t arrays on
- * the device hold positions and slots, int32_t ones lengths and page numbers;
- * they need natural alignment only.  Values on the device that point outside
- * their tensor (a position, a slot, a page, a length) are never followed:
- * they set the device status (sgq_device_status -> SGQ_ERR_INVALID_ARG) and
- * the outputs that they concern are undefined.
+ * operand; fp16 ones to full precision from 2^-23 of a row's largest weight on,
+ * smaller ones to 2^-34 of it).  Strides are in elements, the innermost one is
+ * 1; every address and stride is a multiple of 16 bytes, i.e. 8 elements.
+ * int64_t arrays on the device hold positions and slots, int32_t ones lengths
+ * and page numbers; they need natural alignment only.  Values on the device
+ * that point outside their tensor (a position, a slot, a page, a length) are
+ * never followed: they set the device status (sgq_device_status ->
+ * SGQ_ERR_INVALID_ARG) and the outputs that they concern are undefined.
  */
 #define SGQ_BF16 0
 #define SGQ_FP16 1

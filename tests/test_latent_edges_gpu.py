@@ -1,0 +1,106 @@
+"""Latent attention on the GPU where numbers or calls are at the edge, against its definition in 64 bits (latent_ref.py)."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import fp8_block_scaled_sgq_gb300 as sgq
+import latent_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+def normal(*shape, dtype, seed, std=1.0, mean=0.0):
+    g = torch.Generator("cpu").manual_seed(seed)
+    return (torch.randn(*shape, generator=g) * std + mean).to(dtype).cuda()
+
+
+def ints(values, dtype=torch.int32):
+    return torch.tensor(values, dtype=dtype, device="cuda")
+
+
+@pytest.fixture(autouse=True)
+def status_is_clean():
+    yield
+    assert sgq.sgq_device_status() == 0
+
+
+# ---------------------------------------------------------------- small weights behind a dominant key, fp16
+
+def check_small(got, lse, want, values):
+    """The rows' bound, and what fp16 cannot hold of weights below its normal range: they are rounded to a multiple of
+    2^-24 as operands that are 2^9 times what they are to the row's largest one, i.e. each is off by 2^-34 of it at
+    most, which moves a row by 2^-34 sum_j |v_j|."""
+    out, want_lse, mag, e = want
+    u = ref.UNIT[torch.float16]
+    tol = u * np.abs(out) + (u + 2 * e[:, None] + 2.0 ** -20) * mag + 2.0 ** -25 + 2.0 ** -34 * np.abs(values).sum(axis=0)
+    err = np.abs(ref.f64(got) - out)
+    assert (err <= tol).all(), f"{(err / tol).max()} times the bound"
+    assert (np.abs(ref.f64(lse) - want_lse) <= e + 2.0 ** -18 + 2.0 ** -21 * np.abs(want_lse)).all()
+
+
+def sink_rows(m, width, depth, at, seed):
+    """Values of mean 1/2, and in their first rotated element scores (in powers of two) `depth` or so below row `at`'s,
+    whose values are 0."""
+    rows = normal(m, width, dtype=torch.float16, seed=seed, mean=0.5)
+    rows[:, -64:] = 0
+    rows[:, -64] = normal(m, dtype=torch.float16, seed=seed + 1, std=0.25)
+    rows[at] = 0
+    rows[at, -64] = depth
+    return rows
+
+
+@pytest.mark.parametrize("at", [0, 9000, 19999])
+@pytest.mark.parametrize("depth", [12.0, 22.0, 26.0, 31.0])
+def test_absorbed_small_weights(depth, at):
+    """Many requests that share their pages, so that no row's keys are cut into parts."""
+    m, L, page, B = 20000, 128, 32, 304
+    rows = sink_rows(m, L + 64, depth, at, seed=41)
+    q = torch.zeros(B, 3, L + 64, dtype=torch.float16, device="cuda")
+    q[..., L] = 1
+    table = torch.arange(m // page, dtype=torch.int32, device="cuda").expand(B, -1).contiguous()
+    lse = torch.empty(B, 3, device="cuda")
+    out = sgq.latent_attention(q, rows.view(-1, page, L + 64), table, ints([m] * B), math.log(2.0), L, lse=lse)
+    assert torch.equal(out, out[:1, :1].expand_as(out)) and torch.equal(lse, lse[:1, :1].expand_as(lse))
+    r = ref.f64(rows)
+    want = ref.attend(ref.f64(q[0, :1]), r, r[:, :L], np.ones((1, m), dtype=bool), math.log(2.0))
+    check_small(out[0, :1], lse[0, :1], want, r[:, :L])
+
+
+@pytest.mark.parametrize("at", [0, 9000, 19999])
+@pytest.mark.parametrize("depth", [12.0, 22.0, 26.0, 31.0])
+def test_expanded_small_weights(depth, at):
+    m, N, n = 20000, 64, 130
+    rows = sink_rows(m, N + 64, depth, at, seed=43)
+    k = torch.zeros(m, 1, N, dtype=torch.float16, device="cuda")
+    q = torch.zeros(n, 1, N + 64, dtype=torch.float16, device="cuda")
+    q[..., N] = 1
+    lse = torch.empty(n, 1, device="cuda")
+    out = sgq.latent_prefill(q, k, rows[:, N:], rows[:, None, :N], ints([0, n]), ints([0, m]), math.log(2.0), causal=False,
+                             lse=lse)
+    assert torch.equal(out, out[:1].expand_as(out)) and torch.equal(lse, lse[:1].expand_as(lse))
+    r = ref.f64(rows)
+    want = ref.attend(ref.f64(q[0, :, N:]), r[:, N:], r[:, :N], np.ones((1, m), dtype=bool), math.log(2.0))
+    check_small(out[0], lse[0], want, r[:, :N])
+
+
+@pytest.mark.parametrize("step", [0.9, 3.9, 7.9, 12.0])
+def test_scores_that_rise_from_tile_to_tile(step):
+    """By less and by more than a reference follows at once: weights stay finite in fp16."""
+    m, L, page = 2000, 128, 16
+    rows = normal(m, L + 64, dtype=torch.float16, seed=45)
+    rows[:, L:] = 0
+    rows[:, L] = (torch.arange(m, device="cuda") // 128 * step).half()
+    q = torch.zeros(1, 5, L + 64, dtype=torch.float16, device="cuda")
+    q[..., L] = 1
+    lse = torch.empty(1, 5, device="cuda")
+    out = sgq.latent_attention(q, rows.view(-1, page, L + 64), torch.arange(m // page, dtype=torch.int32, device="cuda")[None],
+                               ints([m]), math.log(2.0), L, lse=lse)
+    r, seen = ref.f64(rows), np.ones((5, m), dtype=bool)
+    ref.check_rows(out[0], lse[0], *ref.attend(ref.f64(q[0]), r, r[:, :L], seen, math.log(2.0)), torch.float16)
+    k = torch.zeros(m, 1, L, dtype=torch.float16, device="cuda")
+    lse = torch.empty(5, 1, device="cuda")
+    out = sgq.latent_prefill(q[0, :, None], k, rows[:, L:], rows[:, None, :L], ints([0, 5]), ints([0, m]), math.log(2.0),
+                             causal=False, lse=lse)
+    ref.check_rows(out[:, 0], lse[:, 0], *ref.attend(ref.f64(q[0, :, L:]), r[:, L:], r[:, :L], seen, math.log(2.0)), torch.float16)
