@@ -671,7 +671,7 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
             const float total = (sh.sum[group][0][cl] + sh.sum[group][1][cl]) + (sh.sum[group][2][cl] + sh.sum[group][3][cl]);
             const int rows = it.rows;
             const int col = group * HC + cl;                        // of the statistics
-            const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+            const float inv = total == 0.0f ? 0.0f : 1.0f / total;   // (0: nothing seen; NaN stays NaN)
             float f[HC];
 #pragma unroll
             for (int j = 0; j < HC; ++j) f[j] = __shfl_sync(0xFFFFFFFFu, inv, j);
@@ -679,7 +679,7 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
             ptx::tc_fence_after();
             if (it.parts == 1) {
                 if (a.lse != nullptr && quarter == 0 && lane < HC && col < rows)
-                    a.lse[it.row0 + col] = total > 0.0f ? (mine_ref + log2f(total)) * kLn2 : -INFINITY;
+                    a.lse[it.row0 + col] = total == 0.0f ? -INFINITY : (mine_ref + log2f(total)) * kLn2;
                 const bool odd = (lane & 1) != 0;
                 uint32_t* out = reinterpret_cast<uint32_t*>(a.out) +
                                 (((it.row0 + group * HC + (odd ? 1 : 0)) * a.L + quarter * 32 + (lane & ~1)) >> 1);
@@ -828,13 +828,13 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const Args a,
         const int64_t row = int64_t(j.x) + r;
         if (few) {
             if (mine) {
-                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
                 uint2* out = reinterpret_cast<uint2*>(static_cast<T*>(a.out) + row * a.L) + lane;
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
                     if (q < nq)
                         out[q * 32] = make_uint2(Pair<T>::pack(o[q].x * inv, o[q].y * inv), Pair<T>::pack(o[q].z * inv, o[q].w * inv));
-                if (a.lse != nullptr && lane == 0) a.lse[row] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+                if (a.lse != nullptr && lane == 0) a.lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
             }
             continue;
         }
@@ -844,7 +844,7 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const Args a,
         l = 0.0f;
 #pragma unroll
         for (int w = 0; w < kJoinWarps; ++w) l += acc_l[w];
-        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         const int c = 2 * threadIdx.x;
         if (c < 128) {
             float x = 0.0f, y = 0.0f;
@@ -856,7 +856,7 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const Args a,
             }
             *reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + row * a.L + q0 * 128 + c) = Pair<T>::pack(x * inv, y * inv);
         }
-        if (a.lse != nullptr && threadIdx.x == 0 && q0 == 0) a.lse[row] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        if (a.lse != nullptr && threadIdx.x == 0 && q0 == 0) a.lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
         __syncthreads();
     }
 }

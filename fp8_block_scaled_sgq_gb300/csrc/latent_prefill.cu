@@ -507,9 +507,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ptx::tc_fence_after();
                 }
                 if (ok) {
-                    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+                    const float inv = l == 0.0f ? 0.0f : 1.0f / l;   // (0: nothing seen; NaN stays NaN)
                     const int64_t at = (int64_t(r.q0) + q) * a.H + it.head;
-                    if (a.lse != nullptr && q < r.n) a.lse[at] = l > 0.0f ? (ref + log2f(l)) * kLn2 : -INFINITY;
+                    if (a.lse != nullptr && q < r.n) a.lse[at] = l == 0.0f ? -INFINITY : (ref + log2f(l)) * kLn2;
                     uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + at * a.N);
                     const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
 #pragma unroll 1

@@ -391,7 +391,8 @@ sgq_status sgq_latent_append(const void* q, int64_t q_stride_t, int64_t q_stride
  *   out[t, h] = sum_j softmax_j(scale * q[t, h] . c_j) c_j[0 .. L)
  *
  * and lse[t, h] = log sum_j exp(scale * q[t, h] . c_j) (natural logarithm).
- * A query token without a row to see gets zeros, and lse -inf.
+ * A query token without a row to see gets zeros, and lse -inf; one whose
+ * scores hold NaN gets NaN, in lse too.
  *
  * q: [T, H, L + R], every (token, head) row q_stride_row after the one
  * before.  cache: as for sgq_latent_append.  page_table: int32, row b the
@@ -423,7 +424,8 @@ sgq_status sgq_latent_attention(const void* q, int64_t q_stride_row, int64_t T, 
  *                                        + q[i, h, N .. N + R) . k_rot[j])) v[j, h]
  *
  * over j <= m - n + i (causal = 1; n queries, m keys) or all j (causal = 0).
- * A query without a key to see gets zeros, and lse -inf.
+ * A query without a key to see gets zeros, and lse -inf; one whose scores
+ * hold NaN gets NaN, in lse too.
  *
  * q: [T, H, N + R]; k, v: [S, H, N]; k_rot: [S, R]; token (and head) strides,
  * none of them 0 where there is more than one token or head.

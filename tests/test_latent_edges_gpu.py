@@ -104,3 +104,48 @@ def test_scores_that_rise_from_tile_to_tile(step):
     out = sgq.latent_prefill(q[0, :, None], k, rows[:, L:], rows[:, None, :L], ints([0, 5]), ints([0, m]), math.log(2.0),
                              causal=False, lse=lse)
     ref.check_rows(out[:, 0], lse[:, 0], *ref.attend(ref.f64(q[0, :, L:]), r[:, L:], r[:, :L], seen, math.log(2.0)), torch.float16)
+
+
+# ---------------------------------------------------------------- rows whose scores hold NaN
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("lens", [[300, 0, 5], [70000, 0, 5], [3000, 0, 129] * 30])
+def test_nan_queries_are_not_empty_rows(lens, dtype):
+    """A query of NaN gives NaN and a NaN logarithm (an item's own row, and one that is joined from few and from many
+    parts); without a row to see it is empty like any other.  Its neighbours are what they are without it."""
+    L, page, H, B = 128, 64, 5, len(lens)
+    width = -(-max(lens) // page)
+    cache = normal(width, page, L + 64, dtype=dtype, seed=51)
+    table = torch.arange(width, dtype=torch.int32, device="cuda").expand(B, -1).contiguous()
+    q = normal(B, H, L + 64, dtype=dtype, seed=52)
+    bad = q.clone()
+    bad[:, 1] = float("nan")
+    bad[:, 3, 7] = float("nan")
+    lse, bad_lse = (torch.empty(B, H, device="cuda") for _ in range(2))
+    want = sgq.latent_attention(q, cache, table, ints(lens), 0.1, L, lse=lse)
+    got = sgq.latent_attention(bad, cache, table, ints(lens), 0.1, L, lse=bad_lse)
+    some = torch.tensor(lens, device="cuda") > 0
+    for h in range(H):
+        if h in (1, 3):
+            assert got[some, h].isnan().all() and bad_lse[some, h].isnan().all()
+            assert (got[~some, h] == 0).all() and bad_lse[~some, h].isneginf().all()
+        else:
+            assert torch.equal(got[:, h], want[:, h]) and torch.equal(bad_lse[:, h], lse[:, h])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_nan_queries_are_not_empty_rows_expanded(dtype):
+    T, H, starts, kv_starts = 300, 2, [0, 200, 300], [0, 150, 400]
+    up, kr = normal(400, H, 256, dtype=dtype, seed=53), normal(400, 64, dtype=dtype, seed=54)
+    q = normal(T, H, 192, dtype=dtype, seed=55)
+    bad = q.clone()
+    rows = [3, 49, 50, 170, 299]        # (of the first request, rows up to 49 see nothing)
+    bad[rows] = float("nan")
+    lse, bad_lse = (torch.empty(T, H, device="cuda") for _ in range(2))
+    args = (up[..., :128], kr, up[..., 128:], ints(starts), ints(kv_starts), 0.1)
+    want = sgq.latent_prefill(q, *args, lse=lse)
+    got = sgq.latent_prefill(bad, *args, lse=bad_lse)
+    assert got[rows[2:]].isnan().all() and bad_lse[rows[2:]].isnan().all()
+    assert (got[rows[:2]] == 0).all() and bad_lse[rows[:2]].isneginf().all()
+    rest = [t for t in range(T) if t not in rows]
+    assert torch.equal(got[rest], want[rest]) and torch.equal(bad_lse[rest], lse[rest])
