@@ -20,8 +20,8 @@ def _empty(shape, like, stream):
     import torch
     if stream is None:
         return torch.empty(shape, dtype=like.dtype, device=like.device)
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream)
+    if isinstance(stream, int):   # (0 is the default stream's handle; torch makes a new stream of ExternalStream(0))
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=like.dtype, device=like.device)
 

@@ -149,3 +149,28 @@ def test_nan_queries_are_not_empty_rows_expanded(dtype):
     assert (got[rows[:2]] == 0).all() and bad_lse[rows[:2]].isneginf().all()
     rest = [t for t in range(T) if t not in rows]
     assert torch.equal(got[rest], want[rest]) and torch.equal(bad_lse[rest], lse[rest])
+
+
+# ---------------------------------------------------------------- streams
+
+def test_outputs_belong_to_the_calls_stream(monkeypatch):
+    """What a helper allocates comes from the memory of the stream it launches on, the default stream's handle (0)
+    included: the handle of a user's current_stream()."""
+    kv, pos = normal(2, 192, dtype=torch.bfloat16, seed=1), ints([0, 1], torch.int64)
+    table, cache = sgq.rotary_table(4, 64), torch.zeros(2, 16, 192, dtype=torch.bfloat16, device="cuda")
+    q, pages, lens = normal(2, 3, 192, dtype=torch.bfloat16, seed=2), ints([[0], [1]]), ints([1, 1])
+    up, starts = normal(2, 3, 256, dtype=torch.bfloat16, seed=3), ints([0, 2])
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    empty, seen = torch.empty, []
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: seen.append(torch.cuda.current_stream().cuda_stream) or empty(*a, **k))
+    for stream, handle in ((None, 0), (0, 0), (torch.cuda.default_stream(), 0), (side, side.cuda_stream),
+                           (side.cuda_stream, side.cuda_stream)):
+        for call in (lambda: sgq.rotary(q, pos, table, 128, stream=stream),
+                     lambda: sgq.latent_append(q[..., 128:], kv[:, 128:], kv[:, :128], pos, pos, table, cache, stream=stream),
+                     lambda: sgq.latent_attention(q, cache, pages, lens, 0.1, 128, stream=stream),
+                     lambda: sgq.latent_prefill(q, up[..., :128], kv[:, 128:], up[..., 128:], starts, starts, 0.1, stream=stream)):
+            seen.clear()
+            call()
+            assert seen and all(s == handle for s in seen), (stream, seen)
+        torch.cuda.synchronize()
