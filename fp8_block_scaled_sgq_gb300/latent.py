@@ -204,8 +204,8 @@ def latent_attention(q, cache, page_table, kv_lens, scale: float, latent: int, q
     q [T, H, latent + R]; cache [pages, page, latent + R]; page_table int32 [B, width]; kv_lens int32 [B]: rows of each
     request, its query tokens' own rows last.  q_starts int32 [B + 1]: the requests' first query tokens (a chunk sees
     its own tokens causally); None: one token a request.  lse: fp32 [T, H] to receive the logarithm of the softmax
-    sums.  workspace: ``sgq_latent_attention_workspace`` bytes of this device's memory that no call running at the
-    same time uses; None: allocated here.
+    sums.  workspace: a contiguous tensor of ``sgq_latent_attention_workspace`` bytes that no call running at
+    the same time uses; None: allocated here.
     """
     import torch
     dt = _dtype(q, cache, out)
@@ -239,6 +239,8 @@ def latent_attention(q, cache, page_table, kv_lens, scale: float, latent: int, q
         nbytes = _workspace_bytes(T, H, latent)
         workspace = own = torch._C._cuda_cudaCachingAllocator_raw_alloc(nbytes, stream)
     else:
+        if not workspace.is_contiguous():
+            _fail("workspace: not contiguous")
         nbytes = workspace.numel() * workspace.element_size()
     try:
         binding.sgq_latent_attention(q, row, T, H, cache, pages, page, cp, cr, latent, W - latent, page_table,

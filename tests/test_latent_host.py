@@ -35,3 +35,34 @@ def test_table_by_parts_is_the_definition(rot, base, trained):
     assert np.abs(got - want).max() <= 2.0 ** -25 + 2.0 ** -40
     if trained == 131072:
         assert keep[28] == pytest.approx(0.538, abs=1e-3) and keep[31] == pytest.approx(0.308, abs=1e-3)
+
+
+# ---------------------------------------------------------------- what the helpers refuse before a launch
+
+@pytest.fixture
+def launches(monkeypatch):
+    """CPU tensors stand in for a GPU's; a call that reaches the library is recorded instead."""
+    calls = []
+    monkeypatch.setattr("fp8_block_scaled_sgq_gb300.latent._device", lambda *a: None)
+    monkeypatch.setattr("fp8_block_scaled_sgq_gb300.binding._stream", lambda s: 0)
+    for name in ("sgq_rotary", "sgq_latent_append", "sgq_latent_attention", "sgq_latent_prefill"):
+        monkeypatch.setattr(f"fp8_block_scaled_sgq_gb300.binding.{name}", lambda *a, n=name: calls.append((n, a)))
+    return calls
+
+
+def attention_args():
+    q, cache = torch.zeros(2, 16, 192, dtype=torch.bfloat16), torch.zeros(2, 16, 192, dtype=torch.bfloat16)
+    pages, lens = torch.zeros(2, 1, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    return q, cache, pages, lens, 0.1, 128
+
+
+def test_workspace_has_to_be_contiguous(launches):
+    """Elements that share memory, or lie apart, are no workspace of numel() elements."""
+    sgq.latent_attention(*attention_args(), workspace=torch.empty(1 << 20, dtype=torch.uint8))
+    sgq.latent_attention(*attention_args(), workspace=torch.empty(1 << 10, 1 << 8))
+    assert [a[-2] for _, a in launches] == [1 << 20, 1 << 20]
+    for bad in (torch.empty(1, dtype=torch.uint8).expand(1 << 20), torch.empty(1 << 20, dtype=torch.uint8)[::2],
+                torch.empty(1 << 10, 1 << 8).t()):
+        with pytest.raises(ValueError, match="workspace"):
+            sgq.latent_attention(*attention_args(), workspace=bad)
+    assert len(launches) == 2
