@@ -3,8 +3,8 @@
 These helpers check shapes, types and strides, allocate what they return (and
 the attention's workspace) on the stream of the call, and call the binding; the
 work is in ``libsgq.so`` (``include/sgq.h``, "Latent attention").  Tensors are
-bfloat16 or float16, one type for a call.  Wrong shapes, types or strides raise
-ValueError before anything is launched.
+bfloat16 or float16, one type for a call, on the current device.  Wrong shapes,
+types or strides raise ValueError before anything is launched.
 """
 from __future__ import annotations
 
@@ -62,13 +62,18 @@ def _index(name: str, t, dtype, n: int):
         _fail(f"{name}: expected {n} contiguous {dtype} entries, got {tuple(t.shape)} of {t.dtype}")
 
 
-def _device(x, *others):
+def _device(x, *others) -> int:
+    """The index of the tensors' device, which is the current one: stream, workspace and launch are its own."""
+    import torch
     if not x.is_cuda:
         _fail("the tensors are not on a CUDA device")
     at = x.get_device()
     for t in others:
         if t is not None and t.get_device() != at:
             _fail("the tensors are on different devices")
+    if at != torch.cuda.current_device():
+        _fail(f"the tensors are on device {at}, the current one is {torch.cuda.current_device()}")
+    return at
 
 
 def _contiguous(name: str, t, shape, dtype=None):
@@ -193,7 +198,8 @@ def latent_append(q_rot, k_rot, latent, positions, slots, table, cache, interlea
 
 
 @functools.lru_cache(maxsize=256)
-def _workspace_bytes(T: int, H: int, latent: int) -> int:
+def _workspace_bytes(T: int, H: int, latent: int, device: int) -> int:
+    """(of the current device, which is the last argument: sizes go by its number of SMs)"""
     return binding.sgq_latent_attention_workspace(T, H, latent)
 
 
@@ -225,7 +231,7 @@ def latent_attention(q, cache, page_table, kv_lens, scale: float, latent: int, q
         _index("q_starts", q_starts, torch.int32, B + 1)
     elif T != B:
         _fail(f"{T} query tokens for {B} requests, without q_starts")
-    _device(q, cache, page_table, kv_lens, q_starts, out, lse, workspace)
+    device = _device(q, cache, page_table, kv_lens, q_starts, out, lse, workspace)
     if out is None:
         out = _empty((T, H, latent), q, stream)
     else:
@@ -236,7 +242,7 @@ def latent_attention(q, cache, page_table, kv_lens, scale: float, latent: int, q
     if workspace is None:
         # Memory of torch's allocator without a tensor around it (a short call's 21 us of host time -> 19); it
         # belongs to the call's stream, and goes back to that stream's memory as soon as the call is queued.
-        nbytes = _workspace_bytes(T, H, latent)
+        nbytes = _workspace_bytes(T, H, latent, device)
         workspace = own = torch._C._cuda_cudaCachingAllocator_raw_alloc(nbytes, stream)
     else:
         if not workspace.is_contiguous():

@@ -66,3 +66,44 @@ def test_workspace_has_to_be_contiguous(launches):
         with pytest.raises(ValueError, match="workspace"):
             sgq.latent_attention(*attention_args(), workspace=bad)
     assert len(launches) == 2
+
+
+class OnDevice:
+    is_cuda = True
+
+    def __init__(self, index):
+        self.index = index
+
+    def get_device(self):
+        return self.index
+
+
+def test_tensors_of_another_device_than_the_current_one(monkeypatch):
+    """A call's stream, workspace and launch are the current device's."""
+    from fp8_block_scaled_sgq_gb300 import latent
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    latent._device(OnDevice(0), None, OnDevice(0))
+    with pytest.raises(ValueError, match="different devices"):
+        latent._device(OnDevice(0), OnDevice(1))
+    with pytest.raises(ValueError, match="current"):
+        latent._device(OnDevice(1), None, OnDevice(1))
+
+
+def test_workspace_size_is_a_devices(monkeypatch):
+    """Its size goes by the device's number of SMs: one that was asked for on another device is not taken."""
+    from fp8_block_scaled_sgq_gb300 import binding, latent
+    device = [0]
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: device[0])
+    monkeypatch.setattr(torch.cuda, "caching_allocator_alloc", lambda n, *a, **k: 16)
+    monkeypatch.setattr(torch.cuda, "caching_allocator_delete", lambda p: None)
+    monkeypatch.setattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", lambda n, *a: 16, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", lambda p: None, raising=False)
+    monkeypatch.setattr(binding, "sgq_latent_attention_workspace", lambda T, H, L: 1000 * (1 + device[0]))
+    monkeypatch.setattr(binding, "_stream", lambda s: 0)
+    monkeypatch.setattr(latent, "_device", lambda x, *a: device[0])
+    sizes = []
+    monkeypatch.setattr(binding, "sgq_latent_attention", lambda *a: sizes.append(a[-2]))
+    for device[0] in (0, 1, 0):
+        sgq.latent_attention(*attention_args())
+    assert sizes == [1000, 2000, 1000]
