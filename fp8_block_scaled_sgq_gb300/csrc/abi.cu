@@ -33,6 +33,11 @@ bool good_strides(std::initializer_list<int64_t> strides) {
         if (s < 0 || s % 8 != 0 || s > (int64_t(1) << 40)) return false;
     return true;
 }
+// Tokens and heads of the absorbed attention: fewer than 2^31 rows (tokens
+// first, so that the product does not wrap).
+bool good_rows(int64_t T, int64_t H) {
+    return T >= 0 && T < (int64_t(1) << 31) && H > 0 && H <= 65535 && T * H < (int64_t(1) << 31);
+}
 
 }  // namespace
 
@@ -63,6 +68,7 @@ using sgq::aligned16;
 using sgq::aligned_to;
 using sgq::good_dtype;
 using sgq::good_rotation;
+using sgq::good_rows;
 using sgq::good_strides;
 
 extern "C" {
@@ -281,7 +287,7 @@ sgq_status sgq_latent_append(const void* q, int64_t q_stride_t, int64_t q_stride
 }
 
 sgq_status sgq_latent_attention_workspace(int64_t T, int64_t H, int64_t L, int64_t* bytes) {
-    if (bytes == nullptr || T < 0 || H <= 0 || H > 65535 || L <= 0 || L % 128 != 0 || L > 512) return SGQ_ERR_INVALID_ARG;
+    if (bytes == nullptr || !good_rows(T, H) || L <= 0 || L % 128 != 0 || L > 512) return SGQ_ERR_INVALID_ARG;
     return sgq::latent_attention_workspace(T, H, L, bytes);
 }
 
@@ -290,13 +296,12 @@ sgq_status sgq_latent_attention(const void* q, int64_t q_stride_row, int64_t T, 
                                 int64_t L, int R, const int32_t* page_table, int64_t table_width, int64_t B,
                                 const int32_t* kv_lens, const int32_t* q_starts, float scale, int dtype, void* out,
                                 float* lse, void* workspace, int64_t workspace_bytes, sgq_stream_t stream) {
-    if (T < 0 || B < 0 || H <= 0 || H > 65535 || T * H >= (int64_t(1) << 31) || B >= (int64_t(1) << 31) || L <= 0 ||
-        L % 128 != 0 || L > 512 || R < 8 || R > 64 || R % 8 != 0 || !good_dtype(dtype) ||
+    if (!good_rows(T, H) || B < 0 || B >= (int64_t(1) << 31) || L <= 0 || L % 128 != 0 || L > 512 || R < 8 || R > 64 || R % 8 != 0 || !good_dtype(dtype) ||
         !good_strides({q_stride_row, cache_stride_page, cache_stride_row}) || !(std::isfinite(scale) && scale > 0.0f))
         return SGQ_ERR_INVALID_ARG;
     if (pages <= 0 || pages >= (int64_t(1) << 31) || page <= 0 || page % 16 != 0 || page >= (int64_t(1) << 31) ||
-        table_width < 0 || table_width * page > (int64_t(1) << 31) - 256 || q_stride_row < L + R ||
-        cache_stride_row < L + R || cache_stride_page < cache_stride_row * page)
+        table_width < 0 || table_width >= (int64_t(1) << 31) || table_width * page > (int64_t(1) << 31) - 256 ||
+        q_stride_row < L + R || cache_stride_row < L + R || cache_stride_page / page < cache_stride_row)
         return SGQ_ERR_INVALID_ARG;
     if (q_starts == nullptr && T != B) return SGQ_ERR_INVALID_ARG;
     if (T == 0) return SGQ_OK;

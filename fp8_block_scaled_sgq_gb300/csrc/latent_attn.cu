@@ -974,8 +974,9 @@ sgq_status launch_latent_attention(const LatentArgs& x, cudaStream_t st) {
     // (more head blocks than that are a walk of one CTA: teams would leave CTAs over)
     a.team = a.hb <= 4 ? a.hb : 1;
     a.scale2 = x.scale * kLog2e;
-    // No more CTAs than the tables could hold tiles.
-    const int64_t most = (x.T + x.B) * (a.hb / a.team) * std::max<int64_t>(1, (x.table_width * x.page + kTile - 1) / kTile);
+    // No more CTAs than the tables could hold tiles (a request's counted up to the largest grid).
+    const int64_t tiles = std::min<int64_t>(kMaxGrid, std::max<int64_t>(1, (x.table_width * x.page + kTile - 1) / kTile));
+    const int64_t most = (x.T + x.B) * (a.hb / a.team) * tiles;
     const int sms = std::min(di.sm_count, kMaxGrid) / a.team * a.team;
     const int grid = static_cast<int>(std::min<int64_t>(sms, most * a.team));
     a.inv_teams = grid == a.team ? 0 : ~uint64_t(0) / static_cast<uint64_t>(grid / a.team) + 1;

@@ -399,7 +399,7 @@ sgq_status sgq_latent_append(const void* q, int64_t q_stride_t, int64_t q_stride
  * page numbers of request b, table_width columns.  out: [T, H, L], lse: fp32
  * [T, H] or NULL, both contiguous.  q_starts: int32 [B + 1], rising, ending
  * at T.  L in {128, 256, 384, 512}; R % 8 == 0, 8 <= R <= 64; page % 16 == 0;
- * H <= 65535; scale > 0.  The cached rows of a request are finite, those
+ * H <= 65535; T H < 2^31; table_width page <= 2^31 - 256; scale > 0.  The cached rows of a request are finite, those
  * that are newer than some of its query tokens included; rows at kv_lens[b]
  * and later may hold anything.
  *

@@ -6,6 +6,13 @@ import pytest
 import torch
 
 import fp8_block_scaled_sgq_gb300 as sgq
+from fp8_block_scaled_sgq_gb300 import binding, build
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return binding.load_library()
 
 
 # ---------------------------------------------------------------- rotary tables of stretched contexts
@@ -92,7 +99,7 @@ def test_tensors_of_another_device_than_the_current_one(monkeypatch):
 
 def test_workspace_size_is_a_devices(monkeypatch):
     """Its size goes by the device's number of SMs: one that was asked for on another device is not taken."""
-    from fp8_block_scaled_sgq_gb300 import binding, latent
+    from fp8_block_scaled_sgq_gb300 import latent
     device = [0]
     monkeypatch.setattr(torch.cuda, "current_device", lambda: device[0])
     monkeypatch.setattr(torch.cuda, "caching_allocator_alloc", lambda n, *a, **k: 16)
@@ -107,3 +114,19 @@ def test_workspace_size_is_a_devices(monkeypatch):
     for device[0] in (0, 1, 0):
         sgq.latent_attention(*attention_args())
     assert sizes == [1000, 2000, 1000]
+
+
+# ---------------------------------------------------------------- the C ABI's bounds
+
+def test_products_of_sizes_that_wrap(lib):
+    """Token and table counts whose products with heads and pages pass 2^63 (and would wrap to small numbers)."""
+    import ctypes
+    from test_latent import ATT, INV, caller
+    f = caller(lib.sgq_latent_attention, list(ATT), ATT)
+    fake = 0x70000
+    for bad in (dict(T=1 << 48, H=65535, starts=fake), dict(T=(1 << 62) + 4, starts=fake), dict(T=1 << 31, H=1, starts=fake),
+                dict(page=1 << 30, width=1, cr=1 << 40, cp=1 << 40), dict(width=1 << 60), dict(width=1 << 62, page=32, cp=18432), dict(width=1 << 31, page=16)):
+        assert f(**bad) == INV, bad
+    n = ctypes.c_int64()
+    for bad in ((1 << 48, 65535, 512), ((1 << 62) + 4, 16, 512), (1 << 27, 16, 512)):
+        assert lib.sgq_latent_attention_workspace(*bad, ctypes.byref(n)) == INV, bad
