@@ -4,7 +4,8 @@ Each function has the name and argument order of the C call in
 ``include/sgq.h``.  Tensor arguments may be torch CUDA tensors (their
 ``data_ptr()`` is passed) or raw integer device addresses; ``stream`` may be a
 ``torch.cuda.Stream``, a raw ``cudaStream_t`` integer, or None for the current
-torch stream.  A non-OK status raises :class:`SgqError`.  There is no
+torch stream.  A non-OK status raises :class:`SgqError`; that of a wrong
+argument is a ValueError, too (:class:`SgqArgumentError`).  There is no
 fallback: if the library is missing or fails to load, every call raises.
 """
 from __future__ import annotations
@@ -67,6 +68,10 @@ class SgqError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
         super().__init__(f"{what} failed: {status_string(status)} ({status})")
+
+
+class SgqArgumentError(SgqError, ValueError):
+    """The status of a wrong argument (SGQ_ERR_INVALID_ARG, SGQ_ERR_MISALIGNED): nothing was launched."""
 
 
 _lock = threading.Lock()
@@ -155,7 +160,7 @@ def _stream(s):
 
 def _check(rc: int, what: str):
     if rc != SGQ_OK:
-        raise SgqError(rc, what)
+        raise (SgqArgumentError if rc in (SGQ_ERR_INVALID_ARG, SGQ_ERR_MISALIGNED) else SgqError)(rc, what)
 
 
 def status_string(status: int) -> str:

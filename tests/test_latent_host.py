@@ -130,3 +130,38 @@ def test_products_of_sizes_that_wrap(lib):
     n = ctypes.c_int64()
     for bad in ((1 << 48, 65535, 512), ((1 << 62) + 4, 16, 512), (1 << 27, 16, 512)):
         assert lib.sgq_latent_attention_workspace(*bad, ctypes.byref(n)) == INV, bad
+
+
+def test_what_the_library_refuses_is_a_value_error(lib, monkeypatch):
+    """Shapes, strides and addresses that only the C ABI looks at: ValueError (and SgqError with its status)."""
+    monkeypatch.setattr("fp8_block_scaled_sgq_gb300.latent._device", lambda *a: 0)
+    monkeypatch.setattr(binding, "_stream", lambda s: 0)
+    bf16, ws = torch.bfloat16, torch.empty(1 << 10, dtype=torch.uint8)
+    pages, lens = torch.zeros(2, 1, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+
+    def attention(page=16, width=192, latent=128, gap=0, skip=0):
+        q = torch.zeros(2 * 16 * (width + gap) + 8, dtype=bf16)[skip:skip + 2 * 16 * (width + gap)].view(2, 16, width + gap)
+        return lambda: sgq.latent_attention(q[..., :width], torch.zeros(2, page, width, dtype=bf16), pages, lens, 0.1, latent,
+                                            workspace=ws)
+
+    def prefill(plain, rot):
+        k = torch.zeros(2, 3, plain, dtype=bf16)
+        return lambda: sgq.latent_prefill(torch.zeros(2, 3, plain + rot, dtype=bf16), k, torch.zeros(2, rot, dtype=bf16), k,
+                                          lens, lens, 0.1)
+
+    def rotate(rot, offset=0, interleaved=True):
+        return lambda: sgq.rotary(torch.zeros(2, 3, 64, dtype=bf16), torch.zeros(2, dtype=torch.int64), torch.zeros(4, rot),
+                                  offset, interleaved)
+
+    kv, pos = torch.zeros(2, 128 + 64 + 4, dtype=bf16), torch.zeros(2, dtype=torch.int64)
+    refused = [(attention(page=24), 1), (attention(width=164, latent=100), 1), (attention(width=200), 1), (attention(gap=4), 1),
+               (attention(skip=4), 3), (prefill(96, 64), 1), (prefill(128, 72), 1), (rotate(12), 1), (rotate(24, 0, False), 1),
+               (rotate(32, 40), 1),
+               (lambda: sgq.latent_append(None, kv[:, 128:192], kv[:, :128], pos, pos, torch.zeros(4, 64),
+                                          torch.zeros(2, 16, 192, dtype=bf16)), 1)]
+    for call, status in refused:
+        with pytest.raises(ValueError) as e:
+            call()
+        assert isinstance(e.value, sgq.SgqError) and e.value.status == status
+    # what is not about arguments stays an SgqError alone
+    assert not isinstance(binding.SgqError(binding.SGQ_ERR_CUDA, "call"), ValueError)
