@@ -165,3 +165,38 @@ def test_what_the_library_refuses_is_a_value_error(lib, monkeypatch):
         assert isinstance(e.value, sgq.SgqError) and e.value.status == status
     # what is not about arguments stays an SgqError alone
     assert not isinstance(binding.SgqError(binding.SGQ_ERR_CUDA, "call"), ValueError)
+
+
+def test_inputs_that_require_a_gradient(launches):
+    """No operator records one: refused while gradients are recorded, instead of an output that has lost it."""
+    bf16 = torch.bfloat16
+    pos, table, starts = torch.zeros(2, dtype=torch.int64), torch.zeros(4, 64), torch.zeros(3, dtype=torch.int32)
+
+    def zeros(*shape):
+        return torch.zeros(*shape, dtype=bf16)
+
+    def rotary(x):
+        sgq.rotary(x, pos, table)
+
+    def append(q, k, latent):
+        sgq.latent_append(q, k, latent, pos, pos, table, zeros(2, 16, 192))
+
+    def attention(q, cache):
+        sgq.latent_attention(q, cache, *attention_args()[2:], workspace=torch.empty(16))
+
+    def prefill(q, k, k_rot, v):
+        sgq.latent_prefill(q, k, k_rot, v, starts, starts, 0.1)
+
+    for call, args in ((rotary, [zeros(2, 3, 64)]), (append, [zeros(2, 3, 64), zeros(2, 64), zeros(2, 128)]),
+                       (attention, [zeros(2, 16, 192), zeros(2, 16, 192)]),
+                       (prefill, [zeros(2, 3, 192), zeros(2, 3, 128), zeros(2, 64), zeros(2, 3, 128)])):
+        for i in range(len(args)):
+            graded = [t.requires_grad_() if j == i else t for j, t in enumerate(t.detach() for t in args)]
+            with pytest.raises(ValueError, match="gradient"):
+                call(*graded)
+            assert not launches
+            with torch.no_grad():
+                call(*graded)
+            call(*[t.detach() for t in graded])
+            assert len(launches) == 2
+            launches.clear()
