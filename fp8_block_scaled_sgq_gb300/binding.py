@@ -151,8 +151,12 @@ def _ptr(t):
 def _stream(s):
     if s is None:
         import torch
-        # the handle of torch.cuda.current_stream(), without the Stream object around it (2.9 -> 0.3 us)
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        # the handle of torch.cuda.current_stream(), without the Stream object around it (2.9 -> 0.3 us) where
+        # this torch has the names for it, which are not public
+        try:
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        except AttributeError:
+            return torch.cuda.current_stream().cuda_stream
     if isinstance(s, int):
         return s
     return s.cuda_stream

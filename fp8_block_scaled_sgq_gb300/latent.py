@@ -253,10 +253,10 @@ def latent_attention(q, cache, page_table, kv_lens, scale: float, latent: int, q
         _contiguous("lse", lse, (T, H), torch.float32)
     stream, own = binding._stream(stream), None
     if workspace is None:
-        # Memory of torch's allocator without a tensor around it (a short call's 21 us of host time -> 19); it
-        # belongs to the call's stream, and goes back to that stream's memory as soon as the call is queued.
+        # Memory of torch's allocator without a tensor around it; it belongs to the call's stream, and goes back to
+        # that stream's memory as soon as the call is queued.
         nbytes = _workspace_bytes(T, H, latent, device)
-        workspace = own = torch._C._cuda_cudaCachingAllocator_raw_alloc(nbytes, stream)
+        workspace = own = torch.cuda.caching_allocator_alloc(nbytes, device, stream)
     else:
         if not workspace.is_contiguous():
             _fail("workspace: not contiguous")
@@ -266,7 +266,7 @@ def latent_attention(q, cache, page_table, kv_lens, scale: float, latent: int, q
                                      table_width, B, kv_lens, q_starts, scale, dt, out, lse, workspace, nbytes, stream)
     finally:
         if own is not None:
-            torch._C._cuda_cudaCachingAllocator_raw_delete(own)
+            torch.cuda.caching_allocator_delete(own)
     return out
 
 

@@ -89,7 +89,6 @@ def test_tensors_of_another_device_than_the_current_one(monkeypatch):
     """A call's stream, workspace and launch are the current device's."""
     from fp8_block_scaled_sgq_gb300 import latent
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
     latent._device(OnDevice(0), None, OnDevice(0))
     with pytest.raises(ValueError, match="different devices"):
         latent._device(OnDevice(0), OnDevice(1))
@@ -97,15 +96,22 @@ def test_tensors_of_another_device_than_the_current_one(monkeypatch):
         latent._device(OnDevice(1), None, OnDevice(1))
 
 
-def test_workspace_size_is_a_devices(monkeypatch):
+@pytest.fixture
+def sizes_asked_anew():
+    """No workspace size of this test is kept for others, and none of theirs for this one."""
+    from fp8_block_scaled_sgq_gb300 import latent
+    latent._workspace_bytes.cache_clear()
+    yield
+    latent._workspace_bytes.cache_clear()
+
+
+def test_workspace_size_is_a_devices(monkeypatch, sizes_asked_anew):
     """Its size goes by the device's number of SMs: one that was asked for on another device is not taken."""
     from fp8_block_scaled_sgq_gb300 import latent
     device = [0]
     monkeypatch.setattr(torch.cuda, "current_device", lambda: device[0])
     monkeypatch.setattr(torch.cuda, "caching_allocator_alloc", lambda n, *a, **k: 16)
     monkeypatch.setattr(torch.cuda, "caching_allocator_delete", lambda p: None)
-    monkeypatch.setattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", lambda n, *a: 16, raising=False)
-    monkeypatch.setattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", lambda p: None, raising=False)
     monkeypatch.setattr(binding, "sgq_latent_attention_workspace", lambda T, H, L: 1000 * (1 + device[0]))
     monkeypatch.setattr(binding, "_stream", lambda s: 0)
     monkeypatch.setattr(latent, "_device", lambda x, *a: device[0])
@@ -200,3 +206,23 @@ def test_inputs_that_require_a_gradient(launches):
             call(*[t.detach() for t in graded])
             assert len(launches) == 2
             launches.clear()
+
+
+# ---------------------------------------------------------------- torch's public interface
+
+def test_public_names_of_torch_do(monkeypatch, sizes_asked_anew):
+    """The current stream and the workspace's memory, where torch has no names but its public ones."""
+    for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice", "_cuda_cudaCachingAllocator_raw_alloc",
+                 "_cuda_cudaCachingAllocator_raw_delete"):
+        monkeypatch.delattr(torch._C, name, raising=False)
+    stream = type("Stream", (), {"cuda_stream": 7})()
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: stream)
+    assert binding._stream(None) == 7 and binding._stream(stream) == 7 and binding._stream(5) == 5
+    held, calls = [], []
+    monkeypatch.setattr(torch.cuda, "caching_allocator_alloc", lambda n, device, stream: held.append((n, device, stream)) or 64)
+    monkeypatch.setattr(torch.cuda, "caching_allocator_delete", lambda p: held.remove((512, 0, 7)) if p == 64 else None)
+    monkeypatch.setattr("fp8_block_scaled_sgq_gb300.latent._device", lambda *a: 0)
+    monkeypatch.setattr(binding, "sgq_latent_attention_workspace", lambda *a: 512)
+    monkeypatch.setattr(binding, "sgq_latent_attention", lambda *a: calls.append((list(held), a[-3:])))
+    sgq.latent_attention(*attention_args())
+    assert calls == [([(512, 0, 7)], (64, 512, 7))] and held == []
