@@ -4,8 +4,9 @@
 // angle, pair i of a head's rotated part becomes
 //     (a, b) -> (a c - b s, b c + a s)        inverse: s -> -s
 // where pair i is elements (2i, 2i + 1) (interleaved) or (i, i + R/2) (half).
-// The inverse is the transpose of the rotation, i.e. its gradient.  The
-// arithmetic is fp32 with one rounding on the way out.
+// The inverse is the transpose, i.e. the gradient (and the way back where the
+// table's pairs have length 1).  The arithmetic is fp32 with one rounding on the
+// way out.
 //
 // Both kernels are bound by HBM: every element is read and written once, and
 // the table's rows (4 R bytes a token) are small beside a token's heads.  A

@@ -139,7 +139,8 @@ def rotary(x, positions, table, offset: int = 0, interleaved: bool = True, inver
     """x [T, H, D] with elements [offset, offset + rot) of every head rotated by its token's position.
 
     positions: int64 [T]; table: ``rotary_table``.  interleaved: pairs (2i, 2i + 1), else (i, i + rot/2).
-    inverse: rotate back, which is also the gradient.  out may be x (in place); returns out.
+    inverse: the transpose, i.e. the gradient; it rotates back where the table's ``attention_factor`` is 1 (else x comes
+    back times its square).  out may be x (in place); returns out.
     """
     import torch
     _no_gradient(x)

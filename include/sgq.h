@@ -351,8 +351,9 @@ sgq_status sgq_fp8_scaled_mm(const void* Aq, const float* sa, int64_t sa_n, cons
  * the R/2 cosines and then the R/2 sines of position p's angles (any base and
  * any long-context scaling are the table's).  Pair i, (a, b) -> (a cos - b
  * sin, b cos + a sin), is elements 2i, 2i + 1 (interleaved = 1) or i, i + R/2
- * (interleaved = 0).  inverse = 1 rotates back: the transpose, i.e. the
- * gradient.
+ * (interleaved = 0).  inverse = 1 takes -sin: the transpose, i.e. the gradient,
+ * and the way back where the table's pairs have length 1 (a table scaled by f
+ * gives f^2 x after both).
  *
  * x, y: [T, H, D] with token and head strides; y == x (and equal strides)
  * rotates in place, otherwise they do not overlap.  pos: int64 [T].

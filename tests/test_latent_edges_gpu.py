@@ -174,3 +174,23 @@ def test_outputs_belong_to_the_calls_stream(monkeypatch):
             call()
             assert seen and all(s == handle for s in seen), (stream, seen)
         torch.cuda.synchronize()
+
+
+# ---------------------------------------------------------------- rotation by a scaled table
+
+@pytest.mark.parametrize("interleaved", [True, False])
+def test_inverse_is_the_transpose_of_a_scaled_table(interleaved):
+    """With an attention factor f the inverse stays the gradient (<w, rotary(x)> = <rotary(w, inverse), x>), and both
+    together are f^2 x.  fp16: each of the two rounds once, 2^-11 of what is of order |x| f and |x| f^2."""
+    table = sgq.rotary_table(300, 32, factor=4.0, original_max=100, attention_factor=1.5)
+    pos = ints([0, 17, 255, 299], torch.int64)
+    x, w = (normal(4, 3, 32, dtype=torch.float16, seed=s) for s in (61, 62))
+    p, t = pos.cpu().numpy(), ref.f64(table)
+    back = sgq.rotary(w, pos, table, 0, interleaved, inverse=True)
+    ref.check_rotation(back, *ref.rotate(ref.f64(w), p, t, 0, interleaved, True), torch.float16)
+    forth = ref.rotate(ref.f64(x), p, t, 0, interleaved)[0]
+    transposed = ref.rotate(ref.f64(w), p, t, 0, interleaved, True)[0]
+    assert abs((ref.f64(w) * forth).sum() - (transposed * ref.f64(x)).sum()) < 1e-9
+    both = sgq.rotary(sgq.rotary(x, pos, table, 0, interleaved), pos, table, 0, interleaved, inverse=True)
+    size = np.abs(ref.f64(x)).max() * 1.5 ** 2 * 2 ** 0.5
+    assert np.abs(ref.f64(both) - 2.25 * ref.f64(x)).max() <= 2 * 2.0 ** -11 * size * 2 ** 0.5
