@@ -25,7 +25,9 @@ namespace {
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
 
-sgq_status get_encoder() {
+}  // namespace
+
+sgq_status get_encoder(TensorMapEncoder* out) {
     std::call_once(g_encode_once, [] {
         void* fn = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -34,8 +36,11 @@ sgq_status get_encoder() {
             q == cudaDriverEntryPointSuccess)
             g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     });
+    if (out) *out = g_encode;
     return g_encode ? SGQ_OK : SGQ_ERR_CUDA;
 }
+
+namespace {
 
 // 2-D map over a [rows, K] uint8 matrix, box = 128 K-bytes x box_rows rows,
 // 128-byte swizzle (the UMMA K-major SW128 layout).
@@ -484,7 +489,7 @@ int dual_mode(int64_t M, int64_t N, int64_t K, int blk_k, uint32_t flags, const 
 sgq_status launch(const void* Aq, const float* As, const void* Wq, const float* Ws, void* D, int64_t M,
                   int64_t N, int64_t K, int blk_n, int blk_k, uint32_t flags, bool noalloc, const Fuse* fuse,
                   cudaStream_t st, const Chan* chan = nullptr) {
-    if (get_encoder() != SGQ_OK) return SGQ_ERR_CUDA;
+    if (get_encoder(nullptr) != SGQ_OK) return SGQ_ERR_CUDA;
     DeviceInfo di;
     sgq_status rc = device_info(&di);
     if (rc != SGQ_OK) return rc;
@@ -659,7 +664,7 @@ sgq_status launch_ue8m0(const void* Aq, const uint8_t* Ae, const void* Wq, const
                                        void* D, int64_t M, int64_t N, int64_t K, int blk_n, int blk_k,
                                        uint32_t flags, cudaStream_t st) {
     if (M == 0) return SGQ_OK;
-    if (get_encoder() != SGQ_OK) return SGQ_ERR_CUDA;
+    if (get_encoder(nullptr) != SGQ_OK) return SGQ_ERR_CUDA;
     DeviceInfo di;
     sgq_status rc = device_info(&di);
     if (rc != SGQ_OK) return rc;

@@ -42,7 +42,6 @@
 // kernel joins in order: the result does not depend on timing.
 #include <cuda.h>
 #include <cuda_runtime.h>
-#include <cudaTypedefs.h>
 
 #include <algorithm>
 #include <type_traits>
@@ -95,7 +94,7 @@ struct Args {
     uint32_t* status;
     int64_t T, B, pages, width, c_page, c_row;   // strides in bytes
     uint32_t box_bytes;                          // a box's span, fetched ahead into L2 (0: not)
-    int H, L, R, page, box;
+    int H, L, page, box;
     int tpn, hb;         // tokens a block, head blocks a token (one of them is 1)
     uint64_t inv_teams;  // 2^64 / teams, rounded up
     int team;            // CTAs that walk over the same tiles, a head block each: hb, or 1
@@ -863,18 +862,6 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const Args a,
 
 // ---------------------------------------------------------------- host
 
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    }();
-    return fn;
-}
-
 // Rows (token, head) of a block: as many as a request has on average, up to 64.
 int row_block(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
@@ -944,7 +931,10 @@ sgq_status launch_latent_attention(const LatentArgs& x, cudaStream_t st) {
     DeviceInfo di;
     sgq_status rc = device_info(&di);
     if (rc != SGQ_OK) return rc;
-    if (di.cc_major != 10 || encoder() == nullptr) return SGQ_ERR_UNSUPPORTED;
+    if (di.cc_major != 10) return SGQ_ERR_UNSUPPORTED;
+    gemm::TensorMapEncoder encode;
+    rc = gemm::get_encoder(&encode);
+    if (rc != SGQ_OK) return rc;
     Args a{};
     rc = gemm::status_word(&a.status);
     if (rc != SGQ_OK) return rc;
@@ -963,7 +953,6 @@ sgq_status launch_latent_attention(const LatentArgs& x, cudaStream_t st) {
     a.width = x.table_width;
     a.H = x.H;
     a.L = x.L;
-    a.R = x.R;
     a.page = x.page;
     a.box = std::min(x.page & -x.page, kTile);   // rows of a box: whole boxes in a page and in a tile
     // (rows that lie apart, as those of a layer between others, are not: what is between them is not wanted)
@@ -993,7 +982,7 @@ sgq_status launch_latent_attention(const LatentArgs& x, cudaStream_t st) {
         const cuuint64_t dims[3] = {W, static_cast<cuuint64_t>(x.page), static_cast<cuuint64_t>(x.pages)};
         const cuuint64_t strides[2] = {static_cast<cuuint64_t>(x.c_row) * 2, static_cast<cuuint64_t>(x.c_page) * 2};
         const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(a.box), 1};
-        if (encoder()(&tm_cache, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(x.cache), dims, strides, box, ones,
+        if (encode(&tm_cache, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(x.cache), dims, strides, box, ones,
                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return SGQ_ERR_CUDA;
@@ -1002,7 +991,7 @@ sgq_status launch_latent_attention(const LatentArgs& x, cudaStream_t st) {
         const cuuint64_t dims[2] = {W, static_cast<cuuint64_t>(x.T * x.H)};
         const cuuint64_t strides[1] = {static_cast<cuuint64_t>(x.q_row) * 2};
         const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(NR)};
-        if (encoder()(&tm_q, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(x.q), dims, strides, box, ones,
+        if (encode(&tm_q, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(x.q), dims, strides, box, ones,
                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return SGQ_ERR_CUDA;

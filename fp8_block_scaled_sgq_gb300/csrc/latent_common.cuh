@@ -1,5 +1,5 @@
 // Shared by the latent-attention kernels (latent_rope.cu, latent_attn.cu,
-// latent_prefill.cu): the two element types and the checks of host arguments.
+// latent_prefill.cu): the two element types and the range of softmax weights.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

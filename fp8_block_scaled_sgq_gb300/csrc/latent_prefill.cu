@@ -35,7 +35,6 @@
 // us; taking over items 469; asking late 453; the order of the items 429.
 #include <cuda.h>
 #include <cuda_runtime.h>
-#include <cudaTypedefs.h>
 
 #include <algorithm>
 #include <type_traits>
@@ -67,7 +66,7 @@ struct Args {
     float* lse;
     uint32_t* status;
     int64_t T, S, B;
-    int H, N, R, causal, span_size;
+    int H, N, causal, span_size;
     float scale2;
 };
 
@@ -570,38 +569,26 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---------------------------------------------------------------- host
 
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    }();
-    return fn;
-}
-
 // [rows, heads, width] as boxes of 64 columns x 128 rows of one head.
-sgq_status head_map(CUtensorMap* m, const void* p, int64_t width, int64_t heads, int64_t rows, int64_t s_head,
+sgq_status head_map(gemm::TensorMapEncoder encode, CUtensorMap* m, const void* p, int64_t width, int64_t heads, int64_t rows, int64_t s_head,
                     int64_t s_row) {
     if (heads == 1) s_head = width;   // (a dimension of one entry has no stride that counts)
     if (rows == 1) s_row = width;
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(s_head) * 2, static_cast<cuuint64_t>(s_row) * 2};
     const cuuint32_t box[3] = {64, 1, kTile}, ones[3] = {1, 1, 1};
-    return encoder()(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(p), dims, strides, box, ones,
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(p), dims, strides, box, ones,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? SGQ_OK
                : SGQ_ERR_CUDA;
 }
-sgq_status row_map(CUtensorMap* m, const void* p, int64_t width, int64_t rows, int64_t s_row) {
+sgq_status row_map(gemm::TensorMapEncoder encode, CUtensorMap* m, const void* p, int64_t width, int64_t rows, int64_t s_row) {
     if (rows == 1) s_row = width;
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(s_row) * 2};
     const cuuint32_t box[2] = {64, kTile}, ones[2] = {1, 1};
-    return encoder()(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(p), dims, strides, box, ones,
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(p), dims, strides, box, ones,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? SGQ_OK
@@ -639,7 +626,10 @@ sgq_status launch_latent_prefill(const PrefillArgs& x, cudaStream_t st) {
     DeviceInfo di;
     sgq_status rc = device_info(&di);
     if (rc != SGQ_OK) return rc;
-    if (di.cc_major != 10 || encoder() == nullptr) return SGQ_ERR_UNSUPPORTED;
+    if (di.cc_major != 10) return SGQ_ERR_UNSUPPORTED;
+    gemm::TensorMapEncoder encode;
+    rc = gemm::get_encoder(&encode);
+    if (rc != SGQ_OK) return rc;
     Args a{};
     rc = gemm::status_word(&a.status);
     if (rc != SGQ_OK) return rc;
@@ -652,7 +642,6 @@ sgq_status launch_latent_prefill(const PrefillArgs& x, cudaStream_t st) {
     a.B = x.B;
     a.H = x.H;
     a.N = x.N;
-    a.R = x.R;
     a.causal = x.causal;
     a.scale2 = x.scale * kLog2e;
     a.span_size = static_cast<int>((x.B + kSpans - 1) / kSpans);
@@ -662,10 +651,10 @@ sgq_status launch_latent_prefill(const PrefillArgs& x, cudaStream_t st) {
     // (without keys nothing is loaded through the maps of keys and values: any address does)
     const bool none = x.S == 0;
     const int64_t W = x.N + x.R, S = none ? 1 : x.S;
-    if (head_map(&tm[0], x.q, W, x.H, x.T, x.q_h, x.q_t) != SGQ_OK ||
-        head_map(&tm[1], none ? x.q : x.k, x.N, x.H, S, none ? x.q_h : x.k_h, none ? x.q_t : x.k_t) != SGQ_OK ||
-        row_map(&tm[2], none ? x.q : x.k_rot, x.R, S, none ? x.q_t : x.kr_t) != SGQ_OK ||
-        head_map(&tm[3], none ? x.q : x.v, x.N, x.H, S, none ? x.q_h : x.v_h, none ? x.q_t : x.v_t) != SGQ_OK)
+    if (head_map(encode, &tm[0], x.q, W, x.H, x.T, x.q_h, x.q_t) != SGQ_OK ||
+        head_map(encode, &tm[1], none ? x.q : x.k, x.N, x.H, S, none ? x.q_h : x.k_h, none ? x.q_t : x.k_t) != SGQ_OK ||
+        row_map(encode, &tm[2], none ? x.q : x.k_rot, x.R, S, none ? x.q_t : x.kr_t) != SGQ_OK ||
+        head_map(encode, &tm[3], none ? x.q : x.v, x.N, x.H, S, none ? x.q_h : x.v_h, none ? x.q_t : x.v_t) != SGQ_OK)
         return SGQ_ERR_CUDA;
     if (x.N == 128)
         return x.dtype == SGQ_BF16 ? run<__nv_bfloat16, 2>(tm, a, blocks, st) : run<__half, 2>(tm, a, blocks, st);

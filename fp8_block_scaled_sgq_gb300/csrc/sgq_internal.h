@@ -1,7 +1,9 @@
 // Internal host-side interface between the C-ABI layer and the kernel files.
 #pragma once
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 #include "../../include/sgq.h"
 
 namespace sgq {
@@ -68,7 +70,6 @@ struct LatentArgs {
     void* out;
     float* lse;                // or null
     void* workspace;
-    uint32_t* status;
     int64_t q_row, T, B, pages, c_page, c_row, table_width;
     int H, L, R, page, dtype;
     float scale;
@@ -81,7 +82,6 @@ struct PrefillArgs {
     const int32_t *q_starts, *kv_starts;
     void* out;
     float* lse;                // or null
-    uint32_t* status;
     int64_t q_t, q_h, k_t, k_h, kr_t, v_t, v_h, T, S, B;
     int H, N, R, causal, dtype;
     float scale;
@@ -99,6 +99,9 @@ uint64_t allocated_bytes();
 // could not be expressed as UE8M0).
 namespace gemm {
 sgq_status status_word(uint32_t** out);
+// The driver's tensor-map encoder, looked up once a process (out may be null).
+using TensorMapEncoder = PFN_cuTensorMapEncodeTiled_v12000;
+sgq_status get_encoder(TensorMapEncoder* out);
 }
 constexpr uint32_t kStatusBadValue = 2u;
 // Reads and clears the device status word of the current device (after a sync).
