@@ -493,7 +493,7 @@ sgq_status launch(const void* Aq, const float* As, const void* Wq, const float* 
     DeviceInfo di;
     sgq_status rc = device_info(&di);
     if (rc != SGQ_OK) return rc;
-    if (di.cc_major != 10 || di.cc_minor != 3) return SGQ_ERR_UNSUPPORTED;
+    if (!built_for(di)) return SGQ_ERR_UNSUPPORTED;
     // The allocation-free entry point plans within its fixed array: split
     // counts whose partials or counters would not fit are skipped, so such a
     // shape runs with fewer K splits (or, at mid M, on the 128 x 256 tiles
@@ -668,7 +668,7 @@ sgq_status launch_ue8m0(const void* Aq, const uint8_t* Ae, const void* Wq, const
     DeviceInfo di;
     sgq_status rc = device_info(&di);
     if (rc != SGQ_OK) return rc;
-    if (di.cc_major != 10 || di.cc_minor != 3) return SGQ_ERR_UNSUPPORTED;
+    if (!built_for(di)) return SGQ_ERR_UNSUPPORTED;
     flags |= SGQ_GEMM_SCALES_POW2;
     const Plan p = make_plan(M, N, K, blk_k, di.sm_count, (flags & (SGQ_GEMM_ISSUE_ALT | SGQ_GEMM_ISSUE_SINGLE)) != 0);
     const int mode = dual_mode(M, N, K, blk_k, flags, p, di.sm_count, kWsLimit, true);

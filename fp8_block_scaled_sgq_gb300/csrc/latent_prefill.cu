@@ -626,7 +626,7 @@ sgq_status launch_latent_prefill(const PrefillArgs& x, cudaStream_t st) {
     DeviceInfo di;
     sgq_status rc = device_info(&di);
     if (rc != SGQ_OK) return rc;
-    if (di.cc_major != 10) return SGQ_ERR_UNSUPPORTED;
+    if (!built_for(di)) return SGQ_ERR_UNSUPPORTED;
     gemm::TensorMapEncoder encode;
     rc = gemm::get_encoder(&encode);
     if (rc != SGQ_OK) return rc;

@@ -15,6 +15,8 @@ struct DeviceInfo {
     int cc_major = 0, cc_minor = 0;
 };
 sgq_status device_info(DeviceInfo* out);
+// Whether the kernels, compiled for sm_103a alone, run on such a device.
+inline bool built_for(const DeviceInfo& d) { return d.cc_major == 10 && d.cc_minor == 3; }
 
 // Count of kernel launches made by the library (for benchmarks).
 void note_launch(int n = 1);

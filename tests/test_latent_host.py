@@ -226,3 +226,48 @@ def test_public_names_of_torch_do(monkeypatch, sizes_asked_anew):
     monkeypatch.setattr(binding, "sgq_latent_attention", lambda *a: calls.append((list(held), a[-3:])))
     sgq.latent_attention(*attention_args())
     assert calls == [([(512, 0, 7)], (64, 512, 7))] and held == []
+
+
+# ---------------------------------------------------------------- other devices
+
+STUBS = r"""
+// What latent_attn.cu and latent_prefill.cu need of the library's other files, on a device of the given capability.
+#include "sgq_internal.h"
+namespace sgq {
+static DeviceInfo g_device;
+sgq_status device_info(DeviceInfo* out) { *out = g_device; return SGQ_OK; }
+void note_launch(int) {}
+namespace gemm {
+sgq_status status_word(uint32_t** out) { *out = nullptr; return SGQ_ERR_CUDA; }
+sgq_status get_encoder(TensorMapEncoder* out) { *out = nullptr; return SGQ_ERR_CUDA; }
+}
+}
+extern "C" int attention_on(int major, int minor) {
+    sgq::g_device.cc_major = major; sgq::g_device.cc_minor = minor; sgq::g_device.sm_count = 152;
+    return sgq::launch_latent_attention(sgq::LatentArgs{}, nullptr);
+}
+extern "C" int prefill_on(int major, int minor) {
+    sgq::g_device.cc_major = major; sgq::g_device.cc_minor = minor; sgq::g_device.sm_count = 152;
+    return sgq::launch_latent_prefill(sgq::PrefillArgs{}, nullptr);
+}
+"""
+
+
+def test_devices_that_the_library_is_not_built_for(lib, tmp_path):
+    """Compiled for 10.3 alone: any other device is SGQ_ERR_UNSUPPORTED, before anything is asked of the driver (where
+    the stubs return SGQ_ERR_CUDA)."""
+    import ctypes
+    import os
+    import subprocess
+    objects = [os.path.join(build.BUILD, f) for f in ("latent_attn.o", "latent_prefill.o")]
+    if not all(map(os.path.exists, objects)):
+        build.build(force=True)
+    src, so = tmp_path / "stubs.cpp", tmp_path / "stubs.so"
+    src.write_text(STUBS)
+    subprocess.run([build._nvcc(), *build.ARCH, "-std=c++17", "-Xcompiler", "-fPIC", "-I", build.CSRC, "-shared", str(src),
+                    *objects, "-o", str(so)], check=True)
+    stubs = ctypes.CDLL(str(so))
+    for f in (stubs.attention_on, stubs.prefill_on):
+        for major, minor in ((10, 0), (10, 1), (9, 0), (12, 0), (11, 3)):
+            assert f(major, minor) == binding.SGQ_ERR_UNSUPPORTED, (major, minor)
+        assert f(10, 3) == binding.SGQ_ERR_CUDA
