@@ -33,6 +33,7 @@ SGQ_GEMM_SCALES_POW2 = 16
 
 SGQ_BF16 = 0
 SGQ_FP16 = 1
+SGQ_LATENT_TEST_TIMEOUT = 256
 
 # Symbols declared in include/sgq.h (checked by the tests).
 EXPORTS = (

@@ -296,7 +296,10 @@ sgq_status sgq_latent_attention(const void* q, int64_t q_stride_row, int64_t T, 
                                 int64_t L, int R, const int32_t* page_table, int64_t table_width, int64_t B,
                                 const int32_t* kv_lens, const int32_t* q_starts, float scale, int dtype, void* out,
                                 float* lse, void* workspace, int64_t workspace_bytes, sgq_stream_t stream) {
-    if (!good_rows(T, H) || B < 0 || B >= (int64_t(1) << 31) || L <= 0 || L % 128 != 0 || L > 512 || R < 8 || R > 64 || R % 8 != 0 || !good_dtype(dtype) ||
+    const bool stall = dtype == (SGQ_BF16 | SGQ_LATENT_TEST_TIMEOUT);
+    if (stall) dtype = SGQ_BF16;
+    if (!good_rows(T, H) || B < 0 || B >= (int64_t(1) << 31) || L <= 0 || L % 128 != 0 || L > 512 || R < 8 || R > 64 ||
+        R % 8 != 0 || !good_dtype(dtype) ||
         !good_strides({q_stride_row, cache_stride_page, cache_stride_row}) || !(std::isfinite(scale) && scale > 0.0f))
         return SGQ_ERR_INVALID_ARG;
     if (pages <= 0 || pages >= (int64_t(1) << 31) || page <= 0 || page % 16 != 0 || page >= (int64_t(1) << 31) ||
@@ -318,7 +321,8 @@ sgq_status sgq_latent_attention(const void* q, int64_t q_stride_row, int64_t T, 
     a.q = q; a.cache = cache; a.page_table = page_table; a.kv_lens = kv_lens; a.q_starts = q_starts; a.out = out;
     a.lse = lse; a.workspace = workspace; a.q_row = q_stride_row; a.T = T; a.B = B; a.pages = pages;
     a.c_page = cache_stride_page; a.c_row = cache_stride_row; a.table_width = table_width;
-    a.H = static_cast<int>(H); a.L = static_cast<int>(L); a.R = R; a.page = static_cast<int>(page); a.dtype = dtype;
+    a.H = static_cast<int>(H); a.L = static_cast<int>(L); a.R = R; a.page = static_cast<int>(page);
+    a.dtype = dtype; a.stall = stall;
     a.scale = scale;
     return sgq::launch_latent_attention(a, reinterpret_cast<cudaStream_t>(stream));
 }
@@ -328,6 +332,8 @@ sgq_status sgq_latent_prefill(const void* q, int64_t q_stride_t, int64_t q_strid
                               const void* v, int64_t v_stride_t, int64_t v_stride_h, int64_t S, int64_t H, int64_t N,
                               int R, const int32_t* q_starts, const int32_t* kv_starts, int64_t B, float scale,
                               int causal, int dtype, void* out, float* lse, sgq_stream_t stream) {
+    const bool stall = dtype == (SGQ_BF16 | SGQ_LATENT_TEST_TIMEOUT);
+    if (stall) dtype = SGQ_BF16;
     if (T < 0 || S < 0 || B < 0 || H <= 0 || H > 65535 || T >= (int64_t(1) << 31) || S >= (int64_t(1) << 31) ||
         B >= (int64_t(1) << 31) || (N != 64 && N != 128) || R < 8 || R > 64 || R % 8 != 0 || !good_dtype(dtype) ||
         !good_strides({q_stride_t, q_stride_h, k_stride_t, k_stride_h, kr_stride, v_stride_t, v_stride_h}) ||
@@ -346,7 +352,8 @@ sgq_status sgq_latent_prefill(const void* q, int64_t q_stride_t, int64_t q_strid
     a.q = q; a.k = k; a.k_rot = k_rot; a.v = v; a.q_starts = q_starts; a.kv_starts = kv_starts; a.out = out; a.lse = lse;
     a.q_t = q_stride_t; a.q_h = q_stride_h; a.k_t = k_stride_t; a.k_h = k_stride_h; a.kr_t = kr_stride;
     a.v_t = v_stride_t; a.v_h = v_stride_h; a.T = T; a.S = S; a.B = B;
-    a.H = static_cast<int>(H); a.N = static_cast<int>(N); a.R = R; a.causal = causal; a.dtype = dtype;
+    a.H = static_cast<int>(H); a.N = static_cast<int>(N); a.R = R; a.causal = causal;
+    a.dtype = dtype; a.stall = stall;
     a.scale = scale;
     return sgq::launch_latent_prefill(a, reinterpret_cast<cudaStream_t>(stream));
 }

@@ -294,7 +294,8 @@ __device__ __forceinline__ float lane_sums(float (&v)[N]) {
     return v[0];
 }
 
-template <typename T, int NR>
+// kStall: testing; CTA 0 never loads the first pair of its second tile, and waits give up early.
+template <typename T, int NR, bool kStall>
 __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
     latent_attention_kernel(const __grid_constant__ CUtensorMap tm_cache, const __grid_constant__ CUtensorMap tm_q,
                             const Args a) {
@@ -306,7 +307,7 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     Shared& sh = *reinterpret_cast<Shared*>(smem + C::kOffMisc);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const lat::Sync sync{&sh.abort, a.status};
+    const lat::Sync<kStall ? lat::kTestTimeoutClocks : lat::kTimeoutClocks> sync{&sh.abort, a.status};
     auto bar = [](uint64_t& b) { return ptx::smem_u32(&b); };
     const uint32_t s_pairs = ptx::smem_u32(smem), s_rope = s_pairs + C::kOffRope, s_q = s_pairs + C::kOffQ;
 
@@ -412,6 +413,7 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
                     const uint32_t slot = pair % C::kPairs, full = bar(sh.full[slot]);
                     ok = lat::wait_warp(bar(sh.empty[slot]), ((pair / C::kPairs) & 1u) ^ 1u, sync);
                     if (!ok) break;
+                    if (kStall && blockIdx.x == 0 && pair == static_cast<uint32_t>(np)) continue;
                     if (lane == 0) ptx::mbar_arrive_expect_tx(full, boxes * a.box * 256);
                     __syncwarp();
                     if (lane < boxes) {
@@ -877,10 +879,10 @@ Sizes workspace_of(int64_t grid, int64_t NR, int64_t L) {
     return s;
 }
 
-template <typename T, int NR>
+template <typename T, int NR, bool kStall = false>
 sgq_status run(const CUtensorMap& tm_cache, const CUtensorMap& tm_q, const Args& a, int grid, int join_grid,
                cudaStream_t st) {
-    auto kern = latent_attention_kernel<T, NR>;
+    auto kern = latent_attention_kernel<T, NR, kStall>;
     static bool configured[64] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SGQ_ERR_CUDA;
@@ -909,12 +911,12 @@ sgq_status run(const CUtensorMap& tm_cache, const CUtensorMap& tm_q, const Args&
     note_launch();
     return SGQ_OK;
 }
-template <typename T>
+template <typename T, bool kStall = false>
 sgq_status run_rows(int NR, const CUtensorMap& tm_cache, const CUtensorMap& tm_q, const Args& a, int grid,
                     int join_grid, cudaStream_t st) {
-    if (NR == 16) return run<T, 16>(tm_cache, tm_q, a, grid, join_grid, st);
-    if (NR == 32) return run<T, 32>(tm_cache, tm_q, a, grid, join_grid, st);
-    return run<T, 64>(tm_cache, tm_q, a, grid, join_grid, st);
+    if (NR == 16) return run<T, 16, kStall>(tm_cache, tm_q, a, grid, join_grid, st);
+    if (NR == 32) return run<T, 32, kStall>(tm_cache, tm_q, a, grid, join_grid, st);
+    return run<T, 64, kStall>(tm_cache, tm_q, a, grid, join_grid, st);
 }
 
 }  // namespace
@@ -997,6 +999,7 @@ sgq_status launch_latent_attention(const LatentArgs& x, cudaStream_t st) {
             return SGQ_ERR_CUDA;
     }
     const int join_grid = di.sm_count * 8;   // (a row's loads wait for one another: 4 an SM 171.6 us where 8 take 170.4, 2 take 177)
+    if (x.stall) return run_rows<__nv_bfloat16, true>(NR, tm_cache, tm_q, a, grid, join_grid, st);
     return x.dtype == SGQ_BF16 ? run_rows<__nv_bfloat16>(NR, tm_cache, tm_q, a, grid, join_grid, st)
                                : run_rows<__half>(NR, tm_cache, tm_q, a, grid, join_grid, st);
 }

@@ -165,8 +165,9 @@ __device__ __forceinline__ Item find_item(const Args& a, const Shared& sh, int i
     return it;
 }
 
-// VC: chunks of 64 columns of the values (N / 64).
-template <typename T, int VC>
+// VC: chunks of 64 columns of the values (N / 64).  kStall: testing; CTA 0 never loads the keys of its second tile,
+// and waits give up early.
+template <typename T, int VC, bool kStall>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                           const __grid_constant__ CUtensorMap tm_r, const __grid_constant__ CUtensorMap tm_v, const Args a) {
@@ -183,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     Shared& sh = *reinterpret_cast<Shared*>(smem + kOffMisc);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const lat::Sync sync{&sh.abort, a.status};
+    const lat::Sync<kStall ? lat::kTestTimeoutClocks : lat::kTimeoutClocks> sync{&sh.abort, a.status};
     auto bar = [](uint64_t& b) { return ptx::smem_u32(&b); };
     const uint32_t s_ring = ptx::smem_u32(smem), s_q = s_ring + kOffQ;
 
@@ -292,6 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t full = bar(sh.k_full[kt & 3]);
                 if (kt >= kBackK) ok = lat::wait_warp(bar(sh.k_empty[back & 3]), (back >> 2) & 1, sync);
                 if (!ok) break;
+                if (kStall && blockIdx.x == 0 && kt == 1) continue;
                 if (lane == 0) {
                     ptx::mbar_arrive_expect_tx(full, KC * kChunkBytes);
                     lat::tma_load_3d(s_ring + (n % kSlots) * kChunkBytes, &tm_k, 0, it.head, row, full);
@@ -595,9 +597,9 @@ sgq_status row_map(gemm::TensorMapEncoder encode, CUtensorMap* m, const void* p,
                : SGQ_ERR_CUDA;
 }
 
-template <typename T, int VC>
+template <typename T, int VC, bool kStall = false>
 sgq_status run(const CUtensorMap (&tm)[4], const Args& a, int64_t grid, cudaStream_t st) {
-    auto kern = latent_prefill_kernel<T, VC>;
+    auto kern = latent_prefill_kernel<T, VC, kStall>;
     static bool configured[64] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SGQ_ERR_CUDA;
@@ -656,6 +658,7 @@ sgq_status launch_latent_prefill(const PrefillArgs& x, cudaStream_t st) {
         row_map(encode, &tm[2], none ? x.q : x.k_rot, x.R, S, none ? x.q_t : x.kr_t) != SGQ_OK ||
         head_map(encode, &tm[3], none ? x.q : x.v, x.N, x.H, S, none ? x.q_h : x.v_h, none ? x.q_t : x.v_t) != SGQ_OK)
         return SGQ_ERR_CUDA;
+    if (x.stall) return x.N == 128 ? run<__nv_bfloat16, 2, true>(tm, a, blocks, st) : run<__nv_bfloat16, 1, true>(tm, a, blocks, st);
     if (x.N == 128)
         return x.dtype == SGQ_BF16 ? run<__nv_bfloat16, 2>(tm, a, blocks, st) : run<__half, 2>(tm, a, blocks, st);
     return x.dtype == SGQ_BF16 ? run<__nv_bfloat16, 1>(tm, a, blocks, st) : run<__half, 1>(tm, a, blocks, st);

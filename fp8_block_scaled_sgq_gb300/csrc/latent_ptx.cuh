@@ -180,7 +180,9 @@ __device__ __forceinline__ bool named_any(int id, int threads, bool x) {
 // device status; every other wait of the CTA then gives up as well.
 constexpr uint32_t kStatusTimeout = 1u;
 constexpr long long kTimeoutClocks = 4000000000ll;    // about 2 s
+constexpr long long kTestTimeoutClocks = 1ll << 21;   // about 1 ms (SGQ_LATENT_TEST_TIMEOUT)
 constexpr long long kAbortPollClocks = 2000000ll;
+template <long long kLimit>
 struct Sync {
     volatile uint32_t* abort_flag;
     uint32_t* status;
@@ -188,13 +190,14 @@ struct Sync {
 // The whole warp waits for a phase; false: gave up.  All lanes poll together:
 // a warp whose lane 0 went through a polling loop alone stayed split in two
 // afterwards, and its MMA issue slowed down three to four times.
-static __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, const Sync& s) {
+template <long long kLimit>
+static __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, const Sync<kLimit>& s) {
     const long long t0 = clock64();
     for (uint32_t spins = 1;; ++spins) {
         if (__all_sync(0xFFFFFFFFu, ptx::mbar_try_wait(bar, parity))) return true;
         if ((spins & 63u) == 0) {
             const long long dt = clock64() - t0;
-            if (__any_sync(0xFFFFFFFFu, dt > kTimeoutClocks)) {
+            if (__any_sync(0xFFFFFFFFu, dt > kLimit)) {
                 *s.abort_flag = 1u;
                 if ((threadIdx.x & 31) == 0) atomicOr(s.status, kStatusTimeout);
                 __syncwarp();
@@ -204,7 +207,8 @@ static __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, con
         }
     }
 }
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const Sync& s) {
+template <long long kLimit>
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const Sync<kLimit>& s) {
     if (__all_sync(0xFFFFFFFFu, ptx::mbar_try_wait(bar, parity))) return true;
     return wait_slow(bar, parity, s);
 }

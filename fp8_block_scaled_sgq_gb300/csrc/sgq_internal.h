@@ -73,7 +73,7 @@ struct LatentArgs {
     float* lse;                // or null
     void* workspace;
     int64_t q_row, T, B, pages, c_page, c_row, table_width;
-    int H, L, R, page, dtype;
+    int H, L, R, page, dtype, stall;
     float scale;
 };
 sgq_status latent_attention_workspace(int64_t T, int64_t H, int64_t L, int64_t* bytes);
@@ -85,7 +85,7 @@ struct PrefillArgs {
     void* out;
     float* lse;                // or null
     int64_t q_t, q_h, k_t, k_h, kr_t, v_t, v_h, T, S, B;
-    int H, N, R, causal, dtype;
+    int H, N, R, causal, dtype, stall;
     float scale;
 };
 sgq_status launch_latent_prefill(const PrefillArgs& a, cudaStream_t stream);

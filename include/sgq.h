@@ -344,6 +344,13 @@ sgq_status sgq_fp8_scaled_mm(const void* Aq, const float* sa, int64_t sa_n, cons
  */
 #define SGQ_BF16 0
 #define SGQ_FP16 1
+/* Testing only, or-ed to SGQ_BF16 for sgq_latent_attention and
+ * sgq_latent_prefill: the first CTA never loads part of its second tile of 128
+ * rows (keys), so its bounded waits run out, after about 1 ms instead of about
+ * 2 s.  The kernel lets its copies and tensor-core operations land, frees its
+ * tensor memory and returns; sgq_device_status reports SGQ_ERR_TIMEOUT and the
+ * outputs are undefined.  The stream stays usable. */
+#define SGQ_LATENT_TEST_TIMEOUT 256
 
 /*
  * Rotary positions: y = x with elements [offset, offset + R) of every head

@@ -194,3 +194,47 @@ def test_inverse_is_the_transpose_of_a_scaled_table(interleaved):
     both = sgq.rotary(sgq.rotary(x, pos, table, 0, interleaved), pos, table, 0, interleaved, inverse=True)
     size = np.abs(ref.f64(x)).max() * 1.5 ** 2 * 2 ** 0.5
     assert np.abs(ref.f64(both) - 2.25 * ref.f64(x)).max() <= 2 * 2.0 ** -11 * size * 2 ** 0.5
+
+
+# ---------------------------------------------------------------- waits that run out
+
+@pytest.mark.parametrize("L,H,B,m", [(512, 16, 1, 128 * 400), (128, 16, 3, 128 * 300), (512, 20, 200, 640), (512, 128, 200, 640)])
+def test_absorbed_wait_runs_out_and_the_stream_recovers(L, H, B, m):
+    """With SGQ_LATENT_TEST_TIMEOUT the first CTA never loads part of its second tile: the kernel returns on its own, the
+    status says so once, and the next call on the stream gives what the one before gave (every CTA's run has more than
+    one tile: a long request, some, and many short ones, in the three row blocks)."""
+    from fp8_block_scaled_sgq_gb300 import binding
+    page, R = 64, 64
+    cache = normal(m // page, page, L + R, dtype=torch.bfloat16, seed=71)
+    table = torch.arange(m // page, dtype=torch.int32, device="cuda").expand(B, -1).contiguous()
+    q, lens = normal(B, H, L + R, dtype=torch.bfloat16, seed=72), ints([m] * B)
+    want = sgq.latent_attention(q, cache, table, lens, 0.05, L)
+    ws = torch.empty(sgq.sgq_latent_attention_workspace(B, H, L), dtype=torch.uint8, device="cuda")
+    out = torch.empty_like(want)
+    binding.sgq_latent_attention(q, L + R, B, H, cache, m // page, page, page * (L + R), L + R, L, R, table, m // page, B, lens,
+                                 None, 0.05, binding.SGQ_BF16 | binding.SGQ_LATENT_TEST_TIMEOUT, out, None, ws, ws.numel())
+    assert sgq.sgq_device_status() == binding.SGQ_ERR_TIMEOUT
+    assert sgq.sgq_device_status() == binding.SGQ_OK
+    for _ in range(2):
+        assert torch.equal(sgq.latent_attention(q, cache, table, lens, 0.05, L), want)
+    assert sgq.sgq_device_status() == binding.SGQ_OK
+
+
+@pytest.mark.parametrize("N", [64, 128])
+@pytest.mark.parametrize("T,H", [(300, 1), (1000, 3), (2000, 64)])
+def test_expanded_wait_runs_out_and_the_stream_recovers(T, H, N):
+    """The same for the expanded form: one item a CTA, and items that CTAs take over."""
+    from fp8_block_scaled_sgq_gb300 import binding
+    R = 64
+    up, kr = normal(T, H, 2 * N, dtype=torch.bfloat16, seed=73), normal(T, R, dtype=torch.bfloat16, seed=74)
+    q, starts = normal(T, H, N + R, dtype=torch.bfloat16, seed=75), ints([0, T])
+    k, v = up[..., :N], up[..., N:]
+    want = sgq.latent_prefill(q, k, kr, v, starts, starts, 0.1)
+    out = torch.empty_like(want)
+    binding.sgq_latent_prefill(q, H * (N + R), N + R, T, k, H * 2 * N, 2 * N, kr, R, v, H * 2 * N, 2 * N, T, H, N, R, starts, starts,
+                               1, 0.1, True, binding.SGQ_BF16 | binding.SGQ_LATENT_TEST_TIMEOUT, out, None)
+    assert sgq.sgq_device_status() == binding.SGQ_ERR_TIMEOUT
+    assert sgq.sgq_device_status() == binding.SGQ_OK
+    for _ in range(2):
+        assert torch.equal(sgq.latent_prefill(q, k, kr, v, starts, starts, 0.1), want)
+    assert sgq.sgq_device_status() == binding.SGQ_OK
