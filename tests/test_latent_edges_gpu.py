@@ -238,3 +238,65 @@ def test_expanded_wait_runs_out_and_the_stream_recovers(T, H, N):
     for _ in range(2):
         assert torch.equal(sgq.latent_prefill(q, k, kr, v, starts, starts, 0.1), want)
     assert sgq.sgq_device_status() == binding.SGQ_OK
+
+
+# ---------------------------------------------------------------- calls that overlap, and graphs of them
+
+def layer_calls(dtype, seed):
+    """Inputs of all operators and a function that calls each once, in an order that the results depend on: the
+    attention reads the rows that the append writes."""
+    T, H, L, R, page = 3, 16, 512, 64, 32
+    table = sgq.rotary_table(64, R)
+    lens = ints([2000, 33, 500])
+    width = 63
+    pages = torch.randperm(3 * width, generator=torch.Generator().manual_seed(seed)).int().view(3, width).cuda()
+    cache = normal(3 * width, page, L + R, dtype=dtype, seed=seed)
+    kv, q = normal(T, L + R, dtype=dtype, seed=seed + 1), normal(T, H, L + R, dtype=dtype, seed=seed + 2)
+    pos = ints([5, 63, 0], torch.int64)
+    slots = torch.stack([pages[b, (n - 1) // page].long() * page + (n - 1) % page for b, n in enumerate((2000, 33, 500))])
+    x = normal(700, 4, 192, dtype=dtype, seed=seed + 3)
+    up, kr, starts = normal(700, 4, 256, dtype=dtype, seed=seed + 4), normal(700, R, dtype=dtype, seed=seed + 5), ints([0, 301, 700])
+    xpos = torch.arange(700, device="cuda") % 64
+
+    def run(stream=None):
+        q_rot = sgq.latent_append(q[..., L:], kv[:, L:], kv[:, :L], pos, slots, table, cache, stream=stream)
+        o = sgq.latent_attention(q, cache, pages, lens, 0.05, L, stream=stream)
+        y = sgq.rotary(x, xpos, table, 128, stream=stream)
+        p = sgq.latent_prefill(y, up[..., :128], kr, up[..., 128:], starts, starts, 0.05, stream=stream)
+        return q_rot, o, y, p
+    return run, (q, kv, x, up)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_two_streams_at_once(dtype):
+    """Two callers' work in flight together: each gets what it gets alone, whatever memory the allocator hands out."""
+    (a, _), (b, _) = layer_calls(dtype, 100), layer_calls(dtype, 200)
+    want = [a(), b()]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(20):
+        for i, run in enumerate((a, b)):
+            got[i].append(run(streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for outputs in got[i]:
+            assert all(torch.equal(g, w) for g, w in zip(outputs, want[i]))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_graph_of_all_operators(dtype):
+    """A captured step, replayed on new inputs."""
+    run, inputs = layer_calls(dtype, 300)
+    run()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = run()
+    for i in range(3):
+        for j, t in enumerate(inputs):
+            t.copy_(normal(*t.shape, dtype=dtype, seed=400 + 10 * i + j))
+        want = run()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
