@@ -4,8 +4,8 @@ These helpers check shapes, types and strides, allocate what they return (and
 the attention's workspace) on the stream of the call, and call the binding; the
 work is in ``libsgq.so`` (``include/sgq.h``, "Latent attention").  Tensors are
 bfloat16 or float16, one type for a call, on the current device.  Wrong shapes,
-types or strides raise ValueError before anything is launched, and so does an
-input that requires a gradient while gradients are recorded: none is here.
+types or strides raise ValueError before anything is launched, and so does a
+tensor that requires a gradient while gradients are recorded: none is here.
 """
 from __future__ import annotations
 
@@ -32,10 +32,15 @@ def _empty(shape, like, stream):
 
 def _dtype(x, *others) -> int:
     import torch
-    dt = x.dtype
+    dt, graded = x.dtype, torch.is_grad_enabled()
+    if graded and x.requires_grad:
+        _graded()
     for t in others:
-        if t is not None and t.dtype != dt:
-            raise ValueError(f"one element type a call: {dt} and {t.dtype}")
+        if t is not None:
+            if t.dtype != dt:
+                raise ValueError(f"one element type a call: {dt} and {t.dtype}")
+            if graded and t.requires_grad:
+                _graded()
     if dt == torch.bfloat16:
         return binding.SGQ_BF16
     if dt == torch.float16:
@@ -47,13 +52,9 @@ def _fail(what: str):
     raise ValueError(what)
 
 
-def _no_gradient(*inputs):
-    import torch
-    if torch.is_grad_enabled():
-        for t in inputs:
-            if t is not None and t.requires_grad:
-                _fail("an input requires a gradient, and none is recorded here: detach it, or call under "
-                      "torch.no_grad() (rotary's gradient is rotary with inverse=True)")
+def _graded():
+    _fail("a tensor requires a gradient, and none is recorded here: detach it, or call under torch.no_grad() "
+          "(rotary's gradient is rotary with inverse=True)")
 
 
 def _strides(name: str, t, dims: int):
@@ -143,7 +144,6 @@ def rotary(x, positions, table, offset: int = 0, interleaved: bool = True, inver
     back times its square).  out may be x (in place); returns out.
     """
     import torch
-    _no_gradient(x)
     dt = _dtype(x, out)
     if x.dim() != 3:
         _fail(f"x: expected [T, H, D], got {tuple(x.shape)}")
@@ -172,7 +172,6 @@ def latent_append(q_rot, k_rot, latent, positions, slots, table, cache, interlea
     receives the rotated keys.
     """
     import torch
-    _no_gradient(q_rot, k_rot, latent)
     dt = _dtype(k_rot, q_rot, latent, cache, q_out, k_out)
     (kt,), (lt,), (cp, cr) = _strides("k_rot", k_rot, 2), _strides("latent", latent, 2), _strides("cache", cache, 3)
     T, R = k_rot.shape
@@ -227,7 +226,6 @@ def latent_attention(q, cache, page_table, kv_lens, scale: float, latent: int, q
     the same time uses; None: allocated here.
     """
     import torch
-    _no_gradient(q, cache)
     dt = _dtype(q, cache, out)
     (qt, qh), (cp, cr) = _strides("q", q, 3), _strides("cache", cache, 3)
     T, H, W = q.shape
@@ -280,7 +278,6 @@ def latent_prefill(q, k, k_rot, v, q_starts, kv_starts, scale: float, causal: bo
     logarithm of the softmax sums.
     """
     import torch
-    _no_gradient(q, k, k_rot, v)
     dt = _dtype(q, k, k_rot, v, out)
     (qt, qh), (kt, kh), (vt, vh) = _strides("q", q, 3), _strides("k", k, 3), _strides("v", v, 3)
     rt, = _strides("k_rot", k_rot, 2)
