@@ -29,10 +29,11 @@
 // and its barriers and tensor memory stay.
 //
 // Measured, 4096 tokens x 128 heads, causal, bf16: 427 us in bursts of 20 ms,
-// 1610 TFLOP/s (0.87 of the measured bf16 rate); 466 us repeated for seconds,
-// where the power limit holds the clock at 1.69 GHz (0.86 of what a library
-// product sustains).  On the way, in bursts: CTAs that end with their item 492
-// us; taking over items 469; asking late 453; the order of the items 429.
+// 1610 TFLOP/s (0.87 of the measured bf16 burst rate); 466 to 478 us repeated for
+// seconds, where the power limit holds the clock at 1.69 GHz (0.83 to 0.86 of
+// what a library product sustains).  On the way, in bursts: CTAs that end with
+// their item 492 us; taking over items 469; asking late 453; the order of the
+// items 429.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

@@ -15,9 +15,9 @@
 // so its cosines and sines are loaded once for all of them.  Its first heads
 // are on their way before it asks for the position, whose table row is two
 // dependent loads away.  Four blocks an SM (a register bound of 64) keep
-// enough of them in flight: 4096 x 128 x 192 fp16 (403 MB) in 70.8 us against
+// enough of them in flight: 4096 x 128 x 192 fp16 (403 MB) in 70.0 us against
 // 80.8 us without the bound, and 60.4 us at the measured copy rate; appending
-// 4099 tokens of 128 heads (145 MB) in 24.1 us against 21.7 us.
+// 4099 tokens of 128 heads (145 MB) in 23.9 us against 21.7 us.
 #include <cuda_runtime.h>
 
 #include "latent_common.cuh"

@@ -378,7 +378,8 @@ sgq_status sgq_rotary(const void* x, int64_t T, int64_t H, int64_t D, int64_t x_
  *
  * cache: [pages, page, L + R] with page and row strides; token t goes to
  * page slots[t] / page, row slots[t] % page.  A negative slot is padding: no
- * row is written.  Slots of one call are distinct.  k_out: the rotated keys
+ * row is written (its position is one of the table's all the same: queries and
+ * k_out are rotated by it).  Slots of one call are distinct.  k_out: the rotated keys
  * [T, R], or NULL.  H = 0: no queries (q and q_out NULL).  q_out == q rotates
  * in place.  L % 8 == 0, R as for sgq_rotary, R <= 256.
  */
