@@ -3,8 +3,9 @@
 The compute lives in ``libsgq.so`` (hand-written CUDA behind the C ABI of
 ``include/sgq.h``).  This package holds the ctypes binding (``binding``), the
 nvcc build (``build``), seeded synthetic inputs (``synth``), a few
-torch-facing helpers below that only allocate outputs and call the binding, and
-the latent attention between the linears (``latent``).
+torch-facing helpers below that only allocate outputs and call the binding, the
+latent attention between the linears (``latent``), the linears in 4 bits
+(``fp4``) and the norms around them (``norms``).
 """
 from __future__ import annotations
 
@@ -18,8 +19,13 @@ from .binding import (  # noqa: F401
     sgq_gemm_plan, sgq_gemm_plan_pow2,
     sgq_quant_weight_block, sgq_version, status_string,
     SGQ_BF16, SGQ_FP16, sgq_rotary, sgq_latent_append, sgq_latent_attention, sgq_latent_attention_workspace,
-    sgq_latent_prefill)
+    sgq_latent_prefill,
+    SGQ_MXFP4, SGQ_NVFP4, SGQ_OUT_NONE, SGQ_OUT_16, SGQ_OUT_FP8, SGQ_OUT_MXFP4, SGQ_OUT_NVFP4, SGQ_OUT_GROUP_128,
+    SGQ_OUT_POW2, SGQ_OUT_UE8M0, sgq_quant_fp4, sgq_dequant_fp4, sgq_fp4_gemm, sgq_norm)
+from .fp4 import (  # noqa: F401
+    dequant_fp4, fp4_gemm, fp4_scales_from_tiles, fp4_scales_to_tiles, fp4_tensor_scale, quant_fp4)
 from .latent import latent_append, latent_attention, latent_prefill, rotary, rotary_table  # noqa: F401
+from .norms import norm_add, rms_norm  # noqa: F401
 
 
 def quant_token_group(x, group: int, ue8m0: bool, stream=None):

@@ -35,6 +35,17 @@ SGQ_BF16 = 0
 SGQ_FP16 = 1
 SGQ_LATENT_TEST_TIMEOUT = 256
 
+SGQ_MXFP4 = 0
+SGQ_NVFP4 = 1
+SGQ_OUT_NONE = 0
+SGQ_OUT_16 = 1
+SGQ_OUT_FP8 = 2
+SGQ_OUT_MXFP4 = 3
+SGQ_OUT_NVFP4 = 4
+SGQ_OUT_GROUP_128 = 8
+SGQ_OUT_POW2 = 16
+SGQ_OUT_UE8M0 = 32
+
 # Symbols declared in include/sgq.h (checked by the tests).
 EXPORTS = (
     "sgq_quant_token_group",
@@ -55,6 +66,10 @@ EXPORTS = (
     "sgq_latent_attention_workspace",
     "sgq_latent_attention",
     "sgq_latent_prefill",
+    "sgq_quant_fp4",
+    "sgq_dequant_fp4",
+    "sgq_fp4_gemm",
+    "sgq_norm",
     "sgq_status_string",
     "sgq_device_status",
     "sgq_launch_count",
@@ -119,8 +134,12 @@ def load_library(path: str = LIB_PATH):
                                              ci, P, P, P, i64, P]
         lib.sgq_latent_prefill.argtypes = [P, i64, i64, i64, P, i64, i64, P, i64, P, i64, i64, i64, i64, i64, ci, P, P,
                                            i64, cf, ci, ci, P, P, P]
+        lib.sgq_quant_fp4.argtypes = [P, i64, i64, i64, ci, P, ci, ci, P, P, P]
+        lib.sgq_dequant_fp4.argtypes = [P, P, i64, i64, ci, P, ci, P, P]
+        lib.sgq_fp4_gemm.argtypes = [P, P, P, P, P, P, P, i64, i64, i64, ci, ci, P]
+        lib.sgq_norm.argtypes = [P, i64, P, P, i64, i64, P, i64, P, i64, P, i64, i64, cf, cf, cf, cf, ci, ci, P, P, P, P]
         for f in ("sgq_rotary", "sgq_latent_append", "sgq_latent_attention_workspace", "sgq_latent_attention",
-                  "sgq_latent_prefill"):
+                  "sgq_latent_prefill", "sgq_quant_fp4", "sgq_dequant_fp4", "sgq_fp4_gemm", "sgq_norm"):
             getattr(lib, f).restype = ci
         lib.sgq_status_string.argtypes = [ci]
         lib.sgq_status_string.restype = ctypes.c_char_p
@@ -287,6 +306,29 @@ def sgq_latent_prefill(q, q_stride_t, q_stride_h, T, k, k_stride_t, k_stride_h, 
                                              _ptr(k_rot), kr_stride, _ptr(v), v_stride_t, v_stride_h, S, H, N, R,
                                              _ptr(q_starts), _ptr(kv_starts), B, scale, int(causal), dtype, _ptr(out),
                                              _ptr(lse), _stream(stream)), "sgq_latent_prefill")
+
+
+def sgq_quant_fp4(x, M, K, x_stride, fmt, tensor_scale, silu_mul, dtype, xq, xs, stream=None):
+    _check(load_library().sgq_quant_fp4(_ptr(x), M, K, x_stride, fmt, _ptr(tensor_scale), int(silu_mul), dtype, _ptr(xq),
+                                        _ptr(xs), _stream(stream)), "sgq_quant_fp4")
+
+
+def sgq_dequant_fp4(xq, xs, M, K, fmt, tensor_scale, dtype, y, stream=None):
+    _check(load_library().sgq_dequant_fp4(_ptr(xq), _ptr(xs), M, K, fmt, _ptr(tensor_scale), dtype, _ptr(y),
+                                          _stream(stream)), "sgq_dequant_fp4")
+
+
+def sgq_fp4_gemm(Aq, As, a_scale, Wq, Ws, w_scale, D, M, N, K, fmt, dtype, stream=None):
+    _check(load_library().sgq_fp4_gemm(_ptr(Aq), _ptr(As), _ptr(a_scale), _ptr(Wq), _ptr(Ws), _ptr(w_scale), _ptr(D), M,
+                                       N, K, fmt, dtype, _stream(stream)), "sgq_fp4_gemm")
+
+
+def sgq_norm(x, x_stride, post_weight, gate, gate_stride, gate_rows, residual, residual_stride, h, h_stride, weight, M, K,
+             eps, offset, scale, residual_scale, dtype, out, tensor_scale, y, ys, stream=None):
+    _check(load_library().sgq_norm(_ptr(x), x_stride, _ptr(post_weight), _ptr(gate), gate_stride, gate_rows,
+                                   _ptr(residual), residual_stride, _ptr(h), h_stride, _ptr(weight), M, K, eps, offset,
+                                   scale, residual_scale, dtype, out, _ptr(tensor_scale), _ptr(y), _ptr(ys),
+                                   _stream(stream)), "sgq_norm")
 
 
 def sgq_device_status(stream=None) -> int:

@@ -33,6 +33,12 @@ bool good_strides(std::initializer_list<int64_t> strides) {
         if (s < 0 || s % 8 != 0 || s > (int64_t(1) << 40)) return false;
     return true;
 }
+// A tensor in the 4-bit form: M rows of K values, of which only the two-level
+// format takes a tensor scale; int32 columns, and spans of 512 that uint32 counts.
+bool good_fp4(int64_t M, int64_t K, int format, const float* tensor_scale) {
+    return M >= 0 && M < (int64_t(1) << 31) && K > 0 && K < (int64_t(1) << 31) && K % 32 == 0 &&
+           M * K <= (int64_t(1) << 40) && (format == SGQ_NVFP4 || (format == SGQ_MXFP4 && !tensor_scale));
+}
 // Tokens and heads of the absorbed attention: fewer than 2^31 rows (tokens
 // first, so that the product does not wrap).
 bool good_rows(int64_t T, int64_t H) {
@@ -67,6 +73,7 @@ sgq_status device_info(DeviceInfo* out) {
 using sgq::aligned16;
 using sgq::aligned_to;
 using sgq::good_dtype;
+using sgq::good_fp4;
 using sgq::good_rotation;
 using sgq::good_rows;
 using sgq::good_strides;
@@ -356,6 +363,78 @@ sgq_status sgq_latent_prefill(const void* q, int64_t q_stride_t, int64_t q_strid
     a.dtype = dtype; a.stall = stall;
     a.scale = scale;
     return sgq::launch_latent_prefill(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+sgq_status sgq_quant_fp4(const void* x, int64_t M, int64_t K, int64_t x_stride, int format, const float* tensor_scale,
+                         int silu_mul, int dtype, void* xq, void* xs, sgq_stream_t stream) {
+    if (!good_fp4(M, K, format, tensor_scale) || (silu_mul != 0 && silu_mul != 1) || !good_dtype(dtype) ||
+        !good_strides({x_stride}) || (M > 1 && x_stride < (silu_mul ? 2 * K : K)))
+        return SGQ_ERR_INVALID_ARG;
+    if (M == 0) return SGQ_OK;
+    if (!x || !xq || !xs) return SGQ_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(xq) || !aligned16(xs) || !aligned_to(tensor_scale, 4)) return SGQ_ERR_MISALIGNED;
+    return sgq::launch_quant_fp4(x, M, K, x_stride, format, tensor_scale, silu_mul, dtype, xq, xs,
+                                 reinterpret_cast<cudaStream_t>(stream));
+}
+
+sgq_status sgq_dequant_fp4(const void* xq, const void* xs, int64_t M, int64_t K, int format, const float* tensor_scale,
+                           int dtype, void* y, sgq_stream_t stream) {
+    if (!good_fp4(M, K, format, tensor_scale) || !good_dtype(dtype)) return SGQ_ERR_INVALID_ARG;
+    if (M == 0) return SGQ_OK;
+    if (!xq || !xs || !y) return SGQ_ERR_INVALID_ARG;
+    if (!aligned16(xq) || !aligned16(xs) || !aligned16(y) || !aligned_to(tensor_scale, 4)) return SGQ_ERR_MISALIGNED;
+    return sgq::launch_dequant_fp4(xq, xs, M, K, format, tensor_scale, dtype, y, reinterpret_cast<cudaStream_t>(stream));
+}
+
+sgq_status sgq_fp4_gemm(const void* Aq, const void* As, const float* a_scale, const void* Wq, const void* Ws,
+                        const float* w_scale, void* D, int64_t M, int64_t N, int64_t K, int format, int dtype,
+                        sgq_stream_t stream) {
+    if (!good_fp4(M, K, format, a_scale) || !good_fp4(N, K, format, w_scale) || N == 0 || N % 8 != 0 || !good_dtype(dtype))
+        return SGQ_ERR_INVALID_ARG;
+    if (M == 0) return SGQ_OK;
+    if (!Aq || !As || !Wq || !Ws || !D) return SGQ_ERR_INVALID_ARG;
+    if (!aligned16(Aq) || !aligned16(As) || !aligned16(Wq) || !aligned16(Ws) || !aligned16(D) ||
+        !aligned_to(a_scale, 4) || !aligned_to(w_scale, 4))
+        return SGQ_ERR_MISALIGNED;
+    sgq::Fp4GemmArgs a{};
+    a.Aq = Aq; a.As = As; a.a_t = a_scale; a.Wq = Wq; a.Ws = Ws; a.w_t = w_scale; a.D = D; a.M = M; a.N = N; a.K = K;
+    a.format = format; a.dtype = dtype;
+    return sgq::launch_fp4_gemm(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+sgq_status sgq_norm(const void* x, int64_t x_stride, const void* post_weight, const void* gate, int64_t gate_stride,
+                    int64_t gate_rows, const void* residual, int64_t residual_stride, void* h, int64_t h_stride,
+                    const void* weight, int64_t M, int64_t K, float eps, float offset, float scale,
+                    float residual_scale, int dtype, int out, const float* tensor_scale, void* y, void* ys,
+                    sgq_stream_t stream) {
+    const bool fp8 = (out & ~(SGQ_OUT_GROUP_128 | SGQ_OUT_POW2 | SGQ_OUT_UE8M0)) == SGQ_OUT_FP8 &&
+                     (out & (SGQ_OUT_POW2 | SGQ_OUT_UE8M0)) != (SGQ_OUT_POW2 | SGQ_OUT_UE8M0);
+    const int64_t group = fp8 ? (out & SGQ_OUT_GROUP_128 ? 128 : 32) : out == SGQ_OUT_MXFP4 || out == SGQ_OUT_NVFP4 ? 32 : 8;
+    if (M < 0 || M >= (int64_t(1) << 31) || K <= 0 || K > 32768 || K % group != 0 || !good_dtype(dtype) ||
+        !(std::isfinite(eps) && eps >= 0.0f) || !std::isfinite(offset) || !std::isfinite(scale) ||
+        !std::isfinite(residual_scale) || !good_strides({x_stride, gate_stride, residual_stride, h_stride}))
+        return SGQ_ERR_INVALID_ARG;
+    if (!fp8 && (out < SGQ_OUT_NONE || out > SGQ_OUT_NVFP4 || out == SGQ_OUT_FP8)) return SGQ_ERR_INVALID_ARG;
+    if (tensor_scale && out != SGQ_OUT_NVFP4) return SGQ_ERR_INVALID_ARG;
+    if ((residual == nullptr) != (h == nullptr) && M > 0) return SGQ_ERR_INVALID_ARG;
+    if (!residual && M > 0 && (post_weight || gate || out == SGQ_OUT_NONE)) return SGQ_ERR_INVALID_ARG;
+    if (gate && gate_rows <= 0) return SGQ_ERR_INVALID_ARG;
+    if (M > 1 && (x_stride < K || (residual && (residual_stride < K || h_stride < K)))) return SGQ_ERR_INVALID_ARG;
+    if (gate && M > gate_rows && gate_stride < K) return SGQ_ERR_INVALID_ARG;
+    if (M == 0) return SGQ_OK;
+    // rows are written after all of them are read, by the threads that read them: in place, or not overlapping
+    if ((x == h && x_stride != h_stride) || (residual && residual == h && residual_stride != h_stride)) return SGQ_ERR_INVALID_ARG;
+    const bool scales = out != SGQ_OUT_NONE && out != SGQ_OUT_16;
+    if (!x || (out != SGQ_OUT_NONE && (!weight || !y)) || (scales && !ys)) return SGQ_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(post_weight) || !aligned16(gate) || !aligned16(residual) || !aligned16(h) ||
+        !aligned16(weight) || !aligned16(y) || !aligned16(ys) || !aligned_to(tensor_scale, 4))
+        return SGQ_ERR_MISALIGNED;
+    sgq::NormArgs a{};
+    a.x = x; a.post = post_weight; a.gate = gate; a.residual = residual; a.weight = weight; a.tensor_scale = tensor_scale;
+    a.h = h; a.y = y; a.ys = ys; a.M = M; a.K = K; a.x_s = x_stride; a.r_s = residual_stride; a.h_s = h_stride;
+    a.gate_s = gate_stride; a.gate_rows = gate_rows; a.eps = eps; a.offset = offset; a.scale = scale;
+    a.residual_scale = residual_scale; a.out = out; a.dtype = dtype;
+    return sgq::launch_norm(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 const char* sgq_status_string(sgq_status s) {

@@ -1,0 +1,141 @@
+// The 4-bit form shared by its quantisers (fp4_quant.cu, norm.cu) and its
+// GEMM (fp4_gemm.cu): E2M1 codes, two a byte, the even element in the low
+// half, and one scale byte a group:
+//   MXFP4  32 values, UE8M0 (2^(byte - 127)):  s = max(amax, 1e-10) / 6 rounded
+//          up to a power of two, as the FP8 quantisers round theirs;
+//   NVFP4  16 values, E4M3, and one fp32 scale t a tensor:  s = E4M3(amax / (6 t)),
+//          at least 2^-9 and at most 448; the values are code * (s t).
+// A code is E2M1(x / s) or E2M1(x / (s t)): an IEEE fp32 division, then round to
+// nearest even, saturating at 6.  A group that holds a NaN or an infinity gets
+// the NaN scale byte and codes of zero.
+//
+// Scale bytes lie in tiles of 128 rows x 4 groups, 512 bytes each, tiles of a
+// row block one after the other along K: the byte of (row r, group j) is
+// (r % 32) * 16 + (r % 128) / 32 * 4 + j % 4 of its tile, the order in which
+// tcgen05.cp (32 lanes x 128 bits, copied to all four lane quarters) puts them
+// where the block-scaled MMA looks for them.  Groups past K are 0; rows past
+// the last one are never used and may hold anything.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cstdint>
+
+#include "latent_common.cuh"
+#include "quant_math.cuh"
+
+namespace sgq {
+namespace fp4 {
+
+using lat::Pair;
+
+constexpr float kMax = 6.0f;            // largest E2M1 value
+constexpr uint32_t kNanE8 = 0xFFu;      // NaN as UE8M0
+constexpr uint32_t kNanE4 = 0x7Fu;      // NaN as E4M3
+constexpr float kMinE4 = 0.001953125f;  // 2^-9, the smallest E4M3 value above 0
+constexpr uint32_t kInf = 0x7F800000u;
+
+__host__ __device__ constexpr int group_of(bool nv) { return nv ? 16 : 32; }
+// Tiles of scales along K.
+__host__ __device__ constexpr int64_t scale_tiles(int64_t K, bool nv) { return (K + (nv ? 63 : 127)) / (nv ? 64 : 128); }
+
+// Byte offset of a row's word of four groups (group j of it in byte j) in tile kb.
+__device__ __forceinline__ int64_t scale_word_at(int64_t row, int64_t kb, int64_t tiles) {
+    return ((row >> 7) * tiles + kb) * 512 + (row & 31) * 16 + ((row & 127) >> 5) * 4;
+}
+
+// Eight fp32 values -> eight E2M1 codes (saturating, to nearest even).
+__device__ __forceinline__ uint32_t codes8(const float (&q)[8]) {
+    uint32_t r;
+    asm("{\n.reg .b8 a, b, c, d;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\ncvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\ncvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
+        "mov.b32 %0, {a, b, c, d};\n}"
+        : "=r"(r)
+        : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
+    return r;
+}
+// And back: eight codes -> their values, as four fp16 pairs.
+__device__ __forceinline__ void values8(uint32_t codes, uint32_t (&h)[4]) {
+    asm("{\n.reg .b8 a, b, c, d;\nmov.b32 {a, b, c, d}, %4;\n"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\ncvt.rn.f16x2.e2m1x2 %1, b;\n"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\ncvt.rn.f16x2.e2m1x2 %3, d;\n}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(codes));
+}
+
+// fp32 -> E4M3 byte (saturating) and back.
+__device__ __forceinline__ uint32_t e4m3_of(float x) {
+    return static_cast<uint32_t>(__nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3));
+}
+__device__ __forceinline__ float of_e4m3(uint32_t b) {
+    const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(b), __NV_E4M3);
+    return __half2float(*reinterpret_cast<const __half*>(&h));
+}
+// 2^(byte - 127); NaN for 255.
+__device__ __forceinline__ float of_ue8m0(uint32_t b) {
+    return b == kNanE8 ? __uint_as_float(0x7FFFFFFFu) : b == 0 ? __uint_as_float(0x400000u) : __uint_as_float(b << 23);
+}
+
+// A group's scale byte from the bits of its largest magnitude (NaN's bits are
+// above infinity's, and those above every finite value's), and what its values
+// are divided by: s itself, or s t.  kNv: t6 = 6 t.
+template <bool kNv>
+__device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits, float t, float t6, float& div) {
+    if (amax_bits >= kInf) {
+        div = 0.0f;   // (codes of zero: see below)
+        return kNv ? kNanE4 : kNanE8;
+    }
+    const float amax = __uint_as_float(amax_bits);
+    if constexpr (kNv) {
+        const uint32_t b = max(e4m3_of(__fdiv_rn(amax, t6)), 1u);
+        div = __fmul_rn(of_e4m3(b), t);
+        return b;
+    } else {
+        uint32_t u = __float_as_uint(__fdiv_rn(fmaxf(amax, qm::kEps), kMax));
+        if (u & 0x7FFFFFu) u = (u & kInf) + 0x800000u;
+        div = __uint_as_float(u);
+        return u >> 23;
+    }
+}
+// Eight values of a group -> codes.  div == 0: the group is not finite.
+template <bool kNv>
+__device__ __forceinline__ uint32_t encode8(const float (&v)[8], float div) {
+    if (div == 0.0f) return 0u;
+    float q[8];
+    if constexpr (kNv) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(v[i], div);
+    } else {
+        // (a power of two, at least 2^-36: its reciprocal is exact, and x times that is the rounded quotient)
+        const float r = __uint_as_float((254u - (__float_as_uint(div) >> 23)) << 23);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = __fmul_rn(v[i], r);
+    }
+    return codes8(q);
+}
+
+__device__ __forceinline__ uint32_t amax_bits8(const float (&v)[8]) {
+    uint32_t a = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a = max(a, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    return a;
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack8(const uint4& w, float (&v)[8]) {
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = Pair<T>::unpack(x[i]);
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+    }
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+    return make_uint4(Pair<T>::pack(v[0], v[1]), Pair<T>::pack(v[2], v[3]), Pair<T>::pack(v[4], v[5]),
+                      Pair<T>::pack(v[6], v[7]));
+}
+
+}  // namespace fp4
+}  // namespace sgq

@@ -1,0 +1,203 @@
+// 4-bit quantisation with microscales, and its way back, for sm_103a: the form
+// and the rule are in fp4_common.cuh.
+//
+// Both kernels are bound by HBM: 2 bytes an element one way, 0.53 (MXFP4) or
+// 0.56 (NVFP4) the other.  A thread holds 16 consecutive elements, i.e. one
+// NVFP4 group or half an MXFP4 one; a warp walks over spans of 512 elements of
+// a row, so that the four groups of a scale word lie in neighbouring lanes and
+// leave as one store.
+#include <cuda_runtime.h>
+
+#include "fp4_common.cuh"
+#include "ptx.cuh"
+#include "sgq_internal.h"
+
+namespace sgq {
+namespace {
+
+using namespace fp4;
+
+constexpr int kThreads = 256;
+constexpr int kSpan = 512;   // elements of a warp's span
+
+// silu(g) * u in fp32: within 2^-18 of its value.
+__device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
+
+template <typename T, bool kNv, bool kSilu>
+__global__ void __launch_bounds__(kThreads) quant_fp4_kernel(const T* __restrict__ x, int64_t stride,
+                                                             const float* __restrict__ tensor_scale, uint2* __restrict__ xq,
+                                                             uint8_t* __restrict__ xs, uint32_t K, uint32_t spans,
+                                                             uint32_t total) {
+    ptx::launch_dependents();
+    ptx::grid_dependency_wait();
+    const float t = kNv && tensor_scale ? __ldg(tensor_scale) : 1.0f;
+    const float t6 = __fmul_rn(t, kMax);
+    const uint32_t lane = threadIdx.x & 31;
+    const uint32_t nwarps = gridDim.x * (kThreads / 32);
+    const int64_t tiles = scale_tiles(K, kNv);
+    constexpr int kUnroll = kSilu ? 1 : 2;
+    for (uint64_t w0 = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); w0 < total; w0 += uint64_t(nwarps) * kUnroll) {
+        uint4 raw[kUnroll][kSilu ? 4 : 2];
+        uint32_t row[kUnroll], col[kUnroll];
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) {
+            const uint64_t w = w0 + uint64_t(nwarps) * i;
+            row[i] = static_cast<uint32_t>(w) / spans;
+            col[i] = (static_cast<uint32_t>(w) - row[i] * spans) * kSpan + lane * 16;
+            if (w >= total) col[i] = 0xFFFFFFFFu;   // past the end
+            if (col[i] < K) {
+                const uint4* p = reinterpret_cast<const uint4*>(x + row[i] * stride + col[i]);
+                raw[i][0] = __ldg(p);
+                raw[i][1] = __ldg(p + 1);
+                if constexpr (kSilu) {
+                    const uint4* u = reinterpret_cast<const uint4*>(x + row[i] * stride + K + col[i]);
+                    raw[i][2] = __ldg(u);
+                    raw[i][3] = __ldg(u + 1);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < (kSilu ? 4 : 2); ++j) raw[i][j] = make_uint4(0, 0, 0, 0);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) {
+            float v[2][8];
+            unpack8<T>(raw[i][0], v[0]);
+            unpack8<T>(raw[i][1], v[1]);
+            if constexpr (kSilu) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float u[8];
+                    unpack8<T>(raw[i][2 + h], u);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[h][j] = silu_mul(v[h][j], u[j]);
+                }
+            }
+            uint32_t amax = max(amax_bits8(v[0]), amax_bits8(v[1]));
+            if constexpr (!kNv) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+            float div;
+            uint32_t byte = scale_byte<kNv>(amax, t, t6, div);
+            if (col[i] >= K) byte = 0;   // groups past K
+            const uint2 q = make_uint2(encode8<kNv>(v[0], div), encode8<kNv>(v[1], div));
+            // the word of four groups, gathered in the first of their lanes
+            constexpr int kStep = kNv ? 1 : 2;   // lanes a group
+            byte |= __shfl_down_sync(0xFFFFFFFFu, byte, kStep) << 8;
+            byte |= __shfl_down_sync(0xFFFFFFFFu, byte, 2 * kStep) << 16;
+            if (col[i] < K) {
+                xq[(row[i] * int64_t(K) + col[i]) / 16] = q;
+                if (lane % (4 * kStep) == 0)
+                    *reinterpret_cast<uint32_t*>(xs + scale_word_at(row[i], col[i] / (kNv ? 64 : 128), tiles)) = byte;
+            }
+        }
+    }
+}
+
+template <typename T, bool kNv>
+__global__ void __launch_bounds__(kThreads) dequant_fp4_kernel(const uint2* __restrict__ xq, const uint8_t* __restrict__ xs,
+                                                               const float* __restrict__ tensor_scale, uint4* __restrict__ y,
+                                                               uint32_t units, uint64_t total) {
+    ptx::launch_dependents();
+    ptx::grid_dependency_wait();
+    const float t = kNv && tensor_scale ? __ldg(tensor_scale) : 1.0f;
+    const int64_t tiles = scale_tiles(int64_t(units) * 16, kNv);
+    const uint64_t step = uint64_t(gridDim.x) * kThreads;
+    for (uint64_t i = uint64_t(blockIdx.x) * kThreads + threadIdx.x; i < total; i += step) {
+        const uint64_t row = i / units;
+        const uint32_t u = static_cast<uint32_t>(i - row * units);   // 16 elements: one NVFP4 group, half an MXFP4 one
+        const uint32_t g = kNv ? u : u / 2;
+        const uint2 q = __ldg(xq + i);
+        const uint32_t b = __ldg(xs + scale_word_at(static_cast<int64_t>(row), g / 4, tiles) + g % 4);
+        const float s = kNv ? __fmul_rn(of_e4m3(b), t) : of_ue8m0(b);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t p[4];
+            values8(h ? q.y : q.x, p);
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 f = Pair<__half>::unpack(p[j]);
+                v[2 * j] = __fmul_rn(f.x, s);
+                v[2 * j + 1] = __fmul_rn(f.y, s);
+            }
+            y[2 * i + h] = pack8<T>(v);
+        }
+    }
+}
+
+cudaLaunchConfig_t config(cudaLaunchAttribute* attr, int64_t blocks, cudaStream_t st) {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
+template <typename T, bool kNv, bool kSilu>
+sgq_status run_quant(const void* x, int64_t M, int64_t K, int64_t stride, const float* t, void* xq, void* xs, int sms,
+                     cudaStream_t st) {
+    const int64_t spans = (K + kSpan - 1) / kSpan, total = M * spans;
+    const int64_t per = kThreads / 32, cap = int64_t(sms) * 8;
+    const int64_t want = (total + per - 1) / per;
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = config(attr, want < cap ? want : cap, st);
+    if (cudaLaunchKernelEx(&cfg, quant_fp4_kernel<T, kNv, kSilu>, static_cast<const T*>(x), stride, t,
+                           static_cast<uint2*>(xq), static_cast<uint8_t*>(xs), static_cast<uint32_t>(K),
+                           static_cast<uint32_t>(spans), static_cast<uint32_t>(total)) != cudaSuccess)
+        return SGQ_ERR_CUDA;
+    note_launch();
+    return SGQ_OK;
+}
+template <typename T>
+sgq_status pick_quant(const void* x, int64_t M, int64_t K, int64_t stride, bool nv, const float* t, bool silu, void* xq,
+                      void* xs, int sms, cudaStream_t st) {
+    if (nv)
+        return silu ? run_quant<T, true, true>(x, M, K, stride, t, xq, xs, sms, st)
+                    : run_quant<T, true, false>(x, M, K, stride, t, xq, xs, sms, st);
+    return silu ? run_quant<T, false, true>(x, M, K, stride, t, xq, xs, sms, st)
+                : run_quant<T, false, false>(x, M, K, stride, t, xq, xs, sms, st);
+}
+template <typename T, bool kNv>
+sgq_status run_dequant(const void* xq, const void* xs, int64_t M, int64_t K, const float* t, void* y, int sms,
+                       cudaStream_t st) {
+    const int64_t total = M * (K / 16), want = (total + kThreads - 1) / kThreads, cap = int64_t(sms) * 8;
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = config(attr, want < cap ? want : cap, st);
+    if (cudaLaunchKernelEx(&cfg, dequant_fp4_kernel<T, kNv>, static_cast<const uint2*>(xq),
+                           static_cast<const uint8_t*>(xs), t, static_cast<uint4*>(y), static_cast<uint32_t>(K / 16),
+                           static_cast<uint64_t>(total)) != cudaSuccess)
+        return SGQ_ERR_CUDA;
+    note_launch();
+    return SGQ_OK;
+}
+
+}  // namespace
+
+sgq_status launch_quant_fp4(const void* x, int64_t M, int64_t K, int64_t stride, int format, const float* t, int silu,
+                            int dtype, void* xq, void* xs, cudaStream_t st) {
+    DeviceInfo di;
+    const sgq_status rc = device_info(&di);
+    if (rc != SGQ_OK) return rc;
+    if (!built_for(di)) return SGQ_ERR_UNSUPPORTED;
+    return dtype == SGQ_BF16
+               ? pick_quant<__nv_bfloat16>(x, M, K, stride, format == SGQ_NVFP4, t, silu != 0, xq, xs, di.sm_count, st)
+               : pick_quant<__half>(x, M, K, stride, format == SGQ_NVFP4, t, silu != 0, xq, xs, di.sm_count, st);
+}
+
+sgq_status launch_dequant_fp4(const void* xq, const void* xs, int64_t M, int64_t K, int format, const float* t, int dtype,
+                              void* y, cudaStream_t st) {
+    DeviceInfo di;
+    const sgq_status rc = device_info(&di);
+    if (rc != SGQ_OK) return rc;
+    if (!built_for(di)) return SGQ_ERR_UNSUPPORTED;
+    if (format == SGQ_NVFP4)
+        return dtype == SGQ_BF16 ? run_dequant<__nv_bfloat16, true>(xq, xs, M, K, t, y, di.sm_count, st)
+                                 : run_dequant<__half, true>(xq, xs, M, K, t, y, di.sm_count, st);
+    return dtype == SGQ_BF16 ? run_dequant<__nv_bfloat16, false>(xq, xs, M, K, t, y, di.sm_count, st)
+                             : run_dequant<__half, false>(xq, xs, M, K, t, y, di.sm_count, st);
+}
+
+}  // namespace sgq

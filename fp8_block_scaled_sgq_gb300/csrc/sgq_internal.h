@@ -89,6 +89,29 @@ struct PrefillArgs {
     float scale;
 };
 sgq_status launch_latent_prefill(const PrefillArgs& a, cudaStream_t stream);
+sgq_status launch_quant_fp4(const void* x, int64_t M, int64_t K, int64_t stride, int format, const float* t, int silu,
+                            int dtype, void* xq, void* xs, cudaStream_t stream);
+sgq_status launch_dequant_fp4(const void* xq, const void* xs, int64_t M, int64_t K, int format, const float* t, int dtype,
+                              void* y, cudaStream_t stream);
+// Arguments of the 4-bit GEMM.
+struct Fp4GemmArgs {
+    const void *Aq, *As, *Wq, *Ws;
+    const float *a_t, *w_t;    // or null
+    void* D;
+    int64_t M, N, K;
+    int format, dtype;
+};
+sgq_status launch_fp4_gemm(const Fp4GemmArgs& a, cudaStream_t stream);
+// Arguments of the fused norms (strides in elements).
+struct NormArgs {
+    const void *x, *post, *gate, *residual, *weight;   // post, gate, residual (and weight, with it): or null
+    const float* tensor_scale;                         // or null
+    void *h, *y, *ys;
+    int64_t M, K, x_s, r_s, h_s, gate_s, gate_rows;
+    float eps, offset, scale, residual_scale;
+    int out, dtype;
+};
+sgq_status launch_norm(const NormArgs& a, cudaStream_t stream);
 // The GEMM's launch plan for a device with sm_count SMs (host only):
 // out[0..7] = swap-AB, BN, K splits, work items, grid, alternating issuers,
 // cluster split-K, CTA pairs.

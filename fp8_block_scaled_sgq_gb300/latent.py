@@ -15,16 +15,17 @@ import math
 from . import binding
 
 
-def _empty(shape, like, stream):
-    """A new tensor of like's type and device that belongs to the call's stream,
+def _empty(shape, like, stream, dtype=None):
+    """A new tensor of like's type (or the one given) and device that belongs to the call's stream,
     so that its memory is not handed out again while its kernels run."""
     import torch
+    dtype = dtype or like.dtype
     if stream is None:
-        return torch.empty(shape, dtype=like.dtype, device=like.device)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     if isinstance(stream, int):   # (0 is the default stream's handle; torch makes a new stream of ExternalStream(0))
         stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=like.dtype, device=like.device)
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 # The checks below run on every call of a decode step: plain comparisons, the

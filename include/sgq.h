@@ -449,6 +449,106 @@ sgq_status sgq_latent_prefill(const void* q, int64_t q_stride_t, int64_t q_strid
                               int R, const int32_t* q_starts, const int32_t* kv_starts, int64_t B, float scale,
                               int causal, int dtype, void* out, float* lse, sgq_stream_t stream);
 
+/*
+ * 4-bit linears: quantisation to E2M1 codes with microscales, and the product
+ * of two tensors in that form.  Two formats (`format`):
+ *
+ *   SGQ_MXFP4  32 values a group, scale s = 2^(byte - 127) (UE8M0):
+ *              s = smallest power of two >= max(amax, 1e-10) / 6
+ *   SGQ_NVFP4  16 values a group, scale byte s in E4M3, and one fp32 scale t a
+ *              tensor (on the device, positive and finite; NULL: 1):
+ *              s = E4M3_RNE(min(amax / (6 t), 448)), at least 2^-9
+ *
+ * A code is E2M1_RNE(x / s), or of x / (s t) (fp32 operations, s t rounded
+ * first), saturated at +-6: one of +-{0, .5, 1, 1.5, 2, 3, 4, 6}.  A group that
+ * holds a NaN or an infinity gets the NaN scale byte (255, 0x7F) and codes of
+ * zero, so that what is computed from it is NaN.  t is calibrated, or
+ * max|x| / (6 * 448) of the tensor.
+ *
+ * Codes: uint8 [M, K/2], element 2i in the low half of byte i.  Scale bytes:
+ * tiles of 128 rows x 4 groups (512 bytes), [ceil(M/128)][T] of them with
+ * T = ceil(K/64) (NVFP4) or ceil(K/128) (MXFP4); group j of row r is byte
+ * (r % 32) * 16 + (r % 128) / 32 * 4 + j % 4 of tile [r / 128][j / 4].  That is
+ * the order of the tensor cores' scale copies: no call converts it.  Bytes of
+ * groups past K are 0 (written so here, and needed so by the GEMM); those of
+ * rows past M are neither written nor used.
+ *
+ * Element types of x, y and D are SGQ_BF16 or SGQ_FP16 (`dtype`).  K % 32 == 0;
+ * M * K <= 2^40; M == 0 is a no-op.  Addresses are 16-byte aligned (tensor
+ * scales 4-byte).  Launch overlap: these calls and sgq_norm start while the
+ * previous kernel on the stream is still running, and touch memory only after
+ * it has finished; the GEMM's weights, too, may be written by the call before.
+ */
+#define SGQ_MXFP4 0
+#define SGQ_NVFP4 1
+
+/*
+ * x: [M, K], rows x_stride elements apart (x_stride % 8 == 0), or, with
+ * silu_mul = 1, [M, 2K] of rows [gate | up], of which silu(gate) * up is
+ * quantised (fp32, silu(g) = g / (1 + exp(-g)), within 2^-18 of its value; not
+ * rounded to 16 bits between).  xq, xs: codes and scale tiles.
+ */
+sgq_status sgq_quant_fp4(const void* x, int64_t M, int64_t K, int64_t x_stride, int format, const float* tensor_scale,
+                         int silu_mul, int dtype, void* xq, void* xs, sgq_stream_t stream);
+
+/* The values that codes and scales stand for, rounded once: y [M, K] contiguous. */
+sgq_status sgq_dequant_fp4(const void* xq, const void* xs, int64_t M, int64_t K, int format, const float* tensor_scale,
+                           int dtype, void* y, sgq_stream_t stream);
+
+/*
+ * D[m, n] = a_scale w_scale sum_k A[m, k] W[n, k] over the codes times their
+ * group scales, fp32 accumulation in any order, rounded once.  Aq/As: M rows,
+ * Wq/Ws: N rows, both in one format; a_scale, w_scale: their fp32 tensor
+ * scales, or NULL for 1 (NULL for SGQ_MXFP4).  D: [M, N] contiguous, written,
+ * never read.  N % 8 == 0, N > 0; M, N, K < 2^31.  Sums that leave fp32 are
+ * infinite or NaN, as in any fp32 product.  No memory is allocated, and none
+ * is shared between calls.
+ */
+sgq_status sgq_fp4_gemm(const void* Aq, const void* As, const float* a_scale, const void* Wq, const void* Ws,
+                        const float* w_scale, void* D, int64_t M, int64_t N, int64_t K, int format, int dtype,
+                        sgq_stream_t stream);
+
+/*
+ * The norm before a block of linears, and what stands between two blocks.
+ * With N(v, w) = v / sqrt(mean(v^2) + eps) * (w + offset) for every row,
+ *
+ *   without a residual:  y = N(x, weight)
+ *   with one:            u = post_weight ? N(x, post_weight) : x
+ *                        h = residual_scale * residual + scale * gate * u
+ *                        y = N(h, weight)      (h as it is stored, in 16 bits)
+ *
+ * fp32 throughout; h is rounded once, and so is y, to what `out` says:
+ *
+ *   SGQ_OUT_NONE   no y (weight, y, ys NULL; a residual is needed)
+ *   SGQ_OUT_16     y: [M, K] of `dtype`
+ *   SGQ_OUT_FP8    y: E4M3 codes [M, K], ys: scales [M, K/group], by the rule of
+ *                  sgq_quant_token_group (on fp32 values); group 32, or 128 with
+ *                  SGQ_OUT_GROUP_128; fp32 scales, rounded up to powers of two
+ *                  with SGQ_OUT_POW2, as UE8M0 bytes with SGQ_OUT_UE8M0
+ *   SGQ_OUT_MXFP4, SGQ_OUT_NVFP4
+ *                  y: codes, ys: scale tiles, as sgq_quant_fp4 writes them
+ *                  (tensor_scale for SGQ_OUT_NVFP4, or NULL for 1)
+ *
+ * x, residual, h: [M, K] with row strides (h may be x or residual, with equal
+ * strides; otherwise outputs overlap nothing).  gate: row m / gate_rows for row
+ * m, rows gate_stride apart, or NULL for 1.  weight, post_weight: [K].  All of
+ * one `dtype`.  K <= 32768, a multiple of 8 and of the group (32 for the 4-bit
+ * formats); strides multiples of 8; eps >= 0; M == 0 is a no-op.
+ */
+#define SGQ_OUT_NONE 0
+#define SGQ_OUT_16 1
+#define SGQ_OUT_FP8 2
+#define SGQ_OUT_MXFP4 3
+#define SGQ_OUT_NVFP4 4
+#define SGQ_OUT_GROUP_128 8
+#define SGQ_OUT_POW2 16
+#define SGQ_OUT_UE8M0 32
+sgq_status sgq_norm(const void* x, int64_t x_stride, const void* post_weight, const void* gate, int64_t gate_stride,
+                    int64_t gate_rows, const void* residual, int64_t residual_stride, void* h, int64_t h_stride,
+                    const void* weight, int64_t M, int64_t K, float eps, float offset, float scale,
+                    float residual_scale, int dtype, int out, const float* tensor_scale, void* y, void* ys,
+                    sgq_stream_t stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char* sgq_status_string(sgq_status s);
 
