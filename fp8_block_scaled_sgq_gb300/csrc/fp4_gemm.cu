@@ -29,6 +29,7 @@ struct Args {
     int stages;      // K in stages
     int tiles_c;     // token tiles
     int tiles_n, tiles;   // pairs: weight tiles, and all tiles
+    bool stream_out;      // pairs: D is large
     int splits;
     int ring;        // stages in shared memory
 };
@@ -46,34 +47,71 @@ __device__ __forceinline__ uint32_t elect() {
     asm volatile("{\n.reg .pred e;\nelect.sync _|e, 0xffffffff;\nselp.u32 %0, 1, 0, e;\n}" : "=r"(r));
     return r;
 }
-template <bool kNv>
-__device__ __forceinline__ void mma_fp4_if(uint32_t pred, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
-                                           uint32_t sfb, uint32_t acc) {
-    if constexpr (kNv)
-        asm volatile(
-            "{\n.reg .pred p, q;\nsetp.ne.b32 p, %7, 0;\nsetp.ne.b32 q, %6, 0;\n"
-            "@p tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], q;\n}" ::"r"(
-                d),
-            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc), "r"(pred)
-            : "memory");
+// A stage's issue in two blocks of instructions for the elected lane of a
+// converged warp.  An MMA of 256 x 192 x 64 lasts 50 ns; with addresses formed
+// and predicates set anew for each, the warp took 66 ns to issue one.
+//
+// Scales of one row block (kTiles tiles of 128 rows x 4 groups, 512 bytes
+// each) into TMEM, kStep columns apart.
+#define SGQ_FP4_CP(CG)                                                                                            \
+    "{\n.reg .pred e;\n.reg .b32 t1, t2, t3;\n.reg .b64 s1, s2, s3;\nelect.sync _|e, 0xffffffff;\n"             \
+    "add.u32 t1, %0, %2;\nadd.u32 t2, %0, %3;\nadd.u32 t3, %0, %4;\n"                                             \
+    "add.s64 s1, %1, 32;\nadd.s64 s2, %1, 64;\nadd.s64 s3, %1, 96;\n"                                             \
+    "@e tcgen05.cp.cta_group::" CG ".32x128b.warpx4 [%0], %1;\n@e tcgen05.cp.cta_group::" CG ".32x128b.warpx4 [t1], s1;\n"
+#define SGQ_FP4_CP2(CG) \
+    "@e tcgen05.cp.cta_group::" CG ".32x128b.warpx4 [t2], s2;\n@e tcgen05.cp.cta_group::" CG ".32x128b.warpx4 [t3], s3;\n"
+template <int CG, bool kNv, int kStep>
+__device__ __forceinline__ void copy_scales(uint32_t t, uint64_t s) {
+    if constexpr (CG == 1 && kNv)
+        asm volatile(SGQ_FP4_CP("1") SGQ_FP4_CP2("1") "}" ::"r"(t), "l"(s), "n"(kStep), "n"(2 * kStep), "n"(3 * kStep) : "memory");
+    else if constexpr (CG == 1)
+        asm volatile(SGQ_FP4_CP("1") "}" ::"r"(t), "l"(s), "n"(kStep), "n"(2 * kStep), "n"(3 * kStep) : "memory");
+    else if constexpr (kNv)
+        asm volatile(SGQ_FP4_CP("2") SGQ_FP4_CP2("2") "}" ::"r"(t), "l"(s), "n"(kStep), "n"(2 * kStep), "n"(3 * kStep) : "memory");
     else
-        asm volatile(
-            "{\n.reg .pred p, q;\nsetp.ne.b32 p, %7, 0;\nsetp.ne.b32 q, %6, 0;\n"
-            "@p tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], q;\n}" ::"r"(
-                d),
-            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc), "r"(pred)
-            : "memory");
+        asm volatile(SGQ_FP4_CP("2") "}" ::"r"(t), "l"(s), "n"(kStep), "n"(2 * kStep), "n"(3 * kStep) : "memory");
 }
+#undef SGQ_FP4_CP
+#undef SGQ_FP4_CP2
+// A stage's MMAs (n of four; the first one starts the sum over where acc == 0):
+// operands 32 bytes further along K each; with two scales an MMA (MXFP4) a
+// word of four serves two MMAs, its halves chosen in the instruction descriptor.
+#define SGQ_FP4_MMA(CG, VEC)                                                                                       \
+    "{\n.reg .pred e, q, t, f;\n.reg .b32 x1, x2, x3, y1, y2, y3;\n.reg .b64 a1, a2, a3, b1, b2, b3;\n"          \
+    "elect.sync _|e, 0xffffffff;\nsetp.ne.b32 q, %6, 0;\nsetp.eq.u32 t, %0, %0;\n"                                 \
+    "add.s64 a1, %1, 2;\nadd.s64 a2, %1, 4;\nadd.s64 a3, %1, 6;\nadd.s64 b1, %2, 2;\nadd.s64 b2, %2, 4;\nadd.s64 b3, %2, 6;\n" \
+    "add.u32 x1, %4, %9;\nadd.u32 x2, %4, %10;\nadd.u32 x3, %4, %11;\nadd.u32 y1, %5, %12;\nadd.u32 y2, %5, %13;\nadd.u32 y3, %5, %14;\n" \
+    "@e tcgen05.mma.cta_group::" CG ".kind::mxf4nvf4.block_scale.scale_vec::" VEC " [%0], %1, %2, %3, [%4], [%5], q;\n" \
+    "setp.gt.and.u32 f, %8, 1, e;\n"                                                                              \
+    "@f tcgen05.mma.cta_group::" CG ".kind::mxf4nvf4.block_scale.scale_vec::" VEC " [%0], a1, b1, %7, [x1], [y1], t;\n" \
+    "setp.gt.and.u32 f, %8, 2, e;\n"                                                                              \
+    "@f tcgen05.mma.cta_group::" CG ".kind::mxf4nvf4.block_scale.scale_vec::" VEC " [%0], a2, b2, %3, [x2], [y2], t;\n" \
+    "setp.gt.and.u32 f, %8, 3, e;\n"                                                                              \
+    "@f tcgen05.mma.cta_group::" CG ".kind::mxf4nvf4.block_scale.scale_vec::" VEC " [%0], a3, b3, %7, [x3], [y3], t;\n}"
+template <int CG, bool kNv, int kStepA, int kStepB>
+__device__ __forceinline__ void mma_stage(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                          uint32_t acc, uint32_t n) {
+    constexpr int A1 = kNv ? kStepA : 0, A2 = kNv ? 2 * kStepA : kStepA, A3 = kNv ? 3 * kStepA : kStepA;
+    constexpr int B1 = kNv ? kStepB : 0, B2 = kNv ? 2 * kStepB : kStepB, B3 = kNv ? 3 * kStepB : kStepB;
+    const uint32_t second = kNv ? idesc : ptx::idesc_sf_ids(idesc, 2, 2);
+#define SGQ_FP4_OPS                                                                                                      \
+    "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc), "r"(second), "r"(n), "n"(A1), "n"(A2), "n"(A3), "n"(B1), \
+        "n"(B2), "n"(B3)
+    if constexpr (CG == 1 && kNv) asm volatile(SGQ_FP4_MMA("1", "4X")::SGQ_FP4_OPS : "memory");
+    else if constexpr (CG == 1) asm volatile(SGQ_FP4_MMA("1", "2X")::SGQ_FP4_OPS : "memory");
+    else if constexpr (kNv) asm volatile(SGQ_FP4_MMA("2", "4X")::SGQ_FP4_OPS : "memory");
+    else asm volatile(SGQ_FP4_MMA("2", "2X")::SGQ_FP4_OPS : "memory");
+#undef SGQ_FP4_OPS
+}
+#undef SGQ_FP4_MMA
 
+// 16 bytes to a shared-memory address of the cluster.
+__device__ __forceinline__ void st_cluster_v4(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
 __device__ __forceinline__ float tensor_scales(const Args& a) {
     return (a.a_t ? __ldg(a.a_t) : 1.0f) * (a.w_t ? __ldg(a.w_t) : 1.0f);
 }
-template <typename T>
-__device__ __forceinline__ T round_to(float x);
-template <>
-__device__ __forceinline__ __nv_bfloat16 round_to(float x) { return __float2bfloat16_rn(x); }
-template <>
-__device__ __forceinline__ __half round_to(float x) { return __float2half_rn(x); }
 
 // ---------------------------------------------------------------- weights on the 128-row side
 //
@@ -101,7 +139,7 @@ struct TileCfg {
     // never end).
     static constexpr size_t kLeast = size_t(kTmem) * (228 * 1024 / 512) - 1024;
     static size_t need(int ring, int splits) {
-        return size_t(kHead) + size_t(ring) * kStageBytes + (splits > 1 ? size_t(BN) * kRows * 4 : 0) + 1024;
+        return size_t(kHead) + size_t(ring) * kStageBytes + (splits > 1 ? size_t(BN < 4 * splits ? 4 * splits : BN) * kRows * 4 : 0) + 1024;
     }
     static size_t smem(int ring, int splits) { return need(ring, splits) < kLeast ? kLeast : need(ring, splits); }
 };
@@ -179,18 +217,11 @@ __global__ void __launch_bounds__(kTileThreads)
             if (!lat::wait_warp(full(s), r & 1, sync)) break;
             ptx::tc_fence_after();
             const uint32_t sfw = tmem + C::kSfAt + (n & 1) * 2 * C::kSfCols, sfx = sfw + C::kSfCols;
-#pragma unroll
-            for (int j = 0; j < C::kSf / 512; ++j) {
-                ptx::tmem_cp_32x128b_x4_if(e, sfw + 4 * j, wsd + s * (C::kSf >> 4) + 32 * j);
-                ptx::tmem_cp_32x128b_x4_if(e, sfx + 4 * j, xsd + s * (C::kSf >> 4) + 32 * j);
-            }
+            copy_scales<1, kNv, 4>(sfw, wsd + s * (C::kSf >> 4));
+            copy_scales<1, kNv, 4>(sfx, xsd + s * (C::kSf >> 4));
             const int left = a.K - kb * kStageK, mmas = left >= kStageK ? 4 : (left + kMmaK - 1) / kMmaK;
-            for (int j = 0; j < mmas; ++j) {
-                const uint32_t id = kNv ? idesc : ptx::idesc_sf_ids(idesc, (j & 1) * 2, (j & 1) * 2);
-                const uint32_t word = 4 * (kNv ? j : j / 2);
-                mma_fp4_if<kNv>(e, tmem, wd + s * (kRows * kRowBytes >> 4) + 2 * j, xd + s * (BN * kRowBytes >> 4) + 2 * j, id,
-                                sfw + word, sfx + word + sfx_off, n > 0 || j > 0);
-            }
+            mma_stage<1, kNv, 4, 4>(tmem, wd + s * (kRows * kRowBytes >> 4), xd + s * (BN * kRowBytes >> 4), idesc, sfw,
+                                    sfx + sfx_off, n > 0, mmas);
             ptx::tc_commit_if(e, empty(s));
         }
         ptx::tc_commit_if(e, acc_bar);
@@ -199,30 +230,42 @@ __global__ void __launch_bounds__(kTileThreads)
         const int quad = warp & 3, row = quad * 32 + lane;
         const int n = tw * kRows + row;
         const float scale = tensor_scales(a);
-        T* D = static_cast<T*>(a.D) + n;
         const int m0 = tx * BN;
         const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+        // Sums of four tokens for the lane's weight row -> D: lanes exchange with their neighbours, so that each
+        // stores two weight rows of two tokens.
+        T* const D = static_cast<T*>(a.D) + (n & ~1);
+        auto store4 = [&](const float (&v)[4], int m) {
+#pragma unroll
+            for (int c = 0; c < 4; c += 2) {
+                const float other = __shfl_xor_sync(0xFFFFFFFFu, lane & 1 ? v[c] : v[c + 1], 1);
+                const int token = m + c + (lane & 1);
+                const uint32_t two = lane & 1 ? Pair<T>::pack(other * scale, v[c + 1] * scale) : Pair<T>::pack(v[c] * scale, other * scale);
+                if (n < a.N && token < a.M) *reinterpret_cast<uint32_t*>(D + int64_t(token) * a.N) = two;
+            }
+        };
         ok = lat::wait_warp(acc_bar, 0, sync);
         ptx::tc_fence_after();
         if (S > 1) ptx::cluster_wait();
-        const int cols = BN / S;
+        // A part's share of the tokens: whole fours, the last parts of a short tile may have none.
+        const int cols = BN / S < 4 ? 4 : BN / S, shift = 31 - __clz(cols);
+        // received sums: [part][four tokens][row][4]
+        const uint32_t mine = red0 + (rank * cols * kRows + row * 4) * 4;
         if (ok) {
 #pragma unroll 1
-            for (int c0 = 0; c0 < BN; c0 += 16) {
+            for (int c0 = 0; c0 < BN && m0 + c0 < a.M; c0 += 16) {
                 uint32_t v[16];
                 ptx::tmem_ld<16>(t_lane + c0, v);
                 ptx::tmem_wait_ld();
-                if (S > 1) {
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        const int to = (c0 + c) / cols;
-                        const uint32_t at = red0 + ((rank * cols + (c0 + c) - to * cols) * kRows + row) * 4;
-                        ptx::st_cluster_f32(ptx::mapa(at, to), __uint_as_float(v[c]));
+                for (int c = 0; c < 16; c += 4) {
+                    if (S > 1) {
+                        const int to = (c0 + c) >> shift, at = (c0 + c) & (cols - 1);
+                        st_cluster_v4(ptx::mapa(mine + at * kRows * 4, to), v[c], v[c + 1], v[c + 2], v[c + 3]);
+                    } else {
+                        const float f[4] = {__uint_as_float(v[c]), __uint_as_float(v[c + 1]), __uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])};
+                        store4(f, m0 + c0 + c);
                     }
-                } else if (n < a.N) {
-#pragma unroll
-                    for (int c = 0; c < 16; ++c)
-                        if (m0 + c0 + c < a.M) D[int64_t(m0 + c0 + c) * a.N] = round_to<T>(__uint_as_float(v[c]) * scale);
                 }
             }
         }
@@ -230,15 +273,20 @@ __global__ void __launch_bounds__(kTileThreads)
         if (S > 1) {
             ptx::cluster_sync();
             // (the parts of a CTA that gave up are not there: its tile is undefined, as the status says)
-            const float* red = reinterpret_cast<const float*>(ring + (red0 - ring0));
-            if (n < a.N) {
-                for (int c = 0; c < cols; ++c) {
-                    const int m = m0 + rank * cols + c;
-                    if (m >= a.M) break;
-                    float sum = red[c * kRows + row];
-                    for (int r = 1; r < S; ++r) sum += red[(r * cols + c) * kRows + row];
-                    D[int64_t(m) * a.N] = round_to<T>(sum * scale);
+            const float4* red = reinterpret_cast<const float4*>(ring + (red0 - ring0)) + row;
+            for (int c = 0; c < cols; c += 4) {
+                const int m = m0 + rank * cols + c;
+                if (rank * cols >= BN || m >= a.M) break;
+                float4 sum = red[c / 4 * kRows];
+                for (int r = 1; r < S; ++r) {
+                    const float4 x = red[(r * cols + c) / 4 * kRows];
+                    sum.x += x.x;
+                    sum.y += x.y;
+                    sum.z += x.z;
+                    sum.w += x.w;
                 }
+                const float f[4] = {sum.x, sum.y, sum.z, sum.w};
+                store4(f, m);
             }
         }
     }
@@ -272,33 +320,59 @@ __global__ void __launch_bounds__(kTileThreads)
 
 // ---------------------------------------------------------------- many tokens: CTA pairs
 //
-// A pair of CTAs shares a tile of 256 tokens x BN weight rows (.cta_group::2):
-// each holds its 128 tokens and half of the weight rows of every stage, and
-// reads its 128 tokens' sums.  What an SM takes in per operation bounds this
-// product: at 4 bits the tensor cores ask for a 128 x 128 tile's stage every
-// 0.14 us, 36 KB that take an SM 0.3 us.  A pair's tile halves the weights'
-// share.  Two accumulators in TMEM: one is read and written out while the next
-// tile's sums form in the other.
+// A pair of CTAs shares a tile of kHalves * 256 tokens x BN weight rows
+// (.cta_group::2): each holds its tokens and half of the weight rows of every
+// stage, and reads its tokens' sums.  What bounds this product is shared
+// memory: at 4 bits an MMA of 256 x 192 x 64 lasts 96 cycles, in which its
+// operands are read (10 KB an SM) and the next ones written (8.7 KB with one
+// half, 6.5 KB with two that share the weights), at 128 bytes a cycle.
+//
+// TMEM holds two accumulators.  One half: tiles take them in turn, and one is
+// read while the next tile's sums form in the other.  Two halves: one each; a
+// tile's end shows, so it pays where K is long.
 //
 // Warps: 0 loads (TMA; both CTAs' boxes land on the leader's barrier), 1 issues
-// (the leader's), 4-11 read (two a TMEM lane quarter, half of the columns each).
+// (the leader's), 4-7 and 8-11 read an accumulator each (a TMEM lane quarter a
+// warp).
 constexpr int kPairThreads = 384;
-constexpr int kPairTokens = 256;
 
-template <int BN, bool kNv>
+template <int BN, bool kNv, int kHalves>
 struct PairCfg {
     static constexpr int kSf = sf_bytes(kNv);
     static constexpr int kWBlocks = BN > 128 ? 2 : 1;                // row blocks that a tile's weight rows touch
-    static constexpr int kXBytes = kRows * kRowBytes, kWBytes = BN / 2 * kRowBytes;
-    static constexpr int kStageBytes = kXBytes + kWBytes + kSf * (1 + kWBlocks);
-    static constexpr int kRing = (226 * 1024 - 2048) / kStageBytes < 8 ? (226 * 1024 - 2048) / kStageBytes : 8;
-    static constexpr int kSfCols = (kNv ? 16 : 8) * (1 + kWBlocks);  // TMEM columns of a stage's scales
+    static constexpr int kHalfBytes = kRows * kRowBytes;
+    static constexpr int kXBytes = kHalves * kHalfBytes, kWBytes = BN / 2 * kRowBytes;
+    static constexpr int kXSf = kHalves * kSf, kWSf = kWBlocks * kSf;
+    static constexpr int kStageBytes = kXBytes + kWBytes + kXSf + kWSf;
+    static constexpr int kRoom = 227 * 1024 - 2048;
+    static constexpr int kRing = kRoom / kStageBytes < 8 ? kRoom / kStageBytes : 8;
+    static constexpr int kWord = kNv ? 16 : 8;                       // TMEM columns of a row block's scales a stage
+    static constexpr int kSfCols = kWord * (kHalves + kWBlocks);
     static constexpr uint32_t kSfAt = 2 * BN;
     static_assert(kSfAt + 2 * kSfCols <= 512, "TMEM");
     static_assert(BN % 64 == 0 && BN <= 192, "tiles start at a row block or in its middle");
+    static constexpr int kTokens = kHalves * 256;                    // of a pair's tile
     static constexpr size_t kHead = 1024;
     static constexpr size_t kSmem = kHead + size_t(kRing) * kStageBytes + 1024;
 };
+
+// Arrives on a barrier of either CTA of the pair, publishing nothing: what it
+// says is that TMEM has been read, which tcgen05.wait::ld and the fence before
+// it have settled.  (With release semantics it waited for the warp's stores of
+// the tile before: 8192 x 24576 x 1536 took 134.8 us, and 116.9 so.)
+__device__ __forceinline__ void arrive_relaxed_if(uint32_t pred, uint32_t cluster_bar) {
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %1, 0;\n"
+        "@p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n}" ::"r"(cluster_bar), "r"(pred)
+        : "memory");
+}
+// 32 bytes that L2 gives up first: what is written once and is larger than
+// L2 has room for beside the operands makes way for them (116.9 -> 114.3 us).
+__device__ __forceinline__ void st_global_v8_first(void* p, const uint32_t (&w)[8]) {
+    asm volatile("st.global.L1::no_allocate.L2::evict_first.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
 
 // A whole warp waits for a phase that the other CTA of the pair may complete.
 static __device__ __noinline__ bool pair_wait_slow(uint32_t bar, uint32_t parity, const Sync& s) {
@@ -321,25 +395,6 @@ __device__ __forceinline__ bool pair_wait(uint32_t bar, uint32_t parity, const S
     if (__all_sync(0xFFFFFFFFu, ptx::mbar_try_wait_cluster(bar, parity))) return true;
     return pair_wait_slow(bar, parity, s);
 }
-template <bool kNv>
-__device__ __forceinline__ void mma_fp4_pair_if(uint32_t pred, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                                uint32_t sfa, uint32_t sfb, uint32_t acc) {
-    if constexpr (kNv)
-        asm volatile(
-            "{\n.reg .pred p, q;\nsetp.ne.b32 p, %7, 0;\nsetp.ne.b32 q, %6, 0;\n"
-            "@p tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], q;\n}" ::"r"(
-                d),
-            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc), "r"(pred)
-            : "memory");
-    else
-        asm volatile(
-            "{\n.reg .pred p, q;\nsetp.ne.b32 p, %7, 0;\nsetp.ne.b32 q, %6, 0;\n"
-            "@p tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], q;\n}" ::"r"(
-                d),
-            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc), "r"(pred)
-            : "memory");
-}
-
 // Tile i: weight tiles of a group of 16 token tiles before the next group's, so
 // that what runs together shares both operands in L2.
 __device__ __forceinline__ void pair_tile(const Args& a, int i, int& tm, int& tn) {
@@ -349,16 +404,16 @@ __device__ __forceinline__ void pair_tile(const Args& a, int i, int& tm, int& tn
     tm = g * 16 + in - tn * rows;
 }
 
-template <typename T, int BN, bool kNv>
+template <typename T, int BN, bool kNv, int kHalves>
 __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     fp4_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                     const __grid_constant__ CUtensorMap tm_xs, const __grid_constant__ CUtensorMap tm_ws, const Args a) {
-    using C = PairCfg<BN, kNv>;
+    using C = PairCfg<BN, kNv, kHalves>;
     extern __shared__ uint8_t raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     uint32_t* words = reinterpret_cast<uint32_t*>(smem + 512);   // TMEM base, abort flag
     const uint32_t bar0 = ptx::smem_u32(smem), ring0 = bar0 + C::kHead;
-    const uint32_t x0 = ring0, w0 = x0 + C::kRing * C::kXBytes, xs0 = w0 + C::kRing * C::kWBytes, ws0 = xs0 + C::kRing * C::kSf;
+    const uint32_t x0 = ring0, w0 = x0 + C::kRing * C::kXBytes, xs0 = w0 + C::kRing * C::kWBytes, ws0 = xs0 + C::kRing * C::kXSf;
     auto full = [&](int s) { return bar0 + 8u * s; };
     auto empty = [&](int s) { return bar0 + 8u * (8 + s); };
     auto acc_full = [&](int b) { return bar0 + 8u * (16 + b); };
@@ -377,7 +432,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
         }
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(acc_full(b), 1);
-            ptx::mbar_init(acc_empty(b), 16);   // the reading warps of both CTAs
+            ptx::mbar_init(acc_empty(b), 8);   // the reading warps of both CTAs
         }
         ptx::mbar_init(drain_bar, 1);
         words[1] = 0;
@@ -409,7 +464,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
         for (int i = first; i < a.tiles && ok; i += step) {
             int tm, tn;
             pair_tile(a, i, tm, tn);
-            const int row = tm * kPairTokens + static_cast<int>(rank) * kRows, wrow = tn * BN + static_cast<int>(rank) * (BN / 2);
+            const int row = tm * C::kTokens + static_cast<int>(rank) * (kHalves * kRows), wrow = tn * BN + static_cast<int>(rank) * (BN / 2);
             for (int kb = 0; kb < a.stages; ++kb, ++n) {
                 const int s = n % C::kRing, r = n / C::kRing;
                 if (r > 0 && !pair_wait(empty(s), (r - 1) & 1, sync)) {
@@ -420,8 +475,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
                 ptx::mbar_arrive_expect_tx_if(e && rank == 0u, full(s), 2 * C::kStageBytes);
                 ptx::tma_load_2d_pair_if(e, x0 + s * C::kXBytes, &tm_x, kb * kRowBytes, row, bar);
                 ptx::tma_load_2d_pair_if(e, w0 + s * C::kWBytes, &tm_w, kb * kRowBytes, wrow, bar);
-                ptx::tma_load_2d_pair_if(e, xs0 + s * C::kSf, &tm_xs, kb * (C::kSf / 8), tm * 2 + static_cast<int>(rank), bar);
-                ptx::tma_load_2d_pair_if(e, ws0 + s * C::kSf * C::kWBlocks, &tm_ws, kb * (C::kSf / 8), tn * BN / kRows, bar);
+                ptx::tma_load_2d_pair_if(e, xs0 + s * C::kXSf, &tm_xs, kb * (C::kSf / 8), row / kRows, bar);
+                ptx::tma_load_2d_pair_if(e, ws0 + s * C::kWSf, &tm_ws, kb * (C::kSf / 8), tn * BN / kRows, bar);
             }
         }
     } else if (warp == 1 && rank == 0u) {
@@ -436,78 +491,76 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
             int tm, tn;
             pair_tile(a, i, tm, tn);
             const uint32_t off = static_cast<uint32_t>(tn * BN % kRows) / 32;   // first weight row inside its row block
-            const int b = t & 1;
-            if (t > 1 && !pair_wait(acc_empty(b), ((t >> 1) - 1) & 1, sync)) break;
-            ptx::tc_fence_after();
-            const uint32_t d = tmem + b * BN;
+            // use u of accumulator b (of each half, or every other tile's)
+            const int b0 = kHalves == 2 ? 0 : t & 1, u = kHalves == 2 ? t : t >> 1;
             for (int kb = 0; kb < a.stages; ++kb, ++n) {
                 const int s = n % C::kRing, r = n / C::kRing;
-                if (!pair_wait(full(s), r & 1, sync)) {
-                    ok = false;
-                    break;
-                }
+                if (!(ok = pair_wait(full(s), r & 1, sync))) break;
                 ptx::tc_fence_after();
-                const uint32_t sfx = tmem + C::kSfAt + (n & 1) * C::kSfCols, sfw = sfx + (kNv ? 16 : 8);
-#pragma unroll
-                for (int j = 0; j < C::kSf / 512; ++j) {
-                    ptx::tmem_cp_g_if<2>(e, sfx + 4 * j, xsd + s * (C::kSf >> 4) + 32 * j);
-#pragma unroll
-                    for (int q = 0; q < C::kWBlocks; ++q)
-                        ptx::tmem_cp_g_if<2>(e, sfw + 4 * (j * C::kWBlocks + q),
-                                             wsd + s * (C::kSf * C::kWBlocks >> 4) + q * (C::kSf >> 4) + 32 * j);
-                }
+                const uint32_t sfx = tmem + C::kSfAt + (n & 1) * C::kSfCols, sfw = sfx + kHalves * C::kWord;
                 const int mmas = kb + 1 < a.stages ? 4 : last;
-                for (int j = 0; j < mmas; ++j) {
-                    const uint32_t id = kNv ? idesc : ptx::idesc_sf_ids(idesc, (j & 1) * 2, (j & 1) * 2);
-                    const uint32_t word = 4 * (kNv ? j : j / 2);
-                    mma_fp4_pair_if<kNv>(e, d, xd + s * (C::kXBytes >> 4) + 2 * j, wd + s * (C::kWBytes >> 4) + 2 * j, id, sfx + word,
-                                         sfw + word * C::kWBlocks + off, kb > 0 || j > 0);
+#pragma unroll
+                for (int q = 0; q < C::kWBlocks; ++q)
+                    copy_scales<2, kNv, 4 * C::kWBlocks>(sfw + 4 * q, wsd + s * (C::kWSf >> 4) + q * (C::kSf >> 4));
+#pragma unroll
+                for (int h = 0; h < kHalves; ++h) {
+                    const int b = kHalves == 2 ? h : b0;
+                    if (kb == 0) {   // the accumulator's last sums have been read
+                        if (u > 0 && !(ok = pair_wait(acc_empty(b), (u - 1) & 1, sync))) break;
+                        ptx::tc_fence_after();
+                    }
+                    const uint32_t sfh = sfx + h * C::kWord;
+                    copy_scales<2, kNv, 4>(sfh, xsd + s * (C::kXSf >> 4) + h * (C::kSf >> 4));
+                    mma_stage<2, kNv, 4, 4 * C::kWBlocks>(tmem + b * BN, xd + s * (C::kXBytes >> 4) + h * (C::kHalfBytes >> 4),
+                                                          wd + s * (C::kWBytes >> 4), idesc, sfh, sfw + off, kb > 0, mmas);
+                    if (kb + 1 == a.stages) ptx::tc_commit_g_if<2>(e, acc_full(b));
                 }
+                if (!ok) break;
                 ptx::tc_commit_g_if<2>(e, empty(s));
             }
-            if (ok) ptx::tc_commit_g_if<2>(e, acc_full(b));
         }
         ptx::tc_commit_local_g_if<2>(e, drain_bar);
         if (!ptx::mbar_try_wait(drain_bar, 0)) lat::wait_warp(drain_bar, 0, sync);
     } else if (warp >= 4) {
         ptx::grid_dependency_wait();   // the tensor scales; and D may still be read
-        const int quad = warp & 3, half = (warp - 4) >> 2;
+        const int quad = warp & 3, b = (warp - 4) >> 2;   // accumulator b
         const float scale = tensor_scales(a);
-        const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+        const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16) + b * BN;
         T* const D = static_cast<T*>(a.D);
         const bool wide = ((reinterpret_cast<uintptr_t>(D) | (static_cast<uintptr_t>(a.N) * 2u)) & 31u) == 0;
-        int t = 0;
-        for (int i = first; i < a.tiles; i += step, ++t) {
+        const int mine = kHalves == 2 ? step : 2 * step;
+        int u = 0;
+        for (int i = first + (kHalves == 2 ? 0 : b * step); i < a.tiles; i += mine, ++u) {
             int tm, tn;
             pair_tile(a, i, tm, tn);
-            const int b = t & 1;
-            if (!pair_wait(acc_full(b), (t >> 1) & 1, sync)) break;
+            if (!pair_wait(acc_full(b), u & 1, sync)) break;
             ptx::tc_fence_after();
-            constexpr int kCols = BN / 2;
-            uint32_t w[kCols / 2];
+            // all of a row goes to registers before any of it is stored: the accumulator is free sooner
+            uint32_t w[BN / 2];
 #pragma unroll
-            for (int c = 0; c < kCols; c += 16) {
-                uint32_t v[16];
-                ptx::tmem_ld<16>(t_lane + b * BN + half * kCols + c, v);
+            for (int c = 0; c < BN; c += 32) {
+                uint32_t v[32];
+                ptx::tmem_ld<32>(acc + c, v);
                 ptx::tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
+                for (int j = 0; j < 16; ++j)
                     w[c / 2 + j] = Pair<T>::pack(__uint_as_float(v[2 * j]) * scale, __uint_as_float(v[2 * j + 1]) * scale);
             }
             ptx::tc_fence_before();
             __syncwarp();
-            ptx::mbar_arrive_cluster_if(lane == 0 ? 1u : 0u, ptx::mapa(acc_empty(b), 0u));
-            const int m = tm * kPairTokens + static_cast<int>(rank) * kRows + quad * 32 + lane;
-            const int n0 = tn * BN + half * kCols;
+            arrive_relaxed_if(lane == 0 ? 1u : 0u, ptx::mapa(acc_empty(b), 0u));
+            const int m = tm * C::kTokens + (static_cast<int>(rank) * kHalves + (kHalves == 2 ? b : 0)) * kRows + quad * 32 + lane;
+            const int n0 = tn * BN;
             if (m < a.M) {
                 T* row = D + int64_t(m) * a.N + n0;
 #pragma unroll
-                for (int c = 0; c < kCols; c += 16) {
+                for (int c = 0; c < BN; c += 16) {
                     uint32_t q[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) q[j] = w[c / 2 + j];
                     if (wide && n0 + c + 16 <= a.N) {
-                        ptx::st_global_v8(row + c, q);
+                        if (a.stream_out) st_global_v8_first(row + c, q);
+                        else ptx::st_global_v8(row + c, q);
                     } else {
                         if (n0 + c < a.N) *reinterpret_cast<uint4*>(row + c) = make_uint4(q[0], q[1], q[2], q[3]);
                         if (n0 + c + 8 < a.N) *reinterpret_cast<uint4*>(row + c + 8) = make_uint4(q[4], q[5], q[6], q[7]);
@@ -567,6 +620,46 @@ struct Maps {
 
 sgq_status device_of(int* dev) { return cudaGetDevice(dev) == cudaSuccess && *dev >= 0 && *dev < 64 ? SGQ_OK : SGQ_ERR_CUDA; }
 
+// K splits of the tile kernel: doubled while every CTA still has an SM of its own and a stage to do.
+int tile_splits(int64_t tiles, int stages, int sms) {
+    int splits = 1;
+    while (splits < 8 && splits * 2 <= stages && tiles * splits * 2 <= sms) splits *= 2;
+    return splits;
+}
+
+// Which kernel serves more than 64 tokens: the one whose time, in us, is least
+// by what they measured (NVFP4; MXFP4 is 3 to 8 % faster everywhere).  A stage
+// costs an issuing warp 0.31 us, 0.48 us with two halves; a tile's end 0.25 and
+// 1.2; the sum over the parts of a split tile 0.8 and 0.8 for each 64 tokens;
+// a second CTA on an SM counts half for 64 tokens and whole for 128, whose
+// loads already fill the SM's share of L2.  Measured, us:
+//   N, K, M              64 tokens  128 tokens  pairs, one half  two halves
+//   1536, 7168, 128         6.4         7.2          11.8           15.5
+//   1536, 7168, 301         8.9         8.7          11.6           17.0
+//   7168, 2048, 301         6.8         8.0           7.1            9.3
+//   24576, 1536, 128       11.9         8.8           9.4           12.3
+//   7168, 7168, 1024       41.0        30.2          21.5           20.2
+//   7168, 7168, 4096      156.9        96.3          70.6           58.9
+//   24576, 1536, 8192       410         263           114            116
+enum Way { kTile64, kTile128, kPair1, kPair2 };
+Way way_of(int64_t M, int64_t N, int stages, int sms) {
+    auto tile = [&](int bn) {
+        const int64_t tiles = (N + kRows - 1) / kRows * ((M + bn - 1) / bn);
+        const int splits = tile_splits(tiles, stages, sms);
+        const double waves = tiles * splits <= sms ? 1.0 : double((tiles + 2 * sms - 1) / (2 * sms)) * (bn == 64 ? 1.5 : 2.0);
+        return 2.9 + waves * ((stages + splits - 1) / splits) * 0.31 + (splits > 1 ? 0.8 + 0.8 * bn / 64 : 0.0);
+    };
+    auto pair = [&](int64_t tokens, double stage, double end) {
+        const int64_t tiles = (M + tokens - 1) / tokens * ((N + 191) / 192), pairs = sms / 2;
+        return 2.6 + double((tiles + pairs - 1) / pairs) * (stages * stage + end);
+    };
+    const double t[4] = {tile(64), tile(128), pair(256, 0.31, 0.25), pair(512, 0.48, 1.2)};
+    int best = kPair1;
+    for (int i = 0; i < 4; ++i)
+        if (t[i] < t[best]) best = i;
+    return static_cast<Way>(best);
+}
+
 template <typename T, int BN, bool kNv>
 sgq_status run_tile(gemm::TensorMapEncoder encode, const Fp4GemmArgs& g, Args a, int sms, int smem_max, cudaStream_t st) {
     using C = TileCfg<BN, kNv>;
@@ -576,11 +669,11 @@ sgq_status run_tile(gemm::TensorMapEncoder encode, const Fp4GemmArgs& g, Args a,
         return SGQ_ERR_CUDA;
     a.tiles_c = static_cast<int>((g.M + BN - 1) / BN);
     const int64_t tiles = (g.N + kRows - 1) / kRows * a.tiles_c;
-    a.splits = 1;
-    while (a.splits < 8 && a.splits * 2 <= a.stages && tiles * a.splits * 2 <= sms) a.splits *= 2;
+    a.splits = tile_splits(tiles, a.stages, sms);
     const int per = (a.stages + a.splits - 1) / a.splits;
     a.ring = per < C::kMaxRing ? per : C::kMaxRing;
-    while (a.ring > 2 && C::need(a.ring, a.splits) > 113 * 1024) --a.ring;
+    const size_t room = (tiles * a.splits <= sms ? 226 : 113) * 1024;   // of an SM for one CTA, or for two
+    while (a.ring > 2 && C::need(a.ring, a.splits) > room) --a.ring;
     if (tiles * a.splits > INT32_MAX) return SGQ_ERR_INVALID_ARG;
     auto kern = fp4_tile_kernel<T, BN, kNv>;
     int dev = 0;
@@ -608,20 +701,22 @@ sgq_status run_tile(gemm::TensorMapEncoder encode, const Fp4GemmArgs& g, Args a,
     return SGQ_OK;
 }
 
-template <typename T, int BN, bool kNv>
+template <typename T, int BN, bool kNv, int kHalves>
 sgq_status run_pair(gemm::TensorMapEncoder encode, const Fp4GemmArgs& g, Args a, int sms, cudaStream_t st) {
-    using C = PairCfg<BN, kNv>;
+    using C = PairCfg<BN, kNv, kHalves>;
     Maps tm;
-    if (code_map(encode, &tm.w, g.Wq, g.N, g.K, BN / 2) != SGQ_OK || code_map(encode, &tm.x, g.Aq, g.M, g.K, kRows) != SGQ_OK ||
+    if (code_map(encode, &tm.w, g.Wq, g.N, g.K, BN / 2) != SGQ_OK ||
+        code_map(encode, &tm.x, g.Aq, g.M, g.K, kHalves * kRows) != SGQ_OK ||
         scale_map(encode, &tm.ws, g.Ws, g.N, g.K, kNv, C::kWBlocks) != SGQ_OK ||
-        scale_map(encode, &tm.xs, g.As, g.M, g.K, kNv, 1) != SGQ_OK)
+        scale_map(encode, &tm.xs, g.As, g.M, g.K, kNv, kHalves) != SGQ_OK)
         return SGQ_ERR_CUDA;
-    const int64_t tiles_m = (g.M + kPairTokens - 1) / kPairTokens, tiles_n = (g.N + BN - 1) / BN;
+    const int64_t tiles_m = (g.M + C::kTokens - 1) / C::kTokens, tiles_n = (g.N + BN - 1) / BN;
     if (tiles_m * tiles_n > INT32_MAX || 16 * tiles_n > INT32_MAX) return SGQ_ERR_INVALID_ARG;
     a.tiles_c = static_cast<int>(tiles_m);
     a.tiles_n = static_cast<int>(tiles_n);
     a.tiles = static_cast<int>(tiles_m * tiles_n);
-    auto kern = fp4_pair_kernel<T, BN, kNv>;
+    a.stream_out = g.M * g.N * 2 > (int64_t(32) << 20);
+    auto kern = fp4_pair_kernel<T, BN, kNv, kHalves>;
     int dev = 0;
     if (device_of(&dev) != SGQ_OK) return SGQ_ERR_CUDA;
     static bool configured[64] = {};
@@ -651,8 +746,13 @@ sgq_status pick(gemm::TensorMapEncoder encode, const Fp4GemmArgs& g, const Args&
     if (g.M <= 16) return run_tile<T, 16, kNv>(encode, g, a, di.sm_count, di.max_smem_optin, st);
     if (g.M <= 32) return run_tile<T, 32, kNv>(encode, g, a, di.sm_count, di.max_smem_optin, st);
     if (g.M <= 64) return run_tile<T, 64, kNv>(encode, g, a, di.sm_count, di.max_smem_optin, st);
-    if (g.M > 512) return run_pair<T, 192, kNv>(encode, g, a, di.sm_count, st);
-    return run_tile<T, 128, kNv>(encode, g, a, di.sm_count, di.max_smem_optin, st);
+    switch (way_of(g.M, g.N, a.stages, di.sm_count)) {
+        case kTile64: return run_tile<T, 64, kNv>(encode, g, a, di.sm_count, di.max_smem_optin, st);
+        case kTile128: return run_tile<T, 128, kNv>(encode, g, a, di.sm_count, di.max_smem_optin, st);
+        case kPair1: return run_pair<T, 192, kNv, 1>(encode, g, a, di.sm_count, st);
+        case kPair2: return run_pair<T, 192, kNv, 2>(encode, g, a, di.sm_count, st);
+    }
+    return SGQ_ERR_INVALID_ARG;
 }
 
 }  // namespace
