@@ -21,6 +21,7 @@
 #include <cstdint>
 
 #include "latent_common.cuh"
+#include "latent_ptx.cuh"
 #include "quant_math.cuh"
 
 namespace sgq {
@@ -97,19 +98,43 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits, float t, floa
         return u >> 23;
     }
 }
-// Eight values of a group -> codes.  div == 0: the group is not finite.
+// q = x / d correctly rounded, for eight values given as n = -x, two at a time.
+// With r = 1/d rounded, x r is corrected twice by its exact remainder: after
+// the first the quotient is within one unit, and after the second it is the
+// rounded one (Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990, theorem on the last step of a division).  On
+// negated values so that a zero keeps its sign.  Remainders are exact while
+// nothing leaves fp32's normal range: other divisors take the division itself.
+__device__ __forceinline__ void divide8(const float (&n)[8], float d, float (&q)[8]) {
+    if (!(d >= 0x1p-60f && d <= 0x1p100f)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(-n[i], d);
+        return;
+    }
+    const float r = -__frcp_rn(d);
+    const float2 r2 = make_float2(r, r), d2 = make_float2(d, d);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        const float2 n2 = make_float2(n[i], n[i + 1]);
+        float2 x = lat::mul2(n2, r2);
+        x = lat::fma2(lat::fma2(x, d2, n2), r2, x);
+        x = lat::fma2(lat::fma2(x, d2, n2), r2, x);
+        q[i] = x.x;
+        q[i + 1] = x.y;
+    }
+}
+// Eight values of a group, negated -> codes.  div == 0: the group is not finite.
 template <bool kNv>
-__device__ __forceinline__ uint32_t encode8(const float (&v)[8], float div) {
+__device__ __forceinline__ uint32_t encode8(const float (&n)[8], float div) {
     if (div == 0.0f) return 0u;
     float q[8];
     if constexpr (kNv) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(v[i], div);
+        divide8(n, div, q);
     } else {
         // (a power of two, at least 2^-36: its reciprocal is exact, and x times that is the rounded quotient)
-        const float r = __uint_as_float((254u - (__float_as_uint(div) >> 23)) << 23);
+        const float r = -__uint_as_float((254u - (__float_as_uint(div) >> 23)) << 23);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = __fmul_rn(v[i], r);
+        for (int i = 0; i < 8; ++i) q[i] = __fmul_rn(n[i], r);
     }
     return codes8(q);
 }

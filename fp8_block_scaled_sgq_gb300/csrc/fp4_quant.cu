@@ -20,8 +20,26 @@ using namespace fp4;
 constexpr int kThreads = 256;
 constexpr int kSpan = 512;   // elements of a warp's span
 
-// silu(g) * u in fp32: within 2^-18 of its value.
-__device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
+// -silu(g) * u of -g and u in fp32: within 2^-18 of its value.
+__device__ __forceinline__ float minus_silu_mul(float minus_g, float u) {
+    return __fdividef(minus_g, 1.0f + __expf(minus_g)) * u;
+}
+// The same 16-bit values with the other sign.
+__device__ __forceinline__ uint4 negate(uint4 w) {
+    return make_uint4(w.x ^ 0x80008000u, w.y ^ 0x80008000u, w.z ^ 0x80008000u, w.w ^ 0x80008000u);
+}
+
+// The fp32 bits of the largest magnitude among 16 values: magnitudes of one
+// sign order as whole numbers do, NaN above infinity, two a comparison.
+template <typename T>
+__device__ __forceinline__ uint32_t amax_bits16(const uint4& a, const uint4& b) {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t m = w[0] & 0x7FFF7FFFu;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+    m = max(m & 0xFFFFu, m >> 16);
+    return __float_as_uint(Pair<T>::unpack(m).x);
+}
 
 template <typename T, bool kNv, bool kSilu>
 __global__ void __launch_bounds__(kThreads) quant_fp4_kernel(const T* __restrict__ x, int64_t stride,
@@ -35,17 +53,17 @@ __global__ void __launch_bounds__(kThreads) quant_fp4_kernel(const T* __restrict
     const uint32_t lane = threadIdx.x & 31;
     const uint32_t nwarps = gridDim.x * (kThreads / 32);
     const int64_t tiles = scale_tiles(K, kNv);
-    constexpr int kUnroll = kSilu ? 1 : 2;
+    constexpr int kUnroll = kSilu ? 1 : 4;
+    constexpr int kVecs = kSilu ? 4 : 2;
     for (uint64_t w0 = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); w0 < total; w0 += uint64_t(nwarps) * kUnroll) {
-        uint4 raw[kUnroll][kSilu ? 4 : 2];
+        uint4 raw[kUnroll][kVecs];
         uint32_t row[kUnroll], col[kUnroll];
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i) {
             const uint64_t w = w0 + uint64_t(nwarps) * i;
             row[i] = static_cast<uint32_t>(w) / spans;
             col[i] = (static_cast<uint32_t>(w) - row[i] * spans) * kSpan + lane * 16;
-            if (w >= total) col[i] = 0xFFFFFFFFu;   // past the end
-            if (col[i] < K) {
+            if (w < total && col[i] < K) {
                 const uint4* p = reinterpret_cast<const uint4*>(x + row[i] * stride + col[i]);
                 raw[i][0] = __ldg(p);
                 raw[i][1] = __ldg(p + 1);
@@ -56,24 +74,27 @@ __global__ void __launch_bounds__(kThreads) quant_fp4_kernel(const T* __restrict
                 }
             } else {
 #pragma unroll
-                for (int j = 0; j < (kSilu ? 4 : 2); ++j) raw[i][j] = make_uint4(0, 0, 0, 0);
+                for (int j = 0; j < kVecs; ++j) raw[i][j] = make_uint4(0, 0, 0, 0);
             }
         }
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i) {
-            float v[2][8];
-            unpack8<T>(raw[i][0], v[0]);
-            unpack8<T>(raw[i][1], v[1]);
+            if (w0 + uint64_t(nwarps) * i >= total) break;   // (the whole warp)
+            float v[2][8];   // negated (encode8)
+            unpack8<T>(negate(raw[i][0]), v[0]);
+            unpack8<T>(negate(raw[i][1]), v[1]);
             if constexpr (kSilu) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     float u[8];
                     unpack8<T>(raw[i][2 + h], u);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[h][j] = silu_mul(v[h][j], u[j]);
+                    for (int j = 0; j < 8; ++j) v[h][j] = minus_silu_mul(v[h][j], u[j]);
                 }
             }
-            uint32_t amax = max(amax_bits8(v[0]), amax_bits8(v[1]));
+            uint32_t amax;
+            if constexpr (kSilu) amax = max(amax_bits8(v[0]), amax_bits8(v[1]));
+            else amax = amax_bits16<T>(raw[i][0], raw[i][1]);
             if constexpr (!kNv) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
             float div;
             uint32_t byte = scale_byte<kNv>(amax, t, t6, div);
@@ -94,32 +115,56 @@ __global__ void __launch_bounds__(kThreads) quant_fp4_kernel(const T* __restrict
 
 template <typename T, bool kNv>
 __global__ void __launch_bounds__(kThreads) dequant_fp4_kernel(const uint2* __restrict__ xq, const uint8_t* __restrict__ xs,
-                                                               const float* __restrict__ tensor_scale, uint4* __restrict__ y,
-                                                               uint32_t units, uint64_t total) {
+                                                               const float* __restrict__ tensor_scale, T* __restrict__ y,
+                                                               uint32_t K, uint32_t spans, uint32_t total) {
     ptx::launch_dependents();
     ptx::grid_dependency_wait();
     const float t = kNv && tensor_scale ? __ldg(tensor_scale) : 1.0f;
-    const int64_t tiles = scale_tiles(int64_t(units) * 16, kNv);
-    const uint64_t step = uint64_t(gridDim.x) * kThreads;
-    for (uint64_t i = uint64_t(blockIdx.x) * kThreads + threadIdx.x; i < total; i += step) {
-        const uint64_t row = i / units;
-        const uint32_t u = static_cast<uint32_t>(i - row * units);   // 16 elements: one NVFP4 group, half an MXFP4 one
-        const uint32_t g = kNv ? u : u / 2;
-        const uint2 q = __ldg(xq + i);
-        const uint32_t b = __ldg(xs + scale_word_at(static_cast<int64_t>(row), g / 4, tiles) + g % 4);
-        const float s = kNv ? __fmul_rn(of_e4m3(b), t) : of_ue8m0(b);
+    const int64_t tiles = scale_tiles(K, kNv);
+    const uint32_t lane = threadIdx.x & 31;
+    const uint32_t nwarps = gridDim.x * (kThreads / 32);
+    const bool wide = (reinterpret_cast<uintptr_t>(y) & 31u) == 0;
+    constexpr int kUnroll = 4;
+    for (uint64_t w0 = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); w0 < total; w0 += uint64_t(nwarps) * kUnroll) {
+        uint2 q[kUnroll];
+        uint32_t byte[kUnroll];
+        int64_t at[kUnroll];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint32_t p[4];
-            values8(h ? q.y : q.x, p);
-            float v[8];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 f = Pair<__half>::unpack(p[j]);
-                v[2 * j] = __fmul_rn(f.x, s);
-                v[2 * j + 1] = __fmul_rn(f.y, s);
+        for (int i = 0; i < kUnroll; ++i) {
+            const uint64_t w = w0 + uint64_t(nwarps) * i;
+            const uint32_t row = static_cast<uint32_t>(w) / spans;
+            const uint32_t col = (static_cast<uint32_t>(w) - row * spans) * kSpan + lane * 16;
+            at[i] = w < total && col < K ? row * int64_t(K) + col : -1;
+            q[i] = make_uint2(0, 0);
+            byte[i] = 0;
+            if (at[i] >= 0) {
+                const uint32_t g = kNv ? col / 16 : col / 32;
+                q[i] = __ldg(xq + at[i] / 16);
+                byte[i] = __ldg(xs + scale_word_at(row, g / 4, tiles) + g % 4);
             }
-            y[2 * i + h] = pack8<T>(v);
+        }
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) {
+            if (at[i] < 0) continue;   // past the row, or past the end
+            const float s = kNv ? __fmul_rn(of_e4m3(byte[i]), t) : of_ue8m0(byte[i]);
+            const float2 s2 = make_float2(s, s);
+            uint32_t out[8];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t p[4];
+                values8(h ? q[i].y : q[i].x, p);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 v = lat::mul2(Pair<__half>::unpack(p[j]), s2);
+                    out[4 * h + j] = Pair<T>::pack(v.x, v.y);
+                }
+            }
+            if (wide) {
+                ptx::st_global_v8(y + at[i], out);
+            } else {
+                *reinterpret_cast<uint4*>(y + at[i]) = make_uint4(out[0], out[1], out[2], out[3]);
+                *reinterpret_cast<uint4*>(y + at[i] + 8) = make_uint4(out[4], out[5], out[6], out[7]);
+            }
         }
     }
 }
@@ -163,12 +208,14 @@ sgq_status pick_quant(const void* x, int64_t M, int64_t K, int64_t stride, bool 
 template <typename T, bool kNv>
 sgq_status run_dequant(const void* xq, const void* xs, int64_t M, int64_t K, const float* t, void* y, int sms,
                        cudaStream_t st) {
-    const int64_t total = M * (K / 16), want = (total + kThreads - 1) / kThreads, cap = int64_t(sms) * 8;
+    const int64_t spans = (K + kSpan - 1) / kSpan, total = M * spans;
+    const int64_t per = kThreads / 32, cap = int64_t(sms) * 8;
+    const int64_t want = (total + per - 1) / per;
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = config(attr, want < cap ? want : cap, st);
-    if (cudaLaunchKernelEx(&cfg, dequant_fp4_kernel<T, kNv>, static_cast<const uint2*>(xq),
-                           static_cast<const uint8_t*>(xs), t, static_cast<uint4*>(y), static_cast<uint32_t>(K / 16),
-                           static_cast<uint64_t>(total)) != cudaSuccess)
+    if (cudaLaunchKernelEx(&cfg, dequant_fp4_kernel<T, kNv>, static_cast<const uint2*>(xq), static_cast<const uint8_t*>(xs), t,
+                           static_cast<T*>(y), static_cast<uint32_t>(K), static_cast<uint32_t>(spans),
+                           static_cast<uint32_t>(total)) != cudaSuccess)
         return SGQ_ERR_CUDA;
     note_launch();
     return SGQ_OK;

@@ -30,9 +30,11 @@ struct Args {
     const void *x, *post, *gate, *residual, *weight;
     const float* tensor_scale;
     void *h, *y, *ys;
-    int64_t M, x_s, r_s, h_s, gate_s, gate_rows;
-    int K, group, scale_kind;   // FP8: values a group; scales fp32 (0), fp32 powers of two (1), UE8M0 bytes (2)
-    float eps, offset, scale, residual_scale;
+    int64_t M, x_s, r_s, h_s, gate_s;
+    uint32_t gate_rows;
+    int depth;                  // rows under way (norm_walk_kernel)
+    int K, group_shift, scale_kind;   // FP8: columns of 8 a group, as a power of two; scales fp32 (0), fp32 powers of two (1), UE8M0 bytes (2)
+    float inv_k, eps, offset, scale, residual_scale;
 };
 
 // Sum over the kRow threads of a row (whole warps), in every one of them.
@@ -51,7 +53,137 @@ __device__ __forceinline__ float row_sum(float s, float* part) {
     return s;
 }
 
-// kRow threads a row, each with up to kVec columns of 8 elements, kRow columns apart.
+template <typename T>
+__device__ __forceinline__ uint4 column(const void* p, int64_t at, int c) {
+    return __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p) + at) + c);
+}
+// Arithmetic on eight values, two an instruction.
+__device__ __forceinline__ float2 two(const float (&v)[8], int j) { return make_float2(v[2 * j], v[2 * j + 1]); }
+__device__ __forceinline__ void set(float (&v)[8], int j, float2 x) {
+    v[2 * j] = x.x;
+    v[2 * j + 1] = x.y;
+}
+template <int kVec>
+__device__ __forceinline__ float squares(const float (&v)[kVec][8]) {
+    float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < kVec; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s = lat::fma2(two(v[i], j), two(v[i], j), s);
+    return s.x + s.y;
+}
+__device__ __forceinline__ float rstd_of(float sum, const Args& a) {
+    return __frsqrt_rn(fmaf(sum, a.inv_k, a.eps));
+}
+// v * factor * (weight + offset)
+template <typename T>
+__device__ __forceinline__ void weigh(float (&v)[8], float factor, const uint4& weight, float offset) {
+    float w[8];
+    unpack8<T>(weight, w);
+    const float2 f = make_float2(factor, factor), o = make_float2(offset, offset);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) set(v, j, lat::mul2(lat::mul2(two(v, j), f), lat::add2(two(w, j), o)));
+}
+// v * gate
+template <typename T>
+__device__ __forceinline__ void open(float (&v)[8], const uint4& gate) {
+    float g[8];
+    unpack8<T>(gate, g);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) set(v, j, lat::mul2(two(v, j), two(g, j)));
+}
+// h = residual_scale * residual + scale * u: what is stored, and its values.
+template <typename T>
+__device__ __forceinline__ uint4 add_residual(float (&v)[8], const uint4& residual, const Args& a) {
+    float r[8];
+    unpack8<T>(residual, r);
+    const float2 s = make_float2(a.scale, a.scale), t = make_float2(a.residual_scale, a.residual_scale);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) set(r, j, lat::fma2(s, two(v, j), lat::mul2(t, two(r, j))));
+    const uint4 h = pack8<T>(r);
+    unpack8<T>(h, v);
+    return h;
+}
+
+// qm::group_scale with the division by 448 as a product and two corrections by
+// its exact remainder (divide8's argument; 1/448 is rounded by the compiler).
+__device__ __forceinline__ float fp8_scale(float amax, bool pow2) {
+    constexpr float r = 1.0f / qm::kFp8Max;
+    const float x = fmaxf(amax, qm::kEps);
+    float s = __fmul_rn(x, r);
+    s = __fmaf_rn(__fmaf_rn(-s, qm::kFp8Max, x), r, s);
+    s = __fmaf_rn(__fmaf_rn(-s, qm::kFp8Max, x), r, s);
+    if (pow2) {
+        uint32_t u = __float_as_uint(s);
+        if (u & 0x7FFFFFu) u = (u & kInf) + 0x800000u;
+        s = __uint_as_float(u);
+    }
+    return s;
+}
+
+// Column c of row m of y, in what `out` asks for.  v: its values, negated where
+// they are to be quantised (divide8).  All lanes of a warp call it, those past
+// the row's end (in == false) too: groups lie in neighbouring lanes, and are
+// whole.
+template <typename T, Out kOut>
+__device__ __forceinline__ void emit(const Args& a, int64_t m, int c, bool in, const float (&v)[8], float t, float t6) {
+    const int cols = a.K / 8;
+    if constexpr (kOut == kSame) {
+        if (in) static_cast<uint4*>(a.y)[m * cols + c] = pack8<T>(v);
+    } else if constexpr (kOut == kFp8) {
+        float amax = in ? qm::amax8(v) : 0.0f;
+        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+        if (a.group_shift == 4) {
+            amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 4));
+            amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 8));
+        }
+        const float s = fp8_scale(amax, a.scale_kind != 0);
+        if (in) {
+            float q[8];
+            divide8(v, s, q);
+            uint32_t p[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                p[j] = __nv_cvt_float2_to_fp8x2(make_float2(q[2 * j], q[2 * j + 1]), __NV_SATFINITE, __NV_E4M3);
+            static_cast<uint2*>(a.y)[m * cols + c] = make_uint2(p[0] | (p[1] << 16), p[2] | (p[3] << 16));
+            if ((c & ((1 << a.group_shift) - 1)) == 0) {
+                const int64_t g = m * (cols >> a.group_shift) + (c >> a.group_shift);
+                if (a.scale_kind == 2) static_cast<uint8_t*>(a.ys)[g] = static_cast<uint8_t>(__float_as_uint(s) >> 23);
+                else static_cast<float*>(a.ys)[g] = s;
+            }
+        }
+    } else {
+        constexpr bool kNv = kOut == kNv4;
+        constexpr int kLanes = kNv ? 2 : 4;   // a group's
+        uint32_t amax = in ? amax_bits8(v) : 0u;
+        amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+        if constexpr (!kNv) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+        float div;
+        uint32_t byte = scale_byte<kNv>(amax, t, t6, div);
+        if (!in) byte = 0;
+        byte |= __shfl_down_sync(0xFFFFFFFFu, byte, kLanes) << 8;
+        byte |= __shfl_down_sync(0xFFFFFFFFu, byte, 2 * kLanes) << 16;
+        if (in) {
+            static_cast<uint32_t*>(a.y)[m * cols + c] = encode8<kNv>(v, div);
+            if (c % (4 * kLanes) == 0)
+                *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.ys) +
+                                             scale_word_at(m, c / (4 * kLanes), scale_tiles(a.K, kNv))) = byte;
+        }
+    }
+}
+template <Out kOut>
+__device__ __forceinline__ void tensor_scale_of(const Args& a, float& t, float& t6) {
+    t = 1.0f;
+    if constexpr (kOut == kNv4)
+        if (a.tensor_scale) t = __ldg(a.tensor_scale);
+    t6 = __fmul_rn(t, kMax);
+}
+__host__ __device__ constexpr bool negated(Out out) { return out == kFp8 || out == kMx4 || out == kNv4; }
+
+// Few rows, or narrow ones: kRow threads a row, each with up to kVec columns of
+// 8 elements, kRow columns apart; a CTA does one row (four, a warp each, where
+// kRow is 32) and ends.
 template <typename T, int kRow, int kVec, Out kOut>
 __global__ void __launch_bounds__(kRow == 32 ? 128 : kRow) norm_kernel(const Args a) {
     __shared__ float part[2][32];
@@ -61,10 +193,6 @@ __global__ void __launch_bounds__(kRow == 32 ? 128 : kRow) norm_kernel(const Arg
     const int64_t m = kRow == 32 ? int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5) : int64_t(blockIdx.x);
     if (m >= a.M) return;   // (a whole warp, which meets no other)
     const int cols = a.K / 8;
-    const float inv_k = 1.0f / static_cast<float>(a.K);
-    // (x and residual may be h: plain loads)
-    auto row_of = [&](const void* p, int64_t at, int c) { return reinterpret_cast<const uint4*>(static_cast<const T*>(p) + at)[c]; };
-    auto load = [&](const void* p, int64_t at, int c) { return __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p) + at) + c); };
 
     float v[kVec][8];
     uint4 r[kVec];
@@ -73,116 +201,180 @@ __global__ void __launch_bounds__(kRow == 32 ? 128 : kRow) norm_kernel(const Arg
         const int c = tid + i * kRow;
         uint4 w = make_uint4(0, 0, 0, 0);
         r[i] = w;
-        if (c < cols) {
-            w = row_of(a.x, m * a.x_s, c);
-            if (a.residual) r[i] = row_of(a.residual, m * a.r_s, c);
+        if (c < cols) {   // (x and residual may be h: plain loads)
+            w = reinterpret_cast<const uint4*>(static_cast<const T*>(a.x) + m * a.x_s)[c];
+            if (a.residual) r[i] = reinterpret_cast<const uint4*>(static_cast<const T*>(a.residual) + m * a.r_s)[c];
         }
         unpack8<T>(w, v[i]);
     }
-    auto rstd_of = [&](float* p) {
-        float s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kVec; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) s = fmaf(v[i][j], v[i][j], s);
-        return __frsqrt_rn(row_sum<kRow>(s, p) * inv_k + a.eps);
-    };
     if (a.residual) {
         if (a.post) {
-            const float rstd = rstd_of(part[0]);
+            const float rstd = rstd_of(row_sum<kRow>(squares(v), part[0]), a);
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) {
-                const int c = tid + i * kRow;
-                if (c >= cols) continue;
-                float w[8];
-                unpack8<T>(load(a.post, 0, c), w);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rstd * (w[j] + a.offset);
-            }
+            for (int i = 0; i < kVec; ++i)
+                if (tid + i * kRow < cols) weigh<T>(v[i], rstd, column<T>(a.post, 0, tid + i * kRow), a.offset);
         }
         if (a.gate) {
-            const int64_t at = m / a.gate_rows * a.gate_s;
+            const int64_t at = static_cast<uint32_t>(m) / a.gate_rows * a.gate_s;
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) {
-                const int c = tid + i * kRow;
-                if (c >= cols) continue;
-                float g[8];
-                unpack8<T>(load(a.gate, at, c), g);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] *= g[j];
-            }
+            for (int i = 0; i < kVec; ++i)
+                if (tid + i * kRow < cols) open<T>(v[i], column<T>(a.gate, at, tid + i * kRow));
         }
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
-            const int c = tid + i * kRow;
-            float f[8];
-            unpack8<T>(r[i], f);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = fmaf(a.scale, v[i][j], a.residual_scale * f[j]);
-            const uint4 h = pack8<T>(f);
-            if (c < cols) reinterpret_cast<uint4*>(static_cast<T*>(a.h) + m * a.h_s)[c] = h;
-            unpack8<T>(h, v[i]);   // what is stored
+            const uint4 h = add_residual<T>(v[i], r[i], a);
+            if (tid + i * kRow < cols) reinterpret_cast<uint4*>(static_cast<T*>(a.h) + m * a.h_s)[tid + i * kRow] = h;
         }
     }
-    if constexpr (kOut == kNone) return;
-
-    const float rstd = rstd_of(part[1]);
-    float t = 1.0f, t6 = kMax;
-    if constexpr (kOut == kNv4) {
-        if (a.tensor_scale) t = __ldg(a.tensor_scale);
-        t6 = __fmul_rn(t, kMax);
+    if constexpr (kOut != kNone) {
+        float rstd = rstd_of(row_sum<kRow>(squares(v), part[1]), a);
+        if constexpr (negated(kOut)) rstd = -rstd;
+        float t, t6;
+        tensor_scale_of<kOut>(a, t, t6);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+            const int c = tid + i * kRow;
+            if (c < cols) weigh<T>(v[i], rstd, column<T>(a.weight, 0, c), a.offset);
+            emit<T, kOut>(a, m, c, c < cols, v[i], t, t6);
+        }
     }
+}
+
+// Many rows of more than 1024 elements: the grid fills the SMs once, and each
+// CTA walks over rows, its weights in registers.  Every thread copies its own
+// two columns of the next rows into shared memory (cp.async, 16 bytes each,
+// read back by that thread alone), so that `depth` rows of x, residual and gate
+// are under way while one is summed.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ uint4 take16(uint32_t from) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(from) : "memory");
+    return v;
+}
+// Sum over the CTA's threads (whole warps), in every one of them.
+__device__ __forceinline__ float block_sum(float s, float* part) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
+    __syncthreads();
+    s = (threadIdx.x & 31) < (blockDim.x >> 5) ? part[threadIdx.x & 31] : 0.0f;
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
+    return __shfl_sync(0xFFFFFFFFu, s, 0);   // (at most 16 warps)
+}
+
+template <typename T, int kVec, Out kOut>
+__global__ void __launch_bounds__(kVec == 2 ? 128 : 512, kVec == 2 ? 6 : 1) norm_walk_kernel(const Args a) {
+    extern __shared__ uint4 ring[];
+    __shared__ float part[4][32];
+    ptx::launch_dependents();
+    ptx::grid_dependency_wait();
+    const int tid = threadIdx.x, threads = blockDim.x, cols = a.K / 8;
+    const uint32_t ring0 = ptx::smem_u32(ring) + tid * 16;
+    const int arrays = 1 + (a.residual != nullptr) + (a.gate != nullptr);
+    const uint32_t array_bytes = kVec * threads * 16, row_bytes = arrays * array_bytes;
+    // this thread's columns of a row: tid, tid + threads, ...
+    auto fetch = [&](int64_t m, uint32_t slot) {
+        if (m < a.M) {
+            auto row = [&](const void* p, int64_t at, uint32_t to) {
+                const T* from = static_cast<const T*>(p) + at + tid * 8;
+#pragma unroll
+                for (int i = 0; i < kVec; ++i)
+                    if (tid + i * threads < cols) copy16(to + i * threads * 16, from + i * threads * 8);
+            };
+            row(a.x, m * a.x_s, slot);
+            if (a.residual) row(a.residual, m * a.r_s, slot + array_bytes);
+            if (a.gate) row(a.gate, (a.gate_rows == 1 ? m : static_cast<uint32_t>(m) / a.gate_rows) * a.gate_s, slot + 2 * array_bytes);
+        }
+        ptx::cp_async_commit();
+    };
+    for (int d = 0; d < a.depth; ++d) fetch(blockIdx.x + int64_t(d) * gridDim.x, ring0 + d * row_bytes);
+    uint4 weight[kVec], post[kVec];
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
-        const int c = tid + i * kRow;
-        const bool in = c < cols;
-        if (in) {
-            float w[8];
-            unpack8<T>(load(a.weight, 0, c), w);
+        const int c = tid + i * threads;
+        weight[i] = post[i] = make_uint4(0, 0, 0, 0);
+        if (kOut != kNone && c < cols) weight[i] = column<T>(a.weight, 0, c);
+        if (a.post && c < cols) post[i] = column<T>(a.post, 0, c);
+    }
+    float t, t6;
+    tensor_scale_of<kOut>(a, t, t6);
+    int d = 0, turn = 0;
+    for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x, turn ^= 1) {
+        ptx::cp_async_wait_pending(a.depth - 1);
+        const uint32_t slot = ring0 + d * row_bytes;
+        float v[kVec][8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rstd * (w[j] + a.offset);
+        for (int i = 0; i < kVec; ++i) {
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (tid + i * threads < cols) x = take16(slot + i * threads * 16);
+            unpack8<T>(x, v[i]);
         }
-        // (groups are whole, and of neighbouring lanes: rows are whole warps' columns)
-        if constexpr (kOut == kSame) {
-            if (in) static_cast<uint4*>(a.y)[m * cols + c] = pack8<T>(v[i]);
-        } else if constexpr (kOut == kFp8) {
-            float amax = in ? qm::amax8(v[i]) : 0.0f;
-            const int lanes = a.group / 8;
-            amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-            amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-            if (lanes == 16) {
-                amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 4));
-                amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 8));
+        // (a row's first sum is met by all before the next row's is written: two sums take turns where there is no other)
+        if (a.residual) {
+            if (a.post) {
+                const float rstd = rstd_of(block_sum(squares(v), part[2 * turn]), a);
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) weigh<T>(v[i], rstd, post[i], a.offset);
             }
-            const bool pow2 = a.scale_kind != 0;
-            const float s = qm::group_scale(amax, pow2);
-            if (in) {
-                static_cast<uint2*>(a.y)[m * cols + c] = qm::quantize8(v[i], s, pow2);
-                if (c % lanes == 0) {
-                    const int64_t g = (m * cols + c) / lanes;
-                    if (a.scale_kind == 2) static_cast<uint8_t*>(a.ys)[g] = static_cast<uint8_t>(__float_as_uint(s) >> 23);
-                    else static_cast<float*>(a.ys)[g] = s;
-                }
+            if (a.gate) {
+#pragma unroll
+                for (int i = 0; i < kVec; ++i)
+                    if (tid + i * threads < cols) open<T>(v[i], take16(slot + 2 * array_bytes + i * threads * 16));
             }
-        } else {
-            constexpr bool kNv = kOut == kNv4;
-            constexpr int kLanes = kNv ? 2 : 4;   // a group's
-            uint32_t amax = in ? amax_bits8(v[i]) : 0u;
-            amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-            if constexpr (!kNv) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-            float div;
-            uint32_t byte = scale_byte<kNv>(amax, t, t6, div);
-            if (!in) byte = 0;
-            byte |= __shfl_down_sync(0xFFFFFFFFu, byte, kLanes) << 8;
-            byte |= __shfl_down_sync(0xFFFFFFFFu, byte, 2 * kLanes) << 16;
-            if (in) {
-                static_cast<uint32_t*>(a.y)[m * cols + c] = encode8<kNv>(v[i], div);
-                if (c % (4 * kLanes) == 0)
-                    *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.ys) +
-                                                 scale_word_at(m, c / (4 * kLanes), scale_tiles(a.K, kNv))) = byte;
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) {
+                if (tid + i * threads >= cols) continue;
+                const uint4 h = add_residual<T>(v[i], take16(slot + array_bytes + i * threads * 16), a);
+                reinterpret_cast<uint4*>(static_cast<T*>(a.h) + m * a.h_s)[tid + i * threads] = h;
+            }
+        }
+        float rstd = 0.0f;
+        if constexpr (kOut != kNone) rstd = rstd_of(block_sum(squares(v), part[2 * turn + 1]), a);
+        fetch(m + int64_t(a.depth) * gridDim.x, slot);   // (what was in the slot has been used)
+        if (++d == a.depth) d = 0;
+        if constexpr (kOut != kNone) {
+            if constexpr (negated(kOut)) rstd = -rstd;
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) {
+                const int c = tid + i * threads;
+                weigh<T>(v[i], rstd, weight[i], a.offset);
+                emit<T, kOut>(a, m, c, c < cols, v[i], t, t6);
             }
         }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+template <typename T, int kVec, Out kOut>
+sgq_status walk(Args a, int sms, cudaStream_t st) {
+    const int cols = a.K / 8, threads = (cols + 32 * kVec - 1) / (32 * kVec) * 32;
+    const int ctas = (kVec == 2 ? 768 : 512) / threads, share = 208 * 1024 / ctas;
+    const int row_bytes = (1 + (a.residual != nullptr) + (a.gate != nullptr)) * kVec * threads * 16;
+    a.depth = share / row_bytes < 4 ? share / row_bytes : 4;
+    auto kern = norm_walk_kernel<T, kVec, kOut>;
+    static bool configured[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SGQ_ERR_CUDA;
+    if (!configured[dev]) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 208 * 1024) != cudaSuccess) return SGQ_ERR_CUDA;
+        configured[dev] = true;
+    }
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(sms * ctas));
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(a.depth) * row_bytes;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) return SGQ_ERR_CUDA;
+    note_launch();
+    return SGQ_OK;
 }
 
 template <typename T, int kRow, int kVec, Out kOut>
@@ -201,21 +393,25 @@ sgq_status run(const Args& a, cudaStream_t st) {
     return SGQ_OK;
 }
 template <typename T, Out kOut>
-sgq_status by_width(const Args& a, cudaStream_t st) {
+sgq_status by_width(const Args& a, int sms, cudaStream_t st) {
+    // More rows than a grid that fills the SMs twice: CTAs walk.
+    const bool many = a.K > 1024 && a.K <= 16384 && a.M > int64_t(sms) * 2;
+    if (many) return a.K <= 2048 ? walk<T, 2, kOut>(a, sms, st) : walk<T, 4, kOut>(a, sms, st);
     if (a.K <= 1024) return run<T, 32, 4, kOut>(a, st);
-    if (a.K <= 4096) return run<T, 128, 4, kOut>(a, st);
-    if (a.K <= 8192) return run<T, 256, 4, kOut>(a, st);
-    if (a.K <= 16384) return run<T, 512, 4, kOut>(a, st);
+    if (a.K <= 2048) return run<T, 128, 2, kOut>(a, st);
+    if (a.K <= 4096) return run<T, 256, 2, kOut>(a, st);
+    if (a.K <= 8192) return run<T, 512, 2, kOut>(a, st);
+    if (a.K <= 16384) return run<T, 1024, 2, kOut>(a, st);
     return run<T, 1024, 4, kOut>(a, st);
 }
 template <typename T>
-sgq_status by_out(const Args& a, Out out, cudaStream_t st) {
+sgq_status by_out(const Args& a, Out out, int sms, cudaStream_t st) {
     switch (out) {
-        case kNone: return by_width<T, kNone>(a, st);
-        case kSame: return by_width<T, kSame>(a, st);
-        case kFp8: return by_width<T, kFp8>(a, st);
-        case kMx4: return by_width<T, kMx4>(a, st);
-        case kNv4: return by_width<T, kNv4>(a, st);
+        case kNone: return by_width<T, kNone>(a, sms, st);
+        case kSame: return by_width<T, kSame>(a, sms, st);
+        case kFp8: return by_width<T, kFp8>(a, sms, st);
+        case kMx4: return by_width<T, kMx4>(a, sms, st);
+        case kNv4: return by_width<T, kNv4>(a, sms, st);
     }
     return SGQ_ERR_INVALID_ARG;
 }
@@ -231,7 +427,8 @@ sgq_status launch_norm(const NormArgs& n, cudaStream_t st) {
     a.x = n.x; a.post = n.post; a.gate = n.gate; a.residual = n.residual; a.weight = n.weight;
     a.tensor_scale = n.tensor_scale; a.h = n.h; a.y = n.y; a.ys = n.ys;
     a.M = n.M; a.x_s = n.x_s; a.r_s = n.r_s; a.h_s = n.h_s; a.gate_s = n.gate_s;
-    a.gate_rows = n.gate_rows; a.K = static_cast<int>(n.K);
+    a.gate_rows = static_cast<uint32_t>(n.gate_rows < n.M ? n.gate_rows : n.M); a.K = static_cast<int>(n.K);
+    a.inv_k = 1.0f / static_cast<float>(n.K);
     a.eps = n.eps; a.offset = n.offset; a.scale = n.scale; a.residual_scale = n.residual_scale;
     Out out = kNone;
     switch (n.out) {
@@ -241,10 +438,10 @@ sgq_status launch_norm(const NormArgs& n, cudaStream_t st) {
         case SGQ_OUT_NVFP4: out = kNv4; break;
         default:
             out = kFp8;
-            a.group = n.out & SGQ_OUT_GROUP_128 ? 128 : 32;
+            a.group_shift = n.out & SGQ_OUT_GROUP_128 ? 4 : 2;
             a.scale_kind = (n.out & SGQ_OUT_UE8M0) != 0 ? 2 : (n.out & SGQ_OUT_POW2) != 0 ? 1 : 0;
     }
-    return n.dtype == SGQ_BF16 ? by_out<__nv_bfloat16>(a, out, st) : by_out<__half>(a, out, st);
+    return n.dtype == SGQ_BF16 ? by_out<__nv_bfloat16>(a, out, di.sm_count, st) : by_out<__half>(a, out, di.sm_count, st);
 }
 
 }  // namespace sgq
