@@ -13,23 +13,44 @@ from __future__ import annotations
 from . import binding
 from .latent import _contiguous, _device, _dtype, _empty, _fail
 
-_FORMAT = {"mxfp4": binding.SGQ_MXFP4, "nvfp4": binding.SGQ_NVFP4}
-_TILE_K = {"mxfp4": 128, "nvfp4": 64}     # values of a row in a tile of scales
+_FORMAT = {"mxfp4": (binding.SGQ_MXFP4, 128), "nvfp4": (binding.SGQ_NVFP4, 64)}    # and values of a row in a tile of scales
 
 
-def _format(fmt) -> int:
+# The smallest calls take less time on the GPU than their checks do on the host.  So each helper asks everything at
+# once, in plain comparisons, and a helper's _why_not finds out what was wrong only when something was.
+
+def _format(fmt):
     try:
         return _FORMAT[fmt]
     except (KeyError, TypeError):
         _fail(f"format {fmt!r} is neither 'mxfp4' nor 'nvfp4'")
 
 
-def _tiles(M: int, K: int, fmt: str):
-    return -(-M // 128), -(-K // _TILE_K[fmt]), 512
+def _current(stream):
+    """(the current device, the call's stream as a handle)."""
+    import torch
+    try:   # (names of this torch that are not public: 0.9 -> 0.2 us)
+        device = torch._C._cuda_getDevice()
+        if stream is None:
+            return device, torch._C._cuda_getCurrentRawStream(device)
+    except AttributeError:
+        device = torch.cuda.current_device()
+    return device, binding._stream(stream)
 
 
-def _scale(name: str, t, fmt: str):
-    """A tensor scale: one fp32 value on the device, of the two-level format only."""
+def _done(rc, what):
+    if rc:
+        binding._check(rc, what)
+
+
+def _new(shape, dtype, x, stream):
+    """A new tensor on x's device that belongs to the call's stream."""
+    import torch
+    return torch.empty(shape, dtype=dtype, device=x.device) if stream is None else _empty(shape, x, stream, dtype)
+
+
+def _scale(name: str, t, fmt):
+    """Whether t is a tensor scale: one fp32 value on the device, of the two-level format only."""
     import torch
     if t is not None:
         if fmt != "nvfp4":
@@ -41,13 +62,12 @@ def _scale(name: str, t, fmt: str):
 
 
 def _packed(name: str, q, s, fmt: str):
-    """(M, K) of a tensor in the 4-bit form."""
+    """Whether q and s are a tensor in the 4-bit form."""
     import torch
     if q.dim() != 2 or q.dtype != torch.uint8 or not q.is_contiguous():
         _fail(f"{name}: expected contiguous uint8 codes [rows, K/2], got {tuple(q.shape)} of {q.dtype}")
     M, K = q.shape[0], 2 * q.shape[1]
-    _contiguous(f"{name}'s scale tiles", s, _tiles(M, K, fmt), torch.uint8)
-    return M, K
+    _contiguous(f"{name}'s scale tiles", s, (-(-M // 128), -(-K // _FORMAT[fmt][1]), 512), torch.uint8)
 
 
 def fp4_tensor_scale(x):
@@ -65,7 +85,8 @@ def fp4_scales_to_tiles(s):
     rows, groups = s.shape
     full = torch.zeros(-(-rows // 128) * 128, -(-groups // 4) * 4, dtype=torch.uint8, device=s.device)
     full[:rows, :groups] = s
-    return full.view(-1, 4, 32, full.shape[1] // 4, 4).permute(0, 3, 2, 1, 4).reshape(-1, full.shape[1] // 4, 512)
+    tiles = full.view(full.shape[0] // 128, 4, 32, full.shape[1] // 4, 4).permute(0, 3, 2, 1, 4)
+    return tiles.reshape(full.shape[0] // 128, full.shape[1] // 4, 512)
 
 
 def fp4_scales_from_tiles(tiles, rows: int, groups: int):
@@ -82,7 +103,31 @@ def quant_fp4(x, fmt: str, tensor_scale=None, silu_mul: bool = False, xq=None, x
     device ("nvfp4"; None: 1).  xq, xs: outputs to write to.
     """
     import torch
-    f, dt = _format(fmt), _dtype(x)
+    f, tile = _format(fmt)
+    t, u8, device_stream = tensor_scale, torch.uint8, _current(stream)
+    device, dt = device_stream[0], _number(x.dtype)
+    shape, strides = x.shape, x.stride()
+    if len(shape) != 2 or dt is None or x.get_device() != device:
+        _why_not_quant(x, silu_mul, t, fmt, xq, xs)
+    M, W = shape
+    K = W // 2 if silu_mul else W
+    if (strides[1] != 1 or K % 32 or not K or (silu_mul and W % 2) or (x.requires_grad and torch.is_grad_enabled())
+            or (t is not None and (t.get_device() != device or fmt != "nvfp4" or t.dtype is not torch.float32
+                                   or t.numel() != 1 or t.requires_grad)) or xq is not None or xs is not None):
+        _why_not_quant(x, silu_mul, t, fmt, xq, xs)
+    if xq is None:
+        xq = _new((M, K // 2), u8, x, stream)
+    if xs is None:
+        xs = _new((-(-M // 128), -(-K // tile), 512), u8, x, stream)
+    _done(binding.load_library().sgq_quant_fp4(x.data_ptr(), M, K, strides[0] if M > 1 else W, f, t if t is None else t.data_ptr(),
+                                               1 if silu_mul else 0, dt, xq.data_ptr(), xs.data_ptr(), device_stream[1]),
+          "sgq_quant_fp4")
+    return xq, xs
+
+
+def _why_not_quant(x, silu_mul, t, fmt, xq, xs):
+    import torch
+    _dtype(x)
     if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
         _fail(f"x: expected rows of contiguous values, got {tuple(x.shape)} with strides {x.stride()}")
     M, K = x.shape
@@ -92,33 +137,51 @@ def quant_fp4(x, fmt: str, tensor_scale=None, silu_mul: bool = False, xq=None, x
         K //= 2
     if K % 32 or K == 0:
         _fail(f"{K} columns are not whole groups of 32")
-    _scale("tensor_scale", tensor_scale, fmt)
-    _device(x, tensor_scale, xq, xs)
-    if xq is None:
-        xq = _empty((M, K // 2), x, stream, torch.uint8)
-    else:
+    _scale("tensor_scale", t, fmt)
+    _device(x, t, xq, xs)
+    if xq is not None:
         _contiguous("xq", xq, (M, K // 2), torch.uint8)
-    if xs is None:
-        xs = _empty(_tiles(M, K, fmt), x, stream, torch.uint8)
-    else:
-        _contiguous("xs", xs, _tiles(M, K, fmt), torch.uint8)
-    binding.sgq_quant_fp4(x, M, K, x.stride(0) if M > 1 else x.shape[1], f, tensor_scale, silu_mul, dt, xq, xs, stream)
-    return xq, xs
+    if xs is not None:
+        _contiguous("xs", xs, (-(-M // 128), -(-K // _FORMAT[fmt][1]), 512), torch.uint8)
+
+
+def _number(dtype):
+    """The C interface's number of an element type, None where it has none."""
+    import torch
+    return binding.SGQ_BF16 if dtype is torch.bfloat16 else binding.SGQ_FP16 if dtype is torch.float16 else None
 
 
 def dequant_fp4(xq, xs, fmt: str, tensor_scale=None, dtype=None, out=None, stream=None):
     """The values [M, K] that codes and scale tiles stand for, in bfloat16 (or dtype, or out's type)."""
     import torch
-    f = _format(fmt)
-    M, K = _packed("xq", xq, xs, fmt)
-    _scale("tensor_scale", tensor_scale, fmt)
-    _device(xq, xs, tensor_scale, out)
+    f, tile = _format(fmt)
+    t, u8, device_stream = tensor_scale, torch.uint8, _current(stream)
+    device, shape = device_stream[0], xq.shape
+    dtype = dtype or (torch.bfloat16 if out is None else out.dtype)
+    dt = _number(dtype)
+    if (len(shape) != 2 or dt is None or xq.dtype is not u8 or xs.dtype is not u8 or not xq.is_contiguous()
+            or not xs.is_contiguous() or xs.shape != (-(-shape[0] // 128), -(-2 * shape[1] // tile), 512)
+            or xq.get_device() != device or xs.get_device() != device or out is not None
+            or (t is not None and (t.get_device() != device or fmt != "nvfp4" or t.dtype is not torch.float32
+                                   or t.numel() != 1 or t.requires_grad))):
+        _packed("xq", xq, xs, fmt)
+        _scale("tensor_scale", t, fmt)
+        _device(xq, xs, t, out)
+        _out(out, dtype, (shape[0], 2 * shape[1]))
+    M, K = shape[0], 2 * shape[1]
     if out is None:
-        out = _empty((M, K), xq, stream, dtype or torch.bfloat16)
-    else:
-        _contiguous("out", out, (M, K), dtype)
-    binding.sgq_dequant_fp4(xq, xs, M, K, f, tensor_scale, _dtype(out), out, stream)
+        out = _new((M, K), dtype, xq, stream)
+    _done(binding.load_library().sgq_dequant_fp4(xq.data_ptr(), xs.data_ptr(), M, K, f, t if t is None else t.data_ptr(), dt,
+                                                 out.data_ptr(), device_stream[1]), "sgq_dequant_fp4")
     return out
+
+
+def _out(out, dtype, shape):
+    if _number(dtype) is None:
+        _fail(f"element type {dtype} is neither bfloat16 nor float16")
+    if out is not None:
+        _contiguous("out", out, shape, dtype)
+        _dtype(out)
 
 
 def fp4_gemm(xq, xs, wq, ws, fmt: str, x_scale=None, w_scale=None, dtype=None, out=None, stream=None):
@@ -127,17 +190,34 @@ def fp4_gemm(xq, xs, wq, ws, fmt: str, x_scale=None, w_scale=None, dtype=None, o
     x_scale, w_scale: the tensors' fp32 scales ("nvfp4"; None: 1).
     """
     import torch
-    f = _format(fmt)
-    M, K = _packed("xq", xq, xs, fmt)
-    N, kw = _packed("wq", wq, ws, fmt)
-    if kw != K:
-        _fail(f"xq has {K} columns, wq {kw}")
-    _scale("x_scale", x_scale, fmt)
-    _scale("w_scale", w_scale, fmt)
-    _device(xq, xs, wq, ws, x_scale, w_scale, out)
+    f, tile = _format(fmt)
+    a, w, u8, f32, device_stream = x_scale, w_scale, torch.uint8, torch.float32, _current(stream)
+    device, xshape, wshape = device_stream[0], xq.shape, wq.shape
+    dtype = dtype or (torch.bfloat16 if out is None else out.dtype)
+    dt = _number(dtype)
+    if (len(xshape) != 2 or len(wshape) != 2 or xshape[1] != wshape[1] or dt is None or xq.dtype is not u8
+            or xs.dtype is not u8 or wq.dtype is not u8 or ws.dtype is not u8 or not xq.is_contiguous()
+            or not xs.is_contiguous() or not wq.is_contiguous() or not ws.is_contiguous()
+            or xs.shape != (-(-xshape[0] // 128), -(-2 * xshape[1] // tile), 512)
+            or ws.shape != (-(-wshape[0] // 128), -(-2 * wshape[1] // tile), 512)
+            or xq.get_device() != device or xs.get_device() != device or wq.get_device() != device
+            or ws.get_device() != device or out is not None
+            or (a is not None and (a.get_device() != device or fmt != "nvfp4" or a.dtype is not f32 or a.numel() != 1
+                                   or a.requires_grad))
+            or (w is not None and (w.get_device() != device or fmt != "nvfp4" or w.dtype is not f32 or w.numel() != 1
+                                   or w.requires_grad))):
+        _packed("xq", xq, xs, fmt)
+        _packed("wq", wq, ws, fmt)
+        if xshape[1] != wshape[1]:
+            _fail(f"xq has {2 * xshape[1]} columns, wq {2 * wshape[1]}")
+        _scale("x_scale", a, fmt)
+        _scale("w_scale", w, fmt)
+        _device(xq, xs, wq, ws, a, w, out)
+        _out(out, dtype, (xshape[0], wshape[0]))
+    M, N = xshape[0], wshape[0]
     if out is None:
-        out = _empty((M, N), xq, stream, dtype or torch.bfloat16)
-    else:
-        _contiguous("out", out, (M, N), dtype)
-    binding.sgq_fp4_gemm(xq, xs, x_scale, wq, ws, w_scale, out, M, N, K, f, _dtype(out), stream)
+        out = _new((M, N), dtype, xq, stream)
+    _done(binding.load_library().sgq_fp4_gemm(xq.data_ptr(), xs.data_ptr(), a if a is None else a.data_ptr(), wq.data_ptr(), ws.data_ptr(),
+                                              w if w is None else w.data_ptr(), out.data_ptr(), M, N, 2 * xshape[1], f, dt,
+                                              device_stream[1]), "sgq_fp4_gemm")
     return out

@@ -9,8 +9,8 @@ that requires a gradient while gradients are recorded: none is here.
 from __future__ import annotations
 
 from . import binding
-from .fp4 import _scale, _tiles
-from .latent import _contiguous, _device, _dtype, _empty, _fail, _strides
+from .fp4 import _current, _done, _FORMAT, _new, _number, _scale
+from .latent import _contiguous, _device, _dtype, _fail
 
 
 def _target(x, M, K, quant, group, ue8m0, tensor_scale, out, out_scales, stream):
@@ -20,18 +20,21 @@ def _target(x, M, K, quant, group, ue8m0, tensor_scale, out, out_scales, stream)
         if tensor_scale is not None or out_scales is not None or ue8m0:
             _fail("tensor_scale, out_scales and ue8m0 go with quant")
         if out is None:
-            return binding.SGQ_OUT_16, _empty((M, K), x, stream), None
+            return binding.SGQ_OUT_16, _new((M, K), x.dtype, x, stream), None
         _contiguous("out", out, (M, K), x.dtype)
+        _dtype(out)
         return binding.SGQ_OUT_16, out, None
-    if quant in ("mxfp4", "nvfp4"):
+    u8 = torch.uint8
+    if quant in _FORMAT:
         if ue8m0:
             _fail("ue8m0 goes with quant='fp8'")
         if K % 32:
             _fail(f"{K} columns are not whole groups of 32")
-        _scale("tensor_scale", tensor_scale, quant)
+        if tensor_scale is not None:
+            _scale("tensor_scale", tensor_scale, quant)
         kind = binding.SGQ_OUT_MXFP4 if quant == "mxfp4" else binding.SGQ_OUT_NVFP4
-        shapes, types = ((M, K // 2), _tiles(M, K, quant)), (torch.uint8, torch.uint8)
-    elif quant in ("fp8", "fp8_ue8m0"):
+        shape, scales, kept = (M, K // 2), (-(-M // 128), -(-K // _FORMAT[quant][1]), 512), u8
+    elif quant == "fp8" or quant == "fp8_ue8m0":
         if tensor_scale is not None:
             _fail("tensor_scale goes with quant='nvfp4'")
         if group not in (32, 128) or K % group:
@@ -40,33 +43,30 @@ def _target(x, M, K, quant, group, ue8m0, tensor_scale, out, out_scales, stream)
             _fail("ue8m0 goes with quant='fp8': 'fp8_ue8m0' writes the scales as bytes")
         kind = binding.SGQ_OUT_FP8 | (binding.SGQ_OUT_GROUP_128 if group == 128 else 0)
         kind |= binding.SGQ_OUT_UE8M0 if quant == "fp8_ue8m0" else binding.SGQ_OUT_POW2 if ue8m0 else 0
-        shapes = (M, K), (M, K // group)
-        types = torch.uint8, torch.uint8 if quant == "fp8_ue8m0" else torch.float32
+        shape, scales, kept = (M, K), (M, K // group), u8 if quant == "fp8_ue8m0" else torch.float32
     else:
         _fail(f"quant: {quant!r} is none of None, 'fp8', 'fp8_ue8m0', 'mxfp4', 'nvfp4'")
     if out is None:
-        out = _empty(shapes[0], x, stream, types[0])
+        out = _new(shape, u8, x, stream)
     else:
-        _contiguous("out", out, shapes[0], types[0])
+        _contiguous("out", out, shape, u8)
     if out_scales is None:
-        out_scales = _empty(shapes[1], x, stream, types[1])
+        out_scales = _new(scales, kept, x, stream)
     else:
-        _contiguous("out_scales", out_scales, shapes[1], types[1])
+        _contiguous("out_scales", out_scales, scales, kept)
     return kind, out, out_scales
 
 
 def _rows(name, t, M, K):
-    """The row stride of a [M, K] tensor."""
+    """Whether t is [M, K], each row contiguous."""
     if t.dim() != 2 or t.shape[0] != M or t.shape[1] != K:
         _fail(f"{name}: expected [{M}, {K}], got {tuple(t.shape)}")
-    s, = _strides(name, t, 2)
-    return s if M > 1 else K
+    if t.stride(1) != 1 and K > 1:
+        _fail(f"{name}: the last dimension is not contiguous")
 
 
-def _grads(t):
-    import torch
-    if t is not None and t.requires_grad and torch.is_grad_enabled():
-        _fail("tensor_scale requires a gradient, and none is recorded here")
+def _vector(name, t, K):
+    _contiguous(name, t, (K,))
 
 
 def rms_norm(x, weight, eps: float = 1e-6, offset: float = 0.0, quant=None, group: int = 128, ue8m0: bool = False,
@@ -77,17 +77,26 @@ def rms_norm(x, weight, eps: float = 1e-6, offset: float = 0.0, quant=None, grou
     (ue8m0: powers of two); "fp8_ue8m0": scales as bytes; "mxfp4", "nvfp4": (codes, scale tiles) as ``quant_fp4`` gives
     them, with tensor_scale.  y is not rounded to 16 bits before it is quantised.  out, out_scales: outputs to write to.
     """
-    dt = _dtype(x, weight)
-    if x.dim() != 2:
-        _fail(f"x: expected [M, K], got {tuple(x.shape)}")
-    M, K = x.shape
-    xt = _rows("x", x, M, K)
-    _contiguous("weight", weight, (K,))
-    _grads(tensor_scale)
-    _device(x, weight, tensor_scale, out, out_scales)
-    kind, y, ys = _target(x, M, K, quant, group, ue8m0, tensor_scale, out, out_scales, stream)
-    binding.sgq_norm(x, xt, None, None, 0, 0, None, 0, None, 0, weight, M, K, eps, offset, 1.0, 1.0, dt, kind, tensor_scale,
-                     y, ys, stream)
+    import torch
+    device, handle = _current(stream)
+    t, kept = tensor_scale, x.dtype
+    dt, shape, strides = _number(kept), x.shape, x.stride()
+    if (dt is None or len(shape) != 2 or strides[1] != 1 or weight.dtype is not kept or weight.shape != shape[1:]
+            or not weight.is_contiguous() or x.get_device() != device or weight.get_device() != device
+            or t is not None or out is not None or out_scales is not None
+            or (torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad))):
+        dt = _dtype(x, weight)
+        if x.dim() != 2:
+            _fail(f"x: expected [M, K], got {tuple(x.shape)}")
+        _rows("x", x, *shape)
+        _vector("weight", weight, shape[1])
+        _device(x, weight, t, out, out_scales)
+    M, K = shape
+    kind, y, ys = _target(x, M, K, quant, group, ue8m0, t, out, out_scales, stream)
+    _done(binding.load_library().sgq_norm(
+        x.data_ptr(), strides[0] if M > 1 else K, None, None, 0, 0, None, 0, None, 0, weight.data_ptr(), M, K, eps, offset, 1.0,
+        1.0, dt, kind, None if t is None else t.data_ptr(), y.data_ptr(), None if ys is None else ys.data_ptr(), handle),
+        "sgq_norm")
     return y if ys is None else (y, ys)
 
 
@@ -100,13 +109,31 @@ def norm_add(x, residual, post_weight=None, gate=None, scale: float = 1.0, resid
     y = the norm of h, as ``rms_norm`` gives it.  gate: [K], or [G, K], each row for M/G consecutive rows of x.  h_out:
     where h goes (it may be residual, or x).  Returns h without weight, else (h, y) or (h, codes, scales).
     """
-    dt = _dtype(x, residual, post_weight, gate, weight, h_out)
-    if x.dim() != 2:
-        _fail(f"x: expected [M, K], got {tuple(x.shape)}")
-    M, K = x.shape
-    xt, rt = _rows("x", x, M, K), _rows("residual", residual, M, K)
-    if post_weight is not None:
-        _contiguous("post_weight", post_weight, (K,))
+    import torch
+    device, handle = _current(stream)
+    t, p, w, kept, graded = tensor_scale, post_weight, weight, x.dtype, torch.is_grad_enabled()
+    dt, shape, strides = _number(kept), x.shape, x.stride()
+    if (dt is None or len(shape) != 2 or strides[1] != 1 or residual.dtype is not kept or residual.shape != shape
+            or residual.stride(1) != 1 or x.get_device() != device or residual.get_device() != device
+            or (graded and (x.requires_grad or residual.requires_grad))
+            or (p is not None and (p.dtype is not kept or p.shape != shape[1:] or not p.is_contiguous()
+                                   or p.get_device() != device or (graded and p.requires_grad)))
+            or (w is not None and (w.dtype is not kept or w.shape != shape[1:] or not w.is_contiguous()
+                                   or w.get_device() != device or (graded and w.requires_grad)))
+            or gate is not None or t is not None or h_out is not None or out is not None or out_scales is not None):
+        dt = _dtype(x, residual, p, gate, w, h_out)
+        if x.dim() != 2:
+            _fail(f"x: expected [M, K], got {tuple(shape)}")
+        _rows("x", x, *shape)
+        _rows("residual", residual, *shape)
+        if p is not None:
+            _vector("post_weight", p, shape[1])
+        if w is not None:
+            _vector("weight", w, shape[1])
+        if h_out is not None:
+            _rows("h_out", h_out, *shape)
+        _device(x, residual, p, gate, w, t, h_out, out, out_scales)
+    M, K = shape
     gs = rows = 0
     if gate is not None:
         if gate.dim() == 1:
@@ -114,20 +141,21 @@ def norm_add(x, residual, post_weight=None, gate=None, scale: float = 1.0, resid
         G = gate.shape[0]
         if gate.dim() != 2 or gate.shape[1] != K or (M % G if G else M):
             _fail(f"gate: expected [K] or [G, K] with G dividing {M}, got {tuple(gate.shape)}")
-        (gs,), rows = _strides("gate", gate, 2), M // G if M else 1
-        gs = gs if G > 1 else K
-    _grads(tensor_scale)
-    _device(x, residual, post_weight, gate, weight, tensor_scale, h_out, out, out_scales)
+        _rows("gate", gate, G, K)
+        gs, rows = gate.stride(0) if G > 1 else K, M // G if M else 1
     if h_out is None:
-        h_out, ht = _empty((M, K), x, stream), K
+        h_out, ht = _new(shape, kept, x, stream), K
     else:
-        ht = _rows("h_out", h_out, M, K)
+        ht = h_out.stride(0) if M > 1 else K
     kind, y, ys = binding.SGQ_OUT_NONE, None, None
-    if weight is not None:
-        _contiguous("weight", weight, (K,))
-        kind, y, ys = _target(x, M, K, quant, group, ue8m0, tensor_scale, out, out_scales, stream)
-    elif quant is not None or out is not None or out_scales is not None or tensor_scale is not None:
+    if w is not None:
+        kind, y, ys = _target(x, M, K, quant, group, ue8m0, t, out, out_scales, stream)
+    elif quant is not None or out is not None or out_scales is not None or t is not None:
         _fail("quant, out, out_scales and tensor_scale go with weight")
-    binding.sgq_norm(x, xt, post_weight, gate, gs, rows, residual, rt, h_out, ht, weight, M, K, eps, offset, scale,
-                     residual_scale, dt, kind, tensor_scale, y, ys, stream)
+    _done(binding.load_library().sgq_norm(
+        x.data_ptr(), strides[0] if M > 1 else K, None if p is None else p.data_ptr(),
+        None if gate is None else gate.data_ptr(), gs, rows, residual.data_ptr(), residual.stride(0) if M > 1 else K,
+        h_out.data_ptr(), ht, None if w is None else w.data_ptr(), M, K, eps, offset, scale, residual_scale, dt, kind,
+        None if t is None else t.data_ptr(), None if y is None else y.data_ptr(), None if ys is None else ys.data_ptr(), handle),
+        "sgq_norm")
     return h_out if y is None else (h_out, y) if ys is None else (h_out, y, ys)
