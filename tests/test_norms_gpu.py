@@ -1,0 +1,197 @@
+"""Fused norms on the GPU against 64 bits."""
+import numpy as np
+import pytest
+import torch
+
+import fp8_block_scaled_sgq_gb300 as sgq
+import fp4_ref as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+TYPES = pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+
+
+def ok():
+    torch.cuda.synchronize()
+    assert sgq.sgq_device_status() == 0
+
+
+def randn(*shape, seed=0, dtype=torch.bfloat16, std=1.0, mean=0.0):
+    g = torch.Generator("cpu").manual_seed(seed)
+    return (torch.randn(*shape, generator=g) * std + mean).to(dtype).to(DEV)
+
+
+def check_rounded(got, want, mag, dtype, what):
+    """got: want rounded once, after fp32 arithmetic on terms of magnitude mag."""
+    tol = ref.UNIT[dtype] * np.abs(want) + ref.NORM * mag + (2.0 ** -25 if dtype == torch.float16 else 0.0)
+    err = np.abs(ref.f64(got) - want)
+    assert np.isfinite(ref.f64(got)).all() and (err <= tol).all(), f"{what}: off by {(err - tol).max()} past the bound"
+
+
+def check_fp8(codes, scales, y, group, kind, what):
+    """FP8 groups of values that are within NORM of y."""
+    q = codes.cpu().view(torch.float8_e4m3fn).float().numpy().astype(np.float64)
+    part = np.abs(y).reshape(y.shape[0], -1, group)
+    amax = np.maximum(part.max(axis=-1), 1e-10) / 448
+    if kind == "bytes":
+        s = 2.0 ** (scales.cpu().numpy().astype(np.float64) - 127)
+    else:
+        s = ref.f64(scales)
+    if kind == "fp32":
+        assert (np.abs(s - amax) <= (ref.NORM + 2.0 ** -23) * amax).all(), f"{what}: scales"
+    else:
+        lo, hi = (2.0 ** np.ceil(np.log2(amax * f)) for f in (1 - 2 * ref.NORM, 1 + 2 * ref.NORM))
+        assert ((s >= lo) & (s <= hi)).all(), f"{what}: scales"
+    big = np.repeat(s, group, axis=1)
+    tol = np.maximum(np.abs(y) * 2.0 ** -4, big * 2.0 ** -10) + 4 * ref.NORM * np.abs(y)     # half a step of E4M3
+    assert (np.abs(q * big - y) <= tol).all(), f"{what}: codes"
+
+
+def run(M, K, dtype, add, post, gate, quant, group=128, ue8m0=False, offset=0.0, eps=1e-6, strided=False, in_place=None, seed=0):
+    wide = K + 64 if strided else K
+    x, r = randn(M, wide, seed=seed, dtype=dtype)[:, :K], randn(M, wide, seed=seed + 1, dtype=dtype, std=3.0)[:, wide - K:]
+    w, p = (randn(K, seed=seed + s, dtype=dtype, std=0.2, mean=1.0 - offset) for s in (2, 3))
+    G = {"none": 0, "all": 1, "token": M, "some": next(d for d in (7, 5, 4, 3, 2, 1) if M % d == 0)}[gate]
+    g = randn(G, K, seed=seed + 4, dtype=dtype) if G else None
+    t = torch.full((1,), 0.0021, device=DEV) if quant == "nvfp4" else None
+    kw = dict(eps=eps, offset=offset, quant=quant, tensor_scale=t)
+    if quant and quant.startswith("fp8"):
+        kw.update(group=group, ue8m0=ue8m0)
+    x0, r0 = ref.f64(x), ref.f64(r)
+    if not add:
+        got = sgq.rms_norm(x, w, **kw)
+        h, got = x0, got if quant else (got,)
+    else:
+        out = {None: None, "residual": r, "x": x}[in_place]
+        res = sgq.norm_add(x, r, post_weight=p if post else None, gate=g, scale=0.75, residual_scale=1.5, weight=w, h_out=out, **kw)
+        assert in_place is None or res[0] is out
+        ok()
+        u, mag = (ref.norm(x0, ref.f64(p), eps, offset),) * 2 if post else (x0, x0)
+        if G:
+            u = u * ref.f64(g)[np.arange(M) * G // M]
+        want = 1.5 * r0 + 0.75 * u
+        check_rounded(res[0], want, np.abs(1.5 * r0) + np.abs(0.75 * u), dtype, "h")
+        h, got = ref.f64(res[0]), res[1:]
+        if in_place != "x":
+            assert np.array_equal(ref.f64(x), x0)
+        if in_place != "residual":
+            assert np.array_equal(ref.f64(r), r0)
+    ok()
+    y = ref.norm(h, ref.f64(w), eps, offset)
+    what = f"{M}x{K} {quant}"
+    if quant is None:
+        check_rounded(got[0], y, np.abs(y), dtype, what)
+    elif quant.startswith("fp8"):
+        check_fp8(got[0], got[1], y, group, "bytes" if quant == "fp8_ue8m0" else "pow2" if ue8m0 else "fp32", what)
+    else:
+        ref.check_codes(ref.unpack(got[0]), ref.from_tiles(got[1], M, K // ref.GROUP[quant]), y, quant,
+                        np.float32(0.0021) if t is not None else np.float32(1), ref.NORM, what)
+        pad = ref.from_tiles(got[1], M, got[1].shape[1] * 4)[:, K // ref.GROUP[quant]:]
+        assert (pad == 0).all()
+
+
+#: Widths at the kernels' borders (a warp a row up to 1024, a CTA up to 32768, walking CTAs from 305 rows on), odd ones.
+WIDTHS = [8, 24, 1024, 1032, 1544, 2048, 2056, 4104, 7168, 8200, 16384, 16392, 32768]
+
+
+@TYPES
+@pytest.mark.parametrize("K", WIDTHS)
+@pytest.mark.parametrize("M", [1, 6, 611])
+def test_norm_of_every_width(dtype, K, M):
+    if M * K > 6_000_000:
+        M = 333 if K <= 16384 else 310
+    run(M, K, dtype, False, False, "none", None, offset=1.0)
+    run(M, K, dtype, True, True, "some", None)
+
+
+@pytest.mark.parametrize("M", [2, 400])
+@pytest.mark.parametrize("add,post,gate", [(False, False, "none"), (True, False, "none"), (True, True, "none"), (True, False, "token"),
+                                           (True, True, "all"), (True, True, "some")])
+@pytest.mark.parametrize("quant,kw", [(None, {}), ("fp8", dict(group=128)), ("fp8", dict(group=32)), ("fp8", dict(group=32, ue8m0=True)),
+                                      ("fp8_ue8m0", dict(group=128)), ("fp8_ue8m0", dict(group=32)), ("mxfp4", {}), ("nvfp4", {})])
+def test_every_step_and_form(M, add, post, gate, quant, kw):
+    for K in (896, 1536, 4224):
+        run(M, K, torch.bfloat16 if K != 1536 else torch.float16, add, post, gate, quant, **kw)
+
+
+@pytest.mark.parametrize("quant", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("K", [32, 96, 1056, 7200, 32768])
+@pytest.mark.parametrize("M", [3, 320])
+def test_four_bits_of_ragged_rows(quant, K, M):
+    run(M, K, torch.bfloat16, True, False, "none", quant)
+
+
+@pytest.mark.parametrize("M", [5, 700])
+@pytest.mark.parametrize("in_place", [None, "residual", "x"])
+def test_rows_apart_and_in_place(M, in_place):
+    for K in (512, 1544, 7168):
+        run(M, K, torch.bfloat16, True, True, "some", None, strided=True, in_place=in_place)
+
+
+@pytest.mark.parametrize("M,K", [(3, 256), (400, 2304)])
+def test_same_codes_as_the_quantisers_on_exact_values(M, K):
+    """Rows of +-1 and zeros with weights that are powers of two: with eps 0 the norm is exact where half the row is zero
+    (mean 1/4: 1/sqrt is 2), so that it gives what the quantisers give for the same values."""
+    sign = (torch.randint(0, 2, (M, K), generator=torch.Generator().manual_seed(1)) * 2 - 1).bfloat16()
+    sign[:, ::4], sign[:, 1::4], sign[:, 2::4] = 0, 0, 0
+    x, w = sign.to(DEV), (2.0 ** torch.randint(-3, 4, (K,)).float()).bfloat16().to(DEV)
+    y = sgq.rms_norm(x, w, eps=0.0)
+    assert torch.equal(y, 2 * x * w)
+    for quant, other in (("fp8", lambda: sgq.quant_token_group(y, 128, False)), ("fp8_ue8m0", lambda: sgq.quant_token_group_ue8m0(y, 128)),
+                         ("mxfp4", lambda: sgq.quant_fp4(y, "mxfp4")), ("nvfp4", lambda: sgq.quant_fp4(y, "nvfp4"))):
+        a, b = sgq.rms_norm(x, w, eps=0.0, quant=quant), other()
+        G = K // (ref.GROUP.get(quant, 128))
+        assert torch.equal(a[0], b[0]), quant
+        if quant in ref.GROUP:
+            assert np.array_equal(ref.from_tiles(a[1], M, G), ref.from_tiles(b[1], M, G))
+        else:
+            assert torch.equal(a[1], b[1])
+    ok()
+
+
+@pytest.mark.parametrize("M", [4, 600])
+def test_rows_that_are_not_finite_and_rows_of_zeros(M):
+    K = 2048
+    x = randn(M, K, seed=3)
+    x[0, 5], x[1, 7], x[2] = float("nan"), float("inf"), 0
+    w = torch.ones(K, dtype=torch.bfloat16, device=DEV)
+    y = sgq.rms_norm(x, w)
+    assert torch.isnan(y[0]).all() and torch.isnan(y[1, 7]) and (y[2] == 0).all() and torch.isfinite(y[3:]).all()
+    assert (sgq.rms_norm(x[2:3], w, eps=0.0).isnan()).all()        # 0 / 0
+    q, s = sgq.rms_norm(x, w, quant="mxfp4")
+    v = sgq.dequant_fp4(q, s, "mxfp4")
+    assert torch.isnan(v[0]).all() and (v[2] == 0).all() and torch.isfinite(v[3:]).all()
+    ok()
+
+
+def test_outputs_between_guards():
+    """Given outputs are written to their borders and not past them."""
+    for M, K in ((3, 96), (310, 1120)):
+        x, r, w = randn(M, K, seed=1), randn(M, K, seed=2), randn(K, seed=3, mean=1.0)
+        want = sgq.norm_add(x, r, weight=w, quant="nvfp4")
+        hb = torch.full((M * K + 64,), 7.0, dtype=torch.bfloat16, device=DEV)
+        T = want[2].shape
+        qb, sb = (torch.full((n + 64,), 0xA5, dtype=torch.uint8, device=DEV) for n in (M * K // 2, T.numel()))
+        got = sgq.norm_add(x, r, weight=w, quant="nvfp4", h_out=hb[32:-32].view(M, K), out=qb[32:-32].view(M, K // 2),
+                           out_scales=sb[32:-32].view(T))
+        ok()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        G = T[1] * 4
+        assert np.array_equal(ref.from_tiles(got[2], M, G), ref.from_tiles(want[2], M, G))
+        for b, v in ((hb, 7.0), (qb, 0xA5), (sb, 0xA5)):
+            assert (b[:32] == v).all() and (b[-32:] == v).all()
+
+
+def test_feeds_the_fp8_linear():
+    """The norm's FP8 groups are what the block-scaled GEMM reads: the same D as from quantising what they stand for."""
+    M, N, K = 64, 512, 2048
+    x, w, n = randn(M, K, seed=1), randn(N, K, seed=2, std=0.02), randn(K, seed=3, std=0.1, mean=1.0)
+    wq, ws = sgq.quant_weight_block(w, 128, 128, True)
+    torch.cuda.synchronize()
+    q, s = sgq.rms_norm(x, n, quant="fp8", group=128, ue8m0=True)
+    d = sgq.fp8_block_gemm(q, s, wq, ws, 128, 128)
+    ok()
+    a = q.cpu().view(torch.float8_e4m3fn).double().numpy() * np.repeat(ref.f64(s), 128, axis=1)
+    b = wq.cpu().view(torch.float8_e4m3fn).double().numpy() * np.repeat(np.repeat(ref.f64(ws), 128, axis=1), 128, axis=0)[:N]
+    want, mag = a @ b.T, np.abs(a) @ np.abs(b).T
+    assert (np.abs(ref.f64(d) - want) <= 2.0 ** -8 * np.abs(want) + 1e-4 * mag).all()
