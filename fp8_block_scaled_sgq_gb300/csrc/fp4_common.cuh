@@ -105,14 +105,10 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits, float t, floa
 // System/6000 processor", 1990, theorem on the last step of a division).  On
 // negated values so that a zero keeps its sign.  Remainders are exact while
 // nothing leaves fp32's normal range: other divisors take the division itself.
-__device__ __forceinline__ void divide8(const float (&n)[8], float d, float (&q)[8]) {
-    if (!(d >= 0x1p-60f && d <= 0x1p100f)) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(-n[i], d);
-        return;
-    }
-    const float r = -__frcp_rn(d);
-    const float2 r2 = make_float2(r, r), d2 = make_float2(d, d);
+__device__ __forceinline__ bool in_range(float d) { return d >= 0x1p-60f && d <= 0x1p100f; }
+// minus_r = -1/d rounded, d in range
+__device__ __forceinline__ void divide8(const float (&n)[8], float d, float minus_r, float (&q)[8]) {
+    const float2 r2 = make_float2(minus_r, minus_r), d2 = make_float2(d, d);
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
         const float2 n2 = make_float2(n[i], n[i + 1]);
@@ -121,6 +117,14 @@ __device__ __forceinline__ void divide8(const float (&n)[8], float d, float (&q)
         x = lat::fma2(lat::fma2(x, d2, n2), r2, x);
         q[i] = x.x;
         q[i + 1] = x.y;
+    }
+}
+__device__ __forceinline__ void divide8(const float (&n)[8], float d, float (&q)[8]) {
+    if (in_range(d)) {
+        divide8(n, d, -__frcp_rn(d), q);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(-n[i], d);
     }
 }
 // Eight values of a group, negated -> codes.  div == 0: the group is not finite.

@@ -121,54 +121,116 @@ __device__ __forceinline__ float fp8_scale(float amax, bool pow2) {
     return s;
 }
 
-// Column c of row m of y, in what `out` asks for.  v: its values, negated where
-// they are to be quantised (divide8).  All lanes of a warp call it, those past
-// the row's end (in == false) too: groups lie in neighbouring lanes, and are
-// whole.
-template <typename T, Out kOut>
-__device__ __forceinline__ void emit(const Args& a, int64_t m, int c, bool in, const float (&v)[8], float t, float t6) {
+// One column of eight values to be quantised, negated (divide8) -> its codes.
+template <Out kOut>
+__device__ __forceinline__ void store_codes(const Args& a, int64_t at, const float (&q)[8]) {
+    if constexpr (kOut == kFp8) {
+        uint32_t p[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            p[j] = __nv_cvt_float2_to_fp8x2(make_float2(q[2 * j], q[2 * j + 1]), __NV_SATFINITE, __NV_E4M3);
+        static_cast<uint2*>(a.y)[at] = make_uint2(p[0] | (p[1] << 16), p[2] | (p[3] << 16));
+    } else {
+        static_cast<uint32_t*>(a.y)[at] = codes8(q);
+    }
+}
+
+// Columns tid, tid + step, ... of row m of y, in what `out` asks for.  v: their
+// values, negated where they are to be quantised.  All lanes of a warp call
+// it, those past the row's end (zeros) too: groups lie in neighbouring lanes,
+// and are whole.
+//
+// A group's largest magnitude, its scale and the reciprocal of it are the same
+// for all of its lanes, so they are taken once: lanes that meet in the maximum
+// over a group each keep half of the columns, until a lane owns one (two of
+// four where a group is two lanes), and hand the quotients' factors back.
+template <typename T, Out kOut, int kVec>
+__device__ __forceinline__ void emit(const Args& a, int64_t m, int tid, int step, const float (&v)[kVec][8], float t, float t6) {
     const int cols = a.K / 8;
     if constexpr (kOut == kSame) {
-        if (in) static_cast<uint4*>(a.y)[m * cols + c] = pack8<T>(v);
-    } else if constexpr (kOut == kFp8) {
-        float amax = in ? qm::amax8(v) : 0.0f;
-        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-        if (a.group_shift == 4) {
-            amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 4));
-            amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 8));
-        }
-        const float s = fp8_scale(amax, a.scale_kind != 0);
-        if (in) {
-            float q[8];
-            divide8(v, s, q);
-            uint32_t p[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                p[j] = __nv_cvt_float2_to_fp8x2(make_float2(q[2 * j], q[2 * j + 1]), __NV_SATFINITE, __NV_E4M3);
-            static_cast<uint2*>(a.y)[m * cols + c] = make_uint2(p[0] | (p[1] << 16), p[2] | (p[3] << 16));
-            if ((c & ((1 << a.group_shift) - 1)) == 0) {
-                const int64_t g = m * (cols >> a.group_shift) + (c >> a.group_shift);
-                if (a.scale_kind == 2) static_cast<uint8_t*>(a.ys)[g] = static_cast<uint8_t>(__float_as_uint(s) >> 23);
-                else static_cast<float*>(a.ys)[g] = s;
+        for (int i = 0; i < kVec; ++i)
+            if (tid + i * step < cols) static_cast<uint4*>(a.y)[m * cols + tid + i * step] = pack8<T>(v[i]);
+    } else {
+        constexpr unsigned kAll = 0xFFFFFFFFu;
+        constexpr bool kNv = kOut == kNv4;
+        constexpr int kOwn = kNv ? kVec / 2 : 1;
+        static_assert(kVec == 2 || kVec == 4, "columns a thread");
+        const int lane = threadIdx.x & 31;
+        const bool odd1 = (lane & 1) != 0, odd2 = (lane & 2) != 0;
+        uint32_t top[kVec], own[2];
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) top[i] = amax_bits8(v[i]);
+        int first;   // the first column that this lane owns
+        if constexpr (kVec == 4) {
+            own[0] = max(odd1 ? top[2] : top[0], __shfl_xor_sync(kAll, odd1 ? top[0] : top[2], 1));
+            own[1] = max(odd1 ? top[3] : top[1], __shfl_xor_sync(kAll, odd1 ? top[1] : top[3], 1));
+            first = odd1 ? 2 : 0;
+            if constexpr (!kNv) {
+                own[0] = max(odd2 ? own[1] : own[0], __shfl_xor_sync(kAll, odd2 ? own[0] : own[1], 2));
+                first += odd2 ? 1 : 0;
+            }
+        } else {
+            own[0] = max(odd1 ? top[1] : top[0], __shfl_xor_sync(kAll, odd1 ? top[0] : top[1], 1));
+            first = odd1 ? 1 : 0;
+            if constexpr (!kNv) own[0] = max(own[0], __shfl_xor_sync(kAll, own[0], 2));
+        }
+        if (kOut == kFp8 && a.group_shift == 4) {
+            own[0] = max(own[0], __shfl_xor_sync(kAll, own[0], 4));
+            own[0] = max(own[0], __shfl_xor_sync(kAll, own[0], 8));
+        }
+        float div[kOwn], rcp[kOwn];
+        bool plain = true;   // the quotients are products (divide8)
+#pragma unroll
+        for (int k = 0; k < kOwn; ++k) {
+            const int c = tid + (first + k) * step;
+            if constexpr (kOut == kFp8) {
+                const float s = fp8_scale(__uint_as_float(own[k]), a.scale_kind != 0);
+                div[k] = s;
+                // the first lanes of a group, one for each column
+                if (c < cols && (lane & ((1 << a.group_shift) - 1)) < kVec) {
+                    const int64_t g = m * (cols >> a.group_shift) + (c >> a.group_shift);
+                    if (a.scale_kind == 2) static_cast<uint8_t*>(a.ys)[g] = static_cast<uint8_t>(__float_as_uint(s) >> 23);
+                    else static_cast<float*>(a.ys)[g] = s;
+                }
+            } else {
+                constexpr int kLanes = kNv ? 2 : 4;   // a group's; a scale word's are four times as many
+                uint32_t byte = scale_byte<kNv>(own[k], t, t6, div[k]);
+                if (c >= cols) byte = 0;              // groups past the row's end
+                byte |= __shfl_down_sync(kAll, byte, kLanes) << 8;
+                byte |= __shfl_down_sync(kAll, byte, 2 * kLanes) << 16;
+                if (c < cols && (lane & (4 * kLanes - 1)) < (kNv ? 2 : kVec))
+                    *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.ys) +
+                                                 scale_word_at(m, c / (4 * kLanes), scale_tiles(a.K, kNv))) = byte;
+            }
+            if constexpr (kOut == kMx4) {
+                rcp[k] = -__uint_as_float((254u - (__float_as_uint(div[k]) >> 23)) << 23);
+                plain &= div[k] != 0.0f;
+            } else {
+                rcp[k] = -__frcp_rn(div[k]);
+                plain &= in_range(div[k]);
             }
         }
-    } else {
-        constexpr bool kNv = kOut == kNv4;
-        constexpr int kLanes = kNv ? 2 : 4;   // a group's
-        uint32_t amax = in ? amax_bits8(v) : 0u;
-        amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-        if constexpr (!kNv) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-        float div;
-        uint32_t byte = scale_byte<kNv>(amax, t, t6, div);
-        if (!in) byte = 0;
-        byte |= __shfl_down_sync(0xFFFFFFFFu, byte, kLanes) << 8;
-        byte |= __shfl_down_sync(0xFFFFFFFFu, byte, 2 * kLanes) << 16;
-        if (in) {
-            static_cast<uint32_t*>(a.y)[m * cols + c] = encode8<kNv>(v, div);
-            if (c % (4 * kLanes) == 0)
-                *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.ys) +
-                                             scale_word_at(m, c / (4 * kLanes), scale_tiles(a.K, kNv))) = byte;
+        const bool all_plain = __all_sync(kAll, plain);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+            const int c = tid + i * step;
+            const int from = kVec == 2 ? (lane & ~1) | i : kNv ? (lane & ~1) | (i >> 1) : (lane & ~3) | (i >> 1) | ((i & 1) << 1);
+            const int k = kVec == 4 && kNv ? i & 1 : 0;
+            const float r = __shfl_sync(kAll, rcp[k], from), d = __shfl_sync(kAll, div[k], from);
+            float q[8];
+            if (all_plain) {
+                if constexpr (kOut == kMx4) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) set(q, j, lat::mul2(two(v[i], j), make_float2(r, r)));
+                } else {
+                    divide8(v[i], d, r, q);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) q[j] = kOut != kFp8 && d == 0.0f ? 0.0f : __fdiv_rn(-v[i][j], d);
+            }
+            if (c < cols) store_codes<kOut>(a, m * cols + c, q);
         }
     }
 }
@@ -232,11 +294,9 @@ __global__ void __launch_bounds__(kRow == 32 ? 128 : kRow) norm_kernel(const Arg
         float t, t6;
         tensor_scale_of<kOut>(a, t, t6);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-            const int c = tid + i * kRow;
-            if (c < cols) weigh<T>(v[i], rstd, column<T>(a.weight, 0, c), a.offset);
-            emit<T, kOut>(a, m, c, c < cols, v[i], t, t6);
-        }
+        for (int i = 0; i < kVec; ++i)
+            if (tid + i * kRow < cols) weigh<T>(v[i], rstd, column<T>(a.weight, 0, tid + i * kRow), a.offset);
+        emit<T, kOut, kVec>(a, m, tid, kRow, v, t, t6);
     }
 }
 
@@ -265,8 +325,8 @@ __device__ __forceinline__ float block_sum(float s, float* part) {
     return __shfl_sync(0xFFFFFFFFu, s, 0);   // (at most 16 warps)
 }
 
-template <typename T, int kVec, Out kOut>
-__global__ void __launch_bounds__(kVec == 2 ? 128 : 512, kVec == 2 ? 6 : 1) norm_walk_kernel(const Args a) {
+template <typename T, int kThreads, int kVec, int kCtas, Out kOut>
+__global__ void __launch_bounds__(kThreads, kCtas) norm_walk_kernel(const Args a) {
     extern __shared__ uint4 ring[];
     __shared__ float part[4][32];
     ptx::launch_dependents();
@@ -338,23 +398,20 @@ __global__ void __launch_bounds__(kVec == 2 ? 128 : 512, kVec == 2 ? 6 : 1) norm
         if constexpr (kOut != kNone) {
             if constexpr (negated(kOut)) rstd = -rstd;
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) {
-                const int c = tid + i * threads;
-                weigh<T>(v[i], rstd, weight[i], a.offset);
-                emit<T, kOut>(a, m, c, c < cols, v[i], t, t6);
-            }
+            for (int i = 0; i < kVec; ++i) weigh<T>(v[i], rstd, weight[i], a.offset);
+            emit<T, kOut, kVec>(a, m, tid, threads, v, t, t6);
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-template <typename T, int kVec, Out kOut>
+template <typename T, int kThreads, int kVec, int kCtas, Out kOut>
 sgq_status walk(Args a, int sms, cudaStream_t st) {
     const int cols = a.K / 8, threads = (cols + 32 * kVec - 1) / (32 * kVec) * 32;
-    const int ctas = (kVec == 2 ? 768 : 512) / threads, share = 208 * 1024 / ctas;
+    const int ctas = kThreads * kCtas / threads, share = 208 * 1024 / ctas;
     const int row_bytes = (1 + (a.residual != nullptr) + (a.gate != nullptr)) * kVec * threads * 16;
     a.depth = share / row_bytes < 4 ? share / row_bytes : 4;
-    auto kern = norm_walk_kernel<T, kVec, kOut>;
+    auto kern = norm_walk_kernel<T, kThreads, kVec, kCtas, kOut>;
     static bool configured[64] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SGQ_ERR_CUDA;
@@ -396,7 +453,8 @@ template <typename T, Out kOut>
 sgq_status by_width(const Args& a, int sms, cudaStream_t st) {
     // More rows than a grid that fills the SMs twice: CTAs walk.
     const bool many = a.K > 1024 && a.K <= 16384 && a.M > int64_t(sms) * 2;
-    if (many) return a.K <= 2048 ? walk<T, 2, kOut>(a, sms, st) : walk<T, 4, kOut>(a, sms, st);
+    if (many && a.K <= 2048) return walk<T, 128, 2, 6, kOut>(a, sms, st);
+    if (many) return a.K <= 8192 ? walk<T, 256, 4, 2, kOut>(a, sms, st) : walk<T, 512, 4, 1, kOut>(a, sms, st);
     if (a.K <= 1024) return run<T, 32, 4, kOut>(a, st);
     if (a.K <= 2048) return run<T, 128, 2, kOut>(a, st);
     if (a.K <= 4096) return run<T, 256, 2, kOut>(a, st);
