@@ -77,27 +77,47 @@ __device__ __forceinline__ float of_ue8m0(uint32_t b) {
     return b == kNanE8 ? __uint_as_float(0x7FFFFFFFu) : b == 0 ? __uint_as_float(0x400000u) : __uint_as_float(b << 23);
 }
 
+__device__ __forceinline__ bool in_range(float d) { return d >= 0x1p-60f && d <= 0x1p100f; }
+// x / d correctly rounded, with r = 1/d rounded and d in range: a product and
+// two corrections by its exact remainder (divide8 says why).
+__device__ __forceinline__ float quotient(float x, float d, float r) {
+    float q = __fmul_rn(x, r);
+    q = __fmaf_rn(-__fmaf_rn(q, d, -x), r, q);
+    return __fmaf_rn(-__fmaf_rn(q, d, -x), r, q);
+}
+// A tensor's scale t, 6 t, and the rounded reciprocal of that (0: divide).
+struct TensorScale {
+    float t, t6, r6;
+    __device__ __forceinline__ explicit TensorScale(const float* p) {
+        t = p ? __ldg(p) : 1.0f;
+        t6 = __fmul_rn(t, kMax);
+        r6 = in_range(t6) ? __frcp_rn(t6) : 0.0f;
+    }
+};
+
 // A group's scale byte from the bits of its largest magnitude (NaN's bits are
 // above infinity's, and those above every finite value's), and what its values
-// are divided by: s itself, or s t.  kNv: t6 = 6 t.
+// are divided by: s itself, or s t.
 template <bool kNv>
-__device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits, float t, float t6, float& div) {
+__device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits, const TensorScale& ts, float& div) {
     if (amax_bits >= kInf) {
         div = 0.0f;   // (codes of zero: see below)
         return kNv ? kNanE4 : kNanE8;
     }
     const float amax = __uint_as_float(amax_bits);
     if constexpr (kNv) {
-        const uint32_t b = max(e4m3_of(__fdiv_rn(amax, t6)), 1u);
-        div = __fmul_rn(of_e4m3(b), t);
+        // (a quotient that the corrections do not settle is far below 2^-9)
+        const uint32_t b = max(e4m3_of(ts.r6 != 0.0f ? quotient(amax, ts.t6, ts.r6) : __fdiv_rn(amax, ts.t6)), 1u);
+        div = __fmul_rn(of_e4m3(b), ts.t);
         return b;
     } else {
-        uint32_t u = __float_as_uint(__fdiv_rn(fmaxf(amax, qm::kEps), kMax));
+        uint32_t u = __float_as_uint(quotient(fmaxf(amax, qm::kEps), kMax, 1.0f / kMax));
         if (u & 0x7FFFFFu) u = (u & kInf) + 0x800000u;
         div = __uint_as_float(u);
         return u >> 23;
     }
 }
+
 // q = x / d correctly rounded, for eight values given as n = -x, two at a time.
 // With r = 1/d rounded, x r is corrected twice by its exact remainder: after
 // the first the quotient is within one unit, and after the second it is the
@@ -105,7 +125,6 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits, float t, floa
 // System/6000 processor", 1990, theorem on the last step of a division).  On
 // negated values so that a zero keeps its sign.  Remainders are exact while
 // nothing leaves fp32's normal range: other divisors take the division itself.
-__device__ __forceinline__ bool in_range(float d) { return d >= 0x1p-60f && d <= 0x1p100f; }
 // minus_r = -1/d rounded, d in range
 __device__ __forceinline__ void divide8(const float (&n)[8], float d, float minus_r, float (&q)[8]) {
     const float2 r2 = make_float2(minus_r, minus_r), d2 = make_float2(d, d);
@@ -142,7 +161,6 @@ __device__ __forceinline__ uint32_t encode8(const float (&n)[8], float div) {
     }
     return codes8(q);
 }
-
 __device__ __forceinline__ uint32_t amax_bits8(const float (&v)[8]) {
     uint32_t a = 0;
 #pragma unroll

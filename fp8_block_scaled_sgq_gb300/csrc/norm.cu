@@ -108,11 +108,7 @@ __device__ __forceinline__ uint4 add_residual(float (&v)[8], const uint4& residu
 // qm::group_scale with the division by 448 as a product and two corrections by
 // its exact remainder (divide8's argument; 1/448 is rounded by the compiler).
 __device__ __forceinline__ float fp8_scale(float amax, bool pow2) {
-    constexpr float r = 1.0f / qm::kFp8Max;
-    const float x = fmaxf(amax, qm::kEps);
-    float s = __fmul_rn(x, r);
-    s = __fmaf_rn(__fmaf_rn(-s, qm::kFp8Max, x), r, s);
-    s = __fmaf_rn(__fmaf_rn(-s, qm::kFp8Max, x), r, s);
+    float s = quotient(fmaxf(amax, qm::kEps), qm::kFp8Max, 1.0f / qm::kFp8Max);
     if (pow2) {
         uint32_t u = __float_as_uint(s);
         if (u & 0x7FFFFFu) u = (u & kInf) + 0x800000u;
@@ -145,7 +141,7 @@ __device__ __forceinline__ void store_codes(const Args& a, int64_t at, const flo
 // over a group each keep half of the columns, until a lane owns one (two of
 // four where a group is two lanes), and hand the quotients' factors back.
 template <typename T, Out kOut, int kVec>
-__device__ __forceinline__ void emit(const Args& a, int64_t m, int tid, int step, const float (&v)[kVec][8], float t, float t6) {
+__device__ __forceinline__ void emit(const Args& a, int64_t m, int tid, int step, const float (&v)[kVec][8], const TensorScale& ts) {
     const int cols = a.K / 8;
     if constexpr (kOut == kSame) {
 #pragma unroll
@@ -195,7 +191,7 @@ __device__ __forceinline__ void emit(const Args& a, int64_t m, int tid, int step
                 }
             } else {
                 constexpr int kLanes = kNv ? 2 : 4;   // a group's; a scale word's are four times as many
-                uint32_t byte = scale_byte<kNv>(own[k], t, t6, div[k]);
+                uint32_t byte = scale_byte<kNv>(own[k], ts, div[k]);
                 if (c >= cols) byte = 0;              // groups past the row's end
                 byte |= __shfl_down_sync(kAll, byte, kLanes) << 8;
                 byte |= __shfl_down_sync(kAll, byte, 2 * kLanes) << 16;
@@ -233,13 +229,6 @@ __device__ __forceinline__ void emit(const Args& a, int64_t m, int tid, int step
             if (c < cols) store_codes<kOut>(a, m * cols + c, q);
         }
     }
-}
-template <Out kOut>
-__device__ __forceinline__ void tensor_scale_of(const Args& a, float& t, float& t6) {
-    t = 1.0f;
-    if constexpr (kOut == kNv4)
-        if (a.tensor_scale) t = __ldg(a.tensor_scale);
-    t6 = __fmul_rn(t, kMax);
 }
 __host__ __device__ constexpr bool negated(Out out) { return out == kFp8 || out == kMx4 || out == kNv4; }
 
@@ -291,12 +280,11 @@ __global__ void __launch_bounds__(kRow == 32 ? 128 : kRow) norm_kernel(const Arg
     if constexpr (kOut != kNone) {
         float rstd = rstd_of(row_sum<kRow>(squares(v), part[1]), a);
         if constexpr (negated(kOut)) rstd = -rstd;
-        float t, t6;
-        tensor_scale_of<kOut>(a, t, t6);
+        const TensorScale ts(kOut == kNv4 ? a.tensor_scale : nullptr);
 #pragma unroll
         for (int i = 0; i < kVec; ++i)
             if (tid + i * kRow < cols) weigh<T>(v[i], rstd, column<T>(a.weight, 0, tid + i * kRow), a.offset);
-        emit<T, kOut, kVec>(a, m, tid, kRow, v, t, t6);
+        emit<T, kOut, kVec>(a, m, tid, kRow, v, ts);
     }
 }
 
@@ -359,8 +347,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_walk_kernel(const Args a
         if (kOut != kNone && c < cols) weight[i] = column<T>(a.weight, 0, c);
         if (a.post && c < cols) post[i] = column<T>(a.post, 0, c);
     }
-    float t, t6;
-    tensor_scale_of<kOut>(a, t, t6);
+    const TensorScale ts(kOut == kNv4 ? a.tensor_scale : nullptr);
     int d = 0, turn = 0;
     for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x, turn ^= 1) {
         ptx::cp_async_wait_pending(a.depth - 1);
@@ -399,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_walk_kernel(const Args a
             if constexpr (negated(kOut)) rstd = -rstd;
 #pragma unroll
             for (int i = 0; i < kVec; ++i) weigh<T>(v[i], rstd, weight[i], a.offset);
-            emit<T, kOut, kVec>(a, m, tid, threads, v, t, t6);
+            emit<T, kOut, kVec>(a, m, tid, threads, v, ts);
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
