@@ -37,6 +37,7 @@ SGQ_LATENT_TEST_TIMEOUT = 256
 
 SGQ_MXFP4 = 0
 SGQ_NVFP4 = 1
+SGQ_FP4_TEST_TIMEOUT = 256
 SGQ_OUT_NONE = 0
 SGQ_OUT_16 = 1
 SGQ_OUT_FP8 = 2

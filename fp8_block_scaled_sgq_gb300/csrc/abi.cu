@@ -389,6 +389,8 @@ sgq_status sgq_dequant_fp4(const void* xq, const void* xs, int64_t M, int64_t K,
 sgq_status sgq_fp4_gemm(const void* Aq, const void* As, const float* a_scale, const void* Wq, const void* Ws,
                         const float* w_scale, void* D, int64_t M, int64_t N, int64_t K, int format, int dtype,
                         sgq_stream_t stream) {
+    const bool stall = format == (SGQ_NVFP4 | SGQ_FP4_TEST_TIMEOUT) && dtype == SGQ_BF16;
+    if (stall) format = SGQ_NVFP4;
     if (!good_fp4(M, K, format, a_scale) || !good_fp4(N, K, format, w_scale) || N == 0 || N % 8 != 0 || !good_dtype(dtype))
         return SGQ_ERR_INVALID_ARG;
     if (M == 0) return SGQ_OK;
@@ -398,7 +400,7 @@ sgq_status sgq_fp4_gemm(const void* Aq, const void* As, const float* a_scale, co
         return SGQ_ERR_MISALIGNED;
     sgq::Fp4GemmArgs a{};
     a.Aq = Aq; a.As = As; a.a_t = a_scale; a.Wq = Wq; a.Ws = Ws; a.w_t = w_scale; a.D = D; a.M = M; a.N = N; a.K = K;
-    a.format = format; a.dtype = dtype;
+    a.format = format; a.dtype = dtype; a.stall = stall;
     return sgq::launch_fp4_gemm(a, reinterpret_cast<cudaStream_t>(stream));
 }
 

@@ -18,8 +18,6 @@ constexpr int kRows = 128;        // rows of the MMA's M side
 constexpr int kStageK = 256;      // elements of K a stage: one 128-byte swizzle row of codes
 constexpr int kMmaK = 64;         // elements of K an MMA
 constexpr int kRowBytes = kStageK / 2;
-constexpr long long kLimit = lat::kTimeoutClocks;
-using Sync = lat::Sync<kLimit>;
 
 struct Args {
     void* D;
@@ -33,6 +31,11 @@ struct Args {
     int splits;
     int ring;        // stages in shared memory
 };
+
+// kStall (SGQ_FP4_TEST_TIMEOUT): the first CTA never loads the second stage's
+// weights, and waits run out early.
+template <bool kStall>
+using SyncOf = lat::Sync<kStall ? lat::kTestTimeoutClocks : lat::kTimeoutClocks>;
 
 // Bytes of one row block's scales a stage (128 rows x 256 values).
 constexpr int sf_bytes(bool nv) { return nv ? 2048 : 1024; }
@@ -144,7 +147,7 @@ struct TileCfg {
     static size_t smem(int ring, int splits) { return need(ring, splits) < kLeast ? kLeast : need(ring, splits); }
 };
 
-template <typename T, int BN, bool kNv>
+template <typename T, int BN, bool kNv, bool kStall = false>
 __global__ void __launch_bounds__(kTileThreads)
     fp4_tile_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                     const __grid_constant__ CUtensorMap tm_ws, const __grid_constant__ CUtensorMap tm_xs, const Args a) {
@@ -163,7 +166,7 @@ __global__ void __launch_bounds__(kTileThreads)
     const uint32_t acc_bar = bar0 + 8u * (2 * C::kMaxRing), drain_bar = acc_bar + 8u;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const Sync sync{words + 1, a.status};
+    const SyncOf<kStall> sync{words + 1, a.status};
     const int S = a.splits;
     const int rank = S > 1 ? static_cast<int>(ptx::cluster_rank()) : 0;
     const int tile = blockIdx.x / S;
@@ -200,7 +203,8 @@ __global__ void __launch_bounds__(kTileThreads)
             const int s = n % a.ring, r = n / a.ring;
             if (r > 0 && !lat::wait_warp(empty(s), (r - 1) & 1, sync)) break;
             ptx::mbar_arrive_expect_tx_if(e, full(s), C::kStageBytes);
-            ptx::tma_load_2d_if(e, w0 + s * (kRows * kRowBytes), &tm_w, kb * kRowBytes, tw * kRows, full(s));
+            if (!(kStall && blockIdx.x == 0 && n == 1))
+                ptx::tma_load_2d_if(e, w0 + s * (kRows * kRowBytes), &tm_w, kb * kRowBytes, tw * kRows, full(s));
             ptx::tma_load_2d_if(e, ws0 + s * C::kSf, &tm_ws, kb * (C::kSf / 8), tw, full(s));
             ptx::tma_load_2d_if(e, x0 + s * (BN * kRowBytes), &tm_x, kb * kRowBytes, tx * BN, full(s));
             ptx::tma_load_2d_if(e, xs0 + s * C::kSf, &tm_xs, kb * (C::kSf / 8), tx * BN / kRows, full(s));
@@ -375,7 +379,8 @@ __device__ __forceinline__ void st_global_v8_first(void* p, const uint32_t (&w)[
 }
 
 // A whole warp waits for a phase that the other CTA of the pair may complete.
-static __device__ __noinline__ bool pair_wait_slow(uint32_t bar, uint32_t parity, const Sync& s) {
+template <long long kLimit>
+static __device__ __noinline__ bool pair_wait_slow(uint32_t bar, uint32_t parity, const lat::Sync<kLimit>& s) {
     const long long t0 = clock64();
     for (uint32_t spins = 1;; ++spins) {
         if (__all_sync(0xFFFFFFFFu, ptx::mbar_try_wait_cluster(bar, parity))) return true;
@@ -391,7 +396,8 @@ static __device__ __noinline__ bool pair_wait_slow(uint32_t bar, uint32_t parity
         }
     }
 }
-__device__ __forceinline__ bool pair_wait(uint32_t bar, uint32_t parity, const Sync& s) {
+template <long long kLimit>
+__device__ __forceinline__ bool pair_wait(uint32_t bar, uint32_t parity, const lat::Sync<kLimit>& s) {
     if (__all_sync(0xFFFFFFFFu, ptx::mbar_try_wait_cluster(bar, parity))) return true;
     return pair_wait_slow(bar, parity, s);
 }
@@ -404,7 +410,7 @@ __device__ __forceinline__ void pair_tile(const Args& a, int i, int& tm, int& tn
     tm = g * 16 + in - tn * rows;
 }
 
-template <typename T, int BN, bool kNv, int kHalves>
+template <typename T, int BN, bool kNv, int kHalves, bool kStall = false>
 __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     fp4_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                     const __grid_constant__ CUtensorMap tm_xs, const __grid_constant__ CUtensorMap tm_ws, const Args a) {
@@ -421,7 +427,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     const uint32_t drain_bar = bar0 + 8u * 20;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const Sync sync{words + 1, a.status};
+    const SyncOf<kStall> sync{words + 1, a.status};
     const uint32_t rank = ptx::cluster_rank();
     const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
@@ -474,7 +480,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
                 const uint32_t bar = ptx::mapa(full(s), 0u);
                 ptx::mbar_arrive_expect_tx_if(e && rank == 0u, full(s), 2 * C::kStageBytes);
                 ptx::tma_load_2d_pair_if(e, x0 + s * C::kXBytes, &tm_x, kb * kRowBytes, row, bar);
-                ptx::tma_load_2d_pair_if(e, w0 + s * C::kWBytes, &tm_w, kb * kRowBytes, wrow, bar);
+                if (!(kStall && blockIdx.x == 0 && n == 1))
+                    ptx::tma_load_2d_pair_if(e, w0 + s * C::kWBytes, &tm_w, kb * kRowBytes, wrow, bar);
                 ptx::tma_load_2d_pair_if(e, xs0 + s * C::kXSf, &tm_xs, kb * (C::kSf / 8), row / kRows, bar);
                 ptx::tma_load_2d_pair_if(e, ws0 + s * C::kWSf, &tm_ws, kb * (C::kSf / 8), tn * BN / kRows, bar);
             }
@@ -660,7 +667,7 @@ Way way_of(int64_t M, int64_t N, int stages, int sms) {
     return static_cast<Way>(best);
 }
 
-template <typename T, int BN, bool kNv>
+template <typename T, int BN, bool kNv, bool kStall = false>
 sgq_status run_tile(gemm::TensorMapEncoder encode, const Fp4GemmArgs& g, Args a, int sms, int smem_max, cudaStream_t st) {
     using C = TileCfg<BN, kNv>;
     Maps tm;
@@ -675,7 +682,7 @@ sgq_status run_tile(gemm::TensorMapEncoder encode, const Fp4GemmArgs& g, Args a,
     const size_t room = (tiles * a.splits <= sms ? 226 : 113) * 1024;   // of an SM for one CTA, or for two
     while (a.ring > 2 && C::need(a.ring, a.splits) > room) --a.ring;
     if (tiles * a.splits > INT32_MAX) return SGQ_ERR_INVALID_ARG;
-    auto kern = fp4_tile_kernel<T, BN, kNv>;
+    auto kern = fp4_tile_kernel<T, BN, kNv, kStall>;
     int dev = 0;
     if (device_of(&dev) != SGQ_OK) return SGQ_ERR_CUDA;
     static bool configured[64] = {};
@@ -701,7 +708,7 @@ sgq_status run_tile(gemm::TensorMapEncoder encode, const Fp4GemmArgs& g, Args a,
     return SGQ_OK;
 }
 
-template <typename T, int BN, bool kNv, int kHalves>
+template <typename T, int BN, bool kNv, int kHalves, bool kStall = false>
 sgq_status run_pair(gemm::TensorMapEncoder encode, const Fp4GemmArgs& g, Args a, int sms, cudaStream_t st) {
     using C = PairCfg<BN, kNv, kHalves>;
     Maps tm;
@@ -716,7 +723,7 @@ sgq_status run_pair(gemm::TensorMapEncoder encode, const Fp4GemmArgs& g, Args a,
     a.tiles_n = static_cast<int>(tiles_n);
     a.tiles = static_cast<int>(tiles_m * tiles_n);
     a.stream_out = g.M * g.N * 2 > (int64_t(32) << 20);
-    auto kern = fp4_pair_kernel<T, BN, kNv, kHalves>;
+    auto kern = fp4_pair_kernel<T, BN, kNv, kHalves, kStall>;
     int dev = 0;
     if (device_of(&dev) != SGQ_OK) return SGQ_ERR_CUDA;
     static bool configured[64] = {};
@@ -775,6 +782,11 @@ sgq_status launch_fp4_gemm(const Fp4GemmArgs& g, cudaStream_t st) {
     a.N = static_cast<int>(g.N);
     a.K = static_cast<int>(g.K);
     a.stages = static_cast<int>((g.K + kStageK - 1) / kStageK);
+    if (g.stall) {   // (the kernels of this flag: bf16, NVFP4)
+        if (g.M <= 64) return run_tile<__nv_bfloat16, 64, true, true>(encode, g, a, di.sm_count, di.max_smem_optin, st);
+        return g.M <= 512 ? run_pair<__nv_bfloat16, 192, true, 1, true>(encode, g, a, di.sm_count, st)
+                          : run_pair<__nv_bfloat16, 192, true, 2, true>(encode, g, a, di.sm_count, st);
+    }
     if (g.dtype == SGQ_BF16)
         return g.format == SGQ_NVFP4 ? pick<__nv_bfloat16, true>(encode, g, a, di, st)
                                      : pick<__nv_bfloat16, false>(encode, g, a, di, st);

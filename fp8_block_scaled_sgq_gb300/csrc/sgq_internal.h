@@ -99,7 +99,7 @@ struct Fp4GemmArgs {
     const float *a_t, *w_t;    // or null
     void* D;
     int64_t M, N, K;
-    int format, dtype;
+    int format, dtype, stall;
 };
 sgq_status launch_fp4_gemm(const Fp4GemmArgs& a, cudaStream_t stream);
 // Arguments of the fused norms (strides in elements).

@@ -1,6 +1,6 @@
 """Times one library entry point on one shape and prints a JSON line.
 
-    python -m fp8_block_scaled_sgq_gb300.measure PATH M N K [--blk B] [--reps R]
+    python -m fp8_block_scaled_sgq_gb300.measure PATH M N K [--blk B] [--format F] [--reps R]
 
 PATH is one of
   quant_per_token   sgq_quant_per_token on x [M, K]            (GB/s: 2 B in + 1 B code per element + 4 B per row)
@@ -13,6 +13,10 @@ PATH is one of
   pair              sgq_quant_token_group then sgq_fp8_block_gemm, back to back on one stream
                     (programmatic dependent launch), [B, B] blocks, UE8M0  (TFLOP/s; GB/s of the
                     quantiser's and the GEMM's algorithmic bytes)
+  quant_fp4         sgq_quant_fp4 on x [M, K], --format mxfp4 or nvfp4     (GB/s)
+  dequant_fp4       sgq_dequant_fp4 to [M, K]                              (GB/s)
+  fp4_gemm          sgq_fp4_gemm                                           (TFLOP/s and GB/s)
+  norm              sgq_norm: norm of x [M, K], residual added, next norm into the format   (GB/s)
 
 The metric's own configurations (the M = 1..8192 sweep, the prefill GEMMs and
 the quantiser at prefill sizes) are timed by bench.py; this times the other
@@ -36,7 +40,8 @@ from . import binding, synth
 L2_BYTES = 129 * 2 ** 20
 
 
-PATHS = ["quant_per_token", "quant_per_tensor", "quant_v2", "scaled_mm", "block_gemm", "linear", "pair"]
+FP4_PATHS = ["quant_fp4", "dequant_fp4", "fp4_gemm", "norm"]
+PATHS = ["quant_per_token", "quant_per_tensor", "quant_v2", "scaled_mm", "block_gemm", "linear", "pair"] + FP4_PATHS
 
 
 def main() -> None:
@@ -46,21 +51,56 @@ def main() -> None:
     ap.add_argument("N", type=int)
     ap.add_argument("K", type=int)
     ap.add_argument("--blk", type=int, default=128)
+    ap.add_argument("--format", choices=("mxfp4", "nvfp4"), default="nvfp4")
     ap.add_argument("--reps", type=int, default=50)
     args = ap.parse_args()
-    print(json.dumps(measure(args.path, args.M, args.N, args.K, args.blk, args.reps)), flush=True)
+    print(json.dumps(measure(args.path, args.M, args.N, args.K, args.blk, args.reps, args.format)), flush=True)
 
 
-def measure(path: str, M: int, N: int, K: int, blk: int, reps: int) -> dict:
+def fp4_calls(path: str, M: int, N: int, K: int, fmt: str, dev):
+    """The calls of a 4-bit path over rotating copies: (calls, bytes a call moves at least, operations)."""
+    from . import dequant_fp4, fp4_gemm, norm_add, quant_fp4
+    packed = lambda rows: rows * K // 2 + rows * K // (32 if fmt == "mxfp4" else 16)  # noqa: E731
+    moved = {"quant_fp4": 2 * M * K + packed(M), "dequant_fp4": 2 * M * K + packed(M), "norm": 6 * M * K + packed(M),
+             "fp4_gemm": packed(M) + packed(N) + 2 * M * N}[path]
+    n_rot = max(2, math.ceil(2 * L2_BYTES / moved) + 1)
+    calls = []
+    if path == "fp4_gemm":
+        xq, xs = quant_fp4(synth.activation(M, K, seed=1).to(dev), fmt)
+        wq, ws = quant_fp4(synth.weight(N, K, seed=2).to(dev), fmt)
+        d = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        rot = [(wq.clone(), ws.clone()) for _ in range(n_rot)]
+        for w in rot:
+            calls.append(lambda sp, w=w: fp4_gemm(xq, xs, *w, fmt, out=d, stream=sp))
+        return calls, moved, 2 * M * N * K
+    x = synth.activation(M, K, seed=1).to(dev)
+    q, s = quant_fp4(x, fmt)
+    y, one = torch.empty_like(x), torch.ones(K, dtype=x.dtype, device=dev)
+    for _ in range(n_rot):
+        if path == "quant_fp4":
+            calls.append(lambda sp, x=x.clone(): quant_fp4(x, fmt, xq=q, xs=s, stream=sp))
+        elif path == "dequant_fp4":
+            calls.append(lambda sp, q=q.clone(), s=s.clone(): dequant_fp4(q, s, fmt, out=y, stream=sp))
+        else:
+            calls.append(lambda sp, x=x.clone(), r=x.clone(): norm_add(x, r, post_weight=one, weight=one, quant=fmt, h_out=y,
+                                                                       out=q, out_scales=s, stream=sp))
+    return calls, moved, 0
+
+
+def measure(path: str, M: int, N: int, K: int, blk: int, reps: int, fmt: str = "nvfp4") -> dict:
     args = argparse.Namespace(path=path, reps=reps)
     dev = torch.device("cuda:0")
     st = torch.cuda.Stream()
     s = st.cuda_stream
-    quant = args.path.startswith("quant")
+    quant = args.path.startswith("quant") or path in FP4_PATHS
     rot_bytes = (M * K * (4 if args.path == "quant_v2" else 2)) if quant else N * K
     n_rot = max(2, math.ceil(2 * L2_BYTES / rot_bytes) + 1)
     calls = []
-    if quant:
+    if path in FP4_PATHS:
+        calls, moved, flops = fp4_calls(path, M, N, K, fmt, dev)
+        n_rot = len(calls)
+        torch.cuda.synchronize()
+    elif quant:
         W = 2 * K if args.path == "quant_v2" else K
         xr = [synth.activation(M, W, seed=i).to(dev) for i in range(min(n_rot, 4))]
         xr = [xr[i % len(xr)].clone() for i in range(n_rot)]
@@ -151,6 +191,8 @@ def measure(path: str, M: int, N: int, K: int, blk: int, reps: int) -> dict:
     if status != 0:
         raise RuntimeError(f"device status {binding.status_string(status)}")
     out = {"path": args.path, "M": M, "N": N, "K": K, "us": round(us, 3), "gbs": round(moved / us / 1e3, 1)}
+    if path in FP4_PATHS:
+        out["format"] = fmt
     if flops:
         out["tflops"] = round(flops / us / 1e6, 2)
         out["blk"] = blk if args.path in ("block_gemm", "linear", "pair") else None

@@ -481,6 +481,13 @@ sgq_status sgq_latent_prefill(const void* q, int64_t q_stride_t, int64_t q_strid
  */
 #define SGQ_MXFP4 0
 #define SGQ_NVFP4 1
+/* Testing only, or-ed to SGQ_NVFP4 for sgq_fp4_gemm with SGQ_BF16: the first
+ * CTA never loads its second stage of weights (K > 256), so its bounded waits
+ * run out, after about 1 ms instead of about 2 s.  The kernel lets its copies
+ * and tensor-core operations land, frees its tensor memory and returns;
+ * sgq_device_status reports SGQ_ERR_TIMEOUT and D is undefined.  The stream
+ * stays usable. */
+#define SGQ_FP4_TEST_TIMEOUT 256
 
 /*
  * x: [M, K], rows x_stride elements apart (x_stride % 8 == 0), or, with

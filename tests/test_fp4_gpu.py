@@ -360,3 +360,20 @@ def test_nothing_is_allocated_by_the_library():
     sgq.fp4_gemm(*sgq.quant_fp4(randn(1, 7168, seed=2), "mxfp4"), *w, "mxfp4")
     ok()
     assert sgq.sgq_allocated_bytes() == before
+
+
+@pytest.mark.parametrize("M,N,K", [(40, 512, 4096), (300, 2048, 2048), (1100, 4096, 2048)])
+def test_wait_that_runs_out(M, N, K):
+    """A stage that never comes: the call returns, the status says so once, and the next calls give what they gave before
+    (tiles whose K is split over a cluster, pairs with one half and with two)."""
+    from fp8_block_scaled_sgq_gb300 import binding
+    a, w = on_gpu(*form(M, K, "nvfp4", 1, True)), on_gpu(*form(N, K, "nvfp4", 2, True))
+    want = sgq.fp4_gemm(*a, *w, "nvfp4")
+    ok()
+    d = torch.empty_like(want)
+    for _ in range(2):
+        sgq.sgq_fp4_gemm(a[0], a[1], None, w[0], w[1], None, d, M, N, K, sgq.SGQ_NVFP4 | binding.SGQ_FP4_TEST_TIMEOUT, sgq.SGQ_BF16)
+        assert sgq.sgq_device_status() == binding.SGQ_ERR_TIMEOUT
+        assert sgq.sgq_device_status() == 0
+        assert torch.equal(sgq.fp4_gemm(*a, *w, "nvfp4"), want)
+    ok()
