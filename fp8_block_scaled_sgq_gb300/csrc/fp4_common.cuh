@@ -78,8 +78,12 @@ __device__ __forceinline__ float of_ue8m0(uint32_t b) {
 }
 
 __device__ __forceinline__ bool in_range(float d) { return d >= 0x1p-60f && d <= 0x1p100f; }
-// x / d correctly rounded, with r = 1/d rounded and d in range: a product and
-// two corrections by its exact remainder (divide8 says why).
+// x / d correctly rounded, with r = 1/d rounded and d in range, as a product
+// and two corrections by its exact remainder: after the first the quotient is
+// within one unit, and after the second it is the rounded one (Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor",
+// 1990, theorem on the last step of a division).  Remainders are exact while
+// nothing leaves fp32's normal range: other divisors take the division itself.
 __device__ __forceinline__ float quotient(float x, float d, float r) {
     float q = __fmul_rn(x, r);
     q = __fmaf_rn(-__fmaf_rn(q, d, -x), r, q);
@@ -101,7 +105,7 @@ struct TensorScale {
 template <bool kNv>
 __device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits, const TensorScale& ts, float& div) {
     if (amax_bits >= kInf) {
-        div = 0.0f;   // (codes of zero: see below)
+        div = 0.0f;
         return kNv ? kNanE4 : kNanE8;
     }
     const float amax = __uint_as_float(amax_bits);
@@ -118,54 +122,35 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits, const TensorS
     }
 }
 
-// q = x / d correctly rounded, for eight values given as n = -x, two at a time.
-// With r = 1/d rounded, x r is corrected twice by its exact remainder: after
-// the first the quotient is within one unit, and after the second it is the
-// rounded one (Markstein, "Computation of elementary functions on the IBM RISC
-// System/6000 processor", 1990, theorem on the last step of a division).  On
-// negated values so that a zero keeps its sign.  Remainders are exact while
-// nothing leaves fp32's normal range: other divisors take the division itself.
-// minus_r = -1/d rounded, d in range
-__device__ __forceinline__ void divide8(const float (&n)[8], float d, float minus_r, float (&q)[8]) {
-    const float2 r2 = make_float2(minus_r, minus_r), d2 = make_float2(d, d);
-#pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-        const float2 n2 = make_float2(n[i], n[i + 1]);
-        float2 x = lat::mul2(n2, r2);
-        x = lat::fma2(lat::fma2(x, d2, n2), r2, x);
-        x = lat::fma2(lat::fma2(x, d2, n2), r2, x);
-        q[i] = x.x;
-        q[i + 1] = x.y;
-    }
+// What eight values of a group are multiplied by, -1/div, where they are
+// themselves results of fp32 arithmetic (a norm, silu): the quotients are
+// within 1.5 units of the division's, far less than the values are off.
+// (-1/2^e is exact, and so are those quotients.)
+template <bool kNv>
+__device__ __forceinline__ float minus_reciprocal(float div) {
+    if constexpr (kNv) return -__frcp_rn(div);
+    else return -__uint_as_float((254u - (__float_as_uint(div) >> 23)) << 23);
 }
-__device__ __forceinline__ void divide8(const float (&n)[8], float d, float (&q)[8]) {
-    if (in_range(d)) {
-        divide8(n, d, -__frcp_rn(d), q);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(-n[i], d);
-    }
-}
-// Eight values of a group, negated -> codes.  div == 0: the group is not finite.
+// Eight values of a group, negated, so that a zero keeps its sign -> codes.
+// div == 0: the group is not finite.
 template <bool kNv>
 __device__ __forceinline__ uint32_t encode8(const float (&n)[8], float div) {
-    if (div == 0.0f) return 0u;
+    const float r = minus_reciprocal<kNv>(div);
     float q[8];
-    if constexpr (kNv) {
-        divide8(n, div, q);
-    } else {
-        // (a power of two, at least 2^-36: its reciprocal is exact, and x times that is the rounded quotient)
-        const float r = -__uint_as_float((254u - (__float_as_uint(div) >> 23)) << 23);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = __fmul_rn(n[i], r);
-    }
-    return codes8(q);
+    for (int i = 0; i < 8; ++i) q[i] = __fmul_rn(n[i], r);
+    return div == 0.0f ? 0u : codes8(q);
 }
+
+// The larger magnitude of three; NaN where one is.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float y;
+    asm("{\n.reg .f32 x, y, z;\nabs.f32 x, %1;\nabs.f32 y, %2;\nabs.f32 z, %3;\nmax.NaN.f32 %0, x, y, z;\n}" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+// The bits of the largest magnitude among eight (above infinity's for NaN).
 __device__ __forceinline__ uint32_t amax_bits8(const float (&v)[8]) {
-    uint32_t a = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) a = max(a, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-    return a;
+    return __float_as_uint(max3(max3(v[0], v[1], v[2]), max3(v[3], v[4], v[5]), max3(v[6], v[7], v[7])));
 }
 
 template <typename T>

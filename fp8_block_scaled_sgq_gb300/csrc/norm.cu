@@ -105,8 +105,7 @@ __device__ __forceinline__ uint4 add_residual(float (&v)[8], const uint4& residu
     return h;
 }
 
-// qm::group_scale with the division by 448 as a product and two corrections by
-// its exact remainder (divide8's argument; 1/448 is rounded by the compiler).
+// qm::group_scale without the division's branches.
 __device__ __forceinline__ float fp8_scale(float amax, bool pow2) {
     float s = quotient(fmaxf(amax, qm::kEps), qm::kFp8Max, 1.0f / qm::kFp8Max);
     if (pow2) {
@@ -117,7 +116,7 @@ __device__ __forceinline__ float fp8_scale(float amax, bool pow2) {
     return s;
 }
 
-// One column of eight values to be quantised, negated (divide8) -> its codes.
+// The codes of a column's eight quotients.
 template <Out kOut>
 __device__ __forceinline__ void store_codes(const Args& a, int64_t at, const float (&q)[8]) {
     if constexpr (kOut == kFp8) {
@@ -175,14 +174,13 @@ __device__ __forceinline__ void emit(const Args& a, int64_t m, int tid, int step
             own[0] = max(own[0], __shfl_xor_sync(kAll, own[0], 4));
             own[0] = max(own[0], __shfl_xor_sync(kAll, own[0], 8));
         }
-        float div[kOwn], rcp[kOwn];
-        bool plain = true;   // the quotients are products (divide8)
+        float rcp[kOwn];   // 0: codes of zero
 #pragma unroll
         for (int k = 0; k < kOwn; ++k) {
             const int c = tid + (first + k) * step;
             if constexpr (kOut == kFp8) {
                 const float s = fp8_scale(__uint_as_float(own[k]), a.scale_kind != 0);
-                div[k] = s;
+                rcp[k] = -__frcp_rn(s);
                 // the first lanes of a group, one for each column
                 if (c < cols && (lane & ((1 << a.group_shift) - 1)) < kVec) {
                     const int64_t g = m * (cols >> a.group_shift) + (c >> a.group_shift);
@@ -191,7 +189,9 @@ __device__ __forceinline__ void emit(const Args& a, int64_t m, int tid, int step
                 }
             } else {
                 constexpr int kLanes = kNv ? 2 : 4;   // a group's; a scale word's are four times as many
-                uint32_t byte = scale_byte<kNv>(own[k], ts, div[k]);
+                float div;
+                uint32_t byte = scale_byte<kNv>(own[k], ts, div);
+                rcp[k] = div == 0.0f ? 0.0f : minus_reciprocal<kNv>(div);
                 if (c >= cols) byte = 0;              // groups past the row's end
                 byte |= __shfl_down_sync(kAll, byte, kLanes) << 8;
                 byte |= __shfl_down_sync(kAll, byte, 2 * kLanes) << 16;
@@ -199,32 +199,18 @@ __device__ __forceinline__ void emit(const Args& a, int64_t m, int tid, int step
                     *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.ys) +
                                                  scale_word_at(m, c / (4 * kLanes), scale_tiles(a.K, kNv))) = byte;
             }
-            if constexpr (kOut == kMx4) {
-                rcp[k] = -__uint_as_float((254u - (__float_as_uint(div[k]) >> 23)) << 23);
-                plain &= div[k] != 0.0f;
-            } else {
-                rcp[k] = -__frcp_rn(div[k]);
-                plain &= in_range(div[k]);
-            }
         }
-        const bool all_plain = __all_sync(kAll, plain);
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
             const int c = tid + i * step;
             const int from = kVec == 2 ? (lane & ~1) | i : kNv ? (lane & ~1) | (i >> 1) : (lane & ~3) | (i >> 1) | ((i & 1) << 1);
-            const int k = kVec == 4 && kNv ? i & 1 : 0;
-            const float r = __shfl_sync(kAll, rcp[k], from), d = __shfl_sync(kAll, div[k], from);
+            const float r = __shfl_sync(kAll, rcp[kVec == 4 && kNv ? i & 1 : 0], from);
             float q[8];
-            if (all_plain) {
-                if constexpr (kOut == kMx4) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) set(q, j, lat::mul2(two(v[i], j), make_float2(r, r)));
-                } else {
-                    divide8(v[i], d, r, q);
-                }
-            } else {
+            for (int j = 0; j < 4; ++j) set(q, j, lat::mul2(two(v[i], j), make_float2(r, r)));
+            if (kOut != kFp8 && r == 0.0f) {   // (NaN times 0 is no 0)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) q[j] = kOut != kFp8 && d == 0.0f ? 0.0f : __fdiv_rn(-v[i][j], d);
+                for (int j = 0; j < 8; ++j) q[j] = 0.0f;
             }
             if (c < cols) store_codes<kOut>(a, m * cols + c, q);
         }
