@@ -427,6 +427,7 @@ sgq_status by_width(const Args& a, int sms, cudaStream_t st) {
     // More rows than a grid that fills the SMs twice: CTAs walk.
     const bool many = a.K > 1024 && a.K <= 16384 && a.M > int64_t(sms) * 2;
     if (many && a.K <= 2048) return walk<T, 128, 2, 6, kOut>(a, sms, st);
+    if (many && a.K <= 7168) return walk<T, 224, 4, 2, kOut>(a, sms, st);   // (144 registers a thread; 128 spill: 53.9 us)
     if (many) return a.K <= 8192 ? walk<T, 256, 4, 2, kOut>(a, sms, st) : walk<T, 512, 4, 1, kOut>(a, sms, st);
     if (a.K <= 1024) return run<T, 32, 4, kOut>(a, st);
     if (a.K <= 2048) return run<T, 128, 2, kOut>(a, st);
