@@ -393,6 +393,8 @@ sgq_status sgq_fp4_gemm(const void* Aq, const void* As, const float* a_scale, co
     if (stall) format = SGQ_NVFP4;
     if (!good_fp4(M, K, format, a_scale) || !good_fp4(N, K, format, w_scale) || N == 0 || N % 8 != 0 || !good_dtype(dtype))
         return SGQ_ERR_INVALID_ARG;
+    // (tiles end past the last row, in int32; a tile's sum ends well within the kernel's bounded waits)
+    if (M > INT32_MAX - 1024 || N > INT32_MAX - 1024 || K > (int64_t(1) << 26)) return SGQ_ERR_INVALID_ARG;
     if (M == 0) return SGQ_OK;
     if (!Aq || !As || !Wq || !Ws || !D) return SGQ_ERR_INVALID_ARG;
     if (!aligned16(Aq) || !aligned16(As) || !aligned16(Wq) || !aligned16(Ws) || !aligned16(D) ||

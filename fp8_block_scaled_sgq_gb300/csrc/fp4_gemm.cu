@@ -137,14 +137,19 @@ struct TileCfg {
     static constexpr int kMaxRing = 12;
     static constexpr int kHead = 1024;                              // barriers and words, before the ring
     // At least the share of an SM's shared memory that the CTA takes of its
-    // TMEM: CTAs that fit together then never wait for each other's TMEM (a
-    // cluster that did, while it holds what another one's peer waits for, would
-    // never end).
-    static constexpr size_t kLeast = size_t(kTmem) * (228 * 1024 / 512) - 1024;
+    // TMEM, so that CTAs which fit together never wait for each other's TMEM; and
+    // more than half of it for a CTA that waits for others (a split tile's), so
+    // that none with a TMEM of its own fits beside it, another kernel's of another
+    // stream either: two clusters that each hold the TMEM that the other's CTA
+    // waits for would never end.
+    static constexpr size_t kLeast = size_t(kTmem) * (228 * 1024 / 512) - 1024, kAlone = 116 * 1024;
     static size_t need(int ring, int splits) {
         return size_t(kHead) + size_t(ring) * kStageBytes + (splits > 1 ? size_t(BN < 4 * splits ? 4 * splits : BN) * kRows * 4 : 0) + 1024;
     }
-    static size_t smem(int ring, int splits) { return need(ring, splits) < kLeast ? kLeast : need(ring, splits); }
+    static size_t smem(int ring, int splits) {
+        const size_t least = splits > 1 ? kAlone : kLeast, n = need(ring, splits);
+        return n < least ? least : n;
+    }
 };
 
 template <typename T, int BN, bool kNv, bool kStall = false>
@@ -211,6 +216,7 @@ __global__ void __launch_bounds__(kTileThreads)
         }
     } else if (warp == 1) {
         const uint32_t e = elect();
+        ptx::grid_dependency_wait();   // (so that the limit of a wait below is not spent on the preceding kernel)
         constexpr uint32_t idesc = idesc_fp4(kRows, BN, kNv);
         const uint64_t wd = ptx::smem_desc(w0, 16, 1024, ptx::kLayoutSw128), xd = ptx::smem_desc(x0, 16, 1024, ptx::kLayoutSw128);
         const uint64_t wsd = ptx::smem_desc(ws0, 128, 128, ptx::kLayoutNone), xsd = ptx::smem_desc(xs0, 128, 128, ptx::kLayoutNone);
@@ -488,6 +494,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
         }
     } else if (warp == 1 && rank == 0u) {
         const uint32_t e = elect();
+        ptx::grid_dependency_wait();   // (so that the limit of a wait below is not spent on the preceding kernel)
         constexpr uint32_t idesc = idesc_fp4(2 * kRows, BN, kNv);
         const uint64_t xd = ptx::smem_desc(x0, 16, 1024, ptx::kLayoutSw128), wd = ptx::smem_desc(w0, 16, 1024, ptx::kLayoutSw128);
         const uint64_t xsd = ptx::smem_desc(xs0, 128, 128, ptx::kLayoutNone), wsd = ptx::smem_desc(ws0, 128, 128, ptx::kLayoutNone);
@@ -635,11 +642,12 @@ int tile_splits(int64_t tiles, int stages, int sms) {
 }
 
 // Which kernel serves more than 64 tokens: the one whose time, in us, is least
-// by what they measured (NVFP4; MXFP4 is 3 to 8 % faster everywhere).  A stage
-// costs an issuing warp 0.31 us, 0.48 us with two halves; a tile's end 0.25 and
-// 1.2; the sum over the parts of a split tile 0.8 and 0.8 for each 64 tokens;
-// a second CTA on an SM counts half for 64 tokens and whole for 128, whose
-// loads already fill the SM's share of L2.  Measured, us:
+// by what they measured (NVFP4; MXFP4 is 3 to 8 % faster everywhere).  A call
+// costs 2.9 (tiles) or 3.2 (pairs); a stage costs an issuing warp 0.31, 0.48
+// with two halves; a pair's tile ends in 0.25 and 1.2; the sum over the parts of
+// a split tile takes 1.3 for 64 tokens and 3 for 128; where tiles outnumber the
+// SMs, two CTAs on an SM take 1.5 times one's time for 64 tokens and 2.6 for
+// 128, whose loads already fill the SM's share of L2.  Measured, us:
 //   N, K, M              64 tokens  128 tokens  pairs, one half  two halves
 //   1536, 7168, 128         6.4         7.2          11.8           15.5
 //   1536, 7168, 301         8.9         8.7          11.6           17.0
@@ -653,12 +661,12 @@ Way way_of(int64_t M, int64_t N, int stages, int sms) {
     auto tile = [&](int bn) {
         const int64_t tiles = (N + kRows - 1) / kRows * ((M + bn - 1) / bn);
         const int splits = tile_splits(tiles, stages, sms);
-        const double waves = tiles * splits <= sms ? 1.0 : double((tiles + 2 * sms - 1) / (2 * sms)) * (bn == 64 ? 1.5 : 2.0);
-        return 2.9 + waves * ((stages + splits - 1) / splits) * 0.31 + (splits > 1 ? 0.8 + 0.8 * bn / 64 : 0.0);
+        const double waves = tiles * splits <= sms ? 1.0 : double((tiles + 2 * sms - 1) / (2 * sms)) * (bn == 64 ? 1.5 : 2.6);
+        return 2.9 + waves * ((stages + splits - 1) / splits) * 0.31 + (splits == 1 ? 0.0 : bn == 64 ? 1.3 : 3.0);
     };
     auto pair = [&](int64_t tokens, double stage, double end) {
         const int64_t tiles = (M + tokens - 1) / tokens * ((N + 191) / 192), pairs = sms / 2;
-        return 2.6 + double((tiles + pairs - 1) / pairs) * (stages * stage + end);
+        return 3.2 + double((tiles + pairs - 1) / pairs) * (stages * stage + end);
     };
     const double t[4] = {tile(64), tile(128), pair(256, 0.31, 0.25), pair(512, 0.48, 1.2)};
     int best = kPair1;

@@ -493,7 +493,8 @@ sgq_status sgq_latent_prefill(const void* q, int64_t q_stride_t, int64_t q_strid
  * x: [M, K], rows x_stride elements apart (x_stride % 8 == 0), or, with
  * silu_mul = 1, [M, 2K] of rows [gate | up], of which silu(gate) * up is
  * quantised (fp32, silu(g) = g / (1 + exp(-g)), within 2^-18 of its value; not
- * rounded to 16 bits between).  xq, xs: codes and scale tiles.
+ * rounded to 16 bits between; its quotients are products with 1 / s or 1 / (s t)).
+ * xq, xs: codes and scale tiles.
  */
 sgq_status sgq_quant_fp4(const void* x, int64_t M, int64_t K, int64_t x_stride, int format, const float* tensor_scale,
                          int silu_mul, int dtype, void* xq, void* xs, sgq_stream_t stream);
@@ -507,7 +508,7 @@ sgq_status sgq_dequant_fp4(const void* xq, const void* xs, int64_t M, int64_t K,
  * group scales, fp32 accumulation in any order, rounded once.  Aq/As: M rows,
  * Wq/Ws: N rows, both in one format; a_scale, w_scale: their fp32 tensor
  * scales, or NULL for 1 (NULL for SGQ_MXFP4).  D: [M, N] contiguous, written,
- * never read.  N % 8 == 0, N > 0; M, N, K < 2^31.  Sums that leave fp32 are
+ * never read.  N % 8 == 0, N > 0; M, N < 2^31 - 1024; K <= 2^26.  Sums that leave fp32 are
  * infinite or NaN, as in any fp32 product.  No memory is allocated, and none
  * is shared between calls.
  */
@@ -529,7 +530,8 @@ sgq_status sgq_fp4_gemm(const void* Aq, const void* As, const float* a_scale, co
  *   SGQ_OUT_NONE   no y (weight, y, ys NULL; a residual is needed)
  *   SGQ_OUT_16     y: [M, K] of `dtype`
  *   SGQ_OUT_FP8    y: E4M3 codes [M, K], ys: scales [M, K/group], by the rule of
- *                  sgq_quant_token_group (on fp32 values); group 32, or 128 with
+ *                  sgq_quant_token_group on fp32 values (which are within 2^-18
+ *                  of their own; quotients are products with 1 / s); group 32, or 128 with
  *                  SGQ_OUT_GROUP_128; fp32 scales, rounded up to powers of two
  *                  with SGQ_OUT_POW2, as UE8M0 bytes with SGQ_OUT_UE8M0
  *   SGQ_OUT_MXFP4, SGQ_OUT_NVFP4

@@ -49,7 +49,7 @@ def test_gemm_validation(lib):
     f = caller(lib.sgq_fp4_gemm, dict(aq=A, as_=B, at=G, wq=C, ws=D, wt=H, d=E, M=4, N=16, K=64, fmt=1, dtype=0))
     for bad in (dict(M=-1), dict(N=0), dict(N=12), dict(K=16), dict(K=0), dict(fmt=0), dict(fmt=0, at=None), dict(fmt=3),
                 dict(dtype=-1), dict(aq=None), dict(as_=None), dict(wq=None), dict(ws=None), dict(d=None), dict(N=1 << 31),
-                dict(M=1 << 31)):
+                dict(M=1 << 31), dict(M=(1 << 31) - 1024), dict(N=(1 << 31) - 1024), dict(K=(1 << 26) + 64)):
         assert f(**bad) == INV, bad
     for bad in (dict(aq=A + 8), dict(as_=B + 8), dict(wq=C + 2), dict(ws=D + 4), dict(d=E + 8), dict(at=G + 2), dict(wt=H + 1)):
         assert f(**bad) == MIS, bad

@@ -1,4 +1,8 @@
 """4-bit linears on the GPU: codes and scales against the rule, products and chains against 64 bits."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -377,3 +381,29 @@ def test_wait_that_runs_out(M, N, K):
         assert sgq.sgq_device_status() == 0
         assert torch.equal(sgq.fp4_gemm(*a, *w, "nvfp4"), want)
     ok()
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    """Nothing has to be called once before a graph is captured."""
+    code = """
+import sys
+import torch
+sys.path.insert(0, %r)
+import fp8_block_scaled_sgq_gb300 as sgq
+x, w = torch.randn(96, 512, device="cuda").bfloat16(), torch.randn(1024, 512, device="cuda").bfloat16()
+n = torch.ones(512, device="cuda").bfloat16()
+def f():
+    q = sgq.rms_norm(x, n, quant="nvfp4")
+    wq = sgq.quant_fp4(w, "nvfp4")
+    return sgq.fp4_gemm(*q, *wq, "nvfp4"), sgq.dequant_fp4(*q, "nvfp4"), sgq.norm_add(x, x, weight=n)[1]
+side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.stream(side), torch.cuda.graph(g, stream=side):
+    got = f()
+g.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, f()))
+print("same")
+""" % os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip().endswith("same"), r.stderr[-2000:]
