@@ -665,7 +665,7 @@ Way way_of(int64_t M, int64_t N, int stages, int sms) {
         return 2.9 + waves * ((stages + splits - 1) / splits) * 0.31 + (splits == 1 ? 0.0 : bn == 64 ? 1.3 : 3.0);
     };
     auto pair = [&](int64_t tokens, double stage, double end) {
-        const int64_t tiles = (M + tokens - 1) / tokens * ((N + 191) / 192), pairs = sms / 2;
+        const int64_t tiles = (M + tokens - 1) / tokens * ((N + 191) / 192), pairs = sms > 1 ? sms / 2 : 1;
         return 3.2 + double((tiles + pairs - 1) / pairs) * (stages * stage + end);
     };
     const double t[4] = {tile(64), tile(128), pair(256, 0.31, 0.25), pair(512, 0.48, 1.2)};
@@ -744,7 +744,7 @@ sgq_status run_pair(gemm::TensorMapEncoder encode, const Fp4GemmArgs& g, Args a,
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    const int pairs = sms / 2 < a.tiles ? sms / 2 : a.tiles;
+    const int most = sms > 1 ? sms / 2 : 1, pairs = most < a.tiles ? most : a.tiles;
     cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
     cfg.blockDim = dim3(kPairThreads);
     cfg.dynamicSmemBytes = C::kSmem;
