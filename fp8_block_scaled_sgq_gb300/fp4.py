@@ -13,7 +13,17 @@ from __future__ import annotations
 from . import binding
 from .latent import _contiguous, _device, _dtype, _empty, _fail
 
+torch = None        # imported with the first call: the package itself does without it
+_NUMBER = {}        # the C interface's numbers of the element types
 _FORMAT = {"mxfp4": (binding.SGQ_MXFP4, 128), "nvfp4": (binding.SGQ_NVFP4, 64)}    # and values of a row in a tile of scales
+
+
+def _load():
+    global torch
+    import torch as t
+    _NUMBER.update({t.bfloat16: binding.SGQ_BF16, t.float16: binding.SGQ_FP16})
+    torch = t
+    return t
 
 
 # The smallest calls take less time on the GPU than their checks do on the host.  So each helper asks everything at
@@ -28,7 +38,6 @@ def _format(fmt):
 
 def _current(stream):
     """(the current device, the call's stream as a handle)."""
-    import torch
     try:   # (names of this torch that are not public: 0.9 -> 0.2 us)
         device = torch._C._cuda_getDevice()
         if stream is None:
@@ -38,20 +47,13 @@ def _current(stream):
     return device, binding._stream(stream)
 
 
-def _done(rc, what):
-    if rc:
-        binding._check(rc, what)
-
-
 def _new(shape, dtype, x, stream):
     """A new tensor on x's device that belongs to the call's stream."""
-    import torch
     return torch.empty(shape, dtype=dtype, device=x.device) if stream is None else _empty(shape, x, stream, dtype)
 
 
 def _scale(name: str, t, fmt):
     """Whether t is a tensor scale: one fp32 value on the device, of the two-level format only."""
-    import torch
     if t is not None:
         if fmt != "nvfp4":
             _fail(f"{name}: 'mxfp4' has no tensor scale")
@@ -63,7 +65,6 @@ def _scale(name: str, t, fmt):
 
 def _packed(name: str, q, s, fmt: str):
     """Whether q and s are a tensor in the 4-bit form."""
-    import torch
     if q.dim() != 2 or q.dtype != torch.uint8 or not q.is_contiguous():
         _fail(f"{name}: expected contiguous uint8 codes [rows, K/2], got {tuple(q.shape)} of {q.dtype}")
     M, K = q.shape[0], 2 * q.shape[1]
@@ -72,14 +73,16 @@ def _packed(name: str, q, s, fmt: str):
 
 def fp4_tensor_scale(x):
     """fp32 [1]: the "nvfp4" tensor scale of x, max|x| / (6 * 448) (1 where x holds only zeros)."""
-    import torch
+    if torch is None:
+        _load()
     t = (x.detach().abs().amax().float() / (6.0 * 448.0)).reshape(1)
     return torch.where(t > 0, t.clamp_min(torch.finfo(torch.float32).tiny), torch.ones_like(t))
 
 
 def fp4_scales_to_tiles(s):
     """Scale bytes uint8 [rows, groups] in rows -> the tiles that the product reads (once, when weights are loaded)."""
-    import torch
+    if torch is None:
+        _load()
     if s.dim() != 2 or s.dtype != torch.uint8:
         _fail(f"expected uint8 [rows, groups], got {tuple(s.shape)} of {s.dtype}")
     rows, groups = s.shape
@@ -102,10 +105,11 @@ def quant_fp4(x, fmt: str, tensor_scale=None, silu_mul: bool = False, xq=None, x
     silu_mul: x is [M, 2K], rows of [gate | up], and silu(gate) * up is quantised.  tensor_scale: fp32 [1] on the
     device ("nvfp4"; None: 1).  xq, xs: outputs to write to.
     """
-    import torch
+    if torch is None:
+        _load()
     f, tile = _format(fmt)
-    t, u8, device_stream = tensor_scale, torch.uint8, _current(stream)
-    device, dt = device_stream[0], _number(x.dtype)
+    t, u8, dt = tensor_scale, torch.uint8, _NUMBER.get(x.dtype)
+    device, handle = _current(stream)
     shape, strides = x.shape, x.stride()
     if len(shape) != 2 or dt is None or x.get_device() != device:
         _why_not_quant(x, silu_mul, t, fmt, xq, xs)
@@ -119,14 +123,15 @@ def quant_fp4(x, fmt: str, tensor_scale=None, silu_mul: bool = False, xq=None, x
         xq = _new((M, K // 2), u8, x, stream)
     if xs is None:
         xs = _new((-(-M // 128), -(-K // tile), 512), u8, x, stream)
-    _done(binding.load_library().sgq_quant_fp4(x.data_ptr(), M, K, strides[0] if M > 1 else W, f, t if t is None else t.data_ptr(),
-                                               1 if silu_mul else 0, dt, xq.data_ptr(), xs.data_ptr(), device_stream[1]),
-          "sgq_quant_fp4")
+    rc = (binding._lib or binding.load_library()).sgq_quant_fp4(
+        x.data_ptr(), M, K, strides[0] if M > 1 else W, f, t if t is None else t.data_ptr(), 1 if silu_mul else 0, dt,
+        xq.data_ptr(), xs.data_ptr(), handle)
+    if rc:
+        binding._check(rc, "sgq_quant_fp4")
     return xq, xs
 
 
 def _why_not_quant(x, silu_mul, t, fmt, xq, xs):
-    import torch
     _dtype(x)
     if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
         _fail(f"x: expected rows of contiguous values, got {tuple(x.shape)} with strides {x.stride()}")
@@ -145,20 +150,15 @@ def _why_not_quant(x, silu_mul, t, fmt, xq, xs):
         _contiguous("xs", xs, (-(-M // 128), -(-K // _FORMAT[fmt][1]), 512), torch.uint8)
 
 
-def _number(dtype):
-    """The C interface's number of an element type, None where it has none."""
-    import torch
-    return binding.SGQ_BF16 if dtype is torch.bfloat16 else binding.SGQ_FP16 if dtype is torch.float16 else None
-
-
 def dequant_fp4(xq, xs, fmt: str, tensor_scale=None, dtype=None, out=None, stream=None):
     """The values [M, K] that codes and scale tiles stand for, in bfloat16 (or dtype, or out's type)."""
-    import torch
+    if torch is None:
+        _load()
     f, tile = _format(fmt)
-    t, u8, device_stream = tensor_scale, torch.uint8, _current(stream)
-    device, shape = device_stream[0], xq.shape
+    t, u8, shape = tensor_scale, torch.uint8, xq.shape
+    device, handle = _current(stream)
     dtype = dtype or (torch.bfloat16 if out is None else out.dtype)
-    dt = _number(dtype)
+    dt = _NUMBER.get(dtype)
     if (len(shape) != 2 or dt is None or xq.dtype is not u8 or xs.dtype is not u8 or not xq.is_contiguous()
             or not xs.is_contiguous() or xs.shape != (-(-shape[0] // 128), -(-2 * shape[1] // tile), 512)
             or xq.get_device() != device or xs.get_device() != device or out is not None
@@ -171,13 +171,15 @@ def dequant_fp4(xq, xs, fmt: str, tensor_scale=None, dtype=None, out=None, strea
     M, K = shape[0], 2 * shape[1]
     if out is None:
         out = _new((M, K), dtype, xq, stream)
-    _done(binding.load_library().sgq_dequant_fp4(xq.data_ptr(), xs.data_ptr(), M, K, f, t if t is None else t.data_ptr(), dt,
-                                                 out.data_ptr(), device_stream[1]), "sgq_dequant_fp4")
+    rc = (binding._lib or binding.load_library()).sgq_dequant_fp4(
+        xq.data_ptr(), xs.data_ptr(), M, K, f, t if t is None else t.data_ptr(), dt, out.data_ptr(), handle)
+    if rc:
+        binding._check(rc, "sgq_dequant_fp4")
     return out
 
 
 def _out(out, dtype, shape):
-    if _number(dtype) is None:
+    if _NUMBER.get(dtype) is None:
         _fail(f"element type {dtype} is neither bfloat16 nor float16")
     if out is not None:
         _contiguous("out", out, shape, dtype)
@@ -189,12 +191,13 @@ def fp4_gemm(xq, xs, wq, ws, fmt: str, x_scale=None, w_scale=None, dtype=None, o
 
     x_scale, w_scale: the tensors' fp32 scales ("nvfp4"; None: 1).
     """
-    import torch
+    if torch is None:
+        _load()
     f, tile = _format(fmt)
-    a, w, u8, f32, device_stream = x_scale, w_scale, torch.uint8, torch.float32, _current(stream)
-    device, xshape, wshape = device_stream[0], xq.shape, wq.shape
+    a, w, u8, f32, xshape, wshape = x_scale, w_scale, torch.uint8, torch.float32, xq.shape, wq.shape
+    device, handle = _current(stream)
     dtype = dtype or (torch.bfloat16 if out is None else out.dtype)
-    dt = _number(dtype)
+    dt = _NUMBER.get(dtype)
     if (len(xshape) != 2 or len(wshape) != 2 or xshape[1] != wshape[1] or dt is None or xq.dtype is not u8
             or xs.dtype is not u8 or wq.dtype is not u8 or ws.dtype is not u8 or not xq.is_contiguous()
             or not xs.is_contiguous() or not wq.is_contiguous() or not ws.is_contiguous()
@@ -217,7 +220,9 @@ def fp4_gemm(xq, xs, wq, ws, fmt: str, x_scale=None, w_scale=None, dtype=None, o
     M, N = xshape[0], wshape[0]
     if out is None:
         out = _new((M, N), dtype, xq, stream)
-    _done(binding.load_library().sgq_fp4_gemm(xq.data_ptr(), xs.data_ptr(), a if a is None else a.data_ptr(), wq.data_ptr(), ws.data_ptr(),
-                                              w if w is None else w.data_ptr(), out.data_ptr(), M, N, 2 * xshape[1], f, dt,
-                                              device_stream[1]), "sgq_fp4_gemm")
+    rc = (binding._lib or binding.load_library()).sgq_fp4_gemm(
+        xq.data_ptr(), xs.data_ptr(), a if a is None else a.data_ptr(), wq.data_ptr(), ws.data_ptr(),
+        w if w is None else w.data_ptr(), out.data_ptr(), M, N, 2 * xshape[1], f, dt, handle)
+    if rc:
+        binding._check(rc, "sgq_fp4_gemm")
     return out

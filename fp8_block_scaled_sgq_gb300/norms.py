@@ -8,14 +8,13 @@ that requires a gradient while gradients are recorded: none is here.
 """
 from __future__ import annotations
 
-from . import binding
-from .fp4 import _current, _done, _FORMAT, _new, _number, _scale
+from . import binding, fp4
+from .fp4 import _current, _FORMAT, _new, _NUMBER, _scale
 from .latent import _contiguous, _device, _dtype, _fail
 
 
 def _target(x, M, K, quant, group, ue8m0, tensor_scale, out, out_scales, stream):
     """(the call's `out`, where y goes, where its scales go)."""
-    import torch
     if quant is None:
         if tensor_scale is not None or out_scales is not None or ue8m0:
             _fail("tensor_scale, out_scales and ue8m0 go with quant")
@@ -24,7 +23,7 @@ def _target(x, M, K, quant, group, ue8m0, tensor_scale, out, out_scales, stream)
         _contiguous("out", out, (M, K), x.dtype)
         _dtype(out)
         return binding.SGQ_OUT_16, out, None
-    u8 = torch.uint8
+    u8 = fp4.torch.uint8
     if quant in _FORMAT:
         if ue8m0:
             _fail("ue8m0 goes with quant='fp8'")
@@ -43,7 +42,7 @@ def _target(x, M, K, quant, group, ue8m0, tensor_scale, out, out_scales, stream)
             _fail("ue8m0 goes with quant='fp8': 'fp8_ue8m0' writes the scales as bytes")
         kind = binding.SGQ_OUT_FP8 | (binding.SGQ_OUT_GROUP_128 if group == 128 else 0)
         kind |= binding.SGQ_OUT_UE8M0 if quant == "fp8_ue8m0" else binding.SGQ_OUT_POW2 if ue8m0 else 0
-        shape, scales, kept = (M, K), (M, K // group), u8 if quant == "fp8_ue8m0" else torch.float32
+        shape, scales, kept = (M, K), (M, K // group), u8 if quant == "fp8_ue8m0" else fp4.torch.float32
     else:
         _fail(f"quant: {quant!r} is none of None, 'fp8', 'fp8_ue8m0', 'mxfp4', 'nvfp4'")
     if out is None:
@@ -77,10 +76,10 @@ def rms_norm(x, weight, eps: float = 1e-6, offset: float = 0.0, quant=None, grou
     (ue8m0: powers of two); "fp8_ue8m0": scales as bytes; "mxfp4", "nvfp4": (codes, scale tiles) as ``quant_fp4`` gives
     them, with tensor_scale.  y is not rounded to 16 bits before it is quantised.  out, out_scales: outputs to write to.
     """
-    import torch
+    torch = fp4.torch or fp4._load()
     device, handle = _current(stream)
     t, kept = tensor_scale, x.dtype
-    dt, shape, strides = _number(kept), x.shape, x.stride()
+    dt, shape, strides = _NUMBER.get(kept), x.shape, x.stride()
     if (dt is None or len(shape) != 2 or strides[1] != 1 or weight.dtype is not kept or weight.shape != shape[1:]
             or not weight.is_contiguous() or x.get_device() != device or weight.get_device() != device
             or t is not None or out is not None or out_scales is not None
@@ -93,10 +92,11 @@ def rms_norm(x, weight, eps: float = 1e-6, offset: float = 0.0, quant=None, grou
         _device(x, weight, t, out, out_scales)
     M, K = shape
     kind, y, ys = _target(x, M, K, quant, group, ue8m0, t, out, out_scales, stream)
-    _done(binding.load_library().sgq_norm(
+    rc = (binding._lib or binding.load_library()).sgq_norm(
         x.data_ptr(), strides[0] if M > 1 else K, None, None, 0, 0, None, 0, None, 0, weight.data_ptr(), M, K, eps, offset, 1.0,
-        1.0, dt, kind, None if t is None else t.data_ptr(), y.data_ptr(), None if ys is None else ys.data_ptr(), handle),
-        "sgq_norm")
+        1.0, dt, kind, None if t is None else t.data_ptr(), y.data_ptr(), None if ys is None else ys.data_ptr(), handle)
+    if rc:
+        binding._check(rc, "sgq_norm")
     return y if ys is None else (y, ys)
 
 
@@ -109,10 +109,10 @@ def norm_add(x, residual, post_weight=None, gate=None, scale: float = 1.0, resid
     y = the norm of h, as ``rms_norm`` gives it.  gate: [K], or [G, K], each row for M/G consecutive rows of x.  h_out:
     where h goes (it may be residual, or x).  Returns h without weight, else (h, y) or (h, codes, scales).
     """
-    import torch
+    torch = fp4.torch or fp4._load()
     device, handle = _current(stream)
     t, p, w, kept, graded = tensor_scale, post_weight, weight, x.dtype, torch.is_grad_enabled()
-    dt, shape, strides = _number(kept), x.shape, x.stride()
+    dt, shape, strides = _NUMBER.get(kept), x.shape, x.stride()
     if (dt is None or len(shape) != 2 or strides[1] != 1 or residual.dtype is not kept or residual.shape != shape
             or residual.stride(1) != 1 or x.get_device() != device or residual.get_device() != device
             or (graded and (x.requires_grad or residual.requires_grad))
@@ -152,10 +152,11 @@ def norm_add(x, residual, post_weight=None, gate=None, scale: float = 1.0, resid
         kind, y, ys = _target(x, M, K, quant, group, ue8m0, t, out, out_scales, stream)
     elif quant is not None or out is not None or out_scales is not None or t is not None:
         _fail("quant, out, out_scales and tensor_scale go with weight")
-    _done(binding.load_library().sgq_norm(
+    rc = (binding._lib or binding.load_library()).sgq_norm(
         x.data_ptr(), strides[0] if M > 1 else K, None if p is None else p.data_ptr(),
         None if gate is None else gate.data_ptr(), gs, rows, residual.data_ptr(), residual.stride(0) if M > 1 else K,
         h_out.data_ptr(), ht, None if w is None else w.data_ptr(), M, K, eps, offset, scale, residual_scale, dt, kind,
-        None if t is None else t.data_ptr(), None if y is None else y.data_ptr(), None if ys is None else ys.data_ptr(), handle),
-        "sgq_norm")
+        None if t is None else t.data_ptr(), None if y is None else y.data_ptr(), None if ys is None else ys.data_ptr(), handle)
+    if rc:
+        binding._check(rc, "sgq_norm")
     return h_out if y is None else (h_out, y) if ys is None else (h_out, y, ys)

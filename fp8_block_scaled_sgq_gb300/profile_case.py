@@ -4,6 +4,8 @@
                                                       [--pow2 | --ue8m0-bytes]
     python -m fp8_block_scaled_sgq_gb300.profile_case --shape M N K BLK [...]
 
+    python -m fp8_block_scaled_sgq_gb300.profile_case --shape M N K BLK --fp4 mxfp4|nvfp4
+
 WORKLOAD/INDEX pick a case from ``synth.WORKLOADS`` (e.g. ``decode_block32 2``
 is M=16, N=7168, K=2048 with [32,32] blocks); --shape takes any shape with
 [BLK, BLK] blocks and UE8M0 scales (x ~ N(0,1), W ~ N(0,0.02)).  Each iteration launches the
@@ -13,7 +15,9 @@ kernel at decode-sized M); with --quant-only only the quantisation kernel;
 --pow2 passes SGQ_GEMM_SCALES_POW2 to the GEMM; --ue8m0-bytes runs the
 byte-output quantiser and sgq_fp8_block_gemm_ue8m0 (the weight scales
 converted to bytes once up front).  The weight is quantised once up front
-(one extra launch; two with --ue8m0-bytes).  The run ends with
+(one extra launch; two with --ue8m0-bytes).  With --fp4 each iteration is a
+4-bit linear (BLK unused): norm_add of [M, K] into the format, of the same into
+FP8 groups of 128, quant_fp4 of x, and fp4_gemm.  The run ends with
 the device status word checked and one line of wall-clock timing, which is
 not a benchmark number (use bench.py for those).
 """
@@ -28,6 +32,23 @@ import torch
 from . import binding, synth
 
 
+def fp4_case(M: int, N: int, K: int, fmt: str, iters: int) -> None:
+    from . import fp4_gemm, norm_add, quant_fp4
+    x = synth.activation(M, K, seed=1).to("cuda:0")
+    w = quant_fp4(synth.weight(N, K, seed=2).to("cuda:0"), fmt)
+    n = torch.ones(K, dtype=x.dtype, device=x.device)
+    gate = torch.ones_like(n)
+    for _ in range(iters):
+        norm_add(x, x, post_weight=n, gate=gate, weight=n, quant=fmt)
+        norm_add(x, x, post_weight=n, gate=gate, weight=n, quant="fp8")
+        fp4_gemm(*quant_fp4(x, fmt), *w, fmt)
+    torch.cuda.synchronize()
+    status = binding.sgq_device_status()
+    if status != 0:
+        raise RuntimeError(f"device status {binding.status_string(status)}")
+    print(json.dumps({"case": "fp4", "format": fmt, "M": M, "N": N, "K": K, "iters": iters}))
+
+
 def main() -> None:
     ap = argparse.ArgumentParser()
     ap.add_argument("workload", nargs="?", choices=sorted(synth.WORKLOADS))
@@ -38,7 +59,12 @@ def main() -> None:
     ap.add_argument("--quant-only", action="store_true", help="launch only the activation quantiser")
     ap.add_argument("--pow2", action="store_true", help="GEMM with SGQ_GEMM_SCALES_POW2 (UE8M0 scales)")
     ap.add_argument("--ue8m0-bytes", action="store_true", help="UE8M0 scale bytes (quantiser and GEMM)")
+    ap.add_argument("--fp4", choices=("mxfp4", "nvfp4"), help="the 4-bit linear and the norms before it")
     args = ap.parse_args()
+    if args.fp4:
+        if not args.shape:
+            ap.error("--fp4 goes with --shape")
+        return fp4_case(*args.shape[:3], args.fp4, args.iters)
     if args.shape:
         M, N, K, blk = args.shape
         c = synth.Case(f"shape_M{M}_N{N}_K{K}_b{blk}", M, N, K, blk, blk, True)
