@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kRow == 32 ? 128 : kRow) norm_kernel(const Arg
     }
 }
 
-// Many rows of more than 1024 elements: the grid fills the SMs once, and each
+// Many rows of more than 1024 elements (by_width): the grid fills the SMs once, and each
 // CTA walks over rows, its weights in registers.  Every thread copies its own
 // columns of the next rows into shared memory (cp.async, 16 bytes each, read
 // back by that thread alone), so that `depth` rows of x, residual and gate are
@@ -430,8 +430,10 @@ sgq_status run(const Args& a, cudaStream_t st) {
 }
 template <typename T, Out kOut>
 sgq_status by_width(const Args& a, int sms, cudaStream_t st) {
-    // More rows than a grid that fills the SMs twice: CTAs walk.
-    const bool many = a.K > 1024 && a.K <= 16384 && a.M > int64_t(sms) * 2;
+    // CTAs walk where the rows are more than L2 holds and come from HBM; a CTA a row is sooner done with what is in L2
+    // (a norm, residual, norm in a graph, us, walking / a row each: 1600 x 4096 10.0 / 8.2, 4096 x 4096 27.4 / 28.6,
+    // 1216 x 7168 11.5 / 11.9, 4096 x 7168 43.6 / 53.4, 4096 x 1536 9.9 / 8.3, 16384 x 1536 35.1 / 39.8).
+    const bool many = a.K > 1024 && a.K <= 16384 && a.M * a.K > (int64_t(10) << 20);
     if (many && a.K <= 2048) return walk<T, 128, 2, 6, kOut>(a, sms, st);
     if (many && a.K <= 7168) return walk<T, 224, 4, 2, kOut>(a, sms, st);   // (as 256 threads some registers spill: 48.8 -> 53.9 us)
     if (many) return a.K <= 8192 ? walk<T, 256, 4, 2, kOut>(a, sms, st) : walk<T, 512, 4, 1, kOut>(a, sms, st);
