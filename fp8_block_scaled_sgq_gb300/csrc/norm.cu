@@ -142,13 +142,13 @@ __device__ __forceinline__ void store_codes(const Args& a, int64_t at, const flo
 // for all of its lanes, so they are taken once: lanes that meet in the maximum
 // over a group each keep half of the columns, until a lane owns one (two of
 // four where a group is two lanes), and hand the quotients' factors back.
-template <typename T, Out kOut, int kVec>
+template <typename T, Out kOut, int kVec, bool kFull>
 __device__ __forceinline__ void emit(const Args& a, int64_t m, int tid, int step, const float (&v)[kVec][8], const TensorScale& ts) {
     const int cols = a.K / 8;
     if constexpr (kOut == kSame) {
 #pragma unroll
         for (int i = 0; i < kVec; ++i)
-            if (tid + i * step < cols) static_cast<uint4*>(a.y)[m * cols + tid + i * step] = pack8<T>(v[i]);
+            if (kFull || tid + i * step < cols) static_cast<uint4*>(a.y)[m * cols + tid + i * step] = pack8<T>(v[i]);
     } else {
         constexpr unsigned kAll = 0xFFFFFFFFu;
         constexpr bool kNv = kOut == kNv4;
@@ -185,7 +185,7 @@ __device__ __forceinline__ void emit(const Args& a, int64_t m, int tid, int step
                 const float s = fp8_scale(__uint_as_float(own[k]), a.scale_kind != 0);
                 rcp[k] = -__frcp_rn(s);
                 // the first lanes of a group, one for each column
-                if (c < cols && (lane & ((1 << a.group_shift) - 1)) < kVec) {
+                if ((kFull || c < cols) && (lane & ((1 << a.group_shift) - 1)) < kVec) {
                     const int64_t g = m * (cols >> a.group_shift) + (c >> a.group_shift);
                     if (a.scale_kind == 2) static_cast<uint8_t*>(a.ys)[g] = static_cast<uint8_t>(__float_as_uint(s) >> 23);
                     else static_cast<float*>(a.ys)[g] = s;
@@ -195,10 +195,10 @@ __device__ __forceinline__ void emit(const Args& a, int64_t m, int tid, int step
                 float div;
                 uint32_t byte = scale_byte<kNv>(own[k], ts, div);
                 rcp[k] = div == 0.0f ? 0.0f : minus_reciprocal<kNv>(div);
-                if (c >= cols) byte = 0;              // groups past the row's end
+                if (!kFull && c >= cols) byte = 0;              // groups past the row's end
                 byte |= __shfl_down_sync(kAll, byte, kLanes) << 8;
                 byte |= __shfl_down_sync(kAll, byte, 2 * kLanes) << 16;
-                if (c < cols && (lane & (4 * kLanes - 1)) < (kNv ? 2 : kVec))
+                if ((kFull || c < cols) && (lane & (4 * kLanes - 1)) < (kNv ? 2 : kVec))
                     *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.ys) +
                                                  scale_word_at(m, c / (4 * kLanes), scale_tiles(a.K, kNv))) = byte;
             }
@@ -215,7 +215,7 @@ __device__ __forceinline__ void emit(const Args& a, int64_t m, int tid, int step
 #pragma unroll
                 for (int j = 0; j < 8; ++j) q[j] = 0.0f;
             }
-            if (c < cols) store_codes<kOut>(a, m * cols + c, q);
+            if (kFull || c < cols) store_codes<kOut>(a, m * cols + c, q);
         }
     }
 }
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kRow == 32 ? 128 : kRow) norm_kernel(const Arg
 #pragma unroll
         for (int i = 0; i < kVec; ++i)
             if (tid + i * kRow < cols) weigh<T>(v[i], rstd, column<T>(a.weight, 0, tid + i * kRow), a.offset);
-        emit<T, kOut, kVec>(a, m, tid, kRow, v, ts);
+        emit<T, kOut, kVec, false>(a, m, tid, kRow, v, ts);
     }
 }
 
@@ -284,7 +284,9 @@ __global__ void __launch_bounds__(kRow == 32 ? 128 : kRow) norm_kernel(const Arg
 // under way while one is summed.  Four columns a thread: what a row costs beside
 // its elements (two sums over the CTA) falls with fewer warps, and two CTAs of
 // 14 warps keep HBM busy where nothing is quantised (with two columns and twice
-// the warps every step into FP8 took 61.3 us instead of 58.4).
+// the warps every step into FP8 took 61.3 us instead of 58.4).  kFull: every
+// thread has all of its columns (K a multiple of 256 kVec), and no branch
+// stands between them (48.7 -> 38.4 us).
 __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
@@ -305,7 +307,7 @@ __device__ __forceinline__ float block_sum(float s, float* part) {
     return __shfl_sync(0xFFFFFFFFu, s, 0);   // (at most 16 warps)
 }
 
-template <typename T, int kThreads, int kVec, int kCtas, Out kOut>
+template <typename T, int kThreads, int kVec, int kCtas, Out kOut, bool kFull>
 __global__ void __launch_bounds__(kThreads, kCtas) norm_walk_kernel(const Args a) {
     extern __shared__ uint4 ring[];
     __shared__ float part[4][32];
@@ -322,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_walk_kernel(const Args a
                 const T* from = static_cast<const T*>(p) + at + tid * 8;
 #pragma unroll
                 for (int i = 0; i < kVec; ++i)
-                    if (tid + i * threads < cols) copy16(to + i * threads * 16, from + i * threads * 8);
+                    if (kFull || tid + i * threads < cols) copy16(to + i * threads * 16, from + i * threads * 8);
             };
             row(a.x, m * a.x_s, slot);
             if (a.residual) row(a.residual, m * a.r_s, slot + array_bytes);
@@ -336,8 +338,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_walk_kernel(const Args a
     for (int i = 0; i < kVec; ++i) {
         const int c = tid + i * threads;
         weight[i] = post[i] = make_uint4(0, 0, 0, 0);
-        if (kOut != kNone && c < cols) weight[i] = column<T>(a.weight, 0, c);
-        if (a.post && c < cols) post[i] = column<T>(a.post, 0, c);
+        if (kOut != kNone && (kFull || c < cols)) weight[i] = column<T>(a.weight, 0, c);
+        if (a.post && (kFull || c < cols)) post[i] = column<T>(a.post, 0, c);
     }
     const TensorScale ts(kOut == kNv4 ? a.tensor_scale : nullptr);
     int d = 0, turn = 0;
@@ -348,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_walk_kernel(const Args a
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
             uint4 x = make_uint4(0, 0, 0, 0);
-            if (tid + i * threads < cols) x = take16(slot + i * threads * 16);
+            if (kFull || tid + i * threads < cols) x = take16(slot + i * threads * 16);
             unpack8<T>(x, v[i]);
         }
         // (a row's first sum is met by all before the next row's is written: two sums take turns where there is no other)
@@ -361,11 +363,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_walk_kernel(const Args a
             if (a.gate) {
 #pragma unroll
                 for (int i = 0; i < kVec; ++i)
-                    if (tid + i * threads < cols) open<T>(v[i], take16(slot + 2 * array_bytes + i * threads * 16));
+                    if (kFull || tid + i * threads < cols) open<T>(v[i], take16(slot + 2 * array_bytes + i * threads * 16));
             }
 #pragma unroll
             for (int i = 0; i < kVec; ++i) {
-                if (tid + i * threads >= cols) continue;
+                if (!kFull && tid + i * threads >= cols) continue;
                 const uint4 h = add_residual<T>(v[i], take16(slot + array_bytes + i * threads * 16), a);
                 reinterpret_cast<uint4*>(static_cast<T*>(a.h) + m * a.h_s)[tid + i * threads] = h;
             }
@@ -378,19 +380,19 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_walk_kernel(const Args a
             if constexpr (negated(kOut)) rstd = -rstd;
 #pragma unroll
             for (int i = 0; i < kVec; ++i) weigh<T>(v[i], rstd, weight[i], a.offset);
-            emit<T, kOut, kVec>(a, m, tid, threads, v, ts);
+            emit<T, kOut, kVec, kFull>(a, m, tid, threads, v, ts);
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-template <typename T, int kThreads, int kVec, int kCtas, Out kOut>
+template <typename T, int kThreads, int kVec, int kCtas, Out kOut, bool kFull>
 sgq_status walk(Args a, int sms, cudaStream_t st) {
     const int cols = a.K / 8, threads = (cols + 32 * kVec - 1) / (32 * kVec) * 32;
     const int ctas = kThreads * kCtas / threads, share = 208 * 1024 / ctas;
     const int row_bytes = (1 + (a.residual != nullptr) + (a.gate != nullptr)) * kVec * threads * 16;
     a.depth = share / row_bytes < 4 ? share / row_bytes : 4;
-    auto kern = norm_walk_kernel<T, kThreads, kVec, kCtas, kOut>;
+    auto kern = norm_walk_kernel<T, kThreads, kVec, kCtas, kOut, kFull>;
     static bool configured[64] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SGQ_ERR_CUDA;
@@ -434,9 +436,14 @@ sgq_status by_width(const Args& a, int sms, cudaStream_t st) {
     // (a norm, residual, norm in a graph, us, walking / a row each: 1600 x 4096 10.0 / 8.2, 4096 x 4096 27.4 / 28.6,
     // 1216 x 7168 11.5 / 11.9, 4096 x 7168 43.6 / 53.4, 4096 x 1536 9.9 / 8.3, 16384 x 1536 35.1 / 39.8).
     const bool many = a.K > 1024 && a.K <= 16384 && a.M * a.K > (int64_t(10) << 20);
-    if (many && a.K <= 2048) return walk<T, 128, 2, 6, kOut>(a, sms, st);
-    if (many && a.K <= 7168) return walk<T, 224, 4, 2, kOut>(a, sms, st);   // (as 256 threads some registers spill: 48.8 -> 53.9 us)
-    if (many) return a.K <= 8192 ? walk<T, 256, 4, 2, kOut>(a, sms, st) : walk<T, 512, 4, 1, kOut>(a, sms, st);
+    if (many && a.K <= 2048)
+        return a.K % 512 == 0 ? walk<T, 128, 2, 6, kOut, true>(a, sms, st) : walk<T, 128, 2, 6, kOut, false>(a, sms, st);
+    // (7168: as 256 threads some registers spill, 48.8 -> 53.9 us)
+    if (many && a.K % 1024 == 0)
+        return a.K <= 7168   ? walk<T, 224, 4, 2, kOut, true>(a, sms, st)
+               : a.K <= 8192 ? walk<T, 256, 4, 2, kOut, true>(a, sms, st)
+                             : walk<T, 512, 4, 1, kOut, true>(a, sms, st);
+    if (many) return a.K <= 8192 ? walk<T, 256, 4, 2, kOut, false>(a, sms, st) : walk<T, 512, 4, 1, kOut, false>(a, sms, st);
     if (a.K <= 1024) return run<T, 32, 4, kOut>(a, st);
     if (a.K <= 2048) return run<T, 128, 2, kOut>(a, st);
     if (a.K <= 4096) return run<T, 256, 2, kOut>(a, st);

@@ -101,7 +101,7 @@ def walking(K):
 
 
 #: Widths at the kernels' borders (a warp a row up to 1024, a CTA up to 32768), odd ones.
-WIDTHS = [8, 24, 1024, 1032, 1544, 2048, 2056, 4104, 7168, 8200, 16384, 16392, 32768]
+WIDTHS = [8, 24, 1024, 1032, 1536, 1544, 2048, 2056, 4096, 4104, 7168, 8192, 8200, 16384, 16392, 32768]
 
 
 @TYPES
