@@ -94,6 +94,17 @@ def test_quant_of_groups_that_are_not_finite(fmt, dtype):
 
 
 @BOTH
+@pytest.mark.parametrize("shift", [0, 8, 16, 24])
+@pytest.mark.parametrize("K", [512, 1024, 1056])
+def test_quant_of_rows_that_start_anywhere(fmt, shift, K):
+    """Rows on 16 bytes or on 32, whole spans of 512 or not, even and odd numbers of rows."""
+    for M in (1, 2, 301, 2000):
+        wide = randn(M * (K + 40) + 64, seed=shift)
+        for step in (K + 8, K + 16):
+            check_quant(torch.as_strided(wide, (M, K), (step, 1), shift), fmt)
+
+
+@BOTH
 def test_quant_of_rows_apart_into_given_outputs(fmt):
     """x is a part of wider rows; outputs lie between guards that stay."""
     wide = randn(257, 2048 + 64, seed=3)
