@@ -345,8 +345,8 @@ __global__ void __launch_bounds__(kTileThreads)
 // operands are read (10 KB an SM) and the next ones written (8.7 KB with one
 // half, 6.5 KB with two that share the weights), at 128 bytes a cycle.
 // Measured in a graph, two halves: 4096 x 7168 x 7168 NVFP4 58 us (7.2 PFLOP/s),
-// MXFP4 56 us; 8192 x 24576 x 1536 MXFP4 108 us (114 with one half), of which
-// 27 tile ends take 1.2 us each and the stores of D show with some 25.
+// MXFP4 56 us; 8192 x 24576 x 1536 MXFP4 108 us (115 with one half): its 402 MB of
+// D take HBM 99 us by themselves (a fill), and the rest 81 without them.
 //
 // TMEM holds two accumulators.  One half: tiles take them in turn, and one is
 // read while the next tile's sums form in the other.  Two halves: one each; a

@@ -6,8 +6,8 @@
 // NVFP4 group or half an MXFP4 one; a warp takes a span of 512 elements of
 // every so many rows, so that the four groups of a scale word lie in
 // neighbouring lanes and leave as one store, and no index is divided on the way.
-// Measured, 4099 x 7168: MXFP4 13.6 us (5.5 TB/s), NVFP4 15.9 (4.7), of
-// silu(gate) * up 25.5 and 24.6 (5.4), back to 16 bits 10.2 and 10.9 (7.0, the
+// Measured, 4099 x 7168: MXFP4 13.1 us (5.7 TB/s), NVFP4 15.3 (4.9), of
+// silu(gate) * up 24.0 and 24.3 (5.5), back to 16 bits 10.2 and 10.9 (7.0, the
 // codes being in L2).  The scale words, 4 bytes to a 32-byte sector, cost 1.3 us.
 #include <cuda_runtime.h>
 

@@ -12,10 +12,11 @@
 // (fp4_common.cuh).
 //
 // Each of x, residual, h and y passes once; a row stays in registers (8 elements
-// a 16-byte load) between its one or two sums.  Measured, 4096 x 7168 in bf16: a norm 19.1 us (6.2 TB/s), residual alone
-// 26.2 (6.7), with the next norm 41.9 (5.6): HBM.  Into FP8 groups 22.0 (4.0), with every step
-// before it 48.8 (4.2): instructions, some 250 a warp for 8 elements a lane, at half of the
-// issue rate.  One row: 3.2 us in a graph.
+// a 16-byte load) between its one or two sums.  Measured, 4096 x 7168 in bf16: a
+// norm 17.6 us (6.7 TB/s), residual alone 25.9 (6.8), with the next norm 40.0
+// (5.9): HBM.  Into FP8 groups 19.2 (4.6), with every step before it 38.2 (5.4):
+// instructions beside it, 197 a warp for 8 elements a lane.  One row: 3.2 us in a
+// graph.
 #include <cuda_runtime.h>
 
 #include "fp4_common.cuh"
