@@ -131,10 +131,24 @@ __device__ __forceinline__ float minus_reciprocal(float div) {
     if constexpr (kNv) return -__frcp_rn(div);
     else return -__uint_as_float((254u - (__float_as_uint(div) >> 23)) << 23);
 }
+// Eight negated values -> codes, by divisions: for divisors outside in_range,
+// whose reciprocals may leave fp32.  div == 0: the group is not finite.  (Out
+// of line, and in registers.)
+static __device__ __noinline__ uint32_t divided8(float4 a, float4 b, float div) {
+    const float n[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    float q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(n[i], -div);
+    return div == 0.0f ? 0u : codes8(q);
+}
+__device__ __forceinline__ uint32_t divided8(const float (&n)[8], float div) {
+    return divided8(make_float4(n[0], n[1], n[2], n[3]), make_float4(n[4], n[5], n[6], n[7]), div);
+}
 // Eight values of a group, negated, so that a zero keeps its sign -> codes.
 // div == 0: the group is not finite.
 template <bool kNv>
 __device__ __forceinline__ uint32_t encode8(const float (&n)[8], float div) {
+    if (kNv && !in_range(div)) return divided8(n, div);
     const float r = minus_reciprocal<kNv>(div);
     float q[8];
 #pragma unroll
@@ -142,11 +156,21 @@ __device__ __forceinline__ uint32_t encode8(const float (&n)[8], float div) {
     return div == 0.0f ? 0u : codes8(q);
 }
 
-// The larger magnitude of three; NaN where one is.
+// The largest magnitude of three; NaN where one is.
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float y;
     asm("{\n.reg .f32 x, y, z;\nabs.f32 x, %1;\nabs.f32 y, %2;\nabs.f32 z, %3;\nmax.NaN.f32 %0, x, y, z;\n}" : "=f"(y) : "f"(a), "f"(b), "f"(c));
     return y;
+}
+// The same without the NaNs among them (NaN where all are).
+__device__ __forceinline__ float max3_of_numbers(float a, float b, float c) {
+    float y;
+    asm("{\n.reg .f32 x, y, z;\nabs.f32 x, %1;\nabs.f32 y, %2;\nabs.f32 z, %3;\nmax.f32 %0, x, y, z;\n}" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+// The bits of the largest magnitude among eight, of those that are no NaN (0 where all are).
+__device__ __forceinline__ uint32_t amax_bits8_of_numbers(const float (&v)[8]) {
+    return __float_as_uint(max3_of_numbers(max3_of_numbers(v[0], v[1], v[2]), max3_of_numbers(v[3], v[4], v[5]), max3_of_numbers(v[6], v[7], 0.0f)));
 }
 // The bits of the largest magnitude among eight (above infinity's for NaN).
 __device__ __forceinline__ uint32_t amax_bits8(const float (&v)[8]) {

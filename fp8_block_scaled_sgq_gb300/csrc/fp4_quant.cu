@@ -7,7 +7,7 @@
 // every so many rows, so that the four groups of a scale word lie in
 // neighbouring lanes and leave as one store, and no index is divided on the way.
 // Measured, 4099 x 7168: MXFP4 13.1 us (5.7 TB/s), NVFP4 15.3 (4.9), of
-// silu(gate) * up 24.0 and 24.3 (5.5), back to 16 bits 10.2 and 10.9 (7.0, the
+// silu(gate) * up 23.7 (5.6), back to 16 bits 10.2 and 10.9 (7.0, the
 // codes being in L2).  The scale words, 4 bytes to a 32-byte sector, cost 1.3 us.
 #include <cuda_runtime.h>
 
@@ -25,13 +25,17 @@ using namespace fp4;
 constexpr int kThreads = 256;
 constexpr int kSpan = 512;   // elements of a warp's span
 
-// -silu(g) * u of -g and u in fp32: within 2^-18 of its value.
-__device__ __forceinline__ float minus_silu_mul(float minus_g, float u) {
-    return __fdividef(minus_g, 1.0f + __expf(minus_g)) * u;
-}
-// The same 16-bit values with the other sign.
-__device__ __forceinline__ uint4 negate(uint4 w) {
-    return make_uint4(w.x ^ 0x80008000u, w.y ^ 0x80008000u, w.z ^ 0x80008000u, w.w ^ 0x80008000u);
+// -silu(g) * u of h = -g/4 and u in fp32, as h / (1/4 + exp(-g)/4) * u, so that
+// the divisor stays below 2^126 and its reciprocal a normal number down to the
+// last g whose exp(-g) is finite (-88.7).  Within 2^-17 of its value: an
+// exponent near 127 is off by half a unit, 2^-18, and the product with log2 e by
+// as much.
+__device__ __forceinline__ float minus_silu_mul(float h, float u) {
+    constexpr float kLog2e = 1.44269504088896341f;
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmaf_rn(h, 4.0f * kLog2e, -2.0f)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e + 0.25f));
+    return h * r * u;
 }
 
 // 16 elements, in one load where they start on 32 bytes.
@@ -140,10 +144,10 @@ __device__ __forceinline__ void silu_row(const uint4 (&raw)[4], const TensorScal
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         float u[8];
-        unpack8<T>(negate(raw[h]), v[h]);
+        unpack8<T>(raw[h], v[h]);
         unpack8<T>(raw[2 + h], u);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[h][j] = minus_silu_mul(v[h][j], u[j]);
+        for (int j = 0; j < 8; ++j) v[h][j] = minus_silu_mul(-0.25f * v[h][j], u[j]);
     }
     uint32_t amax = max(amax_bits8(v[0]), amax_bits8(v[1]));
     if constexpr (!kNv) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));

@@ -109,9 +109,10 @@ __device__ __forceinline__ uint4 add_residual(float (&v)[8], const uint4& residu
     return h;
 }
 
-// qm::group_scale without the division's branches.
+// qm::group_scale without the division's branches.  (An infinity stays one: its remainder is none.)
 __device__ __forceinline__ float fp8_scale(float amax, bool pow2) {
     float s = quotient(fmaxf(amax, qm::kEps), qm::kFp8Max, 1.0f / qm::kFp8Max);
+    if (__float_as_uint(amax) == kInf) s = amax;
     if (pow2) {
         uint32_t u = __float_as_uint(s);
         if (u & 0x7FFFFFu) u = (u & kInf) + 0x800000u;
@@ -159,7 +160,7 @@ __device__ __forceinline__ void emit(const Args& a, int64_t m, int tid, int step
         const bool odd1 = (lane & 1) != 0, odd2 = (lane & 2) != 0;
         uint32_t top[kVec], own[2];
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) top[i] = amax_bits8(v[i]);
+        for (int i = 0; i < kVec; ++i) top[i] = kOut == kFp8 ? amax_bits8_of_numbers(v[i]) : amax_bits8(v[i]);
         int first;   // the first column that this lane owns
         if constexpr (kVec == 4) {
             own[0] = max(odd1 ? top[2] : top[0], __shfl_xor_sync(kAll, odd1 ? top[0] : top[2], 1));
@@ -178,7 +179,7 @@ __device__ __forceinline__ void emit(const Args& a, int64_t m, int tid, int step
             own[0] = max(own[0], __shfl_xor_sync(kAll, own[0], 4));
             own[0] = max(own[0], __shfl_xor_sync(kAll, own[0], 8));
         }
-        float rcp[kOwn];   // 0: codes of zero
+        float rcp[kOwn];   // what the group's values are multiplied by; in 4 bits, not below 0: what they are divided by (divided8)
 #pragma unroll
         for (int k = 0; k < kOwn; ++k) {
             const int c = tid + (first + k) * step;
@@ -195,7 +196,7 @@ __device__ __forceinline__ void emit(const Args& a, int64_t m, int tid, int step
                 constexpr int kLanes = kNv ? 2 : 4;   // a group's; a scale word's are four times as many
                 float div;
                 uint32_t byte = scale_byte<kNv>(own[k], ts, div);
-                rcp[k] = div == 0.0f ? 0.0f : minus_reciprocal<kNv>(div);
+                rcp[k] = (kNv ? in_range(div) : div != 0.0f) ? minus_reciprocal<kNv>(div) : div;
                 if (!kFull && c >= cols) byte = 0;              // groups past the row's end
                 byte |= __shfl_down_sync(kAll, byte, kLanes) << 8;
                 byte |= __shfl_down_sync(kAll, byte, 2 * kLanes) << 16;
@@ -209,14 +210,14 @@ __device__ __forceinline__ void emit(const Args& a, int64_t m, int tid, int step
             const int c = tid + i * step;
             const int from = kVec == 2 ? (lane & ~1) | i : kNv ? (lane & ~1) | (i >> 1) : (lane & ~3) | (i >> 1) | ((i & 1) << 1);
             const float r = __shfl_sync(kAll, rcp[kVec == 4 && kNv ? i & 1 : 0], from);
-            float q[8];
+            if (kOut != kFp8 && r >= 0.0f) {
+                if (kFull || c < cols) static_cast<uint32_t*>(a.y)[m * cols + c] = divided8(v[i], r);
+            } else {
+                float q[8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) set(q, j, lat::mul2(two(v[i], j), make_float2(r, r)));
-            if (kOut != kFp8 && r == 0.0f) {   // (NaN times 0 is no 0)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) q[j] = 0.0f;
+                for (int j = 0; j < 4; ++j) set(q, j, lat::mul2(two(v[i], j), make_float2(r, r)));
+                if (kFull || c < cols) store_codes<kOut>(a, m * cols + c, q);
             }
-            if (kFull || c < cols) store_codes<kOut>(a, m * cols + c, q);
         }
     }
 }

@@ -462,8 +462,9 @@ sgq_status sgq_latent_prefill(const void* q, int64_t q_stride_t, int64_t q_strid
  * A code is E2M1_RNE(x / s), or of x / (s t) (fp32 operations, s t rounded
  * first), saturated at +-6: one of +-{0, .5, 1, 1.5, 2, 3, 4, 6}.  A group that
  * holds a NaN or an infinity gets the NaN scale byte (255, 0x7F) and codes of
- * zero, so that what is computed from it is NaN.  t is calibrated, or
- * max|x| / (6 * 448) of the tensor.
+ * zero, so that what is computed from it is NaN.  Codes are zero, too, where
+ * s t is below fp32's smallest value.  t is calibrated, or max|x| / (6 * 448)
+ * of the tensor.
  *
  * Codes: uint8 [M, K/2], element 2i in the low half of byte i.  Scale bytes:
  * tiles of 128 rows x 4 groups (512 bytes), [ceil(M/128)][T] of them with
@@ -492,7 +493,7 @@ sgq_status sgq_latent_prefill(const void* q, int64_t q_stride_t, int64_t q_strid
 /*
  * x: [M, K], rows x_stride elements apart (x_stride % 8 == 0), or, with
  * silu_mul = 1, [M, 2K] of rows [gate | up], of which silu(gate) * up is
- * quantised (fp32, silu(g) = g / (1 + exp(-g)), within 2^-18 of its value; not
+ * quantised (fp32, silu(g) = g / (1 + exp(-g)), within 2^-17 of its value; not
  * rounded to 16 bits between; its quotients are products with 1 / s or 1 / (s t)).
  * xq, xs: codes and scale tiles.
  */

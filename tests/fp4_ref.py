@@ -50,10 +50,11 @@ def quantise(x, fmt, t=1.0):
     bad = ~np.isfinite(part).all(axis=-1)
     part = np.where(bad[..., None], np.float32(0), part)
     byte, d = scale_bytes(np.abs(part).max(axis=-1), fmt, t)
+    none = (bad | (d == 0))[..., None]       # (a product s t below fp32's smallest value stands for zeros, whatever the codes)
     with np.errstate(over="ignore"):
-        q = part / d[..., None]
+        q = np.where(none, 0, part) / np.where(none, 1, d[..., None])
     nib = nearest(np.minimum(np.abs(q), 6).astype(np.float64), LEVELS) + 8 * np.signbit(part)
-    nib = np.where(bad[..., None], 0, nib)
+    nib = np.where(none, 0, nib)
     byte = np.where(bad, 255 if fmt == "mxfp4" else 0x7F, byte)
     return nib.reshape(x.shape).astype(np.uint8), byte.astype(np.uint8)
 
@@ -102,7 +103,8 @@ def check_codes(nib, byte, x, fmt, t, d, what=""):
     lo, hi = scale_bytes(amax * (1 - d), fmt, t)[0], scale_bytes(amax * (1 + d), fmt, t)[0]
     assert ((byte >= lo) & (byte <= hi)).all(), f"{what}: scale bytes"
     s = values(np.full_like(nib, 2), byte, fmt, t)      # a code's step is in units of s
-    q, v = np.abs(x) / s, LEVELS[nib & 7]
+    assert (nib[s == 0] == 0).all(), f"{what}: codes under scales of zero"
+    q, v = np.where(s == 0, 0, np.abs(x)) / np.where(s == 0, 1, s), LEVELS[nib & 7]
     up, down = np.append(LEVELS, 9.0)[(nib & 7) + 1], LEVELS[np.maximum((nib & 7).astype(int) - 1, 0)]
     slack = d * q + 2.0 ** -22 * q
     assert (np.where(v < 6, q <= (v + up) / 2 + slack, True)).all() and (q >= np.where(v > 0, (v + down) / 2, 0) - slack).all(), \

@@ -137,6 +137,33 @@ def test_quant_silu_mul(fmt, dtype, M, K):
 
 
 @BOTH
+def test_quant_silu_mul_of_gates_far_below_zero(fmt):
+    """silu(g) is 2^-120 and less here, times u up to bf16's largest; to where exp(-g) leaves fp32."""
+    K = 512
+    g = -torch.linspace(80, 88.5, 9).bfloat16()[:, None].expand(9, K)
+    u = (torch.rand(9, K, generator=torch.Generator().manual_seed(3)) + 0.5).mul(2.0 ** 126).bfloat16()
+    q, s = sgq.quant_fp4(torch.cat([g, u], 1).to(DEV), fmt, silu_mul=True)
+    ok()
+    g, u = ref.f64(g), ref.f64(u)
+    y = g / (1 + np.exp(-g)) * u
+    # the exponent, 127 and less, is off by 2^-18 (its rounding) and 127 2^-26 (log2 e's): 1.5 2^-18 times ln 2
+    ref.check_codes(ref.unpack(q), ref.from_tiles(s, 9, K // ref.GROUP[fmt]), y, fmt, np.float32(1), 2.0 ** -17, fmt)
+
+
+@pytest.mark.parametrize("t", [2.0 ** -126, 2.0 ** -131, 2.0 ** -149])
+def test_quant_under_the_smallest_tensor_scales(t):
+    """Divisors below fp32's normal numbers, whose reciprocals are infinite; groups of zeros.  silu(32) is 32 within 2^-46."""
+    K = 1056
+    u = (randn(5, K, seed=1).float().cpu() * 2.0 ** torch.linspace(-133, -122, K // 16).repeat_interleave(16)).bfloat16()
+    u[:, 16:32] = 0
+    check_quant(u.to(DEV), "nvfp4", t)
+    q, s = sgq.quant_fp4(torch.cat([torch.full_like(u, 32.0), u], 1).to(DEV), "nvfp4", tensor_scale=one(t), silu_mul=True)
+    ok()
+    ref.check_codes(ref.unpack(q), ref.from_tiles(s, 5, K // 16), 32 * ref.f64(u), "nvfp4", np.float32(t), 2.0 ** -17)
+    assert ((ref.unpack(q) & 7)[:, 16:32] == 0).all()
+
+
+@BOTH
 @TYPES
 @pytest.mark.parametrize("M,K", [(1, 32), (129, 544), (300, 1568)])
 def test_dequant_is_the_rounded_value(fmt, dtype, M, K):

@@ -173,6 +173,49 @@ def test_rows_that_are_not_finite_and_rows_of_zeros(M):
     ok()
 
 
+@pytest.mark.parametrize("M,K", [(3, 384), (5, 1408), (6900, 1664), (10300, 1536)])
+@pytest.mark.parametrize("quant,kw", [("fp8", {}), ("fp8", dict(ue8m0=True)), ("fp8_ue8m0", {})])
+def test_fp8_groups_with_weights_that_are_not_finite(M, K, quant, kw):
+    """The FP8 quantisers' rule: a group's NaNs leave its scale to its other values, an infinity is one of them."""
+    x = torch.ones(M, K, dtype=torch.bfloat16, device=DEV)
+    w = torch.full((K,), 2.0, dtype=torch.bfloat16, device=DEV)
+    clean = sgq.rms_norm(x, w, eps=0.0, quant=quant, **kw)
+    w[5], w[130], w[256:384] = float("nan"), float("-inf"), float("nan")
+    q, s = sgq.rms_norm(x, w, eps=0.0, quant=quant, **kw)
+    ok()
+    nan = torch.zeros(K, dtype=torch.bool, device=DEV)
+    nan[5] = nan[130] = True
+    nan[256:384] = True
+    assert torch.equal((q & 0x7F) == 0x7F, nan.expand(M, K))                     # NaN, and infinity / infinity
+    assert ((q[:, 128:256] & 0x7F)[:, ~nan[128:256]] == 0).all()                 # finite / infinity
+    keep = ~nan
+    keep[128:256] = False
+    assert torch.equal(q[:, keep], clean[0][:, keep])
+    assert torch.equal(s[:, 0], clean[1][:, 0]) and torch.equal(s[:, 3:], clean[1][:, 3:])
+    assert (s[:, 1] == 255).all() if quant == "fp8_ue8m0" else torch.isposinf(s[:, 1].float()).all()
+    zero = sgq.rms_norm(torch.zeros_like(x), w.nan_to_num(1.0, 1.0, 1.0), quant=quant, **kw)[1]
+    assert torch.equal(s[:, 2], zero[:, 2])                                      # no number at all: the smallest scale
+
+
+@pytest.mark.parametrize("M,K", [(3, 384), (6900, 1664), (10300, 1536)])
+def test_nvfp4_scales_past_the_reciprocals_range(M, K):
+    """Rows of ones with eps 0: y is the weights, exactly; values and tensor scales down to fp32's smallest."""
+    x = torch.ones(M, K, dtype=torch.bfloat16, device=DEV)
+    sizes = 2.0 ** torch.linspace(-133, -120, K // 16)
+    w = (randn(K, seed=4).float().cpu().view(-1, 16) * sizes[:, None]).flatten().bfloat16()
+    w = w + 0.0                     # (no zero has a sign here: w + offset has none)
+    w[16:32] = 0
+    for t in (2.0 ** -126, 2.0 ** -131, 2.0 ** -149, 2.0 ** 120):
+        y = w if t < 1 else (w.double() * 2.0 ** 240).bfloat16()
+        q, s = sgq.rms_norm(x, y.to(DEV), eps=0.0, quant="nvfp4", tensor_scale=torch.full((1,), t, device=DEV))
+        ok()
+        nib, byte = ref.quantise(y.float().numpy()[None], "nvfp4", np.float32(t))
+        rows = slice(None) if M < 10 else [0, 1, M // 2, M - 1]
+        got = ref.unpack(q[rows])
+        assert (got == nib).all(), t
+        assert (ref.from_tiles(s, M, K // 16)[rows] == byte).all(), t
+
+
 def test_outputs_between_guards():
     """Given outputs are written to their borders and not past them."""
     for M, K in ((3, 96), (310, 1120), (9400, 1120)):
