@@ -396,6 +396,33 @@ def test_weights_written_by_the_call_before():
     ok()
 
 
+@BOTH
+def test_offsets_past_32_bits(fmt):
+    """Every 997 rows of x are the same rows, so those of each output are; 4.4e9 elements of x, 2.2e9 of D."""
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    R, T, K, N = 997, 612, 7168, 3520
+    M = R * T
+    base = randn(R, K, seed=1)
+    x = base.repeat(T, 1)
+    q, s = sgq.quant_fp4(x, fmt)
+    del x
+    bq, bs = sgq.quant_fp4(base, fmt)
+    assert (q.view(T, R, K // 2) == bq).all()
+    G = K // ref.GROUP[fmt]
+    r, j = torch.arange(M - R, M, device=DEV)[:, None], torch.arange(G, device=DEV)[None]
+    assert np.array_equal(s[r // 128, j // 4, r % 32 * 16 + r % 128 // 32 * 4 + j % 4].cpu().numpy(), ref.from_tiles(bs, R, G))
+    y, by = sgq.dequant_fp4(q, s, fmt), sgq.dequant_fp4(bq, bs, fmt)
+    assert (y.view(T, R, K) == by).all()
+    del y
+    wq, ws = sgq.quant_fp4(randn(N, K, seed=2, std=0.05), fmt)
+    d = sgq.fp4_gemm(q, s, wq, ws, fmt)
+    ok()
+    assert (d.view(T, R, N) == d[:R]).all()
+    ref.check_product(d[-R:], ref.values(ref.unpack(bq), ref.from_tiles(bs, R, G), fmt), ref.values(ref.unpack(wq), ref.from_tiles(ws, N, G), fmt),
+                  1.0, torch.bfloat16, fmt)
+
+
 def test_nothing_is_allocated_by_the_library():
     before = sgq.sgq_allocated_bytes()
     w = sgq.quant_fp4(randn(1536, 7168, seed=1), "mxfp4")

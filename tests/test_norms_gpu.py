@@ -234,6 +234,28 @@ def test_outputs_between_guards():
             assert (b[:32] == v).all() and (b[-32:] == v).all()
 
 
+@pytest.mark.parametrize("quant", [None, "fp8", "nvfp4"])
+def test_offsets_past_32_bits(quant):
+    """Every 997 rows are the same rows, so those of each output are; 4.4e9 elements of x and of h."""
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB")
+    R, T, K = 997, 612, 7168
+    base, res, w = randn(R, K, seed=1), randn(R, K, seed=2), randn(K, seed=3, std=0.2, mean=1.0)
+    got = sgq.norm_add(base.repeat(T, 1), res.repeat(T, 1), weight=w, quant=quant)
+    ok()
+    for g in got[:2] if quant == "nvfp4" else got:
+        assert (g.view(T, R, -1) == g[:R]).all()
+    assert torch.equal(got[0][:R], sgq.norm_add(base, res))
+    if quant == "nvfp4":
+        G, M = K // 16, R * T
+        r, j = torch.arange(M - R, M, device=DEV)[:, None], torch.arange(G, device=DEV)[None]
+        last = got[2][r // 128, j // 4, r % 32 * 16 + r % 128 // 32 * 4 + j % 4].cpu().numpy()
+        assert np.array_equal(last, ref.from_tiles(got[2], R, G))
+    elif quant is None:
+        y = ref.norm(ref.f64(got[0][-R:]), ref.f64(w), 1e-6, 0.0)
+        check_rounded(got[1][-R:], y, np.abs(y), torch.bfloat16, "y")
+
+
 def test_feeds_the_fp8_linear():
     """The norm's FP8 groups are what the block-scaled GEMM reads: the same D as from quantising what they stand for."""
     M, N, K = 64, 512, 2048
