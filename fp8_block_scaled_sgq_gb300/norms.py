@@ -29,8 +29,9 @@ def _target(x, M, K, quant, group, ue8m0, tensor_scale, out, out_scales, stream)
             _fail("ue8m0 goes with quant='fp8'")
         if K % 32:
             _fail(f"{K} columns are not whole groups of 32")
-        if tensor_scale is not None:
-            _scale("tensor_scale", tensor_scale, quant)
+        t = tensor_scale
+        if t is not None and (quant != "nvfp4" or t.dtype is not fp4.torch.float32 or t.numel() != 1 or t.requires_grad):
+            _scale("tensor_scale", t, quant)
         kind = binding.SGQ_OUT_MXFP4 if quant == "mxfp4" else binding.SGQ_OUT_NVFP4
         shape, scales, kept = (M, K // 2), (-(-M // 128), -(-K // _FORMAT[quant][1]), 512), u8
     elif quant == "fp8" or quant == "fp8_ue8m0":
@@ -82,7 +83,7 @@ def rms_norm(x, weight, eps: float = 1e-6, offset: float = 0.0, quant=None, grou
     dt, shape, strides = _NUMBER.get(kept), x.shape, x.stride()
     if (dt is None or len(shape) != 2 or strides[1] != 1 or weight.dtype is not kept or weight.shape != shape[1:]
             or not weight.is_contiguous() or x.get_device() != device or weight.get_device() != device
-            or t is not None or out is not None or out_scales is not None
+            or (t is not None and t.get_device() != device) or out is not None or out_scales is not None
             or (torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad))):
         dt = _dtype(x, weight)
         if x.dim() != 2:
@@ -120,7 +121,10 @@ def norm_add(x, residual, post_weight=None, gate=None, scale: float = 1.0, resid
                                    or p.get_device() != device or (graded and p.requires_grad)))
             or (w is not None and (w.dtype is not kept or w.shape != shape[1:] or not w.is_contiguous()
                                    or w.get_device() != device or (graded and w.requires_grad)))
-            or gate is not None or t is not None or h_out is not None or out is not None or out_scales is not None):
+            or (gate is not None and (gate.dtype is not kept or gate.get_device() != device
+                                      or (graded and gate.requires_grad)))
+            or (t is not None and t.get_device() != device)
+            or h_out is not None or out is not None or out_scales is not None):
         dt = _dtype(x, residual, p, gate, w, h_out)
         if x.dim() != 2:
             _fail(f"x: expected [M, K], got {tuple(shape)}")
@@ -138,11 +142,13 @@ def norm_add(x, residual, post_weight=None, gate=None, scale: float = 1.0, resid
     if gate is not None:
         if gate.dim() == 1:
             gate = gate[None]
-        G = gate.shape[0]
-        if gate.dim() != 2 or gate.shape[1] != K or (M % G if G else M):
+        G = gate.shape[0] if gate.dim() == 2 and gate.shape[1] == K else -1
+        if G < 0 or (M % G if G else M):
             _fail(f"gate: expected [K] or [G, K] with G dividing {M}, got {tuple(gate.shape)}")
-        _rows("gate", gate, G, K)
-        gs, rows = gate.stride(0) if G > 1 else K, M // G if M else 1
+        gs, unit = gate.stride()
+        if unit != 1:
+            _rows("gate", gate, G, K)
+        gs, rows = gs if G > 1 else K, M // G if M else 1
     if h_out is None:
         h_out, ht = _new(shape, kept, x, stream), K
     else:
