@@ -138,19 +138,19 @@ __device__ __forceinline__ void store_codes(const Args& a, int64_t at, const flo
 // Columns tid, tid + step, ... of row m of y, in what `out` asks for.  v: their
 // values, negated where they are to be quantised.  All lanes of a warp call
 // it, those past the row's end (zeros) too: groups lie in neighbouring lanes,
-// and are whole.
+// and are whole.  The first kSure columns are within the row for every thread.
 //
 // A group's largest magnitude, its scale and the reciprocal of it are the same
 // for all of its lanes, so they are taken once: lanes that meet in the maximum
 // over a group each keep half of the columns, until a lane owns one (two of
 // four where a group is two lanes), and hand the quotients' factors back.
-template <typename T, Out kOut, int kVec, bool kFull>
+template <typename T, Out kOut, int kVec, int kSure>
 __device__ __forceinline__ void emit(const Args& a, int64_t m, int tid, int step, const float (&v)[kVec][8], const TensorScale& ts) {
     const int cols = a.K / 8;
     if constexpr (kOut == kSame) {
 #pragma unroll
         for (int i = 0; i < kVec; ++i)
-            if (kFull || tid + i * step < cols) static_cast<uint4*>(a.y)[m * cols + tid + i * step] = pack8<T>(v[i]);
+            if (i < kSure || tid + i * step < cols) static_cast<uint4*>(a.y)[m * cols + tid + i * step] = pack8<T>(v[i]);
     } else {
         constexpr unsigned kAll = 0xFFFFFFFFu;
         constexpr bool kNv = kOut == kNv4;
@@ -187,7 +187,7 @@ __device__ __forceinline__ void emit(const Args& a, int64_t m, int tid, int step
                 const float s = fp8_scale(__uint_as_float(own[k]), a.scale_kind != 0);
                 rcp[k] = -__frcp_rn(s);
                 // the first lanes of a group, one for each column
-                if ((kFull || c < cols) && (lane & ((1 << a.group_shift) - 1)) < kVec) {
+                if ((kSure == kVec || c < cols) && (lane & ((1 << a.group_shift) - 1)) < kVec) {
                     const int64_t g = m * (cols >> a.group_shift) + (c >> a.group_shift);
                     if (a.scale_kind == 2) static_cast<uint8_t*>(a.ys)[g] = static_cast<uint8_t>(__float_as_uint(s) >> 23);
                     else static_cast<float*>(a.ys)[g] = s;
@@ -197,10 +197,10 @@ __device__ __forceinline__ void emit(const Args& a, int64_t m, int tid, int step
                 float div;
                 uint32_t byte = scale_byte<kNv>(own[k], ts, div);
                 rcp[k] = (kNv ? in_range(div) : div != 0.0f) ? minus_reciprocal<kNv>(div) : div;
-                if (!kFull && c >= cols) byte = 0;              // groups past the row's end
+                if (kSure < kVec && c >= cols) byte = 0;              // groups past the row's end
                 byte |= __shfl_down_sync(kAll, byte, kLanes) << 8;
                 byte |= __shfl_down_sync(kAll, byte, 2 * kLanes) << 16;
-                if ((kFull || c < cols) && (lane & (4 * kLanes - 1)) < (kNv ? 2 : kVec))
+                if ((kSure == kVec || c < cols) && (lane & (4 * kLanes - 1)) < (kNv ? 2 : kVec))
                     *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.ys) +
                                                  scale_word_at(m, c / (4 * kLanes), scale_tiles(a.K, kNv))) = byte;
             }
@@ -211,12 +211,12 @@ __device__ __forceinline__ void emit(const Args& a, int64_t m, int tid, int step
             const int from = kVec == 2 ? (lane & ~1) | i : kNv ? (lane & ~1) | (i >> 1) : (lane & ~3) | (i >> 1) | ((i & 1) << 1);
             const float r = __shfl_sync(kAll, rcp[kVec == 4 && kNv ? i & 1 : 0], from);
             if (kOut != kFp8 && r >= 0.0f) {
-                if (kFull || c < cols) static_cast<uint32_t*>(a.y)[m * cols + c] = divided8(v[i], r);
+                if (i < kSure || c < cols) static_cast<uint32_t*>(a.y)[m * cols + c] = divided8(v[i], r);
             } else {
                 float q[8];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) set(q, j, lat::mul2(two(v[i], j), make_float2(r, r)));
-                if (kFull || c < cols) store_codes<kOut>(a, m * cols + c, q);
+                if (i < kSure || c < cols) store_codes<kOut>(a, m * cols + c, q);
             }
         }
     }
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kRow == 32 ? 128 : kRow) norm_kernel(const Arg
 #pragma unroll
         for (int i = 0; i < kVec; ++i)
             if (tid + i * kRow < cols) weigh<T>(v[i], rstd, column<T>(a.weight, 0, tid + i * kRow), a.offset);
-        emit<T, kOut, kVec, false>(a, m, tid, kRow, v, ts);
+        emit<T, kOut, kVec, 0>(a, m, tid, kRow, v, ts);
     }
 }
 
@@ -286,9 +286,10 @@ __global__ void __launch_bounds__(kRow == 32 ? 128 : kRow) norm_kernel(const Arg
 // under way while one is summed.  Four columns a thread: what a row costs beside
 // its elements (two sums over the CTA) falls with fewer warps, and two CTAs of
 // 14 warps keep HBM busy where nothing is quantised (with two columns and twice
-// the warps every step into FP8 took 61.3 us instead of 58.4).  kFull: every
-// thread has all of its columns (K a multiple of 256 kVec), and no branch
-// stands between them (48.7 -> 38.4 us).
+// the warps every step into FP8 took 61.3 us instead of 58.4).  No
+// branch stands between a thread's columns (48.7 -> 38.4 us for every step into
+// FP8): only its last one may be none, which is zeros then.  kFull: it is none
+// nowhere (K a multiple of 256 kVec).
 __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
@@ -320,13 +321,14 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_walk_kernel(const Args a
     const int arrays = 1 + (a.residual != nullptr) + (a.gate != nullptr);
     const uint32_t array_bytes = kVec * threads * 16, row_bytes = arrays * array_bytes;
     // this thread's columns of a row: tid, tid + threads, ...
+    const bool last = kFull || tid + (kVec - 1) * threads < cols;   // whether its last column is one
     auto fetch = [&](int64_t m, uint32_t slot) {
         if (m < a.M) {
             auto row = [&](const void* p, int64_t at, uint32_t to) {
                 const T* from = static_cast<const T*>(p) + at + tid * 8;
 #pragma unroll
                 for (int i = 0; i < kVec; ++i)
-                    if (kFull || tid + i * threads < cols) copy16(to + i * threads * 16, from + i * threads * 8);
+                    if (i + 1 < kVec || last) copy16(to + i * threads * 16, from + i * threads * 8);
             };
             row(a.x, m * a.x_s, slot);
             if (a.residual) row(a.residual, m * a.r_s, slot + array_bytes);
@@ -340,21 +342,23 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_walk_kernel(const Args a
     for (int i = 0; i < kVec; ++i) {
         const int c = tid + i * threads;
         weight[i] = post[i] = make_uint4(0, 0, 0, 0);
-        if (kOut != kNone && (kFull || c < cols)) weight[i] = column<T>(a.weight, 0, c);
-        if (a.post && (kFull || c < cols)) post[i] = column<T>(a.post, 0, c);
+        if (kOut != kNone && (i + 1 < kVec || last)) weight[i] = column<T>(a.weight, 0, c);
+        if (a.post && (i + 1 < kVec || last)) post[i] = column<T>(a.post, 0, c);
     }
     const TensorScale ts(kOut == kNv4 ? a.tensor_scale : nullptr);
     int d = 0, turn = 0;
     for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x, turn ^= 1) {
         ptx::cp_async_wait_pending(a.depth - 1);
         const uint32_t slot = ring0 + d * row_bytes;
+        // this thread's column i of an array (zeros where it has none)
+        auto taken = [&](uint32_t array, int i) {
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (i + 1 < kVec || last) x = take16(array + i * threads * 16);
+            return x;
+        };
         float v[kVec][8];
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (kFull || tid + i * threads < cols) x = take16(slot + i * threads * 16);
-            unpack8<T>(x, v[i]);
-        }
+        for (int i = 0; i < kVec; ++i) unpack8<T>(taken(slot, i), v[i]);
         // (a row's first sum is met by all before the next row's is written: two sums take turns where there is no other)
         if (a.residual) {
             if (a.post) {
@@ -364,14 +368,12 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_walk_kernel(const Args a
             }
             if (a.gate) {
 #pragma unroll
-                for (int i = 0; i < kVec; ++i)
-                    if (kFull || tid + i * threads < cols) open<T>(v[i], take16(slot + 2 * array_bytes + i * threads * 16));
+                for (int i = 0; i < kVec; ++i) open<T>(v[i], taken(slot + 2 * array_bytes, i));
             }
 #pragma unroll
             for (int i = 0; i < kVec; ++i) {
-                if (!kFull && tid + i * threads >= cols) continue;
-                const uint4 h = add_residual<T>(v[i], take16(slot + array_bytes + i * threads * 16), a);
-                reinterpret_cast<uint4*>(static_cast<T*>(a.h) + m * a.h_s)[tid + i * threads] = h;
+                const uint4 h = add_residual<T>(v[i], taken(slot + array_bytes, i), a);
+                if (i + 1 < kVec || last) reinterpret_cast<uint4*>(static_cast<T*>(a.h) + m * a.h_s)[tid + i * threads] = h;
             }
         }
         float rstd = 0.0f;
@@ -382,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_walk_kernel(const Args a
             if constexpr (negated(kOut)) rstd = -rstd;
 #pragma unroll
             for (int i = 0; i < kVec; ++i) weigh<T>(v[i], rstd, weight[i], a.offset);
-            emit<T, kOut, kVec, kFull>(a, m, tid, threads, v, ts);
+            emit<T, kOut, kVec, kFull ? kVec : kVec - 1>(a, m, tid, threads, v, ts);
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -438,8 +440,9 @@ sgq_status by_width(const Args& a, int sms, cudaStream_t st) {
     // (a norm, residual, norm in a graph, us, walking / a row each: 1600 x 4096 10.0 / 8.2, 4096 x 4096 27.4 / 28.6,
     // 1216 x 7168 11.5 / 11.9, 4096 x 7168 43.6 / 53.4, 4096 x 1536 9.9 / 8.3, 16384 x 1536 35.1 / 39.8).
     const bool many = a.K > 1024 && a.K <= 16384 && a.M * a.K > (int64_t(10) << 20);
-    if (many && a.K <= 2048)
-        return a.K % 512 == 0 ? walk<T, 128, 2, 6, kOut, true>(a, sms, st) : walk<T, 128, 2, 6, kOut, false>(a, sms, st);
+    // (four columns a thread leave only the last one without some threads' part from 288 columns on)
+    if (many && a.K < 288 * 8)
+        return a.K % 512 == 0 ? walk<T, 192, 2, 4, kOut, true>(a, sms, st) : walk<T, 192, 2, 4, kOut, false>(a, sms, st);
     // (7168: as 256 threads some registers spill, 48.8 -> 53.9 us)
     if (many && a.K % 1024 == 0)
         return a.K <= 7168   ? walk<T, 224, 4, 2, kOut, true>(a, sms, st)
