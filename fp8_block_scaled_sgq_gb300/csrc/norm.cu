@@ -14,7 +14,7 @@
 // Each of x, residual, h and y passes once; a row stays in registers (8 elements
 // a 16-byte load) between its one or two sums.  Measured, 4096 x 7168 in bf16: a
 // norm 17.6 us (6.7 TB/s), residual alone 25.9 (6.8), with the next norm 40.0
-// (5.9): HBM.  Into FP8 groups 19.2 (4.6), with every step before it 38.2 (5.4):
+// (5.9): HBM.  Into FP8 groups 17.6 (5.0), with every step before it 38.2 (5.4):
 // instructions beside it, 197 a warp for 8 elements a lane.  One row: 3.2 us in a
 // graph.
 #include <cuda_runtime.h>
@@ -289,7 +289,9 @@ __global__ void __launch_bounds__(kRow == 32 ? 128 : kRow) norm_kernel(const Arg
 // the warps every step into FP8 took 61.3 us instead of 58.4).  No
 // branch stands between a thread's columns (48.7 -> 38.4 us for every step into
 // FP8): only its last one may be none, which is zeros then.  kFull: it is none
-// nowhere (K a multiple of 256 kVec).
+// nowhere (K a multiple of 256 kVec).  kAlone: without a residual; the registers
+// of a second norm's weights go to half as many warps again, which a norm into
+// FP8 or 4 bits has work for (4096 x 7168 to FP8 19.5 -> 17.6 us, NVFP4 25.2 -> 22.9).
 __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
@@ -298,7 +300,8 @@ __device__ __forceinline__ uint4 take16(uint32_t from) {
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(from) : "memory");
     return v;
 }
-// Sum over the CTA's threads (whole warps), in every one of them.
+// Sum over the CTA's threads (whole warps, up to kMost), in every one of them.
+template <int kMost>
 __device__ __forceinline__ float block_sum(float s, float* part) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
@@ -306,11 +309,11 @@ __device__ __forceinline__ float block_sum(float s, float* part) {
     __syncthreads();
     s = (threadIdx.x & 31) < (blockDim.x >> 5) ? part[threadIdx.x & 31] : 0.0f;
 #pragma unroll
-    for (int off = 8; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
-    return __shfl_sync(0xFFFFFFFFu, s, 0);   // (at most 16 warps)
+    for (int off = kMost > 512 ? 16 : 8; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
+    return kMost > 512 ? s : __shfl_sync(0xFFFFFFFFu, s, 0);
 }
 
-template <typename T, int kThreads, int kVec, int kCtas, Out kOut, bool kFull>
+template <typename T, int kThreads, int kVec, int kCtas, Out kOut, bool kFull, bool kAlone>
 __global__ void __launch_bounds__(kThreads, kCtas) norm_walk_kernel(const Args a) {
     extern __shared__ uint4 ring[];
     __shared__ float part[4][32];
@@ -318,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_walk_kernel(const Args a
     ptx::grid_dependency_wait();
     const int tid = threadIdx.x, threads = blockDim.x, cols = a.K / 8;
     const uint32_t ring0 = ptx::smem_u32(ring) + tid * 16;
-    const int arrays = 1 + (a.residual != nullptr) + (a.gate != nullptr);
+    const int arrays = kAlone ? 1 : 1 + (a.residual != nullptr) + (a.gate != nullptr);
     const uint32_t array_bytes = kVec * threads * 16, row_bytes = arrays * array_bytes;
     // this thread's columns of a row: tid, tid + threads, ...
     const bool last = kFull || tid + (kVec - 1) * threads < cols;   // whether its last column is one
@@ -331,8 +334,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_walk_kernel(const Args a
                     if (i + 1 < kVec || last) copy16(to + i * threads * 16, from + i * threads * 8);
             };
             row(a.x, m * a.x_s, slot);
-            if (a.residual) row(a.residual, m * a.r_s, slot + array_bytes);
-            if (a.gate) row(a.gate, (a.gate_rows == 1 ? m : static_cast<uint32_t>(m) / a.gate_rows) * a.gate_s, slot + 2 * array_bytes);
+            if (!kAlone && a.residual) row(a.residual, m * a.r_s, slot + array_bytes);
+            if (!kAlone && a.gate) row(a.gate, (a.gate_rows == 1 ? m : static_cast<uint32_t>(m) / a.gate_rows) * a.gate_s, slot + 2 * array_bytes);
         }
         ptx::cp_async_commit();
     };
@@ -343,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_walk_kernel(const Args a
         const int c = tid + i * threads;
         weight[i] = post[i] = make_uint4(0, 0, 0, 0);
         if (kOut != kNone && (i + 1 < kVec || last)) weight[i] = column<T>(a.weight, 0, c);
-        if (a.post && (i + 1 < kVec || last)) post[i] = column<T>(a.post, 0, c);
+        if (!kAlone && a.post && (i + 1 < kVec || last)) post[i] = column<T>(a.post, 0, c);
     }
     const TensorScale ts(kOut == kNv4 ? a.tensor_scale : nullptr);
     int d = 0, turn = 0;
@@ -360,9 +363,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_walk_kernel(const Args a
 #pragma unroll
         for (int i = 0; i < kVec; ++i) unpack8<T>(taken(slot, i), v[i]);
         // (a row's first sum is met by all before the next row's is written: two sums take turns where there is no other)
-        if (a.residual) {
+        if (!kAlone && a.residual) {
             if (a.post) {
-                const float rstd = rstd_of(block_sum(squares(v), part[2 * turn]), a);
+                const float rstd = rstd_of(block_sum<kThreads>(squares(v), part[2 * turn]), a);
 #pragma unroll
                 for (int i = 0; i < kVec; ++i) weigh<T>(v[i], rstd, post[i], a.offset);
             }
@@ -377,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_walk_kernel(const Args a
             }
         }
         float rstd = 0.0f;
-        if constexpr (kOut != kNone) rstd = rstd_of(block_sum(squares(v), part[2 * turn + 1]), a);
+        if constexpr (kOut != kNone) rstd = rstd_of(block_sum<kThreads>(squares(v), part[2 * turn + 1]), a);
         fetch(m + int64_t(a.depth) * gridDim.x, slot);   // (what was in the slot has been used)
         if (++d == a.depth) d = 0;
         if constexpr (kOut != kNone) {
@@ -390,13 +393,13 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_walk_kernel(const Args a
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-template <typename T, int kThreads, int kVec, int kCtas, Out kOut, bool kFull>
+template <typename T, int kThreads, int kVec, int kCtas, Out kOut, bool kFull, bool kAlone>
 sgq_status walk(Args a, int sms, cudaStream_t st) {
     const int cols = a.K / 8, threads = (cols + 32 * kVec - 1) / (32 * kVec) * 32;
     const int ctas = kThreads * kCtas / threads, share = 208 * 1024 / ctas;
     const int row_bytes = (1 + (a.residual != nullptr) + (a.gate != nullptr)) * kVec * threads * 16;
     a.depth = share / row_bytes < 4 ? share / row_bytes : 4;
-    auto kern = norm_walk_kernel<T, kThreads, kVec, kCtas, kOut, kFull>;
+    auto kern = norm_walk_kernel<T, kThreads, kVec, kCtas, kOut, kFull, kAlone>;
     static bool configured[64] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SGQ_ERR_CUDA;
@@ -417,6 +420,12 @@ sgq_status walk(Args a, int sms, cudaStream_t st) {
     if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) return SGQ_ERR_CUDA;
     note_launch();
     return SGQ_OK;
+}
+
+template <typename T, int kThreads, int kVec, int kCtas, Out kOut, bool kAlone>
+sgq_status walk_rows(const Args& a, int sms, cudaStream_t st) {
+    return a.K % (256 * kVec) == 0 ? walk<T, kThreads, kVec, kCtas, kOut, true, kAlone>(a, sms, st)
+                                   : walk<T, kThreads, kVec, kCtas, kOut, false, kAlone>(a, sms, st);
 }
 
 template <typename T, int kRow, int kVec, Out kOut>
@@ -441,14 +450,16 @@ sgq_status by_width(const Args& a, int sms, cudaStream_t st) {
     // 1216 x 7168 11.5 / 11.9, 4096 x 7168 43.6 / 53.4, 4096 x 1536 9.9 / 8.3, 16384 x 1536 35.1 / 39.8).
     const bool many = a.K > 1024 && a.K <= 16384 && a.M * a.K > (int64_t(10) << 20);
     // (four columns a thread leave only the last one without some threads' part from 288 columns on)
-    if (many && a.K < 288 * 8)
-        return a.K % 512 == 0 ? walk<T, 192, 2, 4, kOut, true>(a, sms, st) : walk<T, 192, 2, 4, kOut, false>(a, sms, st);
-    // (7168: as 256 threads some registers spill, 48.8 -> 53.9 us)
-    if (many && a.K % 1024 == 0)
-        return a.K <= 7168   ? walk<T, 224, 4, 2, kOut, true>(a, sms, st)
-               : a.K <= 8192 ? walk<T, 256, 4, 2, kOut, true>(a, sms, st)
-                             : walk<T, 512, 4, 1, kOut, true>(a, sms, st);
-    if (many) return a.K <= 8192 ? walk<T, 256, 4, 2, kOut, false>(a, sms, st) : walk<T, 512, 4, 1, kOut, false>(a, sms, st);
+    const bool four = a.K >= 288 * 8;
+    if constexpr (negated(kOut)) {
+        if (many && !a.residual && a.K <= 12288 && (four || a.K % 1024 == 0))
+            return a.K <= 8192 ? walk_rows<T, 256, 4, 3, kOut, true>(a, sms, st) : walk_rows<T, 384, 4, 2, kOut, true>(a, sms, st);
+    }
+    if (many && !four) return walk_rows<T, 192, 2, 4, kOut, false>(a, sms, st);
+    if (many && a.K <= 8192) return walk_rows<T, 256, 4, 2, kOut, false>(a, sms, st);
+    // (9216 to 12288: two columns keep 18 to 24 warps busy, four 9 to 12; norm, residual, norm into NVFP4 of 3255 x 9216 45.7 -> 39.7 us)
+    if (many && a.K <= 12288) return walk_rows<T, 768, 2, 1, kOut, false>(a, sms, st);
+    if (many) return walk_rows<T, 512, 4, 1, kOut, false>(a, sms, st);
     if (a.K <= 1024) return run<T, 32, 4, kOut>(a, st);
     if (a.K <= 2048) return run<T, 128, 2, kOut>(a, st);
     if (a.K <= 4096) return run<T, 256, 2, kOut>(a, st);
