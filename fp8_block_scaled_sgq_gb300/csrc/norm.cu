@@ -15,7 +15,7 @@
 // a 16-byte load) between its one or two sums.  Measured, 4096 x 7168 in bf16: a
 // norm 17.6 us (6.7 TB/s), residual alone 25.9 (6.8), with the next norm 40.0
 // (5.9): HBM.  Into FP8 groups 17.6 (5.0), with every step before it 38.2 (5.4):
-// instructions beside it, 197 a warp for 8 elements a lane.  One row: 3.2 us in a
+// instructions beside it, 204 a warp for 8 elements a lane.  One row: 3.2 us in a
 // graph.
 #include <cuda_runtime.h>
 
