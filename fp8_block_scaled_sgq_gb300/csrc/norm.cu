@@ -445,10 +445,13 @@ sgq_status run(const Args& a, cudaStream_t st) {
 }
 template <typename T, Out kOut>
 sgq_status by_width(const Args& a, int sms, cudaStream_t st) {
-    // CTAs walk where the rows are more than L2 holds and come from HBM; a CTA a row is sooner done with what is in L2
-    // (a norm, residual, norm in a graph, us, walking / a row each: 1600 x 4096 10.0 / 8.2, 4096 x 4096 27.4 / 28.6,
-    // 1216 x 7168 11.5 / 11.9, 4096 x 7168 43.6 / 53.4, 4096 x 1536 9.9 / 8.3, 16384 x 1536 35.1 / 39.8).
-    const bool many = a.K > 1024 && a.K <= 16384 && a.M * a.K > (int64_t(10) << 20);
+    // CTAs walk where there are more rows than CTAs of norm_kernel at once, 1024 threads an SM; up to 2048 elements, where
+    // the rows are more than L2 holds (a norm / residual and norm / every step into FP8 in a graph, us, a row each ->
+    // walking: 456 x 5120 3.9 / 4.5 / 7.3 -> 3.1 / 3.6 / 4.6, 1024 x 4096 4.5 / 5.3 / 7.8 -> 4.1 / 5.3 / 7.6, 1024 x 7168
+    // 7.1 / 8.5 / 13.3 -> 5.7 / 8.0 / 12.3, 456 x 16384 7.2 / 8.8 / 13.3 -> 5.7 / 8.1 / 10.7; but 304 x 7168 2.8 / 3.2 / 4.5
+    // -> 3.0 / 3.5 / 4.7, 2432 x 2048 4.6 / 5.5 / 8.0 -> 4.7 / 6.0 / 9.6).
+    const int64_t wave = int64_t(sms) * (a.K <= 4096 ? 4 : a.K <= 8192 ? 2 : 1);
+    const bool many = a.K > 2048 ? a.K <= 16384 && a.M > wave : a.K > 1024 && a.M * a.K > (int64_t(10) << 20);
     // (four columns a thread leave only the last one without some threads' part from 288 columns on)
     const bool four = a.K >= 288 * 8;
     if constexpr (negated(kOut)) {
