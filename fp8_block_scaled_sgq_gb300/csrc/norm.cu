@@ -41,11 +41,11 @@ struct Args {
     float inv_k, eps, offset, scale, residual_scale;
 };
 
-// Sum over the kRow threads of a row (whole warps), in every one of them.
+// Sum over the kRow threads of a row (16 neighbouring lanes, or whole warps), in every one of them.
 template <int kRow>
 __device__ __forceinline__ float row_sum(float s, float* part) {
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
+    for (int off = kRow < 32 ? kRow / 2 : 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
     if constexpr (kRow > 32) {
         if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
         __syncthreads();
@@ -138,15 +138,14 @@ __device__ __forceinline__ void store_codes(const Args& a, int64_t at, const flo
 // Columns tid, tid + step, ... of row m of y, in what `out` asks for.  v: their
 // values, negated where they are to be quantised.  All lanes of a warp call
 // it, those past the row's end (zeros) too: groups lie in neighbouring lanes,
-// and are whole.  The first kSure columns are within the row for every thread.
+// and are whole.  cols: the row's, or 0 for none.  The first kSure columns are within the row for every thread.
 //
 // A group's largest magnitude, its scale and the reciprocal of it are the same
 // for all of its lanes, so they are taken once: lanes that meet in the maximum
 // over a group each keep half of the columns, until a lane owns one (two of
 // four where a group is two lanes), and hand the quotients' factors back.
 template <typename T, Out kOut, int kVec, int kSure>
-__device__ __forceinline__ void emit(const Args& a, int64_t m, int tid, int step, const float (&v)[kVec][8], const TensorScale& ts) {
-    const int cols = a.K / 8;
+__device__ __forceinline__ void emit(const Args& a, int64_t m, int cols, int tid, int step, const float (&v)[kVec][8], const TensorScale& ts) {
     if constexpr (kOut == kSame) {
 #pragma unroll
         for (int i = 0; i < kVec; ++i)
@@ -154,8 +153,8 @@ __device__ __forceinline__ void emit(const Args& a, int64_t m, int tid, int step
     } else {
         constexpr unsigned kAll = 0xFFFFFFFFu;
         constexpr bool kNv = kOut == kNv4;
-        constexpr int kOwn = kNv ? kVec / 2 : 1;
-        static_assert(kVec == 2 || kVec == 4, "columns a thread");
+        constexpr int kOwn = kNv && kVec == 4 ? 2 : 1;
+        static_assert(kVec == 1 || kVec == 2 || kVec == 4, "columns a thread");
         const int lane = threadIdx.x & 31;
         const bool odd1 = (lane & 1) != 0, odd2 = (lane & 2) != 0;
         uint32_t top[kVec], own[2];
@@ -171,8 +170,9 @@ __device__ __forceinline__ void emit(const Args& a, int64_t m, int tid, int step
                 first += odd2 ? 1 : 0;
             }
         } else {
-            own[0] = max(odd1 ? top[1] : top[0], __shfl_xor_sync(kAll, odd1 ? top[0] : top[1], 1));
-            first = odd1 ? 1 : 0;
+            if constexpr (kVec == 2) own[0] = max(odd1 ? top[1] : top[0], __shfl_xor_sync(kAll, odd1 ? top[0] : top[1], 1));
+            else own[0] = max(top[0], __shfl_xor_sync(kAll, top[0], 1));
+            first = kVec == 2 && odd1 ? 1 : 0;
             if constexpr (!kNv) own[0] = max(own[0], __shfl_xor_sync(kAll, own[0], 2));
         }
         if (kOut == kFp8 && a.group_shift == 4) {
@@ -200,7 +200,7 @@ __device__ __forceinline__ void emit(const Args& a, int64_t m, int tid, int step
                 if (kSure < kVec && c >= cols) byte = 0;              // groups past the row's end
                 byte |= __shfl_down_sync(kAll, byte, kLanes) << 8;
                 byte |= __shfl_down_sync(kAll, byte, 2 * kLanes) << 16;
-                if ((kSure == kVec || c < cols) && (lane & (4 * kLanes - 1)) < (kNv ? 2 : kVec))
+                if ((kSure == kVec || c < cols) && (lane & (4 * kLanes - 1)) < (kNv && kVec > 1 ? 2 : kVec))
                     *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.ys) +
                                                  scale_word_at(m, c / (4 * kLanes), scale_tiles(a.K, kNv))) = byte;
             }
@@ -208,7 +208,7 @@ __device__ __forceinline__ void emit(const Args& a, int64_t m, int tid, int step
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
             const int c = tid + i * step;
-            const int from = kVec == 2 ? (lane & ~1) | i : kNv ? (lane & ~1) | (i >> 1) : (lane & ~3) | (i >> 1) | ((i & 1) << 1);
+            const int from = kVec == 1 ? lane : kVec == 2 ? (lane & ~1) | i : kNv ? (lane & ~1) | (i >> 1) : (lane & ~3) | (i >> 1) | ((i & 1) << 1);
             const float r = __shfl_sync(kAll, rcp[kVec == 4 && kNv ? i & 1 : 0], from);
             if (kOut != kFp8 && r >= 0.0f) {
                 if (i < kSure || c < cols) static_cast<uint32_t*>(a.y)[m * cols + c] = divided8(v[i], r);
@@ -223,17 +223,87 @@ __device__ __forceinline__ void emit(const Args& a, int64_t m, int tid, int step
 }
 __host__ __device__ constexpr bool negated(Out out) { return out == kFp8 || out == kMx4 || out == kNv4; }
 
-// Few rows, or narrow ones: kRow threads a row, each with up to kVec columns of
-// 8 elements, kRow columns apart; a CTA does one row (four, a warp each, where
-// kRow is 32) and ends.
+// Narrow rows, up to 512 elements: kRow lanes a row (two rows a warp where they
+// are 16), and kN steps of them at once, so that enough loads are under way.  A
+// grid that fills the SMs walks over them: 234375 x 128 in 16 bits 22.2 us (5.4
+// TB/s), with a residual 42.0, into FP8 27.4 (a warp a row in CTAs of four rows:
+// 97.8, 130.9, 114.1).
+template <typename T, int kRow, int kVec, int kN, Out kOut>
+__global__ void __launch_bounds__(128, kVec == 2 ? 5 : 6) norm_rows_kernel(const Args a) {
+    ptx::launch_dependents();
+    ptx::grid_dependency_wait();
+    const int lane = threadIdx.x & 31, tid = lane & (kRow - 1), cols = a.K / 8;
+    constexpr int kRows = 32 / kRow;   // of a warp
+    uint4 weight[kVec], post[kVec];
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+        const int c = tid + i * kRow;
+        weight[i] = post[i] = make_uint4(0, 0, 0, 0);
+        if (kOut != kNone && c < cols) weight[i] = column<T>(a.weight, 0, c);
+        if (a.post && c < cols) post[i] = column<T>(a.post, 0, c);
+    }
+    const TensorScale ts(kOut == kNv4 ? a.tensor_scale : nullptr);
+    const int64_t step = int64_t(gridDim.x) * 4 * kRows * kN;
+    for (int64_t m0 = (int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5)) * kRows * kN; m0 < a.M; m0 += step) {
+        uint4 x[kN][kVec], r[kN][kVec];
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+            const int64_t m = m0 + n * kRows + lane / kRow;
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) {
+                const int c = tid + i * kRow;
+                x[n][i] = r[n][i] = make_uint4(0, 0, 0, 0);
+                if (m < a.M && c < cols) {   // (x and residual may be h: plain loads)
+                    x[n][i] = reinterpret_cast<const uint4*>(static_cast<const T*>(a.x) + m * a.x_s)[c];
+                    if (a.residual) r[n][i] = reinterpret_cast<const uint4*>(static_cast<const T*>(a.residual) + m * a.r_s)[c];
+                }
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+            const int64_t m = m0 + n * kRows + lane / kRow;
+            const int live = m < a.M ? cols : 0;
+            float v[kVec][8];
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) unpack8<T>(x[n][i], v[i]);
+            if (a.residual) {
+                if (a.post) {
+                    const float rstd = rstd_of(row_sum<kRow>(squares(v), nullptr), a);
+#pragma unroll
+                    for (int i = 0; i < kVec; ++i) weigh<T>(v[i], rstd, post[i], a.offset);
+                }
+                if (a.gate) {
+                    const int64_t at = static_cast<uint32_t>(m) / a.gate_rows * a.gate_s;
+#pragma unroll
+                    for (int i = 0; i < kVec; ++i)
+                        if (tid + i * kRow < live) open<T>(v[i], column<T>(a.gate, at, tid + i * kRow));
+                }
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) {
+                    const uint4 h = add_residual<T>(v[i], r[n][i], a);
+                    if (tid + i * kRow < live) reinterpret_cast<uint4*>(static_cast<T*>(a.h) + m * a.h_s)[tid + i * kRow] = h;
+                }
+            }
+            if constexpr (kOut != kNone) {
+                float rstd = rstd_of(row_sum<kRow>(squares(v), nullptr), a);
+                if constexpr (negated(kOut)) rstd = -rstd;
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) weigh<T>(v[i], rstd, weight[i], a.offset);
+                emit<T, kOut, kVec, 0>(a, m, live, tid, kRow, v, ts);
+            }
+        }
+    }
+}
+
+// Few rows: a CTA of kRow threads each, with up to kVec columns of 8 elements a
+// thread, kRow columns apart.
 template <typename T, int kRow, int kVec, Out kOut>
-__global__ void __launch_bounds__(kRow == 32 ? 128 : kRow) norm_kernel(const Args a) {
+__global__ void __launch_bounds__(kRow) norm_kernel(const Args a) {
     __shared__ float part[2][32];
     ptx::launch_dependents();
     ptx::grid_dependency_wait();
-    const int tid = kRow == 32 ? threadIdx.x & 31 : threadIdx.x;
-    const int64_t m = kRow == 32 ? int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5) : int64_t(blockIdx.x);
-    if (m >= a.M) return;   // (a whole warp, which meets no other)
+    const int tid = threadIdx.x;
+    const int64_t m = blockIdx.x;
     const int cols = a.K / 8;
 
     float v[kVec][8];
@@ -275,11 +345,11 @@ __global__ void __launch_bounds__(kRow == 32 ? 128 : kRow) norm_kernel(const Arg
 #pragma unroll
         for (int i = 0; i < kVec; ++i)
             if (tid + i * kRow < cols) weigh<T>(v[i], rstd, column<T>(a.weight, 0, tid + i * kRow), a.offset);
-        emit<T, kOut, kVec, 0>(a, m, tid, kRow, v, ts);
+        emit<T, kOut, kVec, 0>(a, m, cols, tid, kRow, v, ts);
     }
 }
 
-// Many rows of more than 1024 elements (by_width): the grid fills the SMs once, and each
+// Many rows of more than 512 elements (by_width): the grid fills the SMs once, and each
 // CTA walks over rows, its weights in registers.  Every thread copies its own
 // columns of the next rows into shared memory (cp.async, 16 bytes each, read
 // back by that thread alone), so that `depth` rows of x, residual and gate are
@@ -387,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_walk_kernel(const Args a
             if constexpr (negated(kOut)) rstd = -rstd;
 #pragma unroll
             for (int i = 0; i < kVec; ++i) weigh<T>(v[i], rstd, weight[i], a.offset);
-            emit<T, kOut, kVec, kFull ? kVec : kVec - 1>(a, m, tid, threads, v, ts);
+            emit<T, kOut, kVec, kFull ? kVec : kVec - 1>(a, m, cols, tid, threads, v, ts);
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -434,8 +504,8 @@ sgq_status run(const Args& a, cudaStream_t st) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(kRow == 32 ? (a.M + 3) / 4 : a.M));
-    cfg.blockDim = dim3(kRow == 32 ? 128 : kRow);
+    cfg.gridDim = dim3(static_cast<unsigned>(a.M));
+    cfg.blockDim = dim3(kRow);
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -443,15 +513,39 @@ sgq_status run(const Args& a, cudaStream_t st) {
     note_launch();
     return SGQ_OK;
 }
+template <typename T, int kRow, int kVec, int kN, Out kOut>
+sgq_status narrow(const Args& a, int sms, cudaStream_t st) {
+    // rows that all fit at once: one step of one row for each warp
+    if (kN > 1 && a.M <= int64_t(sms) * 16 * (32 / kRow)) return narrow<T, kRow, kVec, 1, kOut>(a, sms, st);
+    auto kern = norm_rows_kernel<T, kRow, kVec, kN, kOut>;
+    static const int fit = [&] {   // CTAs an SM
+        int n = 0;
+        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, 128, 0) == cudaSuccess ? n : 0;
+    }();
+    if (fit <= 0) return SGQ_ERR_CUDA;
+    const int64_t rows = 4 * (32 / kRow) * kN, want = (a.M + rows - 1) / rows, most = int64_t(sms) * fit;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(want < most ? want : most));
+    cfg.blockDim = dim3(128);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) return SGQ_ERR_CUDA;
+    note_launch();
+    return SGQ_OK;
+}
 template <typename T, Out kOut>
 sgq_status by_width(const Args& a, int sms, cudaStream_t st) {
-    // CTAs walk where there are more rows than CTAs of norm_kernel at once, 1024 threads an SM; up to 2048 elements, where
+    // CTAs walk where there are more rows than CTAs of norm_kernel at once, 1024 threads an SM; 513 to 2048 elements, where
     // the rows are more than L2 holds (a norm / residual and norm / every step into FP8 in a graph, us, a row each ->
     // walking: 456 x 5120 3.9 / 4.5 / 7.3 -> 3.1 / 3.6 / 4.6, 1024 x 4096 4.5 / 5.3 / 7.8 -> 4.1 / 5.3 / 7.6, 1024 x 7168
     // 7.1 / 8.5 / 13.3 -> 5.7 / 8.0 / 12.3, 456 x 16384 7.2 / 8.8 / 13.3 -> 5.7 / 8.1 / 10.7; but 304 x 7168 2.8 / 3.2 / 4.5
     // -> 3.0 / 3.5 / 4.7, 2432 x 2048 4.6 / 5.5 / 8.0 -> 4.7 / 6.0 / 9.6).
     const int64_t wave = int64_t(sms) * (a.K <= 4096 ? 4 : a.K <= 8192 ? 2 : 1);
-    const bool many = a.K > 2048 ? a.K <= 16384 && a.M > wave : a.K > 1024 && a.M * a.K > (int64_t(10) << 20);
+    const bool many = a.K > 2048 ? a.K <= 16384 && a.M > wave : a.K > 512 && a.M * a.K > (int64_t(10) << 20);
     // (four columns a thread leave only the last one without some threads' part from 288 columns on)
     const bool four = a.K >= 288 * 8;
     if constexpr (negated(kOut)) {
@@ -463,7 +557,10 @@ sgq_status by_width(const Args& a, int sms, cudaStream_t st) {
     // (9216 to 12288: two columns keep 18 to 24 warps busy, four 9 to 12; norm, residual, norm into NVFP4 of 3255 x 9216 45.7 -> 39.7 us)
     if (many && a.K <= 12288) return walk_rows<T, 768, 2, 1, kOut, false>(a, sms, st);
     if (many) return walk_rows<T, 512, 4, 1, kOut, false>(a, sms, st);
-    if (a.K <= 1024) return run<T, 32, 4, kOut>(a, st);
+    if (a.K <= 128) return narrow<T, 16, 1, 4, kOut>(a, sms, st);
+    if (a.K <= 256) return narrow<T, 32, 1, 4, kOut>(a, sms, st);
+    if (a.K <= 512) return narrow<T, 32, 2, 2, kOut>(a, sms, st);
+    if (a.K <= 1024) return run<T, 64, 2, kOut>(a, st);
     if (a.K <= 2048) return run<T, 128, 2, kOut>(a, st);
     if (a.K <= 4096) return run<T, 256, 2, kOut>(a, st);
     if (a.K <= 8192) return run<T, 512, 2, kOut>(a, st);
