@@ -123,6 +123,16 @@ def test_every_step_and_form(many, add, post, gate, quant, kw):
         run(walking(K) if many else 5, K, torch.bfloat16 if K != 1536 else torch.float16, add, post, gate, quant, **kw)
 
 
+@pytest.mark.parametrize("quant", [None, "fp8", "mxfp4", "nvfp4"])
+@pytest.mark.parametrize("K", [32, 64, 128, 160, 256, 288, 512, 544, 768, 1024])
+@pytest.mark.parametrize("M", [9731, 41002])
+def test_many_narrow_rows(quant, K, M):
+    """More rows than fit at once: several a warp and step, the last step not whole; in place, too."""
+    kw = dict(group=32) if quant == "fp8" else {}
+    run(M, K, torch.bfloat16, False, False, "none", quant, **kw)
+    run(M, K, torch.bfloat16, True, True, "token" if M < 10000 else "some", quant, in_place="residual", **kw)
+
+
 @pytest.mark.parametrize("quant", ["mxfp4", "nvfp4"])
 @pytest.mark.parametrize("K", [32, 96, 1056, 7200, 9248, 32768])
 @pytest.mark.parametrize("M", [3, 320, "walking"])
