@@ -32,7 +32,7 @@ using lat::Pair;
 constexpr float kMax = 6.0f;            // largest E2M1 value
 constexpr uint32_t kNanE8 = 0xFFu;      // NaN as UE8M0
 constexpr uint32_t kNanE4 = 0x7Fu;      // NaN as E4M3
-constexpr float kMinE4 = 0.001953125f;  // 2^-9, the smallest E4M3 value above 0
+constexpr float kMaxE4 = 448.0f;        // the largest
 constexpr uint32_t kInf = 0x7F800000u;
 
 __host__ __device__ constexpr int group_of(bool nv) { return nv ? 16 : 32; }
@@ -84,6 +84,7 @@ __device__ __forceinline__ bool in_range(float d) { return d >= 0x1p-60f && d <=
 // "Computation of elementary functions on the IBM RISC System/6000 processor",
 // 1990, theorem on the last step of a division).  Remainders are exact while
 // nothing leaves fp32's normal range: other divisors take the division itself.
+// A quotient past fp32's largest value comes out as NaN.
 __device__ __forceinline__ float quotient(float x, float d, float r) {
     float q = __fmul_rn(x, r);
     q = __fmaf_rn(-__fmaf_rn(q, d, -x), r, q);
@@ -110,8 +111,10 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits, const TensorS
     }
     const float amax = __uint_as_float(amax_bits);
     if constexpr (kNv) {
-        // (a quotient that the corrections do not settle is far below 2^-9)
-        const uint32_t b = max(e4m3_of(ts.r6 != 0.0f ? quotient(amax, ts.t6, ts.r6) : __fdiv_rn(amax, ts.t6)), 1u);
+        // (a quotient that the corrections do not settle is far below 2^-9, or past fp32's largest value: it is infinite
+        // then, and the corrections make infinity - infinity of it, NaN, of which fminf takes the other operand)
+        const float q = ts.r6 != 0.0f ? quotient(amax, ts.t6, ts.r6) : __fdiv_rn(amax, ts.t6);
+        const uint32_t b = max(e4m3_of(fminf(q, kMaxE4)), 1u);
         div = __fmul_rn(of_e4m3(b), ts.t);
         return b;
     } else {

@@ -62,8 +62,8 @@ __device__ __forceinline__ uint32_t amax_bits16(const uint4& a, const uint4& b) 
     return __float_as_uint(Pair<T>::unpack(m).x);
 }
 
-// A group under a tensor scale of an extreme size, by divisions: scale byte
-// and codes.  (Out of line: with it inline the arrays of quant_rows went
+// A group under a tensor scale of an extreme size, or far past its tensor
+// scale, by divisions: scale byte and codes.  (Out of line: with it inline the arrays of quant_rows went
 // through local memory, 16.3 -> 21.4 us.)
 template <typename T>
 __device__ __noinline__ uint4 extreme_group(uint4 a, uint4 b, uint32_t amax, float t, float t6) {
@@ -90,7 +90,8 @@ __device__ __noinline__ uint4 extreme_group(uint4 a, uint4 b, uint32_t amax, flo
 // even with an approximate reciprocal: compared with the division for each
 // significand of x and of d, over quotients from 2^-4 to 2^5, no code differs
 // (without the correction 319 of 8.6e9 do in bf16, 2202 of 6.9e10 in fp16).
-// Divisors outside in_range divide.
+// Divisors outside in_range divide, and so does what is so far past its tensor
+// scale that a quotient leaves fp32.
 template <typename T, bool kNv, int kN>
 __device__ __forceinline__ void quant_rows(const uint4 (&raw)[kN][2], const TensorScale& ts, uint32_t (&byte)[kN], uint2 (&q)[kN]) {
     uint32_t amax[kN];
@@ -101,11 +102,11 @@ __device__ __forceinline__ void quant_rows(const uint4 (&raw)[kN][2], const Tens
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
         if constexpr (kNv) {
-            // (NaN and infinity come out as the NaN byte)
+            // (NaN and infinity come out as the NaN byte, and so does a finite group whose quotient leaves fp32, which is divided)
             byte[i] = max(e4m3_of(quotient(__uint_as_float(amax[i]), ts.t6, ts.r6)), 1u);
             div[i] = __fmul_rn(of_e4m3(byte[i]), ts.t);
             asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r[i]) : "f"(div[i]));
-            odd |= !in_range(div[i]) && byte[i] != kNanE4;
+            odd |= byte[i] == kNanE4 ? amax[i] < kInf : !in_range(div[i]);
         } else {
             amax[i] = max(amax[i], __shfl_xor_sync(0xFFFFFFFFu, amax[i], 1));
             byte[i] = scale_byte<false>(amax[i], ts, div[i]);

@@ -1,0 +1,75 @@
+"""4-bit linears and the norms into 4 bits on the GPU, where values or tensor scales are at the ends of fp32."""
+import numpy as np
+import pytest
+import torch
+
+import fp8_block_scaled_sgq_gb300 as sgq
+import fp4_ref as ref
+from test_fp4_gpu import check_quant, ok, one
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+#: Tensor scales and a group's largest magnitude, of which amax / (6 t) is past fp32's largest value, next to it on both
+#: sides, or far below it.
+FAR = [(1e-2, 3e38), (1e-10, 1e30), (2.0 ** -61, 2.0 ** 70), (2.0 ** -20, 2.0 ** 120), (2.0 ** -57, 2.0 ** 73.7), (2.0 ** -57, 2.0 ** 73.5),
+       (2.0 ** -57, 2.0 ** 20), (2.0 ** -70, 2.0 ** 100)]
+
+
+def groups(rows, K, top, seed=0):
+    """bf16 [rows, K]: groups of 16 with values up to `top`, of both signs; among them groups of small values, of zeros, with a NaN
+    and with an infinity."""
+    g = torch.Generator().manual_seed(seed)
+    x = (torch.rand(rows, K // 16, 16, generator=g, dtype=torch.float64) * 1.9 - 0.95) * top
+    x[..., 0] = top * torch.where(torch.rand(rows, K // 16, generator=g) < 0.5, -1.0, 1.0).double()
+    x[:, 1] *= 1e-30
+    x[:, 2] = 0
+    x = x.clamp(-3.3e38, 3.3e38).flatten(1).bfloat16()
+    if rows > 2:
+        x[1, 5], x[2, K - 1] = float("nan"), -float("inf")
+    return x
+
+
+# ---------------------------------------------------------------- groups far past their tensor scale saturate
+
+@pytest.mark.parametrize("t,top", FAR)
+@pytest.mark.parametrize("M,K", [(1, 64), (5, 512), (300, 1056)])
+def test_quant_of_groups_far_past_their_tensor_scale(t, top, M, K):
+    """s = min(amax / (6 t), 448) and codes of +-6, however large the quotient is: no finite group becomes NaN."""
+    x = groups(M, K, top)
+    q, s = check_quant(x.to(DEV), "nvfp4", t)
+    finite = torch.isfinite(x).view(M, -1, 16).all(-1).numpy()
+    byte = ref.from_tiles(s, M, K // 16)
+    assert ((byte == 0x7F) == ~finite).all()
+
+
+@pytest.mark.parametrize("t,top", FAR)
+@pytest.mark.parametrize("M,K", [(1, 64), (300, 1056)])
+def test_silu_of_groups_far_past_their_tensor_scale(t, top, M, K):
+    """silu(32) is 32 within 2^-46, so values are 32 u within 2^-17."""
+    u = groups(M, K, top / 40)
+    x = torch.cat([torch.full_like(u, 32.0), u], 1).to(DEV)
+    q, s = sgq.quant_fp4(x, "nvfp4", tensor_scale=one(t), silu_mul=True)
+    ok()
+    finite = torch.isfinite(u).view(M, -1, 16).all(-1).numpy()
+    nib, byte = ref.unpack(q), ref.from_tiles(s, M, K // 16)
+    assert ((byte == 0x7F) == ~finite).all()
+    bad = np.repeat(~finite, 16, axis=1)
+    assert (nib[bad] == 0).all()
+    rows = finite.all(axis=1)
+    with np.errstate(over="ignore"):
+        ref.check_codes(nib[rows], byte[rows], 32 * ref.f64(u)[rows], "nvfp4", np.float32(t), 2.0 ** -17)
+
+
+@pytest.mark.parametrize("t,top", FAR)
+@pytest.mark.parametrize("M,K", [(3, 384), (41002, 128), (6900, 1664), (10300, 1536)])
+def test_norm_of_groups_far_past_their_tensor_scale(t, top, M, K):
+    """Rows of ones with eps 0: y is the weights, exactly (a CTA a row, narrow rows, CTAs that walk)."""
+    w = groups(1, K, top)[0] + 0.0                  # (w + offset: no zero has a sign)
+    x = torch.ones(M, K, dtype=torch.bfloat16, device=DEV)
+    q, s = sgq.rms_norm(x, w.to(DEV), eps=0.0, quant="nvfp4", tensor_scale=one(t))
+    ok()
+    nib, byte = ref.quantise(w.float().numpy()[None], "nvfp4", np.float32(t))
+    rows = slice(None) if M < 10 else [0, 1, M // 2, M - 1]
+    assert (ref.from_tiles(s, M, K // 16)[rows] == byte).all()
+    assert (ref.unpack(q[rows]) == nib).all()
