@@ -1,0 +1,15 @@
+"""4-bit linears and norms without a GPU: tensor scales of unusual tensors."""
+import torch
+
+import fp8_block_scaled_sgq_gb300 as sgq
+
+
+def test_tensor_scale_is_of_the_finite_values():
+    """An infinity or a NaN makes its own group NaN: the tensor's scale stays positive and finite, the one of the other values."""
+    x = torch.tensor([[1.0, -13.44], [0.0, 2.0]]).bfloat16()
+    for dtype in (torch.bfloat16, torch.float16, torch.float32):
+        clean = sgq.fp4_tensor_scale(x.to(dtype))
+        for bad in (float("inf"), -float("inf"), float("nan")):
+            y = torch.cat([x.to(dtype), torch.full((1, 2), bad, dtype=dtype)])
+            assert torch.equal(sgq.fp4_tensor_scale(y), clean)
+            assert sgq.fp4_tensor_scale(y[2:]).item() == 1.0

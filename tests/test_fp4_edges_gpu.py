@@ -73,3 +73,21 @@ def test_norm_of_groups_far_past_their_tensor_scale(t, top, M, K):
     rows = slice(None) if M < 10 else [0, 1, M // 2, M - 1]
     assert (ref.from_tiles(s, M, K // 16)[rows] == byte).all()
     assert (ref.unpack(q[rows]) == nib).all()
+
+
+def test_a_value_that_is_not_finite_is_its_own_groups():
+    """Codes, scales and products beside an infinity and a NaN are those of the tensor without them."""
+    x, w = groups(1, 512, 3.0).to(DEV).expand(130, 512).contiguous(), sgq.quant_fp4(groups(64, 512, 0.1).nan_to_num(0, 0, 0).to(DEV), "nvfp4")
+    bad = x.clone()
+    bad[7, 100], bad[9, 300] = float("inf"), float("nan")
+    got = []
+    for v in (x, bad):
+        t = sgq.fp4_tensor_scale(v)
+        q, s = sgq.quant_fp4(v, "nvfp4", tensor_scale=t)
+        got.append((t, q, ref.from_tiles(s, 130, 32), sgq.fp4_gemm(q, s, *w, "nvfp4", x_scale=t)))
+    ok()
+    assert torch.equal(got[0][0], got[1][0])
+    rows = [r for r in range(130) if r not in (7, 9)]
+    assert torch.equal(got[0][1][rows], got[1][1][rows]) and (got[0][2][rows] == got[1][2][rows]).all()
+    assert torch.equal(got[0][3][rows], got[1][3][rows]) and torch.isnan(got[1][3][[7, 9]]).all()
+    assert (got[1][2] == 0x7F).sum() == 2
