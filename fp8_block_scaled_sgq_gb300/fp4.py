@@ -72,11 +72,13 @@ def _packed(name: str, q, s, fmt: str):
 
 
 def fp4_tensor_scale(x):
-    """fp32 [1]: the "nvfp4" tensor scale of x, max|x| / (6 * 448) over its finite values (1 where these are only zeros):
-    infinities and NaN are for their own groups alone.
+    """fp32 [1]: the "nvfp4" tensor scale of x, max|x| / (6 * 448) over its finite values (1 where these are only zeros
+    or none): infinities and NaN are for their own groups alone.
     """
     if torch is None:
         _load()
+    if x.numel() == 0:
+        return torch.ones(1, dtype=torch.float32, device=x.device)
     t = (x.detach().nan_to_num(0.0, 0.0, 0.0).abs().amax().float() / (6.0 * 448.0)).reshape(1)
     return torch.where(t > 0, t.clamp_min(torch.finfo(torch.float32).tiny), torch.ones_like(t))
 

@@ -13,3 +13,10 @@ def test_tensor_scale_is_of_the_finite_values():
             y = torch.cat([x.to(dtype), torch.full((1, 2), bad, dtype=dtype)])
             assert torch.equal(sgq.fp4_tensor_scale(y), clean)
             assert sgq.fp4_tensor_scale(y[2:]).item() == 1.0
+
+
+def test_tensor_scale_of_nothing():
+    """As for zeros: no tokens are no error anywhere else."""
+    for shape in ((0,), (0, 64)):
+        t = sgq.fp4_tensor_scale(torch.zeros(shape, dtype=torch.bfloat16))
+        assert t.shape == (1,) and t.dtype == torch.float32 and t.item() == 1.0
