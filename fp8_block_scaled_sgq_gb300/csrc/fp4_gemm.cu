@@ -112,9 +112,26 @@ __device__ __forceinline__ void mma_stage(uint32_t d, uint64_t a, uint64_t b, ui
 __device__ __forceinline__ void st_cluster_v4(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
-__device__ __forceinline__ float tensor_scales(const Args& a) {
-    return (a.a_t ? __ldg(a.a_t) : 1.0f) * (a.w_t ? __ldg(a.w_t) : 1.0f);
-}
+// Both tensor scales, as the factors that a sum is multiplied by, first and then
+// second: their product and 1; or, where their product is no normal fp32
+// number, the larger one and the smaller one, since what they make of the sum
+// may be one all the same.  (MXFP4 has none.)
+template <bool kNv>
+struct Scales {
+    float first = 1.0f, second = 1.0f;
+    __device__ __forceinline__ explicit Scales(const Args& a) {
+        if constexpr (kNv) {
+            const float x = a.a_t ? __ldg(a.a_t) : 1.0f, w = a.w_t ? __ldg(a.w_t) : 1.0f, xw = x * w;
+            const bool normal = fabsf(xw) >= 0x1p-126f && fabsf(xw) <= 0x1.fffffep127f, larger = fabsf(x) >= fabsf(w);
+            first = normal ? xw : larger ? x : w;
+            second = normal ? 1.0f : larger ? w : x;
+        }
+    }
+    __device__ __forceinline__ float2 scaled(float u, float v) const {
+        if constexpr (!kNv) return make_float2(u, v);
+        return lat::mul2(lat::mul2(make_float2(u, v), make_float2(first, first)), make_float2(second, second));
+    }
+};
 
 // ---------------------------------------------------------------- weights on the 128-row side
 //
@@ -247,7 +264,7 @@ __global__ void __launch_bounds__(kTileThreads)
         ptx::grid_dependency_wait();   // the tensor scales; and D may still be read
         const int quad = warp & 3, row = quad * 32 + lane;
         const int n = tw * kRows + row;
-        const float scale = tensor_scales(a);
+        const Scales<kNv> scales(a);
         const int m0 = tx * BN;
         const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16);
         // Sums of four tokens for the lane's weight row -> D: lanes exchange with their neighbours, so that each
@@ -256,9 +273,10 @@ __global__ void __launch_bounds__(kTileThreads)
         auto store4 = [&](const float (&v)[4], int m) {
 #pragma unroll
             for (int c = 0; c < 4; c += 2) {
-                const float other = __shfl_xor_sync(0xFFFFFFFFu, lane & 1 ? v[c] : v[c + 1], 1);
+                const float2 d = scales.scaled(v[c], v[c + 1]);
+                const float other = __shfl_xor_sync(0xFFFFFFFFu, lane & 1 ? d.x : d.y, 1);
                 const int token = m + c + (lane & 1);
-                const uint32_t two = lane & 1 ? Pair<T>::pack(other * scale, v[c + 1] * scale) : Pair<T>::pack(v[c] * scale, other * scale);
+                const uint32_t two = lane & 1 ? Pair<T>::pack(other, d.y) : Pair<T>::pack(d.x, other);
                 if (n < a.N && token < a.M) *reinterpret_cast<uint32_t*>(D + int64_t(token) * a.N) = two;
             }
         };
@@ -549,7 +567,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     } else if (warp >= 4) {
         ptx::grid_dependency_wait();   // the tensor scales; and D may still be read
         const int quad = warp & 3, b = (warp - 4) >> 2;   // accumulator b
-        const float scale = tensor_scales(a);
+        const Scales<kNv> scales(a);
         const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16) + b * BN;
         T* const D = static_cast<T*>(a.D);
         const bool wide = ((reinterpret_cast<uintptr_t>(D) | (static_cast<uintptr_t>(a.N) * 2u)) & 31u) == 0;
@@ -568,8 +586,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
                 ptx::tmem_ld<32>(acc + c, v);
                 ptx::tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    w[c / 2 + j] = Pair<T>::pack(__uint_as_float(v[2 * j]) * scale, __uint_as_float(v[2 * j + 1]) * scale);
+                for (int j = 0; j < 16; ++j) {
+                    const float2 d = scales.scaled(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+                    w[c / 2 + j] = Pair<T>::pack(d.x, d.y);
+                }
             }
             ptx::tc_fence_before();
             __syncwarp();

@@ -508,8 +508,8 @@ sgq_status sgq_dequant_fp4(const void* xq, const void* xs, int64_t M, int64_t K,
  * D[m, n] = a_scale w_scale sum_k A[m, k] W[n, k] over the codes times their
  * group scales, fp32 accumulation in any order, rounded once.  Aq/As: M rows,
  * Wq/Ws: N rows, both in one format; a_scale, w_scale: their fp32 tensor
- * scales, or NULL for 1 (NULL for SGQ_MXFP4).  D: [M, N] contiguous, written,
- * never read.  N % 8 == 0, N > 0; M, N < 2^31 - 1024; K <= 2^26.  Sums that leave fp32 are
+ * scales, or NULL for 1 (NULL for SGQ_MXFP4); their product may leave fp32 as
+ * long as what it makes of the sum does not.  D: [M, N] contiguous, written, never read.  N % 8 == 0, N > 0; M, N < 2^31 - 1024; K <= 2^26.  Sums that leave fp32 are
  * infinite or NaN, as in any fp32 product.  No memory is allocated, and none
  * is shared between calls.
  */

@@ -5,7 +5,7 @@ import torch
 
 import fp8_block_scaled_sgq_gb300 as sgq
 import fp4_ref as ref
-from test_fp4_gpu import check_quant, ok, one
+from test_fp4_gpu import check_quant, ok, on_gpu, one
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -91,3 +91,39 @@ def test_a_value_that_is_not_finite_is_its_own_groups():
     assert torch.equal(got[0][1][rows], got[1][1][rows]) and (got[0][2][rows] == got[1][2][rows]).all()
     assert torch.equal(got[0][3][rows], got[1][3][rows]) and torch.isnan(got[1][3][[7, 9]]).all()
     assert (got[1][2] == 0x7F).sum() == 2
+
+
+# ---------------------------------------------------------------- tensor scales whose product leaves fp32
+
+#: Sizes of each kernel: a tile, tiles whose K is split, pairs with 256 and with 512 tokens.
+KERNELS = [(3, 8, 96), (40, 512, 4096), (300, 4096, 512), (1300, 4096, 1568)]
+
+
+@pytest.mark.parametrize("M,N,K", KERNELS)
+@pytest.mark.parametrize("swap", [False, True])
+def test_product_whose_tensor_scales_product_is_tiny(M, N, K, swap):
+    """1.76 2^-149 is no fp32 number, 2^31 times it is."""
+    rng = np.random.default_rng(M)
+    a, w = ((rng.choice([5, 6, 7], (r, K)).astype(np.uint8), rng.integers(0x70, 0x7F, (r, K // 16)).astype(np.uint8)) for r in (M, N))
+    s, t = (1.375 * 2.0 ** -75, 1.28125 * 2.0 ** -74) if not swap else (1.28125 * 2.0 ** -140, 1.375 * 2.0 ** -9)
+    d = sgq.fp4_gemm(*on_gpu(*a), *on_gpu(*w), "nvfp4", x_scale=one(s), w_scale=one(t))
+    ok()
+    # bf16's smallest normal number is fp32's, and values below it are 2^-134 off at most
+    av, wv, alpha = ref.values(*a, "nvfp4"), ref.values(*w, "nvfp4"), float(np.float32(s)) * float(np.float32(t))
+    want, mag = av @ wv.T * alpha, np.abs(av) @ np.abs(wv).T * alpha
+    assert (np.abs(want) > 2.0 ** -125).mean() > 0.9
+    tol = 2.0 ** -8 * np.abs(want) + (K / 16 * 2.0 ** -23 + 2.0 ** -22) * mag + 2.0 ** -133
+    assert (np.abs(ref.f64(d) - want) <= tol).all()
+
+
+@pytest.mark.parametrize("M,N,K", KERNELS)
+def test_product_whose_tensor_scales_product_is_huge(M, N, K):
+    """The scales' product is past fp32's largest value, the results are not; a token of zeros gives zeros, not 0 * infinity."""
+    rng = np.random.default_rng(M)
+    a, w = ((rng.integers(0, 16, (r, K)).astype(np.uint8), np.full((r, K // 16), 1, np.uint8)) for r in (M, N))
+    a[0][M // 2] = 0
+    s, t = 1.375 * 2.0 ** 69, 1.28125 * 2.0 ** 60
+    d = sgq.fp4_gemm(*on_gpu(*a), *on_gpu(*w), "nvfp4", x_scale=one(s), w_scale=one(t))
+    ok()
+    assert (d[M // 2] == 0).all()
+    ref.check_product(d, ref.values(*a, "nvfp4"), ref.values(*w, "nvfp4"), float(np.float32(s)) * float(np.float32(t)), torch.bfloat16)
