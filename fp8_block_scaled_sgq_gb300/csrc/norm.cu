@@ -21,6 +21,7 @@
 
 #include "fp4_common.cuh"
 #include "ptx.cuh"
+#include "resident.h"
 #include "sgq_internal.h"
 
 namespace sgq {
@@ -518,10 +519,13 @@ sgq_status narrow(const Args& a, int sms, cudaStream_t st) {
     // rows that all fit at once: one step of one row for each warp
     if (kN > 1 && a.M <= int64_t(sms) * 16 * (32 / kRow)) return narrow<T, kRow, kVec, 1, kOut>(a, sms, st);
     auto kern = norm_rows_kernel<T, kRow, kVec, kN, kOut>;
-    static const int fit = [&] {   // CTAs an SM
+    static Resident resident;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return SGQ_ERR_CUDA;
+    const int fit = resident.on(dev, [&] {   // CTAs an SM
         int n = 0;
         return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, 128, 0) == cudaSuccess ? n : 0;
-    }();
+    });
     if (fit <= 0) return SGQ_ERR_CUDA;
     const int64_t rows = 4 * (32 / kRow) * kN, want = (a.M + rows - 1) / rows, most = int64_t(sms) * fit;
     cudaLaunchAttribute attr[1];
