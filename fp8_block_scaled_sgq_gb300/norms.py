@@ -24,6 +24,8 @@ def _target(x, M, K, quant, group, ue8m0, tensor_scale, out, out_scales, stream)
         _dtype(out)
         return binding.SGQ_OUT_16, out, None
     u8 = fp4.torch.uint8
+    if not isinstance(quant, str):
+        _fail(f"quant: {quant!r} is none of None, 'fp8', 'fp8_ue8m0', 'mxfp4', 'nvfp4'")
     if quant in _FORMAT:
         if ue8m0:
             _fail("ue8m0 goes with quant='fp8'")

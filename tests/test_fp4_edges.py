@@ -1,7 +1,8 @@
-"""4-bit linears and norms without a GPU: tensor scales of unusual tensors."""
+"""4-bit linears and norms without a GPU: tensor scales of unusual tensors, and calls that have to be refused."""
 import torch
 
 import fp8_block_scaled_sgq_gb300 as sgq
+from test_fp4 import bf, launches, refused  # noqa: F401  (launches: a fixture)
 
 
 def test_tensor_scale_is_of_the_finite_values():
@@ -20,3 +21,11 @@ def test_tensor_scale_of_nothing():
     for shape in ((0,), (0, 64)):
         t = sgq.fp4_tensor_scale(torch.zeros(shape, dtype=torch.bfloat16))
         assert t.shape == (1,) and t.dtype == torch.float32 and t.item() == 1.0
+
+
+def test_forms_that_no_dictionary_takes(launches):  # noqa: F811
+    x, w = bf(4, 128), bf(128)
+    for quant in (["nvfp4"], {"nvfp4"}, {}):
+        refused(sgq.rms_norm, x, w, quant=quant)
+        refused(sgq.norm_add, x, x, weight=w, quant=quant)
+    assert not launches
