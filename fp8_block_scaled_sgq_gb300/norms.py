@@ -158,8 +158,8 @@ def norm_add(x, residual, post_weight=None, gate=None, scale: float = 1.0, resid
     kind, y, ys = binding.SGQ_OUT_NONE, None, None
     if w is not None:
         kind, y, ys = _target(x, M, K, quant, group, ue8m0, t, out, out_scales, stream)
-    elif quant is not None or out is not None or out_scales is not None or t is not None:
-        _fail("quant, out, out_scales and tensor_scale go with weight")
+    elif quant is not None or out is not None or out_scales is not None or t is not None or ue8m0:
+        _fail("quant, ue8m0, out, out_scales and tensor_scale go with weight")
     rc = (binding._lib or binding.load_library()).sgq_norm(
         x.data_ptr(), strides[0] if M > 1 else K, None if p is None else p.data_ptr(),
         None if gate is None else gate.data_ptr(), gs, rows, residual.data_ptr(), residual.stride(0) if M > 1 else K,

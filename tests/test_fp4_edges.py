@@ -29,3 +29,10 @@ def test_forms_that_no_dictionary_takes(launches):  # noqa: F811
         refused(sgq.rms_norm, x, w, quant=quant)
         refused(sgq.norm_add, x, x, weight=w, quant=quant)
     assert not launches
+
+
+def test_powers_of_two_go_with_a_form(launches):  # noqa: F811
+    """As in rms_norm, an argument that nothing would heed is refused."""
+    x = bf(4, 128)
+    refused(sgq.norm_add, x, x, ue8m0=True)
+    assert not launches
