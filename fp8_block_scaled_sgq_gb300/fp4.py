@@ -6,12 +6,12 @@ allocate what they return on the stream of the call.  Formats: "mxfp4" (32 value
 (16 values a scale, E4M3, and one fp32 scale a tensor).  A tensor of M rows and K columns in that form is two uint8
 tensors: codes [M, K/2] and scale tiles [ceil(M/128), T, 512], T = ceil(K/128) ("mxfp4") or ceil(K/64) ("nvfp4").
 Wrong shapes, types or strides raise ValueError before anything is launched, and so does a tensor that requires a
-gradient while gradients are recorded: none is here.
+gradient while gradients are recorded, or carries a forward-mode tangent: no derivative is recorded here.
 """
 from __future__ import annotations
 
 from . import binding
-from .latent import _contiguous, _device, _dtype, _empty, _fail
+from .latent import _contiguous, _device, _dtype, _dual, _empty, _fail, _no_tangent
 
 torch = None        # imported with the first call: the package itself does without it
 _NUMBER = {}        # the C interface's numbers of the element types
@@ -61,6 +61,8 @@ def _scale(name: str, t, fmt):
             _fail(f"{name}: expected one float32 value, got {tuple(t.shape)} of {t.dtype}")
         if t.requires_grad and torch.is_grad_enabled():
             _fail(f"{name} requires a gradient, and none is recorded here")
+        if _dual():
+            _no_tangent(t)
 
 
 def _packed(name: str, q, s, fmt: str):
@@ -121,7 +123,7 @@ def quant_fp4(x, fmt: str, tensor_scale=None, silu_mul: bool = False, xq=None, x
     K = W // 2 if silu_mul else W
     if (strides[1] != 1 or K % 32 or not K or (silu_mul and W % 2) or (x.requires_grad and torch.is_grad_enabled())
             or (t is not None and (t.get_device() != device or fmt != "nvfp4" or t.dtype is not torch.float32
-                                   or t.numel() != 1 or t.requires_grad)) or xq is not None or xs is not None):
+                                   or t.numel() != 1 or t.requires_grad)) or xq is not None or xs is not None or _dual()):
         _why_not_quant(x, silu_mul, t, fmt, xq, xs)
     if xq is None:
         xq = _new((M, K // 2), u8, x, stream)
@@ -167,7 +169,7 @@ def dequant_fp4(xq, xs, fmt: str, tensor_scale=None, dtype=None, out=None, strea
             or not xs.is_contiguous() or xs.shape != (-(-shape[0] // 128), -(-2 * shape[1] // tile), 512)
             or xq.get_device() != device or xs.get_device() != device or out is not None
             or (t is not None and (t.get_device() != device or fmt != "nvfp4" or t.dtype is not torch.float32
-                                   or t.numel() != 1 or t.requires_grad))):
+                                   or t.numel() != 1 or t.requires_grad or _dual()))):
         _packed("xq", xq, xs, fmt)
         _scale("tensor_scale", t, fmt)
         _device(xq, xs, t, out)
@@ -212,7 +214,7 @@ def fp4_gemm(xq, xs, wq, ws, fmt: str, x_scale=None, w_scale=None, dtype=None, o
             or (a is not None and (a.get_device() != device or fmt != "nvfp4" or a.dtype is not f32 or a.numel() != 1
                                    or a.requires_grad))
             or (w is not None and (w.get_device() != device or fmt != "nvfp4" or w.dtype is not f32 or w.numel() != 1
-                                   or w.requires_grad))):
+                                   or w.requires_grad)) or _dual()):
         _packed("xq", xq, xs, fmt)
         _packed("wq", wq, ws, fmt)
         if xshape[1] != wshape[1]:

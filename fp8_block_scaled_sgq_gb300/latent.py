@@ -5,7 +5,8 @@ the attention's workspace) on the stream of the call, and call the binding; the
 work is in ``libsgq.so`` (``include/sgq.h``, "Latent attention").  Tensors are
 bfloat16 or float16, one type for a call, on the current device.  Wrong shapes,
 types or strides raise ValueError before anything is launched, and so does a
-tensor that requires a gradient while gradients are recorded: none is here.
+tensor that requires a gradient while gradients are recorded, or carries a
+forward-mode tangent: no derivative is recorded here.
 """
 from __future__ import annotations
 
@@ -42,6 +43,8 @@ def _dtype(x, *others) -> int:
                 raise ValueError(f"one element type a call: {dt} and {t.dtype}")
             if graded and t.requires_grad:
                 _graded()
+    if _dual():
+        _no_tangent(x, *others)
     if dt == torch.bfloat16:
         return binding.SGQ_BF16
     if dt == torch.float16:
@@ -56,6 +59,19 @@ def _fail(what: str):
 def _graded():
     _fail("a tensor requires a gradient, and none is recorded here: detach it, or call under torch.no_grad() "
           "(rotary's gradient is rotary with inverse=True)")
+
+
+def _dual() -> bool:
+    """Whether forward-mode derivatives are being taken, so that tensors may carry tangents."""
+    import torch
+    return getattr(torch.autograd.forward_ad, "_current_level", 0) >= 0   # (not public; without it, tensors are always asked)
+
+
+def _no_tangent(*tensors):
+    import torch
+    for t in tensors:
+        if t is not None and t.is_floating_point() and torch.autograd.forward_ad.unpack_dual(t).tangent is not None:
+            _fail("a tensor carries a forward-mode tangent, and none is passed on here: take its primal")
 
 
 def _strides(name: str, t, dims: int):

@@ -4,13 +4,13 @@ quantised for the linear that reads it.
 
 The work is in ``libsgq.so`` (``include/sgq.h``, sgq_norm).  Tensors are bfloat16 or float16, one type for a call, on
 the current device.  Wrong shapes, types or strides raise ValueError before anything is launched, and so does a tensor
-that requires a gradient while gradients are recorded: none is here.
+that requires a gradient while gradients are recorded, or carries a forward-mode tangent: no derivative is recorded here.
 """
 from __future__ import annotations
 
 from . import binding, fp4
 from .fp4 import _current, _FORMAT, _new, _NUMBER, _scale
-from .latent import _contiguous, _device, _dtype, _fail
+from .latent import _contiguous, _device, _dtype, _dual, _fail
 
 
 def _target(x, M, K, quant, group, ue8m0, tensor_scale, out, out_scales, stream):
@@ -32,7 +32,8 @@ def _target(x, M, K, quant, group, ue8m0, tensor_scale, out, out_scales, stream)
         if K % 32:
             _fail(f"{K} columns are not whole groups of 32")
         t = tensor_scale
-        if t is not None and (quant != "nvfp4" or t.dtype is not fp4.torch.float32 or t.numel() != 1 or t.requires_grad):
+        if t is not None and (quant != "nvfp4" or t.dtype is not fp4.torch.float32 or t.numel() != 1 or t.requires_grad
+                              or _dual()):
             _scale("tensor_scale", t, quant)
         kind = binding.SGQ_OUT_MXFP4 if quant == "mxfp4" else binding.SGQ_OUT_NVFP4
         shape, scales, kept = (M, K // 2), (-(-M // 128), -(-K // _FORMAT[quant][1]), 512), u8
@@ -86,7 +87,7 @@ def rms_norm(x, weight, eps: float = 1e-6, offset: float = 0.0, quant=None, grou
     if (dt is None or len(shape) != 2 or strides[1] != 1 or weight.dtype is not kept or weight.shape != shape[1:]
             or not weight.is_contiguous() or x.get_device() != device or weight.get_device() != device
             or (t is not None and t.get_device() != device) or out is not None or out_scales is not None
-            or (torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad))):
+            or (torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad)) or _dual()):
         dt = _dtype(x, weight)
         if x.dim() != 2:
             _fail(f"x: expected [M, K], got {tuple(x.shape)}")
@@ -126,7 +127,7 @@ def norm_add(x, residual, post_weight=None, gate=None, scale: float = 1.0, resid
             or (gate is not None and (gate.dtype is not kept or gate.get_device() != device
                                       or (graded and gate.requires_grad)))
             or (t is not None and t.get_device() != device)
-            or h_out is not None or out is not None or out_scales is not None):
+            or h_out is not None or out is not None or out_scales is not None or _dual()):
         dt = _dtype(x, residual, p, gate, w, h_out)
         if x.dim() != 2:
             _fail(f"x: expected [M, K], got {tuple(shape)}")

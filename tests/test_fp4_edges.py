@@ -1,8 +1,9 @@
 """4-bit linears and norms without a GPU: tensor scales of unusual tensors, and calls that have to be refused."""
+import pytest
 import torch
 
 import fp8_block_scaled_sgq_gb300 as sgq
-from test_fp4 import bf, launches, refused  # noqa: F401  (launches: a fixture)
+from test_fp4 import bf, launches, refused, u8  # noqa: F401  (launches: a fixture)
 
 
 def test_tensor_scale_is_of_the_finite_values():
@@ -36,3 +37,45 @@ def test_powers_of_two_go_with_a_form(launches):  # noqa: F811
     x = bf(4, 128)
     refused(sgq.norm_add, x, x, ue8m0=True)
     assert not launches
+
+
+def test_tensors_with_a_tangent_are_refused(launches):  # noqa: F811
+    """Forward-mode derivatives are not recorded either, and would be lost without a word."""
+    import torch.autograd.forward_ad as ad
+    x, w, t, q, s = bf(4, 128), bf(128), torch.ones(1), u8(4, 64), u8(1, 2, 512)
+    with ad.dual_level():
+        dual = lambda v: ad.make_dual(v, torch.ones_like(v))  # noqa: E731
+        dx, dw, dt = dual(x), dual(w), dual(t)
+        for grad in (True, False):
+            with torch.set_grad_enabled(grad):
+                refused(sgq.quant_fp4, dx, "nvfp4")
+                refused(sgq.quant_fp4, x, "nvfp4", tensor_scale=dt)
+                refused(sgq.dequant_fp4, q, s, "nvfp4", tensor_scale=dt)
+                refused(sgq.fp4_gemm, q, s, q, s, "nvfp4", x_scale=dt)
+                refused(sgq.fp4_gemm, q, s, q, s, "nvfp4", w_scale=dt)
+                refused(sgq.rms_norm, dx, w)
+                refused(sgq.rms_norm, x, dw)
+                refused(sgq.rms_norm, x, w, quant="nvfp4", tensor_scale=dt)
+                for k in (dict(x=dx), dict(residual=dx), dict(post_weight=dw), dict(weight=dw), dict(gate=dw),
+                          dict(weight=w, quant="nvfp4", tensor_scale=dt)):
+                    refused(sgq.norm_add, **{**dict(x=x, residual=x), **k})
+        assert not launches
+        # others are not in the way of a level
+        sgq.rms_norm(x, w)
+        sgq.norm_add(x, x, weight=w, gate=w, quant="nvfp4", tensor_scale=t)
+        sgq.quant_fp4(x, "nvfp4", tensor_scale=t)
+        sgq.fp4_gemm(q, s, u8(8, 64), s, "nvfp4", x_scale=t)
+        sgq.dequant_fp4(q, s, "nvfp4", tensor_scale=t)
+        assert len(launches) == 5
+
+
+def test_latent_helpers_refuse_a_tangent():
+    """The latent helpers' check is the same one."""
+    import torch.autograd.forward_ad as ad
+    from fp8_block_scaled_sgq_gb300.latent import _dtype
+    with ad.dual_level():
+        dx = ad.make_dual(bf(4, 2, 64), torch.ones(4, 2, 64).bfloat16())
+        for args in ((dx,), (bf(2), dx)):
+            with pytest.raises(ValueError):
+                _dtype(*args)
+        _dtype(bf(2), bf(2))
