@@ -127,3 +127,26 @@ def test_product_whose_tensor_scales_product_is_huge(M, N, K):
     ok()
     assert (d[M // 2] == 0).all()
     ref.check_product(d, ref.values(*a, "nvfp4"), ref.values(*w, "nvfp4"), float(np.float32(s)) * float(np.float32(t)), torch.bfloat16)
+
+
+# ---------------------------------------------------------------- codes are those of the division
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_codes_are_the_divisions_for_divisors_of_every_kind(dtype):
+    """Every significand of the type in nine binades up to 6, divided by t, whose significands are 1025 of fp32's (a prime step
+    apart).  Each group of 16 begins with 6 t, rounded: its scale byte is 1's, and the divisor t itself."""
+    n = {torch.bfloat16: 128, torch.float16: 1024}[dtype]
+    x = torch.cat([(1 + torch.arange(n, dtype=torch.float64) / n) * 2.0 ** e for e in range(-6, 3)])
+    x = x[x <= 6.0]
+    x = torch.cat([x, -x])
+    rows = -(-x.numel() // 480)
+    x = torch.cat([x, x])[:rows * 480].view(-1, 15)
+    x = torch.cat([torch.zeros(x.shape[0], 1), x], 1).view(rows, 512).to(dtype)
+    for i in range(0, 1 << 23, 8191):
+        t = np.float32(1 + i / (1 << 23))
+        x[:, ::16] = 6 * float(t)
+        q, s = sgq.quant_fp4(x.to(DEV), "nvfp4", tensor_scale=one(float(t)))
+        nib, byte = ref.quantise(x.float().numpy(), "nvfp4", t)
+        assert (byte == 0x38).all()
+        assert np.array_equal(ref.unpack(q), nib) and np.array_equal(ref.from_tiles(s, rows, 32), byte), i
+    ok()
