@@ -61,10 +61,20 @@ def _graded():
           "(rotary's gradient is rotary with inverse=True)")
 
 
+_forward_ad = None    # torch.autograd.forward_ad, imported with the first call
+
+
 def _dual() -> bool:
     """Whether forward-mode derivatives are being taken, so that tensors may carry tangents."""
-    import torch
-    return getattr(torch.autograd.forward_ad, "_current_level", 0) >= 0   # (not public; without it, tensors are always asked)
+    global _forward_ad
+    try:   # (a name that is not public; without it, tensors are always asked)
+        return _forward_ad._current_level >= 0
+    except AttributeError:
+        if _forward_ad is None:
+            from torch.autograd import forward_ad
+            _forward_ad = forward_ad
+            return _dual()
+        return True
 
 
 def _no_tangent(*tensors):
