@@ -144,8 +144,10 @@ struct Scales {
 // for the sum.  A CTA that has an SM to itself takes all of its shared memory for
 // stages under way: weights at HBM's rate need some 60 KB an SM in flight (64
 // tokens x 7168 x 7168: 13.7 us with 3 stages, 10.1 with 7).  Measured in a
-// graph: 1 x 7168 x 2048 NVFP4 3.9 us, 64 x 24576 x 1536 MXFP4 5.5 us (4.3 TB/s),
-// 301 x 1536 x 7168 NVFP4 8.7 us.
+// graph, other weights for each call, so that they come from HBM: 1 x 7168 x 2048
+// NVFP4 4.8 us (1.7 TB/s), 64 x 7168 x 7168 NVFP4 9.9 (3.0), 64 x 24576 x 1536
+// MXFP4 7.0 (3.3), 301 x 1536 x 7168 NVFP4 9.1.  With the same weights in L2: 3.9,
+// 5.5 for 64 x 24576 x 1536, and 8.7.
 //
 // Warps: 0 loads (TMA), 1 issues, 2-5 read the accumulator (a TMEM lane
 // quarter each).
@@ -162,11 +164,14 @@ struct TileCfg {
     static constexpr int kMaxRing = 12;
     static constexpr int kHead = 1024;                              // barriers and words, before the ring
     // At least the share of an SM's shared memory that the CTA takes of its
-    // TMEM, so that CTAs which fit together never wait for each other's TMEM; and
-    // more than half of it for a CTA that waits for others (a split tile's), so
-    // that none with a TMEM of its own fits beside it, another kernel's of another
-    // stream either: two clusters that each hold the TMEM that the other's CTA
-    // waits for would never end.
+    // TMEM, so that CTAs of this file which fit together never wait for each
+    // other's TMEM; and more than half of it for a CTA that waits for others (a
+    // split tile's), so that no CTA of another cluster fits beside it: two clusters
+    // that each hold the TMEM that the other's CTA waits for would never end.  (All
+    // clusters of the library that hold TMEM take more than 111 KB a CTA, here and
+    // in the FP8 GEMMs.  What does fit is a tile of 16 to 64 tokens without splits,
+    // 57 KB and 128 columns, beside at most 256 of a split one: its columns are
+    // there, and it waits for no other CTA.)
     static constexpr size_t kLeast = size_t(kTmem) * (228 * 1024 / 512) - 1024, kAlone = 116 * 1024;
     static size_t need(int ring, int splits) {
         return size_t(kHead) + size_t(ring) * kStageBytes + (splits > 1 ? size_t(BN < 4 * splits ? 4 * splits : BN) * kRows * 4 : 0) + 1024;
@@ -673,20 +678,31 @@ int tile_splits(int64_t tiles, int stages, int sms) {
 }
 
 // Which kernel serves more than 64 tokens: the one whose time, in us, is least
-// by what they measured (NVFP4; MXFP4 is 3 to 8 % faster everywhere).  A call
-// costs 2.9 (tiles) or 3.2 (pairs); a stage costs an issuing warp 0.31, 0.48
-// with two halves; a pair's tile ends in 0.25 and 1.2; the sum over the parts of
-// a split tile takes 1.3 for 64 tokens and 3 for 128; where tiles outnumber the
-// SMs, two CTAs on an SM take 1.5 times one's time for 64 tokens and 2.6 for
-// 128, whose loads already fill the SM's share of L2.  Measured, us:
+// by a model of a few terms.  A call costs 2.9 (tiles) or 3.2 (pairs); a stage
+// costs an issuing warp 0.31, 0.48 with two halves; a pair's tile ends in 0.25
+// and 1.2; the sum over the parts of a split tile takes 1.3 for 64 tokens and 3
+// for 128; where tiles outnumber the SMs, two CTAs on an SM take 1.5 times one's
+// time for 64 tokens and 2.6 for 128, whose loads already fill the SM's share of
+// L2.  Measured in a graph (NVFP4; MXFP4 is 3 to 8 % faster), and by the model:
 //   N, K, M              64 tokens  128 tokens  pairs, one half  two halves
 //   1536, 7168, 128         6.4         7.2          11.8           15.5
+//                          (6.4         7.1          12.1           17.8)
 //   1536, 7168, 301         8.9         8.7          11.6           17.0
+//                          (8.5         8.1          12.1           17.8)
 //   7168, 2048, 301         6.8         8.0           7.1            9.3
+//                          (6.6         9.3           5.9            8.2)
 //   24576, 1536, 128       11.9         8.8           9.4           12.3
+//                          (8.5         7.7           7.4           11.4)
 //   7168, 7168, 1024       41.0        30.2          21.5           20.2
+//                         (42.0        48.0          21.1           17.8)
 //   7168, 7168, 4096      156.9        96.3          70.6           58.9
+//                        (159.1       138.3          74.6           61.8)
 //   24576, 1536, 8192       410         263           114            116
+//                          (229         201           117            113)
+// So it takes the fastest of four in four of these rows, and one that is 2 to 7 %
+// slower in three: 301 x 7168 x 2048 and 128 x 24576 x 1536, where it holds pairs
+// too short by 1.2 and 2.0, and 8192 x 24576 x 1536.  For many tiles it is far too
+// short on tiles without pairs (to 1.8 times), which are not taken there.
 enum Way { kTile64, kTile128, kPair1, kPair2 };
 Way way_of(int64_t M, int64_t N, int stages, int sms) {
     auto tile = [&](int bn) {

@@ -6,9 +6,11 @@
 // NVFP4 group or half an MXFP4 one; a warp takes a span of 512 elements of
 // every so many rows, so that the four groups of a scale word lie in
 // neighbouring lanes and leave as one store, and no index is divided on the way.
-// Measured, 4099 x 7168: MXFP4 13.1 us (5.7 TB/s), NVFP4 15.3 (4.9), of
-// silu(gate) * up 23.7 (5.6), back to 16 bits 10.2 and 10.9 (7.0, the
-// codes being in L2).  The scale words, 4 bytes to a 32-byte sector, cost 1.3 us.
+// Measured, 4099 x 7168, inputs from HBM: MXFP4 13.1 us (5.7 TB/s), NVFP4 15.3
+// (4.9), of silu(gate) * up 23.6 and 23.8 (5.6), back to 16 bits 11.1 and 11.6
+// (6.7 and 6.5).  The scale words, 4 bytes to a 32-byte sector, cost 1.3 us.
+// What NVFP4 takes longer is instructions: its scales are no powers of two, so
+// every quotient has its correction, two operations an element.
 #include <cuda_runtime.h>
 
 #include <type_traits>
@@ -27,7 +29,8 @@ constexpr int kSpan = 512;   // elements of a warp's span
 
 // -silu(g) * u of h = -g/4 and u in fp32, as h / (1/4 + exp(-g)/4) * u, so that
 // the divisor stays below 2^126 and its reciprocal a normal number down to the
-// last g whose exp(-g) is finite (-88.7).  Within 2^-17 of its value: an
+// last g whose exp(-g) is finite (-88.7; 0 below, as 1 + exp(-g) is infinite in
+// fp32).  Within 2^-17 of its value: an
 // exponent near 127 is off by half a unit, 2^-18, and the product with log2 e by
 // as much.
 __device__ __forceinline__ float minus_silu_mul(float h, float u) {
@@ -89,7 +92,8 @@ __device__ __noinline__ uint4 extreme_group(uint4 a, uint4 b, uint32_t amax, flo
 // Their codes are settled by one correction of the quotient by its remainder,
 // even with an approximate reciprocal: compared with the division for each
 // significand of x and of d, over quotients from 2^-4 to 2^5, no code differs
-// (without the correction 319 of 8.6e9 do in bf16, 2202 of 6.9e10 in fp16).
+// (without the correction 319 of 8.6e9 do in bf16, 2202 of 6.9e10 in fp16; the
+// tests repeat it for 1025 of the divisors).
 // Divisors outside in_range divide, and so does what is so far past its tensor
 // scale that a quotient leaves fp32.
 template <typename T, bool kNv, int kN>

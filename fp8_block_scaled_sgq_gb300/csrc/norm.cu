@@ -12,11 +12,12 @@
 // (fp4_common.cuh).
 //
 // Each of x, residual, h and y passes once; a row stays in registers (8 elements
-// a 16-byte load) between its one or two sums.  Measured, 4096 x 7168 in bf16: a
-// norm 17.6 us (6.7 TB/s), residual alone 25.9 (6.8), with the next norm 40.0
-// (5.9): HBM.  Into FP8 groups 17.6 (5.0), with every step before it 38.2 (5.4):
-// instructions beside it, 204 a warp for 8 elements a lane.  One row: 3.2 us in a
-// graph.
+// a 16-byte load) between its one or two sums.  Measured, 4096 x 7168 in bf16,
+// inputs from HBM: a norm 18.1 us (6.5 TB/s), residual alone 25.5 (6.9), with the
+// next norm 40.1 (5.9): HBM.  A norm into FP8 groups 19.7 (4.5), MXFP4 22.0 (3.4),
+// NVFP4 25.9 (2.9), and with every step before it 38.0 (5.4), 39.1, 42.4 (4.5):
+// instructions beside it, 204 (FP8) to 227 (NVFP4) a warp for 8 elements a lane
+// with every step.  One row: 3.0 us in a graph.
 #include <cuda_runtime.h>
 
 #include "fp4_common.cuh"
@@ -226,9 +227,11 @@ __host__ __device__ constexpr bool negated(Out out) { return out == kFp8 || out 
 
 // Narrow rows, up to 512 elements: kRow lanes a row (two rows a warp where they
 // are 16), and kN steps of them at once, so that enough loads are under way.  A
-// grid that fills the SMs walks over them: 234375 x 128 in 16 bits 22.2 us (5.4
-// TB/s), with a residual 42.0, into FP8 27.4 (a warp a row in CTAs of four rows:
-// 97.8, 130.9, 114.1).
+// grid that fills the SMs walks over them: 234375 x 128 in 16 bits 21.6 us (5.6
+// TB/s), with a residual 41.1, into FP8 28.6 (a warp a row in CTAs of four rows:
+// 97.8, 130.9, 114.1), MXFP4 27.9, NVFP4 31.0.  Quantised, it is instructions: a
+// thread has one column of up to 256 elements, so that each lane takes its group's
+// maximum, scale and reciprocal for itself (emit).
 template <typename T, int kRow, int kVec, int kN, Out kOut>
 __global__ void __launch_bounds__(128, kVec == 2 ? 5 : 6) norm_rows_kernel(const Args a) {
     ptx::launch_dependents();
@@ -297,7 +300,12 @@ __global__ void __launch_bounds__(128, kVec == 2 ? 5 : 6) norm_rows_kernel(const
 }
 
 // Few rows: a CTA of kRow threads each, with up to kVec columns of 8 elements a
-// thread, kRow columns apart.
+// thread, kRow columns apart.  Rows past 16384 elements come here however many
+// they are: four columns of 1024 threads, 64 registers each, of which some spill
+// (up to 168 bytes, bf16), one CTA an SM and nothing fetched ahead.  They run at
+// half of HBM's rate: 1365 x 21504 in 16 bits 37.8 us (3.1 TB/s), with every step
+// 79.8, into FP8 41.8 and 83.9; 896 x 32768 34.1 (3.4 TB/s) and 68.3.  Residual and
+// norm of 456 x 16384, which walks, 10.6 us, of 457 x 16392 16.8.
 template <typename T, int kRow, int kVec, Out kOut>
 __global__ void __launch_bounds__(kRow) norm_kernel(const Args a) {
     __shared__ float part[2][32];
@@ -350,19 +358,20 @@ __global__ void __launch_bounds__(kRow) norm_kernel(const Args a) {
     }
 }
 
-// Many rows of more than 512 elements (by_width): the grid fills the SMs once, and each
+// Many rows of 513 to 16384 elements (by_width): the grid fills the SMs once, and each
 // CTA walks over rows, its weights in registers.  Every thread copies its own
 // columns of the next rows into shared memory (cp.async, 16 bytes each, read
 // back by that thread alone), so that `depth` rows of x, residual and gate are
 // under way while one is summed.  Four columns a thread: what a row costs beside
-// its elements (two sums over the CTA) falls with fewer warps, and two CTAs of
-// 14 warps keep HBM busy where nothing is quantised (with two columns and twice
-// the warps every step into FP8 took 61.3 us instead of 58.4).  No
+// its elements (two sums over the CTA) falls with fewer warps, and the 14 warps of
+// an SM's two CTAs keep HBM busy where nothing is quantised (with two columns and
+// twice the warps every step into FP8 took 61.3 us instead of 58.4).  No
 // branch stands between a thread's columns (48.7 -> 38.4 us for every step into
 // FP8): only its last one may be none, which is zeros then.  kFull: it is none
 // nowhere (K a multiple of 256 kVec).  kAlone: without a residual; the registers
 // of a second norm's weights go to half as many warps again, which a norm into
-// FP8 or 4 bits has work for (4096 x 7168 to FP8 19.5 -> 17.6 us, NVFP4 25.2 -> 22.9).
+// FP8 or 4 bits has work for (4096 x 7168, x in L2, to FP8 19.5 -> 17.6 us, NVFP4
+// 25.2 -> 22.9; 80 registers each, of which bf16 spills 8 to 16 bytes).
 __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }

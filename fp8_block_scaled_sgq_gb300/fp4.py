@@ -110,6 +110,10 @@ def quant_fp4(x, fmt: str, tensor_scale=None, silu_mul: bool = False, xq=None, x
 
     silu_mul: x is [M, 2K], rows of [gate | up], and silu(gate) * up is quantised.  tensor_scale: fp32 [1] on the
     device ("nvfp4"; None: 1).  xq, xs: outputs to write to.
+
+    Codes of x are those of fp32 divisions, bit for bit.  silu(gate) * up is within 2^-17 of its value (approximate
+    exponential and reciprocal, unlike ``quant_token_group_v2``'s), and its quotients are products with the scale's
+    reciprocal, so that a code may be the next one where a quotient lies by a border.
     """
     if torch is None:
         _load()
@@ -157,7 +161,7 @@ def _why_not_quant(x, silu_mul, t, fmt, xq, xs):
 
 
 def dequant_fp4(xq, xs, fmt: str, tensor_scale=None, dtype=None, out=None, stream=None):
-    """The values [M, K] that codes and scale tiles stand for, in bfloat16 (or dtype, or out's type)."""
+    """The values [M, K] that codes and scale tiles stand for, formed in fp32, in bfloat16 (or dtype, or out's type)."""
     if torch is None:
         _load()
     f, tile = _format(fmt)

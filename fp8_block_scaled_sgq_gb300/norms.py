@@ -76,9 +76,11 @@ def rms_norm(x, weight, eps: float = 1e-6, offset: float = 0.0, quant=None, grou
              tensor_scale=None, out=None, out_scales=None, stream=None):
     """The norm before a block: y = x / sqrt(mean(x^2) + eps) * (weight + offset) of every row of x [M, K].
 
-    quant None: y, of x's type.  "fp8": (codes [M, K], fp32 scales [M, K/group]) as ``quant_token_group`` gives them
-    (ue8m0: powers of two); "fp8_ue8m0": scales as bytes; "mxfp4", "nvfp4": (codes, scale tiles) as ``quant_fp4`` gives
-    them, with tensor_scale.  y is not rounded to 16 bits before it is quantised.  out, out_scales: outputs to write to.
+    quant None: y, of x's type.  "fp8": (codes [M, K], fp32 scales [M, K/group]) in the form of ``quant_token_group``
+    (ue8m0: powers of two); "fp8_ue8m0": scales as bytes; "mxfp4", "nvfp4": (codes, scale tiles) in that of ``quant_fp4``,
+    with tensor_scale.  y is not rounded to 16 bits before it is quantised; it is within 2^-18 of its value, and quotients
+    are products with the scale's reciprocal where the quantisers divide, so that a code may be the next one where a
+    quotient lies by a border.  out, out_scales: outputs to write to.
     """
     torch = fp4.torch or fp4._load()
     device, handle = _current(stream)

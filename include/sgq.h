@@ -463,7 +463,8 @@ sgq_status sgq_latent_prefill(const void* q, int64_t q_stride_t, int64_t q_strid
  * first), saturated at +-6: one of +-{0, .5, 1, 1.5, 2, 3, 4, 6}.  A group that
  * holds a NaN or an infinity gets the NaN scale byte (255, 0x7F) and codes of
  * zero, so that what is computed from it is NaN.  Codes are zero, too, where
- * s t is below fp32's smallest value.  t is calibrated, or max|x| / (6 * 448)
+ * s t is below fp32's smallest value.  A finite group however far past 448 t
+ * saturates: scale byte 0x7E, codes up to +-6.  t is calibrated, or max|x| / (6 * 448)
  * of the tensor.
  *
  * Codes: uint8 [M, K/2], element 2i in the low half of byte i.  Scale bytes:
@@ -493,14 +494,17 @@ sgq_status sgq_latent_prefill(const void* q, int64_t q_stride_t, int64_t q_strid
 /*
  * x: [M, K], rows x_stride elements apart (x_stride % 8 == 0), or, with
  * silu_mul = 1, [M, 2K] of rows [gate | up], of which silu(gate) * up is
- * quantised (fp32, silu(g) = g / (1 + exp(-g)), within 2^-17 of its value; not
- * rounded to 16 bits between; its quotients are products with 1 / s or 1 / (s t)).
+ * quantised (fp32, silu(g) = g / (1 + exp(-g)), within 2^-17 of its value, and 0
+ * where exp(-g) leaves fp32, below g = -88.7; not rounded to 16 bits between; its
+ * quotients are products with 1 / s or 1 / (s t)).
  * xq, xs: codes and scale tiles.
  */
 sgq_status sgq_quant_fp4(const void* x, int64_t M, int64_t K, int64_t x_stride, int format, const float* tensor_scale,
                          int silu_mul, int dtype, void* xq, void* xs, sgq_stream_t stream);
 
-/* The values that codes and scales stand for, rounded once: y [M, K] contiguous. */
+/* The values that codes and scales stand for, code times s or s t: y [M, K]
+ * contiguous.  (s t and its product with the code are fp32 numbers, rounded to 16
+ * bits then; MXFP4's products are exact.) */
 sgq_status sgq_dequant_fp4(const void* xq, const void* xs, int64_t M, int64_t K, int format, const float* tensor_scale,
                            int dtype, void* y, sgq_stream_t stream);
 
@@ -509,9 +513,10 @@ sgq_status sgq_dequant_fp4(const void* xq, const void* xs, int64_t M, int64_t K,
  * group scales, fp32 accumulation in any order, rounded once.  Aq/As: M rows,
  * Wq/Ws: N rows, both in one format; a_scale, w_scale: their fp32 tensor
  * scales, or NULL for 1 (NULL for SGQ_MXFP4); their product may leave fp32 as
- * long as what it makes of the sum does not.  D: [M, N] contiguous, written, never read.  N % 8 == 0, N > 0; M, N < 2^31 - 1024; K <= 2^26.  Sums that leave fp32 are
- * infinite or NaN, as in any fp32 product.  No memory is allocated, and none
- * is shared between calls.
+ * long as what it makes of the sum does not.  D: [M, N] contiguous, written,
+ * never read.  N % 8 == 0, N > 0; M, N < 2^31 - 1024; K <= 2^26.  Sums that leave
+ * fp32 are infinite or NaN, as in any fp32 product.  No memory is allocated, and
+ * none is shared between calls.
  */
 sgq_status sgq_fp4_gemm(const void* Aq, const void* As, const float* a_scale, const void* Wq, const void* Ws,
                         const float* w_scale, void* D, int64_t M, int64_t N, int64_t K, int format, int dtype,
@@ -526,7 +531,8 @@ sgq_status sgq_fp4_gemm(const void* Aq, const void* As, const float* a_scale, co
  *                        h = residual_scale * residual + scale * gate * u
  *                        y = N(h, weight)      (h as it is stored, in 16 bits)
  *
- * fp32 throughout; h is rounded once, and so is y, to what `out` says:
+ * fp32 throughout (a row whose sum of squares leaves fp32 gives zeros, and NaN for
+ * an infinity in it); h is rounded once, and so is y, to what `out` says:
  *
  *   SGQ_OUT_NONE   no y (weight, y, ys NULL; a residual is needed)
  *   SGQ_OUT_16     y: [M, K] of `dtype`
